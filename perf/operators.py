@@ -1,0 +1,459 @@
+"""Cases and plain forms of the mixture-of-experts operators.
+
+The operators are what surrounds the batched compression of a
+mixture-of-experts all-to-all: the router that picks the experts, the dispatch
+that puts the rows in expert order, the experts' products in 8-bit floating
+point with a scale for each block of 128, and the combination of the experts'
+rows.  Where `own` is false `run` computes them with elementary torch
+operations in 32 bits; where it is true it calls the package.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+INF = float("inf")
+BLOCK = 128          # values under one scale
+E4M3_MAX = 448.0     # the largest finite e4m3 value
+AMAX_MIN = 2.0 ** -100  # a block's largest magnitude counts as at least this
+
+
+def listed():
+    return [
+        # one token of a serving step through the router of the all-to-all workload (64 experts, top-8)
+        dict(name="route_token", op="route", tokens=1, experts=64, top_k=8, groups=1, top_groups=1, score="softmax",
+             renorm=True, bias=False, dtype="f32", pad=0.0, grad=False),
+        # a training step's router of the all-to-all workload: 16384 tokens, 64 experts, top-8, with its gradient
+        dict(name="route_train", op="route", tokens=16384, experts=64, top_k=8, groups=1, top_groups=1, score="softmax",
+             renorm=False, bias=False, dtype="bf16", pad=0.0, grad=True),
+        # many experts in groups, sigmoid scores and a balancing bias, an odd token count with padded tokens
+        dict(name="route_groups_train", op="route", tokens=8191, experts=256, top_k=8, groups=8, top_groups=4,
+             score="sigmoid", renorm=True, bias=True, dtype="f32", pad=0.03, grad=True),
+        # a small serving batch put in expert order
+        dict(name="dispatch_step", op="dispatch", tokens=33, experts=64, top_k=8, hidden=2048, pad=0.0),
+        # the payload of the all-to-all workload: 16384 tokens x top-8 rows of 2048
+        dict(name="dispatch_a2a", op="dispatch", tokens=16384, experts=64, top_k=8, hidden=2048, pad=0.01),
+        # the small serving batch's rows weighted and added back
+        dict(name="combine_step", op="combine", tokens=33, experts=64, top_k=8, hidden=2048, pad=0.0, grad=False),
+        # the all-to-all workload's rows combined, with the gradients of the rows and of the weights
+        dict(name="combine_train", op="combine", tokens=16384, experts=64, top_k=8, hidden=2048, pad=0.01, grad=True),
+        # one token through the 4096 x 14336 weight of the all-gather workload
+        dict(name="linear_token", op="linear", rows=1, tail=0, experts=1, k=4096, n=14336, grad=False),
+        # the small serving batch's rows through 64 experts: a few rows each, some none
+        dict(name="linear_experts_step", op="linear", rows=264, tail=0, experts=64, k=2048, n=1024, grad=False),
+        # the all-to-all workload's 131072 rows through 64 experts
+        dict(name="linear_experts", op="linear", rows=131072, tail=1000, experts=64, k=2048, n=1024, grad=False),
+        # the gradients of a dense layer with the all-gather workload's weight
+        dict(name="linear_dense_grad", op="linear", rows=4096, tail=0, experts=1, k=4096, n=14336, grad=True),
+        # the gradients of a ragged batch through 64 experts, odd sizes everywhere
+        dict(name="linear_experts_grad", op="linear", rows=16411, tail=37, experts=64, k=2000, n=1000, grad=True),
+    ]
+
+
+def _log(rng, lo, hi):
+    """A whole number spread over [lo, hi] by its logarithm."""
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["route", "route", "dispatch", "combine", "linear", "linear"])
+    if op == "route":
+        groups = rng.choice([1, 1, 2, 4, 8])
+        per = _log(rng, 2, 512 // groups)
+        top_groups = rng.randint(1, groups)
+        top_k = rng.randint(1, min(12, top_groups * per))
+        return dict(op=op, tokens=_log(rng, 1, 16384), experts=groups * per, top_k=top_k,
+                    groups=groups, top_groups=top_groups, score=rng.choice(["softmax", "sigmoid"]),
+                    # a single renormalised weight is constant: it has no gradient to compare
+                    renorm=top_k > 1 and rng.random() < 0.5, bias=rng.random() < 0.5, dtype=rng.choice(["f32", "bf16"]),
+                    pad=rng.choice([0.0, 0.05]), grad=rng.random() < 0.7)
+    if op in ("dispatch", "combine"):
+        experts = _log(rng, 2, 256)
+        case = dict(op=op, tokens=_log(rng, 1, 16384), experts=experts, top_k=rng.randint(1, min(8, experts)),
+                    hidden=8 * rng.choice([v for v in range(1, 257) if v != 384]), pad=rng.choice([0.0, 0.05]))
+        if op == "combine":
+            case["grad"] = rng.random() < 0.6
+        return case
+    experts = rng.choice([1, _log(rng, 2, 64)])
+    k, n = (rng.choice([_log(rng, 64, 4096), 16 * rng.randint(4, 256)]) for _ in range(2))
+    k, n = (v + 16 if v == 3072 else v for v in (k, n))
+    return dict(op=op, rows=_log(rng, 1, 16384), tail=rng.choice([0, 0, 19]) if experts > 1 else 0, experts=experts, k=k,
+                n=n, grad=rng.random() < 0.4)
+
+
+# ---- inputs -----------------------------------------------------------------
+def _popularity(experts):
+    """The all-to-all workload's expert probabilities: Zipf with exponent 1.2."""
+    p = (np.arange(experts, dtype=np.float64) + 1.0) ** -1.2
+    return p / p.sum()
+
+
+def _logits(g, tokens, experts, pad):
+    """log p + Gumbel noise, as the all-to-all workload draws its experts; a share `pad` of the tokens is
+    padding (no expert available), and as many single experts are masked."""
+    logp = torch.log(torch.tensor(_popularity(experts), dtype=torch.float32, device="cuda"))
+    logp = logp[torch.randperm(experts, generator=g, device="cuda")]
+    u = torch.rand(tokens, experts, generator=g, device="cuda").clamp(1e-6, 1 - 1e-6)
+    x = logp - torch.log(-torch.log(u))
+    if pad:
+        x = x.masked_fill(torch.rand(tokens, experts, generator=g, device="cuda") < pad / 2, -INF)
+        x = x.masked_fill(torch.rand(tokens, 1, generator=g, device="cuda") < pad, -INF)
+    return x
+
+
+def _chosen(g, c):
+    """Expert indices of a routed batch, -1 where a token has none."""
+    v, i = torch.sort(_logits(g, c["tokens"], c["experts"], c["pad"]), dim=1, descending=True, stable=True)
+    i = torch.where(v == -INF, -1, i)
+    return i[:, : c["top_k"]].to(torch.int32).contiguous()
+
+
+def _counts(c):
+    """Rows of each expert, by popularity: the same for every seed up to a permutation."""
+    share = _popularity(c["experts"]) * c["rows"]
+    n = np.floor(share).astype(np.int64)
+    n[np.argsort(n - share, kind="stable")[: c["rows"] - int(n.sum())]] += 1
+    return n
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def prepare(case, seed):
+    c = dict(case)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    s = {"c": c}
+    if own:
+        import lossless_bf16_exponent_split_gb300 as z
+    if c["op"] == "route":
+        s["logits"] = _logits(g, c["tokens"], c["experts"], c["pad"]).to(torch.bfloat16 if c["dtype"] == "bf16" else torch.float32)
+        # a balancing bias moves in steps of one thousandth
+        s["bias"] = torch.randint(-100, 101, (c["experts"],), generator=g, device="cuda").float() / 1000 if c["bias"] else None
+        s["grad_weights"] = _randn(g, c["tokens"], c["top_k"])
+    if c["op"] in ("dispatch", "combine"):
+        s["idx"] = _chosen(g, c)
+    if c["op"] == "dispatch":
+        s["x"] = _randn(g, c["tokens"], c["hidden"]).bfloat16()
+    if c["op"] == "combine":
+        s["pos"] = _places(s["idx"], c["experts"])[0]
+        s["y"] = _randn(g, c["tokens"] * c["top_k"], c["hidden"]).bfloat16()
+        w = torch.rand(c["tokens"], c["top_k"], generator=g, device="cuda") + 0.05
+        s["weights"] = torch.where(s["idx"] < 0, 0.0, w / w.sum(1, keepdim=True))
+        s["grad"] = _randn(g, c["tokens"], c["hidden"]).bfloat16()
+    if c["op"] in ("route", "dispatch", "combine") and own:
+        more = dict(score=c["score"], groups=c["groups"], top_groups=c["top_groups"], renormalize=c["renorm"]) if c["op"] == "route" else {}
+        s["moe"] = z.Moe(c["experts"], c["top_k"], **more)
+    if c["op"] == "linear":
+        rows = c["rows"] + c["tail"]
+        n = _counts(c)[torch.randperm(c["experts"], generator=g, device="cuda").cpu().numpy()]
+        s["counts"] = n.tolist()
+        # a dense layer has no table of groups
+        s["offsets"] = None if c["experts"] == 1 else torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device="cuda")
+        # rows of differing size, as a layer's inputs and gradients have them
+        s["x"] = (_randn(g, rows, c["k"]) * torch.exp(_randn(g, rows, 1))).bfloat16()
+        w = _randn(g, c["experts"], c["n"], c["k"]) * c["k"] ** -0.5
+        s["q"], s["scale"] = _quantize_weight(w)
+        del w
+        if c["grad"]:
+            s["grad"] = (_randn(g, rows, c["n"]) * 1e-3 * torch.exp(_randn(g, rows, 1))).bfloat16()
+        if own:
+            s["fp8"] = z.BlockFp8()
+            s["w"] = s["fp8"].weight(s["q"], s["scale"], backward=c["grad"])
+    return s
+
+
+# ---- plain forms ------------------------------------------------------------
+def _tree_sum(x):
+    """The sum over the last axis by halves, so that its rounding does not depend on who computes it."""
+    n = 1 << max(0, (x.shape[-1] - 1).bit_length())
+    x = torch.nn.functional.pad(x, (0, n - x.shape[-1]))
+    while n > 1:
+        n //= 2
+        x = x[..., :n] + x[..., n:]
+    return x[..., 0]
+
+
+def _route(s):
+    c, l, k = s["c"], s["logits"].float(), s["c"]["top_k"]
+    if c["score"] == "softmax":
+        m = l.amax(1, keepdim=True)
+        e = torch.exp(l - torch.where(m == -INF, 0.0, m))
+        total = _tree_sum(e)[:, None]
+        score = e / torch.where(total == 0, 1.0, total)
+    else:
+        score = 1.0 / (1.0 + torch.exp(-l))
+    v = (score if s["bias"] is None else score + s["bias"]).masked_fill(l == -INF, -INF)
+    if c["groups"] > 1:
+        by = v.reshape(v.shape[0], c["groups"], -1)
+        top = torch.sort(by, dim=2, descending=True).values[:, :, :2]
+        none = top[:, :, 0] == -INF
+        top = top.masked_fill(top == -INF, 0.0).sum(2).masked_fill(none, -INF)
+        order = torch.sort(top, dim=1, descending=True, stable=True).indices
+        keep = torch.zeros_like(top, dtype=torch.bool).scatter_(1, order[:, : c["top_groups"]], True)
+        v = by.masked_fill(~keep[:, :, None], -INF).reshape(v.shape)
+    top, idx = (t[:, :k] for t in torch.sort(v, dim=1, descending=True, stable=True))
+    there = top != -INF
+    w = torch.where(there, score.gather(1, idx), 0.0)
+    if c["renorm"]:
+        total = w.sum(1, keepdim=True)
+        w = w / torch.where(total == 0, 1.0, total)
+    out = {"idx": torch.where(there, idx, -1).to(torch.int32), "weights": w}
+    if c["grad"]:
+        gw = torch.where(there, s["grad_weights"], 0.0)
+        if c["renorm"]:
+            inner = gw - (gw * w).sum(1, keepdim=True)
+            part = w * inner if c["score"] == "softmax" else w * (1.0 - score.gather(1, idx)) * inner
+            grad = torch.zeros_like(l).scatter_(1, idx, torch.where(there, part, 0.0))
+        elif c["score"] == "softmax":
+            up = torch.zeros_like(l).scatter_(1, idx, gw)
+            grad = score * (up - (score * up).sum(1, keepdim=True))
+        else:
+            p = score.gather(1, idx)
+            grad = torch.zeros_like(l).scatter_(1, idx, torch.where(there, gw * p * (1.0 - p), 0.0))
+        out["grad"] = grad.to(s["logits"].dtype)
+    return out
+
+
+def _places(idx, experts):
+    """(pos, counts, offsets, order): each slot's row in expert order (-1: none), the rows of each expert and
+    where they begin, and the slot of each row; slots without an expert come last."""
+    key = torch.where(idx < 0, experts, idx).reshape(-1).long()
+    order = torch.sort(key, stable=True).indices
+    pos = torch.empty_like(order).scatter_(0, order, torch.arange(order.numel(), device=idx.device))
+    pos = torch.where(key == experts, -1, pos).to(torch.int32).reshape(idx.shape)
+    counts = torch.zeros(experts + 1, dtype=torch.int32, device=idx.device)
+    counts.scatter_add_(0, key, torch.ones_like(key, dtype=torch.int32))
+    counts = counts[:experts]
+    offsets = torch.nn.functional.pad(torch.cumsum(counts, 0), (1, 0)).to(torch.int32)
+    return pos, counts, offsets, order
+
+
+def _dispatch(s):
+    idx, c = s["idx"], s["c"]
+    pos, counts, offsets, order = _places(idx, c["experts"])
+    rows = s["x"][order // c["top_k"]]
+    rows = torch.where((idx.reshape(-1)[order] < 0)[:, None], 0.0, rows)
+    return {"rows": rows, "pos": pos, "counts": counts, "offsets": offsets}
+
+
+def _combine(s):
+    there = s["pos"] >= 0
+    at = s["pos"].clamp(min=0).long()
+    w = torch.where(there, s["weights"], 0.0)
+    y = s["y"][at].float()
+    out = {"out": (y * w[:, :, None]).sum(1).to(torch.bfloat16)}
+    if s["c"]["grad"]:
+        up = s["grad"].float()
+        out["grad_weights"] = torch.where(there, (y * up[:, None, :]).sum(2), 0.0)
+        rows = (up[:, None, :] * w[:, :, None]).to(torch.bfloat16)
+        grad = torch.zeros_like(s["y"])
+        grad[at[there]] = rows[there]
+        out["grad_y"] = grad
+    return out
+
+
+def _codes(x, amax):
+    """x as the e4m3 codes (held in 32 bits) under a scale that puts amax at 448, and that scale."""
+    a = amax.clamp(min=AMAX_MIN)
+    return (x * (E4M3_MAX / a)).to(torch.float8_e4m3fn), a / E4M3_MAX
+
+
+def _quantize_weight(w):
+    """[E, N, K] in blocks of 128 x 128: codes and scales [E, N blocks, K blocks]."""
+    e, n, k = w.shape
+    p = torch.nn.functional.pad(w, (0, -k % BLOCK, 0, -n % BLOCK))
+    b = p.reshape(e, p.shape[1] // BLOCK, BLOCK, p.shape[2] // BLOCK, BLOCK)
+    amax = b.abs().amax((2, 4), keepdim=True)
+    q, scale = _codes(b, amax)
+    return q.reshape(p.shape)[:, :n, :k].contiguous(), scale[:, :, 0, :, 0].contiguous()
+
+
+def _rows_blocked(x):
+    """x rounded to e4m3 in blocks of 128 along its last axis, as the values that the codes stand for."""
+    r, k = x.shape
+    nb = -(-k // BLOCK)
+    b = torch.nn.functional.pad(x, (0, nb * BLOCK - k)).reshape(r, nb, BLOCK)
+    q, scale = _codes(b, b.abs().amax(2, keepdim=True))
+    return (q.float() * scale).reshape(r, nb * BLOCK)[:, :k]
+
+
+def _linear(s):
+    c, x = s["c"], s["x"].float()
+    scale = s["scale"].repeat_interleave(BLOCK, 1).repeat_interleave(BLOCK, 2)[:, : c["n"], : c["k"]]
+    w = s["q"].float() * scale
+    parts = s["counts"] + [c["tail"]]
+    if not c["grad"]:
+        y = [a @ w[e].T for e, a in enumerate(torch.split(_rows_blocked(x), parts)[:-1])]
+        return {"y": torch.cat(y + [x.new_zeros(c["tail"], c["n"])]).bfloat16()}
+    up = s["grad"].float()
+    dx = [a @ w[e] for e, a in enumerate(torch.split(_rows_blocked(up), parts)[:-1])]
+    dx = torch.cat(dx + [x.new_zeros(c["tail"], c["k"])]).bfloat16()
+    # the weight's gradient sums over an expert's rows: there both factors' blocks run along the rows
+    pairs = zip(torch.split(up, parts)[:-1], torch.split(x, parts)[:-1])
+    dw = torch.stack([_rows_blocked(a.T) @ _rows_blocked(b.T).T for a, b in pairs]).bfloat16()
+    return {"grad_x": dx, "grad_w": dw}
+
+
+def run(state):
+    s = state
+    op = s["c"]["op"]
+    if not own:
+        return {"route": _route, "dispatch": _dispatch, "combine": _combine, "linear": _linear}[op](s)
+    if op == "route":
+        idx, weights = s["moe"].route(s["logits"], s["bias"])
+        out = {"idx": idx, "weights": weights}
+        if s["c"]["grad"]:
+            out["grad"] = s["moe"].route_backward(s["logits"], idx, s["grad_weights"])
+        return out
+    if op == "dispatch":
+        d = s["moe"].dispatch(s["x"], s["idx"])
+        return {"rows": d.rows, "pos": d.pos, "counts": d.counts, "offsets": d.offsets}
+    if op == "combine":
+        out = {"out": s["moe"].combine(s["y"], s["pos"], s["weights"])}
+        if s["c"]["grad"]:
+            out["grad_y"], out["grad_weights"] = s["moe"].combine_backward(s["grad"], s["y"], s["pos"], s["weights"])
+        return out
+    if not s["c"]["grad"]:
+        return {"y": s["fp8"].linear(s["x"], s["w"], s["offsets"])}
+    dx, dw = s["fp8"].linear_backward(s["grad"], s["x"], s["w"], s["offsets"])
+    return {"grad_x": dx, "grad_w": dw}
+
+
+# ---- what a pass cannot do without ------------------------------------------
+def work(case):
+    c = case
+    if c["op"] == "route":
+        t, e, k, b = c["tokens"], c["experts"], c["top_k"], 2 if c["dtype"] == "bf16" else 4
+        once = t * e * b + 8 * t * k + (4 * e if c["bias"] else 0)
+        # the gradient also reads the weights' gradient and writes the logits'
+        return {"bytes": once + (t * e * b + 4 * t * k if c["grad"] else 0), "flops": (4 if c["grad"] else 2) * t * e}
+    if c["op"] == "dispatch":
+        t, k, h = c["tokens"], c["top_k"], c["hidden"]
+        return {"bytes": 2 * t * h + 2 * t * k * h + 8 * t * k + 8 * c["experts"], "flops": 0}
+    if c["op"] == "combine":
+        t, k, h = c["tokens"], c["top_k"], c["hidden"]
+        bytes_, flops = 2 * t * k * h + 2 * t * h + 8 * t * k, 2 * t * k * h
+        if c["grad"]:
+            bytes_ += 2 * t * k * h + 2 * t * h + 4 * t * k
+            flops += 3 * t * k * h
+        return {"bytes": bytes_, "flops": flops}
+    r, k, n = c["rows"], c["k"], c["n"]
+    used = int((_counts(c) > 0).sum())
+    blocks = used * -(-n // BLOCK) * -(-k // BLOCK)
+    weight = used * n * k + 4 * blocks
+    all_rows = r + c["tail"]
+    if not c["grad"]:
+        return {"bytes": 2 * r * k + weight + 2 * all_rows * n, "flops": 2 * r * k * n}
+    return {"bytes": 2 * r * (k + n) + weight + 2 * all_rows * k + 2 * c["experts"] * n * k, "flops": 4 * r * k * n}
+
+
+# ---- the definitions in 64 bits ---------------------------------------------
+def _exact_route(s):
+    c, l = s["c"], s["logits"].double()
+    off = torch.isinf(l) & (l < 0)
+    score = torch.nan_to_num(torch.softmax(l, 1), nan=0.0) if c["score"] == "softmax" else torch.sigmoid(l)
+    v = score.clone() if s["bias"] is None else score + s["bias"].double()
+    v[off] = -INF
+    if c["groups"] > 1:
+        by = v.view(v.shape[0], c["groups"], -1)
+        two = torch.topk(by, min(2, by.shape[2]), dim=2).values
+        value = torch.where(two == -INF, 0.0, two).sum(2)
+        value[two[:, :, 0] == -INF] = -INF
+        ranks = torch.argsort(torch.argsort(value, dim=1, descending=True, stable=True), dim=1)
+        v = torch.where((ranks < c["top_groups"])[:, :, None], by, -INF).flatten(1)
+    rank = torch.argsort(v, dim=1, descending=True, stable=True)[:, : c["top_k"]]
+    mask = torch.zeros_like(v).scatter_(1, rank, 1.0) * (v != -INF)
+    l0 = torch.where(off, 0.0, l)
+    with torch.enable_grad():
+        x = l0.clone().requires_grad_()
+        p = torch.softmax(x.masked_fill(off, -1e300), 1) if c["score"] == "softmax" else torch.sigmoid(x)
+        chosen = p * mask
+        w = chosen / chosen.sum(1, keepdim=True).clamp(min=1e-300) if c["renorm"] else chosen
+        w = w.gather(1, rank)
+        out = {"idx": None, "weights": w.detach()}
+        if c["grad"]:
+            live = mask.gather(1, rank)
+            (grad,) = torch.autograd.grad((w * live * s["grad_weights"].double()).sum(), x)
+            out["grad"] = torch.where(off, 0.0, grad)
+    return out
+
+
+def _exact_combine(s):
+    y, w, pos = s["y"].double(), s["weights"].double(), s["pos"].long()
+    t, h = s["grad"].shape
+    out = torch.zeros(t, h, dtype=torch.float64, device="cuda")
+    gw = torch.zeros_like(w)
+    gy = torch.zeros_like(y)
+    up = s["grad"].double()
+    for k in range(pos.shape[1]):
+        has = pos[:, k] >= 0
+        at = pos[has, k]
+        out[has] += y[at] * w[has, k, None]
+        gw[has, k] = (y[at] * up[has]).sum(1)
+        gy[at] = up[has] * w[has, k, None]
+    return {"out": out, "grad_weights": gw, "grad_y": gy} if s["c"]["grad"] else {"out": out}
+
+
+def _round_e4m3(v):
+    """The nearest e4m3 value in 64 bits: 3 fraction bits, exponents down to -6, at most 448, ties to even."""
+    _, ex = torch.frexp(v)
+    step = torch.ldexp(torch.ones_like(v), (ex - 1).clamp(min=-6) - 3)
+    return (torch.round(v / step) * step).clamp(-448.0, 448.0)
+
+
+def _exact_blocked(x):
+    """x rounded in blocks of 128 along its first axis."""
+    out = torch.empty_like(x)
+    for lo in range(0, x.shape[0], BLOCK):
+        part = x[lo:lo + BLOCK]
+        a = part.abs().max(0).values.clamp(min=AMAX_MIN)
+        out[lo:lo + BLOCK] = _round_e4m3(part * (448.0 / a)) * (a / 448.0)
+    return out
+
+
+def _exact_linear(s):
+    c = s["c"]
+    w = torch.empty(s["q"].shape, dtype=torch.float64, device="cuda")
+    for i in range(s["scale"].shape[1]):
+        for j in range(s["scale"].shape[2]):
+            r, k = slice(i * BLOCK, (i + 1) * BLOCK), slice(j * BLOCK, (j + 1) * BLOCK)
+            w[:, r, k] = s["q"][:, r, k].double() * s["scale"][:, i, j, None, None].double()
+    left = s["x"].double() if not c["grad"] else s["grad"].double()
+    dense = _exact_blocked(left.T.contiguous()).T
+    first = torch.zeros(left.shape[0], c["k"] if c["grad"] else c["n"], dtype=torch.float64, device="cuda")
+    dw = torch.zeros_like(w) if c["grad"] else None
+    lo = 0
+    for e, m in enumerate(s["counts"]):
+        hi = lo + m
+        if m:
+            first[lo:hi] = dense[lo:hi] @ (w[e] if c["grad"] else w[e].T)
+            if c["grad"]:
+                dw[e] = _exact_blocked(left[lo:hi]).T @ _exact_blocked(s["x"][lo:hi].double())
+        lo = hi
+    return {"grad_x": first, "grad_w": dw} if c["grad"] else {"y": first}
+
+
+def exact(case, seed):
+    global own
+    was, own = own, False  # the inputs alone: no handle of the package
+    try:
+        s = prepare(case, seed)
+    finally:
+        own = was
+    op = case["op"]
+    if op == "route":
+        return _exact_route(s)
+    if op == "combine":
+        return _exact_combine(s)
+    if op == "linear":
+        return _exact_linear(s)
+    # the rows are copies and the rest whole numbers; only the rows are floating values
+    rows = torch.zeros(s["idx"].numel(), case["hidden"], dtype=torch.float64, device="cuda")
+    flat = s["idx"].reshape(-1).cpu().numpy()
+    slots = np.argsort(flat, kind="stable")
+    slots = slots[flat[slots] >= 0]
+    rows[: slots.size] = s["x"][torch.from_numpy(slots // case["top_k"]).cuda()].double()
+    return {"rows": rows, "pos": None, "counts": None, "offsets": None}
