@@ -138,7 +138,7 @@ def prepare(case, seed):
     if c["op"] == "dispatch":
         s["x"] = _randn(g, c["tokens"], c["hidden"]).bfloat16()
     if c["op"] == "combine":
-        s["pos"] = _places(s["idx"], c["experts"])[0]
+        s["pos"], _, s["offsets"], _ = _places(s["idx"], c["experts"])
         s["y"] = _randn(g, c["tokens"] * c["top_k"], c["hidden"]).bfloat16()
         w = torch.rand(c["tokens"], c["top_k"], generator=g, device="cuda") + 0.05
         s["weights"] = torch.where(s["idx"] < 0, 0.0, w / w.sum(1, keepdim=True))
@@ -314,7 +314,7 @@ def run(state):
     if op == "combine":
         out = {"out": s["moe"].combine(s["y"], s["pos"], s["weights"])}
         if s["c"]["grad"]:
-            out["grad_y"], out["grad_weights"] = s["moe"].combine_backward(s["grad"], s["y"], s["pos"], s["weights"])
+            out["grad_y"], out["grad_weights"] = s["moe"].combine_backward(s["grad"], s["y"], s["pos"], s["weights"], s["offsets"])
         return out
     if not s["c"]["grad"]:
         return {"y": s["fp8"].linear(s["x"], s["w"], s["offsets"])}
