@@ -317,6 +317,114 @@ typedef struct {
  * outside its range.  Host only. */
 zccl_status_t zccl_rs_plan(const zccl_rs_model_t* model, zccl_rs_plan_t* plan);
 
+/* ---- mixture of experts: the two sides of the all-to-all ---------------------
+ *
+ * The payload of the all-to-all that zccl_compress_batched codes (ZipCCL 2.D)
+ * is made by a router and a dispatch, and its far side runs the experts'
+ * products and combines their rows.  The paper takes that payload as given;
+ * these calls make it and use it.  T tokens, E experts, K chosen per token; a
+ * slot is one (token, k) pair, numbered t * K + k.  The calls follow the
+ * conventions above, with alignments stated per call. */
+#define ZCCL_MAX_EXPERTS 512u /* experts per call                               */
+#define ZCCL_MAX_TOP_K 32u    /* experts chosen per token                       */
+
+typedef enum { ZCCL_BF16 = 0, ZCCL_F32 = 1 } zccl_dtype_t;
+typedef enum { ZCCL_SCORE_SOFTMAX = 0, ZCCL_SCORE_SIGMOID = 1 } zccl_score_t;
+
+/* How a router picks its experts. */
+typedef struct {
+    uint32_t experts;     /* E: 1..ZCCL_MAX_EXPERTS                                */
+    uint32_t top_k;       /* K: 1..min(ZCCL_MAX_TOP_K, top_groups * E / groups)    */
+    uint32_t groups;      /* divides E, 1..32; experts of a group are consecutive  */
+    uint32_t top_groups;  /* groups a token may choose from, 1..groups             */
+    int score;            /* zccl_score_t                                          */
+    int renormalize;      /* nonzero: a token's weights are divided by their sum   */
+    float scale;          /* the weights' factor; finite                           */
+} zccl_route_t;
+
+/* Routing.  For each row l of E logits (type dtype, rows `stride` elements
+ * apart):
+ *   score   softmax: p = exp(l - max l) / Z, Z summed over the experts by
+ *           halves (x[i] + x[i + n/2], n = E rounded up to a power of two);
+ *           sigmoid: p = 1 / (1 + exp(-l))
+ *   value   v = p + d_bias[e] (d_bias NULL: v = p), all in fp32
+ *   groups  (groups > 1) a group's value is the sum of its two largest v; the
+ *           top_groups groups of largest value are kept
+ *   choice  the K experts of largest v in them, in that order; ties go to the
+ *           lower index (experts and groups alike), so a choice does not depend
+ *           on anything but its row
+ *   weight  scale * p, or scale * p / (sum of the chosen p) with renormalize,
+ *           computed from the logits so that a common factor cannot underflow
+ * The bias takes part in the choice only.  A logit (or bias) of -infinity makes
+ * its expert unavailable; where fewer than K are available the remaining slots
+ * hold index -1 and weight 0.  A row with a NaN (or, for softmax, a +infinite)
+ * logit or a NaN bias chooses nothing, and *d_status gets INVALID_ARG.
+ * d_idx: int32 [T][K]; d_weights: float [T][K].  T < 2^31 / K. */
+zccl_status_t zccl_route(const zccl_route_t* cfg, const void* d_logits, int dtype, uint64_t stride,
+                         const float* d_bias, uint64_t tokens, int32_t* d_idx, float* d_weights,
+                         uint32_t* d_status, cudaStream_t stream);
+
+/* Gradient of zccl_route's weights with respect to the logits, the choice
+ * held fixed: d_grad_logits [T] rows of E, `grad_stride` elements apart, of the
+ * logits' type, every element written (zero where a row chose nothing).  d_idx:
+ * the choice; entries outside 0..E-1 choose nothing. */
+zccl_status_t zccl_route_backward(const zccl_route_t* cfg, const void* d_logits, int dtype, uint64_t stride,
+                                  const int32_t* d_idx, const float* d_grad_weights, uint64_t tokens,
+                                  void* d_grad_logits, uint64_t grad_stride, cudaStream_t stream);
+
+/* Workspace of zccl_dispatch (zeroed once before its first use, as above). */
+zccl_status_t zccl_dispatch_workspace_bytes(uint64_t tokens, uint32_t experts, uint32_t top_k, uint64_t* bytes);
+
+/* Room for the streams of a dispatch's segment table: `rows` rows of `hidden`
+ * values over 2 * experts segments, however they are shared out. */
+uint64_t zccl_dispatch_stream_bytes(uint64_t rows, uint64_t hidden, uint32_t experts);
+
+/* Dispatch: the rows of the tokens in expert order, each token's row once per
+ * expert it chose.
+ *   d_idx      int32 [T][K]; an entry outside 0..E-1 sends nothing
+ *   d_x        BF16 [T] rows of `hidden` values, `stride` elements apart (both
+ *              multiples of 8, d_x 16-byte aligned); NULL: no rows are moved
+ *   d_rows     BF16 [T * K][hidden], 16-byte aligned: the rows of expert 0, then
+ *              those of expert 1, ..., within an expert in slot order (a stable
+ *              order: it does not change from run to run); the rows after the
+ *              last expert's are zero
+ *   d_pos      int32 [T][K]: a slot's row in d_rows, -1 where it has none
+ *   d_counts   int32 [E]; d_offsets: int32 [E + 1], where each expert's rows
+ *              begin and, last, how many rows there are
+ * With d_segs (device, 2 * E entries, 8-byte aligned) it also writes the table
+ * that zccl_compress_batched reads: entry 2e is expert e's static part, its
+ * first min(count, capacity) rows, and entry 2e + 1 the rest (ZipCCL 2.D); the
+ * streams go to consecutive places of d_streams (16-byte aligned,
+ * stream_bytes >= zccl_dispatch_stream_bytes(T * K, hidden, E)), so the routing's
+ * sizes never visit the host.  E <= ZCCL_MAX_EXPERTS, K <= ZCCL_MAX_TOP_K,
+ * T * K < 2^31, hidden < 2^24. */
+zccl_status_t zccl_dispatch(const int32_t* d_idx, uint64_t tokens, uint32_t experts, uint32_t top_k,
+                            const uint16_t* d_x, uint64_t stride, uint64_t hidden, uint16_t* d_rows,
+                            int32_t* d_pos, int32_t* d_counts, int32_t* d_offsets, zccl_segment_t* d_segs,
+                            uint64_t capacity, void* d_streams, uint64_t stream_bytes, void* d_ws,
+                            uint64_t ws_bytes, cudaStream_t stream);
+
+/* Combine: d_out[t] = sum over k of d_weights[t][k] * d_y[d_pos[t][k]], added in
+ * fp32 in the order of k and rounded once to BF16.  d_y: BF16 [rows][hidden];
+ * slots whose d_pos is outside 0..rows-1 add nothing; a token with no slot gets
+ * zeros.  d_weights NULL: all 1 (the gradient of a dispatch with respect to its
+ * tokens).  hidden a multiple of 8, < 2^24; d_y and d_out 16-byte aligned. */
+zccl_status_t zccl_combine(const uint16_t* d_y, uint64_t rows, uint64_t hidden, const int32_t* d_pos,
+                           const float* d_weights, uint64_t tokens, uint32_t top_k, uint16_t* d_out,
+                           cudaStream_t stream);
+
+/* Gradients of zccl_combine: d_grad_y[d_pos[t][k]] = d_weights[t][k] *
+ * d_grad_out[t] (rounded once to BF16) and d_grad_weights[t][k] = the fp32 dot
+ * product of d_grad_out[t] and d_y[d_pos[t][k]] (0 where a slot has no row).
+ * d_pos is a dispatch's: each row has one slot.  With d_total (device int32, the
+ * last entry of the dispatch's d_offsets) the rows from *d_total on, which no
+ * slot points to, get zeros; without it they are not written.  d_y and
+ * d_grad_weights may both be NULL (the rows' gradient alone). */
+zccl_status_t zccl_combine_backward(const uint16_t* d_grad_out, const uint16_t* d_y, uint64_t rows,
+                                    uint64_t hidden, const int32_t* d_pos, const float* d_weights,
+                                    const int32_t* d_total, uint64_t tokens, uint32_t top_k,
+                                    uint16_t* d_grad_y, float* d_grad_weights, cudaStream_t stream);
+
 /* Static text for a status code. */
 const char* zccl_status_string(zccl_status_t status);
 

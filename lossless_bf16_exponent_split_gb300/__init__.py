@@ -10,7 +10,8 @@ of the codec runs in the library's CUDA kernels; there is no Python or CPU
 fallback -- if ``libzccl.so`` is missing, every call raises.
 
 ``Codec`` is a convenience layer over the same calls that allocates buffers
-with PyTorch (device memory and streams only).
+with PyTorch (device memory and streams only); ``Moe`` does the same for the
+calls around a mixture-of-experts all-to-all.
 """
 from __future__ import annotations
 
@@ -23,6 +24,10 @@ from . import build as _build
 OK, INVALID_ARG, BUFFER_TOO_SMALL, CORRUPT_STREAM, CUDA_ERROR, TIMEOUT = range(6)
 OP_COMPRESS, OP_DECOMPRESS, OP_COMPRESS_BATCHED, OP_DECOMPRESS_REDUCE = range(4)
 POLL_COUNTER, POLL_FLAG = 1, 2
+BF16, F32 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+MAX_EXPERTS = 512
+MAX_TOP_K = 32
 MAX_SEGMENTS = 4096
 MAX_SHARDS = 1024
 CHUNK = 4096
@@ -72,6 +77,24 @@ _SIGS = {
     "zccl_lut_from_data": ([ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p],
                            ctypes.c_int),
     "zccl_rs_plan": ([ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "zccl_route": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_void_p,
+                    ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p],
+                   ctypes.c_int),
+    "zccl_route_backward": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_void_p,
+                             ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p],
+                            ctypes.c_int),
+    "zccl_dispatch_workspace_bytes": ([ctypes.c_uint64, ctypes.c_uint32, ctypes.c_uint32,
+                                       ctypes.POINTER(ctypes.c_uint64)], ctypes.c_int),
+    "zccl_dispatch_stream_bytes": ([ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint32], ctypes.c_uint64),
+    "zccl_dispatch": ([ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_uint32, ctypes.c_void_p,
+                       ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_uint64,
+                       ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p], ctypes.c_int),
+    "zccl_combine": ([ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p,
+                      ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "zccl_combine_backward": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p,
+                               ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p,
+                               ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
     "zccl_status_string": ([ctypes.c_int], ctypes.c_char_p),
 }
 
@@ -88,6 +111,13 @@ class RsPlan(ctypes.Structure):
     """zccl_rs_plan_t"""
     _fields_ = [("zipped", ctypes.c_int), ("native_us", ctypes.c_double), ("zipped_us", ctypes.c_double),
                 ("breakeven_link_gbs", ctypes.c_double)]
+
+
+class Route(ctypes.Structure):
+    """zccl_route_t"""
+    _fields_ = [("experts", ctypes.c_uint32), ("top_k", ctypes.c_uint32), ("groups", ctypes.c_uint32),
+                ("top_groups", ctypes.c_uint32), ("score", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("scale", ctypes.c_float)]
 
 
 class ZcclError(RuntimeError):
@@ -236,6 +266,46 @@ def zccl_rs_plan(ranks, nbytes, ratio, link_gbs, link_latency_us, compress_gbs, 
             "breakeven_link_gbs": p.breakeven_link_gbs}
 
 
+def zccl_route(cfg, d_logits, dtype, stride, d_bias, tokens, d_idx, d_weights, d_status, stream) -> int:
+    """The experts and weights of each row of logits; cfg: a Route."""
+    return lib().zccl_route(ctypes.addressof(cfg), d_logits, dtype, stride, d_bias, tokens, d_idx, d_weights,
+                            d_status, stream)
+
+
+def zccl_route_backward(cfg, d_logits, dtype, stride, d_idx, d_grad_weights, tokens, d_grad_logits, grad_stride,
+                        stream) -> int:
+    return lib().zccl_route_backward(ctypes.addressof(cfg), d_logits, dtype, stride, d_idx, d_grad_weights, tokens,
+                                     d_grad_logits, grad_stride, stream)
+
+
+def zccl_dispatch_workspace_bytes(tokens: int, experts: int, top_k: int) -> int:
+    out = ctypes.c_uint64(0)
+    check(lib().zccl_dispatch_workspace_bytes(tokens, experts, top_k, ctypes.byref(out)),
+          "zccl_dispatch_workspace_bytes")
+    return int(out.value)
+
+
+def zccl_dispatch_stream_bytes(rows: int, hidden: int, experts: int) -> int:
+    return int(lib().zccl_dispatch_stream_bytes(rows, hidden, experts))
+
+
+def zccl_dispatch(d_idx, tokens, experts, top_k, d_x, stride, hidden, d_rows, d_pos, d_counts, d_offsets, d_segs,
+                  capacity, d_streams, stream_bytes, d_ws, ws_bytes, stream_handle) -> int:
+    """Rows into expert order; with d_segs also the table zccl_compress_batched reads."""
+    return lib().zccl_dispatch(d_idx, tokens, experts, top_k, d_x, stride, hidden, d_rows, d_pos, d_counts,
+                               d_offsets, d_segs, capacity, d_streams, stream_bytes, d_ws, ws_bytes, stream_handle)
+
+
+def zccl_combine(d_y, rows, hidden, d_pos, d_weights, tokens, top_k, d_out, stream) -> int:
+    return lib().zccl_combine(d_y, rows, hidden, d_pos, d_weights, tokens, top_k, d_out, stream)
+
+
+def zccl_combine_backward(d_grad_out, d_y, rows, hidden, d_pos, d_weights, d_total, tokens, top_k, d_grad_y,
+                          d_grad_weights, stream) -> int:
+    return lib().zccl_combine_backward(d_grad_out, d_y, rows, hidden, d_pos, d_weights, d_total, tokens, top_k,
+                                       d_grad_y, d_grad_weights, stream)
+
+
 def zccl_status_string(status: int) -> str:
     return lib().zccl_status_string(status).decode()
 
@@ -253,6 +323,7 @@ def check(status: int, what: str) -> None:
 
 
 from .codec import Codec  # noqa: E402  (torch-based convenience layer)
+from .moe import Dispatch, Moe  # noqa: E402
 
 __all__ = [n for n in list(globals()) if n.startswith("zccl_")] + [
-    "Codec", "ZcclError", "check", "lib", "status_string"]
+    "Codec", "Dispatch", "Moe", "ZcclError", "check", "lib", "status_string"]

@@ -1,0 +1,202 @@
+// zccl_combine.cu -- the experts' rows weighted and added back into their
+// tokens' rows, and the gradients of the rows and of the weights.
+//
+// Both are bound by HBM.  Forward: 2 T K H bytes read and 2 T H written; a
+// thread owns one 16-byte piece of a token's row and has the K rows' pieces in
+// flight together.  Backward: 2 T K H read and as many written (the token's
+// gradient row comes from L1/L2 for all but one of its K slots); a warp owns
+// one slot, so the dot product needs no other warp.
+#include "zccl_ops.cuh"
+
+namespace zccl {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct CombineArgs {
+    const uint16_t* y;
+    uint64_t rows;
+    uint32_t pieces;  // 16-byte pieces of a row
+    const int32_t* pos;
+    const float* weights;
+    uint64_t tokens;
+    uint32_t K;
+    uint16_t* out;
+    // backward
+    const uint16_t* grad_out;
+    const int32_t* total;
+    uint16_t* grad_y;
+    float* grad_weights;
+};
+
+__device__ __forceinline__ void add_piece(float (&acc)[8], float w, const uint4& v)
+{
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        acc[2 * i] = fmaf(w, bf16_lo(q[i]), acc[2 * i]);
+        acc[2 * i + 1] = fmaf(w, bf16_hi(q[i]), acc[2 * i + 1]);
+    }
+}
+
+// `lanes` threads (32, 64, 128 or 256) own a token.
+__global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a, uint32_t lanes)
+{
+    pdl_wait();
+    const uint32_t per_cta = kThreads / lanes, sub = threadIdx.x / lanes, at = threadIdx.x - sub * lanes;
+    const uint64_t t = (uint64_t)blockIdx.x * per_cta + sub;
+    if (t >= a.tokens) return;
+    const int32_t* pos = a.pos + t * a.K;
+    const float* weights = a.weights != nullptr ? a.weights + t * a.K : nullptr;
+    for (uint32_t c = at; c < a.pieces; c += lanes) {
+        float acc[8] = {};
+        for (uint32_t k0 = 0; k0 < a.K; k0 += 8) {
+            uint4 v[8];
+            float w[8];
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+                const int32_t row = k0 + k < a.K ? pos[k0 + k] : -1;
+                const bool there = row >= 0 && (uint64_t)row < a.rows;
+                w[k] = there ? (weights != nullptr ? weights[k0 + k] : 1.0f) : 0.0f;
+                v[k] = there ? ld_once(reinterpret_cast<const uint4*>(a.y) + (uint64_t)row * a.pieces + c)
+                             : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) add_piece(acc, w[k], v[k]);
+        }
+        reinterpret_cast<uint4*>(a.out)[t * a.pieces + c] =
+            make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]), pack_bf16(acc[4], acc[5]),
+                       pack_bf16(acc[6], acc[7]));
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) combine_backward_kernel(CombineArgs a)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const uint64_t i = (uint64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);  // a slot, and a row of grad_y
+    if (i < a.tokens * a.K) {
+        const int32_t row = a.pos[i];
+        const bool there = row >= 0 && (uint64_t)row < a.rows;
+        float dot = 0.0f;
+        if (there) {
+            const float w = a.weights != nullptr ? a.weights[i] : 1.0f;
+            const uint4* up = reinterpret_cast<const uint4*>(a.grad_out) + (i / a.K) * a.pieces;
+            const uint4* y = reinterpret_cast<const uint4*>(a.y) + (uint64_t)row * a.pieces;
+            uint4* gy = reinterpret_cast<uint4*>(a.grad_y) + (uint64_t)row * a.pieces;
+            constexpr int kFlight = 4;
+            for (uint32_t c0 = lane; c0 < a.pieces; c0 += 32 * kFlight) {
+                uint4 g[kFlight], v[kFlight];
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u) {
+                    const bool in = c0 + 32 * u < a.pieces;
+                    g[u] = in ? up[c0 + 32 * u] : make_uint4(0, 0, 0, 0);
+                    v[u] = in && a.y != nullptr ? ld_once(y + c0 + 32 * u) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u) {
+                    const uint32_t gq[4] = {g[u].x, g[u].y, g[u].z, g[u].w}, vq[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float lo = bf16_lo(gq[q]), hi = bf16_hi(gq[q]);
+                        dot = fmaf(lo, bf16_lo(vq[q]), dot);
+                        dot = fmaf(hi, bf16_hi(vq[q]), dot);
+                        o[q] = pack_bf16(w * lo, w * hi);
+                    }
+                    if (c0 + 32 * u < a.pieces) __stcs(gy + c0 + 32 * u, make_uint4(o[0], o[1], o[2], o[3]));
+                }
+            }
+            dot = warp_sum(dot);
+        }
+        if (lane == 0 && a.grad_weights != nullptr) a.grad_weights[i] = dot;
+    }
+    // rows that no slot points to
+    if (a.total != nullptr && i < a.rows && (int64_t)i >= (int64_t)*a.total) {
+        uint4* gy = reinterpret_cast<uint4*>(a.grad_y) + i * a.pieces;
+        for (uint32_t c = lane; c < a.pieces; c += 32) gy[c] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+bool combine_sizes_ok(uint64_t rows, uint64_t hidden, uint64_t tokens, uint32_t top_k)
+{
+    return top_k >= 1 && top_k <= ZCCL_MAX_TOP_K && tokens < (1ull << 31) / top_k && rows < (1ull << 31) &&
+           hidden % 8 == 0 && hidden < (1ull << 24) && rows * hidden < kMaxElems && tokens * hidden < kMaxElems;
+}
+
+template <typename... A>
+cudaError_t launch_plain(void (*kernel)(A...), uint64_t grid, cudaStream_t stream, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((uint32_t)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+
+}  // namespace zccl
+
+using namespace zccl;
+
+extern "C" {
+
+zccl_status_t zccl_combine(const uint16_t* d_y, uint64_t rows, uint64_t hidden, const int32_t* d_pos,
+                           const float* d_weights, uint64_t tokens, uint32_t top_k, uint16_t* d_out,
+                           cudaStream_t stream)
+{
+    if (!combine_sizes_ok(rows, hidden, tokens, top_k) || !is_aligned(d_weights, 4)) return ZCCL_ERR_INVALID_ARG;
+    if (tokens == 0 || hidden == 0) return ZCCL_OK;
+    if ((rows > 0 && d_y == nullptr) || !is_aligned(d_y, 16) || !good_ptr(d_pos, 4) || !good_ptr(d_out, 16))
+        return ZCCL_ERR_INVALID_ARG;
+    CombineArgs a{};
+    a.y = d_y;
+    a.rows = rows;
+    a.pieces = (uint32_t)(hidden / 8);
+    a.pos = d_pos;
+    a.weights = d_weights;
+    a.tokens = tokens;
+    a.K = top_k;
+    a.out = d_out;
+    uint32_t lanes = 32;
+    while (lanes < kThreads && lanes < a.pieces) lanes *= 2;
+    const uint32_t per_cta = kThreads / lanes;
+    return launched(launch_plain(combine_kernel, (tokens + per_cta - 1) / per_cta, stream, a, lanes));
+}
+
+zccl_status_t zccl_combine_backward(const uint16_t* d_grad_out, const uint16_t* d_y, uint64_t rows, uint64_t hidden,
+                                    const int32_t* d_pos, const float* d_weights, const int32_t* d_total,
+                                    uint64_t tokens, uint32_t top_k, uint16_t* d_grad_y, float* d_grad_weights,
+                                    cudaStream_t stream)
+{
+    if (!combine_sizes_ok(rows, hidden, tokens, top_k) || !is_aligned(d_weights, 4) || !is_aligned(d_total, 4) ||
+        !is_aligned(d_y, 16) || !is_aligned(d_grad_y, 16) || !is_aligned(d_grad_weights, 4) ||
+        (d_grad_weights != nullptr && rows > 0 && hidden > 0 && d_y == nullptr))
+        return ZCCL_ERR_INVALID_ARG;
+    if (tokens > 0 && (!good_ptr(d_pos, 4) || (hidden > 0 && !good_ptr(d_grad_out, 16)))) return ZCCL_ERR_INVALID_ARG;
+    if (rows > 0 && hidden > 0 && d_grad_y == nullptr) return ZCCL_ERR_INVALID_ARG;
+    const uint64_t slots = tokens * top_k, items = slots > rows ? slots : rows;
+    if (items == 0) return ZCCL_OK;
+    CombineArgs a{};
+    a.y = d_grad_weights != nullptr ? d_y : nullptr;
+    a.rows = rows;
+    a.pieces = (uint32_t)(hidden / 8);
+    a.pos = d_pos;
+    a.weights = d_weights;
+    a.tokens = tokens;
+    a.K = top_k;
+    a.grad_out = d_grad_out;
+    a.total = d_total;
+    a.grad_y = d_grad_y;
+    a.grad_weights = d_grad_weights;
+    return launched(launch_plain(combine_backward_kernel, (items + kThreads / 32 - 1) / (kThreads / 32), stream, a));
+}
+
+}  // extern "C"
