@@ -425,6 +425,65 @@ zccl_status_t zccl_combine_backward(const uint16_t* d_grad_out, const uint16_t* 
                                     const int32_t* d_total, uint64_t tokens, uint32_t top_k,
                                     uint16_t* d_grad_y, float* d_grad_weights, cudaStream_t stream);
 
+/* ---- block-scaled e4m3 layers: the experts' products --------------------------
+ *
+ * y = x W^T by groups of rows (an expert's; one group: a dense layer), both
+ * factors in e4m3 with a scale for each block of 128.  A block of values v with
+ * largest magnitude m (counted as at least 2^-100) is held as the codes
+ * rne(v * (448 * (1 / m))), saturated at 448, and the scale m / 448, every
+ * operation rounded in fp32:
+ *   x        a block is 128 consecutive values of a row
+ *   W        a block is 128 x 128 values; the last blocks of an axis may be cut
+ * and y[r][n] = sum over blocks b of (sx[r][b] sw[n/128][b]) (sum of the block's
+ * code products), added in fp32 and rounded once.  The gradients are
+ *   dx = dy W, with dy quantised by rows as x is, and
+ *   dW = dy^T x, summed over a group's rows: there the blocks of both factors
+ *        are 128 consecutive rows of the group, column by column.
+ * A row (column, for dW) that holds a NaN or an infinity gives NaN; the others
+ * are not touched by it.
+ * Extents: 1 <= k, n < 2^24, rows < 2^31 and at most 2^31 blocks an operand. */
+
+/* Bytes of a packed weight of `groups` matrices [n][k].  The packed form
+ * depends on n and k and is good for any number of calls. */
+zccl_status_t zccl_fp8_weight_bytes(uint32_t groups, uint64_t n, uint64_t k, uint64_t* bytes);
+
+/* Quantise and pack a weight (BF16 or fp32 [groups][n][k], contiguous): d_weight
+ * for zccl_fp8_linear (zccl_fp8_weight_bytes(groups, n, k)) and d_weight_t, the
+ * same codes with exchanged axes, for zccl_fp8_linear_backward
+ * (zccl_fp8_weight_bytes(groups, k, n)); either may be NULL.  16-byte aligned. */
+zccl_status_t zccl_fp8_weight_quantize(const void* d_w, int dtype, uint32_t groups, uint64_t n, uint64_t k,
+                                       void* d_weight, void* d_weight_t, cudaStream_t stream);
+
+/* The same from e4m3 codes [groups][n][k] and scales [groups][n/128][k/128]
+ * (extents rounded up), e.g. a checkpoint's. */
+zccl_status_t zccl_fp8_weight_pack(const void* d_codes, const float* d_scale, uint32_t groups, uint64_t n,
+                                   uint64_t k, void* d_weight, void* d_weight_t, cudaStream_t stream);
+
+/* Workspace of zccl_fp8_linear (backward = 0) or zccl_fp8_linear_backward; its
+ * contents before a call do not matter. */
+zccl_status_t zccl_fp8_linear_workspace_bytes(uint64_t rows, uint64_t k, uint64_t n, uint32_t groups, int backward,
+                                              uint64_t* bytes);
+
+/* d_out [rows][n] (out_dtype) = d_x [rows] of k values, `stride` elements apart,
+ * times the packed weight.  d_offsets: device int32 [groups + 1], non-decreasing
+ * from 0: group g has rows d_offsets[g] .. d_offsets[g+1] - 1 (a dispatch's
+ * d_offsets); rows after the last group's get zeros.  NULL with one group: all
+ * rows.  d_status gets ZCCL_ERR_TIMEOUT if a device wait ran out. */
+zccl_status_t zccl_fp8_linear(const void* d_x, int dtype, uint64_t stride, uint64_t rows, uint64_t k,
+                              const void* d_weight, uint64_t n, uint32_t groups, const int32_t* d_offsets,
+                              void* d_out, int out_dtype, void* d_ws, uint64_t ws_bytes, uint32_t* d_status,
+                              cudaStream_t stream);
+
+/* Gradients of zccl_fp8_linear: d_grad_x [rows][k] (rows after the last group's
+ * zero) and d_grad_w [groups][n][k] (zero for a group without rows); either may
+ * be NULL.  d_grad: [rows] of n values; d_x: the layer's input (read for d_grad_w
+ * only); both of type dtype. */
+zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int dtype, uint64_t grad_stride,
+                                       uint64_t x_stride, uint64_t rows, uint64_t k, const void* d_weight_t,
+                                       uint64_t n, uint32_t groups, const int32_t* d_offsets, void* d_grad_x,
+                                       void* d_grad_w, int out_dtype, void* d_ws, uint64_t ws_bytes,
+                                       uint32_t* d_status, cudaStream_t stream);
+
 /* Static text for a status code. */
 const char* zccl_status_string(zccl_status_t status);
 

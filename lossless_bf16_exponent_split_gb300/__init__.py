@@ -11,7 +11,8 @@ fallback -- if ``libzccl.so`` is missing, every call raises.
 
 ``Codec`` is a convenience layer over the same calls that allocates buffers
 with PyTorch (device memory and streams only); ``Moe`` does the same for the
-calls around a mixture-of-experts all-to-all.
+calls around a mixture-of-experts all-to-all, ``BlockFp8`` for the experts'
+products.
 """
 from __future__ import annotations
 
@@ -95,6 +96,22 @@ _SIGS = {
     "zccl_combine_backward": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p,
                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p,
                                ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "zccl_fp8_weight_bytes": ([ctypes.c_uint32, ctypes.c_uint64, ctypes.c_uint64, ctypes.POINTER(ctypes.c_uint64)],
+                              ctypes.c_int),
+    "zccl_fp8_weight_quantize": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_uint64,
+                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "zccl_fp8_weight_pack": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_uint64,
+                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "zccl_fp8_linear_workspace_bytes": ([ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint32,
+                                         ctypes.c_int, ctypes.POINTER(ctypes.c_uint64)], ctypes.c_int),
+    "zccl_fp8_linear": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64,
+                         ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p,
+                         ctypes.c_int, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p],
+                        ctypes.c_int),
+    "zccl_fp8_linear_backward": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_uint64,
+                                  ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_uint64,
+                                  ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                  ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
     "zccl_status_string": ([ctypes.c_int], ctypes.c_char_p),
 }
 
@@ -306,6 +323,40 @@ def zccl_combine_backward(d_grad_out, d_y, rows, hidden, d_pos, d_weights, d_tot
                                        d_grad_y, d_grad_weights, stream)
 
 
+def zccl_fp8_weight_bytes(groups: int, n: int, k: int) -> int:
+    out = ctypes.c_uint64(0)
+    check(lib().zccl_fp8_weight_bytes(groups, n, k, ctypes.byref(out)), "zccl_fp8_weight_bytes")
+    return int(out.value)
+
+
+def zccl_fp8_weight_quantize(d_w, dtype, groups, n, k, d_weight, d_weight_t, stream) -> int:
+    return lib().zccl_fp8_weight_quantize(d_w, dtype, groups, n, k, d_weight, d_weight_t, stream)
+
+
+def zccl_fp8_weight_pack(d_codes, d_scale, groups, n, k, d_weight, d_weight_t, stream) -> int:
+    return lib().zccl_fp8_weight_pack(d_codes, d_scale, groups, n, k, d_weight, d_weight_t, stream)
+
+
+def zccl_fp8_linear_workspace_bytes(rows: int, k: int, n: int, groups: int, backward: bool) -> int:
+    out = ctypes.c_uint64(0)
+    check(lib().zccl_fp8_linear_workspace_bytes(rows, k, n, groups, 1 if backward else 0, ctypes.byref(out)),
+          "zccl_fp8_linear_workspace_bytes")
+    return int(out.value)
+
+
+def zccl_fp8_linear(d_x, dtype, stride, rows, k, d_weight, n, groups, d_offsets, d_out, out_dtype, d_ws, ws_bytes,
+                    d_status, stream) -> int:
+    """y = x W^T by groups of rows, both factors in e4m3 with a scale per block of 128."""
+    return lib().zccl_fp8_linear(d_x, dtype, stride, rows, k, d_weight, n, groups, d_offsets, d_out, out_dtype, d_ws,
+                                 ws_bytes, d_status, stream)
+
+
+def zccl_fp8_linear_backward(d_grad, d_x, dtype, grad_stride, x_stride, rows, k, d_weight_t, n, groups, d_offsets,
+                             d_grad_x, d_grad_w, out_dtype, d_ws, ws_bytes, d_status, stream) -> int:
+    return lib().zccl_fp8_linear_backward(d_grad, d_x, dtype, grad_stride, x_stride, rows, k, d_weight_t, n, groups,
+                                          d_offsets, d_grad_x, d_grad_w, out_dtype, d_ws, ws_bytes, d_status, stream)
+
+
 def zccl_status_string(status: int) -> str:
     return lib().zccl_status_string(status).decode()
 
@@ -324,6 +375,7 @@ def check(status: int, what: str) -> None:
 
 from .codec import Codec  # noqa: E402  (torch-based convenience layer)
 from .moe import Dispatch, Moe  # noqa: E402
+from .fp8 import BlockFp8, Fp8Weight  # noqa: E402
 
 __all__ = [n for n in list(globals()) if n.startswith("zccl_")] + [
-    "Codec", "Dispatch", "Moe", "ZcclError", "check", "lib", "status_string"]
+    "BlockFp8", "Codec", "Dispatch", "Fp8Weight", "Moe", "ZcclError", "check", "lib", "status_string"]
