@@ -34,19 +34,17 @@ namespace {
 
 constexpr uint32_t kTileM = 128;
 constexpr uint32_t kTileN = 256;
-constexpr uint32_t kStages = 4;
+constexpr uint32_t kStages = 3;
 constexpr uint32_t kABytes = kTileM * kFp8Block, kBBytes = kTileN * kFp8Block;
 constexpr uint32_t kScaleSlots = 6;
 constexpr uint32_t kScaleLag = 4;      // a block's scales are reported this many blocks after their copies are issued
-constexpr uint32_t kOutBytes = 64;     // bytes of a staged output row
-constexpr uint32_t kOutPitch = kOutBytes + 16;  // 16 more, against bank conflicts
-constexpr uint32_t kThreads = 384;     // warps 0..3: load, issue, idle, scales; 4..11: two warpgroups that add
+constexpr uint32_t kSumWarps = 8;      // warps that add, two to 32 rows of a tile
+constexpr uint32_t kSumCols = 128;     // columns of one of them
+constexpr uint32_t kThreads = 128 + 32 * kSumWarps;  // warps 0..3: load, issue, schedule, scales; then those that add
 constexpr uint32_t kTmemColumns = 2 * kTileN;
 constexpr uint32_t kBandRows = 8;      // tiles of a band share their weight columns in L2
-// registers: 384 threads x 168 at launch = 128 x 104 + 256 x 200; with another split, or
-// wider pieces out of tensor memory, registers spill, and a spilled register's
-// reload misses the little L1 that is left: it cost a block 1000 cycles
-constexpr int kRegsFew = 104, kRegsMany = 200;
+// registers: 384 threads x 168 at launch = 128 x 56 + 256 x 224
+constexpr int kRegsFew = 56, kRegsMany = 224;
 
 struct TileArgs {
     const float* sa;
@@ -54,28 +52,34 @@ struct TileArgs {
     const int32_t* offsets;
     uint32_t rows, m, n, KB, G, blocks;
     void* out;
+    int tma_out;           // whether the output has a tensor map
     uint32_t* status;
 };
 
+// One output tile, as the scheduling warp hands it to the others.
+struct alignas(16) Tile {
+    uint32_t m0, n0;       // first row (of the output, within its group for a weight gradient) and column
+    uint32_t row_end;      // rows of the tile end here
+    uint32_t blocks;       // blocks of the reduction; kNoTile: there are no more tiles
+    uint32_t a0, b0;       // first operand rows
+    uint32_t sa0, sb0;     // first scales
+    uint32_t g, pad[3];    // group
+};
+constexpr uint32_t kNoTile = 0xFFFFFFFFu;
+constexpr uint32_t kTileSlots = 4;
+constexpr uint32_t kTileReaders = 3 + kSumWarps;  // warps that read a tile
+
 struct Smem {
-    alignas(16) uint8_t out[8][32 * kOutPitch];        // by warp: 32 rows of a finished tile
+    alignas(1024) uint8_t out[kSumWarps][2][32 * 128];  // by warp, twice: 32 rows of 128 bytes of a finished tile, swizzled
     alignas(16) float row_scale[kScaleSlots][kTileM];
     alignas(16) float col_scale[kScaleSlots][kTileN];  // weight gradient: by column; else one per 128 columns
-    uint64_t full[kStages], empty[kStages], done[2], taken[2], drain;
+    Tile tile[kTileSlots];
+    uint64_t full[kStages], empty[kStages], told[kTileSlots], read[kTileSlots], done[2], drain;
     uint32_t tmem;
     uint32_t prefix[kMaxGroupsFp8 + 1];
 };
 constexpr uint32_t kSmemBytes = 1024 + kStages * (kABytes + kBBytes) + sizeof(Smem);
 static_assert(kSmemBytes <= 232448, "fits the shared memory of a CTA");
-
-// One output tile.
-struct Tile {
-    uint32_t g, m0, n0;    // group, first row (of the output) and column
-    uint32_t row_end;      // rows of the tile end here
-    uint32_t blocks;       // blocks of the reduction
-    uint32_t a0, a_step;   // operand rows: a0 + block * a_step
-    uint32_t b0, b_step;
-};
 
 // kWgrad = false: tiles of group g are its blocks of 128 rows (prefix) by
 // columns; the blocks after the last group's are the rows outside every group.
@@ -124,13 +128,13 @@ __device__ __forceinline__ Tile tile_at(const TileArgs& a, const uint32_t* prefi
     c.m0 = lo + (band * kBandRows + in_band - col * height) * kTileM;
     c.n0 = col * kTileN;
     if (kWgrad) {
-        c.a_step = a.m;
-        c.b_step = a.n;
-        c.a0 = prefix[c.g] * a.m + c.m0;
-        c.b0 = prefix[c.g] * a.n + c.n0;
+        c.sa0 = prefix[c.g] * a.m;
+        c.sb0 = prefix[c.g] * a.n;
+        c.a0 = c.sa0 + c.m0;
+        c.b0 = c.sb0 + c.n0;
     } else {
-        c.a_step = a.rows;
-        c.b_step = a.n;
+        c.sa0 = 0;
+        c.sb0 = c.g * (uint32_t)blocks_of(a.n) * a.KB;
         c.a0 = c.m0;
         c.b0 = c.g * a.KB * a.n + c.n0;
     }
@@ -138,77 +142,99 @@ __device__ __forceinline__ Tile tile_at(const TileArgs& a, const uint32_t* prefi
 }
 
 // Waits for a phase, a whole warp at once: the vote makes the result uniform,
-// so that no lane can leave the others behind.  Reading the timer takes longer
-// than a phase, so the timed wait comes after many untimed tries.  After a
-// timeout the CTA's roles run out without waiting for one another.
+// so that no lane can leave the others behind.  The clock is read every 256
+// tries only, and the loop is short: the waits are inlined in many places, and
+// the kernel's code has to stay in the instruction cache.  After a timeout the
+// CTA's roles run out without waiting for one another.
+constexpr int64_t kWaitCycles = 2000000000;  // about a second
+
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t phase, uint32_t* status)
 {
+    const int64_t t0 = clock64();
 #pragma unroll 1
-    for (uint32_t i = 0; i < 1024; ++i)
+    for (uint32_t i = 0;; ++i) {
         if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, phase))) return true;
-    const uint64_t t0 = globaltimer();
-#pragma unroll 1
-    for (;;) {
-        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, phase))) return true;
-        if (__any_sync(0xFFFFFFFFu, globaltimer() - t0 > kSpinTimeoutNs)) break;
+        if ((i & 255) == 255 && __any_sync(0xFFFFFFFFu, clock64() - t0 > kWaitCycles)) break;
     }
     report(status, ZCCL_ERR_TIMEOUT);
     return false;
 }
 
-// Waits for two phases: one vote and no taken branch where both are there.
-__device__ __forceinline__ bool wait_both(uint64_t* bar0, uint32_t phase0, uint64_t* bar1, uint32_t phase1, uint32_t* status)
-{
-    const bool t0 = mbar_try_wait(bar0, phase0), t1 = mbar_try_wait(bar1, phase1);
-    if (__builtin_expect(__all_sync(0xFFFFFFFFu, t0 && t1), 1)) return true;
-    return wait_phase(bar0, phase0, status) && wait_phase(bar1, phase1, status);
-}
-
-// The sums of a warp's 32 rows x 128 columns (lane = row, columns acc[0..127])
-// to the output rows at out, columns n..n_end, `rows` of them inside the
-// output, through the warp's staging buffer.
+// The sums of a warp's 32 rows x 128 columns (lane = row) to the output, from
+// row `row` (of `rows` inside the output, counted from there) and column n on,
+// through the warp's two staging buffers in turn: rows of 128 bytes whose 16-byte
+// pieces are XOR-swizzled with the row.  A whole box goes by one asynchronous TMA
+// store that runs beside the next tile (all CTAs end their tiles together: stored
+// by the threads, a tile's 64 KB took 4000 cycles); cut rows go by the threads.
 template <typename T>
-__device__ __forceinline__ void store_rows(uint8_t* buf, T* out, uint64_t pitch, uint32_t rows, uint32_t n, uint32_t n_end,
-                                           const float (&acc)[128])
+__device__ __forceinline__ void store_rows(uint8_t (&bufs)[2][32 * 128], const CUtensorMap* map, int tma, T* out,
+                                           uint64_t row, uint32_t rows, uint32_t n, uint32_t n_end, uint32_t* turn,
+                                           const float (&acc)[kSumCols])
 {
-    constexpr uint32_t kCols = kOutBytes / sizeof(T);  // columns of a staged row
-    constexpr uint32_t kPer = 16 / sizeof(T);    // columns of a store
+    constexpr uint32_t kCols = 128 / sizeof(T);  // columns of a staged row
+    constexpr uint32_t kPer = 16 / sizeof(T);    // columns of a piece
     const uint32_t lane = threadIdx.x & 31;
-    const bool vec = ((uintptr_t)out & 15) == 0 && (pitch * sizeof(T)) % 16 == 0;
 #pragma unroll
-    for (uint32_t h = 0; h < 128; h += kCols) {
+    for (uint32_t h = 0; h < kSumCols; h += kCols) {
+        if (n + h >= n_end) break;
+        uint8_t* buf = bufs[*turn & 1];
+        if (lane == 0) bulk_wait_read1();  // the buffer's last store: all but the other buffer's, the latest
+        __syncwarp();
 #pragma unroll
-        for (uint32_t i = 0; i < kCols; i += kPer) {
-            const float* x = &acc[h + i];
+        for (uint32_t p = 0; p < 8; ++p) {
+            const float* x = &acc[h + p * kPer];
             uint4 v;
             if (sizeof(T) == 2)
                 v = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4 % kPer], x[5 % kPer]),
                                pack_bf16(x[6 % kPer], x[7 % kPer]));
             else
                 v = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-            *reinterpret_cast<uint4*>(buf + lane * kOutPitch + i * sizeof(T)) = v;
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((p ^ (lane & 7)) * 16)) = v;
         }
-        __syncwarp();
-        if (vec) {  // an end of the output within a store is impossible: its width is a multiple of kPer
-            const uint32_t r0 = lane >> 2, c = (lane & 3) * kPer;
-            T* to = out + r0 * pitch + n + h + c;
-            const uint8_t* from = buf + r0 * kOutPitch + c * sizeof(T);
-            const bool in = n + h + c < n_end;
-#pragma unroll
-            for (uint32_t r = 0; r < 32; r += 8) {
-                const uint4 v = *reinterpret_cast<const uint4*>(from + r * kOutPitch);
-                if (in && r0 + r < rows) *reinterpret_cast<uint4*>(to + r * pitch) = v;
+        if (tma && rows >= 32) {
+            ++*turn;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(map, buf, (int32_t)(n + h), (int32_t)row);
+                bulk_commit();
             }
-        } else {  // a value at a time, consecutive lanes consecutive columns
+            __syncwarp();
+        } else if (tma) {  // cut rows, in whole pieces: the output's width is a multiple of a piece's
+            __syncwarp();
+            const uint32_t p = lane & 7;
+            T* to = out + (row + (lane >> 3)) * n_end + n + h + p * kPer;
 #pragma unroll 1
+            for (uint32_t r = lane >> 3; r < 32; r += 4, to += 4 * (uint64_t)n_end)
+                if (r < rows && n + h + p * kPer < n_end)
+                    *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(buf + r * 128 + ((p ^ (r & 7)) * 16));
+            __syncwarp();
+        } else {  // a value at a time, consecutive lanes consecutive columns
+            __syncwarp();
+            const uint32_t cols = min(kCols, n_end - n - h);
+            T* to = out + row * n_end + n + h;
+#pragma unroll 4
             for (uint32_t i = lane; i < 32 * kCols; i += 32) {
                 const uint32_t r = i / kCols, j = i % kCols;
-                if (r < rows && n + h + j < n_end)
-                    out[r * pitch + n + h + j] = *reinterpret_cast<const T*>(buf + r * kOutPitch + j * sizeof(T));
+                if (r < rows && j < cols)
+                    to[(uint64_t)r * n_end + j] =
+                        reinterpret_cast<const T*>(buf + r * 128 + (((j / kPer) ^ (r & 7)) * 16))[j % kPer];
             }
+            __syncwarp();
         }
-        __syncwarp();
     }
+}
+
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // Four bytes to shared memory, asynchronously.
@@ -224,9 +250,23 @@ __device__ __forceinline__ void arrive_lane0(uint64_t* bar, uint32_t lane)
                  : "memory");
 }
 
+// The next tile, copied out of its slot by a whole warp; false at the end (or
+// after a timeout).
+__device__ __forceinline__ bool next_tile(Smem* s, uint32_t* k, Tile* c, uint32_t lane, uint32_t* status)
+{
+    const uint32_t slot = *k % kTileSlots;
+    if (!wait_phase(&s->told[slot], (*k / kTileSlots) & 1, status)) return false;
+    *c = s->tile[slot];
+    __syncwarp();
+    arrive_lane0(&s->read[slot], lane);
+    ++*k;
+    return c->blocks != kNoTile;
+}
+
 template <bool kWgrad, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
-    gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, TileArgs a)
+    gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                const __grid_constant__ CUtensorMap map_out, TileArgs a)
 {
     extern __shared__ uint8_t raw[];
     uint8_t* ring = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
@@ -235,12 +275,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < kStages; ++i) {
-            mbar_init(&s->full[i], 1);
+            mbar_init(&s->full[i], 1 + kSumWarps);  // the operands, and the accumulator's release
             mbar_init(&s->empty[i], 1);
+        }
+        for (uint32_t i = 0; i < kTileSlots; ++i) {
+            mbar_init(&s->told[i], 1);
+            mbar_init(&s->read[i], kTileReaders);
         }
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(&s->done[i], 1 + 32);  // the products' commit, and the warp that brought the scales
-            mbar_init(&s->taken[i], 8);
         }
         mbar_init(&s->drain, 1);
         fence_mbar_init();
@@ -255,28 +298,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s->tmem;
-    uint32_t tail0 = a.rows;
-    if (!kWgrad && a.offsets != nullptr) {
-        const int32_t t = ld_l2(a.offsets + a.G);
-        tail0 = t < 0 ? 0u : min((uint32_t)t, a.rows);
-    }
-    const uint32_t tiles = tile_count<kWgrad>(a, s->prefix, tail0);
 
     if (warp < 4) {
         regs_fewer<kRegsFew>();
+        Tile c;
+        uint32_t k = 0;
+        bool ok = true;
         if (warp == 0) {
             // ---- operand tiles into the ring
+            const uint32_t a_step = kWgrad ? a.m : a.rows, b_step = a.n;
             uint32_t stage = 0, phase = 0;
-            bool ok = true;
-            for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                const Tile c = tile_at<kWgrad>(a, s->prefix, tail0, t);
+            while (ok && next_tile(s, &k, &c, lane, a.status)) {
                 for (uint32_t b = 0; b < c.blocks; ++b) {
                     if (!(ok = wait_phase(&s->empty[stage], phase ^ 1, a.status))) break;
                     if (lane == 0) {
                         uint8_t* at = ring + stage * (kABytes + kBBytes);
                         mbar_arrive_expect_tx(&s->full[stage], kABytes + kBBytes);
-                        tma_load_2d(at, &map_a, 0, (int32_t)(c.a0 + b * c.a_step), &s->full[stage]);
-                        tma_load_2d(at + kABytes, &map_b, 0, (int32_t)(c.b0 + b * c.b_step), &s->full[stage]);
+                        tma_load_2d(at, &map_a, 0, (int32_t)(c.a0 + b * a_step), &s->full[stage]);
+                        tma_load_2d(at + kABytes, &map_b, 0, (int32_t)(c.b0 + b * b_step), &s->full[stage]);
                     }
                     __syncwarp();
                     if (++stage == kStages) stage = 0, phase ^= 1;
@@ -294,51 +333,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++stage == kStages) stage = 0, phase ^= 1;
             }
         } else if (warp == 1) {
-            // ---- matrix instructions
-            uint32_t count = 0;
-            bool ok = true;
+            // ---- matrix instructions.  What the warp does between two blocks has to fit beside those it has
+            // queued, so it waits on one barrier: a block's operands and its accumulator's release arrive together
             constexpr uint32_t idesc = instr_desc(kTileM, kTileN);
-            for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                const uint32_t end = count + tile_at<kWgrad>(a, s->prefix, tail0, t).blocks;
-                for (; count < end; ++count) {
-                    const uint32_t stage = count % kStages, buf = count & 1;
-                    if (!(ok = wait_both(&s->taken[buf], ((count >> 1) & 1) ^ 1, &s->full[stage], (count / kStages) & 1,
-                                         a.status)))
+            const uint64_t desc0 = smem_desc(smem_addr(ring));
+            uint32_t stage = 0, phase = 0, buf = 0;
+            while (ok && next_tile(s, &k, &c, lane, a.status)) {
+                const uint32_t blocks = __shfl_sync(0xFFFFFFFFu, c.blocks, 0);
+#pragma unroll 1
+                for (uint32_t b = 0; b < blocks; ++b) {
+                    if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&s->full[stage], phase)) &&
+                        !(ok = wait_phase(&s->full[stage], phase, a.status)))
                         break;
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t at = smem_addr(ring) + stage * (kABytes + kBBytes);
-                        const uint64_t da = smem_desc(at), db = smem_desc(at + kABytes);
-#pragma unroll
-                        for (uint32_t k = 0; k < kFp8Block / 32; ++k)
-                            mma_e4m3(tmem + buf * kTileN, da + 2 * k, db + 2 * k, idesc, k > 0);
-                        mma_commit(&s->done[buf]);
-                    }
-                    __syncwarp();
+                    const uint64_t da = desc0 + stage * ((kABytes + kBBytes) >> 4);
+                    mma_block_e4m3(tmem + buf * kTileN, da, da + (kABytes >> 4), idesc, &s->done[buf]);
+                    if (++stage == kStages) stage = 0, phase ^= 1;
+                    buf ^= 1;
                 }
             }
             if (!ok) {  // the accumulators are freed below: let the instructions issued so far end
-                if (lane == 0) mma_commit(&s->drain);
-                __syncwarp();
+                mma_commit(&s->drain);
                 mbar_wait(&s->drain, 0);
                 __syncwarp();
             }
-        } else if (warp == 3) {
+        } else if (warp == 2) {
+            // ---- the tiles, in an order of their own for each CTA
+            uint32_t tail0 = a.rows;
+            if (!kWgrad && a.offsets != nullptr) {
+                const int32_t t = ld_l2(a.offsets + a.G);
+                tail0 = t < 0 ? 0u : min((uint32_t)t, a.rows);
+            }
+            const uint32_t tiles = tile_count<kWgrad>(a, s->prefix, tail0);
+            for (uint32_t t = blockIdx.x;; t += gridDim.x, ++k) {
+                const uint32_t slot = k % kTileSlots;
+                if (t < tiles)
+                    c = tile_at<kWgrad>(a, s->prefix, tail0, t);
+                else
+                    c.blocks = kNoTile;
+                if (!wait_phase(&s->read[slot], ((k / kTileSlots) & 1) ^ 1, a.status)) break;
+                if (lane == 0) s->tile[slot] = c;
+                __syncwarp();
+                arrive_lane0(&s->told[slot], lane);
+                if (t >= tiles) break;
+            }
+        } else {
             // ---- scales: 32 threads, four rows and (weight gradient) eight columns each.  A block's slot is free
-            // once the block six before it was taken; its scales are reported four blocks later, when the block two
-            // before it is done with the barrier.
-            uint32_t count = 0, slot = 0;
-            bool ok = true;
-            for (uint32_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                const Tile c = tile_at<kWgrad>(a, s->prefix, tail0, t);
-                const uint32_t last = (kWgrad ? a.m : a.rows) - 1, nbs = (uint32_t)blocks_of(a.n);
-                const float* row = a.sa + (kWgrad ? (uint64_t)s->prefix[c.g] * a.m : 0);
-                const float* col = kWgrad ? a.sb + (uint64_t)s->prefix[c.g] * a.n
-                                          : a.sb + ((uint64_t)c.g * nbs + min(c.n0 / kFp8Block + lane, nbs - 1)) * a.KB;
+            // once the block six before it was taken, which the barrier of the block four before it says; its scales
+            // are reported four blocks later, when the block two before it is done with the barrier.
+            const uint32_t last = (kWgrad ? a.m : a.rows) - 1, nbs = (uint32_t)blocks_of(a.n);
+            uint32_t count = 0, slot = 0, stage = 2 % kStages, phase = 0;
+            while (ok && next_tile(s, &k, &c, lane, a.status)) {
+                const float* row = a.sa + c.sa0;
+                const float* col = a.sb + c.sb0 + (kWgrad ? 0 : min(c.n0 / kFp8Block + lane, nbs - 1) * a.KB);
                 for (uint32_t b = 0; b < c.blocks; ++b, ++count) {
                     if (count >= kScaleSlots) {
-                        const uint32_t old = count - kScaleSlots;
-                        if (!(ok = wait_phase(&s->taken[old & 1], (old >> 1) & 1, a.status))) break;
+                        if (!(ok = wait_phase(&s->full[stage], phase, a.status))) break;
+                        if (++stage == kStages) stage = 0, phase ^= 1;
                     }
 #pragma unroll
                     for (uint32_t j = lane; j < kTileM; j += 32) copy4_async(&s->row_scale[slot][j], row + min(c.m0 + j, last));
@@ -372,71 +423,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_more<kRegsMany>();
         // ---- sums: warpgroup wg has columns 128 wg .. 128 wg + 127, warp w of it lanes 32 w .. 32 w + 31
         const uint32_t wg = (warp - 4) >> 2, sub = warp & 3;
-        const uint32_t taddr = tmem + ((sub * 32) << 16) + wg * 128;
-        uint32_t count = 0, slot = 0;
-        bool ok = true;      // after a timeout the loops run out without waiting
-        bool there = false;  // whether the next block is known to be done
-        for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-            const Tile c = tile_at<kWgrad>(a, s->prefix, tail0, t);
-            float acc[128];
+        const uint32_t taddr = tmem + ((sub * 32) << 16) + wg * kSumCols;
+        uint32_t k = 0, count = 0, slot = 0, stage = 0, stage2 = 2 % kStages, turn = 0;
+        bool ok = true;
+        Tile c;
+        arrive_lane0(&s->full[0], lane);  // both accumulators are free for the first two blocks
+        arrive_lane0(&s->full[1], lane);
+        while (ok && next_tile(s, &k, &c, lane, a.status)) {
+            float acc[kSumCols];
 #pragma unroll
-            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+            for (uint32_t i = 0; i < kSumCols; ++i) acc[i] = 0.0f;
+            uint32_t r[2][32];   // pieces of 32 columns, one on its way while the other is added
+            bool there = false;  // whether this block is known to be done and its first piece is on its way
+            float sa = 0.0f;
 #pragma unroll 1
             for (uint32_t b = 0; b < c.blocks; ++b) {
                 const uint32_t buf = count & 1;
-                if (__builtin_expect(!there && ok, 0)) ok = wait_phase(&s->done[buf], (count >> 1) & 1, a.status);
-                // the products are done, so their stage is free
-                if (warp == 4) arrive_lane0(&s->empty[count % kStages], lane);
-                ++count;
-                __syncwarp();
-                tc_fence_after();
                 const uint32_t from = taddr + buf * kTileN;
-                uint32_t r[2][16];
-                tmem_load16(from, r[0]);
-                float sa = s->row_scale[slot][sub * 32 + lane];
-                if (!kWgrad) sa *= s->col_scale[slot][wg];
-                bool next = false;
+                if (!there) {
+                    if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&s->done[buf], (count >> 1) & 1)) &&
+                        !(ok = wait_phase(&s->done[buf], (count >> 1) & 1, a.status)))
+                        break;
+                    tc_fence_after();
+                    tmem_load32(from, r[0]);
+                    sa = s->row_scale[slot][sub * 32 + lane];
+                    if (!kWgrad) sa *= s->col_scale[slot][wg];
+                }
+                // the products are done, so their stage is free
+                if (warp == 4) arrive_lane0(&s->empty[stage], lane);
+                if (++stage == kStages) stage = 0;
+                ++count;
+                uint64_t* const free_for = &s->full[stage2];  // the accumulator's next block
+                if (++stage2 == kStages) stage2 = 0;
+                const uint32_t next_slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
+                const bool more = b + 1 < c.blocks;
+                float next_sa = 0.0f;
+                there = false;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    tmem_wait16(r[q & 1]);
-                    if (q < 7) tmem_load16(from + 16 * (q + 1), r[(q + 1) & 1]);
-                    if (q == 6) next = mbar_try_wait(&s->done[count & 1], (count >> 1) & 1);
-                    if (q == 7 && !kWgrad) {
-                        tc_fence_before();
-                        __syncwarp();
-                        arrive_lane0(&s->taken[buf], lane);
+                for (int q = 0; q < 4; ++q) {
+                    tmem_wait32(r[q & 1]);
+                    if (q < 3) tmem_load32(from + 32 * (q + 1), r[(q + 1) & 1]);
+                    if (q == 3) {
+                        if (!kWgrad) {
+                            tc_fence_before();
+                            __syncwarp();
+                            arrive_lane0(free_for, lane);
+                        }
+                        // the next block, if it is done, before the last columns of this one
+                        there = __all_sync(0xFFFFFFFFu, more && mbar_test_wait(&s->done[count & 1], (count >> 1) & 1));
+                        if (there) {
+                            tc_fence_after();
+                            tmem_load32(taddr + (count & 1) * kTileN, r[0]);
+                            next_sa = s->row_scale[next_slot][sub * 32 + lane];
+                            if (!kWgrad) next_sa *= s->col_scale[next_slot][wg];
+                        }
                     }
                     if (kWgrad) {
-                        const float4* col = reinterpret_cast<const float4*>(&s->col_scale[slot][wg * 128 + 16 * q]);
+                        const float4* col = reinterpret_cast<const float4*>(&s->col_scale[slot][wg * kSumCols + 32 * q]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 8; ++i) {
                             const float4 f = col[i];
                             // the scales first: their product overflows only where the sum does
-                            const float x[4] = {f.x * sa, f.y * sa, f.z * sa, f.w * sa};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                acc[16 * q + 4 * i + j] =
-                                    fmaf(__uint_as_float(r[q & 1][4 * i + j]), x[j], acc[16 * q + 4 * i + j]);
+                            const float2 x0 = mul2(f.x, f.y, sa), x1 = mul2(f.z, f.w, sa);
+                            float* to = &acc[32 * q + 4 * i];
+                            const uint32_t* from_r = &r[q & 1][4 * i];
+                            fma2(to[0], to[1], __uint_as_float(from_r[0]), __uint_as_float(from_r[1]), x0.x, x0.y);
+                            fma2(to[2], to[3], __uint_as_float(from_r[2]), __uint_as_float(from_r[3]), x1.x, x1.y);
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[16 * q + i] = fmaf(__uint_as_float(r[q & 1][i]), sa, acc[16 * q + i]);
+                        for (int i = 0; i < 32; i += 2)
+                            fma2(acc[32 * q + i], acc[32 * q + i + 1], __uint_as_float(r[q & 1][i]),
+                                 __uint_as_float(r[q & 1][i + 1]), sa, sa);
                     }
                 }
                 if (kWgrad) {  // the column scales are read to the end
                     tc_fence_before();
                     __syncwarp();
-                    arrive_lane0(&s->taken[buf], lane);
+                    arrive_lane0(free_for, lane);
                 }
-                there = __all_sync(0xFFFFFFFFu, next);
-                if (++slot == kScaleSlots) slot = 0;
+                sa = next_sa;
+                slot = next_slot;
             }
-            const uint32_t row = c.m0 + sub * 32, n = c.n0 + wg * 128;
-            if (ok && row < c.row_end && n < a.n) {
-                const uint64_t at = ((kWgrad ? (uint64_t)c.g * a.m : 0) + row) * a.n;
-                store_rows(s->out[warp - 4], reinterpret_cast<T*>(a.out) + at, a.n, c.row_end - row, n, a.n, acc);
-            }
+            const uint32_t row = c.m0 + sub * 32, n = c.n0 + wg * kSumCols;
+            if (ok && row < c.row_end && n < a.n)
+                store_rows(s->out[warp - 4], &map_out, a.tma_out, reinterpret_cast<T*>(a.out),
+                           (kWgrad ? (uint64_t)c.g * a.m : 0) + row, c.row_end - row, n, a.n, &turn, acc);
         }
+        if (lane == 0) bulk_wait0();
     }
     __syncwarp();
     tc_fence_before();
@@ -466,27 +540,36 @@ EncodeTiled encoder()
     return reinterpret_cast<EncodeTiled>(f);
 }
 
-// Rows of 128 codes; a box is `box` of them, swizzled.  Boxes that reach past
-// the last row read zeros there.
-bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box)
+// A matrix of `rows` rows of `cols` elements, contiguous; a box is 128 bytes of
+// each of `box` rows, swizzled.  Boxes that reach past the matrix read zeros
+// there and write nothing.
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, uint32_t size, const void* base, uint64_t cols, uint64_t rows,
+              uint32_t box)
 {
     const EncodeTiled encode = encoder();
     if (encode == nullptr) return false;
-    const cuuint64_t dims[2] = {kFp8Block, rows};
-    const cuuint64_t strides[1] = {kFp8Block};
-    const cuuint32_t boxes[2] = {kFp8Block, box};
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {cols * size};
+    const cuuint32_t boxes[2] = {128 / size, box};
     const cuuint32_t steps[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, boxes, steps,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, type, 2, const_cast<void*>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
 }
 
 template <bool kWgrad, typename T>
-cudaError_t launch_tiles(const TileArgs& a, const uint8_t* qa, uint64_t rows_a, const uint8_t* qb, uint64_t rows_b,
-                         uint64_t most_tiles, int sms, cudaStream_t stream)
+cudaError_t launch_tiles(TileArgs a, const uint8_t* qa, uint64_t rows_a, const uint8_t* qb, uint64_t rows_b,
+                         uint64_t rows_out, uint64_t most_tiles, int sms, cudaStream_t stream)
 {
-    CUtensorMap map_a, map_b;
-    if (!make_map(&map_a, qa, rows_a, kTileM) || !make_map(&map_b, qb, rows_b, kTileN)) return cudaErrorUnknown;
+    CUtensorMap map_a, map_b, map_out = {};
+    if (!make_map(&map_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, qa, kFp8Block, rows_a, kTileM) ||
+        !make_map(&map_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, qb, kFp8Block, rows_b, kTileN))
+        return cudaErrorUnknown;
+    // the TMA wants rows that begin on 16 bytes, and coordinates in 31 bits
+    a.tma_out = (uint64_t)a.n * sizeof(T) % 16 == 0 && is_aligned(a.out, 16) && rows_out < (1ull << 31);
+    if (a.tma_out && !make_map(&map_out, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                               sizeof(T), a.out, a.n, rows_out, 32))
+        return cudaErrorUnknown;
     const cudaError_t e =
         cudaFuncSetAttribute(gemm_kernel<kWgrad, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -500,7 +583,7 @@ cudaError_t launch_tiles(const TileArgs& a, const uint8_t* qa, uint64_t rows_a, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gemm_kernel<kWgrad, T>, map_a, map_b, a);
+    return cudaLaunchKernelEx(&cfg, gemm_kernel<kWgrad, T>, map_a, map_b, map_out, a);
 }
 
 }  // namespace
@@ -520,7 +603,7 @@ cudaError_t launch_matmul(const MatmulArgs& m, int sms, cudaStream_t stream)
     a.status = m.status;
     const uint64_t most = (blocks_of(m.rows) + m.G) * ((m.n + kTileN - 1) / kTileN);
     const auto launch = m.out_f32 ? launch_tiles<false, float> : launch_tiles<false, __nv_bfloat16>;
-    return launch(a, m.a, (uint64_t)m.KB * m.rows, m.b, (uint64_t)m.G * m.KB * m.n, most, sms, stream);
+    return launch(a, m.a, (uint64_t)m.KB * m.rows, m.b, (uint64_t)m.G * m.KB * m.n, m.rows, most, sms, stream);
 }
 
 cudaError_t launch_wgrad(const WgradArgs& w, int sms, cudaStream_t stream)
@@ -538,7 +621,7 @@ cudaError_t launch_wgrad(const WgradArgs& w, int sms, cudaStream_t stream)
     a.status = w.status;
     const uint64_t most = (uint64_t)w.G * ((w.m + kTileM - 1) / kTileM) * ((w.n + kTileN - 1) / kTileN);
     const auto launch = w.out_f32 ? launch_tiles<true, float> : launch_tiles<true, __nv_bfloat16>;
-    return launch(a, w.a, (uint64_t)w.blocks * w.m, w.b, (uint64_t)w.blocks * w.n, most, sms, stream);
+    return launch(a, w.a, (uint64_t)w.blocks * w.m, w.b, (uint64_t)w.blocks * w.n, (uint64_t)w.G * w.m, most, sms, stream);
 }
 
 }  // namespace zccl

@@ -39,43 +39,81 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr)
 // Instruction descriptor: fp32 accumulator, e4m3 operands, both K-major.
 __host__ __device__ constexpr uint32_t instr_desc(uint32_t m, uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24); }
 
-// d (+)= a b over 32 values of the reduction axis.  One thread issues it.
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+// d = a b over a block of 128 values of the reduction axis (four instructions of
+// 32, 32 bytes apart in the swizzled rows), then an arrival on `bar` when they are
+// done.  A whole warp calls it, so that its operands stay in uniform registers;
+// one elected lane issues.
+__device__ __forceinline__ void mma_block_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint64_t* bar)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n .reg .pred one, add, set;\n .reg .b64 a1, b1, a2, b2, a3, b3;\n"
+        " elect.sync _|one, 0xFFFFFFFF;\n setp.eq.u32 add, 0, 0;\n setp.ne.u32 set, 0, 0;\n"
+        " add.u64 a1, %1, 2;\n add.u64 b1, %2, 2;\n add.u64 a2, %1, 4;\n add.u64 b2, %2, 4;\n"
+        " add.u64 a3, %1, 6;\n add.u64 b3, %2, 6;\n"
+        " @one tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, set;\n"
+        " @one tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, add;\n"
+        " @one tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, add;\n"
+        " @one tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, add;\n"
+        " @one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(smem_addr(bar))
         : "memory");
 }
 
 // Arrives on `bar` when the matrix instructions this thread issued so far are done.
 __device__ __forceinline__ void mma_commit(uint64_t* bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+    asm volatile(
+        "{\n .reg .pred one;\n elect.sync _|one, 0xFFFFFFFF;\n"
+        " @one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_addr(bar))
+        : "memory");
 }
 
-// 16 columns of the warp's 32 lanes of tensor memory: lane l, column i in r[i].
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16])
+// 32 columns of the warp's 32 lanes of tensor memory: lane l, column i in r[i].
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32])
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
 
 // Waits for this thread's tensor-memory loads.  The registers pass through, so
 // that no use of them can move above the wait.
-__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16])
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                  :
                  : "memory");
+}
+
+// Two fp32 values in an instruction, each rounded on its own.  At half the rate
+// of the single ones they do no more in a second, but they leave every other
+// issue slot to the warps that keep the tensor cores fed.
+__device__ __forceinline__ void fma2(float& c0, float& c1, float a0, float a1, float b0, float b1)
+{
+    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%0, %1};\n"
+        " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}"
+        : "+f"(c0), "+f"(c1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ float2 mul2(float a0, float a1, float b)
+{
+    float2 d;
+    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mul.rn.f32x2 c, a, b;\n mov.b64 {%0, %1}, c;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a0), "f"(a1), "f"(b));
+    return d;
 }
 
 // A box of a two-dimensional tensor map to shared memory, completing on `bar`.
@@ -86,6 +124,14 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
             smem_addr(dst)),
         "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(y)
         : "memory");
+}
+
+// A box of shared memory to a two-dimensional tensor map (bulk-group completion).
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t x, int32_t y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                 "r"(smem_addr(src)), "r"(x), "r"(y)
+                 : "memory");
 }
 
 template <int kRegs>
