@@ -81,6 +81,8 @@ struct QuantArgs {
     float* scale;
     const int32_t* offsets;  // along rows: the groups
     uint32_t G;
+    uint8_t* q_rows;         // along rows: also the blocks of each row, or nullptr
+    float* scale_rows;
 };
 
 struct PackArgs {
@@ -97,6 +99,8 @@ cudaError_t launch_wgrad(const WgradArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_small(const SmallArgs& a, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_quantize_rows(const QuantArgs& a, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_quantize_tokens(const QuantArgs& a, int dtype, int sms, cudaStream_t stream);
+// Whether launch_quantize_tokens can make the blocks of each row, too.
+bool quantizes_both(const QuantArgs& a, int dtype);
 cudaError_t launch_pack(const PackArgs& a, int dtype, cudaStream_t stream);
 
 }  // namespace zccl

@@ -50,7 +50,8 @@ RowsLayout tokens_layout(uint64_t at, uint64_t rows, uint64_t cols, uint32_t gro
 
 bool takes_small(uint64_t rows, uint32_t groups) { return rows <= kSmallRows * groups; }
 
-// y = x times the transpose of the packed weight [groups][n][k].
+// y = x times the transpose of the packed weight [groups][n][k].  x nullptr (and
+// not few rows): x is quantised in the workspace already.
 zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, uint64_t k, const uint8_t* weight, uint64_t n,
                      uint32_t groups, const int32_t* offsets, void* out, int out_dtype, uint8_t* ws, uint32_t* status,
                      int sms, cudaStream_t stream)
@@ -80,7 +81,7 @@ zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, u
     q.cols = (uint32_t)k;
     q.q = ws + l.q;
     q.scale = reinterpret_cast<float*>(ws + l.scale);
-    if (launch_quantize_rows(q, dtype, sms, stream) != cudaSuccess) return ZCCL_ERR_CUDA;
+    if (x != nullptr && launch_quantize_rows(q, dtype, sms, stream) != cudaSuccess) return ZCCL_ERR_CUDA;
     MatmulArgs m{};
     m.a = q.q;
     m.sa = q.scale;
@@ -194,13 +195,6 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
     const int sms = sm_count();
     if (sms == 0) return ZCCL_ERR_CUDA;
     uint8_t* ws = reinterpret_cast<uint8_t*>(d_ws);
-    if (d_grad_x != nullptr && rows > 0) {
-        const zccl_status_t st =
-            linear(d_grad, dtype, grad_stride, rows, n, reinterpret_cast<const uint8_t*>(d_weight_t), k, groups, d_offsets,
-                   d_grad_x, out_dtype, ws, d_status, sms, stream);
-        if (st != ZCCL_OK) return st;
-    }
-    if (d_grad_w == nullptr) return ZCCL_OK;
     const RowsLayout dy = rows_layout(0, rows, n), dyt = tokens_layout(dy.end, rows, n, groups),
                      xt = tokens_layout(dyt.end, rows, k, groups);
     QuantArgs q{};
@@ -212,15 +206,29 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
     q.cols = (uint32_t)n;
     q.q = ws + dyt.q;
     q.scale = reinterpret_cast<float*>(ws + dyt.scale);
+    const bool small = takes_small(rows, groups);
+    const bool both = d_grad_w != nullptr && d_grad_x != nullptr && rows > 0 && !small && quantizes_both(q, dtype);
+    if (both) {
+        q.q_rows = ws + dy.q;
+        q.scale_rows = reinterpret_cast<float*>(ws + dy.scale);
+    }
+    if (d_grad_w != nullptr && rows > 0 && launch_quantize_tokens(q, dtype, sms, stream) != cudaSuccess)
+        return ZCCL_ERR_CUDA;
+    if (d_grad_x != nullptr && rows > 0) {
+        const zccl_status_t st =
+            linear(both ? nullptr : d_grad, dtype, grad_stride, rows, n, reinterpret_cast<const uint8_t*>(d_weight_t), k,
+                   groups, d_offsets, d_grad_x, out_dtype, ws, d_status, sms, stream);
+        if (st != ZCCL_OK) return st;
+    }
+    if (d_grad_w == nullptr) return ZCCL_OK;
     QuantArgs r = q;
     r.x = d_x;
     r.stride = x_stride;
     r.cols = (uint32_t)k;
     r.q = ws + xt.q;
     r.scale = reinterpret_cast<float*>(ws + xt.scale);
-    if (rows > 0 && (launch_quantize_tokens(q, dtype, sms, stream) != cudaSuccess ||
-                     launch_quantize_tokens(r, dtype, sms, stream) != cudaSuccess))
-        return ZCCL_ERR_CUDA;
+    r.q_rows = nullptr;
+    if (rows > 0 && launch_quantize_tokens(r, dtype, sms, stream) != cudaSuccess) return ZCCL_ERR_CUDA;
     WgradArgs w{};
     w.a = q.q;
     w.sa = q.scale;

@@ -83,6 +83,82 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantArgs a)
     }
 }
 
+// Largest magnitudes of BF16 pairs.
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+__device__ __forceinline__ uint32_t mag_pair(uint32_t a) { return a & 0x7FFF7FFFu; }
+__device__ __forceinline__ float max_of_pair(uint32_t a) { return fmaxf(bf16_lo(a), bf16_hi(a)); }
+
+// Maxima of kRows pairs over kLanes = 2 kRows neighbouring lanes, by halves: in
+// each step a lane gives away the rows that its partner keeps, so kRows
+// exchanges do for kRows rows.  Ends with row owned_row(lane) in each lane.
+template <int kRows>
+__device__ __forceinline__ uint32_t max_rows(uint32_t (&m)[kRows], uint32_t lane)
+{
+#pragma unroll
+    for (int n = kRows / 2; n > 0; n /= 2) {
+        const bool upper = (lane & (2 * n)) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const uint32_t give = upper ? m[i] : m[i + n], keep = upper ? m[i + n] : m[i];
+            m[i] = max_pair(keep, __shfl_xor_sync(0xFFFFFFFFu, give, 2 * n));
+        }
+    }
+    return max_pair(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], 1));
+}
+template <int kRows>
+__device__ __forceinline__ uint32_t owned_row(uint32_t lane) { return (lane / 2) % kRows; }
+// The lane, among the 2 kRows, that owns a row.
+__device__ __forceinline__ constexpr uint32_t owner_of(uint32_t row) { return 2 * row; }
+
+// BF16 rows in 16-byte pieces: as quantize_rows_kernel, with the values kept as
+// they are read and the division done once a row (92 instructions a row of 256
+// values and half the bandwidth before).
+__global__ void __launch_bounds__(kThreads) quantize_rows_bf16_kernel(QuantArgs a)
+{
+    pdl_wait();
+    const uint32_t lane = threadIdx.x & 31, half = lane >> 4, i8 = (lane & 15) * 8;
+    const uint32_t nb = (uint32_t)blocks_of(a.cols), pairs = (nb + 1) / 2;
+    const uint32_t groups = (a.rows + kRowsPerWarp - 1) / kRowsPerWarp;
+    const uint32_t warps = gridDim.x * (kThreads / 32);
+    // consecutive warps take consecutive pairs of blocks of the same rows
+    const uint32_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t step_g = warps / pairs, step_p = warps % pairs;
+    uint32_t g = w / pairs, p = w % pairs;
+    while (g < groups) {
+        const uint32_t r0 = g * kRowsPerWarp, b = 2 * p + half, c = b * kFp8Block + i8;
+        uint4 v[kRowsPerWarp];
+#pragma unroll
+        for (int r = 0; r < kRowsPerWarp; ++r)
+            v[r] = c < a.cols ? ld_once(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.x) +
+                                                                       (uint64_t)min(r0 + r, a.rows - 1) * a.stride + c))
+                              : make_uint4(0, 0, 0, 0);
+        uint32_t m[kRowsPerWarp];
+#pragma unroll
+        for (int r = 0; r < kRowsPerWarp; ++r)
+            m[r] = max_pair(max_pair(mag_pair(v[r].x), mag_pair(v[r].y)), max_pair(mag_pair(v[r].z), mag_pair(v[r].w)));
+        float scale, factor;
+        block_scale(max_of_pair(max_rows<kRowsPerWarp>(m, lane)), &scale, &factor);
+        const uint32_t own = r0 + owned_row<kRowsPerWarp>(lane);
+        if ((lane & 1) == 0 && b < nb && own < a.rows) a.scale[(uint64_t)b * a.rows + own] = scale;
+        uint8_t* q = a.q + ((uint64_t)b * a.rows + r0) * kFp8Block + i8;
+#pragma unroll
+        for (int r = 0; r < kRowsPerWarp; ++r) {
+            const float f = __shfl_sync(0xFFFFFFFFu, factor, (lane & 16) + owner_of(r));
+            if (b < nb && r0 + r < a.rows)
+                *reinterpret_cast<uint2*>(q + r * kFp8Block) =
+                    make_uint2(e4m3x4(bf16_lo(v[r].x) * f, bf16_hi(v[r].x) * f, bf16_lo(v[r].y) * f, bf16_hi(v[r].y) * f),
+                               e4m3x4(bf16_lo(v[r].z) * f, bf16_hi(v[r].z) * f, bf16_lo(v[r].w) * f, bf16_hi(v[r].w) * f));
+        }
+        g += step_g;
+        p += step_p;
+        if (p >= pairs) p -= pairs, ++g;
+    }
+}
+
 // Four values of a row from column c on.  kVec: aligned to four values.
 template <typename T, bool kVec>
 __device__ __forceinline__ void load4(const T* row, uint32_t c, uint32_t cols, bool on, float (&v)[4])
@@ -188,6 +264,82 @@ __global__ void __launch_bounds__(kThreads) quantize_tokens_kernel(QuantArgs a)
     }
 }
 
+// The same for BF16 in 8-byte pieces, the values kept as they are read.  kRows:
+// also the blocks along each row (q_rows, scale_rows, as quantize_rows_kernel
+// makes them), so that a gradient is read once for both its uses; the rows
+// outside every group get none.
+template <bool kRows>
+__global__ void __launch_bounds__(kThreads, 3) quantize_tokens_bf16_kernel(QuantArgs a)
+{
+    __shared__ __align__(16) uint8_t tile[128 * 128];
+    __shared__ uint2 top[8][32];
+    __shared__ uint32_t prefix[kMaxGroupsFp8 + 1];
+    pdl_wait();
+    const uint32_t lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+    group_prefix(a.offsets, a.rows, a.G, kFp8Block, (uint32_t)(a.rows / kFp8Block + a.G), prefix);
+    __syncthreads();
+    const uint32_t tiles = (uint32_t)blocks_of(a.cols);
+    const uint64_t items = (uint64_t)prefix[a.G] * tiles;
+    for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const uint32_t tb = (uint32_t)(it / tiles), cb = (uint32_t)(it - (uint64_t)tb * tiles), c = cb * kFp8Block + 4 * lane;
+        const uint32_t g = group_at(prefix, a.G, tb);
+        uint32_t lo, hi;
+        group_rows(a.offsets, a.rows, g, &lo, &hi);
+        const uint32_t r0 = lo + (tb - prefix[g]) * kFp8Block + 16 * part;
+        const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x) + (uint64_t)r0 * a.stride + c;
+        uint2 v[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            v[r] = r0 + r < hi && c < a.cols ? *reinterpret_cast<const uint2*>(x + r * a.stride) : make_uint2(0, 0);
+        uint2 m = make_uint2(0, 0);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            m.x = max_pair(m.x, mag_pair(v[r].x));
+            m.y = max_pair(m.y, mag_pair(v[r].y));
+        }
+        top[part][lane] = m;
+        if (kRows) {
+            uint32_t mr[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) mr[r] = max_pair(mag_pair(v[r].x), mag_pair(v[r].y));
+            float scale, factor;
+            block_scale(max_of_pair(max_rows<16>(mr, lane)), &scale, &factor);
+            const uint32_t own = r0 + owned_row<16>(lane);
+            if ((lane & 1) == 0 && own < hi) a.scale_rows[(uint64_t)cb * a.rows + own] = scale;
+            uint8_t* q = a.q_rows + ((uint64_t)cb * a.rows + r0) * kFp8Block + 4 * lane;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float f = __shfl_sync(0xFFFFFFFFu, factor, owner_of(r));
+                if (r0 + r < hi)
+                    *reinterpret_cast<uint32_t*>(q + r * kFp8Block) =
+                        e4m3x4(bf16_lo(v[r].x) * f, bf16_hi(v[r].x) * f, bf16_lo(v[r].y) * f, bf16_hi(v[r].y) * f);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            const uint2 o = top[p][lane];
+            m.x = max_pair(m.x, o.x);
+            m.y = max_pair(m.y, o.y);
+        }
+        const float mag[4] = {bf16_lo(m.x), bf16_hi(m.x), bf16_lo(m.y), bf16_hi(m.y)};
+        float f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float scale;
+            block_scale(mag[j], &scale, &f[j]);
+            if (part == 0 && c + j < a.cols) a.scale[(uint64_t)tb * a.cols + c + j] = scale;
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            w[r] = e4m3x4(bf16_lo(v[r].x) * f[0], bf16_hi(v[r].x) * f[1], bf16_lo(v[r].y) * f[2], bf16_hi(v[r].y) * f[3]);
+        exchange_store(w, tile, lane, part);
+        __syncthreads();
+        exchange_out(tile, a.q + ((uint64_t)tb * a.cols + cb * kFp8Block) * kFp8Block, a.cols - cb * kFp8Block);
+    }
+}
+
 // One 128 x 128 block of a weight: quantised (w) or taken as it is (codes,
 // scale), into the packed weight and the one with exchanged axes.
 template <typename T>
@@ -269,17 +421,24 @@ cudaError_t quantize_rows_as(const QuantArgs& a, int sms, cudaStream_t stream)
 {
     const uint64_t warps = (blocks_of(a.cols) + 1) / 2 * ((a.rows + kRowsPerWarp - 1) / kRowsPerWarp);
     const uint32_t grid = capped((warps + kThreads / 32 - 1) / (kThreads / 32), sms, 16);
-    return vectored<T>(a, 8) ? launch_dependent(quantize_rows_kernel<T, true>, grid, kThreads, 0, stream, a)
-                             : launch_dependent(quantize_rows_kernel<T, false>, grid, kThreads, 0, stream, a);
+    void (*kernel)(QuantArgs) = quantize_rows_kernel<T, false>;
+    if (vectored<T>(a, 8)) kernel = sizeof(T) == 2 ? quantize_rows_bf16_kernel : quantize_rows_kernel<T, true>;
+    return launch_dependent(kernel, grid, kThreads, 0, stream, a);
 }
 
 template <typename T>
 cudaError_t quantize_tokens_as(const QuantArgs& a, int sms, cudaStream_t stream)
 {
     const uint64_t tiles = (a.rows / kFp8Block + a.G) * blocks_of(a.cols);
-    const uint32_t grid = capped(tiles, sms, 2);
-    return vectored<T>(a, 4) ? launch_dependent(quantize_tokens_kernel<T, true>, grid, kThreads, 0, stream, a)
-                             : launch_dependent(quantize_tokens_kernel<T, false>, grid, kThreads, 0, stream, a);
+    void (*kernel)(QuantArgs) = quantize_tokens_kernel<T, false>;
+    int per_sm = 2;
+    if (sizeof(T) == 2 && vectored<T>(a, 4)) {
+        kernel = a.q_rows != nullptr ? quantize_tokens_bf16_kernel<true> : quantize_tokens_bf16_kernel<false>;
+        per_sm = 4;
+    } else if (vectored<T>(a, 4)) {
+        kernel = quantize_tokens_kernel<T, true>;
+    }
+    return launch_dependent(kernel, capped(tiles, sms, per_sm), kThreads, 0, stream, a);
 }
 
 }  // namespace
@@ -294,6 +453,8 @@ cudaError_t launch_quantize_tokens(const QuantArgs& a, int dtype, int sms, cudaS
     return dtype == ZCCL_BF16 ? quantize_tokens_as<__nv_bfloat16>(a, sms, stream)
                               : quantize_tokens_as<float>(a, sms, stream);
 }
+
+bool quantizes_both(const QuantArgs& a, int dtype) { return dtype == ZCCL_BF16 && vectored<__nv_bfloat16>(a, 4); }
 
 cudaError_t launch_pack(const PackArgs& a, int dtype, cudaStream_t stream)
 {
