@@ -36,8 +36,8 @@ constexpr uint32_t kTileM = 128;
 constexpr uint32_t kTileN = 256;
 constexpr uint32_t kStages = 3;
 constexpr uint32_t kABytes = kTileM * kFp8Block, kBBytes = kTileN * kFp8Block;
-constexpr uint32_t kScaleSlots = 6;
-constexpr uint32_t kScaleLag = 4;      // a block's scales are reported this many blocks after their copies are issued
+constexpr uint32_t kScaleSlots = 4;
+constexpr uint32_t kScaleLag = 2;      // a block's scales are reported this many blocks after their copies are issued
 constexpr uint32_t kSumWarps = 8;      // warps that add, two to 32 rows of a tile
 constexpr uint32_t kSumCols = 128;     // columns of one of them
 constexpr uint32_t kThreads = 128 + 32 * kSumWarps;  // warps 0..3: load, issue, schedule, scales; then those that add
@@ -72,6 +72,7 @@ constexpr uint32_t kTileReaders = 3 + kSumWarps;  // warps that read a tile
 struct Smem {
     alignas(1024) uint8_t out[kSumWarps][2][32 * 128];  // by warp, twice: 32 rows of 128 bytes of a finished tile, swizzled
     alignas(16) float row_scale[kScaleSlots][kTileM];
+    alignas(16) float scale[kScaleSlots][2][kTileM];   // a row's scale times that of its 128 columns, by warpgroup
     alignas(16) float col_scale[kScaleSlots][kTileN];  // weight gradient: by column; else one per 128 columns
     Tile tile[kTileSlots];
     uint64_t full[kStages], empty[kStages], told[kTileSlots], read[kTileSlots], done[2], drain;
@@ -226,15 +227,22 @@ __device__ __forceinline__ void store_rows(uint8_t (&bufs)[2][32 * 128], const C
 }
 
 // Whether a phase is complete, without waiting.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity)
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+    return v;
 }
 
 // Four bytes to shared memory, asynchronously.
@@ -243,9 +251,9 @@ __device__ __forceinline__ void copy4_async(float* dst, const float* src)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
 // Lane 0 arrives, without a branch.
-__device__ __forceinline__ void arrive_lane0(uint64_t* bar, uint32_t lane)
+__device__ __forceinline__ void arrive_lane0(uint32_t bar, uint32_t lane)
 {
-    asm volatile("{\n .reg .pred p;\n setp.eq.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(smem_addr(bar)),
+    asm volatile("{\n .reg .pred p;\n setp.eq.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar),
                  "r"(lane)
                  : "memory");
 }
@@ -258,7 +266,7 @@ __device__ __forceinline__ bool next_tile(Smem* s, uint32_t* k, Tile* c, uint32_
     if (!wait_phase(&s->told[slot], (*k / kTileSlots) & 1, status)) return false;
     *c = s->tile[slot];
     __syncwarp();
-    arrive_lane0(&s->read[slot], lane);
+    arrive_lane0(smem_addr(&s->read[slot]), lane);
     ++*k;
     return c->blocks != kNoTile;
 }
@@ -347,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     tc_fence_after();
                     const uint64_t da = desc0 + stage * ((kABytes + kBBytes) >> 4);
-                    mma_block_e4m3(tmem + buf * kTileN, da, da + (kABytes >> 4), idesc, &s->done[buf]);
+                    mma_block_e4m3(tmem + buf * kTileN, da, da + (kABytes >> 4), idesc, &s->done[buf], &s->empty[stage]);
                     if (++stage == kStages) stage = 0, phase ^= 1;
                     buf ^= 1;
                 }
@@ -374,19 +382,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait_phase(&s->read[slot], ((k / kTileSlots) & 1) ^ 1, a.status)) break;
                 if (lane == 0) s->tile[slot] = c;
                 __syncwarp();
-                arrive_lane0(&s->told[slot], lane);
+                arrive_lane0(smem_addr(&s->told[slot]), lane);
                 if (t >= tiles) break;
             }
         } else {
             // ---- scales: 32 threads, four rows and (weight gradient) eight columns each.  A block's slot is free
-            // once the block six before it was taken, which the barrier of the block four before it says; its scales
-            // are reported four blocks later, when the block two before it is done with the barrier.
+            // once the block four before it was taken, which the barrier of the block two before it says; its scales
+            // are reported two blocks later, when the block two before it is done with the barrier.
             const uint32_t last = (kWgrad ? a.m : a.rows) - 1, nbs = (uint32_t)blocks_of(a.n);
-            uint32_t count = 0, slot = 0, stage = 2 % kStages, phase = 0;
+            uint32_t count = 0, stage = 2 % kStages, phase = 0;
+            // the scales of block `ready` have landed: multiplies them out and reports them
+            auto report_block = [&](uint32_t ready) {
+                const uint32_t slot = ready % kScaleSlots;
+                __syncwarp();
+                if (!kWgrad) {
+                    const float4 r = *reinterpret_cast<const float4*>(&s->row_scale[slot][4 * lane]);
+#pragma unroll
+                    for (uint32_t w = 0; w < 2; ++w) {
+                        const float f = s->col_scale[slot][w];
+                        *reinterpret_cast<float4*>(&s->scale[slot][w][4 * lane]) = make_float4(r.x * f, r.y * f, r.z * f, r.w * f);
+                    }
+                }
+                if (ready >= 2 && !wait_phase(&s->done[ready & 1], ((ready >> 1) & 1) ^ 1, a.status)) return false;
+                mbar_arrive(&s->done[ready & 1]);
+                return true;
+            };
             while (ok && next_tile(s, &k, &c, lane, a.status)) {
                 const float* row = a.sa + c.sa0;
                 const float* col = a.sb + c.sb0 + (kWgrad ? 0 : min(c.n0 / kFp8Block + lane, nbs - 1) * a.KB);
                 for (uint32_t b = 0; b < c.blocks; ++b, ++count) {
+                    const uint32_t slot = count % kScaleSlots;
                     if (count >= kScaleSlots) {
                         if (!(ok = wait_phase(&s->full[stage], phase, a.status))) break;
                         if (++stage == kStages) stage = 0, phase ^= 1;
@@ -404,61 +429,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ++col;
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (++slot == kScaleSlots) slot = 0;
                     if (count >= kScaleLag) {
                         asm volatile("cp.async.wait_group %0;" ::"n"(kScaleLag) : "memory");
-                        const uint32_t ready = count - kScaleLag;
-                        if (ready >= 2 && !(ok = wait_phase(&s->done[ready & 1], ((ready >> 1) & 1) ^ 1, a.status))) break;
-                        mbar_arrive(&s->done[ready & 1]);
+                        if (!(ok = report_block(count - kScaleLag))) break;
                     }
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
-            for (uint32_t ready = count > kScaleLag ? count - kScaleLag : 0; ok && ready < count; ++ready) {
-                if (ready >= 2 && !(ok = wait_phase(&s->done[ready & 1], ((ready >> 1) & 1) ^ 1, a.status))) break;
-                mbar_arrive(&s->done[ready & 1]);
-            }
+            for (uint32_t ready = count > kScaleLag ? count - kScaleLag : 0; ok && ready < count; ++ready) ok = report_block(ready);
         }
     } else {
         regs_more<kRegsMany>();
         // ---- sums: warpgroup wg has columns 128 wg .. 128 wg + 127, warp w of it lanes 32 w .. 32 w + 31
         const uint32_t wg = (warp - 4) >> 2, sub = warp & 3;
         const uint32_t taddr = tmem + ((sub * 32) << 16) + wg * kSumCols;
-        uint32_t k = 0, count = 0, slot = 0, stage = 0, stage2 = 2 % kStages, turn = 0;
+        const uint32_t done = smem_addr(&s->done[0]);
+        // where a row's scale is in slot 0, and the barriers of the next blocks in turn
+        const uint32_t scales = kWgrad ? smem_addr(&s->row_scale[0][sub * 32 + lane]) : smem_addr(&s->scale[0][wg][sub * 32 + lane]);
+        constexpr uint32_t kScalePitch = kWgrad ? sizeof(s->row_scale[0]) : sizeof(s->scale[0]);
+        uint32_t free0 = smem_addr(&s->full[2 % kStages]), free1 = smem_addr(&s->full[3 % kStages]),
+                 free2 = smem_addr(&s->full[4 % kStages]);
+        static_assert(kStages == 3, "three barriers take turns");
+        uint32_t k = 0, count = 0, turn = 0;
         bool ok = true;
         Tile c;
-        arrive_lane0(&s->full[0], lane);  // both accumulators are free for the first two blocks
-        arrive_lane0(&s->full[1], lane);
+        arrive_lane0(smem_addr(&s->full[0]), lane);  // both accumulators are free for the first two blocks
+        arrive_lane0(smem_addr(&s->full[1]), lane);
+        uint32_t r[2][32];   // pieces of 32 columns, one on its way while the other is added
+        bool there = false;  // whether the next block is known to be done and its first piece is on its way
+        float sa = 0.0f;
         while (ok && next_tile(s, &k, &c, lane, a.status)) {
             float acc[kSumCols];
 #pragma unroll
             for (uint32_t i = 0; i < kSumCols; ++i) acc[i] = 0.0f;
-            uint32_t r[2][32];   // pieces of 32 columns, one on its way while the other is added
-            bool there = false;  // whether this block is known to be done and its first piece is on its way
-            float sa = 0.0f;
 #pragma unroll 1
             for (uint32_t b = 0; b < c.blocks; ++b) {
-                const uint32_t buf = count & 1;
-                const uint32_t from = taddr + buf * kTileN;
+                const uint32_t from = taddr + (count & 1) * kTileN;
                 if (!there) {
-                    if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&s->done[buf], (count >> 1) & 1)) &&
-                        !(ok = wait_phase(&s->done[buf], (count >> 1) & 1, a.status)))
+                    if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&s->done[count & 1], (count >> 1) & 1)) &&
+                        !(ok = wait_phase(&s->done[count & 1], (count >> 1) & 1, a.status)))
                         break;
                     tc_fence_after();
                     tmem_load32(from, r[0]);
-                    sa = s->row_scale[slot][sub * 32 + lane];
-                    if (!kWgrad) sa *= s->col_scale[slot][wg];
+                    sa = lds_f32(scales + (count % kScaleSlots) * kScalePitch);
                 }
-                // the products are done, so their stage is free
-                if (warp == 4) arrive_lane0(&s->empty[stage], lane);
-                if (++stage == kStages) stage = 0;
+                const uint32_t slot = count % kScaleSlots;
+                const float now = sa;
                 ++count;
-                uint64_t* const free_for = &s->full[stage2];  // the accumulator's next block
-                if (++stage2 == kStages) stage2 = 0;
-                const uint32_t next_slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
-                const bool more = b + 1 < c.blocks;
-                float next_sa = 0.0f;
-                there = false;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     tmem_wait32(r[q & 1]);
@@ -467,15 +484,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!kWgrad) {
                             tc_fence_before();
                             __syncwarp();
-                            arrive_lane0(free_for, lane);
+                            arrive_lane0(free0, lane);
                         }
-                        // the next block, if it is done, before the last columns of this one
-                        there = __all_sync(0xFFFFFFFFu, more && mbar_test_wait(&s->done[count & 1], (count >> 1) & 1));
+                        // the next block (of whatever tile), if it is done, before the last columns of this one
+                        there = __all_sync(0xFFFFFFFFu, mbar_test_wait(done + 8 * (count & 1), (count >> 1) & 1));
                         if (there) {
                             tc_fence_after();
                             tmem_load32(taddr + (count & 1) * kTileN, r[0]);
-                            next_sa = s->row_scale[next_slot][sub * 32 + lane];
-                            if (!kWgrad) next_sa *= s->col_scale[next_slot][wg];
+                            sa = lds_f32(scales + (count % kScaleSlots) * kScalePitch);
                         }
                     }
                     if (kWgrad) {
@@ -484,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 8; ++i) {
                             const float4 f = col[i];
                             // the scales first: their product overflows only where the sum does
-                            const float2 x0 = mul2(f.x, f.y, sa), x1 = mul2(f.z, f.w, sa);
+                            const float2 x0 = mul2(f.x, f.y, now), x1 = mul2(f.z, f.w, now);
                             float* to = &acc[32 * q + 4 * i];
                             const uint32_t* from_r = &r[q & 1][4 * i];
                             fma2(to[0], to[1], __uint_as_float(from_r[0]), __uint_as_float(from_r[1]), x0.x, x0.y);
@@ -494,16 +510,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; i += 2)
                             fma2(acc[32 * q + i], acc[32 * q + i + 1], __uint_as_float(r[q & 1][i]),
-                                 __uint_as_float(r[q & 1][i + 1]), sa, sa);
+                                 __uint_as_float(r[q & 1][i + 1]), now, now);
                     }
                 }
                 if (kWgrad) {  // the column scales are read to the end
                     tc_fence_before();
                     __syncwarp();
-                    arrive_lane0(free_for, lane);
+                    arrive_lane0(free0, lane);
                 }
-                sa = next_sa;
-                slot = next_slot;
+                const uint32_t first = free0;
+                free0 = free1;
+                free1 = free2;
+                free2 = first;
             }
             const uint32_t row = c.m0 + sub * 32, n = c.n0 + wg * kSumCols;
             if (ok && row < c.row_end && n < a.n)

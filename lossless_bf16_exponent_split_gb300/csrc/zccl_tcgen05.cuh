@@ -40,10 +40,11 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr)
 __host__ __device__ constexpr uint32_t instr_desc(uint32_t m, uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24); }
 
 // d = a b over a block of 128 values of the reduction axis (four instructions of
-// 32, 32 bytes apart in the swizzled rows), then an arrival on `bar` when they are
-// done.  A whole warp calls it, so that its operands stay in uniform registers;
+// 32, 32 bytes apart in the swizzled rows), then arrivals on two barriers when
+// they are done.  A whole warp calls it, so that its operands stay in uniform registers;
 // one elected lane issues.
-__device__ __forceinline__ void mma_block_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint64_t* bar)
+__device__ __forceinline__ void mma_block_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint64_t* bar0,
+                                               uint64_t* bar1)
 {
     asm volatile(
         "{\n .reg .pred one, add, set;\n .reg .b64 a1, b1, a2, b2, a3, b3;\n"
@@ -54,8 +55,9 @@ __device__ __forceinline__ void mma_block_e4m3(uint32_t d, uint64_t a, uint64_t 
         " @one tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, add;\n"
         " @one tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, add;\n"
         " @one tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, add;\n"
-        " @one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(smem_addr(bar))
+        " @one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n"
+        " @one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(smem_addr(bar0)), "r"(smem_addr(bar1))
         : "memory");
 }
 
