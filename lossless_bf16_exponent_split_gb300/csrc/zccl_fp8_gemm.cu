@@ -72,7 +72,6 @@ constexpr uint32_t kTileReaders = 3 + kSumWarps;  // warps that read a tile
 struct Smem {
     alignas(1024) uint8_t out[kSumWarps][2][32 * 128];  // by warp, twice: 32 rows of 128 bytes of a finished tile, swizzled
     alignas(16) float row_scale[kScaleSlots][kTileM];
-    alignas(16) float scale[kScaleSlots][2][kTileM];   // a row's scale times that of its 128 columns, by warpgroup
     alignas(16) float col_scale[kScaleSlots][kTileN];  // weight gradient: by column; else one per 128 columns
     Tile tile[kTileSlots];
     uint64_t full[kStages], empty[kStages], told[kTileSlots], read[kTileSlots], done[2], drain;
@@ -387,56 +386,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else {
             // ---- scales: 32 threads, four rows and (weight gradient) eight columns each.  A block's slot is free
-            // once the block four before it was taken, which the barrier of the block two before it says; its scales
-            // are reported two blocks later, when the block two before it is done with the barrier.
+            // once the block four before it was taken, which the barrier of the block two before it says; that block's
+            // own scales, which have landed by then, are reported first
             const uint32_t last = (kWgrad ? a.m : a.rows) - 1, nbs = (uint32_t)blocks_of(a.n);
-            uint32_t count = 0, stage = 2 % kStages, phase = 0;
-            // the scales of block `ready` have landed: multiplies them out and reports them
-            auto report_block = [&](uint32_t ready) {
-                const uint32_t slot = ready % kScaleSlots;
-                __syncwarp();
-                if (!kWgrad) {
-                    const float4 r = *reinterpret_cast<const float4*>(&s->row_scale[slot][4 * lane]);
-#pragma unroll
-                    for (uint32_t w = 0; w < 2; ++w) {
-                        const float f = s->col_scale[slot][w];
-                        *reinterpret_cast<float4*>(&s->scale[slot][w][4 * lane]) = make_float4(r.x * f, r.y * f, r.z * f, r.w * f);
-                    }
-                }
-                if (ready >= 2 && !wait_phase(&s->done[ready & 1], ((ready >> 1) & 1) ^ 1, a.status)) return false;
-                mbar_arrive(&s->done[ready & 1]);
-                return true;
-            };
+            uint32_t count = 0, stage = 0, phase = 0;
             while (ok && next_tile(s, &k, &c, lane, a.status)) {
                 const float* row = a.sa + c.sa0;
                 const float* col = a.sb + c.sb0 + (kWgrad ? 0 : min(c.n0 / kFp8Block + lane, nbs - 1) * a.KB);
+#pragma unroll 1
                 for (uint32_t b = 0; b < c.blocks; ++b, ++count) {
                     const uint32_t slot = count % kScaleSlots;
-                    if (count >= kScaleSlots) {
+                    if (count >= kScaleLag) {
                         if (!(ok = wait_phase(&s->full[stage], phase, a.status))) break;
+                        asm volatile("cp.async.wait_group %0;" ::"n"(kScaleLag - 1) : "memory");
+                        mbar_arrive(&s->done[count & 1]);
                         if (++stage == kStages) stage = 0, phase ^= 1;
                     }
 #pragma unroll
-                    for (uint32_t j = lane; j < kTileM; j += 32) copy4_async(&s->row_scale[slot][j], row + min(c.m0 + j, last));
+                    for (uint32_t j = 0; j < kTileM; j += 32)
+                        copy4_async(&s->row_scale[slot][lane + j], row + min(c.m0 + lane + j, last));
                     row += kWgrad ? a.m : a.rows;
                     if (kWgrad) {
 #pragma unroll
-                        for (uint32_t j = lane; j < kTileN; j += 32)
-                            copy4_async(&s->col_scale[slot][j], col + min(c.n0 + j, a.n - 1));
+                        for (uint32_t j = 0; j < kTileN; j += 32)
+                            copy4_async(&s->col_scale[slot][lane + j], col + min(c.n0 + lane + j, a.n - 1));
                         col += a.n;
                     } else {
                         if (lane < kTileN / kFp8Block) copy4_async(&s->col_scale[slot][lane], col);
                         ++col;
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (count >= kScaleLag) {
-                        asm volatile("cp.async.wait_group %0;" ::"n"(kScaleLag) : "memory");
-                        if (!(ok = report_block(count - kScaleLag))) break;
-                    }
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
-            for (uint32_t ready = count > kScaleLag ? count - kScaleLag : 0; ok && ready < count; ++ready) ok = report_block(ready);
+            for (uint32_t ready = count > kScaleLag ? count - kScaleLag : 0; ok && ready < count; ++ready) {
+                if (!(ok = wait_phase(&s->full[stage], phase, a.status))) break;
+                mbar_arrive(&s->done[ready & 1]);
+                if (++stage == kStages) stage = 0, phase ^= 1;
+            }
         }
     } else {
         regs_more<kRegsMany>();
@@ -444,9 +431,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t wg = (warp - 4) >> 2, sub = warp & 3;
         const uint32_t taddr = tmem + ((sub * 32) << 16) + wg * kSumCols;
         const uint32_t done = smem_addr(&s->done[0]);
-        // where a row's scale is in slot 0, and the barriers of the next blocks in turn
-        const uint32_t scales = kWgrad ? smem_addr(&s->row_scale[0][sub * 32 + lane]) : smem_addr(&s->scale[0][wg][sub * 32 + lane]);
-        constexpr uint32_t kScalePitch = kWgrad ? sizeof(s->row_scale[0]) : sizeof(s->scale[0]);
+        // where its scales are, and the barriers of the next blocks in turn
+        const uint32_t rows_at = smem_addr(&s->row_scale[0][sub * 32 + lane]), block_at = smem_addr(&s->col_scale[0][wg]);
+        // a row's scale, times that of its 128 columns if they have one
+        auto scale_of = [&](uint32_t block) {
+            const uint32_t slot = block % kScaleSlots;
+            const float r = lds_f32(rows_at + slot * (kTileM * 4));
+            return kWgrad ? r : r * lds_f32(block_at + slot * (kTileN * 4));
+        };
         uint32_t free0 = smem_addr(&s->full[2 % kStages]), free1 = smem_addr(&s->full[3 % kStages]),
                  free2 = smem_addr(&s->full[4 % kStages]);
         static_assert(kStages == 3, "three barriers take turns");
@@ -471,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     tc_fence_after();
                     tmem_load32(from, r[0]);
-                    sa = lds_f32(scales + (count % kScaleSlots) * kScalePitch);
+                    sa = scale_of(count);
                 }
                 const uint32_t slot = count % kScaleSlots;
                 const float now = sa;
@@ -491,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (there) {
                             tc_fence_after();
                             tmem_load32(taddr + (count & 1) * kTileN, r[0]);
-                            sa = lds_f32(scales + (count % kScaleSlots) * kScalePitch);
+                            sa = scale_of(count);
                         }
                     }
                     if (kWgrad) {
