@@ -42,6 +42,7 @@ struct MatmulArgs {
     uint32_t rows, n, KB, G;
     void* out;               // [rows][n]
     int out_f32;
+    uint32_t* ticket;        // zero before the launch
     uint32_t* status;
 };
 
@@ -57,6 +58,7 @@ struct WgradArgs {
     uint32_t blocks;         // token blocks there is room for: rows / 128 + G
     void* out;               // [G][m][n]
     int out_f32;
+    uint32_t* ticket;        // zero before the launch
     uint32_t* status;
 };
 
@@ -83,6 +85,7 @@ struct QuantArgs {
     uint32_t G;
     uint8_t* q_rows;         // along rows: also the blocks of each row, or nullptr
     float* scale_rows;
+    uint32_t* ticket;        // zeroed for the product that follows
 };
 
 struct PackArgs {

@@ -53,6 +53,7 @@ struct TileArgs {
     uint32_t rows, m, n, KB, G, blocks;
     void* out;
     int tma_out;           // whether the output has a tensor map
+    uint32_t* ticket;      // tiles given out so far
     uint32_t* status;
 };
 
@@ -77,6 +78,7 @@ struct Smem {
     uint64_t full[kStages], empty[kStages], told[kTileSlots], read[kTileSlots], done[2], drain;
     uint32_t tmem;
     uint32_t prefix[kMaxGroupsFp8 + 1];
+    uint16_t order[kMaxGroupsFp8];  // weight gradient: the groups by their blocks, most first
 };
 constexpr uint32_t kSmemBytes = 1024 + kStages * (kABytes + kBBytes) + sizeof(Smem);
 static_assert(kSmemBytes <= 232448, "fits the shared memory of a CTA");
@@ -93,7 +95,8 @@ __device__ __forceinline__ uint32_t tile_count(const TileArgs& a, const uint32_t
 }
 
 template <bool kWgrad>
-__device__ __forceinline__ Tile tile_at(const TileArgs& a, const uint32_t* prefix, uint32_t tail0, uint32_t t)
+__device__ __forceinline__ Tile tile_at(const TileArgs& a, const uint32_t* prefix, const uint16_t* order, uint32_t tail0,
+                                        uint32_t t)
 {
     const uint32_t nt = (a.n + kTileN - 1) / kTileN;
     Tile c;
@@ -102,6 +105,7 @@ __device__ __forceinline__ Tile tile_at(const TileArgs& a, const uint32_t* prefi
         mt = (a.m + kTileM - 1) / kTileM;
         c.g = t / (mt * nt);
         i = t - c.g * mt * nt;
+        c.g = order[c.g];
         c.blocks = prefix[c.g + 1] - prefix[c.g];
         c.row_end = a.m;
     } else {
@@ -304,6 +308,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (kWgrad) {
+        for (uint32_t g = threadIdx.x; g < a.G; g += kThreads) {
+            const uint32_t mine = s->prefix[g + 1] - s->prefix[g];
+            uint32_t before = 0;
+            for (uint32_t h = 0; h < a.G; ++h) {
+                const uint32_t other = s->prefix[h + 1] - s->prefix[h];
+                before += other > mine || (other == mine && h < g) ? 1u : 0u;
+            }
+            s->order[before] = (uint16_t)g;
+        }
+        __syncthreads();
+    }
     const uint32_t tmem = s->tmem;
 
     if (warp < 4) {
@@ -365,24 +381,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
         } else if (warp == 2) {
-            // ---- the tiles, in an order of their own for each CTA
+            // ---- the tiles, by ticket: a CTA that is done early takes more of them, and a weight gradient's
+            // longest tiles go first.  A ticket is drawn while the tile before it waits for its slot.
             uint32_t tail0 = a.rows;
             if (!kWgrad && a.offsets != nullptr) {
                 const int32_t t = ld_l2(a.offsets + a.G);
                 tail0 = t < 0 ? 0u : min((uint32_t)t, a.rows);
             }
             const uint32_t tiles = tile_count<kWgrad>(a, s->prefix, tail0);
-            for (uint32_t t = blockIdx.x;; t += gridDim.x, ++k) {
-                const uint32_t slot = k % kTileSlots;
-                if (t < tiles)
-                    c = tile_at<kWgrad>(a, s->prefix, tail0, t);
-                else
+            uint32_t t = lane == 0 ? atomicAdd(a.ticket, 1u) : 0u;
+            for (;; ++k) {
+                const uint32_t slot = k % kTileSlots, now = __shfl_sync(0xFFFFFFFFu, t, 0);
+                if (now < tiles) {
+                    if (lane == 0) t = atomicAdd(a.ticket, 1u);
+                    c = tile_at<kWgrad>(a, s->prefix, s->order, tail0, now);
+                } else {
                     c.blocks = kNoTile;
+                }
                 if (!wait_phase(&s->read[slot], ((k / kTileSlots) & 1) ^ 1, a.status)) break;
                 if (lane == 0) s->tile[slot] = c;
                 __syncwarp();
                 arrive_lane0(smem_addr(&s->told[slot]), lane);
-                if (t >= tiles) break;
+                if (now >= tiles) break;
             }
         } else {
             // ---- scales: 32 threads, four rows and (weight gradient) eight columns each.  A block's slot is free
@@ -610,6 +630,7 @@ cudaError_t launch_matmul(const MatmulArgs& m, int sms, cudaStream_t stream)
     a.KB = m.KB;
     a.G = m.G;
     a.out = m.out;
+    a.ticket = m.ticket;
     a.status = m.status;
     const uint64_t most = (blocks_of(m.rows) + m.G) * ((m.n + kTileN - 1) / kTileN);
     const auto launch = m.out_f32 ? launch_tiles<false, float> : launch_tiles<false, __nv_bfloat16>;
@@ -628,6 +649,7 @@ cudaError_t launch_wgrad(const WgradArgs& w, int sms, cudaStream_t stream)
     a.G = w.G;
     a.blocks = w.blocks;
     a.out = w.out;
+    a.ticket = w.ticket;
     a.status = w.status;
     const uint64_t most = (uint64_t)w.G * ((w.m + kTileM - 1) / kTileM) * ((w.n + kTileN - 1) / kTileN);
     const auto launch = w.out_f32 ? launch_tiles<true, float> : launch_tiles<true, __nv_bfloat16>;

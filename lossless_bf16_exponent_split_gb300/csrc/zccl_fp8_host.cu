@@ -24,6 +24,9 @@ bool sizes_ok(uint64_t rows, uint64_t k, uint64_t n, uint32_t groups)
 bool float_type(int t) { return t == ZCCL_BF16 || t == ZCCL_F32; }
 uintptr_t size_of(int t) { return t == ZCCL_BF16 ? 2 : 4; }
 
+// A workspace begins with the tile counters of a call's products.
+constexpr uint64_t kTicketBytes = 256;
+
 // Rows of `cols` values quantised by row.
 struct RowsLayout {
     uint64_t q, scale, end;
@@ -73,7 +76,7 @@ zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, u
         s.out_f32 = out_dtype == ZCCL_F32;
         return launched(launch_small(s, dtype, sms, stream));
     }
-    const RowsLayout l = rows_layout(0, rows, k);
+    const RowsLayout l = rows_layout(kTicketBytes, rows, k);
     QuantArgs q{};
     q.x = x;
     q.stride = stride;
@@ -81,6 +84,7 @@ zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, u
     q.cols = (uint32_t)k;
     q.q = ws + l.q;
     q.scale = reinterpret_cast<float*>(ws + l.scale);
+    q.ticket = reinterpret_cast<uint32_t*>(ws);
     if (x != nullptr && launch_quantize_rows(q, dtype, sms, stream) != cudaSuccess) return ZCCL_ERR_CUDA;
     MatmulArgs m{};
     m.a = q.q;
@@ -94,6 +98,7 @@ zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, u
     m.G = groups;
     m.out = out;
     m.out_f32 = out_dtype == ZCCL_F32;
+    m.ticket = reinterpret_cast<uint32_t*>(ws);
     m.status = status;
     return launched(launch_matmul(m, sms, stream));
 }
@@ -149,9 +154,9 @@ zccl_status_t zccl_fp8_linear_workspace_bytes(uint64_t rows, uint64_t k, uint64_
 {
     if (bytes == nullptr || !sizes_ok(rows, k, n, groups)) return ZCCL_ERR_INVALID_ARG;
     if (!backward) {
-        *bytes = takes_small(rows, groups) ? 256 : rows_layout(0, rows, k).end;
+        *bytes = takes_small(rows, groups) ? 256 : rows_layout(kTicketBytes, rows, k).end;
     } else {
-        const RowsLayout dy = rows_layout(0, rows, n), dyt = tokens_layout(dy.end, rows, n, groups);
+        const RowsLayout dy = rows_layout(kTicketBytes, rows, n), dyt = tokens_layout(dy.end, rows, n, groups);
         *bytes = tokens_layout(dyt.end, rows, k, groups).end;
     }
     return ZCCL_OK;
@@ -195,7 +200,7 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
     const int sms = sm_count();
     if (sms == 0) return ZCCL_ERR_CUDA;
     uint8_t* ws = reinterpret_cast<uint8_t*>(d_ws);
-    const RowsLayout dy = rows_layout(0, rows, n), dyt = tokens_layout(dy.end, rows, n, groups),
+    const RowsLayout dy = rows_layout(kTicketBytes, rows, n), dyt = tokens_layout(dy.end, rows, n, groups),
                      xt = tokens_layout(dyt.end, rows, k, groups);
     QuantArgs q{};
     q.rows = (uint32_t)rows;
@@ -211,6 +216,7 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
     if (both) {
         q.q_rows = ws + dy.q;
         q.scale_rows = reinterpret_cast<float*>(ws + dy.scale);
+        q.ticket = reinterpret_cast<uint32_t*>(ws);  // the product of the rows' gradient
     }
     if (d_grad_w != nullptr && rows > 0 && launch_quantize_tokens(q, dtype, sms, stream) != cudaSuccess)
         return ZCCL_ERR_CUDA;
@@ -228,7 +234,8 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
     r.q = ws + xt.q;
     r.scale = reinterpret_cast<float*>(ws + xt.scale);
     r.q_rows = nullptr;
-    if (rows > 0 && launch_quantize_tokens(r, dtype, sms, stream) != cudaSuccess) return ZCCL_ERR_CUDA;
+    r.ticket = reinterpret_cast<uint32_t*>(ws) + 32;
+    if (launch_quantize_tokens(r, dtype, sms, stream) != cudaSuccess) return ZCCL_ERR_CUDA;
     WgradArgs w{};
     w.a = q.q;
     w.sa = q.scale;
@@ -242,6 +249,7 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
     w.blocks = (uint32_t)token_blocks(rows, groups);
     w.out = d_grad_w;
     w.out_f32 = out_dtype == ZCCL_F32;
+    w.ticket = reinterpret_cast<uint32_t*>(ws) + 32;
     w.status = d_status;
     return launched(launch_wgrad(w, sms, stream));
 }

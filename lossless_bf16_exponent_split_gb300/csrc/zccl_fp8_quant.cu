@@ -16,6 +16,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRowsPerWarp = 8;  // rows in flight in a warp
 
+// The tile counter of the product that follows (every earlier use of it is over).
+__device__ __forceinline__ void zero_ticket(const QuantArgs& a)
+{
+    if (blockIdx.x == 0 && threadIdx.x == 0 && a.ticket != nullptr) *a.ticket = 0;
+}
+
 // Eight values of a row from column c on; zeros past the row's end.  kVec: the
 // eight are 16-byte aligned and either all in the row or all past it.
 template <typename T, bool kVec>
@@ -50,6 +56,7 @@ template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantArgs a)
 {
     pdl_wait();
+    zero_ticket(a);
     const uint32_t lane = threadIdx.x & 31, half = lane >> 4, i8 = (lane & 15) * 8;
     const uint32_t nb = (uint32_t)blocks_of(a.cols), pairs = (nb + 1) / 2;
     const uint64_t items = (uint64_t)pairs * ((a.rows + kRowsPerWarp - 1) / kRowsPerWarp);
@@ -120,6 +127,7 @@ __device__ __forceinline__ constexpr uint32_t owner_of(uint32_t row) { return 2 
 __global__ void __launch_bounds__(kThreads) quantize_rows_bf16_kernel(QuantArgs a)
 {
     pdl_wait();
+    zero_ticket(a);
     const uint32_t lane = threadIdx.x & 31, half = lane >> 4, i8 = (lane & 15) * 8;
     const uint32_t nb = (uint32_t)blocks_of(a.cols), pairs = (nb + 1) / 2;
     const uint32_t groups = (a.rows + kRowsPerWarp - 1) / kRowsPerWarp;
@@ -220,17 +228,19 @@ __global__ void __launch_bounds__(kThreads) quantize_tokens_kernel(QuantArgs a)
     __shared__ __align__(16) uint8_t tile[128 * 128];
     __shared__ float4 top[8][32];
     __shared__ uint32_t prefix[kMaxGroupsFp8 + 1];
+    __shared__ uint2 range[kMaxGroupsFp8];
     pdl_wait();
+    zero_ticket(a);
     const uint32_t lane = threadIdx.x & 31, part = threadIdx.x >> 5;
     group_prefix(a.offsets, a.rows, a.G, kFp8Block, (uint32_t)(a.rows / kFp8Block + a.G), prefix);
+    for (uint32_t g = threadIdx.x; g < a.G; g += kThreads) group_rows(a.offsets, a.rows, g, &range[g].x, &range[g].y);
     __syncthreads();
     const uint32_t tiles = (uint32_t)blocks_of(a.cols);
     const uint64_t items = (uint64_t)prefix[a.G] * tiles;
     for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const uint32_t tb = (uint32_t)(it / tiles), c = (uint32_t)(it % tiles) * kFp8Block + 4 * lane;
         const uint32_t g = group_at(prefix, a.G, tb);
-        uint32_t lo, hi;
-        group_rows(a.offsets, a.rows, g, &lo, &hi);
+        const uint32_t lo = range[g].x, hi = range[g].y;
         const uint32_t r0 = lo + (tb - prefix[g]) * kFp8Block + 16 * part;
         float v[16][4], m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -269,22 +279,24 @@ __global__ void __launch_bounds__(kThreads) quantize_tokens_kernel(QuantArgs a)
 // makes them), so that a gradient is read once for both its uses; the rows
 // outside every group get none.
 template <bool kRows>
-__global__ void __launch_bounds__(kThreads, 3) quantize_tokens_bf16_kernel(QuantArgs a)
+__global__ void __launch_bounds__(kThreads, kRows ? 3 : 4) quantize_tokens_bf16_kernel(QuantArgs a)
 {
     __shared__ __align__(16) uint8_t tile[128 * 128];
     __shared__ uint2 top[8][32];
     __shared__ uint32_t prefix[kMaxGroupsFp8 + 1];
+    __shared__ uint2 range[kMaxGroupsFp8];
     pdl_wait();
+    zero_ticket(a);
     const uint32_t lane = threadIdx.x & 31, part = threadIdx.x >> 5;
     group_prefix(a.offsets, a.rows, a.G, kFp8Block, (uint32_t)(a.rows / kFp8Block + a.G), prefix);
+    for (uint32_t g = threadIdx.x; g < a.G; g += kThreads) group_rows(a.offsets, a.rows, g, &range[g].x, &range[g].y);
     __syncthreads();
     const uint32_t tiles = (uint32_t)blocks_of(a.cols);
     const uint64_t items = (uint64_t)prefix[a.G] * tiles;
     for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const uint32_t tb = (uint32_t)(it / tiles), cb = (uint32_t)(it - (uint64_t)tb * tiles), c = cb * kFp8Block + 4 * lane;
         const uint32_t g = group_at(prefix, a.G, tb);
-        uint32_t lo, hi;
-        group_rows(a.offsets, a.rows, g, &lo, &hi);
+        const uint32_t lo = range[g].x, hi = range[g].y;
         const uint32_t r0 = lo + (tb - prefix[g]) * kFp8Block + 16 * part;
         const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x) + (uint64_t)r0 * a.stride + c;
         uint2 v[16];
@@ -434,7 +446,7 @@ cudaError_t quantize_tokens_as(const QuantArgs& a, int sms, cudaStream_t stream)
     int per_sm = 2;
     if (sizeof(T) == 2 && vectored<T>(a, 4)) {
         kernel = a.q_rows != nullptr ? quantize_tokens_bf16_kernel<true> : quantize_tokens_bf16_kernel<false>;
-        per_sm = 4;
+        per_sm = a.q_rows != nullptr ? 3 : 4;
     } else if (vectored<T>(a, 4)) {
         kernel = quantize_tokens_kernel<T, true>;
     }
