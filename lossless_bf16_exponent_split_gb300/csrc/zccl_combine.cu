@@ -52,14 +52,20 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(CombineArgs a, uint32
     for (uint32_t c = at; c < a.pieces; c += lanes) {
         float acc[8] = {};
         for (uint32_t k0 = 0; k0 < a.K; k0 += 8) {
-            uint4 v[8];
+            // the places first: a load behind each would wait for it
+            int32_t row[8];
             float w[8];
 #pragma unroll
             for (uint32_t k = 0; k < 8; ++k) {
-                const int32_t row = k0 + k < a.K ? pos[k0 + k] : -1;
-                const bool there = row >= 0 && (uint64_t)row < a.rows;
-                w[k] = there ? (weights != nullptr ? weights[k0 + k] : 1.0f) : 0.0f;
-                v[k] = there ? ld_once(reinterpret_cast<const uint4*>(a.y) + (uint64_t)row * a.pieces + c)
+                row[k] = k0 + k < a.K ? pos[k0 + k] : -1;
+                w[k] = weights == nullptr ? 1.0f : k0 + k < a.K ? weights[k0 + k] : 0.0f;
+            }
+            uint4 v[8];
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) {
+                const bool there = row[k] >= 0 && (uint64_t)row[k] < a.rows;
+                if (!there) w[k] = 0.0f;
+                v[k] = there ? ld_once(reinterpret_cast<const uint4*>(a.y) + (uint64_t)row[k] * a.pieces + c)
                              : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll

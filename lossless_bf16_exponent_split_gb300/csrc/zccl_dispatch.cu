@@ -16,7 +16,8 @@ namespace zccl {
 
 namespace {
 
-constexpr uint32_t kMoveThreads = 1024;
+constexpr uint32_t kMoveThreads = 512;
+constexpr uint32_t kFlight = 4;  // pieces of rows in flight in a thread
 constexpr uint32_t kMoveWarps = kMoveThreads / 32;
 // Up to this many slots every CTA counts them all itself.
 constexpr uint64_t kSmallSlots = 2048;
@@ -191,14 +192,24 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_move_kernel(DispatchArg
         __syncthreads();
         if (a.x != nullptr) {
             const uint32_t total = tokens * a.pieces;
-            for (uint32_t p = tid; p < total; p += kMoveThreads) {
-                const uint32_t t = p / a.pieces, c = p - t * a.pieces;
-                const uint4 v = ld_once(reinterpret_cast<const uint4*>(a.x + (t0 + t) * a.stride) + c);
-                for (uint32_t k = 0; k < a.K; ++k) {
-                    const int32_t row = place[t * a.K + k];
-                    uint4* dst = reinterpret_cast<uint4*>(a.rows) + (uint64_t)(row < 0 ? ~row : row) * a.pieces + c;
-                    *dst = row < 0 ? make_uint4(0, 0, 0, 0) : v;
+            for (uint32_t p0 = tid; p0 < total; p0 += kFlight * kMoveThreads) {
+                uint4 v[kFlight];
+                uint32_t t[kFlight], c[kFlight];
+#pragma unroll
+                for (uint32_t f = 0; f < kFlight; ++f) {
+                    const uint32_t p = min(p0 + f * kMoveThreads, total - 1);
+                    t[f] = p / a.pieces;
+                    c[f] = p - t[f] * a.pieces;
+                    v[f] = ld_once(reinterpret_cast<const uint4*>(a.x + (t0 + t[f]) * a.stride) + c[f]);
                 }
+#pragma unroll
+                for (uint32_t f = 0; f < kFlight; ++f)
+                    if (p0 + f * kMoveThreads < total)
+                        for (uint32_t k = 0; k < a.K; ++k) {
+                            const int32_t row = place[t[f] * a.K + k];
+                            uint4* dst = reinterpret_cast<uint4*>(a.rows) + (uint64_t)(row < 0 ? ~row : row) * a.pieces + c[f];
+                            *dst = row < 0 ? make_uint4(0, 0, 0, 0) : v[f];
+                        }
             }
         }
         __syncthreads();

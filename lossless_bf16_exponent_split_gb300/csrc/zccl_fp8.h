@@ -62,19 +62,6 @@ struct WgradArgs {
     uint32_t* status;
 };
 
-// Few rows a group: x itself (BF16 or fp32), quantised on the fly.
-struct SmallArgs {
-    const void* x;
-    uint64_t stride;
-    uint32_t K;
-    const uint8_t* b;
-    const float* sb;
-    const int32_t* offsets;
-    uint32_t rows, n, KB, G;
-    void* out;
-    int out_f32;
-};
-
 struct QuantArgs {
     const void* x;
     uint64_t stride;
@@ -99,7 +86,7 @@ struct PackArgs {
 
 cudaError_t launch_matmul(const MatmulArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_wgrad(const WgradArgs& a, int sms, cudaStream_t stream);
-cudaError_t launch_small(const SmallArgs& a, int dtype, int sms, cudaStream_t stream);
+cudaError_t launch_small(const MatmulArgs& a, int sms, cudaStream_t stream);  // few rows a group
 cudaError_t launch_quantize_rows(const QuantArgs& a, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_quantize_tokens(const QuantArgs& a, int dtype, int sms, cudaStream_t stream);
 // Whether launch_quantize_tokens can make the blocks of each row, too.

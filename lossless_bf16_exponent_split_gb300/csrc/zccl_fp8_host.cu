@@ -53,29 +53,13 @@ RowsLayout tokens_layout(uint64_t at, uint64_t rows, uint64_t cols, uint32_t gro
 
 bool takes_small(uint64_t rows, uint32_t groups) { return rows <= kSmallRows * groups; }
 
-// y = x times the transpose of the packed weight [groups][n][k].  x nullptr (and
-// not few rows): x is quantised in the workspace already.
+// y = x times the transpose of the packed weight [groups][n][k].  x nullptr: x is
+// quantised in the workspace already.
 zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, uint64_t k, const uint8_t* weight, uint64_t n,
                      uint32_t groups, const int32_t* offsets, void* out, int out_dtype, uint8_t* ws, uint32_t* status,
                      int sms, cudaStream_t stream)
 {
     const float* sb = reinterpret_cast<const float*>(weight + weight_code_bytes(groups, n, k));
-    if (takes_small(rows, groups)) {
-        SmallArgs s{};
-        s.x = x;
-        s.stride = stride;
-        s.K = (uint32_t)k;
-        s.b = weight;
-        s.sb = sb;
-        s.offsets = offsets;
-        s.rows = (uint32_t)rows;
-        s.n = (uint32_t)n;
-        s.KB = (uint32_t)blocks_of(k);
-        s.G = groups;
-        s.out = out;
-        s.out_f32 = out_dtype == ZCCL_F32;
-        return launched(launch_small(s, dtype, sms, stream));
-    }
     const RowsLayout l = rows_layout(kTicketBytes, rows, k);
     QuantArgs q{};
     q.x = x;
@@ -100,7 +84,7 @@ zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, u
     m.out_f32 = out_dtype == ZCCL_F32;
     m.ticket = reinterpret_cast<uint32_t*>(ws);
     m.status = status;
-    return launched(launch_matmul(m, sms, stream));
+    return launched(takes_small(rows, groups) ? launch_small(m, sms, stream) : launch_matmul(m, sms, stream));
 }
 
 }  // namespace
@@ -154,7 +138,7 @@ zccl_status_t zccl_fp8_linear_workspace_bytes(uint64_t rows, uint64_t k, uint64_
 {
     if (bytes == nullptr || !sizes_ok(rows, k, n, groups)) return ZCCL_ERR_INVALID_ARG;
     if (!backward) {
-        *bytes = takes_small(rows, groups) ? 256 : rows_layout(kTicketBytes, rows, k).end;
+        *bytes = rows_layout(kTicketBytes, rows, k).end;
     } else {
         const RowsLayout dy = rows_layout(kTicketBytes, rows, n), dyt = tokens_layout(dy.end, rows, n, groups);
         *bytes = tokens_layout(dyt.end, rows, k, groups).end;
@@ -211,8 +195,7 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
     q.cols = (uint32_t)n;
     q.q = ws + dyt.q;
     q.scale = reinterpret_cast<float*>(ws + dyt.scale);
-    const bool small = takes_small(rows, groups);
-    const bool both = d_grad_w != nullptr && d_grad_x != nullptr && rows > 0 && !small && quantizes_both(q, dtype);
+    const bool both = d_grad_w != nullptr && d_grad_x != nullptr && rows > 0 && quantizes_both(q, dtype);
     if (both) {
         q.q_rows = ws + dy.q;
         q.scale_rows = reinterpret_cast<float*>(ws + dy.scale);

@@ -5,9 +5,10 @@
 // built to stream them: a warp reads 16 weight rows of a block (2 KB, straight
 // to registers in the layout of the 16 x 8 x 32 matrix instruction: the order
 // of the values along the reduction axis is free as long as both operands share
-// it), and the eight warps of a CTA split the reduction and add up in shared
-// memory.  The rows are quantised on the fly, in registers, so a call is one
-// launch.  The products are exact in the instruction; sums are fp32.
+// it) and multiplies them with 8 rows of x, or two or four times as many.  Where
+// there are too few such pieces for the GPU's warps, up to eight warps split the
+// reduction and add up in shared memory.  Products are exact in the instruction;
+// sums are fp32, in an order that depends on the sizes only.
 #include "zccl_fp8.cuh"
 
 namespace zccl {
@@ -16,7 +17,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr uint32_t kTileRows = 16;  // weight rows of an item
+constexpr uint32_t kTileRows = 16;  // weight rows of a warp
+constexpr int kFlight = 2;          // blocks in flight in a warp
 
 __device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                             uint32_t b1)
@@ -26,153 +28,148 @@ __device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 values of a row from column c on, zeros past its end or without a row.
-template <typename T, bool kVec>
-__device__ __forceinline__ void load16(const T* row, uint32_t c, uint32_t cols, bool on, float (&v)[16])
+// `split` warps (1, 2, 4 or 8) share a warp's weight rows.
+template <typename T, int kNT>
+__global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) small_kernel(MatmulArgs a, uint32_t split)
 {
-    if (kVec) {
-        constexpr int kLoads = 16 * sizeof(T) / 16, kPer = 16 / kLoads;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const bool in = on && c + i * kPer < cols;
-            const uint4 p = in ? *(reinterpret_cast<const uint4*>(row + c) + i) : make_uint4(0, 0, 0, 0);
-            const uint32_t q[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (sizeof(T) == 2) {
-                    v[i * 8 + 2 * j] = bf16_lo(q[j]);
-                    v[i * 8 + 2 * j + 1] = bf16_hi(q[j]);
-                } else {
-                    v[i * 4 + j] = __uint_as_float(q[j]);
-                }
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = on && c + i < cols ? to_float<T>(row[c + i]) : 0.0f;
-    }
-}
-
-template <typename T, bool kVec, int kNT>
-__global__ void __launch_bounds__(kThreads) small_kernel(SmallArgs a)
-{
-    constexpr uint32_t kChunk = 8 * kNT;  // rows of an item
+    constexpr uint32_t kChunk = 8 * kNT;  // rows of x
     __shared__ float sums[kWarps][kNT * 4][32];
     __shared__ uint32_t prefix[kMaxGroupsFp8 + 1];
+    __shared__ uint2 range[kMaxGroupsFp8];
     pdl_wait();
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, q = lane & 3;
     group_prefix(a.offsets, a.rows, a.G, kChunk, 0x7FFFFFFFu, prefix);
+    for (uint32_t g = threadIdx.x; g < a.G; g += kThreads) group_rows(a.offsets, a.rows, g, &range[g].x, &range[g].y);
     __syncthreads();
-    const uint32_t tiles = (a.n + kTileRows - 1) / kTileRows, nbs = (uint32_t)blocks_of(a.n);
+    const uint32_t nbs = (uint32_t)blocks_of(a.n), wide = kWarps / split * kTileRows;  // weight rows of a CTA
+    const uint32_t tiles = (a.n + wide - 1) / wide, first = warp % split;
     const uint64_t items = (uint64_t)prefix[a.G] * tiles;
     for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const uint32_t chunk = (uint32_t)(it / tiles), n0 = (uint32_t)(it % tiles) * kTileRows;
+        const uint32_t chunk = (uint32_t)(it / tiles);
+        const uint32_t n0 = (uint32_t)(it - (uint64_t)chunk * tiles) * wide + warp / split * kTileRows;
         const uint32_t g = group_at(prefix, a.G, chunk);
-        uint32_t lo, hi;
-        group_rows(a.offsets, a.rows, g, &lo, &hi);
-        const uint32_t r0 = lo + (chunk - prefix[g]) * kChunk, count = min(kChunk, hi - r0);
-        const uint32_t na = min(n0 + gq, a.n - 1), nb = min(n0 + gq + 8, a.n - 1);
-        const float* sb = a.sb + ((uint64_t)g * nbs + n0 / kFp8Block) * a.KB;
+        const uint32_t r0 = range[g].x + (chunk - prefix[g]) * kChunk, count = min(kChunk, range[g].y - r0);
         float acc[kNT][4] = {};
-#pragma unroll 2
-        for (uint32_t kb = warp; kb < a.KB; kb += kWarps) {
-            const uint8_t* base = a.b + ((uint64_t)g * a.KB + kb) * a.n * kFp8Block + q * 16;
-            const uint4 wa0 = ld_once(reinterpret_cast<const uint4*>(base + (uint64_t)na * kFp8Block));
-            const uint4 wa1 = ld_once(reinterpret_cast<const uint4*>(base + (uint64_t)na * kFp8Block + 64));
-            const uint4 wb0 = ld_once(reinterpret_cast<const uint4*>(base + (uint64_t)nb * kFp8Block));
-            const uint4 wb1 = ld_once(reinterpret_cast<const uint4*>(base + (uint64_t)nb * kFp8Block + 64));
-            const float sw = sb[kb];
+        if (n0 < a.n) {
+            // lanes past the weight's or x's last row read that row and drop the result
+            const uint8_t* const wa = a.b + ((uint64_t)g * a.KB * a.n + min(n0 + gq, a.n - 1)) * kFp8Block + q * 16;
+            const uint8_t* const wb = a.b + ((uint64_t)g * a.KB * a.n + min(n0 + gq + 8, a.n - 1)) * kFp8Block + q * 16;
+            const float* const sb = a.sb + ((uint64_t)g * nbs + n0 / kFp8Block) * a.KB;
+            const uint64_t wstep = (uint64_t)a.n * kFp8Block, xstep = (uint64_t)a.rows * kFp8Block;
+            for (uint32_t kb0 = first; kb0 < a.KB; kb0 += kFlight * split) {
+                uint4 w[kFlight][4], x[kFlight][kNT][2];
+                float s[kFlight][kNT][2], sw[kFlight];
 #pragma unroll
-            for (int t = 0; t < kNT; ++t) {
-                const uint32_t r = t * 8 + gq;
-                const bool on = r < count;
-                const T* row = reinterpret_cast<const T*>(a.x) + (uint64_t)(r0 + (on ? r : 0)) * a.stride;
-                float v0[16], v1[16], amax = 0.0f;
-                load16<T, kVec>(row, kb * kFp8Block + q * 16, a.K, on, v0);
-                load16<T, kVec>(row, kb * kFp8Block + q * 16 + 64, a.K, on, v1);
+                for (int f = 0; f < kFlight; ++f) {
+                    const uint32_t kb = min(kb0 + f * split, a.KB - 1);
+                    w[f][0] = ld_once(reinterpret_cast<const uint4*>(wa + kb * wstep));
+                    w[f][1] = ld_once(reinterpret_cast<const uint4*>(wa + kb * wstep + 64));
+                    w[f][2] = ld_once(reinterpret_cast<const uint4*>(wb + kb * wstep));
+                    w[f][3] = ld_once(reinterpret_cast<const uint4*>(wb + kb * wstep + 64));
+                }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fmaxf(fabsf(v0[i]), fabsf(v1[i])));
-                amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-                amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-                float scale, f;
-                block_scale(amax, &scale, &f);
-                uint32_t x0[4], x1[4];
+                for (int f = 0; f < kFlight; ++f) {
+                    const uint32_t kb = min(kb0 + f * split, a.KB - 1);
+                    sw[f] = kb0 + f * split < a.KB ? sb[kb] : 0.0f;  // a block too many adds nothing
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) {
+                        const uint8_t* xr = a.a + kb * xstep + (uint64_t)(r0 + min(t * 8 + gq, count - 1)) * kFp8Block + q * 16;
+                        x[f][t][0] = *reinterpret_cast<const uint4*>(xr);
+                        x[f][t][1] = *reinterpret_cast<const uint4*>(xr + 64);
+                        // the instruction's columns are rows 2 q and 2 q + 1
+                        const float* xs = a.sa + (uint64_t)kb * a.rows + r0;
+                        s[f][t][0] = xs[min(t * 8 + 2 * q, count - 1)];
+                        s[f][t][1] = xs[min(t * 8 + 2 * q + 1, count - 1)];
+                    }
+                }
+#pragma unroll
+                for (int f = 0; f < kFlight; ++f) {
+                    if (kb0 + f * split >= a.KB) break;
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t) {
+                        const uint4 x0 = x[f][t][0], x1 = x[f][t][1];
+                        float d[4] = {};
+                        mma_16x8x32(d, w[f][0].x, w[f][2].x, w[f][0].y, w[f][2].y, x0.x, x0.y);
+                        mma_16x8x32(d, w[f][0].z, w[f][2].z, w[f][0].w, w[f][2].w, x0.z, x0.w);
+                        mma_16x8x32(d, w[f][1].x, w[f][3].x, w[f][1].y, w[f][3].y, x1.x, x1.y);
+                        mma_16x8x32(d, w[f][1].z, w[f][3].z, w[f][1].w, w[f][3].w, x1.z, x1.w);
+                        const float s0 = s[f][t][0] * sw[f], s1 = s[f][t][1] * sw[f];
+                        acc[t][0] = fmaf(d[0], s0, acc[t][0]);
+                        acc[t][1] = fmaf(d[1], s1, acc[t][1]);
+                        acc[t][2] = fmaf(d[2], s0, acc[t][2]);
+                        acc[t][3] = fmaf(d[3], s1, acc[t][3]);
+                    }
+                }
+            }
+        }
+        if (split > 1) {
+#pragma unroll
+            for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sums[warp][t * 4 + i][lane] = acc[t][i];
+            __syncthreads();
+            if (first == 0)
+#pragma unroll
+                for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        for (uint32_t w = 1; w < split; ++w) acc[t][i] += sums[warp + w][t * 4 + i][lane];
+            __syncthreads();
+        }
+        if (first == 0)
+#pragma unroll
+            for (int t = 0; t < kNT; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x0[i] = e4m3x4(v0[4 * i] * f, v0[4 * i + 1] * f, v0[4 * i + 2] * f, v0[4 * i + 3] * f);
-                    x1[i] = e4m3x4(v1[4 * i] * f, v1[4 * i + 1] * f, v1[4 * i + 2] * f, v1[4 * i + 3] * f);
+                    const uint32_t r = t * 8 + 2 * q + (i & 1), n = n0 + gq + 8 * (i >> 1);
+                    if (r < count && n < a.n) reinterpret_cast<T*>(a.out)[(uint64_t)(r0 + r) * a.n + n] = from_float<T>(acc[t][i]);
                 }
-                float d[4] = {};
-                mma_16x8x32(d, wa0.x, wb0.x, wa0.y, wb0.y, x0[0], x0[1]);
-                mma_16x8x32(d, wa0.z, wb0.z, wa0.w, wb0.w, x0[2], x0[3]);
-                mma_16x8x32(d, wa1.x, wb1.x, wa1.y, wb1.y, x1[0], x1[1]);
-                mma_16x8x32(d, wa1.z, wb1.z, wa1.w, wb1.w, x1[2], x1[3]);
-                // the instruction's columns are rows 2 q and 2 q + 1 of x
-                const float s0 = sw * __shfl_sync(0xFFFFFFFFu, scale, 8 * q);
-                const float s1 = sw * __shfl_sync(0xFFFFFFFFu, scale, 8 * q + 4);
-                acc[t][0] = fmaf(d[0], s0, acc[t][0]);
-                acc[t][1] = fmaf(d[1], s1, acc[t][1]);
-                acc[t][2] = fmaf(d[2], s0, acc[t][2]);
-                acc[t][3] = fmaf(d[3], s1, acc[t][3]);
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < kNT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sums[warp][t * 4 + i][lane] = acc[t][i];
-        __syncthreads();
-        for (uint32_t o = threadIdx.x; o < kChunk * kTileRows; o += kThreads) {
-            const uint32_t t = o / kTileRows, n = o % kTileRows;
-            const uint32_t i = (t / 8) * 4 + (n / 8) * 2 + (t & 1), l = (n % 8) * 4 + (t % 8) / 2;
-            float sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) sum += sums[w][i][l];
-            if (t < count && n0 + n < a.n) {
-                const uint64_t at = (uint64_t)(r0 + t) * a.n + n0 + n;
-                if (a.out_f32)
-                    reinterpret_cast<float*>(a.out)[at] = sum;
-                else
-                    reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(sum);
-            }
-        }
-        __syncthreads();
     }
     // rows outside every group
     if (a.offsets != nullptr) {
         const int32_t t = ld_l2(a.offsets + a.G);
         const uint64_t tail = t < 0 ? 0u : min((uint32_t)t, a.rows), n = (uint64_t)a.rows * a.n;
-        for (uint64_t i = tail * a.n + blockIdx.x * kThreads + threadIdx.x; i < n; i += (uint64_t)gridDim.x * kThreads) {
-            if (a.out_f32)
-                reinterpret_cast<float*>(a.out)[i] = 0.0f;
-            else
-                reinterpret_cast<uint16_t*>(a.out)[i] = 0;
-        }
+        for (uint64_t i = tail * a.n + blockIdx.x * kThreads + threadIdx.x; i < n; i += (uint64_t)gridDim.x * kThreads)
+            reinterpret_cast<T*>(a.out)[i] = from_float<T>(0.0f);
     }
 }
 
-template <typename T, bool kVec>
-cudaError_t small_as(const SmallArgs& a, int sms, cudaStream_t stream)
+template <typename T, int kNT>
+cudaError_t small_as(const MatmulArgs& a, int sms, cudaStream_t stream)
 {
-    // rows an item takes: the mean rows of a group, rounded up to 8, 16 or 32
+    constexpr int kPerSm = kNT == 1 ? 4 : kNT == 2 ? 3 : 2;
+    // warps at work: at least 16 an SM, by splitting the reduction where the weight rows (of every group that can
+    // have rows) do not give that many.  4096 x 14336 with one row: 9.9 us split four ways, 14.2 not split.
+    const uint64_t groups = a.rows < a.G ? a.rows : a.G, pieces = groups * ((a.n + kTileRows - 1) / kTileRows);
+    uint32_t split = 1;
+    while (split < kWarps && split < a.KB && pieces * split < (uint64_t)sms * 16) split *= 2;
+    const uint32_t wide = kWarps / split * kTileRows;
+    const uint64_t items = ((uint64_t)a.rows / (8 * kNT) + a.G) * ((a.n + wide - 1) / wide), most = (uint64_t)sms * kPerSm;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((uint32_t)(items < most ? items : most));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, small_kernel<T, kNT>, a, split);
+}
+
+template <typename T>
+cudaError_t small_typed(const MatmulArgs& a, int sms, cudaStream_t stream)
+{
+    // rows a warp takes: the mean rows of a group, rounded up to 8, 16 or 32
     const uint32_t mean = (a.rows + a.G - 1) / a.G;
-    const uint32_t chunk = mean <= 8 ? 8 : mean <= 16 ? 16 : 32;
-    const uint64_t items = ((uint64_t)a.rows / chunk + a.G) * ((a.n + kTileRows - 1) / kTileRows);
-    const uint64_t most = (uint64_t)sms * 4;
-    const uint32_t grid = (uint32_t)(items < most ? items : most);
-    if (chunk == 8) return launch_dependent(small_kernel<T, kVec, 1>, grid, kThreads, 0, stream, a);
-    if (chunk == 16) return launch_dependent(small_kernel<T, kVec, 2>, grid, kThreads, 0, stream, a);
-    return launch_dependent(small_kernel<T, kVec, 4>, grid, kThreads, 0, stream, a);
+    return mean <= 8 ? small_as<T, 1>(a, sms, stream) : mean <= 16 ? small_as<T, 2>(a, sms, stream) : small_as<T, 4>(a, sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_small(const SmallArgs& a, int dtype, int sms, cudaStream_t stream)
+cudaError_t launch_small(const MatmulArgs& a, int sms, cudaStream_t stream)
 {
-    const uint32_t values = dtype == ZCCL_BF16 ? 8 : 4;
-    const bool vec = a.K % values == 0 && a.stride % values == 0 && is_aligned(a.x, 16);
-    if (dtype == ZCCL_BF16)
-        return vec ? small_as<__nv_bfloat16, true>(a, sms, stream) : small_as<__nv_bfloat16, false>(a, sms, stream);
-    return vec ? small_as<float, true>(a, sms, stream) : small_as<float, false>(a, sms, stream);
+    return a.out_f32 ? small_typed<float>(a, sms, stream) : small_typed<__nv_bfloat16>(a, sms, stream);
 }
 
 }  // namespace zccl

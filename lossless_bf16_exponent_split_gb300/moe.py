@@ -44,24 +44,30 @@ class Workspaces:
         return ws
 
 
+# The handle of the current stream, without building a Stream object where PyTorch offers it (2 us less a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def current_stream(device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
 def need(t: torch.Tensor, what: str, device, dtypes, ndim: int, rows_strided: bool = False) -> torch.Tensor:
     """Checks a tensor argument: device, type and layout (contiguous, or with
     rows_strided a matrix whose rows are contiguous)."""
-    if not torch.is_tensor(t) or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.device != device:
         raise ValueError(f"{what}: expected a tensor on {device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{what}: expected {ndim} dimensions, got {t.dim()}")
-    if rows_strided:
+    if not t.is_contiguous():
+        if not rows_strided:
+            raise ValueError(f"{what}: expected a contiguous tensor")
         if t.shape[0] > 0 and t.shape[1] > 1 and t.stride(1) != 1:
             raise ValueError(f"{what}: the values of a row have to be contiguous")
-    elif not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous tensor")
     return t
 
 
@@ -87,6 +93,8 @@ class Moe:
         self.device = torch.zeros(0, device=device if device is not None else "cuda").device
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._workspaces = Workspaces()
+        # the workspace for any number of tokens
+        self._ws_bytes = zccl_dispatch_workspace_bytes((1 << 31) // self.top_k - 1, self.experts, self.top_k)
 
     # -- status ---------------------------------------------------------------
     def reset_status(self):
@@ -103,13 +111,15 @@ class Moe:
     # -- calls ----------------------------------------------------------------
     def _logits(self, logits):
         need(logits, "logits", self.device, _DTYPES, 2, rows_strided=True)
-        if logits.shape[1] != self.experts:
-            raise ValueError(f"logits: expected {self.experts} columns, got {logits.shape[1]}")
-        return logits.shape[0], logits.stride(0), _DTYPES[logits.dtype]
+        tokens, experts = logits.shape
+        if experts != self.experts:
+            raise ValueError(f"logits: expected {self.experts} columns, got {experts}")
+        return tokens, logits.stride(0), _DTYPES[logits.dtype]
 
     def _slots(self, t, what, dtype, tokens=None):
         need(t, what, self.device, (dtype,), 2)
-        if t.shape[1] != self.top_k or (tokens is not None and t.shape[0] != tokens):
+        shape = t.shape
+        if shape[1] != self.top_k or (tokens is not None and shape[0] != tokens):
             raise ValueError(f"{what}: expected shape [{'tokens' if tokens is None else tokens}, {self.top_k}]")
         return t
 
@@ -153,8 +163,8 @@ class Moe:
         slots = tokens * self.top_k
         rows = torch.empty(slots, hidden, dtype=torch.bfloat16, device=self.device)
         pos = torch.empty(tokens, self.top_k, dtype=torch.int32, device=self.device)
-        places = torch.empty(2 * self.experts + 1, dtype=torch.int32, device=self.device)
-        counts, offsets = places[: self.experts], places[self.experts:]
+        counts = torch.empty(self.experts, dtype=torch.int32, device=self.device)
+        offsets = torch.empty(self.experts + 1, dtype=torch.int32, device=self.device)
         table = streams = None
         room = 0
         if capacity is not None:
@@ -164,7 +174,7 @@ class Moe:
             table = torch.empty(2 * self.experts * SEGMENT_DTYPE.itemsize, dtype=torch.uint8, device=self.device)
             streams = torch.empty(room, dtype=torch.uint8, device=self.device)
         stream = current_stream(self.device)
-        ws = self._workspaces.get(zccl_dispatch_workspace_bytes(tokens, self.experts, self.top_k), stream, self.device)
+        ws = self._workspaces.get(self._ws_bytes, stream, self.device)
         st = self._lib.zccl_dispatch(
             idx.data_ptr(), tokens, self.experts, self.top_k, x.data_ptr() if slots else None,
             x.stride(0) if tokens > 1 else hidden, hidden, rows.data_ptr(), pos.data_ptr(), counts.data_ptr(),
