@@ -4,9 +4,10 @@
 // A stable counting sort of the T * K slots by expert.  The slots are cut into
 // tiles of whole tokens, one per CTA.  Few slots: one kernel, every CTA counts
 // all slots itself.  Many: a first kernel counts each tile's slots per expert,
-// and its last CTA turns the counts into places (no CTA waits for another);
-// the second kernel ranks its tile's slots and moves the rows.  A token's row
-// is read once and stored K times.  Slots without an expert sort last and
+// one tile per SM, and its last CTA turns the counts into places (no CTA waits
+// for another); in the second kernel 32 CTAs share a tile, each counts the
+// slots of the tile before its own, ranks those and moves the rows.  A token's
+// row is read once and stored K times.  Slots without an expert sort last and
 // store zeros, so every row is written exactly once.
 //
 // Bound by HBM: 2 T H bytes read, 2 T K H written.
@@ -16,7 +17,10 @@ namespace zccl {
 
 namespace {
 
-constexpr uint32_t kMoveThreads = 512;
+constexpr uint32_t kMoveThreads = 256;
+constexpr uint32_t kCountThreads = 512;
+constexpr uint32_t kSubTiles = 32;  // CTAs that move a counted tile's rows: 94 us for the all-to-all's rows, 101 with 8,
+                                    // 106 with 4 (more, smaller CTAs end closer together)
 constexpr uint32_t kFlight = 4;  // pieces of rows in flight in a thread
 constexpr uint32_t kMoveWarps = kMoveThreads / 32;
 // Up to this many slots every CTA counts them all itself.
@@ -37,8 +41,9 @@ struct DispatchArgs {
     zccl_segment_t* segs;
     uint64_t capacity;
     uint8_t* streams;
-    uint32_t tiles;        // CTAs
+    uint32_t tiles;        // tiles that are counted
     uint32_t tile_tokens;  // tokens of a tile
+    uint32_t sub_tokens;   // tokens of a CTA that moves rows
     uint32_t* ticket;      // CTAs of the counting kernel that are done
     int32_t* base;         // [E + 1][tiles]: a tile's count of an expert's slots, then its first row
 };
@@ -93,33 +98,48 @@ __device__ void write_tables(const DispatchArgs& a, const int32_t* first)
 // Counts each tile's slots per expert; the last CTA done makes the counts
 // places.  base is expert-major, so a warp turns an expert's counts into a
 // prefix sum with coalesced loads.
-__global__ void __launch_bounds__(kMoveThreads) dispatch_count_kernel(DispatchArgs a)
+__global__ void __launch_bounds__(kCountThreads) dispatch_count_kernel(DispatchArgs a)
 {
     __shared__ int32_t count[ZCCL_MAX_EXPERTS + 2];
     __shared__ uint32_t order;
     pdl_wait();
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (uint32_t e = tid; e <= a.E; e += kMoveThreads) count[e] = 0;
+    for (uint32_t e = tid; e <= a.E; e += kCountThreads) count[e] = 0;
     __syncthreads();
     const uint64_t lo = (uint64_t)blockIdx.x * a.tile_tokens * a.K;
     const uint64_t hi = min((uint64_t)(blockIdx.x + 1) * a.tile_tokens, a.tokens) * a.K;
-    for (uint64_t i = lo + tid; i < hi; i += kMoveThreads) atomicAdd(&count[bucket_of(a.idx[i], a.E)], 1);
+    for (uint64_t i = lo + tid; i < hi; i += kCountThreads) atomicAdd(&count[bucket_of(a.idx[i], a.E)], 1);
     __syncthreads();
-    for (uint32_t e = tid; e <= a.E; e += kMoveThreads) a.base[(uint64_t)e * a.tiles + blockIdx.x] = count[e];
+    for (uint32_t e = tid; e <= a.E; e += kCountThreads) a.base[(uint64_t)e * a.tiles + blockIdx.x] = count[e];
     __threadfence();
     __syncthreads();
     if (tid == 0) order = atom_inc_acq_rel(a.ticket, a.tiles - 1);  // wraps to 0 for the next call
     __syncthreads();
     if (order != a.tiles - 1) return;
     __threadfence();
-    for (uint32_t e = warp; e <= a.E; e += kMoveWarps) {
+    for (uint32_t e = warp; e <= a.E; e += kCountThreads / 32) {
         int32_t* col = a.base + (uint64_t)e * a.tiles;
         int32_t run = 0;
-        for (uint32_t i = 0; i < a.tiles; i += 32) {
-            const int32_t c = i + lane < a.tiles ? ld_l2(col + i + lane) : 0;
-            const int32_t incl = (int32_t)warp_scan((uint64_t)c);
-            if (i + lane < a.tiles) col[i + lane] = run + incl - c;
-            run += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        constexpr uint32_t kAhead = 8;  // loads in flight: one behind the other they cost 20 us
+        for (uint32_t i0 = 0; i0 < a.tiles; i0 += 32 * kAhead) {
+            int32_t c[kAhead];
+#pragma unroll
+            for (uint32_t j = 0; j < kAhead; ++j) {
+                const uint32_t i = i0 + 32 * j + lane;
+                c[j] = i < a.tiles ? ld_l2(col + i) : 0;
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < kAhead; ++j) {
+                const uint32_t i = i0 + 32 * j + lane;
+                int32_t incl = c[j];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int32_t t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                    if ((int)lane >= o) incl += t;
+                }
+                if (i < a.tiles) col[i] = run + incl - c[j];
+                run += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            }
         }
         if (lane == 0) count[e] = run;
     }
@@ -129,8 +149,8 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_count_kernel(DispatchAr
     write_tables(a, count);
 }
 
-// Ranks a tile's slots and moves their rows.  kSmall: the CTA counts all slots
-// and those before its tile itself (the counting kernel did not run).
+// Ranks a CTA's slots and moves their rows.  kSmall: the CTA counts all slots
+// and those before its own itself (the counting kernel did not run).
 template <bool kSmall>
 __global__ void __launch_bounds__(kMoveThreads) dispatch_move_kernel(DispatchArgs a)
 {
@@ -141,8 +161,11 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_move_kernel(DispatchArg
     int32_t* by_warp = place + kMoveThreads;        // [kMoveWarps][B]
     pdl_wait();
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint64_t lo = (uint64_t)blockIdx.x * a.tile_tokens;
-    const uint64_t hi = min(lo + a.tile_tokens, a.tokens);
+    const uint32_t counted = blockIdx.x / kSubTiles;  // the tile that was counted
+    const uint64_t tile = (uint64_t)counted * a.tile_tokens;
+    const uint64_t lo = kSmall ? (uint64_t)blockIdx.x * a.sub_tokens
+                               : min(tile + (uint64_t)(blockIdx.x % kSubTiles) * a.sub_tokens, a.tokens);
+    const uint64_t hi = min(kSmall ? lo + a.sub_tokens : min(lo + a.sub_tokens, tile + a.tile_tokens), a.tokens);
     if (kSmall) {
         int32_t* all = by_warp;
         int32_t* before = by_warp + B + 1;
@@ -161,7 +184,10 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_move_kernel(DispatchArg
         __syncthreads();
     } else {
         for (uint32_t e = tid; e < B; e += kMoveThreads)
-            first[e] = ld_l2(a.base + (uint64_t)e * a.tiles + blockIdx.x) + ld_l2(a.offsets + e);
+            first[e] = ld_l2(a.base + (uint64_t)e * a.tiles + counted) + ld_l2(a.offsets + e);
+        __syncthreads();
+        for (uint64_t i = tile * a.K + tid; i < lo * a.K; i += kMoveThreads) atomicAdd(&first[bucket_of(a.idx[i], a.E)], 1);
+        __syncthreads();
     }
     const uint32_t step = kMoveThreads / a.K;  // whole tokens of a round
     for (uint64_t t0 = lo; t0 < hi; t0 += step) {
@@ -208,7 +234,7 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_move_kernel(DispatchArg
                         for (uint32_t k = 0; k < a.K; ++k) {
                             const int32_t row = place[t[f] * a.K + k];
                             uint4* dst = reinterpret_cast<uint4*>(a.rows) + (uint64_t)(row < 0 ? ~row : row) * a.pieces + c[f];
-                            *dst = row < 0 ? make_uint4(0, 0, 0, 0) : v[f];
+                            __stcs(dst, row < 0 ? make_uint4(0, 0, 0, 0) : v[f]);
                         }
             }
         }
@@ -217,22 +243,23 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_move_kernel(DispatchArg
 }
 
 struct DispatchPlan {
-    uint32_t tiles, tile_tokens;
+    uint32_t tiles, tile_tokens, sub_tokens, ctas;
     bool small;
-    uint64_t bytes;
 };
 
-// Tiles of whole tokens, two CTAs per SM where there are tokens enough.
-DispatchPlan dispatch_plan(uint64_t tokens, uint32_t experts, uint32_t top_k, int sms)
+// Few slots: a CTA for a token, or for as many as make two CTAs per SM.  Many:
+// one counted tile per SM, moved by kSubTiles CTAs.
+DispatchPlan dispatch_plan(uint64_t tokens, uint32_t top_k, int sms)
 {
     DispatchPlan p{};
-    const uint64_t most = (uint64_t)sms * 2;
+    p.small = tokens * top_k <= kSmallSlots;
+    const uint64_t most = p.small ? (uint64_t)sms * 2 : (uint64_t)sms;
     p.tile_tokens = (uint32_t)((tokens + most - 1) / most);
     if (p.tile_tokens == 0) p.tile_tokens = 1;
     p.tiles = (uint32_t)((tokens + p.tile_tokens - 1) / p.tile_tokens);
     if (p.tiles == 0) p.tiles = 1;
-    p.small = tokens * top_k <= kSmallSlots;
-    p.bytes = round_up(256 + 4ull * (experts + 1) * (uint64_t)p.tiles, 256);
+    p.sub_tokens = p.small ? p.tile_tokens : (p.tile_tokens + kSubTiles - 1) / kSubTiles;
+    p.ctas = p.small ? p.tiles : p.tiles * kSubTiles;
     return p;
 }
 
@@ -290,7 +317,7 @@ zccl_status_t zccl_dispatch(const int32_t* d_idx, uint64_t tokens, uint32_t expe
     if (ws_bytes < need) return ZCCL_ERR_BUFFER_TOO_SMALL;
     const int sms = sm_count();
     if (sms == 0) return ZCCL_ERR_CUDA;
-    const DispatchPlan p = dispatch_plan(tokens, experts, top_k, sms < 512 ? sms : 512);
+    const DispatchPlan p = dispatch_plan(tokens, top_k, sms < 512 ? sms : 512);
     DispatchArgs a{};
     a.idx = d_idx;
     a.tokens = tokens;
@@ -309,6 +336,7 @@ zccl_status_t zccl_dispatch(const int32_t* d_idx, uint64_t tokens, uint32_t expe
     a.streams = reinterpret_cast<uint8_t*>(d_streams);
     a.tiles = p.tiles;
     a.tile_tokens = p.tile_tokens;
+    a.sub_tokens = p.sub_tokens;
     a.ticket = reinterpret_cast<uint32_t*>(d_ws);
     a.base = reinterpret_cast<int32_t*>((uint8_t*)d_ws + 256);
     const size_t smem = sizeof(int32_t) * ((experts + 1) + kMoveThreads + (size_t)(kMoveWarps + 1) * (experts + 1));
@@ -317,10 +345,10 @@ zccl_status_t zccl_dispatch(const int32_t* d_idx, uint64_t tokens, uint32_t expe
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return ZCCL_ERR_CUDA;
     if (!p.small) {
-        const cudaError_t e = launch_dependent(dispatch_count_kernel, p.tiles, kMoveThreads, 0, stream, a);
+        const cudaError_t e = launch_dependent(dispatch_count_kernel, p.tiles, kCountThreads, 0, stream, a);
         if (e != cudaSuccess) return ZCCL_ERR_CUDA;
     }
-    return launched(launch_dependent(kernel, p.tiles, kMoveThreads, smem, stream, a));
+    return launched(launch_dependent(kernel, p.ctas, kMoveThreads, smem, stream, a));
 }
 
 }  // extern "C"

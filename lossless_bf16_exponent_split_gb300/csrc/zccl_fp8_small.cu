@@ -18,7 +18,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kTileRows = 16;  // weight rows of a warp
-constexpr int kFlight = 2;          // blocks in flight in a warp
+constexpr int kFlight = 2;          // blocks in flight in a warp; with three CTAs an SM enough to fill the memory's latency
 
 __device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                             uint32_t b1)
@@ -30,7 +30,7 @@ __device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t
 
 // `split` warps (1, 2, 4 or 8) share a warp's weight rows.
 template <typename T, int kNT>
-__global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) small_kernel(MatmulArgs a, uint32_t split)
+__global__ void __launch_bounds__(kThreads, kNT == 4 ? 2 : 3) small_kernel(MatmulArgs a, uint32_t split)
 {
     constexpr uint32_t kChunk = 8 * kNT;  // rows of x
     __shared__ float sums[kWarps][kNT * 4][32];
@@ -137,9 +137,10 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 4 : kNT == 2 ? 3 : 2) sma
 template <typename T, int kNT>
 cudaError_t small_as(const MatmulArgs& a, int sms, cudaStream_t stream)
 {
-    constexpr int kPerSm = kNT == 1 ? 4 : kNT == 2 ? 3 : 2;
+    constexpr int kPerSm = kNT == 4 ? 2 : 3;
     // warps at work: at least 16 an SM, by splitting the reduction where the weight rows (of every group that can
-    // have rows) do not give that many.  4096 x 14336 with one row: 9.9 us split four ways, 14.2 not split.
+    // have rows) do not give that many (twice as many measured slower: 12.9 us against 11.6 for one row through
+    // 4096 x 14336, 29.1 against 28.3 for 264 rows through 64 experts).
     const uint64_t groups = a.rows < a.G ? a.rows : a.G, pieces = groups * ((a.n + kTileRows - 1) / kTileRows);
     uint32_t split = 1;
     while (split < kWarps && split < a.KB && pieces * split < (uint64_t)sms * 16) split *= 2;
