@@ -441,7 +441,8 @@ zccl_status_t zccl_combine_backward(const uint16_t* d_grad_out, const uint16_t* 
  *        are 128 consecutive rows of the group, column by column.
  * A row (column, for dW) that holds a NaN or an infinity gives NaN; the others
  * are not touched by it.
- * Extents: 1 <= k, n < 2^24, rows < 2^31 and at most 2^31 blocks an operand. */
+ * Extents: 1 <= groups <= ZCCL_MAX_EXPERTS, 1 <= k, n < 2^24, rows < 2^31 and
+ * fewer than 2^31 blocks an operand. */
 
 /* Bytes of a packed weight of `groups` matrices [n][k].  The packed form
  * depends on n and k and is good for any number of calls. */

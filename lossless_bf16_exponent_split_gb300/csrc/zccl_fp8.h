@@ -16,7 +16,7 @@
 namespace zccl {
 
 constexpr uint32_t kFp8Block = 128;
-constexpr uint32_t kMaxGroupsFp8 = 512;  // = ZCCL_MAX_EXPERTS
+constexpr uint32_t kMaxGroupsFp8 = ZCCL_MAX_EXPERTS;
 
 __host__ __device__ inline uint64_t blocks_of(uint64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
 

@@ -32,12 +32,16 @@ class Dispatch(NamedTuple):
 
 
 class Workspaces:
-    """A zeroed workspace per stream: calls on different streams must not share one."""
+    """A zeroed workspace per stream: calls on different streams must not share one.
+    A call that is captured into a CUDA graph gets one of its own, zeroed by the
+    graph, as the graph may be replayed on any stream."""
 
     def __init__(self):
         self._by_stream = {}
 
     def get(self, nbytes: int, stream: int, device) -> torch.Tensor:
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
         ws = self._by_stream.get(stream)
         if ws is None or ws.numel() < nbytes:
             ws = self._by_stream[stream] = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
