@@ -86,7 +86,9 @@ struct PackArgs {
 
 cudaError_t launch_matmul(const MatmulArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_wgrad(const WgradArgs& a, int sms, cudaStream_t stream);
-cudaError_t launch_small(const MatmulArgs& a, int sms, cudaStream_t stream);  // few rows a group
+// Few rows a group: whether launch_small() is the faster of the two.
+bool takes_small(uint64_t rows, uint64_t n, uint32_t groups, int sms);
+cudaError_t launch_small(const MatmulArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_quantize_rows(const QuantArgs& a, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_quantize_tokens(const QuantArgs& a, int dtype, int sms, cudaStream_t stream);
 // Whether launch_quantize_tokens can make the blocks of each row, too.

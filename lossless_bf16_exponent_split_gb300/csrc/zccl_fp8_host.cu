@@ -9,10 +9,6 @@ namespace {
 constexpr uint64_t kMaxDim = 1ull << 24;        // one extent of a product
 constexpr uint64_t kMaxBoxRows = 1ull << 31;    // operand rows of 128 codes, a TMA coordinate
 
-// With at most this many rows a group on average the weights' bytes are the
-// work and the streaming kernel takes the call.
-constexpr uint64_t kSmallRows = 32;
-
 bool sizes_ok(uint64_t rows, uint64_t k, uint64_t n, uint32_t groups)
 {
     return groups >= 1 && groups <= kMaxGroupsFp8 && k >= 1 && n >= 1 && k < kMaxDim && n < kMaxDim &&
@@ -51,8 +47,6 @@ RowsLayout tokens_layout(uint64_t at, uint64_t rows, uint64_t cols, uint32_t gro
     return l;
 }
 
-bool takes_small(uint64_t rows, uint32_t groups) { return rows <= kSmallRows * groups; }
-
 // y = x times the transpose of the packed weight [groups][n][k].  x nullptr: x is
 // quantised in the workspace already.
 zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, uint64_t k, const uint8_t* weight, uint64_t n,
@@ -84,7 +78,7 @@ zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, u
     m.out_f32 = out_dtype == ZCCL_F32;
     m.ticket = reinterpret_cast<uint32_t*>(ws);
     m.status = status;
-    return launched(takes_small(rows, groups) ? launch_small(m, sms, stream) : launch_matmul(m, sms, stream));
+    return launched(takes_small(rows, n, groups, sms) ? launch_small(m, sms, stream) : launch_matmul(m, sms, stream));
 }
 
 }  // namespace
