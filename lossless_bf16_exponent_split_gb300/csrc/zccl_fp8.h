@@ -43,6 +43,9 @@ struct MatmulArgs {
     void* out;               // [rows][n]
     int out_f32;
     uint32_t* ticket;        // zero before the launch
+    uint32_t split;          // matmul_split()
+    uint32_t* counters;      // kJoinCounters, zero before the launch
+    float* parts;            // matmul_part_bytes()
     uint32_t* status;
 };
 
@@ -72,7 +75,8 @@ struct QuantArgs {
     uint32_t G;
     uint8_t* q_rows;         // along rows: also the blocks of each row, or nullptr
     float* scale_rows;
-    uint32_t* ticket;        // zeroed for the product that follows
+    uint32_t* ticket;        // zeroed for the product that follows,
+    uint32_t* counters;      // and so are these kJoinCounters, or nullptr
 };
 
 struct PackArgs {
@@ -84,10 +88,16 @@ struct PackArgs {
     uint8_t* packed_t;       // may be nullptr: the weight with its two axes exchanged
 };
 
+// Parts that the reduction of launch_matmul()'s tiles is cut into, and the room
+// for their sums (0 without parts).
+constexpr uint32_t kJoinParts = 160, kJoinCounters = 8 * kJoinParts;
+uint32_t matmul_split(uint64_t rows, uint64_t n, uint64_t k, uint32_t groups);
+uint64_t matmul_part_bytes(uint32_t split);
+
 cudaError_t launch_matmul(const MatmulArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_wgrad(const WgradArgs& a, int sms, cudaStream_t stream);
 // Few rows a group: whether launch_small() is the faster of the two.
-bool takes_small(uint64_t rows, uint64_t n, uint32_t groups, int sms);
+bool takes_small(uint64_t rows, uint64_t n, uint64_t k, uint32_t groups, int sms);
 cudaError_t launch_small(const MatmulArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_quantize_rows(const QuantArgs& a, int dtype, int sms, cudaStream_t stream);
 cudaError_t launch_quantize_tokens(const QuantArgs& a, int dtype, int sms, cudaStream_t stream);

@@ -54,6 +54,9 @@ struct TileArgs {
     void* out;
     int tma_out;           // whether the output has a tensor map
     uint32_t* ticket;      // tiles given out so far
+    uint32_t split;        // parts of a tile's reduction
+    uint32_t* counters;    // by tile and adding warp: parts that are done
+    float* parts;          // by tile, part and adding warp: its sums, by column and lane
     uint32_t* status;
 };
 
@@ -64,7 +67,9 @@ struct alignas(16) Tile {
     uint32_t blocks;       // blocks of the reduction; kNoTile: there are no more tiles
     uint32_t a0, b0;       // first operand rows
     uint32_t sa0, sb0;     // first scales
-    uint32_t g, pad[3];    // group
+    uint32_t g;            // group
+    uint32_t join;         // tile, of those that are cut into parts
+    uint32_t part, pad;
 };
 constexpr uint32_t kNoTile = 0xFFFFFFFFu;
 constexpr uint32_t kTileSlots = 4;
@@ -87,20 +92,20 @@ static_assert(kSmemBytes <= 232448, "fits the shared memory of a CTA");
 // columns; the blocks after the last group's are the rows outside every group.
 // kWgrad = true: every group has the same tiles; prefix counts token blocks.
 template <bool kWgrad>
-__device__ __forceinline__ uint32_t tile_count(const TileArgs& a, const uint32_t* prefix, uint32_t tail0)
+__device__ __forceinline__ uint32_t tile_count(const TileArgs& a, const uint32_t* prefix, uint32_t tail0, uint32_t split)
 {
     const uint32_t nt = (a.n + kTileN - 1) / kTileN;
     if (kWgrad) return a.G * ((a.m + kTileM - 1) / kTileM) * nt;
-    return (prefix[a.G] + (a.rows - tail0 + kTileM - 1) / kTileM) * nt;
+    return (prefix[a.G] * split + (a.rows - tail0 + kTileM - 1) / kTileM) * nt;
 }
 
 template <bool kWgrad>
 __device__ __forceinline__ Tile tile_at(const TileArgs& a, const uint32_t* prefix, const uint16_t* order, uint32_t tail0,
-                                        uint32_t t)
+                                        uint32_t split, uint32_t t)
 {
     const uint32_t nt = (a.n + kTileN - 1) / kTileN;
     Tile c;
-    uint32_t mt, i, lo = 0;
+    uint32_t mt, i, lo = 0, kb0 = 0;
     if (kWgrad) {
         mt = (a.m + kTileM - 1) / kTileM;
         c.g = t / (mt * nt);
@@ -109,17 +114,21 @@ __device__ __forceinline__ Tile tile_at(const TileArgs& a, const uint32_t* prefi
         c.blocks = prefix[c.g + 1] - prefix[c.g];
         c.row_end = a.m;
     } else {
-        uint32_t mb = t / nt;
+        const uint32_t whole = t / split, mb = whole / nt;
         if (mb < prefix[a.G]) {
+            c.join = whole;
+            c.part = t - whole * split;
+            kb0 = c.part * a.KB / split;
+            t = whole;
             c.g = group_at(prefix, a.G, mb);
             mt = prefix[c.g + 1] - prefix[c.g];
             i = t - prefix[c.g] * nt;
             group_rows(a.offsets, a.rows, c.g, &lo, &c.row_end);
-            c.blocks = a.KB;
+            c.blocks = (c.part + 1) * a.KB / split - kb0;
         } else {  // rows outside every group: zeros
             c.g = 0;
             mt = (a.rows - tail0 + kTileM - 1) / kTileM;
-            i = t - prefix[a.G] * nt;
+            i = t - prefix[a.G] * split * nt;
             lo = tail0;
             c.row_end = a.rows;
             c.blocks = 0;
@@ -137,10 +146,10 @@ __device__ __forceinline__ Tile tile_at(const TileArgs& a, const uint32_t* prefi
         c.a0 = c.sa0 + c.m0;
         c.b0 = c.sb0 + c.n0;
     } else {
-        c.sa0 = 0;
-        c.sb0 = c.g * (uint32_t)blocks_of(a.n) * a.KB;
-        c.a0 = c.m0;
-        c.b0 = c.g * a.KB * a.n + c.n0;
+        c.sa0 = kb0 * a.rows;
+        c.sb0 = c.g * (uint32_t)blocks_of(a.n) * a.KB + kb0;
+        c.a0 = c.sa0 + c.m0;
+        c.b0 = (c.g * a.KB + kb0) * a.n + c.n0;
     }
     return c;
 }
@@ -227,6 +236,32 @@ __device__ __forceinline__ void store_rows(uint8_t (&bufs)[2][32 * 128], const C
             __syncwarp();
         }
     }
+}
+
+// The end of a part of a tile: the warp's sums go to memory; the last warp to
+// come, by the counter, takes those of all parts, added in the parts' order, and
+// returns true.
+__device__ __forceinline__ bool join_parts(const TileArgs& a, const Tile& c, uint32_t split, uint32_t warp, uint32_t lane,
+                                           float (&acc)[kSumCols])
+{
+    constexpr uint32_t kPart = kSumCols * 32;
+    float* at = a.parts + ((uint64_t)c.join * split * kSumWarps + warp) * kPart + lane;
+#pragma unroll
+    for (uint32_t i = 0; i < kSumCols; ++i) __stcg(at + (uint64_t)c.part * kSumWarps * kPart + i * 32, acc[i]);
+    __syncwarp();
+    uint32_t before = 0;
+    if (lane == 0) before = atom_inc_acq_rel(a.counters + c.join * kSumWarps + warp, split - 1);
+    if (__shfl_sync(0xFFFFFFFFu, before, 0) != split - 1) return false;
+    __syncwarp();
+#pragma unroll
+    for (uint32_t i = 0; i < kSumCols; ++i) acc[i] = __ldcg(at + i * 32);
+#pragma unroll 1
+    for (uint32_t p = 1; p < split; ++p) {
+        at += kSumWarps * kPart;
+#pragma unroll
+        for (uint32_t i = 0; i < kSumCols; ++i) acc[i] += __ldcg(at + i * 32);
+    }
+    return true;
 }
 
 // Whether a phase is complete, without waiting.
@@ -321,6 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
     }
     const uint32_t tmem = s->tmem;
+    // there is room for kJoinParts; what the host reckoned with may be less than the groups' blocks
+    const uint32_t split = kWgrad || s->prefix[a.G] * ((a.n + kTileN - 1) / kTileN) * a.split > kJoinParts ? 1 : a.split;
 
     if (warp < 4) {
         regs_fewer<kRegsFew>();
@@ -388,13 +425,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t t = ld_l2(a.offsets + a.G);
                 tail0 = t < 0 ? 0u : min((uint32_t)t, a.rows);
             }
-            const uint32_t tiles = tile_count<kWgrad>(a, s->prefix, tail0);
+            const uint32_t tiles = tile_count<kWgrad>(a, s->prefix, tail0, split);
             uint32_t t = lane == 0 ? atomicAdd(a.ticket, 1u) : 0u;
             for (;; ++k) {
                 const uint32_t slot = k % kTileSlots, now = __shfl_sync(0xFFFFFFFFu, t, 0);
                 if (now < tiles) {
                     if (lane == 0) t = atomicAdd(a.ticket, 1u);
-                    c = tile_at<kWgrad>(a, s->prefix, s->order, tail0, now);
+                    c = tile_at<kWgrad>(a, s->prefix, s->order, tail0, split, now);
                 } else {
                     c.blocks = kNoTile;
                 }
@@ -536,7 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 free2 = first;
             }
             const uint32_t row = c.m0 + sub * 32, n = c.n0 + wg * kSumCols;
-            if (ok && row < c.row_end && n < a.n)
+            if (ok && row < c.row_end && n < a.n &&
+                (kWgrad || split == 1 || c.blocks == 0 || join_parts(a, c, split, warp - 4, lane, acc)))
                 store_rows(s->out[warp - 4], &map_out, a.tma_out, reinterpret_cast<T*>(a.out),
                            (kWgrad ? (uint64_t)c.g * a.m : 0) + row, c.row_end - row, n, a.n, &turn, acc);
         }
@@ -618,6 +656,23 @@ cudaError_t launch_tiles(TileArgs a, const uint8_t* qa, uint64_t rows_a, const u
 
 }  // namespace
 
+// Parts of the reduction where the tiles are too few for the SMs (152 of them).
+// Joining costs about 5 us, so it wants 24 blocks, 8 a part at least: 48 rows by
+// 4096 x 14336 (n x k) 28 us in four parts and 55 whole, by 4096 x 4096 17.2 and
+// 19.6, by 1024 x 2048 (16 blocks) 14.3 and 13.2.  Eight parts: 29.6 and 21.3 for
+// the first two.
+uint32_t matmul_split(uint64_t rows, uint64_t n, uint64_t k, uint32_t groups)
+{
+    const uint64_t active = rows < groups ? rows : groups, by_rows = (rows + kTileM - 1) / kTileM;
+    const uint64_t tiles = (active > by_rows ? active : by_rows) * ((n + kTileN - 1) / kTileN), blocks = blocks_of(k);
+    if (tiles == 0 || blocks < 24) return 1;
+    uint64_t split = 152 / tiles < 4 ? 152 / tiles : 4;
+    if (split > blocks / 8) split = blocks / 8;
+    return split < 2 ? 1 : (uint32_t)split;
+}
+
+uint64_t matmul_part_bytes(uint32_t split) { return split > 1 ? (uint64_t)kJoinParts * kTileM * kTileN * 4 : 0; }
+
 cudaError_t launch_matmul(const MatmulArgs& m, int sms, cudaStream_t stream)
 {
     TileArgs a{};
@@ -631,8 +686,11 @@ cudaError_t launch_matmul(const MatmulArgs& m, int sms, cudaStream_t stream)
     a.G = m.G;
     a.out = m.out;
     a.ticket = m.ticket;
+    a.split = m.split;
+    a.counters = m.counters;
+    a.parts = m.parts;
     a.status = m.status;
-    const uint64_t most = (blocks_of(m.rows) + m.G) * ((m.n + kTileN - 1) / kTileN);
+    const uint64_t most = (blocks_of(m.rows) + m.G) * ((m.n + kTileN - 1) / kTileN) * m.split;
     const auto launch = m.out_f32 ? launch_tiles<false, float> : launch_tiles<false, __nv_bfloat16>;
     return launch(a, m.a, (uint64_t)m.KB * m.rows, m.b, (uint64_t)m.G * m.KB * m.n, m.rows, most, sms, stream);
 }
@@ -650,6 +708,7 @@ cudaError_t launch_wgrad(const WgradArgs& w, int sms, cudaStream_t stream)
     a.blocks = w.blocks;
     a.out = w.out;
     a.ticket = w.ticket;
+    a.split = 1;
     a.status = w.status;
     const uint64_t most = (uint64_t)w.G * ((w.m + kTileM - 1) / kTileM) * ((w.n + kTileN - 1) / kTileN);
     const auto launch = w.out_f32 ? launch_tiles<true, float> : launch_tiles<true, __nv_bfloat16>;

@@ -20,8 +20,10 @@ bool sizes_ok(uint64_t rows, uint64_t k, uint64_t n, uint32_t groups)
 bool float_type(int t) { return t == ZCCL_BF16 || t == ZCCL_F32; }
 uintptr_t size_of(int t) { return t == ZCCL_BF16 ? 2 : 4; }
 
-// A workspace begins with the tile counters of a call's products.
-constexpr uint64_t kTicketBytes = 256;
+// A workspace begins with the counters of a call's products: two tickets, then those of a matmul's parts.
+constexpr uint64_t kCountersAt = 256;
+constexpr uint64_t kTicketBytes = kCountersAt + 4 * kJoinCounters;
+static_assert(kTicketBytes % 256 == 0, "what follows is aligned");
 
 // Rows of `cols` values quantised by row.
 struct RowsLayout {
@@ -48,10 +50,10 @@ RowsLayout tokens_layout(uint64_t at, uint64_t rows, uint64_t cols, uint32_t gro
 }
 
 // y = x times the transpose of the packed weight [groups][n][k].  x nullptr: x is
-// quantised in the workspace already.
+// quantised in the workspace already.  parts: room for matmul_part_bytes().
 zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, uint64_t k, const uint8_t* weight, uint64_t n,
-                     uint32_t groups, const int32_t* offsets, void* out, int out_dtype, uint8_t* ws, uint32_t* status,
-                     int sms, cudaStream_t stream)
+                     uint32_t groups, const int32_t* offsets, void* out, int out_dtype, uint8_t* ws, uint8_t* parts,
+                     uint32_t* status, int sms, cudaStream_t stream)
 {
     const float* sb = reinterpret_cast<const float*>(weight + weight_code_bytes(groups, n, k));
     const RowsLayout l = rows_layout(kTicketBytes, rows, k);
@@ -63,6 +65,8 @@ zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, u
     q.q = ws + l.q;
     q.scale = reinterpret_cast<float*>(ws + l.scale);
     q.ticket = reinterpret_cast<uint32_t*>(ws);
+    const uint32_t split = matmul_split(rows, n, k, groups);
+    q.counters = split > 1 ? reinterpret_cast<uint32_t*>(ws + kCountersAt) : nullptr;
     if (x != nullptr && launch_quantize_rows(q, dtype, sms, stream) != cudaSuccess) return ZCCL_ERR_CUDA;
     MatmulArgs m{};
     m.a = q.q;
@@ -77,8 +81,11 @@ zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, u
     m.out = out;
     m.out_f32 = out_dtype == ZCCL_F32;
     m.ticket = reinterpret_cast<uint32_t*>(ws);
+    m.split = split;
+    m.counters = reinterpret_cast<uint32_t*>(ws + kCountersAt);
+    m.parts = reinterpret_cast<float*>(parts);
     m.status = status;
-    return launched(takes_small(rows, n, groups, sms) ? launch_small(m, sms, stream) : launch_matmul(m, sms, stream));
+    return launched(takes_small(rows, n, k, groups, sms) ? launch_small(m, sms, stream) : launch_matmul(m, sms, stream));
 }
 
 }  // namespace
@@ -132,10 +139,10 @@ zccl_status_t zccl_fp8_linear_workspace_bytes(uint64_t rows, uint64_t k, uint64_
 {
     if (bytes == nullptr || !sizes_ok(rows, k, n, groups)) return ZCCL_ERR_INVALID_ARG;
     if (!backward) {
-        *bytes = rows_layout(kTicketBytes, rows, k).end;
+        *bytes = rows_layout(kTicketBytes, rows, k).end + matmul_part_bytes(matmul_split(rows, n, k, groups));
     } else {
         const RowsLayout dy = rows_layout(kTicketBytes, rows, n), dyt = tokens_layout(dy.end, rows, n, groups);
-        *bytes = tokens_layout(dyt.end, rows, k, groups).end;
+        *bytes = tokens_layout(dyt.end, rows, k, groups).end + matmul_part_bytes(matmul_split(rows, k, n, groups));
     }
     return ZCCL_OK;
 }
@@ -155,8 +162,9 @@ zccl_status_t zccl_fp8_linear(const void* d_x, int dtype, uint64_t stride, uint6
     if (!good_ptr(d_x, size_of(dtype)) || !good_ptr(d_out, size_of(out_dtype))) return ZCCL_ERR_INVALID_ARG;
     const int sms = sm_count();
     if (sms == 0) return ZCCL_ERR_CUDA;
+    uint8_t* ws = reinterpret_cast<uint8_t*>(d_ws);
     return linear(d_x, dtype, stride, rows, k, reinterpret_cast<const uint8_t*>(d_weight), n, groups, d_offsets, d_out,
-                  out_dtype, reinterpret_cast<uint8_t*>(d_ws), d_status, sms, stream);
+                  out_dtype, ws, ws + rows_layout(kTicketBytes, rows, k).end, d_status, sms, stream);
 }
 
 zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int dtype, uint64_t grad_stride,
@@ -194,13 +202,14 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
         q.q_rows = ws + dy.q;
         q.scale_rows = reinterpret_cast<float*>(ws + dy.scale);
         q.ticket = reinterpret_cast<uint32_t*>(ws);  // the product of the rows' gradient
+        if (matmul_split(rows, k, n, groups) > 1) q.counters = reinterpret_cast<uint32_t*>(ws + kCountersAt);
     }
     if (d_grad_w != nullptr && rows > 0 && launch_quantize_tokens(q, dtype, sms, stream) != cudaSuccess)
         return ZCCL_ERR_CUDA;
     if (d_grad_x != nullptr && rows > 0) {
         const zccl_status_t st =
             linear(both ? nullptr : d_grad, dtype, grad_stride, rows, n, reinterpret_cast<const uint8_t*>(d_weight_t), k,
-                   groups, d_offsets, d_grad_x, out_dtype, ws, d_status, sms, stream);
+                   groups, d_offsets, d_grad_x, out_dtype, ws, ws + xt.end, d_status, sms, stream);
         if (st != ZCCL_OK) return st;
     }
     if (d_grad_w == nullptr) return ZCCL_OK;
@@ -211,6 +220,7 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
     r.q = ws + xt.q;
     r.scale = reinterpret_cast<float*>(ws + xt.scale);
     r.q_rows = nullptr;
+    r.counters = nullptr;
     r.ticket = reinterpret_cast<uint32_t*>(ws) + 32;
     if (launch_quantize_tokens(r, dtype, sms, stream) != cudaSuccess) return ZCCL_ERR_CUDA;
     WgradArgs w{};

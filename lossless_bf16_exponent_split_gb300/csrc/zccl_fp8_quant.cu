@@ -16,10 +16,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRowsPerWarp = 8;  // rows in flight in a warp
 
-// The tile counter of the product that follows (every earlier use of it is over).
-__device__ __forceinline__ void zero_ticket(const QuantArgs& a)
+// The counters of the product that follows (every earlier use of them is over).
+__device__ __forceinline__ void zero_counters(const QuantArgs& a)
 {
-    if (blockIdx.x == 0 && threadIdx.x == 0 && a.ticket != nullptr) *a.ticket = 0;
+    if (blockIdx.x != 0) return;
+    if (threadIdx.x == 0 && a.ticket != nullptr) *a.ticket = 0;
+    if (a.counters != nullptr)
+        for (uint32_t i = threadIdx.x; i < kJoinCounters; i += kThreads) a.counters[i] = 0;
 }
 
 // Eight values of a row from column c on; zeros past the row's end.  kVec: the
@@ -56,7 +59,7 @@ template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantArgs a)
 {
     pdl_wait();
-    zero_ticket(a);
+    zero_counters(a);
     const uint32_t lane = threadIdx.x & 31, half = lane >> 4, i8 = (lane & 15) * 8;
     const uint32_t nb = (uint32_t)blocks_of(a.cols), pairs = (nb + 1) / 2;
     const uint64_t items = (uint64_t)pairs * ((a.rows + kRowsPerWarp - 1) / kRowsPerWarp);
@@ -127,7 +130,7 @@ __device__ __forceinline__ constexpr uint32_t owner_of(uint32_t row) { return 2 
 __global__ void __launch_bounds__(kThreads) quantize_rows_bf16_kernel(QuantArgs a)
 {
     pdl_wait();
-    zero_ticket(a);
+    zero_counters(a);
     const uint32_t lane = threadIdx.x & 31, half = lane >> 4, i8 = (lane & 15) * 8;
     const uint32_t nb = (uint32_t)blocks_of(a.cols), pairs = (nb + 1) / 2;
     const uint32_t groups = (a.rows + kRowsPerWarp - 1) / kRowsPerWarp;
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) quantize_tokens_kernel(QuantArgs a)
     __shared__ uint32_t prefix[kMaxGroupsFp8 + 1];
     __shared__ uint2 range[kMaxGroupsFp8];
     pdl_wait();
-    zero_ticket(a);
+    zero_counters(a);
     const uint32_t lane = threadIdx.x & 31, part = threadIdx.x >> 5;
     group_prefix(a.offsets, a.rows, a.G, kFp8Block, (uint32_t)(a.rows / kFp8Block + a.G), prefix);
     for (uint32_t g = threadIdx.x; g < a.G; g += kThreads) group_rows(a.offsets, a.rows, g, &range[g].x, &range[g].y);
@@ -286,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, kRows ? 3 : 4) quantize_tokens_bf16_
     __shared__ uint32_t prefix[kMaxGroupsFp8 + 1];
     __shared__ uint2 range[kMaxGroupsFp8];
     pdl_wait();
-    zero_ticket(a);
+    zero_counters(a);
     const uint32_t lane = threadIdx.x & 31, part = threadIdx.x >> 5;
     group_prefix(a.offsets, a.rows, a.G, kFp8Block, (uint32_t)(a.rows / kFp8Block + a.G), prefix);
     for (uint32_t g = threadIdx.x; g < a.G; g += kThreads) group_rows(a.offsets, a.rows, g, &range[g].x, &range[g].y);

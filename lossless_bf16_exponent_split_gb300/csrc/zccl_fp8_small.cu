@@ -177,20 +177,23 @@ cudaError_t small_typed(const MatmulArgs& a, int sms, cudaStream_t stream)
 // The two products by what a block of the reduction costs, in ps.  This one:
 // 23, 38 or 54 a weight row and chunk of 8, 16 or 32 rows of x (the conversion
 // of e4m3 operands bounds it), and some groups have a chunk more than the mean
-// says.  The other: 0.55 us a round of its tiles, or 25 ps a weight row, the
-// memory's time.  Measured, this one and the other, in us a call:
-//   4096 x 14336, 1 group: 1 row 13.9, 26.9; 8 rows 14.1, 23.6; 32 rows 36.8, 22.4
-//   4096 x 4096, 1 group: 1 row 8.1, 19.5; 32 rows 14.7, 19.1; 48 rows 22.5, 19.6
-//   4096 x 4096, 8 groups: 8 rows 21.7, 27.3; 64 rows 34.1, 29.4; 256 rows 83.8, 29.9
-//   2048 x 1024, 64 groups: 64 rows 21.1, 28.4; 256 rows 30.8, 31.1; 768 rows 45.7, 32.4
-bool takes_small(uint64_t rows, uint64_t n, uint32_t groups, int sms)
+// says.  The other: 0.55 us a round of its tiles (less in parts, and 5 us a call
+// to join them), or 25 ps a weight row, the memory's time.  Measured, this one
+// and the other, in us a call (n x k):
+//   14336 x 4096, 1 group: 1 row 13.9, 25.5; 8 rows 14.1, 21.8; 32 rows 36.8, 21.3
+//   4096 x 4096, 1 group: 1 row 8.1, 18.0; 32 rows 14.7, 16.1; 48 rows 22.5, 17.2
+//   4096 x 4096, 8 groups: 8 rows 21.7, 29.1; 64 rows 34.1, 29.8; 256 rows 83.8, 30.4
+//   1024 x 2048, 64 groups: 64 rows 21.1, 28.7; 256 rows 30.8, 31.4; 768 rows 45.7, 32.8
+bool takes_small(uint64_t rows, uint64_t n, uint64_t k, uint32_t groups, int sms)
 {
     if (rows > 32ull * groups) return false;
     const uint32_t nt = row_tiles(rows, groups);
     const uint64_t active = rows < groups ? rows : groups;
     const uint64_t chunks = groups == 1 ? (rows + 8 * nt - 1) / (8 * nt) : active + rows / 32;
     const uint64_t here = chunks * n * (nt == 1 ? 23 : nt == 2 ? 38 : 54);
-    const uint64_t rounds = (active * ((n + 255) / 256) + sms - 1) / sms, by_tiles = rounds * 550000, by_bytes = active * n * 25;
+    const uint64_t rounds = (active * ((n + 255) / 256) + sms - 1) / sms, by_bytes = active * n * 25;
+    const uint32_t split = matmul_split(rows, n, k, groups);
+    const uint64_t by_tiles = rounds * 550000 / split + (split > 1 ? 5000000 / blocks_of(k) : 0);
     return here <= (by_tiles > by_bytes ? by_tiles : by_bytes);
 }
 
