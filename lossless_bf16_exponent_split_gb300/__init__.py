@@ -17,6 +17,7 @@ products.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -337,6 +338,7 @@ def zccl_fp8_weight_pack(d_codes, d_scale, groups, n, k, d_weight, d_weight_t, s
     return lib().zccl_fp8_weight_pack(d_codes, d_scale, groups, n, k, d_weight, d_weight_t, stream)
 
 
+@functools.lru_cache(maxsize=1024)
 def zccl_fp8_linear_workspace_bytes(rows: int, k: int, n: int, groups: int, backward: bool) -> int:
     out = ctypes.c_uint64(0)
     check(lib().zccl_fp8_linear_workspace_bytes(rows, k, n, groups, 1 if backward else 0, ctypes.byref(out)),

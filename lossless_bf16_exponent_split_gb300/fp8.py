@@ -10,7 +10,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import (BF16, F32, OK, ZcclError, check, lib, zccl_fp8_linear_workspace_bytes, zccl_fp8_weight_bytes)
-from .moe import current_stream, need
+from .moe import Workspaces, current_stream, need
 
 _DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
 BLOCK = 128
@@ -26,12 +26,14 @@ class Fp8Weight(NamedTuple):
 
 
 class BlockFp8:
-    """A device status word and the calls of the block-scaled e4m3 layers."""
+    """A device status word, workspaces and the calls of the block-scaled e4m3 layers."""
 
     def __init__(self, device=None):
         self._lib = lib()
         self.device = torch.zeros(0, device=device if device is not None else "cuda").device
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        # a call's workspace costs 1.5 us to allocate: a serving step's is kept, a large one is not
+        self._workspaces = Workspaces(zeroed=False, most=64 << 20)
 
     # -- status ---------------------------------------------------------------
     def reset_status(self):
@@ -104,11 +106,12 @@ class BlockFp8:
         off = self._offsets(offsets, weight)
         rows = x.shape[0]
         out = torch.empty(rows, weight.n, dtype=out_dtype, device=self.device)
-        ws = torch.empty(zccl_fp8_linear_workspace_bytes(rows, weight.k, weight.n, weight.groups, False),
-                         dtype=torch.uint8, device=self.device)
+        stream = current_stream(self.device)
+        ws = self._workspaces.get(zccl_fp8_linear_workspace_bytes(rows, weight.k, weight.n, weight.groups, False), stream,
+                                  self.device)
         st = self._lib.zccl_fp8_linear(ptr, _DTYPES[x.dtype], stride, rows, weight.k, weight.packed.data_ptr(), weight.n,
                                        weight.groups, off, out.data_ptr(), _out_type(out_dtype), ws.data_ptr(),
-                                       ws.numel(), self.status.data_ptr(), current_stream(self.device))
+                                       ws.numel(), self.status.data_ptr(), stream)
         check(st, "zccl_fp8_linear")
         return out
 
@@ -127,13 +130,14 @@ class BlockFp8:
             raise ValueError("weight: packed without backward=True")
         dx = torch.empty(rows, weight.k, dtype=out_dtype, device=self.device) if input_grad else None
         dw = torch.empty(weight.groups, weight.n, weight.k, dtype=out_dtype, device=self.device) if weight_grad else None
-        ws = torch.empty(zccl_fp8_linear_workspace_bytes(rows, weight.k, weight.n, weight.groups, True),
-                         dtype=torch.uint8, device=self.device)
+        stream = current_stream(self.device)
+        ws = self._workspaces.get(zccl_fp8_linear_workspace_bytes(rows, weight.k, weight.n, weight.groups, True), stream,
+                                  self.device)
         st = self._lib.zccl_fp8_linear_backward(
             gptr, xptr, _DTYPES[grad.dtype], gstride, xstride, rows, weight.k,
             None if weight.packed_t is None else weight.packed_t.data_ptr(), weight.n, weight.groups, off,
             None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(), _out_type(out_dtype),
-            ws.data_ptr(), ws.numel(), self.status.data_ptr(), current_stream(self.device))
+            ws.data_ptr(), ws.numel(), self.status.data_ptr(), stream)
         check(st, "zccl_fp8_linear_backward")
         return dx, dw
 

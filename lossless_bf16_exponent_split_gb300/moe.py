@@ -32,19 +32,22 @@ class Dispatch(NamedTuple):
 
 
 class Workspaces:
-    """A zeroed workspace per stream: calls on different streams must not share one.
-    A call that is captured into a CUDA graph gets one of its own, zeroed by the
-    graph, as the graph may be replayed on any stream."""
+    """A workspace per stream, zeroed where the calls want that: calls on different
+    streams must not share one.  A call that is captured into a CUDA graph gets one
+    of its own, as the graph may be replayed on any stream, and so does one that
+    wants more than `most` bytes."""
 
-    def __init__(self):
+    def __init__(self, zeroed: bool = True, most: int = 1 << 62):
         self._by_stream = {}
+        self._new = torch.zeros if zeroed else torch.empty
+        self._most = most
 
     def get(self, nbytes: int, stream: int, device) -> torch.Tensor:
-        if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        if nbytes > self._most or torch.cuda.is_current_stream_capturing():
+            return self._new(max(nbytes, 256), dtype=torch.uint8, device=device)
         ws = self._by_stream.get(stream)
         if ws is None or ws.numel() < nbytes:
-            ws = self._by_stream[stream] = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+            ws = self._by_stream[stream] = self._new(max(nbytes, 256), dtype=torch.uint8, device=device)
         return ws
 
 
