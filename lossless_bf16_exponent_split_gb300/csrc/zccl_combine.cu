@@ -5,7 +5,8 @@
 // thread owns one 16-byte piece of a token's row and has the K rows' pieces in
 // flight together.  Backward: 2 T K H read and as many written (the token's
 // gradient row comes from L1/L2 for all but one of its K slots); a warp owns
-// one slot, so the dot product needs no other warp.
+// one slot, so the dot product needs no other warp.  16384 tokens, 8
+// slots, hidden 2048: forward 96 us (6.3 TB/s), backward 177 us (6.5 TB/s).
 #include "zccl_ops.cuh"
 
 namespace zccl {

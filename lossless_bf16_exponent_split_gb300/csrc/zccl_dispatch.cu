@@ -4,13 +4,14 @@
 // A stable counting sort of the T * K slots by expert.  The slots are cut into
 // tiles of whole tokens, one per CTA.  Few slots: one kernel, every CTA counts
 // all slots itself.  Many: a first kernel counts each tile's slots per expert,
-// one tile per SM, and its last CTA turns the counts into places (no CTA waits
-// for another); in the second kernel 32 CTAs share a tile, each counts the
+// at most a tile per SM, and its last CTA turns the counts into places (no CTA waits
+// for another); in the second kernel several CTAs share a tile, each counts the
 // slots of the tile before its own, ranks those and moves the rows.  A token's
 // row is read once and stored K times.  Slots without an expert sort last and
 // store zeros, so every row is written exactly once.
 //
-// Bound by HBM: 2 T H bytes read, 2 T K H written.
+// Bound by HBM: 2 T H bytes read, 2 T K H written.  16384 tokens, 8 slots, hidden
+// 2048: 100 us a call (6.1 TB/s).
 #include "zccl_ops.cuh"
 
 namespace zccl {
@@ -19,12 +20,19 @@ namespace {
 
 constexpr uint32_t kMoveThreads = 256;
 constexpr uint32_t kCountThreads = 512;
-constexpr uint32_t kSubTiles = 32;  // CTAs that move a counted tile's rows: 94 us for the all-to-all's rows, 101 with 8,
-                                    // 106 with 4 (more, smaller CTAs end closer together)
 constexpr uint32_t kFlight = 4;  // pieces of rows in flight in a thread
 constexpr uint32_t kMoveWarps = kMoveThreads / 32;
-// Up to this many slots every CTA counts them all itself.
-constexpr uint64_t kSmallSlots = 2048;
+// Up to this many slots every CTA counts them all itself.  Measured so and with
+// the counting kernel, in us: top 8 of 64, hidden 2048, 4096 slots 6.0 and 9.5, 16384:
+// 15.5 and 17.5, 32768: 33.8 and 30.1; top 8 of 256, hidden 256, 16384: 7.9 and 9.6,
+// 32768: 12.4 and 10.8.
+constexpr uint64_t kSmallSlots = 24576;
+constexpr uint64_t kTileSlots = 2048;  // a counted tile has at least these, so that its last CTA has few counts to add up
+// A counted tile's rows are moved by CTAs that store about this much each, but by
+// no more than 64 (more, smaller CTAs end closer together: 100 us for the
+// all-to-all's rows, 104 with four times as much each, 120 with four CTAs a tile).
+constexpr uint64_t kSubBytes = 65536;
+constexpr uint32_t kSubTiles = 64;
 
 struct DispatchArgs {
     const int32_t* idx;
@@ -44,8 +52,9 @@ struct DispatchArgs {
     uint32_t tiles;        // tiles that are counted
     uint32_t tile_tokens;  // tokens of a tile
     uint32_t sub_tokens;   // tokens of a CTA that moves rows
+    uint32_t subs;         // CTAs that move a counted tile's rows
     uint32_t* ticket;      // CTAs of the counting kernel that are done
-    int32_t* base;         // [E + 1][tiles]: a tile's count of an expert's slots, then its first row
+    int32_t* base;         // [tiles][E + 1]: a tile's count of an expert's slots, then its first row
 };
 
 __device__ __forceinline__ uint32_t bucket_of(int32_t e, uint32_t E) { return (uint32_t)e < E ? (uint32_t)e : E; }
@@ -96,52 +105,42 @@ __device__ void write_tables(const DispatchArgs& a, const int32_t* first)
 }
 
 // Counts each tile's slots per expert; the last CTA done makes the counts
-// places.  base is expert-major, so a warp turns an expert's counts into a
-// prefix sum with coalesced loads.
+// places, a thread an expert, 32 tiles' counts in flight (a warp an expert, with
+// shuffles, took 10 us for 64 experts and 28 for 512).
 __global__ void __launch_bounds__(kCountThreads) dispatch_count_kernel(DispatchArgs a)
 {
     __shared__ int32_t count[ZCCL_MAX_EXPERTS + 2];
     __shared__ uint32_t order;
     pdl_wait();
-    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (uint32_t e = tid; e <= a.E; e += kCountThreads) count[e] = 0;
+    const uint32_t tid = threadIdx.x, B = a.E + 1;
+    for (uint32_t e = tid; e < B; e += kCountThreads) count[e] = 0;
     __syncthreads();
     const uint64_t lo = (uint64_t)blockIdx.x * a.tile_tokens * a.K;
     const uint64_t hi = min((uint64_t)(blockIdx.x + 1) * a.tile_tokens, a.tokens) * a.K;
     for (uint64_t i = lo + tid; i < hi; i += kCountThreads) atomicAdd(&count[bucket_of(a.idx[i], a.E)], 1);
     __syncthreads();
-    for (uint32_t e = tid; e <= a.E; e += kCountThreads) a.base[(uint64_t)e * a.tiles + blockIdx.x] = count[e];
+    for (uint32_t e = tid; e < B; e += kCountThreads) a.base[blockIdx.x * B + e] = count[e];
     __threadfence();
     __syncthreads();
     if (tid == 0) order = atom_inc_acq_rel(a.ticket, a.tiles - 1);  // wraps to 0 for the next call
     __syncthreads();
     if (order != a.tiles - 1) return;
     __threadfence();
-    for (uint32_t e = warp; e <= a.E; e += kCountThreads / 32) {
-        int32_t* col = a.base + (uint64_t)e * a.tiles;
+    for (uint32_t e = tid; e < B; e += kCountThreads) {
+        int32_t* at = a.base + e;
         int32_t run = 0;
-        constexpr uint32_t kAhead = 8;  // loads in flight: one behind the other they cost 20 us
-        for (uint32_t i0 = 0; i0 < a.tiles; i0 += 32 * kAhead) {
+        constexpr uint32_t kAhead = 32;
+        for (uint32_t t0 = 0; t0 < a.tiles; t0 += kAhead) {
             int32_t c[kAhead];
 #pragma unroll
-            for (uint32_t j = 0; j < kAhead; ++j) {
-                const uint32_t i = i0 + 32 * j + lane;
-                c[j] = i < a.tiles ? ld_l2(col + i) : 0;
-            }
+            for (uint32_t j = 0; j < kAhead; ++j) c[j] = t0 + j < a.tiles ? ld_l2(at + (t0 + j) * B) : 0;
 #pragma unroll
             for (uint32_t j = 0; j < kAhead; ++j) {
-                const uint32_t i = i0 + 32 * j + lane;
-                int32_t incl = c[j];
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int32_t t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                    if ((int)lane >= o) incl += t;
-                }
-                if (i < a.tiles) col[i] = run + incl - c[j];
-                run += __shfl_sync(0xFFFFFFFFu, incl, 31);
+                if (t0 + j < a.tiles) at[(t0 + j) * B] = run;
+                run += c[j];
             }
         }
-        if (lane == 0) count[e] = run;
+        count[e] = run;
     }
     __syncthreads();
     scan_warp0(count, a.E + 1);
@@ -161,10 +160,10 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_move_kernel(DispatchArg
     int32_t* by_warp = place + kMoveThreads;        // [kMoveWarps][B]
     pdl_wait();
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t counted = blockIdx.x / kSubTiles;  // the tile that was counted
+    const uint32_t counted = blockIdx.x / a.subs;  // the tile that was counted
     const uint64_t tile = (uint64_t)counted * a.tile_tokens;
     const uint64_t lo = kSmall ? (uint64_t)blockIdx.x * a.sub_tokens
-                               : min(tile + (uint64_t)(blockIdx.x % kSubTiles) * a.sub_tokens, a.tokens);
+                               : min(tile + (uint64_t)(blockIdx.x % a.subs) * a.sub_tokens, a.tokens);
     const uint64_t hi = min(kSmall ? lo + a.sub_tokens : min(lo + a.sub_tokens, tile + a.tile_tokens), a.tokens);
     if (kSmall) {
         int32_t* all = by_warp;
@@ -184,7 +183,7 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_move_kernel(DispatchArg
         __syncthreads();
     } else {
         for (uint32_t e = tid; e < B; e += kMoveThreads)
-            first[e] = ld_l2(a.base + (uint64_t)e * a.tiles + counted) + ld_l2(a.offsets + e);
+            first[e] = ld_l2(a.base + counted * B + e) + ld_l2(a.offsets + e);
         __syncthreads();
         for (uint64_t i = tile * a.K + tid; i < lo * a.K; i += kMoveThreads) atomicAdd(&first[bucket_of(a.idx[i], a.E)], 1);
         __syncthreads();
@@ -243,23 +242,28 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_move_kernel(DispatchArg
 }
 
 struct DispatchPlan {
-    uint32_t tiles, tile_tokens, sub_tokens, ctas;
+    uint32_t tiles, tile_tokens, sub_tokens, subs, ctas;
     bool small;
 };
 
 // Few slots: a CTA for a token, or for as many as make two CTAs per SM.  Many:
-// one counted tile per SM, moved by kSubTiles CTAs.
-DispatchPlan dispatch_plan(uint64_t tokens, uint32_t top_k, int sms)
+// counted tiles, one per SM at most, each moved by several CTAs.
+DispatchPlan dispatch_plan(uint64_t tokens, uint32_t top_k, uint64_t hidden, int sms)
 {
     DispatchPlan p{};
     p.small = tokens * top_k <= kSmallSlots;
-    const uint64_t most = p.small ? (uint64_t)sms * 2 : (uint64_t)sms;
+    const uint64_t full = (tokens * top_k + kTileSlots - 1) / kTileSlots;
+    const uint64_t most = p.small ? (uint64_t)sms * 2 : full < (uint64_t)sms ? full : (uint64_t)sms;
     p.tile_tokens = (uint32_t)((tokens + most - 1) / most);
     if (p.tile_tokens == 0) p.tile_tokens = 1;
     p.tiles = (uint32_t)((tokens + p.tile_tokens - 1) / p.tile_tokens);
     if (p.tiles == 0) p.tiles = 1;
-    p.sub_tokens = p.small ? p.tile_tokens : (p.tile_tokens + kSubTiles - 1) / kSubTiles;
-    p.ctas = p.small ? p.tiles : p.tiles * kSubTiles;
+    uint64_t sub = kSubBytes / (2 * top_k * hidden + 1) + 1;
+    const uint32_t least = (p.tile_tokens + kSubTiles - 1) / kSubTiles;
+    if (sub < least) sub = least;
+    p.sub_tokens = p.small || sub > p.tile_tokens ? p.tile_tokens : (uint32_t)sub;
+    p.subs = p.small ? 1 : (p.tile_tokens + p.sub_tokens - 1) / p.sub_tokens;
+    p.ctas = p.tiles * p.subs;
     return p;
 }
 
@@ -317,7 +321,7 @@ zccl_status_t zccl_dispatch(const int32_t* d_idx, uint64_t tokens, uint32_t expe
     if (ws_bytes < need) return ZCCL_ERR_BUFFER_TOO_SMALL;
     const int sms = sm_count();
     if (sms == 0) return ZCCL_ERR_CUDA;
-    const DispatchPlan p = dispatch_plan(tokens, top_k, sms < 512 ? sms : 512);
+    const DispatchPlan p = dispatch_plan(tokens, top_k, move ? hidden : 0, sms < 512 ? sms : 512);
     DispatchArgs a{};
     a.idx = d_idx;
     a.tokens = tokens;
@@ -337,6 +341,7 @@ zccl_status_t zccl_dispatch(const int32_t* d_idx, uint64_t tokens, uint32_t expe
     a.tiles = p.tiles;
     a.tile_tokens = p.tile_tokens;
     a.sub_tokens = p.sub_tokens;
+    a.subs = p.subs;
     a.ticket = reinterpret_cast<uint32_t*>(d_ws);
     a.base = reinterpret_cast<int32_t*>((uint8_t*)d_ws + 256);
     const size_t smem = sizeof(int32_t) * ((experts + 1) + kMoveThreads + (size_t)(kMoveWarps + 1) * (experts + 1));

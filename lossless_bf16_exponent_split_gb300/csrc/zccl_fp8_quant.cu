@@ -6,7 +6,9 @@
 // group; a CTA takes 128 x 128 values, keeps them in registers between the
 // maximum and the conversion, and exchanges the axes of the codes in shared
 // memory.  All are bound by HBM: each value is read once (2 bytes for BF16)
-// and written once (1 byte).
+// and written once (1 byte).  131072 x 2048 BF16 by rows: 122 us, 6.6 TB/s; 4096 x
+// 14336 along the rows and by rows in one pass: 52 us, 4.5 TB/s (the exchange and
+// 7 waves of tiles), 4096 x 4096 along the rows alone 12 us.
 #include "zccl_fp8.cuh"
 
 namespace zccl {
