@@ -45,7 +45,7 @@ struct MatmulArgs {
     uint32_t* ticket;        // zero before the launch
     uint32_t split;          // matmul_split()
     uint32_t* counters;      // kJoinCounters, zero before the launch
-    float* parts;            // matmul_part_bytes()
+    float* parts;            // part_bytes()
     uint32_t* status;
 };
 
@@ -62,6 +62,9 @@ struct WgradArgs {
     void* out;               // [G][m][n]
     int out_f32;
     uint32_t* ticket;        // zero before the launch
+    uint32_t split;          // wgrad_split()
+    uint32_t* counters;      // kJoinCounters, zero before the launch
+    float* parts;            // part_bytes()
     uint32_t* status;
 };
 
@@ -88,11 +91,12 @@ struct PackArgs {
     uint8_t* packed_t;       // may be nullptr: the weight with its two axes exchanged
 };
 
-// Parts that the reduction of launch_matmul()'s tiles is cut into, and the room
-// for their sums (0 without parts).
+// Parts that the reduction of a product's tiles is cut into, and the room for
+// their sums (0 without parts).
 constexpr uint32_t kJoinParts = 160, kJoinCounters = 8 * kJoinParts;
 uint32_t matmul_split(uint64_t rows, uint64_t n, uint64_t k, uint32_t groups);
-uint64_t matmul_part_bytes(uint32_t split);
+uint32_t wgrad_split(uint64_t rows, uint64_t m, uint64_t n, uint32_t groups);
+uint64_t part_bytes(uint32_t split);
 
 cudaError_t launch_matmul(const MatmulArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_wgrad(const WgradArgs& a, int sms, cudaStream_t stream);

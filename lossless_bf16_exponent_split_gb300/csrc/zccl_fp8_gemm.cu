@@ -103,7 +103,7 @@ template <bool kWgrad>
 __device__ __forceinline__ uint32_t tile_count(const TileArgs& a, const uint32_t* prefix, uint32_t tail0, uint32_t split)
 {
     const uint32_t nt = (a.n + kTileN - 1) / kTileN;
-    if (kWgrad) return a.G * ((a.m + kTileM - 1) / kTileM) * nt;
+    if (kWgrad) return a.G * ((a.m + kTileM - 1) / kTileM) * nt * split;
     return (prefix[a.G] * split + (a.rows - tail0 + kTileM - 1) / kTileM) * nt;
 }
 
@@ -116,10 +116,14 @@ __device__ __forceinline__ Tile tile_at(const TileArgs& a, const uint32_t* prefi
     uint32_t mt, i, lo = 0, kb0 = 0;
     if (kWgrad) {
         mt = (a.m + kTileM - 1) / kTileM;
-        c.g = t / (mt * nt);
-        i = t - c.g * mt * nt;
+        c.join = t / split;
+        c.part = t - c.join * split;
+        c.g = c.join / (mt * nt);
+        i = c.join - c.g * mt * nt;
         c.g = order[c.g];
-        c.blocks = prefix[c.g + 1] - prefix[c.g];
+        const uint32_t blocks = prefix[c.g + 1] - prefix[c.g];
+        kb0 = c.part * blocks / split;
+        c.blocks = (c.part + 1) * blocks / split - kb0;
         c.row_end = a.m;
     } else {
         const uint32_t whole = t / split, mb = whole / nt;
@@ -149,8 +153,8 @@ __device__ __forceinline__ Tile tile_at(const TileArgs& a, const uint32_t* prefi
     c.m0 = lo + (band * kBandRows + in_band - col * height) * kTileM;
     c.n0 = col * kTileN;
     if (kWgrad) {
-        c.sa0 = prefix[c.g] * a.m;
-        c.sb0 = prefix[c.g] * a.n;
+        c.sa0 = (prefix[c.g] + kb0) * a.m;
+        c.sb0 = (prefix[c.g] + kb0) * a.n;
         c.a0 = c.sa0 + c.m0;
         c.b0 = c.sb0 + c.n0;
     } else {
@@ -365,7 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint32_t tmem = s->tmem;
     // there is room for kJoinParts; what the host reckoned with may be less than the groups' blocks
-    const uint32_t split = kWgrad || s->prefix[a.G] * ((a.n + kTileN - 1) / kTileN) * a.split > kJoinParts ? 1 : a.split;
+    const uint32_t row_tiles = kWgrad ? a.G * ((a.m + kTileM - 1) / kTileM) : s->prefix[a.G];
+    const uint32_t split = row_tiles * ((a.n + kTileN - 1) / kTileN) * a.split > kJoinParts ? 1 : a.split;
 
     if (warp < 4) {
         regs_fewer<kRegsFew>();
@@ -582,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint32_t row = c.m0 + sub * 32, n = c.n0 + wg * kSumCols;
             if (ok && row < c.row_end && n < a.n &&
-                (kWgrad || split == 1 || c.blocks == 0 || join_parts(a, c, split, warp - 4, lane, acc)))
+                (split == 1 || (!kWgrad && c.blocks == 0) || join_parts(a, c, split, warp - 4, lane, acc)))
                 store_rows(s->out[warp - 4], &map_out, a.tma_out, reinterpret_cast<T*>(a.out),
                            (kWgrad ? (uint64_t)c.g * a.m : 0) + row, c.row_end - row, n, a.n, &turn, acc);
         }
@@ -669,17 +674,27 @@ cudaError_t launch_tiles(TileArgs a, const uint8_t* qa, uint64_t rows_a, const u
 // 4096 x 14336 (n x k) 28 us in four parts and 55 whole, by 4096 x 4096 17.2 and
 // 19.6, by 1024 x 2048 (16 blocks) 14.3 and 13.2.  Eight parts: 29.6 and 21.3 for
 // the first two.
-uint32_t matmul_split(uint64_t rows, uint64_t n, uint64_t k, uint32_t groups)
+static uint32_t split_of(uint64_t tiles, uint64_t blocks)
 {
-    const uint64_t active = rows < groups ? rows : groups, by_rows = (rows + kTileM - 1) / kTileM;
-    const uint64_t tiles = (active > by_rows ? active : by_rows) * ((n + kTileN - 1) / kTileN), blocks = blocks_of(k);
     if (tiles == 0 || blocks < 24) return 1;
     uint64_t split = 152 / tiles < 4 ? 152 / tiles : 4;
     if (split > blocks / 8) split = blocks / 8;
     return split < 2 ? 1 : (uint32_t)split;
 }
 
-uint64_t matmul_part_bytes(uint32_t split) { return split > 1 ? (uint64_t)kJoinParts * kTileM * kTileN * 4 : 0; }
+uint32_t matmul_split(uint64_t rows, uint64_t n, uint64_t k, uint32_t groups)
+{
+    const uint64_t active = rows < groups ? rows : groups, by_rows = (rows + kTileM - 1) / kTileM;
+    return split_of((active > by_rows ? active : by_rows) * ((n + kTileN - 1) / kTileN), blocks_of(k));
+}
+
+// The mean group's blocks stand for those of all.
+uint32_t wgrad_split(uint64_t rows, uint64_t m, uint64_t n, uint32_t groups)
+{
+    return split_of(groups * ((m + kTileM - 1) / kTileM) * ((n + kTileN - 1) / kTileN), rows / kFp8Block / groups);
+}
+
+uint64_t part_bytes(uint32_t split) { return split > 1 ? (uint64_t)kJoinParts * kTileM * kTileN * 4 : 0; }
 
 cudaError_t launch_matmul(const MatmulArgs& m, int sms, cudaStream_t stream)
 {
@@ -716,9 +731,11 @@ cudaError_t launch_wgrad(const WgradArgs& w, int sms, cudaStream_t stream)
     a.blocks = w.blocks;
     a.out = w.out;
     a.ticket = w.ticket;
-    a.split = 1;
+    a.split = w.split;
+    a.counters = w.counters;
+    a.parts = w.parts;
     a.status = w.status;
-    const uint64_t most = (uint64_t)w.G * ((w.m + kTileM - 1) / kTileM) * ((w.n + kTileN - 1) / kTileN);
+    const uint64_t most = (uint64_t)w.G * ((w.m + kTileM - 1) / kTileM) * ((w.n + kTileN - 1) / kTileN) * w.split;
     const auto launch = w.out_f32 ? launch_tiles<true, float> : launch_tiles<true, __nv_bfloat16>;
     return launch(a, w.a, (uint64_t)w.blocks * w.m, w.b, (uint64_t)w.blocks * w.n, (uint64_t)w.G * w.m, most, sms, stream);
 }

@@ -20,7 +20,7 @@ bool sizes_ok(uint64_t rows, uint64_t k, uint64_t n, uint32_t groups)
 bool float_type(int t) { return t == ZCCL_BF16 || t == ZCCL_F32; }
 uintptr_t size_of(int t) { return t == ZCCL_BF16 ? 2 : 4; }
 
-// A workspace begins with the counters of a call's products: two tickets, then those of a matmul's parts.
+// A workspace begins with the counters of a call's products: two tickets, then those of a product's parts.
 constexpr uint64_t kCountersAt = 256;
 constexpr uint64_t kTicketBytes = kCountersAt + 4 * kJoinCounters;
 static_assert(kTicketBytes % 256 == 0, "what follows is aligned");
@@ -50,7 +50,7 @@ RowsLayout tokens_layout(uint64_t at, uint64_t rows, uint64_t cols, uint32_t gro
 }
 
 // y = x times the transpose of the packed weight [groups][n][k].  x nullptr: x is
-// quantised in the workspace already.  parts: room for matmul_part_bytes().
+// quantised in the workspace already.  parts: room for part_bytes().
 zccl_status_t linear(const void* x, int dtype, uint64_t stride, uint64_t rows, uint64_t k, const uint8_t* weight, uint64_t n,
                      uint32_t groups, const int32_t* offsets, void* out, int out_dtype, uint8_t* ws, uint8_t* parts,
                      uint32_t* status, int sms, cudaStream_t stream)
@@ -139,10 +139,11 @@ zccl_status_t zccl_fp8_linear_workspace_bytes(uint64_t rows, uint64_t k, uint64_
 {
     if (bytes == nullptr || !sizes_ok(rows, k, n, groups)) return ZCCL_ERR_INVALID_ARG;
     if (!backward) {
-        *bytes = rows_layout(kTicketBytes, rows, k).end + matmul_part_bytes(matmul_split(rows, n, k, groups));
+        *bytes = rows_layout(kTicketBytes, rows, k).end + part_bytes(matmul_split(rows, n, k, groups));
     } else {
         const RowsLayout dy = rows_layout(kTicketBytes, rows, n), dyt = tokens_layout(dy.end, rows, n, groups);
-        *bytes = tokens_layout(dyt.end, rows, k, groups).end + matmul_part_bytes(matmul_split(rows, k, n, groups));
+        const uint32_t split = matmul_split(rows, k, n, groups), split_w = wgrad_split(rows, n, k, groups);
+        *bytes = tokens_layout(dyt.end, rows, k, groups).end + part_bytes(split > split_w ? split : split_w);
     }
     return ZCCL_OK;
 }
@@ -220,7 +221,8 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
     r.q = ws + xt.q;
     r.scale = reinterpret_cast<float*>(ws + xt.scale);
     r.q_rows = nullptr;
-    r.counters = nullptr;
+    const uint32_t split = wgrad_split(rows, n, k, groups);
+    r.counters = split > 1 ? reinterpret_cast<uint32_t*>(ws + kCountersAt) : nullptr;
     r.ticket = reinterpret_cast<uint32_t*>(ws) + 32;
     if (launch_quantize_tokens(r, dtype, sms, stream) != cudaSuccess) return ZCCL_ERR_CUDA;
     WgradArgs w{};
@@ -237,6 +239,9 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
     w.out = d_grad_w;
     w.out_f32 = out_dtype == ZCCL_F32;
     w.ticket = reinterpret_cast<uint32_t*>(ws) + 32;
+    w.split = split;
+    w.counters = reinterpret_cast<uint32_t*>(ws + kCountersAt);
+    w.parts = reinterpret_cast<float*>(ws + xt.end);
     w.status = d_status;
     return launched(launch_wgrad(w, sms, stream));
 }
