@@ -457,20 +457,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
             // ---- scales: 32 threads, four rows and (weight gradient) eight columns each.  A block's slot is free
             // once the block four before it was taken, which the barrier of the block two before it says; that block's
-            // own scales, which have landed by then, are reported first
+            // own scales, which have landed by then, are reported first.  A tile without blocks reports what is left:
+            // the sums of a tile before it must not wait for blocks that are more tiles away than there are slots
             const uint32_t last = (kWgrad ? a.m : a.rows) - 1, nbs = (uint32_t)blocks_of(a.n);
-            uint32_t count = 0, stage = 0, phase = 0;
+            uint32_t count = 0, told = 0, stage = 0, phase = 0;  // blocks asked for, and reported
+            auto report_next = [&] {
+                if (!wait_phase(&s->full[stage], phase, a.status)) return false;
+                mbar_arrive(&s->done[told & 1]);
+                ++told;
+                if (++stage == kStages) stage = 0, phase ^= 1;
+                return true;
+            };
+            auto report_all = [&] {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                while (ok && told < count) ok = report_next();
+            };
             while (ok && next_tile(s, &k, &c, lane, a.status)) {
+                if (c.blocks == 0) report_all();
                 const float* row = a.sa + c.sa0;
                 const float* col = a.sb + c.sb0 + (kWgrad ? 0 : min(c.n0 / kFp8Block + lane, nbs - 1) * a.KB);
 #pragma unroll 1
                 for (uint32_t b = 0; b < c.blocks; ++b, ++count) {
                     const uint32_t slot = count % kScaleSlots;
-                    if (count >= kScaleLag) {
-                        if (!(ok = wait_phase(&s->full[stage], phase, a.status))) break;
+                    if (count - told >= kScaleLag) {
                         asm volatile("cp.async.wait_group %0;" ::"n"(kScaleLag - 1) : "memory");
-                        mbar_arrive(&s->done[count & 1]);
-                        if (++stage == kStages) stage = 0, phase ^= 1;
+                        if (!(ok = report_next())) break;
                     }
 #pragma unroll
                     for (uint32_t j = 0; j < kTileM; j += 32)
@@ -488,12 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     asm volatile("cp.async.commit_group;" ::: "memory");
                 }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            for (uint32_t ready = count > kScaleLag ? count - kScaleLag : 0; ok && ready < count; ++ready) {
-                if (!(ok = wait_phase(&s->full[stage], phase, a.status))) break;
-                mbar_arrive(&s->done[ready & 1]);
-                if (++stage == kStages) stage = 0, phase ^= 1;
-            }
+            report_all();
         }
     } else {
         regs_more<kRegsMany>();
