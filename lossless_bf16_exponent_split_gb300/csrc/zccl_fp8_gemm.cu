@@ -187,65 +187,73 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t phase, uint32
 
 // The sums of a warp's 32 rows x 128 columns (lane = row) to the output, from
 // row `row` (of `rows` inside the output, counted from there) and column n on,
-// through the warp's two staging buffers in turn: rows of 128 bytes whose 16-byte
-// pieces are XOR-swizzled with the row.  A whole box goes by one asynchronous TMA
-// store that runs beside the next tile (all CTAs end their tiles together: stored
-// by the threads, a tile's 64 KB took 4000 cycles); cut rows go by the threads.
+// through the warp's two staging buffers, two pieces of 128 bytes a row at a time
+// (one fence for both): rows of 128 bytes whose 16-byte pieces are XOR-swizzled
+// with the row.  A whole box goes by one asynchronous TMA store that runs beside
+// the next tile (all CTAs end their tiles together: stored by the threads, a
+// tile's 64 KB took 4000 cycles); cut rows go by the threads.
 template <typename T>
 __device__ __forceinline__ void store_rows(uint8_t (&bufs)[2][32 * 128], const CUtensorMap* map, int tma, T* out,
-                                           uint64_t row, uint32_t rows, uint32_t n, uint32_t n_end, uint32_t* turn,
+                                           uint64_t row, uint32_t rows, uint32_t n, uint32_t n_end,
                                            const float (&acc)[kSumCols])
 {
     constexpr uint32_t kCols = 128 / sizeof(T);  // columns of a staged row
     constexpr uint32_t kPer = 16 / sizeof(T);    // columns of a piece
     const uint32_t lane = threadIdx.x & 31;
 #pragma unroll
-    for (uint32_t h = 0; h < kSumCols; h += kCols) {
-        if (n + h >= n_end) break;
-        uint8_t* buf = bufs[*turn & 1];
-        if (lane == 0) bulk_wait_read1();  // the buffer's last store: all but the other buffer's, the latest
+    for (uint32_t h0 = 0; h0 < kSumCols; h0 += 2 * kCols) {
+        if (n + h0 >= n_end) break;
+        const bool two = n + h0 + kCols < n_end;
+        if (lane == 0) bulk_wait_read0();  // the buffers' last stores
         __syncwarp();
 #pragma unroll
-        for (uint32_t p = 0; p < 8; ++p) {
-            const float* x = &acc[h + p * kPer];
-            uint4 v;
-            if (sizeof(T) == 2)
-                v = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4 % kPer], x[5 % kPer]),
-                               pack_bf16(x[6 % kPer], x[7 % kPer]));
-            else
-                v = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-            *reinterpret_cast<uint4*>(buf + lane * 128 + ((p ^ (lane & 7)) * 16)) = v;
+        for (uint32_t t = 0; t < 2; ++t) {
+            if (t == 1 && !two) break;
+#pragma unroll
+            for (uint32_t p = 0; p < 8; ++p) {
+                const float* x = &acc[h0 + t * kCols + p * kPer];
+                uint4 v;
+                if (sizeof(T) == 2)
+                    v = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4 % kPer], x[5 % kPer]),
+                                   pack_bf16(x[6 % kPer], x[7 % kPer]));
+                else
+                    v = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+                *reinterpret_cast<uint4*>(bufs[t] + lane * 128 + ((p ^ (lane & 7)) * 16)) = v;
+            }
         }
         if (tma && rows >= 32) {
-            ++*turn;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                tma_store_2d(map, buf, (int32_t)(n + h), (int32_t)row);
+                tma_store_2d(map, bufs[0], (int32_t)(n + h0), (int32_t)row);
+                if (two) tma_store_2d(map, bufs[1], (int32_t)(n + h0 + kCols), (int32_t)row);
                 bulk_commit();
             }
-            __syncwarp();
-        } else if (tma) {  // cut rows, in whole pieces: the output's width is a multiple of a piece's
-            __syncwarp();
-            const uint32_t p = lane & 7;
-            T* to = out + (row + (lane >> 3)) * n_end + n + h + p * kPer;
+            continue;
+        }
+        __syncwarp();
 #pragma unroll 1
-            for (uint32_t r = lane >> 3; r < 32; r += 4, to += 4 * (uint64_t)n_end)
-                if (r < rows && n + h + p * kPer < n_end)
-                    *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(buf + r * 128 + ((p ^ (r & 7)) * 16));
-            __syncwarp();
-        } else {  // a value at a time, consecutive lanes consecutive columns
-            __syncwarp();
-            const uint32_t cols = min(kCols, n_end - n - h);
-            T* to = out + row * n_end + n + h;
+        for (uint32_t t = 0; t < (two ? 2 : 1); ++t) {
+            const uint32_t h = h0 + t * kCols;
+            const uint8_t* buf = bufs[t];
+            if (tma) {  // cut rows, in whole pieces: the output's width is a multiple of a piece's
+                const uint32_t p = lane & 7;
+                T* to = out + (row + (lane >> 3)) * n_end + n + h + p * kPer;
+#pragma unroll 1
+                for (uint32_t r = lane >> 3; r < 32; r += 4, to += 4 * (uint64_t)n_end)
+                    if (r < rows && n + h + p * kPer < n_end)
+                        *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(buf + r * 128 + ((p ^ (r & 7)) * 16));
+            } else {  // a value at a time, consecutive lanes consecutive columns
+                const uint32_t cols = min(kCols, n_end - n - h);
+                T* to = out + row * n_end + n + h;
 #pragma unroll 4
-            for (uint32_t i = lane; i < 32 * kCols; i += 32) {
-                const uint32_t r = i / kCols, j = i % kCols;
-                if (r < rows && j < cols)
-                    to[(uint64_t)r * n_end + j] =
-                        reinterpret_cast<const T*>(buf + r * 128 + (((j / kPer) ^ (r & 7)) * 16))[j % kPer];
+                for (uint32_t i = lane; i < 32 * kCols; i += 32) {
+                    const uint32_t r = i / kCols, j = i % kCols;
+                    if (r < rows && j < cols)
+                        to[(uint64_t)r * n_end + j] =
+                            reinterpret_cast<const T*>(buf + r * 128 + (((j / kPer) ^ (r & 7)) * 16))[j % kPer];
+                }
             }
-            __syncwarp();
         }
     }
 }
@@ -518,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t free0 = smem_addr(&s->full[2 % kStages]), free1 = smem_addr(&s->full[3 % kStages]),
                  free2 = smem_addr(&s->full[4 % kStages]);
         static_assert(kStages == 3, "three barriers take turns");
-        uint32_t k = 0, count = 0, turn = 0;
+        uint32_t k = 0, count = 0;
         bool ok = true;
         Tile c;
         arrive_lane0(smem_addr(&s->full[0]), lane);  // both accumulators are free for the first two blocks
@@ -595,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && row < c.row_end && n < a.n &&
                 (split == 1 || (!kWgrad && c.blocks == 0) || join_parts(a, c, split, warp - 4, lane, acc)))
                 store_rows(s->out[warp - 4], &map_out, a.tma_out, reinterpret_cast<T*>(a.out),
-                           (kWgrad ? (uint64_t)c.g * a.m : 0) + row, c.row_end - row, n, a.n, &turn, acc);
+                           (kWgrad ? (uint64_t)c.g * a.m : 0) + row, c.row_end - row, n, a.n, acc);
         }
         if (lane == 0) bulk_wait0();
     }
