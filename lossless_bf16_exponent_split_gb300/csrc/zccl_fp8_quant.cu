@@ -61,6 +61,7 @@ template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantArgs a)
 {
     pdl_wait();
+    pdl_launch_dependents();  // the product may start: what it reads before its own wait was there before this kernel
     zero_counters(a);
     const uint32_t lane = threadIdx.x & 31, half = lane >> 4, i8 = (lane & 15) * 8;
     const uint32_t nb = (uint32_t)blocks_of(a.cols), pairs = (nb + 1) / 2;
@@ -132,6 +133,7 @@ __device__ __forceinline__ constexpr uint32_t owner_of(uint32_t row) { return 2 
 __global__ void __launch_bounds__(kThreads) quantize_rows_bf16_kernel(QuantArgs a)
 {
     pdl_wait();
+    pdl_launch_dependents();  // the product may start: what it reads before its own wait was there before this kernel
     zero_counters(a);
     const uint32_t lane = threadIdx.x & 31, half = lane >> 4, i8 = (lane & 15) * 8;
     const uint32_t nb = (uint32_t)blocks_of(a.cols), pairs = (nb + 1) / 2;
@@ -235,6 +237,7 @@ __global__ void __launch_bounds__(kThreads) quantize_tokens_kernel(QuantArgs a)
     __shared__ uint32_t prefix[kMaxGroupsFp8 + 1];
     __shared__ uint2 range[kMaxGroupsFp8];
     pdl_wait();
+    pdl_launch_dependents();  // the product may start: what it reads before its own wait was there before this kernel
     zero_counters(a);
     const uint32_t lane = threadIdx.x & 31, part = threadIdx.x >> 5;
     group_prefix(a.offsets, a.rows, a.G, kFp8Block, (uint32_t)(a.rows / kFp8Block + a.G), prefix);
@@ -291,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, kRows ? 3 : 4) quantize_tokens_bf16_
     __shared__ uint32_t prefix[kMaxGroupsFp8 + 1];
     __shared__ uint2 range[kMaxGroupsFp8];
     pdl_wait();
+    pdl_launch_dependents();  // the product may start: what it reads before its own wait was there before this kernel
     zero_counters(a);
     const uint32_t lane = threadIdx.x & 31, part = threadIdx.x >> 5;
     group_prefix(a.offsets, a.rows, a.G, kFp8Block, (uint32_t)(a.rows / kFp8Block + a.G), prefix);

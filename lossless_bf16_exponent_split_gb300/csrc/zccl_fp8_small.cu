@@ -25,6 +25,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kTileRows = 16;  // weight rows of a warp
+constexpr uint32_t kEarly = 4;      // blocks of a warp that are asked for while x is quantised
 constexpr int kFlight = 2;          // blocks in flight in a warp; with three CTAs an SM enough to fill the memory's latency
 
 __device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -35,6 +36,12 @@ __device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Consecutive bytes to L2 (16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // `split` warps (1, 2, 4 or 8) share a warp's weight rows.
 template <typename T, int kNT>
 __global__ void __launch_bounds__(kThreads, kNT == 4 ? 2 : 3) small_kernel(MatmulArgs a, uint32_t split)
@@ -43,14 +50,22 @@ __global__ void __launch_bounds__(kThreads, kNT == 4 ? 2 : 3) small_kernel(Matmu
     __shared__ float sums[kWarps][kNT * 4][32];
     __shared__ uint32_t prefix[kMaxGroupsFp8 + 1];
     __shared__ uint2 range[kMaxGroupsFp8];
-    pdl_wait();
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, q = lane & 3;
+    // The kernel before this one quantises x.  It lets this one start once everything before it is done, so the
+    // groups' table and the weights can be read; x and its scales, and anything written, come after the wait.
     group_prefix(a.offsets, a.rows, a.G, kChunk, 0x7FFFFFFFu, prefix);
     for (uint32_t g = threadIdx.x; g < a.G; g += kThreads) group_rows(a.offsets, a.rows, g, &range[g].x, &range[g].y);
     __syncthreads();
     const uint32_t nbs = (uint32_t)blocks_of(a.n), wide = kWarps / split * kTileRows;  // weight rows of a CTA
     const uint32_t tiles = (a.n + wide - 1) / wide, first = warp % split;
     const uint64_t items = (uint64_t)prefix[a.G] * tiles;
+    if (blockIdx.x < items) {  // the first weights to L2 meanwhile, a lane a block (1 to 2 us less a call)
+        const uint32_t chunk = blockIdx.x / tiles, g = group_at(prefix, a.G, chunk), kb = first + lane * split;
+        const uint32_t n0 = (blockIdx.x - chunk * tiles) * wide + warp / split * kTileRows;
+        if (lane < kEarly && kb < a.KB && n0 < a.n)
+            prefetch_l2(a.b + (((uint64_t)g * a.KB + kb) * a.n + n0) * kFp8Block, min(kTileRows, a.n - n0) * kFp8Block);
+    }
+    pdl_wait();
     for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const uint32_t chunk = (uint32_t)(it / tiles);
         const uint32_t n0 = (uint32_t)(it - (uint64_t)chunk * tiles) * wide + warp / split * kTileRows;
@@ -187,10 +202,10 @@ cudaError_t small_typed(const MatmulArgs& a, int sms, cudaStream_t stream)
 // says.  The other: 0.55 us a round of its tiles (less in parts, and 5 us a call
 // to join them), or 25 ps a weight row, the memory's time.  Measured, this one
 // and the other, in us a call (n x k):
-//   14336 x 4096, 1 group: 1 row 13.9, 25.5; 8 rows 14.1, 21.8; 32 rows 36.8, 21.3
-//   4096 x 4096, 1 group: 1 row 8.1, 18.0; 32 rows 14.7, 16.1; 48 rows 22.5, 17.2
-//   4096 x 4096, 8 groups: 8 rows 21.7, 29.1; 64 rows 34.1, 29.8; 256 rows 83.8, 30.4
-//   1024 x 2048, 64 groups: 64 rows 21.1, 28.7; 256 rows 30.8, 31.4; 768 rows 45.7, 32.8
+//   14336 x 4096, 1 group: 1 row 12.9, 25.5; 8 rows 13.4, 21.8; 32 rows 36.8, 21.3
+//   4096 x 4096, 1 group: 1 row 7.1, 18.0; 32 rows 13.3, 16.1; 48 rows 22.5, 17.2
+//   4096 x 4096, 8 groups: 8 rows 21.1, 29.1; 64 rows 34.1, 29.8; 256 rows 83.8, 30.4
+//   1024 x 2048, 64 groups: 64 rows 19.8, 28.7; 256 rows 30.8, 31.4; 768 rows 45.7, 32.8
 bool takes_small(uint64_t rows, uint64_t n, uint64_t k, uint32_t groups, int sms)
 {
     if (rows > 32ull * groups) return false;
