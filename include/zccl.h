@@ -54,7 +54,9 @@
  * failed, may leave its control words mid-call: zero the workspace again
  * (zccl_workspace_init) before its next use.  A workspace must not be used
  * by two calls that may run at the same time (different streams): they
- * would race.
+ * would race.  Nor by two host threads at once, even on one stream: a call
+ * queues several kernels that hand data over in it, and those of the other
+ * call could come between them.
  */
 #ifndef ZCCL_H
 #define ZCCL_H

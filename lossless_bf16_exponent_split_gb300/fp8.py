@@ -26,7 +26,8 @@ class Fp8Weight(NamedTuple):
 
 
 class BlockFp8:
-    """A device status word, workspaces and the calls of the block-scaled e4m3 layers."""
+    """A device status word, workspaces and the calls of the block-scaled e4m3 layers;
+    any streams and host threads may share one."""
 
     def __init__(self, device=None):
         self._lib = lib()
@@ -107,11 +108,12 @@ class BlockFp8:
         rows = x.shape[0]
         out = torch.empty(rows, weight.n, dtype=out_dtype, device=self.device)
         stream = current_stream(self.device)
-        ws = self._workspaces.get(zccl_fp8_linear_workspace_bytes(rows, weight.k, weight.n, weight.groups, False), stream,
-                                  self.device)
-        st = self._lib.zccl_fp8_linear(ptr, _DTYPES[x.dtype], stride, rows, weight.k, weight.packed.data_ptr(), weight.n,
-                                       weight.groups, off, out.data_ptr(), _out_type(out_dtype), ws.data_ptr(),
-                                       ws.numel(), self.status.data_ptr(), stream)
+        nbytes = zccl_fp8_linear_workspace_bytes(rows, weight.k, weight.n, weight.groups, False)
+        with self._workspaces.lock:
+            ws = self._workspaces.get(nbytes, stream, self.device)
+            st = self._lib.zccl_fp8_linear(ptr, _DTYPES[x.dtype], stride, rows, weight.k, weight.packed.data_ptr(), weight.n,
+                                           weight.groups, off, out.data_ptr(), _out_type(out_dtype), ws.data_ptr(),
+                                           ws.numel(), self.status.data_ptr(), stream)
         check(st, "zccl_fp8_linear")
         return out
 
@@ -131,13 +133,14 @@ class BlockFp8:
         dx = torch.empty(rows, weight.k, dtype=out_dtype, device=self.device) if input_grad else None
         dw = torch.empty(weight.groups, weight.n, weight.k, dtype=out_dtype, device=self.device) if weight_grad else None
         stream = current_stream(self.device)
-        ws = self._workspaces.get(zccl_fp8_linear_workspace_bytes(rows, weight.k, weight.n, weight.groups, True), stream,
-                                  self.device)
-        st = self._lib.zccl_fp8_linear_backward(
-            gptr, xptr, _DTYPES[grad.dtype], gstride, xstride, rows, weight.k,
-            None if weight.packed_t is None else weight.packed_t.data_ptr(), weight.n, weight.groups, off,
-            None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(), _out_type(out_dtype),
-            ws.data_ptr(), ws.numel(), self.status.data_ptr(), stream)
+        nbytes = zccl_fp8_linear_workspace_bytes(rows, weight.k, weight.n, weight.groups, True)
+        with self._workspaces.lock:
+            ws = self._workspaces.get(nbytes, stream, self.device)
+            st = self._lib.zccl_fp8_linear_backward(
+                gptr, xptr, _DTYPES[grad.dtype], gstride, xstride, rows, weight.k,
+                None if weight.packed_t is None else weight.packed_t.data_ptr(), weight.n, weight.groups, off,
+                None if dx is None else dx.data_ptr(), None if dw is None else dw.data_ptr(), _out_type(out_dtype),
+                ws.data_ptr(), ws.numel(), self.status.data_ptr(), stream)
         check(st, "zccl_fp8_linear_backward")
         return dx, dw
 

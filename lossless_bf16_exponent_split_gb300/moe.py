@@ -9,6 +9,7 @@ weights.
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import NamedTuple, Optional
 
 import torch
@@ -35,9 +36,12 @@ class Workspaces:
     """A workspace per stream, zeroed where the calls want that: calls on different
     streams must not share one.  A call that is captured into a CUDA graph gets one
     of its own, as the graph may be replayed on any stream, and so does one that
-    wants more than `most` bytes."""
+    wants more than `most` bytes.  `lock` is held from get() until the call's kernels
+    are queued: they hand data over in the workspace, and a call of another host
+    thread on the same stream, which gets the same one, must not come between them."""
 
     def __init__(self, zeroed: bool = True, most: int = 1 << 62):
+        self.lock = threading.Lock()
         self._by_stream = {}
         self._new = torch.zeros if zeroed else torch.empty
         self._most = most
@@ -79,7 +83,8 @@ def need(t: torch.Tensor, what: str, device, dtypes, ndim: int, rows_strided: bo
 
 
 class Moe:
-    """A router's configuration, its workspaces and a device status word.
+    """A router's configuration, its workspaces and a device status word; any
+    streams and host threads may share one.
 
     experts, top_k: how many there are and how many a token chooses; score
     "softmax" or "sigmoid"; groups / top_groups: experts in consecutive groups of
@@ -181,12 +186,13 @@ class Moe:
             table = torch.empty(2 * self.experts * SEGMENT_DTYPE.itemsize, dtype=torch.uint8, device=self.device)
             streams = torch.empty(room, dtype=torch.uint8, device=self.device)
         stream = current_stream(self.device)
-        ws = self._workspaces.get(self._ws_bytes, stream, self.device)
-        st = self._lib.zccl_dispatch(
-            idx.data_ptr(), tokens, self.experts, self.top_k, x.data_ptr() if slots else None,
-            x.stride(0) if tokens > 1 else hidden, hidden, rows.data_ptr(), pos.data_ptr(), counts.data_ptr(),
-            offsets.data_ptr(), None if table is None else table.data_ptr(), capacity or 0,
-            None if streams is None else streams.data_ptr(), room, ws.data_ptr(), ws.numel(), stream)
+        with self._workspaces.lock:
+            ws = self._workspaces.get(self._ws_bytes, stream, self.device)
+            st = self._lib.zccl_dispatch(
+                idx.data_ptr(), tokens, self.experts, self.top_k, x.data_ptr() if slots else None,
+                x.stride(0) if tokens > 1 else hidden, hidden, rows.data_ptr(), pos.data_ptr(), counts.data_ptr(),
+                offsets.data_ptr(), None if table is None else table.data_ptr(), capacity or 0,
+                None if streams is None else streams.data_ptr(), room, ws.data_ptr(), ws.numel(), stream)
         check(st, "zccl_dispatch")
         return Dispatch(rows, pos, counts, offsets, table, streams)
 
