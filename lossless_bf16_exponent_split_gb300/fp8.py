@@ -27,7 +27,8 @@ class Fp8Weight(NamedTuple):
 
 class BlockFp8:
     """A device status word, workspaces and the calls of the block-scaled e4m3 layers;
-    any streams and host threads may share one."""
+    any streams and host threads may share one.  device: default the current one;
+    calls refuse to run while another one is current."""
 
     def __init__(self, device=None):
         self._lib = lib()

@@ -60,6 +60,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def current_stream(device) -> int:
+    """The handle of the current stream of `device`, which has to be the current one:
+    the library launches there, and the default stream's handle is every device's."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"{device} is not the current CUDA device, on which the library's kernels run "
+                         "(torch.cuda.set_device, or torch.cuda.device as a context)")
     if _raw_stream is not None:
         return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
@@ -89,7 +94,8 @@ class Moe:
     experts, top_k: how many there are and how many a token chooses; score
     "softmax" or "sigmoid"; groups / top_groups: experts in consecutive groups of
     which a token may use the best top_groups (default: all); renormalize: divide
-    a token's weights by their sum; scale: the weights' factor."""
+    a token's weights by their sum; scale: the weights' factor.  device: default
+    the current one; calls refuse to run while another one is current."""
 
     def __init__(self, experts: int, top_k: int, *, score: str = "softmax", groups: int = 1,
                  top_groups: int | None = None, renormalize: bool = True, scale: float = 1.0, device=None):
