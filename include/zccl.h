@@ -442,7 +442,9 @@ zccl_status_t zccl_combine_backward(const uint16_t* d_grad_out, const uint16_t* 
  *   dW = dy^T x, summed over a group's rows: there the blocks of both factors
  *        are 128 consecutive rows of the group, column by column.
  * A row (column, for dW) that holds a NaN or an infinity gives NaN; the others
- * are not touched by it.
+ * are not touched by it.  The two scales are multiplied first, in fp32: blocks
+ * whose largest magnitudes' product is 2^145 or more can make that infinite, and
+ * the result infinite or, where their codes' sum is zero, NaN.
  * Extents: 1 <= groups <= ZCCL_MAX_EXPERTS, 1 <= k, n < 2^24, rows < 2^31 and
  * fewer than 2^31 blocks an operand. */
 

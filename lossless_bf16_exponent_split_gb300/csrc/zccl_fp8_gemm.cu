@@ -575,7 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float4 f = col[i];
-                            // the scales first: their product overflows only where the sum does
+                            // the scales first, as the definition has it: their product is finite for blocks whose
+                            // largest magnitudes' product is below 2^145
                             const float2 x0 = mul2(f.x, f.y, now), x1 = mul2(f.z, f.w, now);
                             float* to = &acc[32 * q + 4 * i];
                             const uint32_t* from_r = &r[q & 1][4 * i];
