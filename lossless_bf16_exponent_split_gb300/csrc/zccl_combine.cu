@@ -2,10 +2,11 @@
 // tokens' rows, and the gradients of the rows and of the weights.
 //
 // Both are bound by HBM.  Forward: 2 T K H bytes read and 2 T H written; a
-// thread owns one 16-byte piece of a token's row and has the K rows' pieces in
-// flight together.  Backward: 2 T K H read and as many written (the token's
-// gradient row comes from L1/L2 for all but one of its K slots); a warp owns
-// one slot, so the dot product needs no other warp.  16384 tokens, 8
+// thread owns up to four 16-byte pieces of a token's row and has eight pieces in
+// flight, of as many slots' rows as there are.  Backward: 2 T K H read and as many
+// written (the token's gradient row comes from L1/L2 for all but one of its K
+// slots); a warp owns one slot, for short rows fewer lanes of it do, so the dot
+// product needs no other warp.  16384 tokens, 8
 // slots, hidden 2048: forward 96 us (6.3 TB/s), backward 177 us (6.5 TB/s).
 #include "zccl_ops.cuh"
 

@@ -27,28 +27,24 @@ __device__ __forceinline__ void zero_counters(const QuantArgs& a)
         for (uint32_t i = threadIdx.x; i < kJoinCounters; i += kThreads) a.counters[i] = 0;
 }
 
-// Eight values of a row from column c on; zeros past the row's end.  kVec: the
-// eight are 16-byte aligned and either all in the row or all past it.
+// Eight values of a row from column c on; zeros past the row's end.  kVec (fp32;
+// BF16 rows that allow it have a kernel of their own): the eight are 16-byte
+// aligned and either all in the row or all past it.
 template <typename T, bool kVec>
 __device__ __forceinline__ void load8(const T* row, uint32_t c, uint32_t cols, float (&v)[8])
 {
-    if (kVec) {
+    if constexpr (kVec) {
+        static_assert(sizeof(T) == 4, "fp32");
         if (c >= cols) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = 0.0f;
             return;
         }
         const uint4 a = ld_once(reinterpret_cast<const uint4*>(row + c));
-        if (sizeof(T) == 2) {
-            const uint32_t q[4] = {a.x, a.y, a.z, a.w};
+        const uint4 b = ld_once(reinterpret_cast<const uint4*>(row + c) + 1);
+        const uint32_t q[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(q[i]), v[2 * i + 1] = bf16_hi(q[i]);
-        } else {
-            const uint4 b = ld_once(reinterpret_cast<const uint4*>(row + c) + 1);
-            const uint32_t q[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(q[i]);
-        }
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(q[i]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_float<T>(row[c + i]) : 0.0f;
@@ -174,16 +170,14 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_bf16_kernel(QuantArgs 
     }
 }
 
-// Four values of a row from column c on.  kVec: aligned to four values.
+// Four values of a row from column c on.  kVec (fp32): aligned to four values.
 template <typename T, bool kVec>
 __device__ __forceinline__ void load4(const T* row, uint32_t c, uint32_t cols, bool on, float (&v)[4])
 {
-    if (kVec) {
+    if constexpr (kVec) {
+        static_assert(sizeof(T) == 4, "fp32");
         if (!on || c >= cols) {
             v[0] = v[1] = v[2] = v[3] = 0.0f;
-        } else if (sizeof(T) == 2) {
-            const uint2 q = *reinterpret_cast<const uint2*>(row + c);
-            v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
         } else {
             const float4 q = *reinterpret_cast<const float4*>(row + c);
             v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
@@ -443,7 +437,12 @@ cudaError_t quantize_rows_as(const QuantArgs& a, int sms, cudaStream_t stream)
     const uint64_t warps = (blocks_of(a.cols) + 1) / 2 * ((a.rows + kRowsPerWarp - 1) / kRowsPerWarp);
     const uint32_t grid = capped((warps + kThreads / 32 - 1) / (kThreads / 32), sms, 16);
     void (*kernel)(QuantArgs) = quantize_rows_kernel<T, false>;
-    if (vectored<T>(a, 8)) kernel = sizeof(T) == 2 ? quantize_rows_bf16_kernel : quantize_rows_kernel<T, true>;
+    if (vectored<T>(a, 8)) {
+        if constexpr (sizeof(T) == 2)
+            kernel = quantize_rows_bf16_kernel;
+        else
+            kernel = quantize_rows_kernel<T, true>;
+    }
     return launch_dependent(kernel, grid, kThreads, 0, stream, a);
 }
 
@@ -453,11 +452,13 @@ cudaError_t quantize_tokens_as(const QuantArgs& a, int sms, cudaStream_t stream)
     const uint64_t tiles = (a.rows / kFp8Block + a.G) * blocks_of(a.cols);
     void (*kernel)(QuantArgs) = quantize_tokens_kernel<T, false>;
     int per_sm = 2;
-    if (sizeof(T) == 2 && vectored<T>(a, 4)) {
-        kernel = a.q_rows != nullptr ? quantize_tokens_bf16_kernel<true> : quantize_tokens_bf16_kernel<false>;
-        per_sm = a.q_rows != nullptr ? 3 : 4;
-    } else if (vectored<T>(a, 4)) {
-        kernel = quantize_tokens_kernel<T, true>;
+    if (vectored<T>(a, 4)) {
+        if constexpr (sizeof(T) == 2) {
+            kernel = a.q_rows != nullptr ? quantize_tokens_bf16_kernel<true> : quantize_tokens_bf16_kernel<false>;
+            per_sm = a.q_rows != nullptr ? 3 : 4;
+        } else {
+            kernel = quantize_tokens_kernel<T, true>;
+        }
     }
     return launch_dependent(kernel, capped(tiles, sms, per_sm), kThreads, 0, stream, a);
 }

@@ -85,13 +85,6 @@ __device__ __forceinline__ uint32_t order_key(float v)
     return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-}
-
 __device__ __forceinline__ float warp_max(float v)
 {
 #pragma unroll
