@@ -360,7 +360,8 @@ typedef struct {
  * The bias takes part in the choice only.  A logit (or bias) of -infinity makes
  * its expert unavailable; where fewer than K are available the remaining slots
  * hold index -1 and weight 0.  A row with a NaN (or, for softmax, a +infinite)
- * logit or a NaN bias chooses nothing, and *d_status gets INVALID_ARG.
+ * logit, or a NaN bias of an expert whose logit is not -infinity, chooses nothing,
+ * and *d_status gets INVALID_ARG.
  * d_idx: int32 [T][K]; d_weights: float [T][K].  T < 2^31 / K. */
 zccl_status_t zccl_route(const zccl_route_t* cfg, const void* d_logits, int dtype, uint64_t stride,
                          const float* d_bias, uint64_t tokens, int32_t* d_idx, float* d_weights,
