@@ -2,6 +2,8 @@
 
 Outputs and workspaces come from PyTorch, raw device addresses go to libzccl on
 the current CUDA stream; quantisation and products run in the library's kernels.
+The gradients are an explicit call, ``linear_backward``; nothing is recorded for
+autograd: what a call returns does not require a gradient, whatever its inputs do.
 """
 from __future__ import annotations
 

@@ -4,7 +4,8 @@ It allocates outputs and the workspace with PyTorch and passes raw device
 addresses to libzccl, on the current CUDA stream; all work runs in the
 library's kernels.  The gradients are explicit calls: ``route_backward``,
 ``combine_backward``, and, for a dispatch's tokens, ``combine`` without
-weights.
+weights.  Nothing is recorded for autograd: what a call returns does not require
+a gradient, whatever its inputs do.
 """
 from __future__ import annotations
 
