@@ -7,7 +7,7 @@
 // written (the token's gradient row comes from L1/L2 for all but one of its K
 // slots); a warp owns one slot, for short rows fewer lanes of it do, so the dot
 // product needs no other warp.  16384 tokens, 8
-// slots, hidden 2048: forward 96 us (6.3 TB/s), backward 177 us (6.5 TB/s).
+// slots, hidden 2048: forward 93 us (6.5 TB/s), backward 178 us (6.4 TB/s).
 #include "zccl_ops.cuh"
 
 namespace zccl {

@@ -14,22 +14,30 @@
 // to the sums in their registers: the scales change from block to block, so a sum
 // cannot stay in tensor memory.
 //
-// A block is 512 cycles of the tensor cores; it takes 890 to 920 here, bound by
-// the warpgroups' chain: a block's end is seen (100 cycles), 128 columns a thread
-// come out of tensor memory in pieces of 32, each waited for alone (a wait is for
-// all of a warp's loads), with the additions of the piece before under it, and
-// the accumulator goes back for the block after the next one.  What was measured
-// on the way: packed additions leave the issue slots that the issuing warp needs
-// (with single ones a block took 1800 cycles); a warp waits once a
-// block, on one barrier that the products and the scales share, and asks for the
-// next block before it has added the last columns of this one; 16 adding warps of
-// 64 columns take 1010 to 1090 cycles, pieces of 64 columns 2 % more than of 32.
-// A tile's end is 2200 cycles, through shared memory and TMA stores (stored from
-// the registers, one row a thread, 6000).
+// A block is 512 cycles of the tensor cores; it takes 890 to 940 here.  The two
+// sides of it, in cycles, 112 blocks a tile, in a build that reads the clock: with
+// the additions left out and the accumulator given back at once 924, with three
+// quarters of the weight operand's loads left out 911, with both 772, as it is
+// 937.  So the adding warps and the way of the operands (48 KB a block) are about
+// equally long, and neither alone is the bound: an adding warp finds the next
+// block done when it asks, before the last columns of this one, in 24 to 30 % of
+// the blocks.  In the weight gradient it does in 72 %: a column's scale is its own
+// there, a packed multiplication and a packed multiply-add a column pair (512
+// issue cycles a block with two warps a scheduler), and the accumulator goes back
+// after all of them, so the adding warps are the bound.  Their block: 128 columns
+// a thread come out of tensor memory in pieces of 32, each waited for alone (a
+// wait is for all of a warp's loads), with the additions of the piece before under
+// it.  What was measured on the way: packed additions leave the issue slots that
+// the issuing warp needs (with single ones a block took 1800 cycles); a warp waits
+// once a block, on one barrier that the products and the scales share; 16 adding
+// warps of 64 columns take 1010 to 1090 cycles, pieces of 64 columns 2 % more than
+// of 32.  Between a tile's last additions and the next tile's first are 2000 to
+// 3400 cycles, 1100 to 1700 of them storing through shared memory and by TMA
+// (stored from the registers, one row a thread, 6000).
 //
 // 4096 x 4096 x 14336 (m, n, k) 204 us, 2.36 PFLOP/s; 131072 rows through 64 experts
-// of 1024 x 2048 237 us, 2.32; the weight gradient of 4096 rows by 14336 x 4096,
-// whose columns have scales of their own, 242 us, 1.99.
+// of 1024 x 2048 234 us, 2.35; the weight gradient of 4096 rows by 14336 x 4096
+// 245 us, 1.96.
 #include <atomic>
 #include <cuda.h>
 
@@ -684,7 +692,8 @@ cudaError_t launch_tiles(TileArgs a, const uint8_t* qa, uint64_t rows_a, const u
 
 }  // namespace
 
-// Parts of the reduction where the tiles are too few for the SMs (152 of them).
+// Parts of the reduction where the tiles are too few for the SMs (152 of them: a
+// number of its own, so that a workspace's size is the same on any device).
 // Joining costs about 5 us, so it wants 24 blocks, 8 a part at least: 48 rows by
 // 4096 x 14336 (n x k) 28 us in four parts and 55 whole, by 4096 x 4096 17.2 and
 // 19.6, by 1024 x 2048 (16 blocks) 14.3 and 13.2.  Eight parts: 29.6 and 21.3 for

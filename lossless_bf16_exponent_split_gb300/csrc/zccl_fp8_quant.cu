@@ -6,9 +6,11 @@
 // group; a CTA takes 128 x 128 values, keeps them in registers between the
 // maximum and the conversion, and exchanges the axes of the codes in shared
 // memory.  All are bound by HBM: each value is read once (2 bytes for BF16)
-// and written once (1 byte).  131072 x 2048 BF16 by rows: 122 us, 6.6 TB/s; 4096 x
-// 14336 along the rows and by rows in one pass: 52 us, 4.5 TB/s (the exchange and
-// 7 waves of tiles), 4096 x 4096 along the rows alone 12 us.
+// and written once (1 byte).  131072 x 2048 BF16 by rows: 125 us, 6.5 TB/s; 4096 x
+// 14336 along the rows and by rows in one pass: 53 us, 4.4 TB/s (the exchange and
+// 7 waves of tiles), 4096 x 4096 along the rows alone 12 us.  Weights are read a
+// value at a time, whatever their extents: 64 x 1024 x 2048 fp32 105 us (6.4 TB/s),
+// 124 with the exchanged form, BF16 243 and 261, codes 231.
 #include "zccl_fp8.cuh"
 
 namespace zccl {

@@ -11,8 +11,10 @@
 // sums are fp32, in an order that depends on the sizes only.
 //
 // The instruction's e4m3 operands are converted in the integer pipe, which bounds
-// the kernel from 16 rows on; one row through 14336 x 4096 (n x k) takes 11.6 us
-// (5.1 TB/s), 264 rows through 64 experts of 1024 x 2048 28.6 us (4.4 TB/s).
+// the kernel from 16 rows on; one row through 14336 x 4096 (n x k) takes 12.9 us
+// with the quantisation (2.0 us alone) that it starts beside, 264 rows through 64
+// experts of 1024 x 2048 28.7 us after theirs (4.4 TB/s).  With two and four eights
+// of rows a warp the register caps spill (188 and 40 bytes a thread).
 // Measured and left out: the weights through a ring in shared memory (bulk copies
 // and these instructions, or TMA and the tensor memory's, every CTA with an equal
 // piece of all the blocks): 10 % less for the 64 experts, 15 % more for one row.

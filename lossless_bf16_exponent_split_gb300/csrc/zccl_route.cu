@@ -7,8 +7,10 @@
 // time); what a call costs are the integer instructions of the choice, at half
 // the issue rate: K rounds of a maximum over the lanes' values and the lanes.
 // Fewer lanes a token and more tokens a warp share a round's instructions.
-// Top 8 of 64 for 16384 tokens (BF16, softmax): 7.4 us forward, 3.4 backward;
-// top 8 of 256 in 8 groups for 8192 (sigmoid): 13.7 and 6.1.
+// The gradient waits for its loads: the choice, then the chosen logits, or all of
+// them for a softmax that is not renormalised.  Top 8 of 64 for 16384 tokens (BF16,
+// softmax): 7.1 us forward, 3.0 backward (4.0 not renormalised); top 8 of 256 in 8
+// groups for 8192 (sigmoid): 13.6 and 5.5.
 #include <cmath>
 
 #include "zccl_ops.cuh"
