@@ -428,6 +428,39 @@ zccl_status_t zccl_combine_backward(const uint16_t* d_grad_out, const uint16_t* 
                                     const int32_t* d_total, uint64_t tokens, uint32_t top_k,
                                     uint16_t* d_grad_y, float* d_grad_weights, cudaStream_t stream);
 
+/* Balance of a routing: a loss that is least when every expert gets as many slots
+ * as any other, and each expert's slots.  A sequence is tokens d_seq[s] ..
+ * d_seq[s + 1] - 1 (d_seq: device int32 [sequences + 1], non-decreasing from 0, at
+ * most tokens; NULL with one sequence: all tokens).  Its tokens with an entry of
+ * d_idx in 0..E-1 count, m of them, with n such entries, c[e] of expert e (an expert
+ * that a token names twice counts twice):
+ *   q       softmax: the row's probabilities; sigmoid: the row's scores over their
+ *           sum.  A logit of -infinity has q = 0, a row of them has zeros
+ *   L_s   = E / (n m) * sum over e of c[e] * (sum over its tokens of q[e])
+ *   loss  = coefficient * (mean of L_s over the sequences with m > 0); 0 without one
+ * L_s is 1 where the slots or the scores are shared out evenly.  Of cfg the fields
+ * experts, top_k and score are used.  Sums of q are held in fp32 in an order that
+ * depends on the sizes alone.  d_loss: float; d_counts: int32 [sequences][E];
+ * d_tokens: int32 [sequences + 1], each sequence's m and, last, how many have one.
+ * sequences: 1..ZCCL_MAX_SEQUENCES.  Workspace: zeroed once before its first use. */
+#define ZCCL_MAX_SEQUENCES 65536u
+zccl_status_t zccl_balance_workspace_bytes(uint32_t sequences, uint32_t experts, uint64_t* bytes);
+zccl_status_t zccl_balance(const zccl_route_t* cfg, const void* d_logits, int dtype, uint64_t stride,
+                           const int32_t* d_idx, uint64_t tokens, const int32_t* d_seq, uint32_t sequences,
+                           float coefficient, float* d_loss, int32_t* d_counts, int32_t* d_tokens, void* d_ws,
+                           uint64_t ws_bytes, cudaStream_t stream);
+
+/* Gradient of zccl_balance's loss with respect to the logits, the choice held fixed
+ * (d_counts and d_tokens: that call's), times *d_grad_loss (device float; NULL: 1).
+ * d_grad_logits as in zccl_route_backward, every element written, zero where a
+ * token does not count; with accumulate nonzero it is added, in fp32 and rounded
+ * once, to what is there (zccl_route_backward's gradient of the same logits). */
+zccl_status_t zccl_balance_backward(const zccl_route_t* cfg, const void* d_logits, int dtype, uint64_t stride,
+                                    const int32_t* d_idx, uint64_t tokens, const int32_t* d_seq, uint32_t sequences,
+                                    const int32_t* d_counts, const int32_t* d_tokens, float coefficient,
+                                    const float* d_grad_loss, void* d_grad_logits, uint64_t grad_stride, int accumulate,
+                                    cudaStream_t stream);
+
 /* ---- block-scaled e4m3 layers: the experts' products --------------------------
  *
  * y = x W^T by groups of rows (an expert's; one group: a dense layer), both
@@ -489,6 +522,83 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
                                        uint64_t n, uint32_t groups, const int32_t* d_offsets, void* d_grad_x,
                                        void* d_grad_w, int out_dtype, void* d_ws, uint64_t ws_bytes,
                                        uint32_t* d_status, cudaStream_t stream);
+
+/* ---- around a block: norms, the residual join, dropout -------------------------
+ *
+ * A block (a mixture of experts, a dense layer) reads the normed residual and its
+ * output joins the residual.  One call does the join and the norm of the next
+ * block's input:
+ *   N(v; w)[i] = w[i] * v[i] / sqrt(mean of v[j]^2 + eps)       (w NULL: 1)
+ *   b = N(y; post_weight) with cfg->post, else y
+ *   r = x + scale * gate * drop(b)                   (gate NULL: 1), rounded once
+ *   h = N(r; weight), of r as it is stored                          rounded once
+ * in fp32.  drop is zccl_dropout's, on row t and column i; a dropped element adds
+ * nothing, whatever it holds.  A row whose sum of squares is beyond fp32 gives
+ * what that makes of the formula (zeros; NaN where it is infinite already). */
+#define ZCCL_MAX_NORM_HIDDEN 65536u /* values of a row                             */
+typedef struct {
+    uint64_t hidden;  /* values of a row: 1..ZCCL_MAX_NORM_HIDDEN                   */
+    int post;         /* nonzero: the block's output is normed (post_weight)        */
+    float eps;        /* finite, > 0                                                */
+    float scale;      /* the block's factor; finite                                 */
+    float dropout;    /* 0..1                                                       */
+    uint64_t seed;    /* of the dropout                                             */
+} zccl_norm_t;
+
+/* The join and the norm, or without d_y the norm alone (h = N(x; weight); d_r NULL).
+ *   d_x       [rows] of x_dtype, x_stride elements apart: the residual; d_r: of the
+ *             same type, contiguous; d_r may be d_x where that is contiguous
+ *   d_y       [rows] of dtype; d_h: of dtype, contiguous, NULL: not computed
+ *   d_weight, d_post_weight  [hidden] of weight_dtype
+ *   d_gate    of gate_dtype: row t / gate_span is token t's (gate_span >= 1; 1: a gate
+ *             of its own for each token, rows: one for all)
+ *   offset    of the dropout, plus *d_offset where that is not NULL
+ * rows < 2^31.  Pointers are aligned to their type; rows that all begin on 16 bytes
+ * (of gate and weights too) are moved 16 bytes at a time. */
+zccl_status_t zccl_residual_norm(const zccl_norm_t* cfg, const void* d_x, int x_dtype, uint64_t x_stride,
+                                 const void* d_y, int dtype, uint64_t y_stride, const void* d_weight,
+                                 const void* d_post_weight, int weight_dtype, const void* d_gate, int gate_dtype,
+                                 uint64_t gate_stride, uint64_t gate_span, uint64_t rows, uint64_t offset,
+                                 const uint64_t* d_offset, void* d_r, void* d_h, cudaStream_t stream);
+
+/* Workspace of zccl_residual_norm_backward; its contents before a call do not matter. */
+zccl_status_t zccl_residual_norm_workspace_bytes(uint64_t hidden, uint64_t rows, uint64_t* bytes);
+
+/* Gradients of zccl_residual_norm, from those of r (d_grad_r, of x_dtype) and h
+ * (d_grad_h, of dtype); either may be NULL (none), not both.  d_r is the r that was
+ * stored (for a norm alone its x), read with d_grad_h; d_y is read with post or
+ * d_grad_gate.  Written, each of the type of what it belongs to and rounded once:
+ *   d_grad_x   [rows][hidden] contiguous, of x_dtype; NULL: not wanted
+ *   d_grad_y   [rows][hidden] contiguous, of dtype; NULL: a norm alone
+ *   d_grad_weight, d_grad_post_weight  [hidden]; d_grad_gate: [rows / gate_span, rounded
+ *              up][hidden], contiguous.  NULL: not wanted.  Their sums over rows are
+ *              held in fp32, in an order that depends on the sizes alone. */
+zccl_status_t zccl_residual_norm_backward(const zccl_norm_t* cfg, const void* d_grad_r, uint64_t grad_r_stride,
+                                          const void* d_grad_h, uint64_t grad_h_stride, const void* d_r, int x_dtype,
+                                          uint64_t r_stride, const void* d_y, int dtype, uint64_t y_stride,
+                                          const void* d_weight, const void* d_post_weight, int weight_dtype,
+                                          const void* d_gate, int gate_dtype, uint64_t gate_stride,
+                                          uint64_t gate_span, uint64_t rows, uint64_t offset,
+                                          const uint64_t* d_offset, void* d_grad_x, void* d_grad_y,
+                                          void* d_grad_weight, void* d_grad_post_weight, void* d_grad_gate, void* d_ws,
+                                          uint64_t ws_bytes, cudaStream_t stream);
+
+/* Dropout with a mask that is never stored: each element is dropped, independently
+ * of the others, where 16 random bits u (a whole number below 2^16) are below
+ * m = 65536 p, rounded to the nearest whole number (halves up), and multiplied by
+ * 1 / (1 - m / 65536) where it is kept (p rounded to m / 65536, so the mean is kept
+ * exactly; p = 1 drops all).  The bits are those of Philox4x32-10 (Salmon, Moraes,
+ * Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) with the key
+ * (low, high word of seed) and the counter (column / 8, row, low, high word of the
+ * offset): columns 8 b + 2 w and 8 b + 2 w + 1 have the low and high half of word w.
+ * The mask is a function of seed, offset, row and column: the gradient is the same
+ * call on the output's gradient.  offset: another one for each mask; *d_offset, where
+ * not NULL, is added to it, so that a captured graph's replays can have masks of
+ * their own.  d_x: [rows] of cols values (dtype), `stride` elements apart; d_out:
+ * contiguous, and may be d_x where that is contiguous.  rows < 2^32, cols < 2^24,
+ * 0 <= p <= 1. */
+zccl_status_t zccl_dropout(const void* d_x, int dtype, uint64_t stride, uint64_t rows, uint64_t cols, float p,
+                           uint64_t seed, uint64_t offset, const uint64_t* d_offset, void* d_out, cudaStream_t stream);
 
 /* Static text for a status code. */
 const char* zccl_status_string(zccl_status_t status);

@@ -12,7 +12,7 @@ fallback -- if ``libzccl.so`` is missing, every call raises.
 ``Codec`` is a convenience layer over the same calls that allocates buffers
 with PyTorch (device memory and streams only); ``Moe`` does the same for the
 calls around a mixture-of-experts all-to-all, ``BlockFp8`` for the experts'
-products.
+products, ``ResidualNorm`` and ``Dropout`` for what joins a block to the residual.
 """
 from __future__ import annotations
 
@@ -30,6 +30,8 @@ BF16, F32 = 0, 1
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 MAX_EXPERTS = 512
 MAX_TOP_K = 32
+MAX_SEQUENCES = 65536
+MAX_NORM_HIDDEN = 65536
 MAX_SEGMENTS = 4096
 MAX_SHARDS = 1024
 CHUNK = 4096
@@ -97,6 +99,14 @@ _SIGS = {
     "zccl_combine_backward": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p,
                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_void_p,
                                ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "zccl_balance_workspace_bytes": ([ctypes.c_uint32, ctypes.c_uint32, ctypes.POINTER(ctypes.c_uint64)], ctypes.c_int),
+    "zccl_balance": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_uint64,
+                      ctypes.c_void_p, ctypes.c_uint32, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p], ctypes.c_int),
+    "zccl_balance_backward": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_void_p,
+                               ctypes.c_uint64, ctypes.c_void_p, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p,
+                               ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_int,
+                               ctypes.c_void_p], ctypes.c_int),
     "zccl_fp8_weight_bytes": ([ctypes.c_uint32, ctypes.c_uint64, ctypes.c_uint64, ctypes.POINTER(ctypes.c_uint64)],
                               ctypes.c_int),
     "zccl_fp8_weight_quantize": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_uint64,
@@ -113,6 +123,22 @@ _SIGS = {
                                   ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_uint64,
                                   ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
                                   ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "zccl_residual_norm": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_int,
+                            ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                            ctypes.c_int, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64,
+                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "zccl_residual_norm_workspace_bytes": ([ctypes.c_uint64, ctypes.c_uint64, ctypes.POINTER(ctypes.c_uint64)],
+                                           ctypes.c_int),
+    "zccl_residual_norm_backward": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_uint64,
+                                     ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_int,
+                                     ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                     ctypes.c_int, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64,
+                                     ctypes.c_void_p], ctypes.c_int),
+    "zccl_dropout": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_float,
+                      ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p],
+                     ctypes.c_int),
     "zccl_status_string": ([ctypes.c_int], ctypes.c_char_p),
 }
 
@@ -136,6 +162,12 @@ class Route(ctypes.Structure):
     _fields_ = [("experts", ctypes.c_uint32), ("top_k", ctypes.c_uint32), ("groups", ctypes.c_uint32),
                 ("top_groups", ctypes.c_uint32), ("score", ctypes.c_int), ("renormalize", ctypes.c_int),
                 ("scale", ctypes.c_float)]
+
+
+class Norm(ctypes.Structure):
+    """zccl_norm_t"""
+    _fields_ = [("hidden", ctypes.c_uint64), ("post", ctypes.c_int), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("dropout", ctypes.c_float), ("seed", ctypes.c_uint64)]
 
 
 class ZcclError(RuntimeError):
@@ -324,6 +356,27 @@ def zccl_combine_backward(d_grad_out, d_y, rows, hidden, d_pos, d_weights, d_tot
                                        d_grad_y, d_grad_weights, stream)
 
 
+@functools.lru_cache(maxsize=1024)
+def zccl_balance_workspace_bytes(sequences: int, experts: int) -> int:
+    out = ctypes.c_uint64(0)
+    check(lib().zccl_balance_workspace_bytes(sequences, experts, ctypes.byref(out)), "zccl_balance_workspace_bytes")
+    return int(out.value)
+
+
+def zccl_balance(cfg, d_logits, dtype, stride, d_idx, tokens, d_seq, sequences, coefficient, d_loss, d_counts, d_tokens,
+                 d_ws, ws_bytes, stream) -> int:
+    """A routing's balance loss and each expert's slots, by sequences; cfg: a Route."""
+    return lib().zccl_balance(ctypes.addressof(cfg), d_logits, dtype, stride, d_idx, tokens, d_seq, sequences, coefficient,
+                              d_loss, d_counts, d_tokens, d_ws, ws_bytes, stream)
+
+
+def zccl_balance_backward(cfg, d_logits, dtype, stride, d_idx, tokens, d_seq, sequences, d_counts, d_tokens, coefficient,
+                          d_grad_loss, d_grad_logits, grad_stride, accumulate, stream) -> int:
+    return lib().zccl_balance_backward(ctypes.addressof(cfg), d_logits, dtype, stride, d_idx, tokens, d_seq, sequences,
+                                       d_counts, d_tokens, coefficient, d_grad_loss, d_grad_logits, grad_stride,
+                                       1 if accumulate else 0, stream)
+
+
 def zccl_fp8_weight_bytes(groups: int, n: int, k: int) -> int:
     out = ctypes.c_uint64(0)
     check(lib().zccl_fp8_weight_bytes(groups, n, k, ctypes.byref(out)), "zccl_fp8_weight_bytes")
@@ -359,6 +412,37 @@ def zccl_fp8_linear_backward(d_grad, d_x, dtype, grad_stride, x_stride, rows, k,
                                           d_offsets, d_grad_x, d_grad_w, out_dtype, d_ws, ws_bytes, d_status, stream)
 
 
+def zccl_residual_norm(cfg, d_x, x_dtype, x_stride, d_y, dtype, y_stride, d_weight, d_post_weight, weight_dtype, d_gate,
+                       gate_dtype, gate_stride, gate_span, rows, offset, d_offset, d_r, d_h, stream) -> int:
+    """r = x + scale gate drop(N(y)) and h = N(r), or h = N(x); cfg: a Norm."""
+    return lib().zccl_residual_norm(ctypes.addressof(cfg), d_x, x_dtype, x_stride, d_y, dtype, y_stride, d_weight,
+                                    d_post_weight, weight_dtype, d_gate, gate_dtype, gate_stride, gate_span, rows, offset,
+                                    d_offset, d_r, d_h, stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def zccl_residual_norm_workspace_bytes(hidden: int, rows: int) -> int:
+    out = ctypes.c_uint64(0)
+    check(lib().zccl_residual_norm_workspace_bytes(hidden, rows, ctypes.byref(out)), "zccl_residual_norm_workspace_bytes")
+    return int(out.value)
+
+
+def zccl_residual_norm_backward(cfg, d_grad_r, grad_r_stride, d_grad_h, grad_h_stride, d_r, x_dtype, r_stride, d_y, dtype,
+                                y_stride, d_weight, d_post_weight, weight_dtype, d_gate, gate_dtype, gate_stride,
+                                gate_span, rows, offset, d_offset, d_grad_x, d_grad_y, d_grad_weight,
+                                d_grad_post_weight, d_grad_gate, d_ws, ws_bytes, stream) -> int:
+    return lib().zccl_residual_norm_backward(ctypes.addressof(cfg), d_grad_r, grad_r_stride, d_grad_h, grad_h_stride, d_r,
+                                             x_dtype, r_stride, d_y, dtype, y_stride, d_weight, d_post_weight,
+                                             weight_dtype, d_gate, gate_dtype, gate_stride, gate_span, rows, offset,
+                                             d_offset, d_grad_x, d_grad_y, d_grad_weight, d_grad_post_weight,
+                                             d_grad_gate, d_ws, ws_bytes, stream)
+
+
+def zccl_dropout(d_x, dtype, stride, rows, cols, p, seed, offset, d_offset, d_out, stream_handle) -> int:
+    """x with elements dropped by a mask of seed, offset, row and column alone; its gradient likewise."""
+    return lib().zccl_dropout(d_x, dtype, stride, rows, cols, p, seed, offset, d_offset, d_out, stream_handle)
+
+
 def zccl_status_string(status: int) -> str:
     return lib().zccl_status_string(status).decode()
 
@@ -376,8 +460,10 @@ def check(status: int, what: str) -> None:
 
 
 from .codec import Codec  # noqa: E402  (torch-based convenience layer)
-from .moe import Dispatch, Moe  # noqa: E402
+from .moe import Balance, Dispatch, Moe  # noqa: E402
 from .fp8 import BlockFp8, Fp8Weight  # noqa: E402
+from .norm import Dropout, ResidualGrads, ResidualNorm  # noqa: E402
 
 __all__ = [n for n in list(globals()) if n.startswith("zccl_")] + [
-    "BlockFp8", "Codec", "Dispatch", "Fp8Weight", "Moe", "ZcclError", "check", "lib", "status_string"]
+    "Balance", "BlockFp8", "Codec", "Dispatch", "Dropout", "Fp8Weight", "Moe", "ResidualGrads", "ResidualNorm", "ZcclError",
+    "check", "lib", "status_string"]

@@ -1,9 +1,9 @@
-"""Moe: a thin convenience layer over the router, dispatch and combine calls.
+"""Moe: a thin convenience layer over the router, balance, dispatch and combine calls.
 
 It allocates outputs and the workspace with PyTorch and passes raw device
 addresses to libzccl, on the current CUDA stream; all work runs in the
 library's kernels.  The gradients are explicit calls: ``route_backward``,
-``combine_backward``, and, for a dispatch's tokens, ``combine`` without
+``balance_backward``, ``combine_backward``, and, for a dispatch's tokens, ``combine`` without
 weights.  Nothing is recorded for autograd: what a call returns does not require
 a gradient, whatever its inputs do.
 """
@@ -16,7 +16,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import (BF16, F32, OK, SCORE_SIGMOID, SCORE_SOFTMAX, Route, ZcclError, check, lib,
-               zccl_dispatch_stream_bytes, zccl_dispatch_workspace_bytes)
+               zccl_balance_workspace_bytes, zccl_dispatch_stream_bytes, zccl_dispatch_workspace_bytes)
 from .codec import SEGMENT_DTYPE
 
 _DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
@@ -31,6 +31,13 @@ class Dispatch(NamedTuple):
     offsets: torch.Tensor           # int32 [E + 1]: each expert's first row; last, how many rows there are
     table: Optional[torch.Tensor]   # the 2 E segments that Codec.compress_batched reads
     streams: Optional[torch.Tensor]  # where their streams go
+
+
+class Balance(NamedTuple):
+    """A routing's balance."""
+    loss: torch.Tensor    # float32 [1]
+    counts: torch.Tensor  # int32 [sequences, E]: each expert's slots
+    tokens: torch.Tensor  # int32 [sequences + 1]: tokens with a choice; last, the sequences that have one
 
 
 class Workspaces:
@@ -112,6 +119,7 @@ class Moe:
         self.device = torch.zeros(0, device=device if device is not None else "cuda").device
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._workspaces = Workspaces()
+        self._balances = Workspaces()
         # the workspace for any number of tokens
         self._ws_bytes = zccl_dispatch_workspace_bytes((1 << 31) // self.top_k - 1, self.experts, self.top_k)
 
@@ -169,6 +177,71 @@ class Moe:
                                            grad_weights.data_ptr(), tokens, grad.data_ptr(), self.experts,
                                            current_stream(self.device))
         check(st, "zccl_route_backward")
+        return grad
+
+    def _sequences(self, sequences):
+        """(address, how many) of the table of the sequences' first tokens."""
+        if sequences is None:
+            return None, 1
+        need(sequences, "sequences", self.device, (torch.int32,), 1)
+        if sequences.shape[0] < 2:
+            raise ValueError("sequences: expected each sequence's first token and, last, where they end")
+        return sequences.data_ptr(), sequences.shape[0] - 1
+
+    def balance(self, logits: torch.Tensor, idx: torch.Tensor, sequences: torch.Tensor | None = None,
+                coefficient: float = 1.0) -> Balance:
+        """How far the choice idx of logits [T, E] is from every expert getting as many
+        slots: a loss that is `coefficient` where the slots or the scores are shared
+        out evenly, and each expert's slots.  sequences: int32 [n + 1], each sequence's
+        first token and, last, where they end: the loss is then the mean of each one's
+        (default: all tokens as one).  Tokens without a choice do not count."""
+        tokens, stride, dtype = self._logits(logits)
+        self._slots(idx, "idx", torch.int32, tokens)
+        seq, n = self._sequences(sequences)
+        loss = torch.empty(1, dtype=torch.float32, device=self.device)
+        counts = torch.empty(n, self.experts, dtype=torch.int32, device=self.device)
+        live = torch.empty(n + 1, dtype=torch.int32, device=self.device)
+        stream = current_stream(self.device)
+        nbytes = zccl_balance_workspace_bytes(n, self.experts)
+        with self._balances.lock:
+            ws = self._balances.get(nbytes, stream, self.device)
+            st = self._lib.zccl_balance(self._config, logits.data_ptr(), dtype, stride, idx.data_ptr(), tokens, seq, n,
+                                        coefficient, loss.data_ptr(), counts.data_ptr(), live.data_ptr(), ws.data_ptr(),
+                                        ws.numel(), stream)
+        check(st, "zccl_balance")
+        return Balance(loss, counts, live)
+
+    def balance_backward(self, logits: torch.Tensor, idx: torch.Tensor, balance: Balance,
+                         sequences: torch.Tensor | None = None, coefficient: float = 1.0,
+                         grad_loss: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+        """The gradient of balance's loss with respect to the logits, in their type,
+        times grad_loss (float32, one value on the device; default 1).  out: a gradient
+        of the same logits (route_backward's) to which it is added in place."""
+        tokens, stride, dtype = self._logits(logits)
+        self._slots(idx, "idx", torch.int32, tokens)
+        seq, n = self._sequences(sequences)
+        need(balance.counts, "balance.counts", self.device, (torch.int32,), 2)
+        need(balance.tokens, "balance.tokens", self.device, (torch.int32,), 1)
+        if tuple(balance.counts.shape) != (n, self.experts) or balance.tokens.shape[0] != n + 1:
+            raise ValueError(f"balance: expected that of {n} sequences")
+        if grad_loss is not None and (grad_loss.device != self.device or grad_loss.dtype != torch.float32 or
+                                      grad_loss.numel() != 1):
+            raise ValueError(f"grad_loss: expected a float32 tensor of one value on {self.device}")
+        grad = out
+        if out is None:
+            grad = torch.empty(tokens, self.experts, dtype=logits.dtype, device=self.device)
+        else:
+            need(out, "out", self.device, (logits.dtype,), 2, rows_strided=True)
+            if out.shape != logits.shape:
+                raise ValueError(f"out: expected shape {tuple(logits.shape)}")
+            if tokens > 1 and out.stride(0) < self.experts:
+                raise ValueError("out: its rows overlap")
+        st = self._lib.zccl_balance_backward(self._config, logits.data_ptr(), dtype, stride, idx.data_ptr(), tokens, seq,
+                                             n, balance.counts.data_ptr(), balance.tokens.data_ptr(), coefficient,
+                                             None if grad_loss is None else grad_loss.data_ptr(), grad.data_ptr(),
+                                             grad.stride(0) if tokens > 1 else self.experts, 0 if out is None else 1,
+                                             current_stream(self.device))
+        check(st, "zccl_balance_backward")
         return grad
 
     def dispatch(self, x: torch.Tensor, idx: torch.Tensor, capacity: int | None = None) -> Dispatch:
