@@ -66,14 +66,97 @@ __global__ void norm_long_kernel(NormArgs a)
     }
 }
 
-template <typename Tx, typename Ty>
-cudaError_t launch_norm_as(const NormArgs& a, bool vec, int sms, cudaStream_t stream)
+// A team a worker: a row is read once and stays in registers, with the next one on its
+// way; weights and the gate stay there too.
+template <typename Tx, typename Ty, bool kVec, int kTeam>
+__global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeamWarps * 32) norm_kernel(NormArgs a)
 {
-    const uint32_t tiles = (a.hidden + kTile - 1) / kTile, threads = 32 * (tiles < 16 ? tiles : 16);
-    const uint64_t most = (uint64_t)sms * 64;
-    return launch_dependent(vec ? norm_long_kernel<Tx, Ty, true> : norm_long_kernel<Tx, Ty, false>,
-                            (uint32_t)(a.rows < most ? a.rows : most), threads, 0, stream, a);
+    __shared__ float red[kTeam == kWarpTeam ? 1 : kTeamRed];
+    uint32_t turn = 0;
+    const uint32_t warp = threadIdx.x >> 5;
+    uint32_t worker = blockIdx.x, tile = warp * kTile;
+    if (kTeam == kWarpTeam) worker = blockIdx.x * kWarpsPerCta + warp, tile = 0;
+    if (kTeam == kClusterTeam) {
+        uint32_t ctas;
+        asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+        worker = blockIdx.x / ctas;
+        tile = (cluster_rank() * (blockDim.x / 32) + warp) * kTile;
+    }
+    pdl_wait();
+    if (kTeam == kClusterTeam) cluster_sync();  // the others' shared memory is there
+    if (kTeam == kWarpTeam && worker >= a.workers) return;
+    const uint64_t offset = drop_offset(a.drop);
+    const uint64_t lo = first_row(a.rows, a.workers, worker), hi = first_row(a.rows, a.workers, worker + 1);
+    const bool join = a.y != nullptr;
+    Piece<Tx, kVec> px;
+    Piece<Ty, kVec> py;
+    const auto load = [&](uint64_t t) {
+        px.load(static_cast<const Tx*>(a.x) + t * a.x_stride, tile, a.hidden);
+        if (join) py.load(static_cast<const Ty*>(a.y) + t * a.y_stride, tile, a.hidden);
+    };
+    py.zero();
+    load(lo);
+    float w[8], k[8];
+    load_vector<kVec>(w, a.weight, 0, tile, a.hidden);
+    uint64_t gate_end = lo;  // where the gate changes
+    for (uint64_t t = lo; t < hi; ++t) {
+        float x[8], y[8];
+        px.get(x), py.get(y);
+        if (t + 1 < hi) load(t + 1);
+        float s[1] = {0.0f};
+        if (join) {
+            if (t == gate_end) {
+                // the join's factor of each column, with the weight of the norm after the block
+                const uint64_t row = t / a.gate_span;
+                float p[8];
+                load_vector<kVec>(k, a.gate, a.gate.p != nullptr ? row * a.gate_stride : 0, tile, a.hidden);
+                load_vector<kVec>(p, a.post_weight, 0, tile, a.hidden);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) k[j] = k[j] * a.factor * p[j];
+                gate_end = a.gate.p != nullptr ? (row + 1) * a.gate_span : a.rows;
+            }
+            const uint32_t kept = a.drop.below > 0 ? kept_piece<kVec>(a.drop, offset, (uint32_t)t, tile) : 0xFFu;
+            float eta = 1.0f;
+            if (a.post) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[0] = fmaf(y[j], y[j], s[0]);
+                team_sum<1, kTeam>(s, red, turn);
+                eta = rsqrtf(s[0] * a.inv_hidden + a.eps);
+                s[0] = 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = (kept >> j) & 1u ? fmaf(k[j], y[j] * eta, x[j]) : x[j];
+            store8<Tx, kVec>(static_cast<Tx*>(a.r) + t * a.hidden, x, tile, a.hidden);
+        }
+        if (a.h == nullptr) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[0] = fmaf(x[j], x[j], s[0]);
+        team_sum<1, kTeam>(s, red, turn);
+        const float rho = rsqrtf(s[0] * a.inv_hidden + a.eps);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = x[j] * rho * w[j];
+        store8<Ty, kVec>(static_cast<Ty*>(a.h) + t * a.hidden, x, tile, a.hidden);
+    }
 }
+
+using NormKernel = void (*)(NormArgs);
+
+template <typename Tx, typename Ty, bool kVec>
+NormKernel norm_for(Team team)
+{
+    return team == kWarpTeam  ? norm_kernel<Tx, Ty, kVec, kWarpTeam>
+           : team == kCtaTeam ? norm_kernel<Tx, Ty, kVec, kCtaTeam>
+           : team == kLong    ? norm_long_kernel<Tx, Ty, kVec>
+                              : norm_kernel<Tx, Ty, kVec, kClusterTeam>;
+}
+template <typename Tx>
+NormKernel norm_for(int dtype, bool vec, Team team)
+{
+    if (dtype == ZCCL_BF16) return vec ? norm_for<Tx, __nv_bfloat16, true>(team) : norm_for<Tx, __nv_bfloat16, false>(team);
+    return vec ? norm_for<Tx, float, true>(team) : norm_for<Tx, float, false>(team);
+}
+
+constexpr uint32_t kSmWarps = 16;
 
 bool dtype_ok(int dtype) { return dtype == ZCCL_BF16 || dtype == ZCCL_F32; }
 uint64_t size_of(int dtype) { return dtype == ZCCL_BF16 ? 2 : 4; }
@@ -112,15 +195,14 @@ bool on_16(const void* p, int dtype, uint64_t stride, uint64_t rows)
 
 }  // namespace
 
-zccl_status_t launch_norm(const NormArgs& a, int x_dtype, int dtype, bool vec, cudaStream_t stream)
+zccl_status_t launch_norm(NormArgs& a, int x_dtype, int dtype, bool vec, cudaStream_t stream)
 {
-    const int sms = sm_count();
-    if (sms == 0) return ZCCL_ERR_CUDA;
-    if (x_dtype == ZCCL_BF16)
-        return launched(dtype == ZCCL_BF16 ? launch_norm_as<__nv_bfloat16, __nv_bfloat16>(a, vec, sms, stream)
-                                           : launch_norm_as<__nv_bfloat16, float>(a, vec, sms, stream));
-    return launched(dtype == ZCCL_BF16 ? launch_norm_as<float, __nv_bfloat16>(a, vec, sms, stream)
-                                       : launch_norm_as<float, float>(a, vec, sms, stream));
+    const Shape s = norm_shape(a.hidden, a.rows, kSmWarps);
+    a.workers = s.workers;
+    const NormKernel kernel =
+        x_dtype == ZCCL_BF16 ? norm_for<__nv_bfloat16>(dtype, vec, s.team) : norm_for<float>(dtype, vec, s.team);
+    return launched(s.team == kClusterTeam ? launch_clusters(kernel, s.grid, s.warps * 32, 0, s.ctas, stream, a)
+                                           : launch_dependent(kernel, s.grid, s.warps * 32, 0, stream, a));
 }
 
 }  // namespace zccl
@@ -161,7 +243,7 @@ zccl_status_t zccl_residual_norm(const zccl_norm_t* cfg, const void* d_x, int x_
 zccl_status_t zccl_residual_norm_workspace_bytes(uint64_t hidden, uint64_t rows, uint64_t* bytes)
 {
     if (bytes == nullptr || hidden == 0 || hidden > ZCCL_MAX_NORM_HIDDEN || rows >= (1ull << 31)) return ZCCL_ERR_INVALID_ARG;
-    *bytes = (uint64_t)norm_workers(hidden, rows) * kSlots * ((hidden + 7) / 8 * 8) * sizeof(float);
+    *bytes = norm_backward_bytes(hidden, rows);
     return ZCCL_OK;
 }
 
@@ -218,7 +300,6 @@ zccl_status_t zccl_residual_norm_backward(const zccl_norm_t* cfg, const void* d_
     a.grad_post_weight = d_grad_post_weight;
     a.grad_gate = d_grad_gate;
     a.sums = static_cast<float*>(d_ws);
-    a.workers = norm_workers(a.hidden, rows);
     const bool vec = a.hidden % 8 == 0 && on_16(a.x, x_dtype, r_stride, rows) && on_16(a.y, dtype, y_stride, rows) &&
                      on_16(d_grad_r, x_dtype, grad_r_stride, rows) && on_16(d_grad_h, dtype, grad_h_stride, rows) &&
                      on_16(d_grad_x, x_dtype, 0, 1) && on_16(d_grad_y, dtype, 0, 1) && on_16(d_weight, weight_dtype, 0, 1) &&

@@ -6,8 +6,6 @@
 
 namespace zccl {
 
-constexpr uint64_t kMaxNormHidden = 65536;
-
 struct NormArgs {
     const void* x;       // forward: the residual; backward: the stored r (with grad_h)
     const void* y;       // nullptr: no join (forward), not read (backward)
@@ -31,15 +29,18 @@ struct NormArgs {
     void* grad_weight;
     void* grad_post_weight;
     void* grad_gate;
-    float* sums;         // workspace: [workers][kSlots][hidden]
-    uint32_t workers;
+    float* sums;         // workspace: weights' sums of each group (a CTA's or a cluster's teams), then gates' parts
+    float* parts;
+    uint32_t groups, workers;
 };
 
-// A backward pass's rows are shared out over workers, each a run of neighbouring
-// rows.  A worker keeps its sums of the weights' gradients over its rows, and of
-// the gate's over the rows of a gate row.  Gate rows that lie within a worker's
-// rows it finishes itself; of the first and the last one it has only a part, maybe.
-enum { kSlotWeight = 0, kSlotPost = 1, kSlotGateFirst = 2, kSlotGateLast = 3, kSlots = 4 };
+// Rows are shared out over workers, each a run of neighbouring rows.  In a backward
+// pass a worker keeps its sums of the weights' gradients over its rows, and of the
+// gate's over the rows of a gate row.  A gate row that lies within a worker's rows it
+// finishes itself; of one that began before its rows, or goes on behind them, it has a
+// part.
+enum { kSlotWeight = 0, kSlotPost = 1, kWeightSlots = 2 };  // sums of the weights: [groups][2][pitch]
+enum { kSlotBefore = 0, kSlotBehind = 1, kGateSlots = 2 };  // parts of gate rows: [workers][2][pitch]
 
 // The first row of worker w.
 __host__ __device__ inline uint64_t first_row(uint64_t rows, uint32_t workers, uint32_t w)
@@ -54,15 +55,121 @@ __host__ __device__ inline uint32_t worker_of(uint64_t rows, uint32_t workers, u
     return (uint32_t)(row < large ? row / (base + 1) : more + (row - large) / base);
 }
 
-// The most workers that a workspace has room for: two to four a SM, fewer for rows so
-// long that their sums would take more than 100 MB.
-constexpr uint32_t kMaxWorkers = 608;
-inline uint32_t norm_workers(uint64_t hidden, uint64_t rows)
+// How a row is held: by a warp (a tile at most), by the warps of a CTA, by those of a
+// cluster's CTAs, or (kLong) read several times by a CTA.
+enum Team { kWarpTeam = 0, kCtaTeam = 1, kClusterTeam = 2, kLong = 3 };
+constexpr uint32_t kTeamWarps = 16;    // the most of a CTA: 4096 columns
+constexpr uint32_t kMaxCluster = 4;    // CTAs: 16384 columns
+constexpr uint32_t kWarpsPerCta = 8;   // of warps that are teams
+
+struct Shape {
+    Team team;
+    uint32_t warps;    // of a CTA
+    uint32_t ctas;     // of a row
+    uint32_t workers;  // teams
+    uint32_t grid;     // CTAs
+};
+
+// `sm_warps`: how many warps an SM is to hold; the SMs are taken as 152.
+inline Shape norm_shape(uint64_t hidden, uint64_t rows, uint32_t sm_warps)
 {
-    uint64_t n = kMaxWorkers * 8192ull / hidden;
-    n = n < kMaxWorkers ? n : kMaxWorkers;
-    n = n < rows ? n : rows;
-    return (uint32_t)(n > 0 ? n : 1);
+    constexpr uint32_t kSms = 152;
+    const uint32_t tiles = (uint32_t)((hidden + kTile - 1) / kTile);
+    Shape s{};
+    const auto at_most_rows = [&](uint64_t n) { return (uint32_t)(n < rows ? n : rows > 0 ? rows : 1); };
+    if (tiles <= 1) {
+        s = {kWarpTeam, kWarpsPerCta, 1, at_most_rows(kSms * sm_warps), 0};
+        s.grid = (s.workers + kWarpsPerCta - 1) / kWarpsPerCta;
+    } else if (tiles <= kTeamWarps * kMaxCluster) {
+        s.ctas = (tiles + kTeamWarps - 1) / kTeamWarps;
+        s.team = s.ctas > 1 ? kClusterTeam : kCtaTeam;
+        s.warps = (tiles + s.ctas - 1) / s.ctas;
+        const uint32_t per_sm = sm_warps / s.warps;
+        s.workers = at_most_rows((uint64_t)kSms * (per_sm > 0 ? per_sm : 1) / s.ctas);
+        s.grid = s.workers * s.ctas;
+    } else {
+        // its sums stay in the workspace: fewer workers for longer rows
+        s = {kLong, kTeamWarps, 1, at_most_rows(kSms * 16384 / hidden * 2), 0};
+        s.grid = s.workers;
+    }
+    return s;
+}
+
+// Sums N values (N <= 8) over a warp: a lane keeps half of the values in each of three
+// steps, so nine exchanges do for all eight.  Lane 4 i holds value i then.
+template <int N>
+__device__ __forceinline__ float warp_sums(const float (&s)[N])
+{
+    const uint32_t lane = threadIdx.x & 31;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < N ? s[i] : 0.0f;
+#pragma unroll
+    for (int h = 4, o = 16; h > 0; h /= 2, o /= 2) {
+        const bool upper = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const float keep = upper ? v[i + h] : v[i], give = upper ? v[i] : v[i + h];
+            v[i] = i < N || i + h < N ? keep + __shfl_xor_sync(0xFFFFFFFFu, give, o) : 0.0f;
+        }
+    }
+    v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 2);
+    return v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 1);
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Stores to the same place of CTA `rank` of the cluster.
+__device__ __forceinline__ void st_cluster(float* p, uint32_t rank, float v)
+{
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+
+// Room for the sums of a team's warps, whose halves take turns by `turn`: a warp may
+// write its sums of the next row while another still reads those of this one, and those
+// of the row after it only when all have been at the barrier between.
+constexpr uint32_t kTeamRed = 2 * kTeamWarps * kMaxCluster * 8;
+
+// Sums N values (N <= 8) over a team, the same way in every thread.
+template <int N, int kTeam>
+__device__ __forceinline__ void team_sum(float (&s)[N], float* red, uint32_t& turn)
+{
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    float v = warp_sums<N>(s);
+    uint32_t each = 4;  // lanes from one value to the next
+    if (kTeam != kWarpTeam) {
+        float* at = red + turn * (kTeamRed / 2);
+        turn ^= 1;
+        uint32_t all = warps;
+        if (kTeam == kClusterTeam) {
+            uint32_t ctas;
+            asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+            // the four lanes that hold a value take a CTA each
+            if ((lane & 3) < ctas && lane / 4 < N) st_cluster(at + (cluster_rank() * warps + warp) * 8 + lane / 4, lane & 3, v);
+            cluster_sync();
+            all = warps * ctas;
+        } else {
+            if ((lane & 3) == 0) at[warp * 8 + lane / 4] = v;
+            __syncthreads();
+        }
+        v = 0.0f;
+        for (uint32_t w = lane / 8; w < all; w += 4) v += (lane & 7) < N ? at[w * 8 + (lane & 7)] : 0.0f;
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+        each = 1;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = __shfl_sync(0xFFFFFFFFu, v, i * each);
 }
 
 // Sums N values over a CTA of `warps` warps, the same way in every thread; `red` holds
@@ -102,8 +209,29 @@ __device__ __forceinline__ uint32_t join_factors(float (&k)[8], const NormArgs& 
     return a.drop.below > 0 ? kept_piece<kVec>(a.drop, offset, (uint32_t)row, tile) : 0xFFu;
 }
 
-zccl_status_t launch_norm(const NormArgs& a, int x_dtype, int dtype, bool vec, cudaStream_t stream);
-zccl_status_t launch_norm_backward(const NormArgs& a, int x_dtype, int dtype, int weight_dtype, bool vec,
-                                   cudaStream_t stream);
+zccl_status_t launch_norm(NormArgs& a, int x_dtype, int dtype, bool vec, cudaStream_t stream);
+zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weight_dtype, bool vec, cudaStream_t stream);
+uint64_t norm_backward_bytes(uint64_t hidden, uint64_t rows);
+
+// Launches `kernel` as launch_dependent does, in clusters of `ctas`.
+inline cudaError_t launch_clusters(void (*kernel)(NormArgs), uint32_t grid, uint32_t threads, size_t smem, uint32_t ctas,
+                                   cudaStream_t stream, const NormArgs& a)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
 
 }  // namespace zccl

@@ -32,6 +32,11 @@ __device__ __forceinline__ void widen(float (&v)[8], const uint4& q)
 template <typename T, bool kVec>
 struct Piece {
     float v[8];
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    }
     __device__ __forceinline__ void load(const T* row, uint32_t tile, uint32_t cols)
     {
         if (kVec) {
@@ -61,6 +66,7 @@ struct Piece {
 template <>
 struct Piece<__nv_bfloat16, true> {
     uint4 q;
+    __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const __nv_bfloat16* row, uint32_t tile, uint32_t cols)
     {
         const uint32_t c = column<true>(tile, 0);
