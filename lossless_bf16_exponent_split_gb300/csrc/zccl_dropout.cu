@@ -8,40 +8,54 @@ namespace zccl {
 namespace {
 
 constexpr int kDropWarps = 8;
+constexpr int kDropCtas = 3;  // of an SM
 
 struct DropoutArgs {
     const void* x;
     uint64_t stride;
     uint64_t rows;
     uint32_t cols, tiles;  // tiles of a row
+    uint32_t step;         // rows that the warps take at a time
     DropArgs drop;
     void* out;
 };
 
+// A warp keeps its place in the rows and goes from row to row, kRows of them on their
+// way at a time.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kDropWarps * 32) dropout_kernel(DropoutArgs a)
+__global__ void __launch_bounds__(kDropWarps * 32, kDropCtas) dropout_kernel(DropoutArgs a)
 {
+    constexpr int kRows = sizeof(T) == 2 ? 4 : 2;
     pdl_wait();
     const uint64_t offset = drop_offset(a.drop);
-    const uint64_t total = a.rows * a.tiles, step = (uint64_t)gridDim.x * kDropWarps;
-    for (uint64_t i = (uint64_t)blockIdx.x * kDropWarps + (threadIdx.x >> 5); i < total; i += step) {
-        const uint64_t row = i / a.tiles;
-        const uint32_t tile = (uint32_t)(i - row * a.tiles) * kTile;
-        float v[8];
-        load8<T, kVec>(v, static_cast<const T*>(a.x) + row * a.stride, tile, a.cols);
-        const uint32_t kept = kept_piece<kVec>(a.drop, offset, (uint32_t)row, tile);
+    const uint32_t warp = blockIdx.x * kDropWarps + (threadIdx.x >> 5);
+    const uint32_t tile = warp % a.tiles * kTile;
+    const uint64_t first = warp / a.tiles;
+    if (first >= a.step) return;
+    for (uint64_t row = first; row < a.rows; row += kRows * a.step) {
+        Piece<T, kVec> p[kRows];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (kept >> j) & 1u ? v[j] * a.drop.gain : 0.0f;
-        store8<T, kVec>(static_cast<T*>(a.out) + row * a.cols, v, tile, a.cols);
+        for (int n = 0; n < kRows; ++n)
+            if (row + n * a.step < a.rows) p[n].load(static_cast<const T*>(a.x) + (row + n * a.step) * a.stride, tile, a.cols);
+#pragma unroll
+        for (int n = 0; n < kRows; ++n) {
+            const uint64_t at = row + n * a.step;
+            if (at >= a.rows) break;
+            const Kept<kVec> kept = kept_piece<kVec>(a.drop, offset, (uint32_t)at, tile);
+            store8<T, kVec>(static_cast<T*>(a.out) + at * a.cols, where_kept<kVec>(kept, mul(p[n].get(), a.drop.gain)), tile, a.cols);
+        }
     }
 }
 
 template <typename T>
-cudaError_t launch_dropout(const DropoutArgs& a, int sms, cudaStream_t stream)
+cudaError_t launch_dropout(DropoutArgs& a, int sms, cudaStream_t stream)
 {
-    const uint64_t warps = a.rows * a.tiles, ctas = (warps + kDropWarps - 1) / kDropWarps, most = (uint64_t)sms * 64;
+    // as many rows at a time as the machine holds: tiles < 2^16, so the CTAs for one row are fewer than 2^13
+    const uint64_t most = (uint64_t)sms * kDropCtas * kDropWarps / a.tiles;
+    a.step = (uint32_t)(a.rows < most ? a.rows : most > 0 ? most : 1);
+    const uint64_t ctas = ((uint64_t)a.step * a.tiles + kDropWarps - 1) / kDropWarps;
     const bool vec = a.cols % 8 == 0 && a.stride * sizeof(T) % 16 == 0 && is_aligned(a.x, 16) && is_aligned(a.out, 16);
-    return launch_dependent(vec ? dropout_kernel<T, true> : dropout_kernel<T, false>, (uint32_t)(ctas < most ? ctas : most),
+    return launch_dependent(vec ? dropout_kernel<T, true> : dropout_kernel<T, false>, (uint32_t)ctas,
                             kDropWarps * 32, 0, stream, a);
 }
 

@@ -10,7 +10,7 @@ namespace {
 
 // A CTA a row, read once for each of its sums: any size.
 template <typename Tx, typename Ty, bool kVec>
-__global__ void norm_long_kernel(NormArgs a)
+__global__ void __launch_bounds__(kTeamWarps * 32) norm_long_kernel(NormArgs a)
 {
     __shared__ float red[2 * 32];
     uint32_t turn = 0;
@@ -21,142 +21,127 @@ __global__ void norm_long_kernel(NormArgs a)
         const Tx* x = static_cast<const Tx*>(a.x) + t * a.x_stride;
         const Ty* y = static_cast<const Ty*>(a.y) + t * a.y_stride;
         Tx* r = static_cast<Tx*>(a.r) + t * a.hidden;
-        float eta[1] = {0.0f}, rho[1] = {0.0f};
+        float eta = 1.0f;
+        float2 sum = twice(0.0f);
         if (a.y != nullptr && a.post) {
             for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
-                float v[8];
-                load8<Ty, kVec>(v, y, tile, a.hidden);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) eta[0] = fmaf(v[j], v[j], eta[0]);
+                const Eight v = load8<Ty, kVec>(y, tile, a.hidden);
+                dot(sum, v, v);
             }
-            cta_sum<1>(eta, red, turn);
-            eta[0] = rsqrtf(eta[0] * a.inv_hidden + a.eps);
+            float s[1] = {sum.x + sum.y};
+            cta_sum<1>(s, red, turn);
+            eta = rsqrtf(s[0] * a.inv_hidden + a.eps);
+            sum = twice(0.0f);
         }
         for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
-            float v[8];
-            load8<Tx, kVec>(v, x, tile, a.hidden);
+            Eight v = load8<Tx, kVec>(x, tile, a.hidden);
             if (a.y != nullptr) {
-                float b[8], k[8];
-                load8<Ty, kVec>(b, y, tile, a.hidden);
-                const uint32_t kept = join_factors<kVec>(k, a, offset, t, tile);
-                if (a.post) {
-                    float w[8];
-                    load_vector<kVec>(w, a.post_weight, 0, tile, a.hidden);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) b[j] = b[j] * eta[0] * w[j];
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = (kept >> j) & 1u ? fmaf(k[j], b[j], v[j]) : v[j];
-                store8<Tx, kVec>(r, v, tile, a.hidden);
+                const Eight k = mul(join_factors<kVec>(a, t, tile), load_vector<kVec>(a.post_weight, 0, tile, a.hidden));
+                const Eight b = mul(load8<Ty, kVec>(y, tile, a.hidden), eta);
+                v = where_kept<kVec>(join_kept<kVec>(a, offset, t, tile), fma(k, b, v), v);
+                v = store8<Tx, kVec>(r, v, tile, a.hidden);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) rho[0] = fmaf(v[j], v[j], rho[0]);
+            dot(sum, v, v);
         }
         if (a.h == nullptr) continue;
-        cta_sum<1>(rho, red, turn);
-        rho[0] = rsqrtf(rho[0] * a.inv_hidden + a.eps);
+        float s[1] = {sum.x + sum.y};
+        cta_sum<1>(s, red, turn);
+        const float rho = rsqrtf(s[0] * a.inv_hidden + a.eps);
         for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
-            float v[8], w[8];
-            load8<Tx, kVec>(v, a.y != nullptr ? r : x, tile, a.hidden);
-            load_vector<kVec>(w, a.weight, 0, tile, a.hidden);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = v[j] * rho[0] * w[j];
-            store8<Ty, kVec>(static_cast<Ty*>(a.h) + t * a.hidden, v, tile, a.hidden);
+            const Eight v = mul(load8<Tx, kVec>(a.y != nullptr ? r : x, tile, a.hidden), rho);
+            store8<Ty, kVec>(static_cast<Ty*>(a.h) + t * a.hidden, mul(v, load_vector<kVec>(a.weight, 0, tile, a.hidden)), tile,
+                             a.hidden);
         }
     }
 }
 
 // A team a worker: a row is read once and stays in registers, with the next one on its
 // way; weights and the gate stay there too.
-template <typename Tx, typename Ty, bool kVec, int kTeam>
-__global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeamWarps * 32) norm_kernel(NormArgs a)
+template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces>
+__global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeamWarps * 32, kTeam == kWarpTeam ? 2 : 1)
+    norm_kernel(NormArgs a)
 {
     __shared__ float red[kTeam == kWarpTeam ? 1 : kTeamRed];
     uint32_t turn = 0;
-    const uint32_t warp = threadIdx.x >> 5;
-    uint32_t worker = blockIdx.x, tile = warp * kTile;
-    if (kTeam == kWarpTeam) worker = blockIdx.x * kWarpsPerCta + warp, tile = 0;
-    if (kTeam == kClusterTeam) {
-        uint32_t ctas;
-        asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
-        worker = blockIdx.x / ctas;
-        tile = (cluster_rank() * (blockDim.x / 32) + warp) * kTile;
-    }
     pdl_wait();
-    if (kTeam == kClusterTeam) cluster_sync();  // the others' shared memory is there
-    if (kTeam == kWarpTeam && worker >= a.workers) return;
+    const Place at = place<kTeam>();
+    if (kTeam == kWarpTeam && at.worker >= a.workers) return;
     const uint64_t offset = drop_offset(a.drop);
-    const uint64_t lo = first_row(a.rows, a.workers, worker), hi = first_row(a.rows, a.workers, worker + 1);
+    const uint64_t lo = first_row(a.rows, a.workers, at.worker), hi = first_row(a.rows, a.workers, at.worker + 1);
     const bool join = a.y != nullptr;
-    Piece<Tx, kVec> px;
-    Piece<Ty, kVec> py;
+    Piece<Tx, kVec> px[kPieces];
+    Piece<Ty, kVec> py[kPieces] = {};
     const auto load = [&](uint64_t t) {
-        px.load(static_cast<const Tx*>(a.x) + t * a.x_stride, tile, a.hidden);
-        if (join) py.load(static_cast<const Ty*>(a.y) + t * a.y_stride, tile, a.hidden);
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+            px[n].load(static_cast<const Tx*>(a.x) + t * a.x_stride, at.tile(n), a.hidden);
+            if (join) py[n].load(static_cast<const Ty*>(a.y) + t * a.y_stride, at.tile(n), a.hidden);
+        }
     };
-    py.zero();
     load(lo);
-    float w[8], k[8];
-    load_vector<kVec>(w, a.weight, 0, tile, a.hidden);
+    Eight w[kPieces], k[kPieces];
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) w[n] = load_vector<kVec>(a.weight, 0, at.tile(n), a.hidden);
     uint64_t gate_end = lo;  // where the gate changes
     for (uint64_t t = lo; t < hi; ++t) {
-        float x[8], y[8];
-        px.get(x), py.get(y);
+        Eight x[kPieces], y[kPieces];
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) x[n] = px[n].get(), y[n] = py[n].get();
         if (t + 1 < hi) load(t + 1);
-        float s[1] = {0.0f};
         if (join) {
             if (t == gate_end) {
                 // the join's factor of each column, with the weight of the norm after the block
-                const uint64_t row = t / a.gate_span;
-                float p[8];
-                load_vector<kVec>(k, a.gate, a.gate.p != nullptr ? row * a.gate_stride : 0, tile, a.hidden);
-                load_vector<kVec>(p, a.post_weight, 0, tile, a.hidden);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) k[j] = k[j] * a.factor * p[j];
-                gate_end = a.gate.p != nullptr ? (row + 1) * a.gate_span : a.rows;
+                for (int n = 0; n < kPieces; ++n)
+                    k[n] = mul(join_factors<kVec>(a, t, at.tile(n)), load_vector<kVec>(a.post_weight, 0, at.tile(n), a.hidden));
+                gate_end = a.gate.p != nullptr ? (t / a.gate_span + 1) * a.gate_span : a.rows;
             }
-            const uint32_t kept = a.drop.below > 0 ? kept_piece<kVec>(a.drop, offset, (uint32_t)t, tile) : 0xFFu;
-            float eta = 1.0f;
             if (a.post) {
+                float2 sum = twice(0.0f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[0] = fmaf(y[j], y[j], s[0]);
+                for (int n = 0; n < kPieces; ++n) dot(sum, y[n], y[n]);
+                float s[1] = {sum.x + sum.y};
                 team_sum<1, kTeam>(s, red, turn);
-                eta = rsqrtf(s[0] * a.inv_hidden + a.eps);
-                s[0] = 0.0f;
+                const float eta = rsqrtf(s[0] * a.inv_hidden + a.eps);
+#pragma unroll
+                for (int n = 0; n < kPieces; ++n) y[n] = mul(y[n], eta);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = (kept >> j) & 1u ? fmaf(k[j], y[j] * eta, x[j]) : x[j];
-            store8<Tx, kVec>(static_cast<Tx*>(a.r) + t * a.hidden, x, tile, a.hidden);
+            for (int n = 0; n < kPieces; ++n) {
+                x[n] = where_kept<kVec>(join_kept<kVec>(a, offset, t, at.tile(n)), fma(k[n], y[n], x[n]), x[n]);
+                x[n] = store8<Tx, kVec>(static_cast<Tx*>(a.r) + t * a.hidden, x[n], at.tile(n), a.hidden);
+            }
         }
         if (a.h == nullptr) continue;
+        float2 sum = twice(0.0f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] = fmaf(x[j], x[j], s[0]);
+        for (int n = 0; n < kPieces; ++n) dot(sum, x[n], x[n]);
+        float s[1] = {sum.x + sum.y};
         team_sum<1, kTeam>(s, red, turn);
         const float rho = rsqrtf(s[0] * a.inv_hidden + a.eps);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = x[j] * rho * w[j];
-        store8<Ty, kVec>(static_cast<Ty*>(a.h) + t * a.hidden, x, tile, a.hidden);
+        for (int n = 0; n < kPieces; ++n)
+            store8<Ty, kVec>(static_cast<Ty*>(a.h) + t * a.hidden, mul(mul(x[n], rho), w[n]), at.tile(n), a.hidden);
     }
 }
 
 using NormKernel = void (*)(NormArgs);
 
 template <typename Tx, typename Ty, bool kVec>
-NormKernel norm_for(Team team)
+NormKernel norm_for(const Shape& s)
 {
-    return team == kWarpTeam  ? norm_kernel<Tx, Ty, kVec, kWarpTeam>
-           : team == kCtaTeam ? norm_kernel<Tx, Ty, kVec, kCtaTeam>
-           : team == kLong    ? norm_long_kernel<Tx, Ty, kVec>
-                              : norm_kernel<Tx, Ty, kVec, kClusterTeam>;
+    constexpr int kMost = kVec && sizeof(Tx) == 2 && sizeof(Ty) == 2 ? 2 : 1;
+    if (s.team == kWarpTeam) return norm_kernel<Tx, Ty, kVec, kWarpTeam, 1>;
+    if (s.team == kLong) return norm_long_kernel<Tx, Ty, kVec>;
+    if (s.pieces == 1) return s.team == kCtaTeam ? norm_kernel<Tx, Ty, kVec, kCtaTeam, 1> : norm_kernel<Tx, Ty, kVec, kClusterTeam, 1>;
+    return s.team == kCtaTeam ? norm_kernel<Tx, Ty, kVec, kCtaTeam, kMost> : norm_kernel<Tx, Ty, kVec, kClusterTeam, kMost>;
 }
 template <typename Tx>
-NormKernel norm_for(int dtype, bool vec, Team team)
+NormKernel norm_for(int dtype, bool vec, const Shape& s)
 {
-    if (dtype == ZCCL_BF16) return vec ? norm_for<Tx, __nv_bfloat16, true>(team) : norm_for<Tx, __nv_bfloat16, false>(team);
-    return vec ? norm_for<Tx, float, true>(team) : norm_for<Tx, float, false>(team);
+    if (dtype == ZCCL_BF16) return vec ? norm_for<Tx, __nv_bfloat16, true>(s) : norm_for<Tx, __nv_bfloat16, false>(s);
+    return vec ? norm_for<Tx, float, true>(s) : norm_for<Tx, float, false>(s);
 }
-
-constexpr uint32_t kSmWarps = 16;
 
 bool dtype_ok(int dtype) { return dtype == ZCCL_BF16 || dtype == ZCCL_F32; }
 uint64_t size_of(int dtype) { return dtype == ZCCL_BF16 ? 2 : 4; }
@@ -197,10 +182,9 @@ bool on_16(const void* p, int dtype, uint64_t stride, uint64_t rows)
 
 zccl_status_t launch_norm(NormArgs& a, int x_dtype, int dtype, bool vec, cudaStream_t stream)
 {
-    const Shape s = norm_shape(a.hidden, a.rows, kSmWarps);
+    const Shape s = norm_shape(a.hidden, a.rows, vec && x_dtype == ZCCL_BF16 && dtype == ZCCL_BF16);
     a.workers = s.workers;
-    const NormKernel kernel =
-        x_dtype == ZCCL_BF16 ? norm_for<__nv_bfloat16>(dtype, vec, s.team) : norm_for<float>(dtype, vec, s.team);
+    const NormKernel kernel = x_dtype == ZCCL_BF16 ? norm_for<__nv_bfloat16>(dtype, vec, s) : norm_for<float>(dtype, vec, s);
     return launched(s.team == kClusterTeam ? launch_clusters(kernel, s.grid, s.warps * 32, 0, s.ctas, stream, a)
                                            : launch_dependent(kernel, s.grid, s.warps * 32, 0, stream, a));
 }
@@ -243,7 +227,9 @@ zccl_status_t zccl_residual_norm(const zccl_norm_t* cfg, const void* d_x, int x_
 zccl_status_t zccl_residual_norm_workspace_bytes(uint64_t hidden, uint64_t rows, uint64_t* bytes)
 {
     if (bytes == nullptr || hidden == 0 || hidden > ZCCL_MAX_NORM_HIDDEN || rows >= (1ull << 31)) return ZCCL_ERR_INVALID_ARG;
-    *bytes = norm_backward_bytes(hidden, rows);
+    const uint64_t narrow = norm_backward_bytes(norm_shape(hidden, rows, true), hidden);
+    const uint64_t wide = norm_backward_bytes(norm_shape(hidden, rows, false), hidden);
+    *bytes = narrow > wide ? narrow : wide;  // whatever the types
     return ZCCL_OK;
 }
 

@@ -58,38 +58,43 @@ __host__ __device__ inline uint32_t worker_of(uint64_t rows, uint32_t workers, u
 // How a row is held: by a warp (a tile at most), by the warps of a CTA, by those of a
 // cluster's CTAs, or (kLong) read several times by a CTA.
 enum Team { kWarpTeam = 0, kCtaTeam = 1, kClusterTeam = 2, kLong = 3 };
-constexpr uint32_t kTeamWarps = 16;    // the most of a CTA: 4096 columns
-constexpr uint32_t kMaxCluster = 4;    // CTAs: 16384 columns
+constexpr uint32_t kTeamWarps = 16;    // the most of a CTA
+constexpr uint32_t kMaxCluster = 4;    // CTAs
 constexpr uint32_t kWarpsPerCta = 8;   // of warps that are teams
 
 struct Shape {
     Team team;
+    uint32_t pieces;   // tiles of a warp: 1 or 2
     uint32_t warps;    // of a CTA
     uint32_t ctas;     // of a row
     uint32_t workers;  // teams
     uint32_t grid;     // CTAs
 };
 
-// `sm_warps`: how many warps an SM is to hold; the SMs are taken as 152.
-inline Shape norm_shape(uint64_t hidden, uint64_t rows, uint32_t sm_warps)
+// 16 warps an SM (128 registers a thread), the SMs taken as 152.  `narrow`: both types
+// have 16 bits and rows begin on 16 bytes, so a warp can hold two tiles: two are better (a row's sums are exchanged
+// by half as many warps) from two tiles on, where they come out even.
+inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow)
 {
     constexpr uint32_t kSms = 152;
     const uint32_t tiles = (uint32_t)((hidden + kTile - 1) / kTile);
+    const uint32_t pieces = narrow && (tiles % 2 == 0 || tiles > 8) ? 2 : 1, units = (tiles + pieces - 1) / pieces;
     Shape s{};
     const auto at_most_rows = [&](uint64_t n) { return (uint32_t)(n < rows ? n : rows > 0 ? rows : 1); };
     if (tiles <= 1) {
-        s = {kWarpTeam, kWarpsPerCta, 1, at_most_rows(kSms * sm_warps), 0};
+        s = {kWarpTeam, 1, kWarpsPerCta, 1, at_most_rows(kSms * 16), 0};
         s.grid = (s.workers + kWarpsPerCta - 1) / kWarpsPerCta;
-    } else if (tiles <= kTeamWarps * kMaxCluster) {
-        s.ctas = (tiles + kTeamWarps - 1) / kTeamWarps;
+    } else if (units <= kTeamWarps * kMaxCluster) {
+        s.ctas = units <= kTeamWarps ? 1 : units <= 2 * kTeamWarps ? 2 : 4;
         s.team = s.ctas > 1 ? kClusterTeam : kCtaTeam;
-        s.warps = (tiles + s.ctas - 1) / s.ctas;
-        const uint32_t per_sm = sm_warps / s.warps;
-        s.workers = at_most_rows((uint64_t)kSms * (per_sm > 0 ? per_sm : 1) / s.ctas);
+        s.pieces = pieces;
+        s.warps = (units + s.ctas - 1) / s.ctas;
+        // clusters of four do not fill every group of SMs: 32 of 38 are taken
+        s.workers = at_most_rows((uint64_t)(s.ctas == 4 ? 128 : kSms) * (16 / s.warps) / s.ctas);
         s.grid = s.workers * s.ctas;
     } else {
         // its sums stay in the workspace: fewer workers for longer rows
-        s = {kLong, kTeamWarps, 1, at_most_rows(kSms * 16384 / hidden * 2), 0};
+        s = {kLong, 1, kTeamWarps, 1, at_most_rows(kSms * 16384 / hidden * 2), 0};
         s.grid = s.workers;
     }
     return s;
@@ -135,6 +140,23 @@ __device__ __forceinline__ void st_cluster(float* p, uint32_t rank, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 
+// A warp's worker, and its tiles of a row.
+struct Place {
+    uint32_t worker, first, step;
+    __device__ __forceinline__ uint32_t tile(int n) const { return first + n * step; }
+};
+template <int kTeam>
+__device__ __forceinline__ Place place()
+{
+    const uint32_t warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if (kTeam == kWarpTeam) return {blockIdx.x * kWarpsPerCta + warp, 0, 0};
+    if (kTeam == kCtaTeam) return {blockIdx.x, warp * kTile, warps * kTile};
+    uint32_t ctas;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+    cluster_sync();  // the others' shared memory is there
+    return {blockIdx.x / ctas, (cluster_rank() * warps + warp) * kTile, ctas * warps * kTile};
+}
+
 // Room for the sums of a team's warps, whose halves take turns by `turn`: a warp may
 // write its sums of the next row while another still reads those of this one, and those
 // of the row after it only when all have been at the barrier between.
@@ -172,7 +194,7 @@ __device__ __forceinline__ void team_sum(float (&s)[N], float* red, uint32_t& tu
     for (int i = 0; i < N; ++i) s[i] = __shfl_sync(0xFFFFFFFFu, v, i * each);
 }
 
-// Sums N values over a CTA of `warps` warps, the same way in every thread; `red` holds
+// Sums N values over a CTA, the same way in every thread; `red` holds
 // 2 * 32 * N floats, whose halves take turns by `turn`.
 template <int N>
 __device__ __forceinline__ void cta_sum(float (&s)[N], float* red, uint32_t& turn)
@@ -197,21 +219,28 @@ __device__ __forceinline__ void cta_sum(float (&s)[N], float* red, uint32_t& tur
     }
 }
 
-// What the block's output is multiplied by before it joins (scale, gate, the
-// dropout's gain), and which of the lane's eight values stay.
-template <bool kVec>
-__device__ __forceinline__ uint32_t join_factors(float (&k)[8], const NormArgs& a, uint64_t offset, uint64_t row,
-                                                 uint32_t tile)
+// Of each group of teams the weights' sums, of each worker its parts of gate rows.
+inline uint64_t norm_backward_bytes(const Shape& s, uint64_t hidden)
 {
-    load_vector<kVec>(k, a.gate, a.gate.p != nullptr ? row / a.gate_span * a.gate_stride : 0, tile, a.hidden);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) k[j] *= a.factor;
-    return a.drop.below > 0 ? kept_piece<kVec>(a.drop, offset, (uint32_t)row, tile) : 0xFFu;
+    return ((uint64_t)(s.grid / s.ctas) * kWeightSlots + (uint64_t)s.workers * kGateSlots) * ((hidden + 7) / 8 * 8) * sizeof(float);
+}
+
+// What the block's output is multiplied by before it joins (scale, gate, the
+// dropout's gain).
+template <bool kVec>
+__device__ __forceinline__ Eight join_factors(const NormArgs& a, uint64_t row, uint32_t tile)
+{
+    return mul(load_vector<kVec>(a.gate, a.gate.p != nullptr ? row / a.gate_span * a.gate_stride : 0, tile, a.hidden), a.factor);
+}
+// Which of the lane's values of it stay.
+template <bool kVec>
+__device__ __forceinline__ Kept<kVec> join_kept(const NormArgs& a, uint64_t offset, uint64_t row, uint32_t tile)
+{
+    return a.drop.below > 0 ? kept_piece<kVec>(a.drop, offset, (uint32_t)row, tile) : kept_all<kVec>();
 }
 
 zccl_status_t launch_norm(NormArgs& a, int x_dtype, int dtype, bool vec, cudaStream_t stream);
 zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weight_dtype, bool vec, cudaStream_t stream);
-uint64_t norm_backward_bytes(uint64_t hidden, uint64_t rows);
 
 // Launches `kernel` as launch_dependent does, in clusters of `ctas`.
 inline cudaError_t launch_clusters(void (*kernel)(NormArgs), uint32_t grid, uint32_t threads, size_t smem, uint32_t ctas,

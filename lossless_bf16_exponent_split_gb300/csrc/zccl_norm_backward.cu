@@ -14,23 +14,7 @@ namespace zccl {
 
 namespace {
 
-constexpr int kSums = 6;
-
-// The sums of a piece: r^2, dh w r, y^2, and k p y times dr, dh w and r.
-__device__ __forceinline__ void add_sums(float (&s)[kSums], const float (&r)[8], const float (&hw)[8], const float (&up)[8],
-                                         const float (&y)[8], const float (&kp)[8])
-{
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float q = kp[j] * y[j];
-        s[0] = fmaf(r[j], r[j], s[0]);
-        s[1] = fmaf(hw[j], r[j], s[1]);
-        s[2] = fmaf(y[j], y[j], s[2]);
-        s[3] = fmaf(q, up[j], s[3]);
-        s[4] = fmaf(q, hw[j], s[4]);
-        s[5] = fmaf(q, r[j], s[5]);
-    }
-}
+constexpr int kSums = 6;  // r^2, dh w r, y^2, and k p y times dr, dh w and r
 
 struct RowFactors {
     float rho, c, eta, cy;
@@ -49,32 +33,51 @@ __device__ __forceinline__ RowFactors row_factors(const NormArgs& a, const float
     return f;
 }
 
-template <typename T, bool kVec>
-__device__ __forceinline__ void load_or_zero(float (&v)[8], const void* p, uint64_t first, uint32_t tile, uint32_t hidden)
+// The pieces' part of a row's sums; kp: the join's factor times p, 0 where dropped.
+__device__ __forceinline__ void add_sums(float2 (&s)[kSums], const NormArgs& a, const Eight& r, const Eight& hw, const Eight& up,
+                                         const Eight& y, const Eight& kp)
 {
-    if (p != nullptr) {
-        load8<T, kVec>(v, static_cast<const T*>(p) + first, tile, hidden);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    if (a.grad_h != nullptr) {
+        dot(s[0], r, r);
+        dot(s[1], hw, r);
+    }
+    if (a.post) {
+        const Eight q = mul(kp, y);
+        dot(s[2], y, y);
+        dot(s[3], q, up);
+        dot(s[4], q, hw);
+        dot(s[5], q, r);
     }
 }
 
-template <bool kVec>
-__device__ __forceinline__ void add_to(float* p, float (&v)[8], bool first, uint32_t tile, uint32_t hidden)
+// The gradient that the join sees: d = dr + rho (dh w - r c).
+__device__ __forceinline__ Eight joined(const RowFactors& f, const Eight& r, const Eight& hw, const Eight& up)
 {
-    if (!first) {
-        float o[8];
-        load8<float, kVec>(o, p, tile, hidden);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += o[j];
-    }
-    store8<float, kVec>(p, v, tile, hidden);
+    return fma(hw, f.rho, fma(r, -f.rho * f.c, up));
+}
+
+// y's gradient.
+__device__ __forceinline__ Eight branch(const NormArgs& a, const RowFactors& f, const Eight& d, const Eight& y, const Eight& kp)
+{
+    const Eight u = mul(kp, d);
+    return a.post ? fma(u, f.eta, mul(y, -f.eta * f.cy)) : u;
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ Eight load_or_zero(const void* p, uint64_t first, uint32_t tile, uint32_t hidden)
+{
+    return p != nullptr ? load8<T, kVec>(static_cast<const T*>(p) + first, tile, hidden) : all_eight(0.0f);
+}
+
+template <bool kVec>
+__device__ __forceinline__ Eight add_to(float* p, const Eight& v, bool first, uint32_t tile, uint32_t hidden)
+{
+    return store8<float, kVec>(p, first ? v : fma(v, 1.0f, load8<float, kVec>(p, tile, hidden)), tile, hidden);
 }
 
 // Writes a gate row's gradient, of its own type.
 template <bool kVec>
-__device__ __forceinline__ void store_gate(const NormArgs& a, uint64_t gate_row, float (&v)[8], uint32_t tile)
+__device__ __forceinline__ void store_gate(const NormArgs& a, uint64_t gate_row, const Eight& v, uint32_t tile)
 {
     if (a.gate.dtype == ZCCL_BF16)
         store8<__nv_bfloat16, kVec>(static_cast<__nv_bfloat16*>(a.grad_gate) + gate_row * a.hidden, v, tile, a.hidden);
@@ -85,7 +88,7 @@ __device__ __forceinline__ void store_gate(const NormArgs& a, uint64_t gate_row,
 // A CTA a worker; its rows are read once for the sums and once for the gradients, and
 // the sums over rows stay in the workspace: any size.
 template <typename Tx, typename Ty, bool kVec>
-__global__ void norm_backward_long_kernel(NormArgs a)
+__global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(NormArgs a)
 {
     __shared__ float red[2 * 32 * kSums];
     uint32_t turn = 0;
@@ -99,246 +102,286 @@ __global__ void norm_backward_long_kernel(NormArgs a)
     const bool join = a.grad_y != nullptr;
     for (uint64_t t = lo; t < hi; ++t) {
         const uint64_t gate_row = t / a.gate_span;
-        float s[kSums] = {};
+        float2 sum[kSums] = {};
         for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
-            float r[8], hw[8], up[8], y[8], kp[8], w[8];
-            load_or_zero<Tx, kVec>(r, a.x, t * a.x_stride, tile, a.hidden);
-            load_or_zero<Ty, kVec>(hw, a.grad_h, t * a.grad_h_stride, tile, a.hidden);
-            load_or_zero<Tx, kVec>(up, a.grad_r, t * a.grad_r_stride, tile, a.hidden);
-            load_or_zero<Ty, kVec>(y, a.y, t * a.y_stride, tile, a.hidden);
-            load_vector<kVec>(w, a.weight, 0, tile, a.hidden);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) hw[j] *= w[j];
-            const uint32_t kept = join_factors<kVec>(kp, a, offset, t, tile);
-            load_vector<kVec>(w, a.post_weight, 0, tile, a.hidden);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) kp[j] = (kept >> j) & 1u ? kp[j] * w[j] : 0.0f;
-            add_sums(s, r, hw, up, y, kp);
+            const Eight r = load_or_zero<Tx, kVec>(a.x, t * a.x_stride, tile, a.hidden);
+            const Eight hw = mul(load_or_zero<Ty, kVec>(a.grad_h, t * a.grad_h_stride, tile, a.hidden),
+                                 load_vector<kVec>(a.weight, 0, tile, a.hidden));
+            const Eight up = load_or_zero<Tx, kVec>(a.grad_r, t * a.grad_r_stride, tile, a.hidden);
+            Eight y = all_eight(0.0f), kp = y;
+            if (a.post) {
+                y = load_or_zero<Ty, kVec>(a.y, t * a.y_stride, tile, a.hidden);
+                kp = mul(join_factors<kVec>(a, t, tile), load_vector<kVec>(a.post_weight, 0, tile, a.hidden));
+                kp = where_kept<kVec>(join_kept<kVec>(a, offset, t, tile), kp);
+            }
+            add_sums(sum, a, r, hw, up, y, kp);
         }
+        float s[kSums];
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) s[i] = sum[i].x + sum[i].y;
         cta_sum<kSums>(s, red, turn);
         const RowFactors f = row_factors(a, s);
         for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
-            float r[8], dh[8], d[8], y[8], k[8], w[8], v[8];
-            load_or_zero<Tx, kVec>(r, a.x, t * a.x_stride, tile, a.hidden);
-            load_or_zero<Ty, kVec>(dh, a.grad_h, t * a.grad_h_stride, tile, a.hidden);
-            load_or_zero<Tx, kVec>(d, a.grad_r, t * a.grad_r_stride, tile, a.hidden);
-            load_vector<kVec>(w, a.weight, 0, tile, a.hidden);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                d[j] += f.rho * (dh[j] * w[j] - r[j] * f.c);
-                v[j] = d[j];
-            }
-            if (a.grad_x != nullptr) store8<Tx, kVec>(static_cast<Tx*>(a.grad_x) + t * a.hidden, v, tile, a.hidden);
-            if (a.grad_weight != nullptr) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = dh[j] * (r[j] * f.rho);
-                add_to<kVec>(sums + kSlotWeight * pitch, v, t == lo, tile, a.hidden);
-            }
+            const Eight r = load_or_zero<Tx, kVec>(a.x, t * a.x_stride, tile, a.hidden);
+            const Eight dh = load_or_zero<Ty, kVec>(a.grad_h, t * a.grad_h_stride, tile, a.hidden);
+            const Eight up = load_or_zero<Tx, kVec>(a.grad_r, t * a.grad_r_stride, tile, a.hidden);
+            const Eight d = joined(f, r, mul(dh, load_vector<kVec>(a.weight, 0, tile, a.hidden)), up);
+            if (a.grad_x != nullptr) store8<Tx, kVec>(static_cast<Tx*>(a.grad_x) + t * a.hidden, d, tile, a.hidden);
+            if (a.grad_weight != nullptr)
+                add_to<kVec>(sums + kSlotWeight * pitch, mul(dh, mul(r, f.rho)), t == lo, tile, a.hidden);
             if (!join) continue;
-            load_or_zero<Ty, kVec>(y, a.y, t * a.y_stride, tile, a.hidden);
-            const uint32_t kept = join_factors<kVec>(k, a, offset, t, tile);
-            load_vector<kVec>(w, a.post_weight, 0, tile, a.hidden);
+            const Eight y = load_or_zero<Ty, kVec>(a.y, t * a.y_stride, tile, a.hidden);
+            const Eight k = join_factors<kVec>(a, t, tile), p = load_vector<kVec>(a.post_weight, 0, tile, a.hidden);
+            const Kept<kVec> kept = join_kept<kVec>(a, offset, t, tile);
+            const Eight e = where_kept<kVec>(kept, mul(d, mul(y, f.eta)));
             if (a.grad_gate != nullptr) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = (kept >> j) & 1u ? a.factor * d[j] * (y[j] * f.eta * w[j]) : 0.0f;
+                const Eight v = mul(e, mul(p, a.factor));
                 const uint64_t begin = gate_row * a.gate_span, end = begin + a.gate_span;
+                Eight all = v;
                 if (a.gate_span > 1)
-                    add_to<kVec>(parts + (begin < lo ? kSlotBefore : kSlotBehind) * pitch, v, t == lo || t == begin, tile, a.hidden);
-                if (begin >= lo && (t + 1 == end || t + 1 == a.rows)) store_gate<kVec>(a, gate_row, v, tile);
+                    all = add_to<kVec>(parts + (begin < lo ? kSlotBefore : kSlotBehind) * pitch, v, t == lo || t == begin, tile, a.hidden);
+                if (begin >= lo && (t + 1 == end || t + 1 == a.rows)) store_gate<kVec>(a, gate_row, all, tile);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) k[j] = (kept >> j) & 1u ? k[j] * d[j] : 0.0f;
-            if (a.grad_post_weight != nullptr) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = k[j] * (y[j] * f.eta);
-                add_to<kVec>(sums + kSlotPost * pitch, v, t == lo, tile, a.hidden);
-            }
-            if (a.post)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) k[j] = f.eta * (k[j] * w[j] - y[j] * f.cy);
-            store8<Ty, kVec>(static_cast<Ty*>(a.grad_y) + t * a.hidden, k, tile, a.hidden);
+            if (a.grad_post_weight != nullptr) add_to<kVec>(sums + kSlotPost * pitch, mul(e, k), t == lo, tile, a.hidden);
+            store8<Ty, kVec>(static_cast<Ty*>(a.grad_y) + t * a.hidden, branch(a, f, d, y, where_kept<kVec>(kept, mul(k, p))), tile,
+                             a.hidden);
         }
     }
 }
 
-// A team a worker.  Weights and the join's factors of the lane's columns are kept in
-// shared memory, the sums over rows in registers.  While a gate stays the same the sums
-// of p's and of the gate's gradient are the same up to a factor of each column,
+// A worker's rows on their way: r, dr, dh and y of the row at hand and of the next one.
+// What the call does not have reads as zero.
+template <typename Tx, typename Ty, bool kVec, int kPieces>
+struct Feed;
+
+// Rows on 16 bytes come by asynchronous copies into places of the thread's own, so that
+// no thread waits for another's and no registers are held.
+__device__ __forceinline__ void copy_16(uint4* to, const void* from, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+template <typename Tx, typename Ty, int kPieces>
+struct Feed<Tx, Ty, true, kPieces> {
+    static constexpr int kX = sizeof(Tx) / 2, kY = sizeof(Ty) / 2, kAll = 2 * kX + 2 * kY;  // 16-byte parts of a piece
+    static constexpr uint32_t kThreadBytes = 2 * kPieces * kAll * 16;
+    uint4* mine;
+    uint32_t turn = 0;
+    __device__ __forceinline__ uint4* at(uint32_t turn, int n, int part) const
+    {
+        return mine + ((turn * kPieces + n) * kAll + part) * blockDim.x;
+    }
+    __device__ __forceinline__ Feed(uint4* smem, const NormArgs& a) : mine(smem + threadIdx.x)
+    {
+        for (int i = 0; i < 2 * kPieces * kAll; ++i) mine[i * blockDim.x] = make_uint4(0, 0, 0, 0);
+    }
+    template <typename T>
+    __device__ __forceinline__ void copy(const void* p, uint64_t row, uint64_t stride, uint32_t turn, int n, int part, uint32_t tile,
+                                         uint32_t hidden)
+    {
+        if (p == nullptr) return;
+        const uint32_t c = column<true>(tile, 0);
+        const T* from = static_cast<const T*>(p) + row * stride;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            copy_16(at(turn, n, part + i), c < hidden ? from + c + 4 * i : from, c < hidden);
+    }
+    // Asks for row t, to be had after the next wait().
+    __device__ __forceinline__ void ask(const NormArgs& a, const Place& place, uint64_t t)
+    {
+        turn ^= 1;
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+            copy<Tx>(a.x, t, a.x_stride, turn, n, 0, place.tile(n), a.hidden);
+            copy<Tx>(a.grad_r, t, a.grad_r_stride, turn, n, kX, place.tile(n), a.hidden);
+            copy<Ty>(a.grad_h, t, a.grad_h_stride, turn, n, 2 * kX, place.tile(n), a.hidden);
+            copy<Ty>(a.y, t, a.y_stride, turn, n, 2 * kX + kY, place.tile(n), a.hidden);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // Until the row that was asked for is there; the caller asks for the next one then and
+    // reads this one.
+    __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+    template <typename T>
+    __device__ __forceinline__ Eight read(uint32_t turn, int n, int part) const
+    {
+        if (sizeof(T) == 2) return widen(*at(turn, n, part));
+        const float4 x = *reinterpret_cast<const float4*>(at(turn, n, part)), y = *reinterpret_cast<const float4*>(at(turn, n, part + 1));
+        return {{make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)}};
+    }
+    struct Row {
+        const Feed& f;
+        uint32_t turn;
+        __device__ __forceinline__ Eight r(int n) const { return f.template read<Tx>(turn, n, 0); }
+        __device__ __forceinline__ Eight up(int n) const { return f.template read<Tx>(turn, n, kX); }
+        __device__ __forceinline__ Eight dh(int n) const { return f.template read<Ty>(turn, n, 2 * kX); }
+        __device__ __forceinline__ Eight y(int n) const { return f.template read<Ty>(turn, n, 2 * kX + kY); }
+    };
+    __device__ __forceinline__ Row row() const { return {*this, turn}; }
+};
+
+// Others by loads of single values into registers.
+template <typename Tx, typename Ty, int kPieces>
+struct Feed<Tx, Ty, false, kPieces> {
+    static constexpr uint32_t kThreadBytes = 0;
+    Piece<Tx, false> pr[kPieces], pu[kPieces];
+    Piece<Ty, false> ph[kPieces], py[kPieces];
+    __device__ __forceinline__ Feed(uint4*, const NormArgs&) : pr{}, pu{}, ph{}, py{} {}
+    __device__ __forceinline__ void ask(const NormArgs& a, const Place& place, uint64_t t)
+    {
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+            if (a.x != nullptr) pr[n].load(static_cast<const Tx*>(a.x) + t * a.x_stride, place.tile(n), a.hidden);
+            if (a.grad_r != nullptr) pu[n].load(static_cast<const Tx*>(a.grad_r) + t * a.grad_r_stride, place.tile(n), a.hidden);
+            if (a.grad_h != nullptr) ph[n].load(static_cast<const Ty*>(a.grad_h) + t * a.grad_h_stride, place.tile(n), a.hidden);
+            if (a.y != nullptr) py[n].load(static_cast<const Ty*>(a.y) + t * a.y_stride, place.tile(n), a.hidden);
+        }
+    }
+    __device__ __forceinline__ void wait() {}
+    struct Row {
+        Piece<Tx, false> pr[kPieces], pu[kPieces];
+        Piece<Ty, false> ph[kPieces], py[kPieces];
+        __device__ __forceinline__ Eight r(int n) const { return pr[n].get(); }
+        __device__ __forceinline__ Eight up(int n) const { return pu[n].get(); }
+        __device__ __forceinline__ Eight dh(int n) const { return ph[n].get(); }
+        __device__ __forceinline__ Eight y(int n) const { return py[n].get(); }
+    };
+    __device__ __forceinline__ Row row() const
+    {
+        Row o;
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) o.pr[n] = pr[n], o.pu[n] = pu[n], o.ph[n] = ph[n], o.py[n] = py[n];
+        return o;
+    }
+};
+
+// A team a worker; the sums over rows stay in registers.  While a gate stays the same
+// the sums of p's and of the gate's gradient are the same up to a factor of each column,
 //   e = sum of (kept) d y eta:   dp += scale gate e,   dgate = scale p e
 // so one sum serves both, and is taken out when the gate changes.
-template <typename Tx, typename Ty, bool kVec, int kTeam>
-__global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeamWarps * 32, kTeam == kWarpTeam ? 2 : 1) norm_backward_kernel(NormArgs a)
+template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces>
+__global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeamWarps * 32, kTeam == kWarpTeam ? 2 : 1)
+    norm_backward_kernel(NormArgs a)
 {
-    extern __shared__ float4 smem[];
+    extern __shared__ uint4 smem[];
+    using Rows = Feed<Tx, Ty, kVec, kPieces>;
+    // a thread's sums of p's gradient (two 16-byte parts a piece), and the teams' sums
+    float4* const post = reinterpret_cast<float4*>(smem) + Rows::kThreadBytes / 16 * blockDim.x + threadIdx.x;
+    float* const red = reinterpret_cast<float*>(smem) + (Rows::kThreadBytes + 32 * kPieces) / 4 * blockDim.x;
     uint32_t turn = 0;
-    const uint32_t warp = threadIdx.x >> 5, threads = blockDim.x;
-    // eight values of each thread's own, by name
-    enum { kW, kP, kK, kDp, kOwn };
-    const auto put = [&](int name, const float (&v)[8]) {
-        smem[(2 * name) * threads + threadIdx.x] = make_float4(v[0], v[1], v[2], v[3]);
-        smem[(2 * name + 1) * threads + threadIdx.x] = make_float4(v[4], v[5], v[6], v[7]);
-    };
-    const auto get = [&](int name, float (&v)[8]) {
-        const float4 x = smem[(2 * name) * threads + threadIdx.x], y = smem[(2 * name + 1) * threads + threadIdx.x];
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-    };
-    float* const red = reinterpret_cast<float*>(smem + 2 * kOwn * threads);
-    uint32_t worker = blockIdx.x, tile = warp * kTile;
-    if (kTeam == kWarpTeam) worker = blockIdx.x * kWarpsPerCta + warp, tile = 0;
-    if (kTeam == kClusterTeam) {
-        uint32_t ctas;
-        asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
-        worker = blockIdx.x / ctas;
-        tile = (cluster_rank() * (threads / 32) + warp) * kTile;
-    }
     pdl_wait();
-    if (kTeam == kClusterTeam) cluster_sync();  // the others' shared memory is there
+    const Place at = place<kTeam>();
     const uint64_t offset = drop_offset(a.drop);
-    const uint64_t lo = worker < a.workers ? first_row(a.rows, a.workers, worker) : 0;
-    const uint64_t hi = worker < a.workers ? first_row(a.rows, a.workers, worker + 1) : 0;
+    const uint64_t lo = at.worker < a.workers ? first_row(a.rows, a.workers, at.worker) : 0;
+    const uint64_t hi = at.worker < a.workers ? first_row(a.rows, a.workers, at.worker + 1) : 0;
     const uint64_t pitch = (a.hidden + 7) / 8 * 8;
     const bool join = a.grad_y != nullptr;
-    float dw[8] = {}, e[8] = {};
-    {
-        float v[8];
-        load_vector<kVec>(v, a.weight, 0, tile, a.hidden);
-        put(kW, v);
-        load_vector<kVec>(v, a.post_weight, 0, tile, a.hidden);
-        put(kP, v);
-        put(kDp, dw);
-    }
-    Piece<Tx, kVec> pr, pu;
-    Piece<Ty, kVec> ph, py;
-    const auto load = [&](uint64_t t) {
-        if (a.x != nullptr) pr.load(static_cast<const Tx*>(a.x) + t * a.x_stride, tile, a.hidden);
-        if (a.grad_h != nullptr) ph.load(static_cast<const Ty*>(a.grad_h) + t * a.grad_h_stride, tile, a.hidden);
-        if (a.grad_r != nullptr) pu.load(static_cast<const Tx*>(a.grad_r) + t * a.grad_r_stride, tile, a.hidden);
-        if (a.y != nullptr) py.load(static_cast<const Ty*>(a.y) + t * a.y_stride, tile, a.hidden);
+    const auto put_post = [&](int n, const Eight& v) {
+        post[(2 * n) * blockDim.x] = make_float4(v[0], v[1], v[2], v[3]);
+        post[(2 * n + 1) * blockDim.x] = make_float4(v[4], v[5], v[6], v[7]);
     };
-    // what is not there stays zero
-    pr.zero(), pu.zero(), ph.zero(), py.zero();
-    if (lo < hi) load(lo);
+    const auto get_post = [&](int n, int warps) -> Eight {
+        const float4 x = post[(2 * n) * blockDim.x + 32 * warps], y = post[(2 * n + 1) * blockDim.x + 32 * warps];
+        return {{make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)}};
+    };
+    Rows rows(smem, a);
+    Eight w[kPieces], kp[kPieces], dw[kPieces], e[kPieces];
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) {
+        w[n] = load_vector<kVec>(a.weight, 0, at.tile(n), a.hidden);
+        kp[n] = dw[n] = e[n] = all_eight(0.0f);
+        put_post(n, e[n]);
+    }
+    if (lo < hi) rows.ask(a, at, lo);
     uint64_t gate_row = lo / a.gate_span, gate_end = lo;  // where the gate changes
     const auto take_out = [&](uint64_t t) {
-        float v[8], o[8];
-        get(kK, v);
-        get(kDp, o);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = fmaf(v[j], e[j], o[j]);
-        put(kDp, o);
-        if (a.grad_gate == nullptr) return;
-        get(kP, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= a.factor * e[j];
         const uint64_t begin = gate_row * a.gate_span;
-        if (begin >= lo && (t == begin + a.gate_span || t == a.rows))
-            store_gate<kVec>(a, gate_row, v, tile);
-        else
-            store8<float, kVec>(a.parts + (worker * kGateSlots + (begin < lo ? kSlotBefore : kSlotBehind)) * pitch, v, tile, a.hidden);
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+            const uint32_t tile = at.tile(n);
+            if (a.grad_post_weight != nullptr) put_post(n, fma(e[n], join_factors<kVec>(a, begin, tile), get_post(n, 0)));
+            if (a.grad_gate == nullptr) continue;
+            const Eight v = mul(e[n], mul(load_vector<kVec>(a.post_weight, 0, tile, a.hidden), a.factor));
+            if (begin >= lo && (t == begin + a.gate_span || t == a.rows))
+                store_gate<kVec>(a, gate_row, v, tile);
+            else
+                store8<float, kVec>(a.parts + ((uint64_t)at.worker * kGateSlots + (begin < lo ? kSlotBefore : kSlotBehind)) * pitch, v,
+                                    tile, a.hidden);
+        }
     };
     for (uint64_t t = lo; t < hi; ++t) {
-        float r[8], dh[8], d[8], y[8];
-        pr.get(r), ph.get(dh), pu.get(d), py.get(y);
-        if (t + 1 < hi) load(t + 1);
+        rows.wait();
+        const auto row = rows.row();
+        if (t + 1 < hi) rows.ask(a, at, t + 1);
         if (join && t == gate_end) {
             if (t > lo) {
                 take_out(t);
                 ++gate_row;
             }
             gate_end = a.gate.p != nullptr ? (gate_row + 1) * a.gate_span : a.rows;
-            float k[8];
-            load_vector<kVec>(k, a.gate, gate_row * a.gate_stride, tile, a.hidden);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) k[j] *= a.factor, e[j] = 0.0f;
-            put(kK, k);
-        }
-        const uint32_t kept = a.drop.below > 0 && join ? kept_piece<kVec>(a.drop, offset, (uint32_t)t, tile) : 0xFFu;
-        float s[kSums] = {};
-        if (a.grad_h != nullptr) {
-            float w[8];
-            get(kW, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                s[0] = fmaf(r[j], r[j], s[0]);
-                s[1] = fmaf(dh[j] * w[j], r[j], s[1]);
+            for (int n = 0; n < kPieces; ++n) {
+                kp[n] = mul(join_factors<kVec>(a, t, at.tile(n)), load_vector<kVec>(a.post_weight, 0, at.tile(n), a.hidden));
+                e[n] = all_eight(0.0f);
             }
         }
-        if (a.post) {
-            float w[8], k[8], p[8];
-            get(kW, w), get(kK, k), get(kP, p);
+        Kept<kVec> kept[kPieces];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float q = (kept >> j) & 1u ? k[j] * p[j] * y[j] : 0.0f;
-                s[2] = fmaf(y[j], y[j], s[2]);
-                s[3] = fmaf(q, d[j], s[3]);
-                s[4] = fmaf(q, dh[j] * w[j], s[4]);
-                s[5] = fmaf(q, r[j], s[5]);
-            }
-        }
+        for (int n = 0; n < kPieces; ++n) kept[n] = join ? join_kept<kVec>(a, offset, t, at.tile(n)) : kept_all<kVec>();
         RowFactors f{0.0f, 0.0f, 1.0f, 0.0f};
         if (a.grad_h != nullptr || a.post) {
-            team_sum<kSums, kTeam>(s, red, turn);
+            float2 sum[kSums] = {};
+#pragma unroll
+            for (int n = 0; n < kPieces; ++n)
+                add_sums(sum, a, row.r(n), mul(row.dh(n), w[n]), row.up(n), row.y(n), where_kept<kVec>(kept[n], kp[n]));
+            float s[kSums];
+#pragma unroll
+            for (int i = 0; i < kSums; ++i) s[i] = sum[i].x + sum[i].y;
+            if (a.post) {
+                team_sum<kSums, kTeam>(s, red, turn);
+            } else {
+                float two[2] = {s[0], s[1]};
+                team_sum<2, kTeam>(two, red, turn);
+                s[0] = two[0], s[1] = two[1];
+            }
             f = row_factors(a, s);
         }
-        float v[8];
-        if (a.grad_h != nullptr) {
-            float w[8];
-            get(kW, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                d[j] += f.rho * (dh[j] * w[j] - r[j] * f.c);
-                dw[j] = fmaf(dh[j], r[j] * f.rho, dw[j]);
-            }
+        for (int n = 0; n < kPieces; ++n) {
+            const uint32_t tile = at.tile(n);
+            const Eight r = row.r(n), dh = row.dh(n), d = joined(f, r, mul(dh, w[n]), row.up(n));
+            dw[n] = fma(dh, mul(r, f.rho), dw[n]);
+            if (a.grad_x != nullptr) store8<Tx, kVec>(static_cast<Tx*>(a.grad_x) + t * a.hidden, d, tile, a.hidden);
+            if (!join) continue;
+            const Eight y = row.y(n);
+            e[n] = fma(d, mul(where_kept<kVec>(kept[n], y), f.eta), e[n]);
+            store8<Ty, kVec>(static_cast<Ty*>(a.grad_y) + t * a.hidden, branch(a, f, d, y, where_kept<kVec>(kept[n], kp[n])), tile,
+                             a.hidden);
         }
-        if (a.grad_x != nullptr) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = d[j];
-            store8<Tx, kVec>(static_cast<Tx*>(a.grad_x) + t * a.hidden, v, tile, a.hidden);
-        }
-        if (!join) continue;
-        float k[8];
-        get(kK, k);
-        if (a.y != nullptr) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] += (kept >> j) & 1u ? d[j] * (y[j] * f.eta) : 0.0f;
-        }
-        if (a.post) {
-            float p[8];
-            get(kP, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) k[j] = f.eta * (((kept >> j) & 1u ? k[j] * d[j] * p[j] : 0.0f) - y[j] * f.cy);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) k[j] = (kept >> j) & 1u ? k[j] * d[j] : 0.0f;
-        }
-        store8<Ty, kVec>(static_cast<Ty*>(a.grad_y) + t * a.hidden, k, tile, a.hidden);
     }
     if (join && lo < hi && a.y != nullptr) take_out(hi);
     pdl_launch_dependents();
-    // the weights' sums: of a CTA's warps where each is a team
-    float dp[8];
-    get(kDp, dp);
+    // the weights' sums, of a CTA's warps where each is a team
+    uint64_t group = at.worker;
     if (kTeam == kWarpTeam) {
-        put(kW, dw);
+        group = blockIdx.x;
         __syncthreads();
-        if (warp > 0) return;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            float sum[8] = {};
-            for (uint32_t i = 0; i < kWarpsPerCta; ++i) {
-                const int name = n == 0 ? kW : kDp;
-                const float4 x = smem[(2 * name) * threads + threadIdx.x + 32 * i];
-                const float4 z = smem[(2 * name + 1) * threads + threadIdx.x + 32 * i];
-                sum[0] += x.x, sum[1] += x.y, sum[2] += x.z, sum[3] += x.w, sum[4] += z.x, sum[5] += z.y, sum[6] += z.z, sum[7] += z.w;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) (n == 0 ? dw : dp)[j] = sum[j];
-        }
+        Eight all = all_eight(0.0f);
+        if (threadIdx.x < 32)
+            for (uint32_t i = 0; i < kWarpsPerCta; ++i) all = fma(get_post(0, i), 1.0f, all);
+        __syncthreads();
+        put_post(0, dw[0]);
+        __syncthreads();
+        if (threadIdx.x >= 32) return;
+        dw[0] = all_eight(0.0f);
+        for (uint32_t i = 0; i < kWarpsPerCta; ++i) dw[0] = fma(get_post(0, i), 1.0f, dw[0]);
+        put_post(0, all);
     }
-    const uint64_t group = kTeam == kWarpTeam ? blockIdx.x : worker;
-    if (a.grad_weight != nullptr) store8<float, kVec>(a.sums + (group * kWeightSlots + kSlotWeight) * pitch, dw, tile, a.hidden);
-    if (a.grad_post_weight != nullptr)
-        store8<float, kVec>(a.sums + (group * kWeightSlots + kSlotPost) * pitch, dp, tile, a.hidden);
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) {
+        float* sums = a.sums + group * kWeightSlots * pitch;
+        if (a.grad_weight != nullptr) store8<float, kVec>(sums + kSlotWeight * pitch, dw[n], at.tile(n), a.hidden);
+        if (a.grad_post_weight != nullptr) store8<float, kVec>(sums + kSlotPost * pitch, get_post(n, 0), at.tile(n), a.hidden);
+    }
 }
 
 // Adds the partial sums up: blockIdx.y = 0, 1 a weight's, 2 + i those of a gate row that
@@ -412,49 +455,49 @@ cudaError_t launch_join(const NormArgs& a, int weight_dtype, cudaStream_t stream
 }
 
 using NormKernel = void (*)(NormArgs);
+struct Launch {
+    NormKernel kernel;
+    uint32_t thread_bytes;  // of shared memory
+};
 
-template <typename Tx, typename Ty, bool kVec>
-NormKernel backward_for(Team team)
+template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces>
+Launch team_launch()
 {
-    return team == kWarpTeam  ? norm_backward_kernel<Tx, Ty, kVec, kWarpTeam>
-           : team == kCtaTeam ? norm_backward_kernel<Tx, Ty, kVec, kCtaTeam>
-           : team == kLong    ? norm_backward_long_kernel<Tx, Ty, kVec>
-                              : norm_backward_kernel<Tx, Ty, kVec, kClusterTeam>;
+    return {norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces>, Feed<Tx, Ty, kVec, kPieces>::kThreadBytes + 32 * kPieces};
+}
+template <typename Tx, typename Ty, bool kVec>
+Launch backward_for(const Shape& s)
+{
+    constexpr int kMost = kVec && sizeof(Tx) == 2 && sizeof(Ty) == 2 ? 2 : 1;
+    if (s.team == kWarpTeam) return team_launch<Tx, Ty, kVec, kWarpTeam, 1>();
+    if (s.team == kLong) return {norm_backward_long_kernel<Tx, Ty, kVec>, 0};
+    if (s.team == kCtaTeam)
+        return s.pieces == 1 ? team_launch<Tx, Ty, kVec, kCtaTeam, 1>() : team_launch<Tx, Ty, kVec, kCtaTeam, kMost>();
+    return s.pieces == 1 ? team_launch<Tx, Ty, kVec, kClusterTeam, 1>() : team_launch<Tx, Ty, kVec, kClusterTeam, kMost>();
 }
 template <typename Tx>
-NormKernel backward_for(int dtype, bool vec, Team team)
+Launch backward_for(int dtype, bool vec, const Shape& s)
 {
-    if (dtype == ZCCL_BF16) return vec ? backward_for<Tx, __nv_bfloat16, true>(team) : backward_for<Tx, __nv_bfloat16, false>(team);
-    return vec ? backward_for<Tx, float, true>(team) : backward_for<Tx, float, false>(team);
+    if (dtype == ZCCL_BF16) return vec ? backward_for<Tx, __nv_bfloat16, true>(s) : backward_for<Tx, __nv_bfloat16, false>(s);
+    return vec ? backward_for<Tx, float, true>(s) : backward_for<Tx, float, false>(s);
 }
-
-constexpr uint32_t kSmWarps = 16;  // of a backward pass: 128 registers a thread
 
 }  // namespace
 
-// Of each group of teams the weights' sums, of each worker its parts of gate rows.
-uint64_t norm_backward_bytes(uint64_t hidden, uint64_t rows)
-{
-    const Shape s = norm_shape(hidden, rows, kSmWarps);
-    const uint64_t groups = s.grid / s.ctas, pitch = (hidden + 7) / 8 * 8;
-    return (groups * kWeightSlots + (uint64_t)s.workers * kGateSlots) * pitch * sizeof(float);
-}
-
 zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weight_dtype, bool vec, cudaStream_t stream)
 {
-    const Shape s = norm_shape(a.hidden, a.rows, kSmWarps);
+    const Shape s = norm_shape(a.hidden, a.rows, vec && x_dtype == ZCCL_BF16 && dtype == ZCCL_BF16);
     a.workers = s.workers;
     a.groups = s.grid / s.ctas;
     a.parts = a.sums + (uint64_t)a.groups * kWeightSlots * ((a.hidden + 7) / 8 * 8);
-    const NormKernel kernel = x_dtype == ZCCL_BF16 ? backward_for<__nv_bfloat16>(dtype, vec, s.team)
-                                                   : backward_for<float>(dtype, vec, s.team);
+    const Launch l = x_dtype == ZCCL_BF16 ? backward_for<__nv_bfloat16>(dtype, vec, s) : backward_for<float>(dtype, vec, s);
     const uint32_t threads = s.warps * 32;
-    const size_t smem = s.team == kLong ? 0 : threads * 4 * 8 * sizeof(float) + kTeamRed * sizeof(float);
+    const size_t smem = s.team == kLong ? 0 : threads * l.thread_bytes + kTeamRed * sizeof(float);
     cudaError_t e = cudaSuccess;
-    if (smem > 48 << 10) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 48 << 10) e = cudaFuncSetAttribute(l.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)
-        e = s.team == kClusterTeam ? launch_clusters(kernel, s.grid, threads, smem, s.ctas, stream, a)
-                                   : launch_dependent(kernel, s.grid, threads, smem, stream, a);
+        e = s.team == kClusterTeam ? launch_clusters(l.kernel, s.grid, threads, smem, s.ctas, stream, a)
+                                   : launch_dependent(l.kernel, s.grid, threads, smem, stream, a);
     if (e == cudaSuccess) e = launch_join(a, weight_dtype, stream);
     return launched(e);
 }

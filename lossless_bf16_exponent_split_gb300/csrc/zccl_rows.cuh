@@ -20,93 +20,138 @@ __device__ __forceinline__ uint32_t column(uint32_t tile, int j)
     return kVec ? tile + lane * 8 + j : tile + j * 32 + lane;
 }
 
-__device__ __forceinline__ void widen(float (&v)[8], const uint4& q)
+// Eight values of a lane as four pairs: most arithmetic on them is two at a time.
+struct Eight {
+    float2 v[4];
+    __device__ __forceinline__ float& operator[](int j) { return j & 1 ? v[j / 2].y : v[j / 2].x; }
+    __device__ __forceinline__ float operator[](int j) const { return j & 1 ? v[j / 2].y : v[j / 2].x; }
+};
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+__device__ __forceinline__ Eight all_eight(float x) { return {{twice(x), twice(x), twice(x), twice(x)}}; }
+// a b, a s, a b + c, a s + c
+__device__ __forceinline__ Eight mul(const Eight& a, const Eight& b)
 {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    Eight o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
+    for (int i = 0; i < 4; ++i) o.v[i] = __fmul2_rn(a.v[i], b.v[i]);
+    return o;
+}
+__device__ __forceinline__ Eight mul(const Eight& a, float s) { return mul(a, all_eight(s)); }
+__device__ __forceinline__ Eight fma(const Eight& a, const Eight& b, const Eight& c)
+{
+    Eight o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.v[i] = __ffma2_rn(a.v[i], b.v[i], c.v[i]);
+    return o;
+}
+__device__ __forceinline__ Eight fma(const Eight& a, float s, const Eight& c) { return fma(a, all_eight(s), c); }
+// The sum of products, added to a pair.
+__device__ __forceinline__ void dot(float2& s, const Eight& a, const Eight& b)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __ffma2_rn(a.v[i], b.v[i], s);
 }
 
-// A piece as it is held in memory, to be widened later: eight values of T (kVec) or
-// their widened form.
+__device__ __forceinline__ Eight widen(const uint4& q)
+{
+    return {{make_float2(bf16_lo(q.x), bf16_hi(q.x)), make_float2(bf16_lo(q.y), bf16_hi(q.y)),
+             make_float2(bf16_lo(q.z), bf16_hi(q.z)), make_float2(bf16_lo(q.w), bf16_hi(q.w))}};
+}
+
+// A lane's eight values of a tile as they are held in memory, to be widened later.
 template <typename T, bool kVec>
-struct Piece {
-    float v[8];
-    __device__ __forceinline__ void zero()
-    {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    }
-    __device__ __forceinline__ void load(const T* row, uint32_t tile, uint32_t cols)
-    {
-        if (kVec) {
-            const uint32_t c = column<true>(tile, 0);
-            if (c < cols) {
-                const float4* p = reinterpret_cast<const float4*>(row + c);
-                const float4 a = p[0], b = p[1];
-                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t c = column<false>(tile, j);
-                v[j] = c < cols ? to_float<T>(row[c]) : 0.0f;
-            }
-        }
-    }
-    __device__ __forceinline__ void get(float (&o)[8]) const
-    {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = v[j];
-    }
-};
+struct Piece;
 template <>
 struct Piece<__nv_bfloat16, true> {
     uint4 q;
-    __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const __nv_bfloat16* row, uint32_t tile, uint32_t cols)
     {
         const uint32_t c = column<true>(tile, 0);
         q = c < cols ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ void get(float (&o)[8]) const { widen(o, q); }
+    __device__ __forceinline__ Eight get() const { return widen(q); }
+};
+template <>
+struct Piece<__nv_bfloat16, false> {
+    uint4 q;
+    __device__ __forceinline__ void load(const __nv_bfloat16* row, uint32_t tile, uint32_t cols)
+    {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t c = column<false>(tile, j);
+            w[j] = c < cols ? p[c] : 0;
+        }
+        q = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+    __device__ __forceinline__ Eight get() const { return widen(q); }
+};
+template <bool kVec>
+struct Piece<float, kVec> {
+    Eight v;
+    __device__ __forceinline__ void load(const float* row, uint32_t tile, uint32_t cols)
+    {
+        if (kVec) {
+            const uint32_t c = column<true>(tile, 0);
+            const float4* p = reinterpret_cast<const float4*>(row + c);
+            const float4 a = c < cols ? p[0] : make_float4(0, 0, 0, 0), b = c < cols ? p[1] : make_float4(0, 0, 0, 0);
+            v = {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t c = column<false>(tile, j);
+                v[j] = c < cols ? row[c] : 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ Eight get() const { return v; }
 };
 
 template <typename T, bool kVec>
-__device__ __forceinline__ void load8(float (&v)[8], const T* row, uint32_t tile, uint32_t cols)
+__device__ __forceinline__ Eight load8(const T* row, uint32_t tile, uint32_t cols)
 {
     Piece<T, kVec> p;
     p.load(row, tile, cols);
-    p.get(v);
+    return p.get();
 }
 
-// Rounds v to T, leaves in v what was stored, and stores it.
+// Stores v rounded to T; what was stored.
 template <typename T, bool kVec>
-__device__ __forceinline__ void store8(T* row, float (&v)[8], uint32_t tile, uint32_t cols)
+__device__ __forceinline__ Eight store8(T* row, const Eight& v, uint32_t tile, uint32_t cols)
 {
+    if (sizeof(T) == 2) {
+        const uint4 q = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        if (kVec) {
+            const uint32_t c = column<true>(tile, 0);
+            if (c < cols) *reinterpret_cast<uint4*>(row + c) = q;
+        } else {
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+            uint16_t* p = reinterpret_cast<uint16_t*>(row);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t c = column<false>(tile, j);
+                if (c < cols) p[c] = (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
+            }
+        }
+        return widen(q);
+    }
     if (kVec) {
         const uint32_t c = column<true>(tile, 0);
-        if (sizeof(T) == 2) {
-            const uint4 q = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-            if (c < cols) *reinterpret_cast<uint4*>(row + c) = q;
-            widen(v, q);
-        } else if (c < cols) {
+        if (c < cols) {
             float4* p = reinterpret_cast<float4*>(row + c);
             p[0] = make_float4(v[0], v[1], v[2], v[3]);
             p[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
     } else {
+        float* p = reinterpret_cast<float*>(row);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t c = column<false>(tile, j);
-            const T t = from_float<T>(v[j]);
-            if (c < cols) row[c] = t;
-            v[j] = to_float<T>(t);
+            if (c < cols) p[c] = v[j];
         }
     }
+    return v;
 }
 
 // A vector of weights or a gate's row, of either type; all ones where there is none.
@@ -115,23 +160,18 @@ struct Vector {
     int dtype;
 };
 template <bool kVec>
-__device__ __forceinline__ void load_vector(float (&v)[8], const Vector& a, uint64_t first, uint32_t tile, uint32_t cols)
+__device__ __forceinline__ Eight load_vector(const Vector& a, uint64_t first, uint32_t tile, uint32_t cols)
 {
-    if (a.p == nullptr) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 1.0f;
-    } else if (a.dtype == ZCCL_BF16) {
-        load8<__nv_bfloat16, kVec>(v, static_cast<const __nv_bfloat16*>(a.p) + first, tile, cols);
-    } else {
-        load8<float, kVec>(v, static_cast<const float*>(a.p) + first, tile, cols);
-    }
+    if (a.p == nullptr) return all_eight(1.0f);
+    if (a.dtype == ZCCL_BF16) return load8<__nv_bfloat16, kVec>(static_cast<const __nv_bfloat16*>(a.p) + first, tile, cols);
+    return load8<float, kVec>(static_cast<const float*>(a.p) + first, tile, cols);
 }
 
 // ---- dropout ----------------------------------------------------------------
 struct DropArgs {
-    uint32_t below;  // of 2^16: how many of an element's values drop it; 0: no dropout
-    float gain;      // 1 / (1 - below / 2^16)
-    uint32_t key[2];
+    uint32_t below;      // of 2^16: how many of an element's values drop it; 0: no dropout
+    float gain;          // 1 / (1 - below / 2^16)
+    uint32_t key[10][2]; // of each round
     uint64_t offset;
     const uint64_t* more;  // device: added to the offset
 };
@@ -142,8 +182,10 @@ inline bool drop_args(float p, uint64_t seed, uint64_t offset, const uint64_t* m
     const double below = floor((double)p * 65536.0 + 0.5);
     d->below = (uint32_t)below;
     d->gain = below < 65536.0 ? (float)(1.0 / (1.0 - below / 65536.0)) : 0.0f;
-    d->key[0] = (uint32_t)seed;
-    d->key[1] = (uint32_t)(seed >> 32);
+    for (uint32_t r = 0; r < 10; ++r) {
+        d->key[r][0] = (uint32_t)seed + r * 0x9E3779B9u;
+        d->key[r][1] = (uint32_t)(seed >> 32) + r * 0xBB67AE85u;
+    }
     d->offset = offset;
     d->more = more;
     return true;
@@ -156,45 +198,90 @@ __device__ __forceinline__ uint64_t drop_offset(const DropArgs& d)
 
 // Philox4x32-10 (Salmon, Moraes, Dror and Shaw, 2011): ten rounds, in each the two
 // even words are multiplied out to 64 bits by a constant, and the halves take each
-// other's places with the odd words and the key, which moves on by a constant.
-__device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1)
+// other's places with the odd words and the round's key.
+__device__ __forceinline__ uint4 philox(uint4 c, const DropArgs& d)
 {
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t a = (uint64_t)c.x * 0xD2511F53u, b = (uint64_t)c.z * 0xCD9E8D57u;
-        c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ k0, (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ k1, (uint32_t)a);
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
+        c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ d.key[r][0], (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ d.key[r][1], (uint32_t)a);
     }
     return c;
 }
 
-// Which of the eight columns of a block (bit j: column 8 block + j) of a row stay.
-__device__ __forceinline__ uint32_t kept_block(const DropArgs& d, uint64_t offset, uint32_t row, uint32_t block)
+// Which of a lane's eight values stay.  A value's 16 bits are compared in the upper
+// half of a word, so no bits have to be cut out of it.
+template <bool kVec>
+struct Kept;
+template <>
+struct Kept<true> {
+    uint4 w;
+    uint32_t below;
+    __device__ __forceinline__ bool operator[](int j) const
+    {
+        const uint32_t x = j / 2 == 0 ? w.x : j / 2 == 1 ? w.y : j / 2 == 2 ? w.z : w.w;
+        return (j & 1 ? x : x << 16) >= below;
+    }
+};
+template <>
+struct Kept<false> {
+    uint32_t bits;
+    __device__ __forceinline__ bool operator[](int j) const { return (bits >> j) & 1u; }
+};
+
+// The bits of the eight columns from 8 block on.
+__device__ __forceinline__ Kept<true> kept_block(const DropArgs& d, uint64_t offset, uint32_t row, uint32_t block)
 {
-    const uint4 u = philox(make_uint4(block, row, (uint32_t)offset, (uint32_t)(offset >> 32)), d.key[0], d.key[1]);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint32_t kept = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        kept |= ((w[i] & 0xFFFFu) >= d.below ? 1u << (2 * i) : 0u) | ((w[i] >> 16) >= d.below ? 2u << (2 * i) : 0u);
-    return kept;
+    Kept<true> k;
+    k.w = philox(make_uint4(block, row, (uint32_t)offset, (uint32_t)(offset >> 32)), d);
+    k.below = d.below << 16;
+    if (d.below == 65536) k.w = make_uint4(0, 0, 0, 0), k.below = 1;  // nothing stays
+    return k;
 }
 
-// Which of the lane's eight values of a tile stay (bit j: its j-th).  The lanes hold
-// a block each; where a lane's columns are 32 apart their bits come from the lanes
-// that have them, so all lanes take part.
+// Which of the lane's values of a tile stay.  The lanes hold a block each; where a
+// lane's columns are 32 apart their bits come from the lanes that have them, so all
+// lanes take part.
 template <bool kVec>
-__device__ __forceinline__ uint32_t kept_piece(const DropArgs& d, uint64_t offset, uint32_t row, uint32_t tile)
+__device__ __forceinline__ Kept<kVec> kept_piece(const DropArgs& d, uint64_t offset, uint32_t row, uint32_t tile);
+template <>
+__device__ __forceinline__ Kept<true> kept_piece<true>(const DropArgs& d, uint64_t offset, uint32_t row, uint32_t tile)
+{
+    return kept_block(d, offset, row, tile / 8 + (threadIdx.x & 31));
+}
+template <>
+__device__ __forceinline__ Kept<false> kept_piece<false>(const DropArgs& d, uint64_t offset, uint32_t row, uint32_t tile)
 {
     const uint32_t lane = threadIdx.x & 31;
-    const uint32_t block = kept_block(d, offset, row, tile / 8 + lane);
-    if (kVec) return block;
-    uint32_t kept = 0;
+    const Kept<true> mine = kept_block(d, offset, row, tile / 8 + lane);
+    uint32_t block = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        kept |= ((__shfl_sync(0xFFFFFFFFu, block, j * 4 + lane / 8) >> (lane % 8)) & 1u) << j;
-    return kept;
+    for (int j = 0; j < 8; ++j) block |= mine[j] ? 1u << j : 0u;
+    Kept<false> k{0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) k.bits |= ((__shfl_sync(0xFFFFFFFFu, block, j * 4 + lane / 8) >> (lane % 8)) & 1u) << j;
+    return k;
+}
+// All stay.
+template <bool kVec>
+__device__ __forceinline__ Kept<kVec> kept_all();
+template <>
+__device__ __forceinline__ Kept<true> kept_all<true>() { return {make_uint4(0, 0, 0, 0), 0}; }
+template <>
+__device__ __forceinline__ Kept<false> kept_all<false>() { return {0xFFu}; }
+
+template <bool kVec>
+__device__ __forceinline__ Eight where_kept(const Kept<kVec>& k, const Eight& a, const Eight& b)
+{
+    Eight o;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = k[j] ? a[j] : b[j];
+    return o;
+}
+template <bool kVec>
+__device__ __forceinline__ Eight where_kept(const Kept<kVec>& k, const Eight& a)
+{
+    return where_kept<kVec>(k, a, all_eight(0.0f));
 }
 
 }  // namespace zccl
