@@ -1,10 +1,11 @@
 // zccl_balance.cu -- how evenly a routing shares its slots out: the balance loss,
 // each expert's slots, and the gradient of the logits.
 //
-// A warp holds a token's logits in registers, expert e in lane e % 32, and adds its
-// scores to sums that it keeps over its tokens.  A sequence's tokens are cut into
-// parts, a CTA each; the last part to arrive adds the parts' sums in their order, and
-// the last sequence the sequences' losses, so results depend on the sizes alone.
+// 8, 16 or 32 lanes hold a token's logits, 8 or 16 each, and keep the sums of their
+// experts' shares over the tokens that come by.  A sequence's tokens are cut into parts
+// of `chunk` tokens, a CTA each; the last part to arrive adds the parts' sums in their
+// order, and the last sequence the sequences' losses, so results depend on the sizes
+// alone.  With very many sequences each is one part.
 #include <cmath>
 
 #include "zccl_ops.cuh"
@@ -13,10 +14,12 @@ namespace zccl {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr uint32_t kMaxParts = 304;  // CTAs of a call with one sequence
-constexpr uint32_t kPartTokens = 32; // at least, for another part
+constexpr int kWarps = 16;
+constexpr uint32_t kFewSequences = 304;  // up to so many are cut into parts
 constexpr uint32_t kCounters = ZCCL_MAX_SEQUENCES + 1;  // the same place for any call, as calls of other sizes may come between
+constexpr int kThreads = kWarps * 32;
+static_assert(kFewSequences < kThreads, "a thread each, and one for where the last ends");
+constexpr float kInf = __builtin_huge_valf();
 
 struct BalanceArgs {
     const void* logits;
@@ -24,7 +27,8 @@ struct BalanceArgs {
     const int32_t* idx;
     uint64_t tokens;
     const int32_t* seq;
-    uint32_t sequences, parts;
+    uint32_t sequences;
+    uint32_t chunk;      // tokens of a part; 0: a sequence is one part
     uint32_t E, K;
     int sigmoid;
     float coefficient;
@@ -34,8 +38,8 @@ struct BalanceArgs {
     // workspace
     uint32_t* arrived;   // [kCounters], 0 between calls: a sequence's parts; last, the sequences
     float* losses;       // [sequences]
-    float* part_scores;  // [sequences][parts][E]
-    int32_t* part_counts;  // [sequences][parts][E + 1]: slots, and last the tokens
+    float* part_scores;    // [parts][E]
+    int32_t* part_counts;  // [parts][E + 1]: slots, and last the tokens
     // backward
     const float* grad_loss;
     void* grad;
@@ -43,77 +47,220 @@ struct BalanceArgs {
     int accumulate;
 };
 
+template <int L>
 __device__ __forceinline__ float lanes_add(float x)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    for (int o = L / 2; o > 0; o /= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
     return x;
 }
 
-// The tokens of a sequence (sequence `sequences`: those behind the last one), whatever
-// the table holds.
-__device__ __forceinline__ void sequence_tokens(const BalanceArgs& a, uint32_t s, uint64_t* lo, uint64_t* hi)
+// A CTA's part: tokens lo..hi-1 of a sequence (`sequences`: the tokens behind the last
+// one) that has `parts` of them, the first of them CTA `first`'s.
+struct Part {
+    uint32_t sequence, first, parts;
+    uint64_t lo, hi;
+};
+
+// Over the CTA: the sum (or the largest) of x of all threads up to this one.
+template <bool kMax>
+__device__ __forceinline__ uint32_t cta_scan(uint32_t x, uint32_t* by_warp)
 {
-    if (a.seq == nullptr) {
-        *lo = s == 0 ? 0 : a.tokens;
-        *hi = a.tokens;
-        return;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if ((int)lane >= o) x = kMax ? max(x, y) : x + y;
     }
-    const int64_t n = (int64_t)a.tokens;
-    int64_t b = ld_l2(a.seq + s), e = s < a.sequences ? ld_l2(a.seq + s + 1) : n;
-    b = b < 0 ? 0 : b > n ? n : b;
-    e = e < b ? b : e > n ? n : e;
-    *lo = (uint64_t)b;
-    *hi = (uint64_t)e;
+    if (lane == 31) by_warp[warp] = x;
+    __syncthreads();
+    uint32_t before = 0;
+    for (uint32_t w = 0; w < warp; ++w) before = kMax ? max(before, by_warp[w]) : before + by_warp[w];
+    __syncthreads();
+    return kMax ? max(x, before) : x + before;
 }
 
-// A row's shares q (softmax, or scores over their sum) and what their slopes multiply.
-template <int J>
-__device__ __forceinline__ void shares(const BalanceArgs& a, const float (&l)[J], float (&q)[J])
+// This CTA's part; false: it has none.  Whatever the table holds, the sequences are
+// taken as runs of 0..tokens-1 one behind the other.  kTail: the tokens behind the last
+// sequence are parts too, and a sequence without tokens is none (else it is one).
+template <bool kTail>
+__device__ __forceinline__ bool part_of(const BalanceArgs& a, Part* p)
+{
+    __shared__ uint32_t begins[kThreads + 1], by_warp[kWarps];
+    __shared__ Part found;
+    const uint32_t id = blockIdx.x, i = threadIdx.x;
+    const auto bound = [&](uint32_t at) -> uint32_t {
+        const int32_t v = ld_l2(a.seq + at);
+        return v < 0 ? 0 : (uint64_t)v > a.tokens ? (uint32_t)a.tokens : (uint32_t)v;
+    };
+    if (a.chunk == 0) {  // a CTA a sequence, and those behind share out the tail
+        const uint32_t s = id < a.sequences ? id : a.sequences;
+        const uint32_t b = bound(s), e = s < a.sequences ? bound(s + 1) : (uint32_t)a.tokens;
+        *p = {s, id, 1, b, e > b ? e : b};
+        if (id >= a.sequences) {
+            const uint64_t n = p->hi - p->lo, k = gridDim.x - a.sequences, j = id - a.sequences;
+            p->hi = p->lo + n * (j + 1) / k;
+            p->lo += n * j / k;
+        }
+        return true;
+    }
+    if (a.seq == nullptr) {
+        const uint32_t all = (uint32_t)((a.tokens + a.chunk - 1) / a.chunk);
+        *p = {0, 0, all > 0 ? all : 1, (uint64_t)id * a.chunk, min((uint64_t)(id + 1) * a.chunk, a.tokens)};
+        return id < p->parts;
+    }
+    begins[i] = cta_scan<true>(i <= a.sequences ? bound(i) : (uint32_t)a.tokens, by_warp);
+    if (i == 0) begins[kThreads] = (uint32_t)a.tokens, found.parts = 0;
+    __syncthreads();
+    const uint32_t n = begins[i + 1] - begins[i], most = kTail ? a.sequences + 1 : a.sequences;
+    uint32_t parts = i < most ? (n + a.chunk - 1) / a.chunk : 0;
+    if (!kTail && i < most && parts == 0) parts = 1;
+    const uint32_t behind = cta_scan<false>(parts, by_warp);
+    if (parts > 0 && id >= behind - parts && id < behind) {
+        const uint64_t lo = begins[i] + (uint64_t)(id - (behind - parts)) * a.chunk;
+        found = {i, behind - parts, parts, lo, min(lo + a.chunk, (uint64_t)begins[i + 1])};
+    }
+    __syncthreads();
+    *p = found;
+    return p->parts > 0;
+}
+
+// A lane's logits of a token, as they are held in memory: with kVec eight neighbours
+// at a time, else L apart.
+template <typename T, bool kVec, int L, int J>
+struct Logits {
+    static constexpr int kWords = kVec ? J * sizeof(T) / 16 : 0;
+    uint4 q[kVec ? kWords : 1];
+    float f[kVec ? 1 : J];
+    static __device__ __forceinline__ uint32_t expert(uint32_t li, int j)
+    {
+        return kVec ? j / 8 * 8 * L + li * 8 + j % 8 : li + L * j;
+    }
+    __device__ __forceinline__ void load(const T* row, uint32_t li, uint32_t E)
+    {
+        if (kVec) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const uint32_t e = expert(li, i * 16 / sizeof(T));
+                q[i] = e < E ? *reinterpret_cast<const uint4*>(row + e) : make_uint4(0, 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < J; ++j) f[j] = expert(li, j) < E ? to_float<T>(row[expert(li, j)]) : 0.0f;
+        }
+    }
+    // -infinity where there is no expert
+    __device__ __forceinline__ void get(float (&l)[J], uint32_t li, uint32_t E) const
+    {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            if (!kVec) {
+                l[j] = f[j];
+            } else {
+                const uint4 v = q[j * sizeof(T) / 16];
+                const uint32_t w = (j * sizeof(T) / 4) % 4, x = w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
+                l[j] = sizeof(T) == 4 ? __uint_as_float(x) : j & 1 ? bf16_hi(x) : bf16_lo(x);
+            }
+            if (expert(li, j) >= E) l[j] = -kInf;
+        }
+    }
+};
+
+template <typename T, bool kVec, int L, int J>
+__device__ __forceinline__ void store_row(T* row, const float (&g)[J], uint32_t li, uint32_t E)
+{
+    using Row = Logits<T, kVec, L, J>;
+    if (kVec) {
+        constexpr int kEach = 16 / sizeof(T);
+#pragma unroll
+        for (int i = 0; i < Row::kWords; ++i) {
+            const uint32_t e = Row::expert(li, i * kEach);
+            const float* v = g + i * kEach;
+            const uint4 q = sizeof(T) == 2
+                                ? make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]))
+                                : make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+            if (e < E) *reinterpret_cast<uint4*>(row + e) = q;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (Row::expert(li, j) < E) row[Row::expert(li, j)] = from_float<T>(g[j]);
+    }
+}
+
+// exp(x) to |x| 2^-23 and two units of the last place, zero below 2^-126, and 1 / x to one unit.
+__device__ __forceinline__ float exp_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504f));
+    return y;
+}
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A row's scores p and the factor that makes them its shares, 0 where it has none; with
+// kSlope also the sigmoid's 1 - p.
+template <bool kSlope, int L, int J>
+__device__ __forceinline__ float scores(const BalanceArgs& a, const float (&l)[J], float (&p)[J], float (&slope)[J])
 {
     float m = l[0];
 #pragma unroll
     for (int j = 1; j < J; ++j) m = fmaxf(m, l[j]);
-    m = warp_max(m);
-    if (m == -__builtin_huge_valf()) m = 0.0f;
+#pragma unroll
+    for (int o = L / 2; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     float total = 0.0f;
     if (a.sigmoid) {
-        // over a common factor, which keeps the largest from underflow
-        const float low = fminf(m, 0.0f);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            q[j] = l[j] >= 0.0f ? 1.0f / (1.0f + expf(-l[j])) : expf(l[j] - low) / (1.0f + expf(l[j]));
-            total += q[j];
+            const float t = exp_fast(-fabsf(l[j])), r = reciprocal(1.0f + t);
+            p[j] = l[j] >= 0.0f ? r : t * r;
+            if (kSlope) slope[j] = l[j] >= 0.0f ? t * r : r;
         }
+        // scores that are all below 2^-86: over a common factor, which keeps the largest from underflow (1 + exp(l) is 1)
+        if (m < -60.0f)
+#pragma unroll
+            for (int j = 0; j < J; ++j) p[j] = m == -kInf ? 0.0f : exp_fast(l[j] - m);
     } else {
+        if (m == -kInf) m = 0.0f;
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            q[j] = expf(l[j] - m);
-            total += q[j];
-        }
+        for (int j = 0; j < J; ++j) p[j] = exp_fast(l[j] - m);
     }
-    total = lanes_add(total);
 #pragma unroll
-    for (int j = 0; j < J; ++j) q[j] = total == 0.0f ? 0.0f : q[j] / total;
+    for (int j = 0; j < J; ++j) total += p[j];
+    total = lanes_add<L>(total);
+    return total == 0.0f ? 0.0f : 1.0f / total;
 }
 
-template <typename T, int J>
-__device__ __forceinline__ void load_row(const BalanceArgs& a, uint64_t t, uint32_t lane, float (&l)[J])
-{
-    const T* row = static_cast<const T*>(a.logits) + t * a.stride;
+// A lane's experts of a token (entries L apart).
+template <int L>
+struct Choices {
+    static constexpr int kEach = ZCCL_MAX_TOP_K / L;
+    int32_t e[kEach];
+    __device__ __forceinline__ void load(const BalanceArgs& a, uint64_t t, bool there, uint32_t li)
+    {
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const uint32_t e = lane + 32 * j;
-        l[j] = e < a.E ? to_float<T>(row[e]) : -__builtin_huge_valf();
+        for (int i = 0; i < kEach; ++i) e[i] = there && li + L * i < a.K ? a.idx[t * a.K + li + L * i] : -1;
     }
-}
-
-// The lane's expert of a token, -1 for none.
-__device__ __forceinline__ int32_t choice(const BalanceArgs& a, uint64_t t, uint32_t lane)
-{
-    const int32_t e = lane < a.K ? a.idx[t * a.K + lane] : -1;
-    return e >= 0 && (uint32_t)e < a.E ? e : -1;
-}
+    // Calls `use` with each of them; whether the token has any.
+    template <typename Use>
+    __device__ __forceinline__ bool each(const BalanceArgs& a, uint32_t li, Use use) const
+    {
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (e[i] >= 0 && (uint32_t)e[i] < a.E) {
+                any = true;
+                use(e[i]);
+            }
+        __syncwarp();
+        const uint32_t lane = threadIdx.x & 31;
+        return (__ballot_sync(0xFFFFFFFFu, any) >> (lane - li) & (0xFFFFFFFFu >> (32 - L))) != 0;
+    }
+};
 
 // Whether this CTA is the last of `n` to come by; what the others wrote before is visible to it then.
 __device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t n)
@@ -125,79 +272,118 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t n)
     return before == n - 1;
 }
 
-template <typename T, int J>
-__global__ void __launch_bounds__(kWarps * 32) balance_kernel(BalanceArgs a)
+template <typename T, bool kVec, int L, int J>
+__global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
 {
-    __shared__ float sums[kWarps][J * 32];
-    __shared__ int32_t slots[J * 32];
+    constexpr int kExperts = L * J, kTokens = 32 / L;
+    __shared__ float sums[kWarps][kExperts];
+    __shared__ int32_t slots[kExperts];
     __shared__ int32_t live_tokens;
     __shared__ float red[kWarps];
-    pdl_wait();
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
-    for (uint32_t e = threadIdx.x; e < J * 32; e += kWarps * 32) slots[e] = 0;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % L;
+    for (uint32_t e = threadIdx.x; e < kExperts; e += kThreads) slots[e] = 0;
     if (threadIdx.x == 0) live_tokens = 0;
     __syncthreads();
-    uint64_t lo, hi;
-    sequence_tokens(a, s, &lo, &hi);
-    const uint64_t n = hi - lo;
-    hi = lo + n * (part + 1) / a.parts;
-    lo = lo + n * part / a.parts;
+    pdl_wait();
+    Part part;
+    if (!part_of<false>(a, &part)) return;
+    const uint32_t s = part.sequence;
+    const uint64_t lo = part.lo, hi = part.hi;
     float sum[J] = {};
     int32_t live = 0;
-    for (uint64_t t = lo + warp; t < hi; t += kWarps) {
-        float l[J], q[J];
-        load_row<T, J>(a, t, lane, l);
-        const int32_t e = choice(a, t, lane);
-        if (__ballot_sync(0xFFFFFFFFu, e >= 0) == 0) continue;
-        ++live;
-        if (e >= 0) atomicAdd(&slots[e], 1);
-        shares<J>(a, l, q);
+    Logits<T, kVec, L, J> row;
+    const T* const logits = static_cast<const T*>(a.logits);
+    const uint64_t t0 = lo + warp * kTokens + lane / L;
+    Choices<L> next;
+    if (t0 < hi) row.load(logits + t0 * a.stride, li, a.E);
+    next.load(a, t0, t0 < hi, li);
+    for (uint64_t t = t0; __any_sync(0xFFFFFFFFu, t < hi); t += kWarps * kTokens) {
+        float l[J], p[J], slope[J];
+        row.get(l, li, a.E);
+        const Choices<L> chosen = next;
+        const uint64_t t1 = t + kWarps * kTokens;
+        if (t1 < hi) row.load(logits + t1 * a.stride, li, a.E);
+        next.load(a, t1, t1 < hi, li);
+        const bool counts = chosen.each(a, li, [&](int32_t e) { atomicAdd(&slots[e], 1); });
+        live += counts && li == 0 ? 1 : 0;
+        if (!__all_sync(0xFFFFFFFFu, counts) && !counts)
 #pragma unroll
-        for (int j = 0; j < J; ++j) sum[j] += q[j];
+            for (int j = 0; j < J; ++j) l[j] = -kInf;  // whatever it holds
+        const float f = scores<false, L, J>(a, l, p, slope);
+#pragma unroll
+        for (int j = 0; j < J; ++j) sum[j] = fmaf(p[j], f, sum[j]);
     }
+    // over the warp's tokens
 #pragma unroll
-    for (int j = 0; j < J; ++j) sums[warp][lane + 32 * j] = sum[j];
+    for (int o = 16; o >= L; o /= 2)
+#pragma unroll
+        for (int j = 0; j < J; ++j) sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], o);
+    if (lane < L)
+#pragma unroll
+        for (int j = 0; j < J; ++j) sums[warp][row.expert(li, j)] = sum[j];
+    live = __reduce_add_sync(0xFFFFFFFFu, live);
     if (lane == 0) atomicAdd(&live_tokens, live);
     __syncthreads();
     // the CTA's sums, then those of the sequence's parts
     float* const all = sums[0];
-    for (uint32_t e = threadIdx.x; e < a.E; e += kWarps * 32) {
+    for (uint32_t e = threadIdx.x; e < a.E; e += kThreads) {
         float x = all[e];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) x += sums[w][e];
         all[e] = x;
     }
-    if (a.parts > 1) {
-        const uint64_t at = (uint64_t)s * a.parts + part;
-        for (uint32_t e = threadIdx.x; e < a.E; e += kWarps * 32) {
+    if (part.parts > 1) {
+        const uint64_t at = blockIdx.x;
+        for (uint32_t e = threadIdx.x; e < a.E; e += kThreads) {
             a.part_scores[at * a.E + e] = all[e];
             a.part_counts[at * (a.E + 1) + e] = slots[e];
         }
         if (threadIdx.x == 0) a.part_counts[at * (a.E + 1) + a.E] = live_tokens;
-        if (!last_of(a.arrived + s, a.parts)) return;
-        const float* scores = a.part_scores + (uint64_t)s * a.parts * a.E;
-        const int32_t* counts = a.part_counts + (uint64_t)s * a.parts * (a.E + 1);
-        for (uint32_t e = threadIdx.x; e <= a.E; e += kWarps * 32) {
-            float x = 0.0f;
-            int32_t c = 0;
-            for (uint32_t p = 0; p < a.parts; ++p) {
-                if (e < a.E) x += scores[(uint64_t)p * a.E + e];
+        if (!last_of(a.arrived + s, part.parts)) return;
+        // the threads take a column each, as many times over as they go into the CTA, and every so many parts
+        const float* scores = a.part_scores + (uint64_t)part.first * a.E;
+        const int32_t* counts = a.part_counts + (uint64_t)part.first * (a.E + 1);
+        constexpr int kSides = kThreads / kExperts > 0 ? kThreads / kExperts : 1;
+        const uint32_t side = threadIdx.x / kExperts, e = threadIdx.x % kExperts;
+        float x = 0.0f;
+        int32_t c = 0;
+        if (e < a.E)
+#pragma unroll 8
+            for (uint32_t p = side; p < part.parts; p += kSides) {
+                x += scores[(uint64_t)p * a.E + e];
                 c += counts[(uint64_t)p * (a.E + 1) + e];
             }
-            if (e < a.E) all[e] = x, slots[e] = c;
-            else live_tokens = c;
+        int32_t m = 0;
+        if (warp == 0)
+            for (uint32_t p = lane; p < part.parts; p += 32) m += counts[(uint64_t)p * (a.E + 1) + a.E];
+        // (the CTA's own sums have been written out; `sums` has room for kSides rows of them and of the counts)
+        static_assert(2 * kSides <= kWarps, "room");
+        sums[side][e] = x;
+        sums[kSides + side][e] = __int_as_float(c);
+        if (warp == 0) {
+            m = __reduce_add_sync(0xFFFFFFFFu, m);
+            if (lane == 0) live_tokens = m;
+        }
+        __syncthreads();
+        if (threadIdx.x < kExperts) {
+            x = sums[0][e];
+            c = __float_as_int(sums[kSides][e]);
+#pragma unroll
+            for (int i = 1; i < kSides; ++i) x += sums[i][e], c += __float_as_int(sums[kSides + i][e]);
+            all[e] = x;
+            slots[e] = c;
         }
         __syncthreads();
     }
     // the sequence's loss
     float dot = 0.0f;
     int32_t used = 0;
-    for (uint32_t e = threadIdx.x; e < a.E; e += kWarps * 32) {
+    for (uint32_t e = threadIdx.x; e < a.E; e += kThreads) {
         dot += (float)slots[e] * all[e];
         used += slots[e];
         a.counts[(uint64_t)s * a.E + e] = slots[e];
     }
-    dot = lanes_add(dot);
+    dot = lanes_add<32>(dot);
     used = __reduce_add_sync(0xFFFFFFFFu, used);
     __shared__ int32_t used_by[kWarps];
     if (lane == 0) red[warp] = dot, used_by[warp] = used;
@@ -211,14 +397,17 @@ __global__ void __launch_bounds__(kWarps * 32) balance_kernel(BalanceArgs a)
         a.live[s] = live_tokens;
     }
     // the call's
-    if (!last_of(a.arrived + kCounters - 1, a.sequences)) return;
+    if (a.sequences == 1)
+        __syncthreads();
+    else if (!last_of(a.arrived + kCounters - 1, a.sequences))
+        return;
     dot = 0.0f;
     int32_t alive = 0;
-    for (uint32_t i = threadIdx.x; i < a.sequences; i += kWarps * 32) {
+    for (uint32_t i = threadIdx.x; i < a.sequences; i += kThreads) {
         dot += a.losses[i];
         alive += a.live[i] > 0 ? 1 : 0;
     }
-    dot = lanes_add(dot);
+    dot = lanes_add<32>(dot);
     alive = __reduce_add_sync(0xFFFFFFFFu, alive);
     if (lane == 0) red[warp] = dot, used_by[warp] = alive;
     __syncthreads();
@@ -232,78 +421,114 @@ __global__ void __launch_bounds__(kWarps * 32) balance_kernel(BalanceArgs a)
     }
 }
 
-template <typename T, int J>
-__global__ void __launch_bounds__(kWarps * 32) balance_backward_kernel(BalanceArgs a)
+template <typename T, bool kVec, int L, int J>
+__global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs a)
 {
+    constexpr int kTokens = 32 / L;
     pdl_wait();
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
-    uint64_t lo, hi;
-    sequence_tokens(a, s, &lo, &hi);
-    const uint64_t n = hi - lo;
-    hi = lo + n * (part + 1) / a.parts;
-    lo = lo + n * part / a.parts;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % L;
+    Part part;
+    if (!part_of<true>(a, &part)) return;
+    const uint32_t s = part.sequence;
+    const uint64_t lo = part.lo, hi = part.hi;
     const bool counted = s < a.sequences;
     if (lo >= hi || (!counted && a.accumulate)) return;
+    Logits<T, kVec, L, J> row;
+    const T* const logits = static_cast<const T*>(a.logits);
+    const uint64_t t0 = lo + warp * kTokens + lane / L;
+    Choices<L> next;
+    if (t0 < hi) row.load(logits + t0 * a.stride, li, a.E);
+    next.load(a, t0, t0 < hi && counted, li);
     // what a unit of an expert's shares adds to the loss
-    float f[J];
+    float f[J] = {};
     if (counted) {
         int32_t c[J], used = 0;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            c[j] = lane + 32 * j < a.E ? a.counts[(uint64_t)s * a.E + lane + 32 * j] : 0;
+            const uint32_t e = row.expert(li, j);
+            c[j] = e < a.E ? a.counts[(uint64_t)s * a.E + e] : 0;
             used += c[j];
         }
-        used = __reduce_add_sync(0xFFFFFFFFu, used);
+#pragma unroll
+        for (int o = L / 2; o > 0; o /= 2) used += __shfl_xor_sync(0xFFFFFFFFu, used, o);
         const float up = a.coefficient * (a.grad_loss != nullptr ? *a.grad_loss : 1.0f);
         const float each = (float)used * (float)a.live[s] * (float)a.live[a.sequences];
         const float unit = each > 0.0f ? up * ((float)a.E / each) : 0.0f;
 #pragma unroll
         for (int j = 0; j < J; ++j) f[j] = unit * (float)c[j];
     }
-    for (uint64_t t = lo + warp; t < hi; t += kWarps) {
-        float l[J], q[J];
-        T* out = static_cast<T*>(a.grad) + t * a.grad_stride;
-        const int32_t e = counted ? choice(a, t, lane) : -1;
-        const bool live = __ballot_sync(0xFFFFFFFFu, e >= 0) != 0;
-        if (!live && a.accumulate) continue;
-        if (live) {
-            load_row<T, J>(a, t, lane, l);
-            shares<J>(a, l, q);
-            float dot = 0.0f;
+    for (uint64_t t = t0; __any_sync(0xFFFFFFFFu, t < hi); t += kWarps * kTokens) {
+        float l[J], g[J], slope[J];
+        row.get(l, li, a.E);
+        const Choices<L> chosen = next;
+        const uint64_t t1 = t + kWarps * kTokens;
+        if (t1 < hi) row.load(logits + t1 * a.stride, li, a.E);
+        next.load(a, t1, t1 < hi && counted, li);
+        const bool there = t < hi, counts = chosen.each(a, li, [](int32_t) {});
+        if (!__all_sync(0xFFFFFFFFu, counts) && !counts)
 #pragma unroll
-            for (int j = 0; j < J; ++j) dot = fmaf(f[j], q[j], dot);
-            dot = lanes_add(dot);
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                q[j] *= f[j] - dot;
-                if (a.sigmoid) q[j] *= 1.0f / (1.0f + expf(l[j]));
-            }
-        }
+            for (int j = 0; j < J; ++j) l[j] = -kInf;  // whatever it holds
+        const float share = scores<true, L, J>(a, l, g, slope);
+        float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const uint32_t x = lane + 32 * j;
-            if (x < a.E) out[x] = from_float<T>((live ? q[j] : 0.0f) + (a.accumulate ? to_float<T>(out[x]) : 0.0f));
+            g[j] *= share;
+            sum = fmaf(f[j], g[j], sum);
         }
+        sum = lanes_add<L>(sum);
+#pragma unroll
+        for (int j = 0; j < J; ++j) g[j] *= a.sigmoid ? slope[j] * (f[j] - sum) : f[j] - sum;
+        if (!there || (a.accumulate && !counts)) continue;
+        T* out = static_cast<T*>(a.grad) + t * a.grad_stride;
+        if (a.accumulate) {
+            Logits<T, kVec, L, J> old;
+            old.load(out, li, a.E);
+            old.get(l, li, a.E);
+#pragma unroll
+            for (int j = 0; j < J; ++j) g[j] += l[j];
+        }
+        store_row<T, kVec, L, J>(out, g, li, a.E);
     }
 }
 
 using BalanceKernel = void (*)(BalanceArgs);
-template <typename T>
+template <typename T, bool kVec>
 BalanceKernel balance_for(uint32_t experts, bool backward)
 {
-    if (experts <= 64) return backward ? balance_backward_kernel<T, 2> : balance_kernel<T, 2>;
-    if (experts <= 128) return backward ? balance_backward_kernel<T, 4> : balance_kernel<T, 4>;
-    if (experts <= 256) return backward ? balance_backward_kernel<T, 8> : balance_kernel<T, 8>;
-    return backward ? balance_backward_kernel<T, 16> : balance_kernel<T, 16>;
+    if (experts <= 64) return backward ? balance_backward_kernel<T, kVec, 8, 8> : balance_kernel<T, kVec, 8, 8>;
+    if (experts <= 128) return backward ? balance_backward_kernel<T, kVec, 16, 8> : balance_kernel<T, kVec, 16, 8>;
+    if (experts <= 256) return backward ? balance_backward_kernel<T, kVec, 32, 8> : balance_kernel<T, kVec, 32, 8>;
+    return backward ? balance_backward_kernel<T, kVec, 32, 16> : balance_kernel<T, kVec, 32, 16>;
+}
+BalanceKernel balance_for(const BalanceArgs& a, int dtype, bool backward)
+{
+    const uint64_t size = dtype == ZCCL_BF16 ? 2 : 4;
+    const auto on_16 = [&](const void* p, uint64_t stride) {
+        return is_aligned(p, 16) && (a.tokens <= 1 || stride * size % 16 == 0);
+    };
+    const bool vec = a.E % 8 == 0 && on_16(a.logits, a.stride) && (!backward || on_16(a.grad, a.grad_stride));
+    if (dtype == ZCCL_BF16) return vec ? balance_for<__nv_bfloat16, true>(a.E, backward) : balance_for<__nv_bfloat16, false>(a.E, backward);
+    return vec ? balance_for<float, true>(a.E, backward) : balance_for<float, false>(a.E, backward);
 }
 
-uint32_t most_parts(uint32_t sequences) { return sequences >= kMaxParts ? 1 : kMaxParts / sequences; }
-
-// Parts of a sequence of average length.
-uint32_t parts_for(uint64_t tokens, uint32_t sequences)
+// Tokens of a part, and the CTAs that there are parts for.  One sequence: as many parts
+// as two a SM hold; several have a part each that is not whole, which is counted in.
+constexpr uint32_t kPartTokens = 64;
+uint64_t most_parts(uint32_t sequences) { return sequences == 1 ? 304 : sequences < 152 ? 304 - sequences : 152; }
+uint32_t chunk_of(uint64_t tokens, uint32_t sequences)
 {
-    const uint64_t parts = tokens / sequences / kPartTokens, most = most_parts(sequences);
-    return (uint32_t)(parts < 1 ? 1 : parts < most ? parts : most);
+    if (sequences > kFewSequences) return 0;
+    const uint64_t most = most_parts(sequences), chunk = (tokens + most - 1) / most;
+    return (uint32_t)(chunk > kPartTokens ? chunk : kPartTokens);
+}
+uint32_t grid_of(uint64_t tokens, uint32_t sequences, uint32_t chunk, bool backward)
+{
+    if (chunk == 0) {
+        const uint64_t tail = (tokens + kPartTokens - 1) / kPartTokens;
+        return sequences + (backward ? (uint32_t)(tail < 1216 ? tail : 1216) : 0);
+    }
+    // each sequence (and the tail) has at most one part that is not whole
+    return (uint32_t)(tokens / chunk) + sequences + 1;
 }
 
 bool balance_config(const zccl_route_t* c, int dtype, uint64_t stride, uint64_t tokens, uint32_t sequences,
@@ -318,7 +543,6 @@ bool balance_config(const zccl_route_t* c, int dtype, uint64_t stride, uint64_t 
     a->tokens = tokens;
     a->seq = d_seq;
     a->sequences = sequences;
-    a->parts = parts_for(tokens, sequences);
     a->E = c->experts;
     a->K = c->top_k;
     a->sigmoid = c->score == ZCCL_SCORE_SIGMOID;
@@ -338,7 +562,7 @@ zccl_status_t zccl_balance_workspace_bytes(uint32_t sequences, uint32_t experts,
 {
     if (bytes == nullptr || sequences == 0 || sequences > ZCCL_MAX_SEQUENCES || experts == 0 || experts > ZCCL_MAX_EXPERTS)
         return ZCCL_ERR_INVALID_ARG;
-    const uint64_t most = most_parts(sequences), parts = most > 1 ? most * sequences : 0;
+    const uint64_t parts = sequences > kFewSequences ? 0 : most_parts(sequences) + sequences + 1;
     *bytes = 4ull * (kCounters + sequences) + 4ull * parts * (2 * experts + 1);
     return ZCCL_OK;
 }
@@ -364,9 +588,10 @@ zccl_status_t zccl_balance(const zccl_route_t* cfg, const void* d_logits, int dt
     a.arrived = static_cast<uint32_t*>(d_ws);
     a.losses = reinterpret_cast<float*>(a.arrived + kCounters);
     a.part_scores = a.losses + sequences;
-    a.part_counts = reinterpret_cast<int32_t*>(a.part_scores + (uint64_t)sequences * a.parts * a.E);
-    return launched(launch_dependent(dtype == ZCCL_BF16 ? balance_for<__nv_bfloat16>(a.E, false) : balance_for<float>(a.E, false),
-                                     sequences * a.parts, kWarps * 32, 0, stream, a));
+    a.chunk = chunk_of(tokens, sequences);
+    const uint32_t grid = grid_of(tokens, sequences, a.chunk, false);
+    a.part_counts = reinterpret_cast<int32_t*>(a.part_scores + (uint64_t)grid * a.E);
+    return launched(launch_dependent(balance_for(a, dtype, false), grid, kThreads, 0, stream, a));
 }
 
 zccl_status_t zccl_balance_backward(const zccl_route_t* cfg, const void* d_logits, int dtype, uint64_t stride,
@@ -392,9 +617,9 @@ zccl_status_t zccl_balance_backward(const zccl_route_t* cfg, const void* d_logit
     a.grad = d_grad_logits;
     a.grad_stride = grad_stride;
     a.accumulate = accumulate != 0;
-    // one more "sequence": the tokens behind the last one
-    return launched(launch_dependent(dtype == ZCCL_BF16 ? balance_for<__nv_bfloat16>(a.E, true) : balance_for<float>(a.E, true),
-                                     (sequences + 1) * a.parts, kWarps * 32, 0, stream, a));
+    a.chunk = chunk_of(tokens, sequences);
+    const uint32_t grid = grid_of(tokens, sequences, a.chunk, true);
+    return launched(launch_dependent(balance_for(a, dtype, true), grid, kThreads, 0, stream, a));
 }
 
 }  // extern "C"
