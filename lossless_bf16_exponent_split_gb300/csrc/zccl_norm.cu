@@ -1,5 +1,5 @@
-// zccl_norm.cu -- the join of a block's output with the residual and the norm of
-// the next block's input, and the host side of both directions.
+// zccl_norm.cu -- the host side of the join of a block's output with the residual and
+// of the norms around it, both directions.
 #include <cmath>
 
 #include "zccl_norm.h"
@@ -7,141 +7,6 @@
 namespace zccl {
 
 namespace {
-
-// A CTA a row, read once for each of its sums: any size.
-template <typename Tx, typename Ty, bool kVec>
-__global__ void __launch_bounds__(kTeamWarps * 32) norm_long_kernel(NormArgs a)
-{
-    __shared__ float red[2 * 32];
-    uint32_t turn = 0;
-    pdl_wait();
-    const uint64_t offset = drop_offset(a.drop);
-    const uint32_t warp = threadIdx.x >> 5, step = blockDim.x / 32 * kTile;
-    for (uint64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
-        const Tx* x = static_cast<const Tx*>(a.x) + t * a.x_stride;
-        const Ty* y = static_cast<const Ty*>(a.y) + t * a.y_stride;
-        Tx* r = static_cast<Tx*>(a.r) + t * a.hidden;
-        float eta = 1.0f;
-        float2 sum = twice(0.0f);
-        if (a.y != nullptr && a.post) {
-            for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
-                const Eight v = load8<Ty, kVec>(y, tile, a.hidden);
-                dot(sum, v, v);
-            }
-            float s[1] = {sum.x + sum.y};
-            cta_sum<1>(s, red, turn);
-            eta = rsqrtf(s[0] * a.inv_hidden + a.eps);
-            sum = twice(0.0f);
-        }
-        for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
-            Eight v = load8<Tx, kVec>(x, tile, a.hidden);
-            if (a.y != nullptr) {
-                const Eight k = mul(join_factors<kVec>(a, t, tile), load_vector<kVec>(a.post_weight, 0, tile, a.hidden));
-                const Eight b = mul(load8<Ty, kVec>(y, tile, a.hidden), eta);
-                v = where_kept<kVec>(join_kept<kVec>(a, offset, t, tile), fma(k, b, v), v);
-                v = store8<Tx, kVec>(r, v, tile, a.hidden);
-            }
-            dot(sum, v, v);
-        }
-        if (a.h == nullptr) continue;
-        float s[1] = {sum.x + sum.y};
-        cta_sum<1>(s, red, turn);
-        const float rho = rsqrtf(s[0] * a.inv_hidden + a.eps);
-        for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
-            const Eight v = mul(load8<Tx, kVec>(a.y != nullptr ? r : x, tile, a.hidden), rho);
-            store8<Ty, kVec>(static_cast<Ty*>(a.h) + t * a.hidden, mul(v, load_vector<kVec>(a.weight, 0, tile, a.hidden)), tile,
-                             a.hidden);
-        }
-    }
-}
-
-// A team a worker: a row is read once and stays in registers, with the next one on its
-// way; weights and the gate stay there too.
-template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces>
-__global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeamWarps * 32, kTeam == kWarpTeam ? 2 : 1)
-    norm_kernel(NormArgs a)
-{
-    __shared__ float red[kTeam == kWarpTeam ? 1 : kTeamRed];
-    uint32_t turn = 0;
-    pdl_wait();
-    const Place at = place<kTeam>();
-    if (kTeam == kWarpTeam && at.worker >= a.workers) return;
-    const uint64_t offset = drop_offset(a.drop);
-    const uint64_t lo = first_row(a.rows, a.workers, at.worker), hi = first_row(a.rows, a.workers, at.worker + 1);
-    const bool join = a.y != nullptr;
-    Piece<Tx, kVec> px[kPieces];
-    Piece<Ty, kVec> py[kPieces] = {};
-    const auto load = [&](uint64_t t) {
-#pragma unroll
-        for (int n = 0; n < kPieces; ++n) {
-            px[n].load(static_cast<const Tx*>(a.x) + t * a.x_stride, at.tile(n), a.hidden);
-            if (join) py[n].load(static_cast<const Ty*>(a.y) + t * a.y_stride, at.tile(n), a.hidden);
-        }
-    };
-    load(lo);
-    Eight w[kPieces], k[kPieces];
-#pragma unroll
-    for (int n = 0; n < kPieces; ++n) w[n] = load_vector<kVec>(a.weight, 0, at.tile(n), a.hidden);
-    uint64_t gate_end = lo;  // where the gate changes
-    for (uint64_t t = lo; t < hi; ++t) {
-        Eight x[kPieces], y[kPieces];
-#pragma unroll
-        for (int n = 0; n < kPieces; ++n) x[n] = px[n].get(), y[n] = py[n].get();
-        if (t + 1 < hi) load(t + 1);
-        if (join) {
-            if (t == gate_end) {
-                // the join's factor of each column, with the weight of the norm after the block
-#pragma unroll
-                for (int n = 0; n < kPieces; ++n)
-                    k[n] = mul(join_factors<kVec>(a, t, at.tile(n)), load_vector<kVec>(a.post_weight, 0, at.tile(n), a.hidden));
-                gate_end = a.gate.p != nullptr ? (t / a.gate_span + 1) * a.gate_span : a.rows;
-            }
-            if (a.post) {
-                float2 sum = twice(0.0f);
-#pragma unroll
-                for (int n = 0; n < kPieces; ++n) dot(sum, y[n], y[n]);
-                float s[1] = {sum.x + sum.y};
-                team_sum<1, kTeam>(s, red, turn);
-                const float eta = rsqrtf(s[0] * a.inv_hidden + a.eps);
-#pragma unroll
-                for (int n = 0; n < kPieces; ++n) y[n] = mul(y[n], eta);
-            }
-#pragma unroll
-            for (int n = 0; n < kPieces; ++n) {
-                x[n] = where_kept<kVec>(join_kept<kVec>(a, offset, t, at.tile(n)), fma(k[n], y[n], x[n]), x[n]);
-                x[n] = store8<Tx, kVec>(static_cast<Tx*>(a.r) + t * a.hidden, x[n], at.tile(n), a.hidden);
-            }
-        }
-        if (a.h == nullptr) continue;
-        float2 sum = twice(0.0f);
-#pragma unroll
-        for (int n = 0; n < kPieces; ++n) dot(sum, x[n], x[n]);
-        float s[1] = {sum.x + sum.y};
-        team_sum<1, kTeam>(s, red, turn);
-        const float rho = rsqrtf(s[0] * a.inv_hidden + a.eps);
-#pragma unroll
-        for (int n = 0; n < kPieces; ++n)
-            store8<Ty, kVec>(static_cast<Ty*>(a.h) + t * a.hidden, mul(mul(x[n], rho), w[n]), at.tile(n), a.hidden);
-    }
-}
-
-using NormKernel = void (*)(NormArgs);
-
-template <typename Tx, typename Ty, bool kVec>
-NormKernel norm_for(const Shape& s)
-{
-    constexpr int kMost = kVec && sizeof(Tx) == 2 && sizeof(Ty) == 2 ? 2 : 1;
-    if (s.team == kWarpTeam) return norm_kernel<Tx, Ty, kVec, kWarpTeam, 1>;
-    if (s.team == kLong) return norm_long_kernel<Tx, Ty, kVec>;
-    if (s.pieces == 1) return s.team == kCtaTeam ? norm_kernel<Tx, Ty, kVec, kCtaTeam, 1> : norm_kernel<Tx, Ty, kVec, kClusterTeam, 1>;
-    return s.team == kCtaTeam ? norm_kernel<Tx, Ty, kVec, kCtaTeam, kMost> : norm_kernel<Tx, Ty, kVec, kClusterTeam, kMost>;
-}
-template <typename Tx>
-NormKernel norm_for(int dtype, bool vec, const Shape& s)
-{
-    if (dtype == ZCCL_BF16) return vec ? norm_for<Tx, __nv_bfloat16, true>(s) : norm_for<Tx, __nv_bfloat16, false>(s);
-    return vec ? norm_for<Tx, float, true>(s) : norm_for<Tx, float, false>(s);
-}
 
 bool dtype_ok(int dtype) { return dtype == ZCCL_BF16 || dtype == ZCCL_F32; }
 uint64_t size_of(int dtype) { return dtype == ZCCL_BF16 ? 2 : 4; }
@@ -184,7 +49,12 @@ zccl_status_t launch_norm(NormArgs& a, int x_dtype, int dtype, bool vec, cudaStr
 {
     const Shape s = norm_shape(a.hidden, a.rows, vec && x_dtype == ZCCL_BF16 && dtype == ZCCL_BF16);
     a.workers = s.workers;
-    const NormKernel kernel = x_dtype == ZCCL_BF16 ? norm_for<__nv_bfloat16>(dtype, vec, s) : norm_for<float>(dtype, vec, s);
+    const bool post = a.post && a.y != nullptr, drop = a.drop.below > 0;
+    const NormKernel kernel = x_dtype == ZCCL_BF16
+                                  ? (dtype == ZCCL_BF16 ? norm_kernel_for<__nv_bfloat16, __nv_bfloat16>(s, vec, post, drop)
+                                                        : norm_kernel_for<__nv_bfloat16, float>(s, vec, post, drop))
+                                  : (dtype == ZCCL_BF16 ? norm_kernel_for<float, __nv_bfloat16>(s, vec, post, drop)
+                                                        : norm_kernel_for<float, float>(s, vec, post, drop));
     return launched(s.team == kClusterTeam ? launch_clusters(kernel, s.grid, s.warps * 32, 0, s.ctas, stream, a)
                                            : launch_dependent(kernel, s.grid, s.warps * 32, 0, stream, a));
 }

@@ -72,20 +72,24 @@ struct Shape {
 };
 
 // 16 warps an SM (128 registers a thread), the SMs taken as 152.  `narrow`: both types
-// have 16 bits and rows begin on 16 bytes, so a warp can hold two tiles: two are better (a row's sums are exchanged
-// by half as many warps) from two tiles on, where they come out even.
+// have 16 bits and rows begin on 16 bytes, so a warp can hold two tiles: two are better
+// (a row's sums are exchanged by half as many warps) from two tiles on, where they come
+// out even.  A CTA alone takes rows of up to 4096 values, then there are two or more of
+// them an SM, which cover one another's waits; clusters cover their own.
 inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow)
 {
     constexpr uint32_t kSms = 152;
     const uint32_t tiles = (uint32_t)((hidden + kTile - 1) / kTile);
     const uint32_t pieces = narrow && (tiles % 2 == 0 || tiles > 8) ? 2 : 1, units = (tiles + pieces - 1) / pieces;
+    // a cluster's CTA holds three rows in shared memory: 15 warps of two 16-bit tiles, or 16 of one tile
+    const uint32_t alone = pieces == 2 ? 8 : 16, most = pieces == 2 ? 15 : 16;
     Shape s{};
     const auto at_most_rows = [&](uint64_t n) { return (uint32_t)(n < rows ? n : rows > 0 ? rows : 1); };
     if (tiles <= 1) {
         s = {kWarpTeam, 1, kWarpsPerCta, 1, at_most_rows(kSms * 16), 0};
         s.grid = (s.workers + kWarpsPerCta - 1) / kWarpsPerCta;
-    } else if (units <= kTeamWarps * kMaxCluster) {
-        s.ctas = units <= kTeamWarps ? 1 : units <= 2 * kTeamWarps ? 2 : 4;
+    } else if (units <= most * kMaxCluster && tiles <= kTeamWarps * kMaxCluster) {
+        s.ctas = units <= alone ? 1 : units <= 2 * most ? 2 : 4;
         s.team = s.ctas > 1 ? kClusterTeam : kCtaTeam;
         s.pieces = pieces;
         s.warps = (units + s.ctas - 1) / s.ctas;
@@ -122,9 +126,18 @@ __device__ __forceinline__ float warp_sums(const float (&s)[N])
     return v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 1);
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
+}
+__device__ __forceinline__ uint32_t cluster_ctas()
+{
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
 }
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -151,8 +164,7 @@ __device__ __forceinline__ Place place()
     const uint32_t warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     if (kTeam == kWarpTeam) return {blockIdx.x * kWarpsPerCta + warp, 0, 0};
     if (kTeam == kCtaTeam) return {blockIdx.x, warp * kTile, warps * kTile};
-    uint32_t ctas;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+    const uint32_t ctas = cluster_ctas();
     cluster_sync();  // the others' shared memory is there
     return {blockIdx.x / ctas, (cluster_rank() * warps + warp) * kTile, ctas * warps * kTile};
 }
@@ -162,37 +174,63 @@ __device__ __forceinline__ Place place()
 // of the row after it only when all have been at the barrier between.
 constexpr uint32_t kTeamRed = 2 * kTeamWarps * kMaxCluster * 8;
 
-// Sums N values (N <= 8) over a team, the same way in every thread.
+// Sums N values (N <= 8) over a team, the same way in every thread, in steps: a warp's
+// own sums (warp_sums), which it puts where all of the team find them, and, behind a
+// barrier, the taking up of all warps'.  The next sums may be put only when these have
+// been waited for: all warps have taken up the ones before then, in whose place they go.
 template <int N, int kTeam>
-__device__ __forceinline__ void team_sum(float (&s)[N], float* red, uint32_t& turn)
-{
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    float v = warp_sums<N>(s);
-    uint32_t each = 4;  // lanes from one value to the next
-    if (kTeam != kWarpTeam) {
+struct TeamSum {
+    float* const red;
+    uint32_t turn = 0;
+    float mine = 0.0f;  // a warp that is a team
+    __device__ __forceinline__ explicit TeamSum(float* red) : red(red) {}
+
+    // v: what warp_sums gave.
+    __device__ __forceinline__ void put(float v)
+    {
+        const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         float* at = red + turn * (kTeamRed / 2);
-        turn ^= 1;
-        uint32_t all = warps;
+        if (kTeam == kWarpTeam) mine = v;
+        if (kTeam == kCtaTeam && (lane & 3) == 0) at[warp * 8 + lane / 4] = v;
         if (kTeam == kClusterTeam) {
-            uint32_t ctas;
-            asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
             // the four lanes that hold a value take a CTA each
-            if ((lane & 3) < ctas && lane / 4 < N) st_cluster(at + (cluster_rank() * warps + warp) * 8 + lane / 4, lane & 3, v);
-            cluster_sync();
-            all = warps * ctas;
-        } else {
-            if ((lane & 3) == 0) at[warp * 8 + lane / 4] = v;
-            __syncthreads();
+            if ((lane & 3) < cluster_ctas() && lane / 4 < N)
+                st_cluster(at + (cluster_rank() * (blockDim.x >> 5) + warp) * 8 + lane / 4, lane & 3, v);
+            __syncwarp();
+            cluster_arrive();
         }
-        v = 0.0f;
-        for (uint32_t w = lane / 8; w < all; w += 4) v += (lane & 7) < N ? at[w * 8 + (lane & 7)] : 0.0f;
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
-        v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
-        each = 1;
+        turn ^= 1;
     }
+    __device__ __forceinline__ void wait()
+    {
+        if (kTeam == kCtaTeam) __syncthreads();
+        if (kTeam == kClusterTeam) cluster_wait();
+    }
+    __device__ __forceinline__ void take(float (&s)[N])
+    {
+        const uint32_t lane = threadIdx.x & 31;
+        float v = mine;
+        if (kTeam != kWarpTeam) {
+            const float* at = red + (turn ^ 1) * (kTeamRed / 2) + (lane & 7);
+            const uint32_t all = (blockDim.x >> 5) * (kTeam == kClusterTeam ? cluster_ctas() : 1);
+            v = 0.0f;
+            if ((lane & 7) < N)
+#pragma unroll 4
+                for (uint32_t w = lane / 8; w < all; w += 4) v += at[w * 8];
+            __syncwarp();
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+        }
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = __shfl_sync(0xFFFFFFFFu, v, i * each);
-}
+        for (int i = 0; i < N; ++i) s[i] = __shfl_sync(0xFFFFFFFFu, v, kTeam == kWarpTeam ? i * 4 : i);
+    }
+    __device__ __forceinline__ void operator()(float (&s)[N])
+    {
+        put(warp_sums<N>(s));
+        wait();
+        take(s);
+    }
+};
 
 // Sums N values over a CTA, the same way in every thread; `red` holds
 // 2 * 32 * N floats, whose halves take turns by `turn`.
@@ -238,6 +276,13 @@ __device__ __forceinline__ Kept<kVec> join_kept(const NormArgs& a, uint64_t offs
 {
     return a.drop.below > 0 ? kept_piece<kVec>(a.drop, offset, (uint32_t)row, tile) : kept_all<kVec>();
 }
+
+using NormKernel = void (*)(NormArgs);
+// The kernels of a pair of types; thread_bytes: shared memory of a thread.
+template <typename Tx, typename Ty>
+NormKernel norm_kernel_for(const Shape& s, bool vec, bool post, bool drop);
+template <typename Tx, typename Ty>
+NormKernel norm_backward_kernel_for(const Shape& s, bool vec, bool post, bool drop, uint32_t* thread_bytes);
 
 zccl_status_t launch_norm(NormArgs& a, int x_dtype, int dtype, bool vec, cudaStream_t stream);
 zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weight_dtype, bool vec, cudaStream_t stream);

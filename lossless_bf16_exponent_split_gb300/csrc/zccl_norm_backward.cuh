@@ -1,0 +1,510 @@
+// zccl_norm_backward.cuh -- gradients of the join of a block's output with the
+// residual and of the norms around it.
+//
+// With a row's rho = rsqrt(mean r^2 + eps), eta = rsqrt(mean y^2 + eps), k = the
+// join's factor (0 where dropped), w and p the two weights:
+//   d    = dr + rho (dh w - r c),     c  = rho^2 mean(dh w r)      the gradient of x
+//   dy   = eta (k d p - y c'),        c' = eta^2 mean(k d p y)     (k d without post)
+//   dw  += dh r rho, dp += k d y eta, dgate += (k / gate) d N(y)
+// c' needs d, but its sum is that of three others, mean(k d p y) = mean(k p y dr) +
+// rho (mean(k p y dh w) - c mean(k p y r)): all six sums of a row are taken at once.
+#pragma once
+
+#include "zccl_norm.h"
+
+namespace zccl {
+
+namespace {
+
+constexpr int kSums = 6;  // r^2, dh w r, y^2, and k p y times dr, dh w and r
+
+struct RowFactors {
+    float rho, c, eta, cy;
+};
+__device__ __forceinline__ RowFactors row_factors(const NormArgs& a, bool post, const float (&s)[kSums])
+{
+    RowFactors f{0.0f, 0.0f, 1.0f, 0.0f};
+    // without dh (which reads as zero, as r does then) nothing is multiplied by these
+    f.rho = rsqrtf(s[0] * a.inv_hidden + a.eps);
+    f.c = s[1] * a.inv_hidden * f.rho * f.rho;
+    if (post) {
+        f.eta = rsqrtf(s[2] * a.inv_hidden + a.eps);
+        f.cy = (s[3] + f.rho * (s[4] - f.c * s[5])) * a.inv_hidden * f.eta * f.eta;
+    }
+    return f;
+}
+
+// The pieces' part of a row's sums; kp: the join's factor times p, 0 where dropped.
+__device__ __forceinline__ void add_sums(float2 (&s)[kSums], bool post, const Eight& r, const Eight& hw, const Eight& up,
+                                         const Eight& y, const Eight& kp)
+{
+    dot(s[0], r, r);
+    dot(s[1], hw, r);
+    if (post) {
+        const Eight q = mul(kp, y);
+        dot(s[2], y, y);
+        dot(s[3], q, up);
+        dot(s[4], q, hw);
+        dot(s[5], q, r);
+    }
+}
+
+// The gradient that the join sees: d = dr + rho (dh w - r c).
+__device__ __forceinline__ Eight joined(const RowFactors& f, const Eight& r, const Eight& hw, const Eight& up)
+{
+    return fma(hw, f.rho, fma(r, -f.rho * f.c, up));
+}
+
+// y's gradient.
+__device__ __forceinline__ Eight branch(bool post, const RowFactors& f, const Eight& d, const Eight& y, const Eight& kp)
+{
+    const Eight u = mul(kp, d);
+    return post ? fma(u, f.eta, mul(y, -f.eta * f.cy)) : u;
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ Eight load_or_zero(const void* p, uint64_t first, uint32_t tile, uint32_t hidden)
+{
+    return p != nullptr ? load8<T, kVec>(static_cast<const T*>(p) + first, tile, hidden) : all_eight(0.0f);
+}
+
+template <bool kVec>
+__device__ __forceinline__ Eight add_to(float* p, const Eight& v, bool first, uint32_t tile, uint32_t hidden)
+{
+    return store8<float, kVec>(p, first ? v : fma(v, 1.0f, load8<float, kVec>(p, tile, hidden)), tile, hidden);
+}
+
+// Writes a gate row's gradient, of its own type.
+template <bool kVec>
+__device__ __forceinline__ void store_gate(const NormArgs& a, uint64_t gate_row, const Eight& v, uint32_t tile)
+{
+    if (a.gate.dtype == ZCCL_BF16)
+        store8<__nv_bfloat16, kVec>(static_cast<__nv_bfloat16*>(a.grad_gate) + gate_row * a.hidden, v, tile, a.hidden);
+    else
+        store8<float, kVec>(static_cast<float*>(a.grad_gate) + gate_row * a.hidden, v, tile, a.hidden);
+}
+
+// A CTA a worker; its rows are read once for the sums and once for the gradients, and
+// the sums over rows stay in the workspace: any size.
+template <typename Tx, typename Ty, bool kVec>
+__global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(NormArgs a)
+{
+    __shared__ float red[2 * 32 * kSums];
+    uint32_t turn = 0;
+    pdl_wait();
+    const uint64_t offset = drop_offset(a.drop);
+    const uint32_t warp = threadIdx.x >> 5, step = blockDim.x / 32 * kTile, wk = blockIdx.x;
+    const uint64_t lo = first_row(a.rows, a.workers, wk), hi = first_row(a.rows, a.workers, wk + 1);
+    const uint64_t pitch = (a.hidden + 7) / 8 * 8;
+    float* sums = a.sums + wk * kWeightSlots * pitch;
+    float* parts = a.parts + wk * kGateSlots * pitch;
+    const bool join = a.grad_y != nullptr;
+    for (uint64_t t = lo; t < hi; ++t) {
+        const uint64_t gate_row = t / a.gate_span;
+        float2 sum[kSums] = {};
+        for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
+            const Eight r = load_or_zero<Tx, kVec>(a.x, t * a.x_stride, tile, a.hidden);
+            const Eight hw = mul(load_or_zero<Ty, kVec>(a.grad_h, t * a.grad_h_stride, tile, a.hidden),
+                                 load_vector<kVec>(a.weight, 0, tile, a.hidden));
+            const Eight up = load_or_zero<Tx, kVec>(a.grad_r, t * a.grad_r_stride, tile, a.hidden);
+            Eight y = all_eight(0.0f), kp = y;
+            if (a.post) {
+                y = load_or_zero<Ty, kVec>(a.y, t * a.y_stride, tile, a.hidden);
+                kp = mul(join_factors<kVec>(a, t, tile), load_vector<kVec>(a.post_weight, 0, tile, a.hidden));
+                kp = where_kept<kVec>(join_kept<kVec>(a, offset, t, tile), kp);
+            }
+            add_sums(sum, a.post, r, hw, up, y, kp);
+        }
+        float s[kSums];
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) s[i] = sum[i].x + sum[i].y;
+        cta_sum<kSums>(s, red, turn);
+        const RowFactors f = row_factors(a, a.post, s);
+        for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
+            const Eight r = load_or_zero<Tx, kVec>(a.x, t * a.x_stride, tile, a.hidden);
+            const Eight dh = load_or_zero<Ty, kVec>(a.grad_h, t * a.grad_h_stride, tile, a.hidden);
+            const Eight up = load_or_zero<Tx, kVec>(a.grad_r, t * a.grad_r_stride, tile, a.hidden);
+            const Eight d = joined(f, r, mul(dh, load_vector<kVec>(a.weight, 0, tile, a.hidden)), up);
+            if (a.grad_x != nullptr) store8<Tx, kVec>(static_cast<Tx*>(a.grad_x) + t * a.hidden, d, tile, a.hidden);
+            if (a.grad_weight != nullptr)
+                add_to<kVec>(sums + kSlotWeight * pitch, mul(dh, mul(r, f.rho)), t == lo, tile, a.hidden);
+            if (!join) continue;
+            const Eight y = load_or_zero<Ty, kVec>(a.y, t * a.y_stride, tile, a.hidden);
+            const Eight k = join_factors<kVec>(a, t, tile), p = load_vector<kVec>(a.post_weight, 0, tile, a.hidden);
+            const Kept<kVec> kept = join_kept<kVec>(a, offset, t, tile);
+            const Eight e = where_kept<kVec>(kept, mul(d, mul(y, f.eta)));
+            if (a.grad_gate != nullptr) {
+                const Eight v = mul(e, mul(p, a.factor));
+                const uint64_t begin = gate_row * a.gate_span, end = begin + a.gate_span;
+                Eight all = v;
+                if (a.gate_span > 1)
+                    all = add_to<kVec>(parts + (begin < lo ? kSlotBefore : kSlotBehind) * pitch, v, t == lo || t == begin, tile, a.hidden);
+                if (begin >= lo && (t + 1 == end || t + 1 == a.rows)) store_gate<kVec>(a, gate_row, all, tile);
+            }
+            if (a.grad_post_weight != nullptr) add_to<kVec>(sums + kSlotPost * pitch, mul(e, k), t == lo, tile, a.hidden);
+            store8<Ty, kVec>(static_cast<Ty*>(a.grad_y) + t * a.hidden, branch(a.post, f, d, y, where_kept<kVec>(kept, mul(k, p))), tile,
+                             a.hidden);
+        }
+    }
+}
+
+// A worker's rows on their way: r, dr, dh and y of the row at hand and of those behind
+// it.  What the call does not have reads as zero.
+template <typename Tx, typename Ty, bool kVec, int kPieces, int kStages>
+struct Feed;
+
+// Where the rows that are asked for next are.
+template <typename Tx, typename Ty>
+struct RowsAt {
+    const Tx* r;
+    const Tx* up;
+    const Ty* dh;
+    const Ty* y;
+    __device__ __forceinline__ RowsAt(const NormArgs& a, uint64_t t)
+        : r(static_cast<const Tx*>(a.x)), up(static_cast<const Tx*>(a.grad_r)), dh(static_cast<const Ty*>(a.grad_h)),
+          y(static_cast<const Ty*>(a.y))
+    {
+        if (r != nullptr) r += t * a.x_stride;
+        if (up != nullptr) up += t * a.grad_r_stride;
+        if (dh != nullptr) dh += t * a.grad_h_stride;
+        if (y != nullptr) y += t * a.y_stride;
+    }
+    __device__ __forceinline__ void next(const NormArgs& a)
+    {
+        if (r != nullptr) r += a.x_stride;
+        if (up != nullptr) up += a.grad_r_stride;
+        if (dh != nullptr) dh += a.grad_h_stride;
+        if (y != nullptr) y += a.y_stride;
+    }
+};
+
+// Rows on 16 bytes come by asynchronous copies into places of the thread's own, so that
+// no thread waits for another's and no registers are held.
+__device__ __forceinline__ void copy_16(uint4* to, const void* from, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+template <typename Tx, typename Ty, int kPieces, int kStages>
+struct Feed<Tx, Ty, true, kPieces, kStages> {
+    static constexpr int kX = sizeof(Tx) / 2, kY = sizeof(Ty) / 2, kAll = 2 * kX + 2 * kY;  // 16-byte parts of a piece
+    static constexpr uint32_t kThreadBytes = kStages * kPieces * kAll * 16;
+    uint4* const mine;
+    uint32_t asked = 0;  // the stage that the next row goes to
+    RowsAt<Tx, Ty> from;
+    __device__ __forceinline__ uint4* at(uint32_t stage, int n, int part) const
+    {
+        return mine + ((stage * kPieces + n) * kAll + part) * blockDim.x;
+    }
+    __device__ __forceinline__ Feed(uint4* smem, const NormArgs& a, uint64_t t) : mine(smem + threadIdx.x), from(a, t)
+    {
+        for (int i = 0; i < kStages * kPieces * kAll; ++i) mine[i * blockDim.x] = make_uint4(0, 0, 0, 0);
+    }
+    template <typename T>
+    __device__ __forceinline__ void copy(const T* row, int n, int part, uint32_t tile, uint32_t hidden)
+    {
+        if (row == nullptr) return;
+        const uint32_t c = column<true>(tile, 0);
+        const T* p = row + (c < hidden ? c : 0);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) copy_16(at(asked, n, part + i), p + 4 * i, c < hidden);
+    }
+    // Asks for the next row (there: it is one of the worker's).
+    __device__ __forceinline__ void ask(const NormArgs& a, const Place& place, bool there)
+    {
+        if (there) {
+#pragma unroll
+            for (int n = 0; n < kPieces; ++n) {
+                copy<Tx>(from.r, n, 0, place.tile(n), a.hidden);
+                copy<Tx>(from.up, n, kX, place.tile(n), a.hidden);
+                copy<Ty>(from.dh, n, 2 * kX, place.tile(n), a.hidden);
+                copy<Ty>(from.y, n, 2 * kX + kY, place.tile(n), a.hidden);
+            }
+            from.next(a);
+        }
+        asked = asked + 1 == kStages ? 0 : asked + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // Until all but the last kLater rows that were asked for are there.
+    template <int kLater>
+    __device__ __forceinline__ void wait()
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kLater) : "memory");
+    }
+    template <typename T>
+    __device__ __forceinline__ Eight read(uint32_t stage, int n, int part) const
+    {
+        if (sizeof(T) == 2) return widen(*at(stage, n, part));
+        const float4 x = *reinterpret_cast<const float4*>(at(stage, n, part)), y = *reinterpret_cast<const float4*>(at(stage, n, part + 1));
+        return {{make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)}};
+    }
+    struct Row {
+        const Feed* f;
+        uint32_t stage;
+        __device__ __forceinline__ Eight r(int n) const { return f->template read<Tx>(stage, n, 0); }
+        __device__ __forceinline__ Eight up(int n) const { return f->template read<Tx>(stage, n, kX); }
+        __device__ __forceinline__ Eight dh(int n) const { return f->template read<Ty>(stage, n, 2 * kX); }
+        __device__ __forceinline__ Eight y(int n) const { return f->template read<Ty>(stage, n, 2 * kX + kY); }
+    };
+    // The row that was asked for before the last `later` ones.
+    __device__ __forceinline__ Row row(uint32_t later) const
+    {
+        const uint32_t stage = asked + kStages - 1 - later;
+        return {this, stage >= kStages ? stage - kStages : stage};
+    }
+};
+
+// Others by loads of single values into registers: one row, and the one that is read.
+template <typename Tx, typename Ty, int kPieces, int kStages>
+struct Feed<Tx, Ty, false, kPieces, kStages> {
+    static constexpr uint32_t kThreadBytes = 0;
+    struct Row {
+        Piece<Tx, false> pr[kPieces], pu[kPieces];
+        Piece<Ty, false> ph[kPieces], py[kPieces];
+        __device__ __forceinline__ Eight r(int n) const { return pr[n].get(); }
+        __device__ __forceinline__ Eight up(int n) const { return pu[n].get(); }
+        __device__ __forceinline__ Eight dh(int n) const { return ph[n].get(); }
+        __device__ __forceinline__ Eight y(int n) const { return py[n].get(); }
+    };
+    Row next;
+    RowsAt<Tx, Ty> from;
+    __device__ __forceinline__ Feed(uint4*, const NormArgs& a, uint64_t t) : next{}, from(a, t) {}
+    __device__ __forceinline__ void ask(const NormArgs& a, const Place& place, bool there)
+    {
+        if (!there) return;
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+            if (from.r != nullptr) next.pr[n].load(from.r, place.tile(n), a.hidden);
+            if (from.up != nullptr) next.pu[n].load(from.up, place.tile(n), a.hidden);
+            if (from.dh != nullptr) next.ph[n].load(from.dh, place.tile(n), a.hidden);
+            if (from.y != nullptr) next.py[n].load(from.y, place.tile(n), a.hidden);
+        }
+        from.next(a);
+    }
+    template <int kLater>
+    __device__ __forceinline__ void wait()
+    {
+    }
+    __device__ __forceinline__ Row row(uint32_t) const { return next; }
+};
+
+// A team a worker; the sums over rows stay in registers.  While a gate stays the same
+// the sums of p's and of the gate's gradient are the same up to a factor of each column,
+//   e = sum of (kept) d y eta:   dp += scale gate e,   dgate = scale p e
+// so one sum serves both, and is taken out when the gate changes.  A cluster's barrier
+// takes longer than a row's arithmetic, so a cluster sums the next row (kAhead) before it
+// waits for this one's sums.  kKind: as in the forward kernel.
+constexpr int kAny = 4;
+template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces, int kKind>
+__global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeamWarps * 32, kTeam == kWarpTeam ? 2 : 1)
+    norm_backward_kernel(NormArgs a)
+{
+    extern __shared__ uint4 smem[];
+    constexpr bool kAhead = kTeam == kClusterTeam && kVec;
+    constexpr int kTeamSums = kKind == kAny || (kKind & 1) ? kSums : 2;
+    using Rows = Feed<Tx, Ty, kVec, kPieces, kAhead ? 3 : 2>;
+    // a thread's sums of p's gradient (two 16-byte parts a piece), and the teams' sums
+    float4* const dp = reinterpret_cast<float4*>(smem) + Rows::kThreadBytes / 16 * blockDim.x + threadIdx.x;
+    TeamSum<kTeamSums, kTeam> team_sum(reinterpret_cast<float*>(smem) + (Rows::kThreadBytes + 32 * kPieces) / 4 * blockDim.x);
+    pdl_wait();
+    const Place at = place<kTeam>();
+    const bool join = a.grad_y != nullptr, reads_y = a.y != nullptr;
+    const bool post = kKind == kAny ? a.post != 0 : (kKind & 1) != 0, drop = kKind == kAny ? a.drop.below > 0 && join : (kKind & 2) != 0;
+    const uint64_t offset = drop ? drop_offset(a.drop) : 0;
+    const uint64_t lo = at.worker < a.workers ? first_row(a.rows, a.workers, at.worker) : 0;
+    const uint64_t hi = at.worker < a.workers ? first_row(a.rows, a.workers, at.worker + 1) : 0;
+    const uint64_t pitch = (a.hidden + 7) / 8 * 8;
+    const auto put_dp = [&](int n, const Eight& v) {
+        dp[(2 * n) * blockDim.x] = make_float4(v[0], v[1], v[2], v[3]);
+        dp[(2 * n + 1) * blockDim.x] = make_float4(v[4], v[5], v[6], v[7]);
+    };
+    const auto get_dp = [&](int n, int warps) -> Eight {
+        const float4 x = dp[(2 * n) * blockDim.x + 32 * warps], y = dp[(2 * n + 1) * blockDim.x + 32 * warps];
+        return {{make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)}};
+    };
+    Rows rows(smem, a, lo);
+    rows.ask(a, at, lo < hi);
+    Eight w[kPieces], kp[kPieces], dw[kPieces], e[kPieces];
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) {
+        w[n] = load_vector<kVec>(a.weight, 0, at.tile(n), a.hidden);
+        kp[n] = dw[n] = e[n] = all_eight(0.0f);
+        put_dp(n, e[n]);
+    }
+    Tx* gx_at = static_cast<Tx*>(a.grad_x) + (a.grad_x != nullptr ? lo * a.hidden : 0);
+    Ty* gy_at = static_cast<Ty*>(a.grad_y) + (join ? lo * a.hidden : 0);
+    // the gate row that e belongs to, and where it ends
+    uint64_t gate_row = lo / a.gate_span, gate_end = a.gate.p != nullptr ? (gate_row + 1) * a.gate_span : a.rows;
+    const auto set_gate = [&](uint64_t t) {
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n)
+            kp[n] = mul(join_factors<kVec>(a, t, at.tile(n)), load_vector<kVec>(a.post_weight, 0, at.tile(n), a.hidden));
+    };
+    const auto take_out = [&](uint64_t t) {
+        const uint64_t begin = gate_row * a.gate_span;
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+            const uint32_t tile = at.tile(n);
+            if (a.grad_post_weight != nullptr) put_dp(n, fma(e[n], join_factors<kVec>(a, begin, tile), get_dp(n, 0)));
+            if (a.grad_gate == nullptr) continue;
+            const Eight v = mul(e[n], mul(load_vector<kVec>(a.post_weight, 0, tile, a.hidden), a.factor));
+            if (begin >= lo && (t == begin + a.gate_span || t == a.rows))
+                store_gate<kVec>(a, gate_row, v, tile);
+            else
+                store8<float, kVec>(a.parts + ((uint64_t)at.worker * kGateSlots + (begin < lo ? kSlotBefore : kSlotBehind)) * pitch, v,
+                                    tile, a.hidden);
+        }
+    };
+    // the factors of row t's gate, 0 where dropped
+    const auto masked = [&](uint64_t t, int n, const Kept<kVec>& kept) -> Eight { return drop ? where_kept<kVec>(kept, kp[n]) : kp[n]; };
+    const auto kept_of = [&](uint64_t t, int n) -> Kept<kVec> {
+        return drop ? kept_piece<kVec>(a.drop, offset, (uint32_t)t, at.tile(n)) : kept_all<kVec>();
+    };
+    // a row's own sums
+    const auto sums_of = [&](const typename Rows::Row& row, uint64_t t, const Kept<kVec> (&kept)[kPieces]) -> float {
+        float2 sum[kSums] = {};
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n)
+            add_sums(sum, post, row.r(n), mul(row.dh(n), w[n]), row.up(n), row.y(n), post ? masked(t, n, kept[n]) : kp[n]);
+        float s[kTeamSums];
+#pragma unroll
+        for (int i = 0; i < kTeamSums; ++i) s[i] = sum[i].x + sum[i].y;
+        return warp_sums<kTeamSums>(s);
+    };
+    const auto factors = [&]() -> RowFactors {
+        float s[kSums] = {}, got[kTeamSums];
+        team_sum.take(got);
+#pragma unroll
+        for (int i = 0; i < kTeamSums; ++i) s[i] = got[i];
+        return row_factors(a, post, s);
+    };
+    // a row's gradients and its part of the sums over rows
+    const auto gradients = [&](const typename Rows::Row& row, uint64_t t, const RowFactors& f, const Kept<kVec> (&kept)[kPieces]) {
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+            const uint32_t tile = at.tile(n);
+            const Eight r = row.r(n), dh = row.dh(n), d = joined(f, r, mul(dh, w[n]), row.up(n));
+            dw[n] = fma(dh, mul(r, f.rho), dw[n]);
+            if (a.grad_x != nullptr) store8<Tx, kVec>(gx_at, d, tile, a.hidden);
+            if (!join) continue;
+            Eight y = all_eight(0.0f);
+            if (reads_y) {
+                y = row.y(n);
+                e[n] = fma(d, mul(drop ? where_kept<kVec>(kept[n], y) : y, f.eta), e[n]);
+            }
+            store8<Ty, kVec>(gy_at, branch(post, f, d, y, masked(t, n, kept[n])), tile, a.hidden);
+        }
+        gx_at += a.hidden;
+        gy_at += a.hidden;
+        if (t + 1 == gate_end && join && t + 1 < hi) {
+            if (reads_y) take_out(t + 1);
+            ++gate_row;
+            gate_end += a.gate_span;
+#pragma unroll
+            for (int n = 0; n < kPieces; ++n) e[n] = all_eight(0.0f);
+        }
+    };
+    if (kAhead) {
+        // sums of a row use its gate's factors before the row before it is done with its own: those are had again then
+        Kept<kVec> kept[kPieces], after[kPieces];
+        rows.ask(a, at, lo + 1 < hi);
+        if (lo < hi) {
+            if (join) set_gate(lo);
+            rows.template wait<1>();
+#pragma unroll
+            for (int n = 0; n < kPieces; ++n) kept[n] = kept_of(lo, n);
+            team_sum.put(sums_of(rows.row(1), lo, kept));
+        }
+        for (uint64_t t = lo; t < hi; ++t) {
+            rows.ask(a, at, t + 2 < hi);  // into the stage of row t - 1
+            const bool more = t + 1 < hi, turns = more && join && t + 1 == gate_end;
+            float s = 0.0f;
+            if (more) {
+                rows.template wait<1>();
+                if (turns) set_gate(t + 1);
+#pragma unroll
+                for (int n = 0; n < kPieces; ++n) after[n] = kept_of(t + 1, n);
+                s = sums_of(rows.row(1), t + 1, after);
+                if (turns) set_gate(t);
+            }
+            team_sum.wait();
+            const RowFactors f = factors();
+            if (more) team_sum.put(s);
+            gradients(rows.row(2), t, f, kept);
+            if (turns) set_gate(t + 1);
+#pragma unroll
+            for (int n = 0; n < kPieces; ++n) kept[n] = after[n];
+        }
+    } else {
+        if (join && lo < hi) set_gate(lo);
+        for (uint64_t t = lo; t < hi; ++t) {
+            rows.template wait<0>();
+            const bool turns = join && t + 1 == gate_end && t + 1 < hi;
+            const auto row = rows.row(0);
+            rows.ask(a, at, t + 1 < hi);
+            Kept<kVec> kept[kPieces];
+#pragma unroll
+            for (int n = 0; n < kPieces; ++n) kept[n] = kept_of(t, n);
+            team_sum.put(sums_of(row, t, kept));
+            team_sum.wait();
+            gradients(row, t, factors(), kept);
+            if (turns) set_gate(t + 1);
+        }
+    }
+    if (reads_y && lo < hi) take_out(hi);
+    pdl_launch_dependents();
+    // the weights' sums, of a CTA's warps where each is a team
+    uint64_t group = at.worker;
+    if (kTeam == kWarpTeam) {
+        group = blockIdx.x;
+        __syncthreads();
+        Eight all = all_eight(0.0f);
+        if (threadIdx.x < 32)
+            for (uint32_t i = 0; i < kWarpsPerCta; ++i) all = fma(get_dp(0, i), 1.0f, all);
+        __syncthreads();
+        put_dp(0, dw[0]);
+        __syncthreads();
+        if (threadIdx.x >= 32) return;
+        dw[0] = all_eight(0.0f);
+        for (uint32_t i = 0; i < kWarpsPerCta; ++i) dw[0] = fma(get_dp(0, i), 1.0f, dw[0]);
+        put_dp(0, all);
+    }
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) {
+        float* sums = a.sums + group * kWeightSlots * pitch;
+        if (a.grad_weight != nullptr) store8<float, kVec>(sums + kSlotWeight * pitch, dw[n], at.tile(n), a.hidden);
+        if (a.grad_post_weight != nullptr) store8<float, kVec>(sums + kSlotPost * pitch, get_dp(n, 0), at.tile(n), a.hidden);
+    }
+}
+
+template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces>
+NormKernel backward_kind(bool post, bool drop, uint32_t* thread_bytes)
+{
+    *thread_bytes = Feed<Tx, Ty, kVec, kPieces, kVec && kTeam == kClusterTeam ? 3 : 2>::kThreadBytes + 32 * kPieces;
+    if constexpr (kVec)
+        return post ? (drop ? norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 3> : norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 1>)
+                    : (drop ? norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 2> : norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 0>);
+    else
+        return norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, kAny>;
+}
+template <typename Tx, typename Ty, bool kVec>
+NormKernel backward_for(const Shape& s, bool post, bool drop, uint32_t* thread_bytes)
+{
+    constexpr int kMost = kVec && sizeof(Tx) == 2 && sizeof(Ty) == 2 ? 2 : 1;
+    if (s.team == kWarpTeam) return backward_kind<Tx, Ty, kVec, kWarpTeam, 1>(post, drop, thread_bytes);
+    if (s.team == kLong) return norm_backward_long_kernel<Tx, Ty, kVec>;
+    if (s.team == kCtaTeam)
+        return s.pieces == 1 ? backward_kind<Tx, Ty, kVec, kCtaTeam, 1>(post, drop, thread_bytes)
+                             : backward_kind<Tx, Ty, kVec, kCtaTeam, kMost>(post, drop, thread_bytes);
+    return s.pieces == 1 ? backward_kind<Tx, Ty, kVec, kClusterTeam, 1>(post, drop, thread_bytes)
+                         : backward_kind<Tx, Ty, kVec, kClusterTeam, kMost>(post, drop, thread_bytes);
+}
+
+}  // namespace
+
+template <typename Tx, typename Ty>
+NormKernel norm_backward_kernel_for(const Shape& s, bool vec, bool post, bool drop, uint32_t* thread_bytes)
+{
+    return vec ? backward_for<Tx, Ty, true>(s, post, drop, thread_bytes) : backward_for<Tx, Ty, false>(s, post, drop, thread_bytes);
+}
+
+}  // namespace zccl

@@ -1,0 +1,6 @@
+// zccl_norm_bf16_bf16.cu -- the forward norm kernels of a residual and a block of these types.
+#include "zccl_norm_forward.cuh"
+
+namespace zccl {
+template NormKernel norm_kernel_for<__nv_bfloat16, __nv_bfloat16>(const Shape&, bool, bool, bool);
+}  // namespace zccl

@@ -1,0 +1,169 @@
+// zccl_norm_forward.cuh -- the join of a block's output with the residual and the norm
+// of the next block's input.
+#pragma once
+
+#include "zccl_norm.h"
+
+namespace zccl {
+
+namespace {
+
+// A CTA a row, read once for each of its sums: any size.
+template <typename Tx, typename Ty, bool kVec>
+__global__ void __launch_bounds__(kTeamWarps * 32) norm_long_kernel(NormArgs a)
+{
+    __shared__ float red[2 * 32];
+    uint32_t turn = 0;
+    pdl_wait();
+    const uint64_t offset = drop_offset(a.drop);
+    const uint32_t warp = threadIdx.x >> 5, step = blockDim.x / 32 * kTile;
+    for (uint64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+        const Tx* x = static_cast<const Tx*>(a.x) + t * a.x_stride;
+        const Ty* y = static_cast<const Ty*>(a.y) + t * a.y_stride;
+        Tx* r = static_cast<Tx*>(a.r) + t * a.hidden;
+        float eta = 1.0f;
+        float2 sum = twice(0.0f);
+        if (a.y != nullptr && a.post) {
+            for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
+                const Eight v = load8<Ty, kVec>(y, tile, a.hidden);
+                dot(sum, v, v);
+            }
+            float s[1] = {sum.x + sum.y};
+            cta_sum<1>(s, red, turn);
+            eta = rsqrtf(s[0] * a.inv_hidden + a.eps);
+            sum = twice(0.0f);
+        }
+        for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
+            Eight v = load8<Tx, kVec>(x, tile, a.hidden);
+            if (a.y != nullptr) {
+                const Eight k = mul(join_factors<kVec>(a, t, tile), load_vector<kVec>(a.post_weight, 0, tile, a.hidden));
+                const Eight b = mul(load8<Ty, kVec>(y, tile, a.hidden), eta);
+                v = where_kept<kVec>(join_kept<kVec>(a, offset, t, tile), fma(k, b, v), v);
+                v = store8<Tx, kVec>(r, v, tile, a.hidden);
+            }
+            dot(sum, v, v);
+        }
+        if (a.h == nullptr) continue;
+        float s[1] = {sum.x + sum.y};
+        cta_sum<1>(s, red, turn);
+        const float rho = rsqrtf(s[0] * a.inv_hidden + a.eps);
+        for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
+            const Eight v = mul(load8<Tx, kVec>(a.y != nullptr ? r : x, tile, a.hidden), rho);
+            store8<Ty, kVec>(static_cast<Ty*>(a.h) + t * a.hidden, mul(v, load_vector<kVec>(a.weight, 0, tile, a.hidden)), tile,
+                             a.hidden);
+        }
+    }
+}
+
+// A team a worker: a row is read once and stays in registers, with the next one on its
+// way; weights and the gate stay there too.  kKind: which of post (1) and dropout (2) the
+// call has; kAny: it is asked at run time (rows that do not begin on 16 bytes).
+constexpr int kAny = 4;
+template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces, int kKind>
+__global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeamWarps * 32, kTeam == kWarpTeam ? 2 : 1)
+    norm_kernel(NormArgs a)
+{
+    __shared__ float red[kTeam == kWarpTeam ? 1 : kTeamRed];
+    TeamSum<1, kTeam> team_sum(red);
+    pdl_wait();
+    const Place at = place<kTeam>();
+    if (kTeam == kWarpTeam && at.worker >= a.workers) return;
+    const bool join = a.y != nullptr, normed = a.h != nullptr;
+    const bool post = kKind == kAny ? a.post && join : (kKind & 1) != 0, drop = kKind == kAny ? a.drop.below > 0 : (kKind & 2) != 0;
+    const uint64_t offset = drop ? drop_offset(a.drop) : 0;
+    const uint64_t lo = first_row(a.rows, a.workers, at.worker), hi = first_row(a.rows, a.workers, at.worker + 1);
+    // where the rows at hand are; those asked for are one ahead
+    const Tx* x_at = static_cast<const Tx*>(a.x) + lo * a.x_stride;
+    const Ty* y_at = static_cast<const Ty*>(a.y) + (join ? lo * a.y_stride : 0);
+    Tx* r_at = static_cast<Tx*>(a.r) + (join ? lo * a.hidden : 0);
+    Ty* h_at = static_cast<Ty*>(a.h) + (normed ? lo * a.hidden : 0);
+    Piece<Tx, kVec> px[kPieces];
+    Piece<Ty, kVec> py[kPieces] = {};
+    const auto ask = [&]() {
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+            px[n].load(x_at, at.tile(n), a.hidden);
+            if (join) py[n].load(y_at, at.tile(n), a.hidden);
+        }
+        x_at += a.x_stride;
+        if (join) y_at += a.y_stride;
+    };
+    ask();
+    Eight w[kPieces], k[kPieces];
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n) w[n] = load_vector<kVec>(a.weight, 0, at.tile(n), a.hidden);
+    uint64_t gate_end = lo;  // where the gate changes
+    for (uint64_t t = lo; t < hi; ++t) {
+        Eight x[kPieces], y[kPieces];
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) x[n] = px[n].get(), y[n] = py[n].get();
+        if (t + 1 < hi) ask();
+        if (join) {
+            if (t == gate_end) {
+                // the join's factor of each column, with the weight of the norm after the block
+#pragma unroll
+                for (int n = 0; n < kPieces; ++n)
+                    k[n] = mul(join_factors<kVec>(a, t, at.tile(n)), load_vector<kVec>(a.post_weight, 0, at.tile(n), a.hidden));
+                gate_end = a.gate.p != nullptr ? (t / a.gate_span + 1) * a.gate_span : a.rows;
+            }
+            if (post) {
+                float2 sum = twice(0.0f);
+#pragma unroll
+                for (int n = 0; n < kPieces; ++n) dot(sum, y[n], y[n]);
+                float s[1] = {sum.x + sum.y};
+                team_sum(s);
+                const float eta = rsqrtf(s[0] * a.inv_hidden + a.eps);
+#pragma unroll
+                for (int n = 0; n < kPieces; ++n) y[n] = mul(y[n], eta);
+            }
+#pragma unroll
+            for (int n = 0; n < kPieces; ++n) {
+                const Eight r = fma(k[n], y[n], x[n]);
+                x[n] = drop ? where_kept<kVec>(kept_piece<kVec>(a.drop, offset, (uint32_t)t, at.tile(n)), r, x[n]) : r;
+                x[n] = store8<Tx, kVec>(r_at, x[n], at.tile(n), a.hidden);
+            }
+            r_at += a.hidden;
+        }
+        if (!normed) continue;
+        float2 sum = twice(0.0f);
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) dot(sum, x[n], x[n]);
+        float s[1] = {sum.x + sum.y};
+        team_sum(s);
+        const float rho = rsqrtf(s[0] * a.inv_hidden + a.eps);
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) store8<Ty, kVec>(h_at, mul(mul(x[n], rho), w[n]), at.tile(n), a.hidden);
+        h_at += a.hidden;
+    }
+}
+
+template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces>
+NormKernel norm_kind(bool post, bool drop)
+{
+    if constexpr (kVec)
+        return post ? (drop ? norm_kernel<Tx, Ty, kVec, kTeam, kPieces, 3> : norm_kernel<Tx, Ty, kVec, kTeam, kPieces, 1>)
+                    : (drop ? norm_kernel<Tx, Ty, kVec, kTeam, kPieces, 2> : norm_kernel<Tx, Ty, kVec, kTeam, kPieces, 0>);
+    else
+        return norm_kernel<Tx, Ty, kVec, kTeam, kPieces, kAny>;
+}
+template <typename Tx, typename Ty, bool kVec>
+NormKernel norm_for(const Shape& s, bool post, bool drop)
+{
+    constexpr int kMost = kVec && sizeof(Tx) == 2 && sizeof(Ty) == 2 ? 2 : 1;
+    if (s.team == kWarpTeam) return norm_kind<Tx, Ty, kVec, kWarpTeam, 1>(post, drop);
+    if (s.team == kLong) return norm_long_kernel<Tx, Ty, kVec>;
+    if (s.team == kCtaTeam)
+        return s.pieces == 1 ? norm_kind<Tx, Ty, kVec, kCtaTeam, 1>(post, drop) : norm_kind<Tx, Ty, kVec, kCtaTeam, kMost>(post, drop);
+    return s.pieces == 1 ? norm_kind<Tx, Ty, kVec, kClusterTeam, 1>(post, drop)
+                         : norm_kind<Tx, Ty, kVec, kClusterTeam, kMost>(post, drop);
+}
+
+}  // namespace
+
+template <typename Tx, typename Ty>
+NormKernel norm_kernel_for(const Shape& s, bool vec, bool post, bool drop)
+{
+    return vec ? norm_for<Tx, Ty, true>(s, post, drop) : norm_for<Tx, Ty, false>(s, post, drop);
+}
+
+}  // namespace zccl

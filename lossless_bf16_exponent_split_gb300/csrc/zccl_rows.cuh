@@ -76,12 +76,14 @@ struct Piece<__nv_bfloat16, false> {
     uint4 q;
     __device__ __forceinline__ void load(const __nv_bfloat16* row, uint32_t tile, uint32_t cols)
     {
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + column<false>(tile, 0);
         uint32_t w[8];
+        if (tile + kTile <= cols) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t c = column<false>(tile, j);
-            w[j] = c < cols ? p[c] : 0;
+            for (int j = 0; j < 8; ++j) w[j] = p[32 * j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = column<false>(tile, j) < cols ? p[32 * j] : 0;
         }
         q = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
     }
@@ -97,12 +99,14 @@ struct Piece<float, kVec> {
             const float4* p = reinterpret_cast<const float4*>(row + c);
             const float4 a = c < cols ? p[0] : make_float4(0, 0, 0, 0), b = c < cols ? p[1] : make_float4(0, 0, 0, 0);
             v = {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
-        } else {
+        } else if (tile + kTile <= cols) {
+            const float* p = row + column<false>(tile, 0);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t c = column<false>(tile, j);
-                v[j] = c < cols ? row[c] : 0.0f;
-            }
+            for (int j = 0; j < 8; ++j) v[j] = p[32 * j];
+        } else {
+            const float* p = row + column<false>(tile, 0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = column<false>(tile, j) < cols ? p[32 * j] : 0.0f;
         }
     }
     __device__ __forceinline__ Eight get() const { return v; }
@@ -127,12 +131,11 @@ __device__ __forceinline__ Eight store8(T* row, const Eight& v, uint32_t tile, u
             if (c < cols) *reinterpret_cast<uint4*>(row + c) = q;
         } else {
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-            uint16_t* p = reinterpret_cast<uint16_t*>(row);
+            uint16_t* p = reinterpret_cast<uint16_t*>(row) + column<false>(tile, 0);
+            const bool whole = tile + kTile <= cols;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t c = column<false>(tile, j);
-                if (c < cols) p[c] = (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
-            }
+            for (int j = 0; j < 8; ++j)
+                if (whole || column<false>(tile, j) < cols) p[32 * j] = (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
         }
         return widen(q);
     }
@@ -262,6 +265,15 @@ __device__ __forceinline__ Kept<false> kept_piece<false>(const DropArgs& d, uint
     for (int j = 0; j < 8; ++j) k.bits |= ((__shfl_sync(0xFFFFFFFFu, block, j * 4 + lane / 8) >> (lane % 8)) & 1u) << j;
     return k;
 }
+__device__ __forceinline__ uint32_t kept_bits(const Kept<true>& k)
+{
+    uint32_t bits = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) bits |= k[j] ? 1u << j : 0u;
+    return bits;
+}
+__device__ __forceinline__ uint32_t kept_bits(const Kept<false>& k) { return k.bits; }
+
 // All stay.
 template <bool kVec>
 __device__ __forceinline__ Kept<kVec> kept_all();
