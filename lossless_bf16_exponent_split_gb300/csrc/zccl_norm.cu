@@ -27,8 +27,8 @@ bool norm_config(const zccl_norm_t* c, int x_dtype, int dtype, const void* d_wei
     a->post_weight = {d_post_weight, weight_dtype};
     a->gate = {d_gate, gate_dtype};
     a->gate_stride = gate_stride;
-    a->gate_span = gate_span;
-    a->rows = rows;
+    a->gate_span = (uint32_t)(gate_span < rows ? gate_span : rows > 0 ? rows : 1);
+    a->rows = (uint32_t)rows;
     a->hidden = (uint32_t)c->hidden;
     a->post = c->post != 0;
     a->inv_hidden = 1.0f / (float)c->hidden;

@@ -11,8 +11,9 @@ struct NormArgs {
     const void* y;       // nullptr: no join (forward), not read (backward)
     uint64_t x_stride, y_stride;
     Vector weight, post_weight, gate;
-    uint64_t gate_stride, gate_span;
-    uint64_t rows;
+    uint64_t gate_stride;
+    uint32_t gate_span;  // at most `rows`, which are below 2^31
+    uint32_t rows;
     uint32_t hidden;
     int post;
     float inv_hidden, eps;
@@ -43,16 +44,16 @@ enum { kSlotWeight = 0, kSlotPost = 1, kWeightSlots = 2 };  // sums of the weigh
 enum { kSlotBefore = 0, kSlotBehind = 1, kGateSlots = 2 };  // parts of gate rows: [workers][2][pitch]
 
 // The first row of worker w.
-__host__ __device__ inline uint64_t first_row(uint64_t rows, uint32_t workers, uint32_t w)
+__host__ __device__ inline uint32_t first_row(uint32_t rows, uint32_t workers, uint32_t w)
 {
-    const uint64_t base = rows / workers, more = rows - base * workers;
+    const uint32_t base = rows / workers, more = rows - base * workers;
     return base * w + (w < more ? w : more);
 }
 // The worker of a row.
-__host__ __device__ inline uint32_t worker_of(uint64_t rows, uint32_t workers, uint64_t row)
+__host__ __device__ inline uint32_t worker_of(uint32_t rows, uint32_t workers, uint32_t row)
 {
-    const uint64_t base = rows / workers, more = rows - base * workers, large = more * (base + 1);
-    return (uint32_t)(row < large ? row / (base + 1) : more + (row - large) / base);
+    const uint32_t base = rows / workers, more = rows - base * workers, large = more * (base + 1);
+    return row < large ? row / (base + 1) : more + (row - large) / base;
 }
 
 // How a row is held: by a warp (a tile at most), by the warps of a CTA, by those of a
@@ -93,8 +94,8 @@ inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow)
         s.team = s.ctas > 1 ? kClusterTeam : kCtaTeam;
         s.pieces = pieces;
         s.warps = (units + s.ctas - 1) / s.ctas;
-        // clusters of four do not fill every group of SMs: 32 of 38 are taken
-        s.workers = at_most_rows((uint64_t)(s.ctas == 4 ? 128 : kSms) * (16 / s.warps) / s.ctas);
+        // clusters of four do not fill every group of SMs: 36 of 38 are taken
+        s.workers = at_most_rows((uint64_t)(s.ctas == 4 ? 144 : kSms) * (16 / s.warps) / s.ctas);
         s.grid = s.workers * s.ctas;
     } else {
         // its sums stay in the workspace: fewer workers for longer rows
@@ -104,26 +105,34 @@ inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow)
     return s;
 }
 
-// Sums N values (N <= 8) over a warp: a lane keeps half of the values in each of three
-// steps, so nine exchanges do for all eight.  Lane 4 i holds value i then.
+// N values, rounded up to a power of two: that many lanes of a warp hold one each.
+template <int N>
+constexpr int kValues = N <= 1 ? 1 : N <= 2 ? 2 : N <= 4 ? 4 : 8;
+
+// Sums N values (N <= 8) over a warp: while a lane holds several it keeps half of them in
+// a step, so that nine exchanges do for all eight.  Lanes 32 / kValues * i and up hold
+// value i then.
 template <int N>
 __device__ __forceinline__ float warp_sums(const float (&s)[N])
 {
+    constexpr int H = kValues<N>;
     const uint32_t lane = threadIdx.x & 31;
-    float v[8];
+    float v[H];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < N ? s[i] : 0.0f;
+    for (int i = 0; i < H; ++i) v[i] = i < N ? s[i] : 0.0f;
+    int o = 16;
 #pragma unroll
-    for (int h = 4, o = 16; h > 0; h /= 2, o /= 2) {
+    for (int h = H / 2; h > 0; h /= 2, o /= 2) {
         const bool upper = (lane & o) != 0;
 #pragma unroll
         for (int i = 0; i < h; ++i) {
             const float keep = upper ? v[i + h] : v[i], give = upper ? v[i] : v[i + h];
-            v[i] = i < N || i + h < N ? keep + __shfl_xor_sync(0xFFFFFFFFu, give, o) : 0.0f;
+            v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
         }
     }
-    v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 2);
-    return v[0] + __shfl_xor_sync(0xFFFFFFFFu, v[0], 1);
+#pragma unroll
+    for (int x = 32 / H / 2; x > 0; x /= 2) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], x);
+    return v[0];
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -180,6 +189,7 @@ constexpr uint32_t kTeamRed = 2 * kTeamWarps * kMaxCluster * 8;
 // been waited for: all warps have taken up the ones before then, in whose place they go.
 template <int N, int kTeam>
 struct TeamSum {
+    static constexpr int H = kValues<N>, kLanes = 32 / H;
     float* const red;
     uint32_t turn = 0;
     float mine = 0.0f;  // a warp that is a team
@@ -189,13 +199,12 @@ struct TeamSum {
     __device__ __forceinline__ void put(float v)
     {
         const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        float* at = red + turn * (kTeamRed / 2);
+        float* at = red + turn * (kTeamRed / 2) + lane / kLanes;
         if (kTeam == kWarpTeam) mine = v;
-        if (kTeam == kCtaTeam && (lane & 3) == 0) at[warp * 8 + lane / 4] = v;
+        if (kTeam == kCtaTeam && lane % kLanes == 0) at[warp * H] = v;
         if (kTeam == kClusterTeam) {
-            // the four lanes that hold a value take a CTA each
-            if ((lane & 3) < cluster_ctas() && lane / 4 < N)
-                st_cluster(at + (cluster_rank() * (blockDim.x >> 5) + warp) * 8 + lane / 4, lane & 3, v);
+            // the lanes that hold a value take a CTA each
+            if (lane % kLanes < cluster_ctas()) st_cluster(at + (cluster_rank() * (blockDim.x >> 5) + warp) * H, lane % kLanes, v);
             __syncwarp();
             cluster_arrive();
         }
@@ -211,18 +220,16 @@ struct TeamSum {
         const uint32_t lane = threadIdx.x & 31;
         float v = mine;
         if (kTeam != kWarpTeam) {
-            const float* at = red + (turn ^ 1) * (kTeamRed / 2) + (lane & 7);
-            const uint32_t all = (blockDim.x >> 5) * (kTeam == kClusterTeam ? cluster_ctas() : 1);
+            const float* at = red + (turn ^ 1) * (kTeamRed / 2);
+            const uint32_t all = (blockDim.x >> 5) * (kTeam == kClusterTeam ? cluster_ctas() : 1) * H;
             v = 0.0f;
-            if ((lane & 7) < N)
-#pragma unroll 4
-                for (uint32_t w = lane / 8; w < all; w += 4) v += at[w * 8];
+            for (uint32_t i = lane; i < all; i += 32) v += at[i];
             __syncwarp();
-            v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
-            v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+#pragma unroll
+            for (int o = 16; o >= H; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
         }
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = __shfl_sync(0xFFFFFFFFu, v, kTeam == kWarpTeam ? i * 4 : i);
+        for (int i = 0; i < N; ++i) s[i] = N == 1 ? v : __shfl_sync(0xFFFFFFFFu, v, kTeam == kWarpTeam ? i * kLanes : i);
     }
     __device__ __forceinline__ void operator()(float (&s)[N])
     {
@@ -266,15 +273,15 @@ inline uint64_t norm_backward_bytes(const Shape& s, uint64_t hidden)
 // What the block's output is multiplied by before it joins (scale, gate, the
 // dropout's gain).
 template <bool kVec>
-__device__ __forceinline__ Eight join_factors(const NormArgs& a, uint64_t row, uint32_t tile)
+__device__ __forceinline__ Eight join_factors(const NormArgs& a, uint32_t row, uint32_t tile)
 {
-    return mul(load_vector<kVec>(a.gate, a.gate.p != nullptr ? row / a.gate_span * a.gate_stride : 0, tile, a.hidden), a.factor);
+    return mul(load_vector<kVec>(a.gate, a.gate.p != nullptr ? (uint64_t)(row / a.gate_span) * a.gate_stride : 0, tile, a.hidden), a.factor);
 }
 // Which of the lane's values of it stay.
 template <bool kVec>
-__device__ __forceinline__ Kept<kVec> join_kept(const NormArgs& a, uint64_t offset, uint64_t row, uint32_t tile)
+__device__ __forceinline__ Kept<kVec> join_kept(const NormArgs& a, uint64_t offset, uint32_t row, uint32_t tile)
 {
-    return a.drop.below > 0 ? kept_piece<kVec>(a.drop, offset, (uint32_t)row, tile) : kept_all<kVec>();
+    return a.drop.below > 0 ? kept_piece<kVec>(a.drop, offset, row, tile) : kept_all<kVec>();
 }
 
 using NormKernel = void (*)(NormArgs);

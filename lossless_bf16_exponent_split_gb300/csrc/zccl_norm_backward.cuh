@@ -76,12 +76,12 @@ __device__ __forceinline__ Eight add_to(float* p, const Eight& v, bool first, ui
 
 // Writes a gate row's gradient, of its own type.
 template <bool kVec>
-__device__ __forceinline__ void store_gate(const NormArgs& a, uint64_t gate_row, const Eight& v, uint32_t tile)
+__device__ __forceinline__ void store_gate(const NormArgs& a, uint32_t gate_row, const Eight& v, uint32_t tile)
 {
     if (a.gate.dtype == ZCCL_BF16)
-        store8<__nv_bfloat16, kVec>(static_cast<__nv_bfloat16*>(a.grad_gate) + gate_row * a.hidden, v, tile, a.hidden);
+        store8<__nv_bfloat16, kVec>(static_cast<__nv_bfloat16*>(a.grad_gate) + (uint64_t)gate_row * a.hidden, v, tile, a.hidden);
     else
-        store8<float, kVec>(static_cast<float*>(a.grad_gate) + gate_row * a.hidden, v, tile, a.hidden);
+        store8<float, kVec>(static_cast<float*>(a.grad_gate) + (uint64_t)gate_row * a.hidden, v, tile, a.hidden);
 }
 
 // A CTA a worker; its rows are read once for the sums and once for the gradients, and
@@ -94,13 +94,13 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(Nor
     pdl_wait();
     const uint64_t offset = drop_offset(a.drop);
     const uint32_t warp = threadIdx.x >> 5, step = blockDim.x / 32 * kTile, wk = blockIdx.x;
-    const uint64_t lo = first_row(a.rows, a.workers, wk), hi = first_row(a.rows, a.workers, wk + 1);
+    const uint32_t lo = first_row(a.rows, a.workers, wk), hi = first_row(a.rows, a.workers, wk + 1);
     const uint64_t pitch = (a.hidden + 7) / 8 * 8;
     float* sums = a.sums + wk * kWeightSlots * pitch;
     float* parts = a.parts + wk * kGateSlots * pitch;
     const bool join = a.grad_y != nullptr;
-    for (uint64_t t = lo; t < hi; ++t) {
-        const uint64_t gate_row = t / a.gate_span;
+    for (uint32_t t = lo; t < hi; ++t) {
+        const uint32_t gate_row = t / a.gate_span;
         float2 sum[kSums] = {};
         for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
             const Eight r = load_or_zero<Tx, kVec>(a.x, t * a.x_stride, tile, a.hidden);
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(Nor
             const Eight dh = load_or_zero<Ty, kVec>(a.grad_h, t * a.grad_h_stride, tile, a.hidden);
             const Eight up = load_or_zero<Tx, kVec>(a.grad_r, t * a.grad_r_stride, tile, a.hidden);
             const Eight d = joined(f, r, mul(dh, load_vector<kVec>(a.weight, 0, tile, a.hidden)), up);
-            if (a.grad_x != nullptr) store8<Tx, kVec>(static_cast<Tx*>(a.grad_x) + t * a.hidden, d, tile, a.hidden);
+            if (a.grad_x != nullptr) store8<Tx, kVec>(static_cast<Tx*>(a.grad_x) + (uint64_t)t * a.hidden, d, tile, a.hidden);
             if (a.grad_weight != nullptr)
                 add_to<kVec>(sums + kSlotWeight * pitch, mul(dh, mul(r, f.rho)), t == lo, tile, a.hidden);
             if (!join) continue;
@@ -135,14 +135,14 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(Nor
             const Eight e = where_kept<kVec>(kept, mul(d, mul(y, f.eta)));
             if (a.grad_gate != nullptr) {
                 const Eight v = mul(e, mul(p, a.factor));
-                const uint64_t begin = gate_row * a.gate_span, end = begin + a.gate_span;
+                const uint32_t begin = gate_row * a.gate_span, end = begin + a.gate_span;
                 Eight all = v;
                 if (a.gate_span > 1)
                     all = add_to<kVec>(parts + (begin < lo ? kSlotBefore : kSlotBehind) * pitch, v, t == lo || t == begin, tile, a.hidden);
                 if (begin >= lo && (t + 1 == end || t + 1 == a.rows)) store_gate<kVec>(a, gate_row, all, tile);
             }
             if (a.grad_post_weight != nullptr) add_to<kVec>(sums + kSlotPost * pitch, mul(e, k), t == lo, tile, a.hidden);
-            store8<Ty, kVec>(static_cast<Ty*>(a.grad_y) + t * a.hidden, branch(a.post, f, d, y, where_kept<kVec>(kept, mul(k, p))), tile,
+            store8<Ty, kVec>(static_cast<Ty*>(a.grad_y) + (uint64_t)t * a.hidden, branch(a.post, f, d, y, where_kept<kVec>(kept, mul(k, p))), tile,
                              a.hidden);
         }
     }
@@ -160,7 +160,7 @@ struct RowsAt {
     const Tx* up;
     const Ty* dh;
     const Ty* y;
-    __device__ __forceinline__ RowsAt(const NormArgs& a, uint64_t t)
+    __device__ __forceinline__ RowsAt(const NormArgs& a, uint32_t t)
         : r(static_cast<const Tx*>(a.x)), up(static_cast<const Tx*>(a.grad_r)), dh(static_cast<const Ty*>(a.grad_h)),
           y(static_cast<const Ty*>(a.y))
     {
@@ -188,16 +188,17 @@ template <typename Tx, typename Ty, int kPieces, int kStages>
 struct Feed<Tx, Ty, true, kPieces, kStages> {
     static constexpr int kX = sizeof(Tx) / 2, kY = sizeof(Ty) / 2, kAll = 2 * kX + 2 * kY;  // 16-byte parts of a piece
     static constexpr uint32_t kThreadBytes = kStages * kPieces * kAll * 16;
-    uint4* const mine;
+    uint4* const mine;   // a warp's parts, 32 lanes each, one behind the other
     uint32_t asked = 0;  // the stage that the next row goes to
     RowsAt<Tx, Ty> from;
     __device__ __forceinline__ uint4* at(uint32_t stage, int n, int part) const
     {
-        return mine + ((stage * kPieces + n) * kAll + part) * blockDim.x;
+        return mine + stage * (kPieces * kAll * 32) + (n * kAll + part) * 32;
     }
-    __device__ __forceinline__ Feed(uint4* smem, const NormArgs& a, uint64_t t) : mine(smem + threadIdx.x), from(a, t)
+    __device__ __forceinline__ Feed(uint4* warp_smem, const NormArgs& a, uint32_t t)
+        : mine(warp_smem + (threadIdx.x & 31)), from(a, t)
     {
-        for (int i = 0; i < kStages * kPieces * kAll; ++i) mine[i * blockDim.x] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kStages * kPieces * kAll; ++i) mine[i * 32] = make_uint4(0, 0, 0, 0);
     }
     template <typename T>
     __device__ __forceinline__ void copy(const T* row, int n, int part, uint32_t tile, uint32_t hidden)
@@ -267,7 +268,7 @@ struct Feed<Tx, Ty, false, kPieces, kStages> {
     };
     Row next;
     RowsAt<Tx, Ty> from;
-    __device__ __forceinline__ Feed(uint4*, const NormArgs& a, uint64_t t) : next{}, from(a, t) {}
+    __device__ __forceinline__ Feed(uint4*, const NormArgs& a, uint32_t t) : next{}, from(a, t) {}
     __device__ __forceinline__ void ask(const NormArgs& a, const Place& place, bool there)
     {
         if (!there) return;
@@ -302,26 +303,28 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
     constexpr bool kAhead = kTeam == kClusterTeam && kVec;
     constexpr int kTeamSums = kKind == kAny || (kKind & 1) ? kSums : 2;
     using Rows = Feed<Tx, Ty, kVec, kPieces, kAhead ? 3 : 2>;
-    // a thread's sums of p's gradient (two 16-byte parts a piece), and the teams' sums
-    float4* const dp = reinterpret_cast<float4*>(smem) + Rows::kThreadBytes / 16 * blockDim.x + threadIdx.x;
-    TeamSum<kTeamSums, kTeam> team_sum(reinterpret_cast<float*>(smem) + (Rows::kThreadBytes + 32 * kPieces) / 4 * blockDim.x);
+    // of each warp: its rows, and its sums of p's gradient (two 16-byte parts a piece); then the teams' sums
+    constexpr uint32_t kWarpParts = Rows::kThreadBytes / 16 * 32 + 2 * kPieces * 32;
+    uint4* const warp_smem = smem + (threadIdx.x >> 5) * kWarpParts;
+    float4* const dp = reinterpret_cast<float4*>(warp_smem) + Rows::kThreadBytes / 16 * 32 + (threadIdx.x & 31);
+    TeamSum<kTeamSums, kTeam> team_sum(reinterpret_cast<float*>(smem + (blockDim.x >> 5) * kWarpParts));
     pdl_wait();
     const Place at = place<kTeam>();
     const bool join = a.grad_y != nullptr, reads_y = a.y != nullptr;
     const bool post = kKind == kAny ? a.post != 0 : (kKind & 1) != 0, drop = kKind == kAny ? a.drop.below > 0 && join : (kKind & 2) != 0;
     const uint64_t offset = drop ? drop_offset(a.drop) : 0;
-    const uint64_t lo = at.worker < a.workers ? first_row(a.rows, a.workers, at.worker) : 0;
-    const uint64_t hi = at.worker < a.workers ? first_row(a.rows, a.workers, at.worker + 1) : 0;
+    const uint32_t lo = at.worker < a.workers ? first_row(a.rows, a.workers, at.worker) : 0;
+    const uint32_t hi = at.worker < a.workers ? first_row(a.rows, a.workers, at.worker + 1) : 0;
     const uint64_t pitch = (a.hidden + 7) / 8 * 8;
     const auto put_dp = [&](int n, const Eight& v) {
-        dp[(2 * n) * blockDim.x] = make_float4(v[0], v[1], v[2], v[3]);
-        dp[(2 * n + 1) * blockDim.x] = make_float4(v[4], v[5], v[6], v[7]);
+        dp[64 * n] = make_float4(v[0], v[1], v[2], v[3]);
+        dp[64 * n + 32] = make_float4(v[4], v[5], v[6], v[7]);
     };
     const auto get_dp = [&](int n, int warps) -> Eight {
-        const float4 x = dp[(2 * n) * blockDim.x + 32 * warps], y = dp[(2 * n + 1) * blockDim.x + 32 * warps];
+        const float4 x = dp[64 * n + warps * kWarpParts], y = dp[64 * n + 32 + warps * kWarpParts];
         return {{make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)}};
     };
-    Rows rows(smem, a, lo);
+    Rows rows(warp_smem, a, lo);
     rows.ask(a, at, lo < hi);
     Eight w[kPieces], kp[kPieces], dw[kPieces], e[kPieces];
 #pragma unroll
@@ -330,17 +333,17 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
         kp[n] = dw[n] = e[n] = all_eight(0.0f);
         put_dp(n, e[n]);
     }
-    Tx* gx_at = static_cast<Tx*>(a.grad_x) + (a.grad_x != nullptr ? lo * a.hidden : 0);
-    Ty* gy_at = static_cast<Ty*>(a.grad_y) + (join ? lo * a.hidden : 0);
+    Tx* gx_at = static_cast<Tx*>(a.grad_x) + (a.grad_x != nullptr ? (uint64_t)lo * a.hidden : 0);
+    Ty* gy_at = static_cast<Ty*>(a.grad_y) + (join ? (uint64_t)lo * a.hidden : 0);
     // the gate row that e belongs to, and where it ends
-    uint64_t gate_row = lo / a.gate_span, gate_end = a.gate.p != nullptr ? (gate_row + 1) * a.gate_span : a.rows;
-    const auto set_gate = [&](uint64_t t) {
+    uint32_t gate_row = lo / a.gate_span, gate_end = a.gate.p != nullptr ? (gate_row + 1) * a.gate_span : a.rows;
+    const auto set_gate = [&](uint32_t t) {
 #pragma unroll
         for (int n = 0; n < kPieces; ++n)
             kp[n] = mul(join_factors<kVec>(a, t, at.tile(n)), load_vector<kVec>(a.post_weight, 0, at.tile(n), a.hidden));
     };
-    const auto take_out = [&](uint64_t t) {
-        const uint64_t begin = gate_row * a.gate_span;
+    const auto take_out = [&](uint32_t t) {
+        const uint32_t begin = gate_row * a.gate_span;
 #pragma unroll
         for (int n = 0; n < kPieces; ++n) {
             const uint32_t tile = at.tile(n);
@@ -355,16 +358,16 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
         }
     };
     // the factors of row t's gate, 0 where dropped
-    const auto masked = [&](uint64_t t, int n, const Kept<kVec>& kept) -> Eight { return drop ? where_kept<kVec>(kept, kp[n]) : kp[n]; };
-    const auto kept_of = [&](uint64_t t, int n) -> Kept<kVec> {
-        return drop ? kept_piece<kVec>(a.drop, offset, (uint32_t)t, at.tile(n)) : kept_all<kVec>();
+    const auto masked = [&](int n, const Kept<kVec>& kept) -> Eight { return drop ? where_kept<kVec>(kept, kp[n]) : kp[n]; };
+    const auto kept_of = [&](uint32_t t, int n) -> Kept<kVec> {
+        return drop ? kept_piece<kVec>(a.drop, offset, t, at.tile(n)) : kept_all<kVec>();
     };
     // a row's own sums
-    const auto sums_of = [&](const typename Rows::Row& row, uint64_t t, const Kept<kVec> (&kept)[kPieces]) -> float {
+    const auto sums_of = [&](const typename Rows::Row& row, const Kept<kVec> (&kept)[kPieces]) -> float {
         float2 sum[kSums] = {};
 #pragma unroll
         for (int n = 0; n < kPieces; ++n)
-            add_sums(sum, post, row.r(n), mul(row.dh(n), w[n]), row.up(n), row.y(n), post ? masked(t, n, kept[n]) : kp[n]);
+            add_sums(sum, post, row.r(n), mul(row.dh(n), w[n]), row.up(n), row.y(n), post ? masked(n, kept[n]) : kp[n]);
         float s[kTeamSums];
 #pragma unroll
         for (int i = 0; i < kTeamSums; ++i) s[i] = sum[i].x + sum[i].y;
@@ -378,20 +381,22 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
         return row_factors(a, post, s);
     };
     // a row's gradients and its part of the sums over rows
-    const auto gradients = [&](const typename Rows::Row& row, uint64_t t, const RowFactors& f, const Kept<kVec> (&kept)[kPieces]) {
+    const auto gradients = [&](const typename Rows::Row& row, uint32_t t, const RowFactors& f, const Kept<kVec> (&kept)[kPieces]) {
 #pragma unroll
         for (int n = 0; n < kPieces; ++n) {
             const uint32_t tile = at.tile(n);
-            const Eight r = row.r(n), dh = row.dh(n), d = joined(f, r, mul(dh, w[n]), row.up(n));
+            const Eight r = row.r(n), dh = row.dh(n);
+            Eight d = joined(f, r, mul(dh, w[n]), row.up(n)), y = all_eight(0.0f);
             dw[n] = fma(dh, mul(r, f.rho), dw[n]);
             if (a.grad_x != nullptr) store8<Tx, kVec>(gx_at, d, tile, a.hidden);
             if (!join) continue;
-            Eight y = all_eight(0.0f);
+            if (drop) d = where_kept<kVec>(kept[n], d);
             if (reads_y) {
                 y = row.y(n);
-                e[n] = fma(d, mul(drop ? where_kept<kVec>(kept[n], y) : y, f.eta), e[n]);
+                // what is dropped may be infinite; with post it would have spoilt the whole row
+                e[n] = fma(d, mul(drop && !post ? where_kept<kVec>(kept[n], y) : y, f.eta), e[n]);
             }
-            store8<Ty, kVec>(gy_at, branch(post, f, d, y, masked(t, n, kept[n])), tile, a.hidden);
+            store8<Ty, kVec>(gy_at, branch(post, f, d, y, kp[n]), tile, a.hidden);
         }
         gx_at += a.hidden;
         gy_at += a.hidden;
@@ -412,9 +417,9 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
             rows.template wait<1>();
 #pragma unroll
             for (int n = 0; n < kPieces; ++n) kept[n] = kept_of(lo, n);
-            team_sum.put(sums_of(rows.row(1), lo, kept));
+            team_sum.put(sums_of(rows.row(1), kept));
         }
-        for (uint64_t t = lo; t < hi; ++t) {
+        for (uint32_t t = lo; t < hi; ++t) {
             rows.ask(a, at, t + 2 < hi);  // into the stage of row t - 1
             const bool more = t + 1 < hi, turns = more && join && t + 1 == gate_end;
             float s = 0.0f;
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
                 if (turns) set_gate(t + 1);
 #pragma unroll
                 for (int n = 0; n < kPieces; ++n) after[n] = kept_of(t + 1, n);
-                s = sums_of(rows.row(1), t + 1, after);
+                s = sums_of(rows.row(1), after);
                 if (turns) set_gate(t);
             }
             team_sum.wait();
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
         }
     } else {
         if (join && lo < hi) set_gate(lo);
-        for (uint64_t t = lo; t < hi; ++t) {
+        for (uint32_t t = lo; t < hi; ++t) {
             rows.template wait<0>();
             const bool turns = join && t + 1 == gate_end && t + 1 < hi;
             const auto row = rows.row(0);
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
             Kept<kVec> kept[kPieces];
 #pragma unroll
             for (int n = 0; n < kPieces; ++n) kept[n] = kept_of(t, n);
-            team_sum.put(sums_of(row, t, kept));
+            team_sum.put(sums_of(row, kept));
             team_sum.wait();
             gradients(row, t, factors(), kept);
             if (turns) set_gate(t + 1);

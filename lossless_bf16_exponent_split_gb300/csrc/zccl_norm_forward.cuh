@@ -17,10 +17,10 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_long_kernel(NormArgs a)
     pdl_wait();
     const uint64_t offset = drop_offset(a.drop);
     const uint32_t warp = threadIdx.x >> 5, step = blockDim.x / 32 * kTile;
-    for (uint64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+    for (uint32_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
         const Tx* x = static_cast<const Tx*>(a.x) + t * a.x_stride;
         const Ty* y = static_cast<const Ty*>(a.y) + t * a.y_stride;
-        Tx* r = static_cast<Tx*>(a.r) + t * a.hidden;
+        Tx* r = static_cast<Tx*>(a.r) + (uint64_t)t * a.hidden;
         float eta = 1.0f;
         float2 sum = twice(0.0f);
         if (a.y != nullptr && a.post) {
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_long_kernel(NormArgs a)
         const float rho = rsqrtf(s[0] * a.inv_hidden + a.eps);
         for (uint32_t tile = warp * kTile; tile < a.hidden; tile += step) {
             const Eight v = mul(load8<Tx, kVec>(a.y != nullptr ? r : x, tile, a.hidden), rho);
-            store8<Ty, kVec>(static_cast<Ty*>(a.h) + t * a.hidden, mul(v, load_vector<kVec>(a.weight, 0, tile, a.hidden)), tile,
+            store8<Ty, kVec>(static_cast<Ty*>(a.h) + (uint64_t)t * a.hidden, mul(v, load_vector<kVec>(a.weight, 0, tile, a.hidden)), tile,
                              a.hidden);
         }
     }
@@ -71,12 +71,12 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
     const bool join = a.y != nullptr, normed = a.h != nullptr;
     const bool post = kKind == kAny ? a.post && join : (kKind & 1) != 0, drop = kKind == kAny ? a.drop.below > 0 : (kKind & 2) != 0;
     const uint64_t offset = drop ? drop_offset(a.drop) : 0;
-    const uint64_t lo = first_row(a.rows, a.workers, at.worker), hi = first_row(a.rows, a.workers, at.worker + 1);
+    const uint32_t lo = first_row(a.rows, a.workers, at.worker), hi = first_row(a.rows, a.workers, at.worker + 1);
     // where the rows at hand are; those asked for are one ahead
     const Tx* x_at = static_cast<const Tx*>(a.x) + lo * a.x_stride;
     const Ty* y_at = static_cast<const Ty*>(a.y) + (join ? lo * a.y_stride : 0);
-    Tx* r_at = static_cast<Tx*>(a.r) + (join ? lo * a.hidden : 0);
-    Ty* h_at = static_cast<Ty*>(a.h) + (normed ? lo * a.hidden : 0);
+    Tx* r_at = static_cast<Tx*>(a.r) + (join ? (uint64_t)lo * a.hidden : 0);
+    Ty* h_at = static_cast<Ty*>(a.h) + (normed ? (uint64_t)lo * a.hidden : 0);
     Piece<Tx, kVec> px[kPieces];
     Piece<Ty, kVec> py[kPieces] = {};
     const auto ask = [&]() {
@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
     Eight w[kPieces], k[kPieces];
 #pragma unroll
     for (int n = 0; n < kPieces; ++n) w[n] = load_vector<kVec>(a.weight, 0, at.tile(n), a.hidden);
-    uint64_t gate_end = lo;  // where the gate changes
-    for (uint64_t t = lo; t < hi; ++t) {
+    uint32_t gate_end = lo;  // where the gate changes
+    for (uint32_t t = lo; t < hi; ++t) {
         Eight x[kPieces], y[kPieces];
 #pragma unroll
         for (int n = 0; n < kPieces; ++n) x[n] = px[n].get(), y[n] = py[n].get();
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
 #pragma unroll
             for (int n = 0; n < kPieces; ++n) {
                 const Eight r = fma(k[n], y[n], x[n]);
-                x[n] = drop ? where_kept<kVec>(kept_piece<kVec>(a.drop, offset, (uint32_t)t, at.tile(n)), r, x[n]) : r;
+                x[n] = drop ? where_kept<kVec>(kept_piece<kVec>(a.drop, offset, t, at.tile(n)), r, x[n]) : r;
                 x[n] = store8<Tx, kVec>(r_at, x[n], at.tile(n), a.hidden);
             }
             r_at += a.hidden;

@@ -6,74 +6,122 @@ namespace zccl {
 
 namespace {
 
-// Adds the partial sums up: blockIdx.y = 0, 1 a weight's, 2 + i those of a gate row that
-// several workers have parts of: gate row i (kByRow), or the one that goes on behind
-// worker i's rows.
-constexpr uint32_t kJoinRows = 32;  // partial sums of a column that are added side by side
-
-template <bool kByRow>
-__global__ void __launch_bounds__(32 * kJoinRows) norm_join_kernel(NormArgs a, int weight_dtype)
+// The workers that have parts of a gate row.
+struct Sharers {
+    uint32_t from, to;
+};
+__device__ __forceinline__ Sharers sharers(const NormArgs& a, uint32_t gate_row)
 {
-    __shared__ float red[kJoinRows][33];
-    pdl_wait();
-    const uint64_t pitch = (a.hidden + 7) / 8 * 8;
-    const uint32_t lane = threadIdx.x & 31, sub = threadIdx.x >> 5, col = blockIdx.x * 32 + lane, job = blockIdx.y;
-    float sum = 0.0f;
-    void* out;
-    int dtype = weight_dtype;
-    uint64_t at = col;
-    if (job < 2) {
-        out = job == 0 ? a.grad_weight : a.grad_post_weight;
-        if (out == nullptr) return;
-        const float* p = a.sums + job * pitch + col;
-        if (col < a.hidden)
-#pragma unroll 8
-            for (uint32_t g = sub; g < a.groups; g += kJoinRows) sum += p[g * kWeightSlots * pitch];
-    } else {
-        uint64_t gate_row = job - 2;
-        if (!kByRow) {
-            const uint64_t next = first_row(a.rows, a.workers, job - 2 + 1);
-            gate_row = (next - 1) / a.gate_span;
-        }
-        const uint64_t begin = gate_row * a.gate_span, end = begin + a.gate_span < a.rows ? begin + a.gate_span : a.rows;
-        const uint32_t from = worker_of(a.rows, a.workers, begin), to = worker_of(a.rows, a.workers, end - 1);
-        if (from == to || (!kByRow && from != job - 2)) return;  // the worker's own, or another's to add up
-        if (col < a.hidden)
-#pragma unroll 4
-            for (uint32_t w = from + sub; w <= to; w += kJoinRows)
-                sum += a.parts[((uint64_t)w * kGateSlots + (w == from ? kSlotBehind : kSlotBefore)) * pitch + col];
-        out = a.grad_gate;
-        dtype = a.gate.dtype;
-        at += gate_row * a.hidden;
-    }
-    red[sub][lane] = sum;
-    __syncthreads();
-    if (sub != 0 || col >= a.hidden) return;
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kJoinRows; ++i) sum += red[i][lane];
-    if (dtype == ZCCL_BF16)
-        static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(sum);
-    else
-        static_cast<float*>(out)[at] = sum;
+    const uint32_t begin = gate_row * a.gate_span, end = begin + a.gate_span < a.rows ? begin + a.gate_span : a.rows;
+    return {worker_of(a.rows, a.workers, begin), worker_of(a.rows, a.workers, end - 1)};
 }
 
-cudaError_t launch_join(const NormArgs& a, int weight_dtype, cudaStream_t stream)
+template <typename T>
+__device__ __forceinline__ void store_as(void* p, int dtype, uint64_t at, T v)
 {
-    const bool gate = a.grad_gate != nullptr && a.gate_span > 1 && a.workers > 1;
-    if (a.grad_weight == nullptr && a.grad_post_weight == nullptr && !gate) return cudaSuccess;
-    const uint64_t gate_rows = (a.rows + a.gate_span - 1) / a.gate_span;
-    const bool by_row = gate_rows < a.workers;
+    if (dtype == ZCCL_BF16)
+        static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<float*>(p)[at] = v;
+}
+
+// Adds the partial sums of 32 columns up: blockIdx.y = 0, 1 a weight's, 2 + i those of
+// gate row i.  Eight lanes hold a row's 32 columns, so that a thread has few rows, all of
+// them on their way at once.
+constexpr uint32_t kJoinThreads = 1024;
+
+__global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(NormArgs a, int weight_dtype)
+{
+    constexpr uint32_t kRows = kJoinThreads / 8;
+    __shared__ float red[kJoinThreads / 32][33];
+    pdl_wait();
+    const uint64_t pitch = (a.hidden + 7) / 8 * 8;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, job = blockIdx.y;
+    const uint32_t col = blockIdx.x * 32 + lane % 8 * 4, first = threadIdx.x / 8;
+    float4 sum = make_float4(0, 0, 0, 0);
+    const auto add = [&](const float* p) {
+        const float4 v = *reinterpret_cast<const float4*>(p + col);
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    };
+    void* out = a.grad_gate;
+    int dtype = a.gate.dtype;
+    uint64_t at = 0;
+    if (job < 2) {
+        out = job == 0 ? a.grad_weight : a.grad_post_weight;
+        dtype = weight_dtype;
+        if (out == nullptr) return;
+        if (col < pitch)
+#pragma unroll 8
+            for (uint32_t g = first; g < a.groups; g += kRows) add(a.sums + ((uint64_t)g * kWeightSlots + job) * pitch);
+    } else {
+        const Sharers s = sharers(a, job - 2);
+        if (s.from == s.to) return;  // its worker's own
+        if (col < pitch)
+#pragma unroll 8
+            for (uint32_t w = s.from + first; w <= s.to; w += kRows)
+                add(a.parts + ((uint64_t)w * kGateSlots + (w == s.from ? kSlotBehind : kSlotBefore)) * pitch);
+        at = (uint64_t)(job - 2) * a.hidden;
+    }
+#pragma unroll
+    for (int o = 16; o >= 8; o /= 2) {
+        sum.x += __shfl_xor_sync(0xFFFFFFFFu, sum.x, o);
+        sum.y += __shfl_xor_sync(0xFFFFFFFFu, sum.y, o);
+        sum.z += __shfl_xor_sync(0xFFFFFFFFu, sum.z, o);
+        sum.w += __shfl_xor_sync(0xFFFFFFFFu, sum.w, o);
+    }
+    if (lane < 8) {
+        float* p = &red[warp][lane * 4];
+        p[0] = sum.x, p[1] = sum.y, p[2] = sum.z, p[3] = sum.w;
+    }
+    __syncthreads();
+    // a warp a column
+    float v = red[lane][warp];
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    const uint32_t c = blockIdx.x * 32 + warp;
+    if (lane == 0 && c < a.hidden) store_as(out, dtype, at + c, v);
+}
+
+// With more gate rows than workers a gate row has parts of two or three workers: a thread
+// a column of the one that goes on behind worker blockIdx.y's rows.
+__global__ void __launch_bounds__(256) norm_join_gates_kernel(NormArgs a)
+{
+    pdl_wait();
+    const uint64_t pitch = (a.hidden + 7) / 8 * 8;
+    const uint32_t col = blockIdx.x * 256 + threadIdx.x, w = blockIdx.y;
+    const uint32_t gate_row = (first_row(a.rows, a.workers, w + 1) - 1) / a.gate_span;
+    const Sharers s = sharers(a, gate_row);
+    if (s.from != w || s.to == w || col >= a.hidden) return;
+    float sum = a.parts[((uint64_t)w * kGateSlots + kSlotBehind) * pitch + col];
+    for (uint32_t i = w + 1; i <= s.to; ++i) sum += a.parts[((uint64_t)i * kGateSlots + kSlotBefore) * pitch + col];
+    store_as(a.grad_gate, a.gate.dtype, (uint64_t)gate_row * a.hidden + col, sum);
+}
+
+template <typename... Args>
+cudaError_t launch_2d(void (*kernel)(Args...), dim3 grid, uint32_t threads, cudaStream_t stream, Args... args)
+{
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.hidden + 31) / 32, !gate ? 2 : by_row ? 2 + (uint32_t)gate_rows : 2 + a.workers - 1);
-    cfg.blockDim = dim3(32 * kJoinRows);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, by_row ? norm_join_kernel<true> : norm_join_kernel<false>, a, weight_dtype);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+cudaError_t launch_join(const NormArgs& a, int weight_dtype, cudaStream_t stream)
+{
+    const bool gate = a.grad_gate != nullptr && a.gate_span > 1 && a.workers > 1;
+    const uint32_t gate_rows = (a.rows - 1) / a.gate_span + 1;
+    const bool by_row = gate && gate_rows < a.workers;
+    cudaError_t e = cudaSuccess;
+    if (gate && !by_row) e = launch_2d(norm_join_gates_kernel, dim3((a.hidden + 255) / 256, a.workers - 1), 256, stream, a);
+    if (e == cudaSuccess && (a.grad_weight != nullptr || a.grad_post_weight != nullptr || by_row))
+        e = launch_2d(norm_join_kernel, dim3((a.hidden + 31) / 32, by_row ? 2 + gate_rows : 2), kJoinThreads, stream, a, weight_dtype);
+    return e;
 }
 
 }  // namespace

@@ -212,24 +212,29 @@ __device__ __forceinline__ uint4 philox(uint4 c, const DropArgs& d)
     return c;
 }
 
-// Which of a lane's eight values stay.  A value's 16 bits are compared in the upper
-// half of a word, so no bits have to be cut out of it.
+// Which of a lane's eight values stay: the 16 bits of two at a time are compared.
 template <bool kVec>
 struct Kept;
 template <>
 struct Kept<true> {
     uint4 w;
-    uint32_t below;
-    __device__ __forceinline__ bool operator[](int j) const
+    uint32_t below;  // in the upper half
+    // of values 2 i and 2 i + 1
+    __device__ __forceinline__ void pair(int i, bool* lo, bool* hi) const
     {
-        const uint32_t x = j / 2 == 0 ? w.x : j / 2 == 1 ? w.y : j / 2 == 2 ? w.z : w.w;
-        return (j & 1 ? x : x << 16) >= below;
+        const uint32_t x = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+        *lo = x << 16 >= below;
+        *hi = x >= below;
     }
 };
 template <>
 struct Kept<false> {
     uint32_t bits;
-    __device__ __forceinline__ bool operator[](int j) const { return (bits >> j) & 1u; }
+    __device__ __forceinline__ void pair(int i, bool* lo, bool* hi) const
+    {
+        *lo = (bits >> (2 * i)) & 1u;
+        *hi = (bits >> (2 * i + 1)) & 1u;
+    }
 };
 
 // The bits of the eight columns from 8 block on.
@@ -259,21 +264,16 @@ __device__ __forceinline__ Kept<false> kept_piece<false>(const DropArgs& d, uint
     const Kept<true> mine = kept_block(d, offset, row, tile / 8 + lane);
     uint32_t block = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) block |= mine[j] ? 1u << j : 0u;
+    for (int i = 0; i < 4; ++i) {
+        bool lo, hi;
+        mine.pair(i, &lo, &hi);
+        block |= (lo ? 1u << (2 * i) : 0u) | (hi ? 2u << (2 * i) : 0u);
+    }
     Kept<false> k{0};
 #pragma unroll
     for (int j = 0; j < 8; ++j) k.bits |= ((__shfl_sync(0xFFFFFFFFu, block, j * 4 + lane / 8) >> (lane % 8)) & 1u) << j;
     return k;
 }
-__device__ __forceinline__ uint32_t kept_bits(const Kept<true>& k)
-{
-    uint32_t bits = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) bits |= k[j] ? 1u << j : 0u;
-    return bits;
-}
-__device__ __forceinline__ uint32_t kept_bits(const Kept<false>& k) { return k.bits; }
-
 // All stay.
 template <bool kVec>
 __device__ __forceinline__ Kept<kVec> kept_all();
@@ -287,7 +287,11 @@ __device__ __forceinline__ Eight where_kept(const Kept<kVec>& k, const Eight& a,
 {
     Eight o;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = k[j] ? a[j] : b[j];
+    for (int i = 0; i < 4; ++i) {
+        bool lo, hi;
+        k.pair(i, &lo, &hi);
+        o.v[i] = make_float2(lo ? a.v[i].x : b.v[i].x, hi ? a.v[i].y : b.v[i].y);
+    }
     return o;
 }
 template <bool kVec>
