@@ -162,20 +162,20 @@ __device__ __forceinline__ void st_cluster(float* p, uint32_t rank, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 
-// A warp's worker, and its tiles of a row.
+// A warp's worker, and its neighbouring tiles of a row.
 struct Place {
-    uint32_t worker, first, step;
-    __device__ __forceinline__ uint32_t tile(int n) const { return first + n * step; }
+    uint32_t worker, first;
+    __device__ __forceinline__ uint32_t tile(int n) const { return first + n * kTile; }
 };
-template <int kTeam>
+template <int kTeam, int kPieces>
 __device__ __forceinline__ Place place()
 {
     const uint32_t warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    if (kTeam == kWarpTeam) return {blockIdx.x * kWarpsPerCta + warp, 0, 0};
-    if (kTeam == kCtaTeam) return {blockIdx.x, warp * kTile, warps * kTile};
+    if (kTeam == kWarpTeam) return {blockIdx.x * kWarpsPerCta + warp, 0};
+    if (kTeam == kCtaTeam) return {blockIdx.x, warp * kPieces * kTile};
     const uint32_t ctas = cluster_ctas();
     cluster_sync();  // the others' shared memory is there
-    return {blockIdx.x / ctas, (cluster_rank() * warps + warp) * kTile, ctas * warps * kTile};
+    return {blockIdx.x / ctas, (cluster_rank() * warps + warp) * kPieces * kTile};
 }
 
 // Room for the sums of a team's warps, whose halves take turns by `turn`: a warp may
@@ -190,10 +190,15 @@ constexpr uint32_t kTeamRed = 2 * kTeamWarps * kMaxCluster * 8;
 template <int N, int kTeam>
 struct TeamSum {
     static constexpr int H = kValues<N>, kLanes = 32 / H;
+    static constexpr int kRounds = ((int)kTeamWarps * (kTeam == kClusterTeam ? (int)kMaxCluster : 1) * H + 31) / 32;
     float* const red;
     uint32_t turn = 0;
-    float mine = 0.0f;  // a warp that is a team
-    __device__ __forceinline__ explicit TeamSum(float* red) : red(red) {}
+    float mine = 0.0f;   // a warp that is a team
+    const uint32_t all;  // values of the team's warps
+    __device__ __forceinline__ explicit TeamSum(float* red)
+        : red(red), all((blockDim.x >> 5) * (kTeam == kClusterTeam ? cluster_ctas() : 1) * H)
+    {
+    }
 
     // v: what warp_sums gave.
     __device__ __forceinline__ void put(float v)
@@ -220,11 +225,11 @@ struct TeamSum {
         const uint32_t lane = threadIdx.x & 31;
         float v = mine;
         if (kTeam != kWarpTeam) {
-            const float* at = red + (turn ^ 1) * (kTeamRed / 2);
-            const uint32_t all = (blockDim.x >> 5) * (kTeam == kClusterTeam ? cluster_ctas() : 1) * H;
+            const float* at = red + (turn ^ 1) * (kTeamRed / 2) + lane;
             v = 0.0f;
-            for (uint32_t i = lane; i < all; i += 32) v += at[i];
-            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kRounds; ++i)
+                if (kTeam == kClusterTeam ? i * 32 < all : true) v += i * 32 + lane < all ? at[i * 32] : 0.0f;
 #pragma unroll
             for (int o = 16; o >= H; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
         }

@@ -153,76 +153,63 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(Nor
 template <typename Tx, typename Ty, bool kVec, int kPieces, int kStages>
 struct Feed;
 
-// Where the rows that are asked for next are.
-template <typename Tx, typename Ty>
-struct RowsAt {
-    const Tx* r;
-    const Tx* up;
-    const Ty* dh;
-    const Ty* y;
-    __device__ __forceinline__ RowsAt(const NormArgs& a, uint32_t t)
-        : r(static_cast<const Tx*>(a.x)), up(static_cast<const Tx*>(a.grad_r)), dh(static_cast<const Ty*>(a.grad_h)),
-          y(static_cast<const Ty*>(a.y))
-    {
-        if (r != nullptr) r += t * a.x_stride;
-        if (up != nullptr) up += t * a.grad_r_stride;
-        if (dh != nullptr) dh += t * a.grad_h_stride;
-        if (y != nullptr) y += t * a.y_stride;
-    }
-    __device__ __forceinline__ void next(const NormArgs& a)
-    {
-        if (r != nullptr) r += a.x_stride;
-        if (up != nullptr) up += a.grad_r_stride;
-        if (dh != nullptr) dh += a.grad_h_stride;
-        if (y != nullptr) y += a.y_stride;
-    }
-};
-
 // Rows on 16 bytes come by asynchronous copies into places of the thread's own, so that
-// no thread waits for another's and no registers are held.
-__device__ __forceinline__ void copy_16(uint4* to, const void* from, bool there)
+// no thread waits for another's and no registers are held.  A lane's addresses move on
+// from row to row; what it copies lies at constant distances from them.
+template <int kTo, int kFrom>
+__device__ __forceinline__ void copy_16(uint32_t to, const char* from, uint32_t bytes)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0+%3], [%1+%4], 16, %2;" ::"r"(to), "l"(from), "r"(bytes), "n"(kTo), "n"(kFrom) : "memory");
 }
 template <typename Tx, typename Ty, int kPieces, int kStages>
 struct Feed<Tx, Ty, true, kPieces, kStages> {
     static constexpr int kX = sizeof(Tx) / 2, kY = sizeof(Ty) / 2, kAll = 2 * kX + 2 * kY;  // 16-byte parts of a piece
     static constexpr uint32_t kThreadBytes = kStages * kPieces * kAll * 16;
-    uint4* const mine;   // a warp's parts, 32 lanes each, one behind the other
-    uint32_t asked = 0;  // the stage that the next row goes to
-    RowsAt<Tx, Ty> from;
-    __device__ __forceinline__ uint4* at(uint32_t stage, int n, int part) const
+    static constexpr uint32_t kStage = kPieces * kAll * 32;  // 16-byte parts of a warp's stage
+    const uint4* const mine;  // a warp's parts, 32 lanes each, one behind the other
+    uint32_t to;              // the stage that the next row goes to
+    uint32_t asked = 0;
+    const char *r, *up, *dh, *y;
+    uint32_t bytes[kPieces];  // 16, or 0 where a piece lies behind the row's end
+    __device__ __forceinline__ Feed(uint4* warp_smem, const NormArgs& a, const Place& place, uint32_t t)
+        : mine(warp_smem + (threadIdx.x & 31)), to(smem_addr(warp_smem + (threadIdx.x & 31)))
     {
-        return mine + stage * (kPieces * kAll * 32) + (n * kAll + part) * 32;
-    }
-    __device__ __forceinline__ Feed(uint4* warp_smem, const NormArgs& a, uint32_t t)
-        : mine(warp_smem + (threadIdx.x & 31)), from(a, t)
-    {
-        for (int i = 0; i < kStages * kPieces * kAll; ++i) mine[i * 32] = make_uint4(0, 0, 0, 0);
-    }
-    template <typename T>
-    __device__ __forceinline__ void copy(const T* row, int n, int part, uint32_t tile, uint32_t hidden)
-    {
-        if (row == nullptr) return;
-        const uint32_t c = column<true>(tile, 0);
-        const T* p = row + (c < hidden ? c : 0);
+        for (uint32_t i = 0; i < kStages * kStage; i += 32) warp_smem[i + (threadIdx.x & 31)] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) copy_16(at(asked, n, part + i), p + 4 * i, c < hidden);
+        for (int n = 0; n < kPieces; ++n) bytes[n] = column<true>(place.tile(n), 0) < a.hidden ? 16 : 0;
+        const uint64_t c = bytes[0] > 0 ? column<true>(place.tile(0), 0) : 0;
+        r = static_cast<const char*>(a.x) + (t * a.x_stride + c) * sizeof(Tx);
+        up = static_cast<const char*>(a.grad_r) + (t * a.grad_r_stride + c) * sizeof(Tx);
+        dh = static_cast<const char*>(a.grad_h) + (t * a.grad_h_stride + c) * sizeof(Ty);
+        y = static_cast<const char*>(a.y) + (t * a.y_stride + c) * sizeof(Ty);
+    }
+    template <typename T, int kPart>
+    __device__ __forceinline__ void copy(const char*& from, uint64_t stride)
+    {
+        copy_piece<T, kPart, 0>(from);
+        if constexpr (kPieces == 2) copy_piece<T, kPart, 1>(from);
+        from += stride * sizeof(T);
+    }
+    template <typename T, int kPart, int n>
+    __device__ __forceinline__ void copy_piece(const char* from)
+    {
+        copy_16<(n * kAll + kPart) * 512, n * (int)(kTile * sizeof(T))>(to, from, bytes[n]);
+        if constexpr (sizeof(T) == 4) copy_16<(n * kAll + kPart + 1) * 512, n * (int)(kTile * sizeof(T)) + 16>(to, from, bytes[n]);
     }
     // Asks for the next row (there: it is one of the worker's).
-    __device__ __forceinline__ void ask(const NormArgs& a, const Place& place, bool there)
+    __device__ __forceinline__ void ask(const NormArgs& a, const Place&, bool there)
     {
         if (there) {
-#pragma unroll
-            for (int n = 0; n < kPieces; ++n) {
-                copy<Tx>(from.r, n, 0, place.tile(n), a.hidden);
-                copy<Tx>(from.up, n, kX, place.tile(n), a.hidden);
-                copy<Ty>(from.dh, n, 2 * kX, place.tile(n), a.hidden);
-                copy<Ty>(from.y, n, 2 * kX + kY, place.tile(n), a.hidden);
+            if (a.grad_h != nullptr) {
+                copy<Tx, 0>(r, a.x_stride);
+                copy<Ty, 2 * kX>(dh, a.grad_h_stride);
             }
-            from.next(a);
+            if (a.grad_r != nullptr) copy<Tx, kX>(up, a.grad_r_stride);
+            if (a.y != nullptr) copy<Ty, 2 * kX + kY>(y, a.y_stride);
         }
-        asked = asked + 1 == kStages ? 0 : asked + 1;
+        const bool last = asked + 1 == kStages;
+        asked = last ? 0 : asked + 1;
+        to = last ? to - (kStages - 1) * kStage * 16 : to + kStage * 16;
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
     // Until all but the last kLater rows that were asked for are there.
@@ -231,26 +218,26 @@ struct Feed<Tx, Ty, true, kPieces, kStages> {
     {
         asm volatile("cp.async.wait_group %0;" ::"n"(kLater) : "memory");
     }
-    template <typename T>
-    __device__ __forceinline__ Eight read(uint32_t stage, int n, int part) const
-    {
-        if (sizeof(T) == 2) return widen(*at(stage, n, part));
-        const float4 x = *reinterpret_cast<const float4*>(at(stage, n, part)), y = *reinterpret_cast<const float4*>(at(stage, n, part + 1));
-        return {{make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)}};
-    }
     struct Row {
-        const Feed* f;
-        uint32_t stage;
-        __device__ __forceinline__ Eight r(int n) const { return f->template read<Tx>(stage, n, 0); }
-        __device__ __forceinline__ Eight up(int n) const { return f->template read<Tx>(stage, n, kX); }
-        __device__ __forceinline__ Eight dh(int n) const { return f->template read<Ty>(stage, n, 2 * kX); }
-        __device__ __forceinline__ Eight y(int n) const { return f->template read<Ty>(stage, n, 2 * kX + kY); }
+        const uint4* at;
+        template <typename T>
+        __device__ __forceinline__ Eight read(int n, int part) const
+        {
+            const uint4* p = at + (n * kAll + part) * 32;
+            if (sizeof(T) == 2) return widen(*p);
+            const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 32);
+            return {{make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)}};
+        }
+        __device__ __forceinline__ Eight r(int n) const { return read<Tx>(n, 0); }
+        __device__ __forceinline__ Eight up(int n) const { return read<Tx>(n, kX); }
+        __device__ __forceinline__ Eight dh(int n) const { return read<Ty>(n, 2 * kX); }
+        __device__ __forceinline__ Eight y(int n) const { return read<Ty>(n, 2 * kX + kY); }
     };
     // The row that was asked for before the last `later` ones.
     __device__ __forceinline__ Row row(uint32_t later) const
     {
         const uint32_t stage = asked + kStages - 1 - later;
-        return {this, stage >= kStages ? stage - kStages : stage};
+        return {mine + (stage >= kStages ? stage - kStages : stage) * kStage};
     }
 };
 
@@ -267,19 +254,21 @@ struct Feed<Tx, Ty, false, kPieces, kStages> {
         __device__ __forceinline__ Eight y(int n) const { return py[n].get(); }
     };
     Row next;
-    RowsAt<Tx, Ty> from;
-    __device__ __forceinline__ Feed(uint4*, const NormArgs& a, uint32_t t) : next{}, from(a, t) {}
+    uint32_t at;  // the row that is asked for next
+    __device__ __forceinline__ Feed(uint4*, const NormArgs&, const Place&, uint32_t t) : next{}, at(t) {}
     __device__ __forceinline__ void ask(const NormArgs& a, const Place& place, bool there)
     {
         if (!there) return;
 #pragma unroll
         for (int n = 0; n < kPieces; ++n) {
-            if (from.r != nullptr) next.pr[n].load(from.r, place.tile(n), a.hidden);
-            if (from.up != nullptr) next.pu[n].load(from.up, place.tile(n), a.hidden);
-            if (from.dh != nullptr) next.ph[n].load(from.dh, place.tile(n), a.hidden);
-            if (from.y != nullptr) next.py[n].load(from.y, place.tile(n), a.hidden);
+            if (a.grad_h != nullptr) {
+                next.pr[n].load(static_cast<const Tx*>(a.x) + at * a.x_stride, place.tile(n), a.hidden);
+                next.ph[n].load(static_cast<const Ty*>(a.grad_h) + at * a.grad_h_stride, place.tile(n), a.hidden);
+            }
+            if (a.grad_r != nullptr) next.pu[n].load(static_cast<const Tx*>(a.grad_r) + at * a.grad_r_stride, place.tile(n), a.hidden);
+            if (a.y != nullptr) next.py[n].load(static_cast<const Ty*>(a.y) + at * a.y_stride, place.tile(n), a.hidden);
         }
-        from.next(a);
+        ++at;
     }
     template <int kLater>
     __device__ __forceinline__ void wait()
@@ -309,7 +298,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
     float4* const dp = reinterpret_cast<float4*>(warp_smem) + Rows::kThreadBytes / 16 * 32 + (threadIdx.x & 31);
     TeamSum<kTeamSums, kTeam> team_sum(reinterpret_cast<float*>(smem + (blockDim.x >> 5) * kWarpParts));
     pdl_wait();
-    const Place at = place<kTeam>();
+    const Place at = place<kTeam, kPieces>();
     const bool join = a.grad_y != nullptr, reads_y = a.y != nullptr;
     const bool post = kKind == kAny ? a.post != 0 : (kKind & 1) != 0, drop = kKind == kAny ? a.drop.below > 0 && join : (kKind & 2) != 0;
     const uint64_t offset = drop ? drop_offset(a.drop) : 0;
@@ -324,7 +313,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
         const float4 x = dp[64 * n + warps * kWarpParts], y = dp[64 * n + 32 + warps * kWarpParts];
         return {{make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)}};
     };
-    Rows rows(warp_smem, a, lo);
+    Rows rows(warp_smem, a, at, lo);
     rows.ask(a, at, lo < hi);
     Eight w[kPieces], kp[kPieces], dw[kPieces], e[kPieces];
 #pragma unroll

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
     __shared__ float red[kTeam == kWarpTeam ? 1 : kTeamRed];
     TeamSum<1, kTeam> team_sum(red);
     pdl_wait();
-    const Place at = place<kTeam>();
+    const Place at = place<kTeam, kPieces>();
     if (kTeam == kWarpTeam && at.worker >= a.workers) return;
     const bool join = a.y != nullptr, normed = a.h != nullptr;
     const bool post = kKind == kAny ? a.post && join : (kKind & 1) != 0, drop = kKind == kAny ? a.drop.below > 0 : (kKind & 2) != 0;
