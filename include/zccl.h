@@ -554,12 +554,15 @@ typedef struct {
  *             of its own for each token, rows: one for all)
  *   offset    of the dropout, plus *d_offset where that is not NULL
  * rows < 2^31.  Pointers are aligned to their type; rows that all begin on 16 bytes
- * (of gate and weights too) are moved 16 bytes at a time. */
+ * (of gate and weights too) are moved 16 bytes at a time.  d_status gets
+ * ZCCL_ERR_TIMEOUT if a device wait ran out (rows of more than 4096 values are held by
+ * several CTAs, which wait for one another's sums); the rows concerned are NaN then. */
 zccl_status_t zccl_residual_norm(const zccl_norm_t* cfg, const void* d_x, int x_dtype, uint64_t x_stride,
                                  const void* d_y, int dtype, uint64_t y_stride, const void* d_weight,
                                  const void* d_post_weight, int weight_dtype, const void* d_gate, int gate_dtype,
                                  uint64_t gate_stride, uint64_t gate_span, uint64_t rows, uint64_t offset,
-                                 const uint64_t* d_offset, void* d_r, void* d_h, cudaStream_t stream);
+                                 const uint64_t* d_offset, void* d_r, void* d_h, uint32_t* d_status,
+                                 cudaStream_t stream);
 
 /* Workspace of zccl_residual_norm_backward; its contents before a call do not matter. */
 zccl_status_t zccl_residual_norm_workspace_bytes(uint64_t hidden, uint64_t rows, uint64_t* bytes);
@@ -581,7 +584,7 @@ zccl_status_t zccl_residual_norm_backward(const zccl_norm_t* cfg, const void* d_
                                           uint64_t gate_span, uint64_t rows, uint64_t offset,
                                           const uint64_t* d_offset, void* d_grad_x, void* d_grad_y,
                                           void* d_grad_weight, void* d_grad_post_weight, void* d_grad_gate, void* d_ws,
-                                          uint64_t ws_bytes, cudaStream_t stream);
+                                          uint64_t ws_bytes, uint32_t* d_status, cudaStream_t stream);
 
 /* Dropout with a mask that is never stored: each element is dropped, independently
  * of the others, where 16 random bits u (a whole number below 2^16) are below

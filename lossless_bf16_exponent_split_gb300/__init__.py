@@ -126,7 +126,7 @@ _SIGS = {
     "zccl_residual_norm": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_int,
                             ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
                             ctypes.c_int, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64,
-                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
     "zccl_residual_norm_workspace_bytes": ([ctypes.c_uint64, ctypes.c_uint64, ctypes.POINTER(ctypes.c_uint64)],
                                            ctypes.c_int),
     "zccl_residual_norm_backward": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_uint64,
@@ -135,7 +135,7 @@ _SIGS = {
                                      ctypes.c_int, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64,
                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_uint64,
-                                     ctypes.c_void_p], ctypes.c_int),
+                                     ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
     "zccl_dropout": ([ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_float,
                       ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p],
                      ctypes.c_int),
@@ -413,11 +413,11 @@ def zccl_fp8_linear_backward(d_grad, d_x, dtype, grad_stride, x_stride, rows, k,
 
 
 def zccl_residual_norm(cfg, d_x, x_dtype, x_stride, d_y, dtype, y_stride, d_weight, d_post_weight, weight_dtype, d_gate,
-                       gate_dtype, gate_stride, gate_span, rows, offset, d_offset, d_r, d_h, stream) -> int:
+                       gate_dtype, gate_stride, gate_span, rows, offset, d_offset, d_r, d_h, d_status, stream) -> int:
     """r = x + scale gate drop(N(y)) and h = N(r), or h = N(x); cfg: a Norm."""
     return lib().zccl_residual_norm(ctypes.addressof(cfg), d_x, x_dtype, x_stride, d_y, dtype, y_stride, d_weight,
                                     d_post_weight, weight_dtype, d_gate, gate_dtype, gate_stride, gate_span, rows, offset,
-                                    d_offset, d_r, d_h, stream)
+                                    d_offset, d_r, d_h, d_status, stream)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -430,12 +430,12 @@ def zccl_residual_norm_workspace_bytes(hidden: int, rows: int) -> int:
 def zccl_residual_norm_backward(cfg, d_grad_r, grad_r_stride, d_grad_h, grad_h_stride, d_r, x_dtype, r_stride, d_y, dtype,
                                 y_stride, d_weight, d_post_weight, weight_dtype, d_gate, gate_dtype, gate_stride,
                                 gate_span, rows, offset, d_offset, d_grad_x, d_grad_y, d_grad_weight,
-                                d_grad_post_weight, d_grad_gate, d_ws, ws_bytes, stream) -> int:
+                                d_grad_post_weight, d_grad_gate, d_ws, ws_bytes, d_status, stream) -> int:
     return lib().zccl_residual_norm_backward(ctypes.addressof(cfg), d_grad_r, grad_r_stride, d_grad_h, grad_h_stride, d_r,
                                              x_dtype, r_stride, d_y, dtype, y_stride, d_weight, d_post_weight,
                                              weight_dtype, d_gate, gate_dtype, gate_stride, gate_span, rows, offset,
                                              d_offset, d_grad_x, d_grad_y, d_grad_weight, d_grad_post_weight,
-                                             d_grad_gate, d_ws, ws_bytes, stream)
+                                             d_grad_gate, d_ws, ws_bytes, d_status, stream)
 
 
 def zccl_dropout(d_x, dtype, stride, rows, cols, p, seed, offset, d_offset, d_out, stream_handle) -> int:

@@ -69,12 +69,13 @@ zccl_status_t zccl_residual_norm(const zccl_norm_t* cfg, const void* d_x, int x_
                                  const void* d_y, int dtype, uint64_t y_stride, const void* d_weight,
                                  const void* d_post_weight, int weight_dtype, const void* d_gate, int gate_dtype,
                                  uint64_t gate_stride, uint64_t gate_span, uint64_t rows, uint64_t offset,
-                                 const uint64_t* d_offset, void* d_r, void* d_h, cudaStream_t stream)
+                                 const uint64_t* d_offset, void* d_r, void* d_h, uint32_t* d_status,
+                                 cudaStream_t stream)
 {
     NormArgs a{};
     if (!norm_config(cfg, x_dtype, dtype, d_weight, d_post_weight, weight_dtype, d_gate, gate_dtype, gate_stride, gate_span,
                      rows, offset, d_offset, &a) ||
-        x_stride >= kMaxElems || y_stride >= kMaxElems)
+        x_stride >= kMaxElems || y_stride >= kMaxElems || !is_aligned(d_status, 4))
         return ZCCL_ERR_INVALID_ARG;
     if (rows == 0) return ZCCL_OK;
     const uint64_t xs = size_of(x_dtype), ys = size_of(dtype);
@@ -88,6 +89,7 @@ zccl_status_t zccl_residual_norm(const zccl_norm_t* cfg, const void* d_x, int x_
     a.y_stride = y_stride;
     a.r = d_r;
     a.h = d_h;
+    a.status = d_status;
     const bool vec = a.hidden % 8 == 0 && on_16(d_x, x_dtype, x_stride, rows) && on_16(d_y, dtype, y_stride, rows) &&
                      on_16(d_r, x_dtype, 0, 1) && on_16(d_h, dtype, 0, 1) && on_16(d_weight, weight_dtype, 0, 1) &&
                      on_16(d_post_weight, weight_dtype, 0, 1) && on_16(d_gate, gate_dtype, gate_stride, rows);
@@ -111,12 +113,13 @@ zccl_status_t zccl_residual_norm_backward(const zccl_norm_t* cfg, const void* d_
                                           uint64_t gate_span, uint64_t rows, uint64_t offset,
                                           const uint64_t* d_offset, void* d_grad_x, void* d_grad_y,
                                           void* d_grad_weight, void* d_grad_post_weight, void* d_grad_gate, void* d_ws,
-                                          uint64_t ws_bytes, cudaStream_t stream)
+                                          uint64_t ws_bytes, uint32_t* d_status, cudaStream_t stream)
 {
     NormArgs a{};
     if (!norm_config(cfg, x_dtype, dtype, d_weight, d_post_weight, weight_dtype, d_gate, gate_dtype, gate_stride, gate_span,
                      rows, offset, d_offset, &a) ||
-        grad_r_stride >= kMaxElems || grad_h_stride >= kMaxElems || r_stride >= kMaxElems || y_stride >= kMaxElems)
+        grad_r_stride >= kMaxElems || grad_h_stride >= kMaxElems || r_stride >= kMaxElems || y_stride >= kMaxElems ||
+        !is_aligned(d_status, 4))
         return ZCCL_ERR_INVALID_ARG;
     const uint64_t xs = size_of(x_dtype), ys = size_of(dtype), ws = size_of(weight_dtype);
     const bool join = d_grad_y != nullptr;
@@ -156,6 +159,7 @@ zccl_status_t zccl_residual_norm_backward(const zccl_norm_t* cfg, const void* d_
     a.grad_post_weight = d_grad_post_weight;
     a.grad_gate = d_grad_gate;
     a.sums = static_cast<float*>(d_ws);
+    a.status = d_status;
     const bool vec = a.hidden % 8 == 0 && on_16(a.x, x_dtype, r_stride, rows) && on_16(a.y, dtype, y_stride, rows) &&
                      on_16(d_grad_r, x_dtype, grad_r_stride, rows) && on_16(d_grad_h, dtype, grad_h_stride, rows) &&
                      on_16(d_grad_x, x_dtype, 0, 1) && on_16(d_grad_y, dtype, 0, 1) && on_16(d_weight, weight_dtype, 0, 1) &&

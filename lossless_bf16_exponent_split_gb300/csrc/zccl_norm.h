@@ -19,6 +19,7 @@ struct NormArgs {
     float inv_hidden, eps;
     float factor;        // scale, times the dropout's gain
     DropArgs drop;
+    uint32_t* status;
     void* r;             // forward
     void* h;
     // backward
@@ -75,15 +76,14 @@ struct Shape {
 // 16 warps an SM (128 registers a thread), the SMs taken as 152.  `narrow`: both types
 // have 16 bits and rows begin on 16 bytes, so a warp can hold two tiles: two are better
 // (a row's sums are exchanged by half as many warps) from two tiles on, where they come
-// out even.  A CTA alone takes rows of up to 4096 values, then there are two or more of
-// them an SM, which cover one another's waits; clusters cover their own.
+// out even.
 inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow)
 {
     constexpr uint32_t kSms = 152;
     const uint32_t tiles = (uint32_t)((hidden + kTile - 1) / kTile);
     const uint32_t pieces = narrow && (tiles % 2 == 0 || tiles > 8) ? 2 : 1, units = (tiles + pieces - 1) / pieces;
     // a cluster's CTA holds three rows in shared memory: 15 warps of two 16-bit tiles, or 16 of one tile
-    const uint32_t alone = pieces == 2 ? 8 : 16, most = pieces == 2 ? 15 : 16;
+    const uint32_t alone = 16, most = pieces == 2 ? 15 : 16;
     Shape s{};
     const auto at_most_rows = [&](uint64_t n) { return (uint32_t)(n < rows ? n : rows > 0 ? rows : 1); };
     if (tiles <= 1) {
@@ -135,12 +135,9 @@ __device__ __forceinline__ float warp_sums(const float (&s)[N])
     return v[0];
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync()
 {
-    cluster_arrive();
-    cluster_wait();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_ctas()
 {
@@ -154,12 +151,35 @@ __device__ __forceinline__ uint32_t cluster_rank()
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-// Stores to the same place of CTA `rank` of the cluster.
-__device__ __forceinline__ void st_cluster(float* p, uint32_t rank, float v)
+// Sends v to the same place of CTA `rank` of the cluster, where its arrival counts on the
+// same barrier.
+__device__ __forceinline__ void send(float* p, uint64_t* bar, uint32_t rank, float v)
 {
-    uint32_t at;
+    uint32_t at, to;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_addr(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(at), "r"(__float_as_uint(v)), "r"(to)
+                 : "memory");
+}
+// Bounded wait for what the cluster sends; false if it did not come.
+__device__ __forceinline__ bool wait_sent(uint64_t* bar, uint32_t parity)
+{
+    const auto there = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        return ok != 0;
+    };
+    if (there()) return true;
+    const uint64_t t0 = globaltimer();
+    for (uint32_t it = 1;; ++it) {
+        if (there()) return true;
+        if ((it & 15) == 0 && globaltimer() - t0 > kSpinTimeoutNs) return false;
+    }
 }
 
 // A warp's worker, and its neighbouring tiles of a row.
@@ -174,30 +194,48 @@ __device__ __forceinline__ Place place()
     if (kTeam == kWarpTeam) return {blockIdx.x * kWarpsPerCta + warp, 0};
     if (kTeam == kCtaTeam) return {blockIdx.x, warp * kPieces * kTile};
     const uint32_t ctas = cluster_ctas();
-    cluster_sync();  // the others' shared memory is there
     return {blockIdx.x / ctas, (cluster_rank() * warps + warp) * kPieces * kTile};
 }
 
-// Room for the sums of a team's warps, whose halves take turns by `turn`: a warp may
-// write its sums of the next row while another still reads those of this one, and those
-// of the row after it only when all have been at the barrier between.
+// Room for the sums of a team's warps, whose halves take turns, and a barrier of each
+// half: a warp may put its sums of the next row while another still takes up those of
+// this one; those of the row after it only when all have put the next row's, which they
+// do after they have taken up this one's.
 constexpr uint32_t kTeamRed = 2 * kTeamWarps * kMaxCluster * 8;
+constexpr uint32_t kTeamBytes = kTeamRed * 4 + 16;
 
 // Sums N values (N <= 8) over a team, the same way in every thread, in steps: a warp's
-// own sums (warp_sums), which it puts where all of the team find them, and, behind a
-// barrier, the taking up of all warps'.  The next sums may be put only when these have
-// been waited for: all warps have taken up the ones before then, in whose place they go.
+// own sums (warp_sums), which it puts where all of the team find them, and, after a wait
+// for all warps', the taking up of them.  A cluster's warps send theirs to each of its
+// CTAs, which wait for the bytes to arrive: a cluster barrier would also wait for every
+// store to global memory.
 template <int N, int kTeam>
 struct TeamSum {
     static constexpr int H = kValues<N>, kLanes = 32 / H;
     static constexpr int kRounds = ((int)kTeamWarps * (kTeam == kClusterTeam ? (int)kMaxCluster : 1) * H + 31) / 32;
     float* const red;
-    uint32_t turn = 0;
+    uint64_t* const bar;
+    uint32_t* const status;
+    uint32_t turn = 0, parity = 0;
     float mine = 0.0f;   // a warp that is a team
+    bool lost = false;   // a wait ran out: no other is begun, and all sums are NaN
     const uint32_t all;  // values of the team's warps
-    __device__ __forceinline__ explicit TeamSum(float* red)
-        : red(red), all((blockDim.x >> 5) * (kTeam == kClusterTeam ? cluster_ctas() : 1) * H)
+    __device__ __forceinline__ TeamSum(void* smem, uint32_t* status)
+        : red(static_cast<float*>(smem)), bar(reinterpret_cast<uint64_t*>(red + kTeamRed)), status(status),
+          all((blockDim.x >> 5) * (kTeam == kClusterTeam ? cluster_ctas() : 1) * H)
     {
+        if (kTeam != kClusterTeam) return;
+        if (threadIdx.x == 0) {
+            mbar_init(bar, 1);
+            mbar_init(bar + 1, 1);
+            fence_mbar_init();
+        }
+        cluster_sync();
+    }
+    // Before the kernel ends: no CTA leaves while another may still send to it.
+    __device__ __forceinline__ void close()
+    {
+        if (kTeam == kClusterTeam) cluster_sync();
     }
 
     // v: what warp_sums gave.
@@ -208,17 +246,20 @@ struct TeamSum {
         if (kTeam == kWarpTeam) mine = v;
         if (kTeam == kCtaTeam && lane % kLanes == 0) at[warp * H] = v;
         if (kTeam == kClusterTeam) {
+            if (threadIdx.x == 0) mbar_arrive_expect_tx(bar + turn, all * 4);
             // the lanes that hold a value take a CTA each
-            if (lane % kLanes < cluster_ctas()) st_cluster(at + (cluster_rank() * (blockDim.x >> 5) + warp) * H, lane % kLanes, v);
+            if (lane % kLanes < cluster_ctas()) send(at + (cluster_rank() * (blockDim.x >> 5) + warp) * H, bar + turn, lane % kLanes, v);
             __syncwarp();
-            cluster_arrive();
         }
         turn ^= 1;
     }
     __device__ __forceinline__ void wait()
     {
         if (kTeam == kCtaTeam) __syncthreads();
-        if (kTeam == kClusterTeam) cluster_wait();
+        if (kTeam == kClusterTeam) {
+            if (!lost && !wait_sent(bar + (turn ^ 1), parity)) lost = true;
+            parity ^= turn ^ 1;  // both halves have been used
+        }
     }
     __device__ __forceinline__ void take(float (&s)[N])
     {
@@ -230,6 +271,10 @@ struct TeamSum {
 #pragma unroll
             for (int i = 0; i < kRounds; ++i)
                 if (kTeam == kClusterTeam ? i * 32 < all : true) v += i * 32 + lane < all ? at[i * 32] : 0.0f;
+            if (kTeam == kClusterTeam && __any_sync(0xFFFFFFFFu, lost)) {
+                v = __uint_as_float(0x7FC00000u);
+                if (lane == 0) report(status, ZCCL_ERR_TIMEOUT);
+            }
 #pragma unroll
             for (int o = 16; o >= H; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
         }

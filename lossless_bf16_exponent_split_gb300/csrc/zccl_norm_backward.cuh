@@ -280,7 +280,7 @@ struct Feed<Tx, Ty, false, kPieces, kStages> {
 // A team a worker; the sums over rows stay in registers.  While a gate stays the same
 // the sums of p's and of the gate's gradient are the same up to a factor of each column,
 //   e = sum of (kept) d y eta:   dp += scale gate e,   dgate = scale p e
-// so one sum serves both, and is taken out when the gate changes.  A cluster's barrier
+// so one sum serves both, and is taken out when the gate changes.  A cluster's exchange
 // takes longer than a row's arithmetic, so a cluster sums the next row (kAhead) before it
 // waits for this one's sums.  kKind: as in the forward kernel.
 constexpr int kAny = 4;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
     constexpr uint32_t kWarpParts = Rows::kThreadBytes / 16 * 32 + 2 * kPieces * 32;
     uint4* const warp_smem = smem + (threadIdx.x >> 5) * kWarpParts;
     float4* const dp = reinterpret_cast<float4*>(warp_smem) + Rows::kThreadBytes / 16 * 32 + (threadIdx.x & 31);
-    TeamSum<kTeamSums, kTeam> team_sum(reinterpret_cast<float*>(smem + (blockDim.x >> 5) * kWarpParts));
+    TeamSum<kTeamSums, kTeam> team_sum(smem + (blockDim.x >> 5) * kWarpParts, a.status);
     pdl_wait();
     const Place at = place<kTeam, kPieces>();
     const bool join = a.grad_y != nullptr, reads_y = a.y != nullptr;
@@ -444,6 +444,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
             if (turns) set_gate(t + 1);
         }
     }
+    team_sum.close();
     if (reads_y && lo < hi) take_out(hi);
     pdl_launch_dependents();
     // the weights' sums, of a CTA's warps where each is a team

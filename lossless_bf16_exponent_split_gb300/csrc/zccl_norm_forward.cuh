@@ -63,8 +63,8 @@ template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces, int kKind
 __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeamWarps * 32, kTeam == kWarpTeam ? 2 : 1)
     norm_kernel(NormArgs a)
 {
-    __shared__ float red[kTeam == kWarpTeam ? 1 : kTeamRed];
-    TeamSum<1, kTeam> team_sum(red);
+    __shared__ __align__(16) char red[kTeam == kWarpTeam ? 16 : kTeamBytes];
+    TeamSum<1, kTeam> team_sum(red, a.status);
     pdl_wait();
     const Place at = place<kTeam, kPieces>();
     if (kTeam == kWarpTeam && at.worker >= a.workers) return;
@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
         for (int n = 0; n < kPieces; ++n) store8<Ty, kVec>(h_at, mul(mul(x[n], rho), w[n]), at.tile(n), a.hidden);
         h_at += a.hidden;
     }
+    team_sum.close();
 }
 
 template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces>

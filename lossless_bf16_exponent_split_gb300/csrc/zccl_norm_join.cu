@@ -141,7 +141,7 @@ zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weig
             : (dtype == ZCCL_BF16 ? norm_backward_kernel_for<float, __nv_bfloat16>(s, vec, post, drop, &thread_bytes)
                                   : norm_backward_kernel_for<float, float>(s, vec, post, drop, &thread_bytes));
     const uint32_t threads = s.warps * 32;
-    const size_t smem = s.team == kLong ? 0 : threads * thread_bytes + kTeamRed * sizeof(float);
+    const size_t smem = s.team == kLong ? 0 : threads * thread_bytes + kTeamBytes;
     cudaError_t e = cudaSuccess;
     if (smem > 48 << 10) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess)

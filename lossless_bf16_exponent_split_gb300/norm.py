@@ -15,7 +15,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import BF16, F32, MAX_NORM_HIDDEN, Norm, check, lib, zccl_residual_norm_workspace_bytes
+from . import BF16, F32, MAX_NORM_HIDDEN, OK, Norm, ZcclError, check, lib, zccl_residual_norm_workspace_bytes
 from .moe import Workspaces, current_stream, need
 
 _DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
@@ -57,7 +57,8 @@ def _stride(t):
 
 class ResidualNorm:
     """The join of a block's output with the residual, and the norm of the next
-    block's input; any streams and host threads may share one.
+    block's input, and a device status word; any streams and host threads may share
+    one.
 
         r = x + scale * gate * drop(b),  h = N(r; weight)
         b = N(y; post_weight) with post, else y
@@ -78,9 +79,23 @@ class ResidualNorm:
         self._lib = lib()
         # the library's own check of the configuration (no rows: nothing is launched)
         check(self._lib.zccl_residual_norm(self._config, None, F32, 0, None, F32, 0, None, None, F32, None, F32, 0, 1, 0,
-                                           0, None, None, None, None), "ResidualNorm")
+                                           0, None, None, None, None, None), "ResidualNorm")
         self.device = torch.zeros(0, device=device if device is not None else "cuda").device
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._status = self.status.data_ptr()
         self._workspaces = Workspaces(zeroed=False, most=64 << 20)
+
+    # -- status ---------------------------------------------------------------
+    def reset_status(self):
+        self.status.zero_()
+
+    def read_status(self) -> int:
+        return int(self.status.item())
+
+    def check_status(self, what="device"):
+        st = self.read_status()
+        if st != OK:
+            raise ZcclError(st, what)
 
     # -- arguments ------------------------------------------------------------
     def _rows(self, t, what, rows=None, dtype=None):
@@ -128,7 +143,7 @@ class ResidualNorm:
         h = torch.empty(rows, self.hidden, dtype=dtype, device=self.device)
         st = self._lib.zccl_residual_norm(self._config, x.data_ptr(), _DTYPES[x.dtype], _stride(x), None, _DTYPES[dtype], 0,
                                           _ptr(weight), None, wt, None, F32, 0, 1, rows, 0, None, None, h.data_ptr(),
-                                          current_stream(self.device))
+                                          self._status, current_stream(self.device))
         check(st, "zccl_residual_norm")
         return h
 
@@ -160,7 +175,7 @@ class ResidualNorm:
         st = self._lib.zccl_residual_norm(self._config, x.data_ptr(), _DTYPES[x.dtype], _stride(x), y.data_ptr(),
                                           _DTYPES[y.dtype], _stride(y), _ptr(weight), _ptr(post_weight), wt, gate_ptr,
                                           gate_type, gate_stride, span, rows, value, at, r.data_ptr(), _ptr(h),
-                                          current_stream(self.device))
+                                          self._status, current_stream(self.device))
         check(st, "zccl_residual_norm")
         return r, h
 
@@ -205,7 +220,7 @@ class ResidualNorm:
                 0 if grad_h is None else _stride(r), _ptr(y), _DTYPES[dtype], 0 if y is None else _stride(y), _ptr(weight),
                 _ptr(post_weight), wt, gate_ptr, gate_type, gate_stride, span, rows, value, at,
                 None if grad_h is None else gx.data_ptr(), _ptr(gy), _ptr(gw), _ptr(gp), _ptr(gg), ws.data_ptr(),
-                ws.numel(), stream)
+                ws.numel(), self._status, stream)
         check(st, "zccl_residual_norm_backward")
         return gx, gy, gw, gp, gg
 

@@ -52,6 +52,9 @@ CASES = [  # rows, hidden, residual, block, weight (None: no weights), post, gat
     (12, 8192, B, B, F, True, 1, 1.0, 0.1),
     (10, 8200, B, B, B, False, 5, 1.0, 0.0),
     (9, 14336, B, B, B, True, 3, 0.25, 0.0),
+    (7, 16384, B, B, F, True, 7, 1.0, 0.1),       # clusters of four
+    (300, 12000, F, F, F, True, 3, 1.0, 0.1),
+    (400, 9600, B, B, B, False, 4, 1.0, 0.2),     # clusters of two, several rows each
     (6, 16385, F, B, F, True, 2, 1.0, 0.1),
     (5, 65536, B, B, F, True, 1, 1.0, 0.0),
     (2500, 64, B, B, F, True, 50, 1.0, 0.0),      # more rows than workers, gate rows shared by some
@@ -108,6 +111,7 @@ def test_forward_and_gradients(z, case):
         assert got.x.dtype == residual and got.y.dtype == block
         again = n.add_backward(gr, gh, None if gh is None else r, y, weights, offset=offset, **more)
         assert all(a is None or torch.equal(a, b) for a, b in zip(got, again))  # no order changes
+    n.check_status()
 
 
 @pytest.mark.parametrize("rows,hidden,residual,block,weight", [
@@ -154,7 +158,7 @@ def test_strided_rows_give_the_same(z, hidden):
     place = x.clone()
     st = z.zccl_residual_norm(n.config, place.data_ptr(), z.BF16, hidden, y.data_ptr(), z.BF16, hidden, w.data_ptr(),
                               more["post_weight"].data_ptr(), z.F32, more["gate"].data_ptr(), z.BF16, hidden, 4, rows, 5,
-                              None, place.data_ptr(), h.data_ptr(), torch.cuda.current_stream().cuda_stream)
+                              None, place.data_ptr(), h.data_ptr(), None, torch.cuda.current_stream().cuda_stream)
     assert st == z.OK and torch.equal(place, r)
 
 
@@ -170,7 +174,7 @@ def test_nothing_is_written_outside(z):
         at = [o.data_ptr() + 256 * o.element_size() for o in outs]
         assert z.zccl_residual_norm(n.config, x.data_ptr(), z.BF16, hidden, y.data_ptr(), z.F32, hidden, w.data_ptr(),
                                     more["post_weight"].data_ptr(), z.F32, more["gate"].data_ptr(), z.F32, hidden, 1, rows, 0,
-                                    None, *at, stream) == z.OK
+                                    None, *at, None, stream) == z.OK
         nbytes = z.zccl_residual_norm_workspace_bytes(hidden, rows)
         ws = torch.full((nbytes + 512,), 7, dtype=torch.uint8, device="cuda")
         backs = [guarded(size, B), guarded(size, F), guarded(hidden, F), guarded(hidden, F), guarded(size, F)]
@@ -179,7 +183,7 @@ def test_nothing_is_written_outside(z):
         assert z.zccl_residual_norm_backward(
             n.config, grad_r.data_ptr(), hidden, grad_h.data_ptr(), hidden, r.data_ptr(), z.BF16, hidden, y.data_ptr(), z.F32,
             hidden, w.data_ptr(), more["post_weight"].data_ptr(), z.F32, more["gate"].data_ptr(), z.F32, hidden, 1, rows, 0, None,
-            *places, ws.data_ptr() + 256, nbytes, stream) == z.OK
+            *places, ws.data_ptr() + 256, nbytes, None, stream) == z.OK
         for o in outs + backs:
             count = o.numel() - 512
             assert bool((o[:256] == 7).all()) and bool((o[256 + count:] == 7).all())

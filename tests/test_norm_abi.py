@@ -29,7 +29,7 @@ BAD_CONFIGS = [dict(hidden=0), dict(hidden=65537), dict(eps=0.0), dict(eps=-1.0)
 def test_norm_refusals(z):
     ok = dict(d_x=A, x_dtype=z.BF16, x_stride=16, d_y=A, dtype=z.BF16, y_stride=16, d_weight=A, d_post_weight=A,
               weight_dtype=z.F32, d_gate=A, gate_dtype=z.BF16, gate_stride=16, gate_span=1, rows=4, offset=0, d_offset=None,
-              d_r=A, d_h=A, stream=None)
+              d_r=A, d_h=A, d_status=A, stream=None)
 
     def call(c=None, **kw):
         return z.zccl_residual_norm(c or config(z), **dict(ok, **kw))
@@ -39,7 +39,7 @@ def test_norm_refusals(z):
     for kw in (dict(d_x=None), dict(d_x=A + 1), dict(x_dtype=2), dict(dtype=-1), dict(weight_dtype=2), dict(gate_dtype=7),
                dict(d_y=A + 1), dict(d_weight=A + 2), dict(d_post_weight=A + 1), dict(d_gate=A + 1), dict(gate_span=0),
                dict(rows=1 << 31), dict(x_stride=1 << 40), dict(y_stride=1 << 40), dict(gate_stride=1 << 40),
-               dict(d_offset=A + 4), dict(d_r=None), dict(d_r=A + 1), dict(d_h=A + 1),
+               dict(d_offset=A + 4), dict(d_r=None), dict(d_r=A + 1), dict(d_h=A + 1), dict(d_status=A + 2),
                dict(d_y=None),                                      # a join's output without a join
                dict(d_y=None, d_r=None),                            # its weights too
                dict(d_y=None, d_r=None, d_gate=None),
@@ -48,7 +48,7 @@ def test_norm_refusals(z):
                dict(x_stride=24)):                                  # rows of x and r in one place, apart differently
         assert call(**kw) == z.INVALID_ARG, kw
     assert call(config(z, post=0)) == z.INVALID_ARG                 # a post weight without post
-    assert z.lib().zccl_residual_norm(None, A, 0, 16, A, 0, 16, A, A, 1, A, 0, 16, 1, 4, 0, None, A, A, None) == z.INVALID_ARG
+    assert z.lib().zccl_residual_norm(None, A, 0, 16, A, 0, 16, A, A, 1, A, 0, 16, 1, 4, 0, None, A, A, None, None) == z.INVALID_ARG
     assert call(rows=0, d_x=None, d_y=None, d_r=None, d_h=None) == z.OK
 
 
@@ -57,7 +57,7 @@ def test_norm_backward_refusals(z):
     ok = dict(d_grad_r=A, grad_r_stride=16, d_grad_h=A, grad_h_stride=16, d_r=A, x_dtype=z.F32, r_stride=16, d_y=A,
               dtype=z.BF16, y_stride=16, d_weight=A, d_post_weight=A, weight_dtype=z.F32, d_gate=A, gate_dtype=z.BF16,
               gate_stride=16, gate_span=2, rows=4, offset=0, d_offset=None, d_grad_x=A, d_grad_y=A, d_grad_weight=A,
-              d_grad_post_weight=A, d_grad_gate=A, d_ws=A, ws_bytes=need, stream=None)
+              d_grad_post_weight=A, d_grad_gate=A, d_ws=A, ws_bytes=need, d_status=None, stream=None)
 
     def call(c=None, **kw):
         return z.zccl_residual_norm_backward(c or config(z), **dict(ok, **kw))
@@ -71,7 +71,7 @@ def test_norm_backward_refusals(z):
                dict(d_weight=None), dict(d_post_weight=None), dict(d_gate=None),  # gradients of what is not there
                dict(d_grad_y=None),                                              # a norm alone with a join's weights
                dict(rows=1 << 31), dict(grad_r_stride=1 << 40), dict(grad_h_stride=1 << 40), dict(r_stride=1 << 40),
-               dict(y_stride=1 << 40), dict(d_ws=None), dict(d_ws=A + 8), dict(d_offset=A + 4)):
+               dict(y_stride=1 << 40), dict(d_ws=None), dict(d_ws=A + 8), dict(d_offset=A + 4), dict(d_status=A + 1)):
         assert call(**kw) == z.INVALID_ARG, kw
     alone = dict(d_grad_y=None, d_gate=None, d_grad_gate=None, d_post_weight=None, d_grad_post_weight=None)
     assert call(**alone, d_grad_x=None, d_grad_weight=None) == z.INVALID_ARG  # nothing is wanted
