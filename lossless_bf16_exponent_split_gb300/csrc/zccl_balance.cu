@@ -125,10 +125,15 @@ __device__ __forceinline__ bool part_of(const BalanceArgs& a, Part* p)
     return p->parts > 0;
 }
 
-// A lane's logits of a token, as they are held in memory: with kVec eight neighbours
-// at a time, else L apart.
-template <typename T, bool kVec, int L, int J>
+// How a token's logits are read: eight neighbours at a time (kNeighbours; kWhole: and the
+// experts are as many as L lanes of J hold), or one by one.
+enum Read { kOneByOne = 0, kNeighbours = 1, kWhole = 2 };
+
+// A lane's logits of a token, as they are held in memory: eight neighbours at a time, or
+// L apart.
+template <typename T, int kRead, int L, int J>
 struct Logits {
+    static constexpr bool kVec = kRead != kOneByOne;
     static constexpr int kWords = kVec ? J * sizeof(T) / 16 : 0;
     uint4 q[kVec ? kWords : 1];
     float f[kVec ? 1 : J];
@@ -161,16 +166,16 @@ struct Logits {
                 const uint32_t w = (j * sizeof(T) / 4) % 4, x = w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
                 l[j] = sizeof(T) == 4 ? __uint_as_float(x) : j & 1 ? bf16_hi(x) : bf16_lo(x);
             }
-            if (expert(li, j) >= E) l[j] = -kInf;
+            if (kRead != kWhole && expert(li, j) >= E) l[j] = -kInf;
         }
     }
 };
 
-template <typename T, bool kVec, int L, int J>
+template <typename T, int kRead, int L, int J>
 __device__ __forceinline__ void store_row(T* row, const float (&g)[J], uint32_t li, uint32_t E)
 {
-    using Row = Logits<T, kVec, L, J>;
-    if (kVec) {
+    using Row = Logits<T, kRead, L, J>;
+    if (Row::kVec) {
         constexpr int kEach = 16 / sizeof(T);
 #pragma unroll
         for (int i = 0; i < Row::kWords; ++i) {
@@ -207,32 +212,46 @@ __device__ __forceinline__ float reciprocal(float x)
 template <bool kSlope, int L, int J>
 __device__ __forceinline__ float scores(const BalanceArgs& a, const float (&l)[J], float (&p)[J], float (&slope)[J])
 {
-    float m = l[0];
+    const auto largest = [&]() {
+        float m = l[0];
 #pragma unroll
-    for (int j = 1; j < J; ++j) m = fmaxf(m, l[j]);
+        for (int j = 1; j < J; ++j) m = fmaxf(m, l[j]);
 #pragma unroll
-    for (int o = L / 2; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    float total = 0.0f;
+        for (int o = L / 2; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        return m == -kInf ? 0.0f : m;
+    };
+    const auto sum = [&]() {
+        float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < J; j += 2) s = __fadd2_rn(s, make_float2(p[j], p[j + 1]));
+        return lanes_add<L>(s.x + s.y);
+    };
+    float total;
     if (a.sigmoid) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const float t = exp_fast(-fabsf(l[j])), r = reciprocal(1.0f + t);
-            p[j] = l[j] >= 0.0f ? r : t * r;
-            if (kSlope) slope[j] = l[j] >= 0.0f ? t * r : r;
+        for (int j = 0; j < J; j += 2) {
+            const float2 t = make_float2(exp_fast(-fabsf(l[j])), exp_fast(-fabsf(l[j + 1])));
+            const float2 n = __fadd2_rn(t, make_float2(1.0f, 1.0f)), r = make_float2(reciprocal(n.x), reciprocal(n.y));
+            const float2 tr = __fmul2_rn(t, r);
+            p[j] = l[j] >= 0.0f ? r.x : tr.x;
+            p[j + 1] = l[j + 1] >= 0.0f ? r.y : tr.y;
+            if (kSlope) slope[j] = l[j] >= 0.0f ? tr.x : r.x, slope[j + 1] = l[j + 1] >= 0.0f ? tr.y : r.y;
         }
-        // scores that are all below 2^-86: over a common factor, which keeps the largest from underflow (1 + exp(l) is 1)
-        if (m < -60.0f)
+        total = sum();
+        // scores whose sum is below 2^-80: over a common factor, which keeps the largest from underflow (1 + exp(l) is 1)
+        if (__any_sync(0xFFFFFFFFu, total < 0x1p-80f)) {
+            const float m = largest();
 #pragma unroll
-            for (int j = 0; j < J; ++j) p[j] = m == -kInf ? 0.0f : exp_fast(l[j] - m);
+            for (int j = 0; j < J; ++j) p[j] = total < 0x1p-80f ? exp_fast(l[j] - m) : p[j];
+            total = sum();
+        }
     } else {
-        if (m == -kInf) m = 0.0f;
+        const float m = largest();
 #pragma unroll
         for (int j = 0; j < J; ++j) p[j] = exp_fast(l[j] - m);
+        total = sum();
     }
-#pragma unroll
-    for (int j = 0; j < J; ++j) total += p[j];
-    total = lanes_add<L>(total);
-    return total == 0.0f ? 0.0f : 1.0f / total;
+    return total == 0.0f ? 0.0f : reciprocal(total);
 }
 
 // A lane's experts of a token (entries L apart).
@@ -272,7 +291,7 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t n)
     return before == n - 1;
 }
 
-template <typename T, bool kVec, int L, int J>
+template <typename T, int kRead, int L, int J>
 __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
 {
     constexpr int kExperts = L * J, kTokens = 32 / L;
@@ -291,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
     const uint64_t lo = part.lo, hi = part.hi;
     float sum[J] = {};
     int32_t live = 0;
-    Logits<T, kVec, L, J> row;
+    Logits<T, kRead, L, J> row;
     const T* const logits = static_cast<const T*>(a.logits);
     const uint64_t t0 = lo + warp * kTokens + lane / L;
     Choices<L> next;
@@ -311,7 +330,10 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
             for (int j = 0; j < J; ++j) l[j] = -kInf;  // whatever it holds
         const float f = scores<false, L, J>(a, l, p, slope);
 #pragma unroll
-        for (int j = 0; j < J; ++j) sum[j] = fmaf(p[j], f, sum[j]);
+        for (int j = 0; j < J; j += 2) {
+            const float2 v = __ffma2_rn(make_float2(p[j], p[j + 1]), make_float2(f, f), make_float2(sum[j], sum[j + 1]));
+            sum[j] = v.x, sum[j + 1] = v.y;
+        }
     }
     // over the warp's tokens
 #pragma unroll
@@ -421,7 +443,7 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
     }
 }
 
-template <typename T, bool kVec, int L, int J>
+template <typename T, int kRead, int L, int J>
 __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs a)
 {
     constexpr int kTokens = 32 / L;
@@ -433,7 +455,7 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs 
     const uint64_t lo = part.lo, hi = part.hi;
     const bool counted = s < a.sequences;
     if (lo >= hi || (!counted && a.accumulate)) return;
-    Logits<T, kVec, L, J> row;
+    Logits<T, kRead, L, J> row;
     const T* const logits = static_cast<const T*>(a.logits);
     const uint64_t t0 = lo + warp * kTokens + lane / L;
     Choices<L> next;
@@ -469,46 +491,56 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs 
 #pragma unroll
             for (int j = 0; j < J; ++j) l[j] = -kInf;  // whatever it holds
         const float share = scores<true, L, J>(a, l, g, slope);
-        float sum = 0.0f;
+        float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            g[j] *= share;
-            sum = fmaf(f[j], g[j], sum);
+        for (int j = 0; j < J; j += 2) {
+            const float2 q = __fmul2_rn(make_float2(g[j], g[j + 1]), make_float2(share, share));
+            part = __ffma2_rn(q, make_float2(f[j], f[j + 1]), part);
+            g[j] = q.x, g[j + 1] = q.y;
         }
-        sum = lanes_add<L>(sum);
+        const float sum = lanes_add<L>(part.x + part.y);
 #pragma unroll
-        for (int j = 0; j < J; ++j) g[j] *= a.sigmoid ? slope[j] * (f[j] - sum) : f[j] - sum;
+        for (int j = 0; j < J; j += 2) {
+            float2 q = __fmul2_rn(make_float2(g[j], g[j + 1]), __fadd2_rn(make_float2(f[j], f[j + 1]), make_float2(-sum, -sum)));
+            if (a.sigmoid) q = __fmul2_rn(q, make_float2(slope[j], slope[j + 1]));
+            g[j] = q.x, g[j + 1] = q.y;
+        }
         if (!there || (a.accumulate && !counts)) continue;
         T* out = static_cast<T*>(a.grad) + t * a.grad_stride;
         if (a.accumulate) {
-            Logits<T, kVec, L, J> old;
+            Logits<T, kRead, L, J> old;
             old.load(out, li, a.E);
             old.get(l, li, a.E);
 #pragma unroll
             for (int j = 0; j < J; ++j) g[j] += l[j];
         }
-        store_row<T, kVec, L, J>(out, g, li, a.E);
+        store_row<T, kRead, L, J>(out, g, li, a.E);
     }
 }
 
 using BalanceKernel = void (*)(BalanceArgs);
-template <typename T, bool kVec>
+template <typename T, int kRead>
 BalanceKernel balance_for(uint32_t experts, bool backward)
 {
-    if (experts <= 64) return backward ? balance_backward_kernel<T, kVec, 8, 8> : balance_kernel<T, kVec, 8, 8>;
-    if (experts <= 128) return backward ? balance_backward_kernel<T, kVec, 16, 8> : balance_kernel<T, kVec, 16, 8>;
-    if (experts <= 256) return backward ? balance_backward_kernel<T, kVec, 32, 8> : balance_kernel<T, kVec, 32, 8>;
-    return backward ? balance_backward_kernel<T, kVec, 32, 16> : balance_kernel<T, kVec, 32, 16>;
+    if (experts <= 64) return backward ? balance_backward_kernel<T, kRead, 8, 8> : balance_kernel<T, kRead, 8, 8>;
+    if (experts <= 128) return backward ? balance_backward_kernel<T, kRead, 16, 8> : balance_kernel<T, kRead, 16, 8>;
+    if (experts <= 256) return backward ? balance_backward_kernel<T, kRead, 32, 8> : balance_kernel<T, kRead, 32, 8>;
+    return backward ? balance_backward_kernel<T, kRead, 32, 16> : balance_kernel<T, kRead, 32, 16>;
+}
+template <typename T>
+BalanceKernel balance_for(const BalanceArgs& a, bool backward)
+{
+    const auto on_16 = [&](const void* p, uint64_t stride) {
+        return is_aligned(p, 16) && (a.tokens <= 1 || stride * sizeof(T) % 16 == 0);
+    };
+    if (a.E % 8 != 0 || !on_16(a.logits, a.stride) || (backward && !on_16(a.grad, a.grad_stride)))
+        return balance_for<T, kOneByOne>(a.E, backward);
+    const bool whole = a.E == 64 || a.E == 128 || a.E == 256 || a.E == ZCCL_MAX_EXPERTS;
+    return whole ? balance_for<T, kWhole>(a.E, backward) : balance_for<T, kNeighbours>(a.E, backward);
 }
 BalanceKernel balance_for(const BalanceArgs& a, int dtype, bool backward)
 {
-    const uint64_t size = dtype == ZCCL_BF16 ? 2 : 4;
-    const auto on_16 = [&](const void* p, uint64_t stride) {
-        return is_aligned(p, 16) && (a.tokens <= 1 || stride * size % 16 == 0);
-    };
-    const bool vec = a.E % 8 == 0 && on_16(a.logits, a.stride) && (!backward || on_16(a.grad, a.grad_stride));
-    if (dtype == ZCCL_BF16) return vec ? balance_for<__nv_bfloat16, true>(a.E, backward) : balance_for<__nv_bfloat16, false>(a.E, backward);
-    return vec ? balance_for<float, true>(a.E, backward) : balance_for<float, false>(a.E, backward);
+    return dtype == ZCCL_BF16 ? balance_for<__nv_bfloat16>(a, backward) : balance_for<float>(a, backward);
 }
 
 // Tokens of a part, and the CTAs that there are parts for.  One sequence: as many parts
