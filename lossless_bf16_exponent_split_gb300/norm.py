@@ -147,12 +147,17 @@ class ResidualNorm:
         check(st, "zccl_residual_norm")
         return h
 
-    def norm_backward(self, grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None = None):
+    def norm_backward(self, grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None = None,
+                      residual: torch.Tensor | None = None):
         """(gradient of x, in its type; gradient of the weight, in its type, or None)
-        from the gradient of norm's output."""
+        from the gradient of norm's output; residual: a gradient of x from elsewhere (of
+        its type, rows may be strided), which is added."""
         self._rows(x, "x")
-        self._rows(grad, "grad", x.shape[0])
-        gx, _, gw, _, _ = self._backward(None, grad, x, None, weight, None, None, 0, x.shape[0], x.dtype, grad.dtype)
+        rows = x.shape[0]
+        self._rows(grad, "grad", rows)
+        if residual is not None:
+            self._rows(residual, "residual", rows, x.dtype)
+        gx, _, gw, _, _ = self._backward(residual, grad, x, None, weight, None, None, 0, rows, x.dtype, grad.dtype)
         return gx, gw
 
     def add(self, x: torch.Tensor, y: torch.Tensor, weight: torch.Tensor | None = None, *,
