@@ -530,9 +530,10 @@ zccl_status_t zccl_fp8_linear_backward(const void* d_grad, const void* d_x, int 
  * block's input:
  *   N(v; w)[i] = w[i] * v[i] / sqrt(mean of v[j]^2 + eps)       (w NULL: 1)
  *   b = N(y; post_weight) with cfg->post, else y
- *   r = x + scale * gate * drop(b)                   (gate NULL: 1), rounded once
+ *   r = x + (scale * gate) * drop(b)                 (gate NULL: 1), rounded once
  *   h = N(r; weight), of r as it is stored                          rounded once
- * in fp32.  drop is zccl_dropout's, on row t and column i; a dropped element adds
+ * in fp32 (the dropout's factor multiplies scale * gate; the product joins x by an
+ * addition of its own).  drop is zccl_dropout's, on row t and column i; a dropped element adds
  * nothing, whatever it holds.  A row whose sum of squares is beyond fp32 gives
  * what that makes of the formula (zeros; NaN where it is infinite already). */
 #define ZCCL_MAX_NORM_HIDDEN 65536u /* values of a row                             */

@@ -33,7 +33,9 @@ bool norm_config(const zccl_norm_t* c, int x_dtype, int dtype, const void* d_wei
     a->post = c->post != 0;
     a->inv_hidden = 1.0f / (float)c->hidden;
     a->eps = c->eps;
-    a->factor = c->scale * (a->drop.below > 0 ? a->drop.gain : 1.0f);
+    a->scale = c->scale;
+    a->gain = a->drop.below > 0 ? a->drop.gain : 1.0f;
+    a->factor = a->scale * a->gain;
     return true;
 }
 

@@ -17,7 +17,8 @@ struct NormArgs {
     uint32_t hidden;
     int post;
     float inv_hidden, eps;
-    float factor;        // scale, times the dropout's gain
+    float scale, gain;   // of the join, and of its dropout (1 without)
+    float factor;        // their product
     DropArgs drop;
     uint32_t* status;
     void* r;             // forward
@@ -325,7 +326,8 @@ inline uint64_t norm_backward_bytes(const Shape& s, uint64_t hidden)
 template <bool kVec>
 __device__ __forceinline__ Eight join_factors(const NormArgs& a, uint32_t row, uint32_t tile)
 {
-    return mul(load_vector<kVec>(a.gate, a.gate.p != nullptr ? (uint64_t)(row / a.gate_span) * a.gate_stride : 0, tile, a.hidden), a.factor);
+    const uint64_t at = a.gate.p != nullptr ? (uint64_t)(row / a.gate_span) * a.gate_stride : 0;
+    return mul(mul(load_vector<kVec>(a.gate, at, tile, a.hidden), a.scale), a.gain);
 }
 // Which of the lane's values of it stay.
 template <bool kVec>

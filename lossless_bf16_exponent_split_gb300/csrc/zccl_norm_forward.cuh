@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_long_kernel(NormArgs a)
             if (a.y != nullptr) {
                 const Eight k = mul(join_factors<kVec>(a, t, tile), load_vector<kVec>(a.post_weight, 0, tile, a.hidden));
                 const Eight b = mul(load8<Ty, kVec>(y, tile, a.hidden), eta);
-                v = where_kept<kVec>(join_kept<kVec>(a, offset, t, tile), fma(k, b, v), v);
+                v = where_kept<kVec>(join_kept<kVec>(a, offset, t, tile), mul_then_add(k, b, v), v);
                 v = store8<Tx, kVec>(r, v, tile, a.hidden);
             }
             dot(sum, v, v);
@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
             }
 #pragma unroll
             for (int n = 0; n < kPieces; ++n) {
-                const Eight r = fma(k[n], y[n], x[n]);
+                // the product rounded by itself: without post r then has the bits of the formula's operations in their order
+                const Eight r = mul_then_add(k[n], y[n], x[n]);
                 x[n] = drop ? where_kept<kVec>(kept_piece<kVec>(a.drop, offset, t, at.tile(n)), r, x[n]) : r;
                 x[n] = store8<Tx, kVec>(r_at, x[n], at.tile(n), a.hidden);
             }

@@ -37,6 +37,16 @@ __device__ __forceinline__ Eight mul(const Eight& a, const Eight& b)
     return o;
 }
 __device__ __forceinline__ Eight mul(const Eight& a, float s) { return mul(a, all_eight(s)); }
+// a b + c with both operations rounded: products of two values an instruction would be
+// fused with the addition.
+__device__ __forceinline__ Eight mul_then_add(const Eight& a, const Eight& b, const Eight& c)
+{
+    Eight o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o.v[i] = __fadd2_rn(make_float2(__fmul_rn(a.v[i].x, b.v[i].x), __fmul_rn(a.v[i].y, b.v[i].y)), c.v[i]);
+    return o;
+}
 __device__ __forceinline__ Eight fma(const Eight& a, const Eight& b, const Eight& c)
 {
     Eight o;

@@ -231,6 +231,18 @@ def test_large_and_small_values(z):
         close(h, at.h(r), at.h(r).abs(), "h")
 
 
+@pytest.mark.parametrize("rows,hidden,gates,dropout", [(300, 696, 1, 0.0), (40, 4104, 4, 0.3), (3, 20000, 3, 0.3), (129, 77, 1, 0.1)])
+def test_join_has_the_bits_of_its_operations(z, rows, hidden, gates, dropout):
+    """Without a norm after the block: each product and sum in 32 bits, rounded in the documented order."""
+    n, x, y, _, more, _, _ = inputs(z, rows, hidden, B, F, None, False, gates, 0.3, dropout)
+    r, _ = n.add(x, y, normed=False, offset=9, **more)
+    k = more["gate"].repeat_interleave(rows // gates, 0) * torch.tensor(0.3, device="cuda")
+    want = x.float() + (k * torch.tensor(ref.gain(dropout), device="cuda") if dropout else k) * y
+    if dropout:
+        want = torch.where(ref.kept(rows, hidden, dropout, 0xFEDCBA9876543210, 9).cuda(), want, x.float())
+    assert torch.equal(r, want.bfloat16())
+
+
 def test_offset_on_the_device_in_a_graph(z):
     """Captured once, replayed with an offset that the graph moves on, beside a second graph and eager calls."""
     n, x, y, w, more, grad_r, grad_h = inputs(z, 50, 2048, B, B, F, True, 2, 1.0, 0.3)
