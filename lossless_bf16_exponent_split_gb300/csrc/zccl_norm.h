@@ -78,7 +78,7 @@ struct Shape {
 // have 16 bits and rows begin on 16 bytes, so a warp can hold two tiles: two are better
 // (a row's sums are exchanged by half as many warps) from two tiles on, where they come
 // out even.
-inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow)
+inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow, bool backward)
 {
     constexpr uint32_t kSms = 152;
     const uint32_t tiles = (uint32_t)((hidden + kTile - 1) / kTile);
@@ -92,6 +92,9 @@ inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow)
         s.grid = (s.workers + kWarpsPerCta - 1) / kWarpsPerCta;
     } else if (units <= most * kMaxCluster && tiles <= kTeamWarps * kMaxCluster) {
         s.ctas = units <= alone ? 1 : units <= 2 * most ? 2 : 4;
+        // 9 or 10 warps leave a third of an SM empty, three clusters' CTAs of 5 do not: 5120 columns forward 45.9 us,
+        // 51.4 with 10 warps; not so the gradients (64.8 and 63.0), with three rows in shared memory
+        if (!backward && (units == 9 || units == 10)) s.ctas = 2;
         s.team = s.ctas > 1 ? kClusterTeam : kCtaTeam;
         s.pieces = pieces;
         s.warps = (units + s.ctas - 1) / s.ctas;

@@ -156,10 +156,15 @@ struct Feed;
 // Rows on 16 bytes come by asynchronous copies into places of the thread's own, so that
 // no thread waits for another's and no registers are held.  A lane's addresses move on
 // from row to row; what it copies lies at constant distances from them.
-template <int kTo, int kFrom>
+// (past L1 where a lane's 16 bytes are all it wants of a 32-byte sector's neighbours; of
+// 32-bit values it wants the other half too.)
+template <bool kPast, int kTo, int kFrom>
 __device__ __forceinline__ void copy_16(uint32_t to, const char* from, uint32_t bytes)
 {
-    asm volatile("cp.async.ca.shared.global [%0+%3], [%1+%4], 16, %2;" ::"r"(to), "l"(from), "r"(bytes), "n"(kTo), "n"(kFrom) : "memory");
+    if (kPast)
+        asm volatile("cp.async.cg.shared.global [%0+%3], [%1+%4], 16, %2;" ::"r"(to), "l"(from), "r"(bytes), "n"(kTo), "n"(kFrom) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0+%3], [%1+%4], 16, %2;" ::"r"(to), "l"(from), "r"(bytes), "n"(kTo), "n"(kFrom) : "memory");
 }
 template <typename Tx, typename Ty, int kPieces, int kStages>
 struct Feed<Tx, Ty, true, kPieces, kStages> {
@@ -193,8 +198,8 @@ struct Feed<Tx, Ty, true, kPieces, kStages> {
     template <typename T, int kPart, int n>
     __device__ __forceinline__ void copy_piece(const char* from)
     {
-        copy_16<(n * kAll + kPart) * 512, n * (int)(kTile * sizeof(T))>(to, from, bytes[n]);
-        if constexpr (sizeof(T) == 4) copy_16<(n * kAll + kPart + 1) * 512, n * (int)(kTile * sizeof(T)) + 16>(to, from, bytes[n]);
+        copy_16<sizeof(T) == 2, (n * kAll + kPart) * 512, n * (int)(kTile * sizeof(T))>(to, from, bytes[n]);
+        if constexpr (sizeof(T) == 4) copy_16<false, (n * kAll + kPart + 1) * 512, n * (int)(kTile * sizeof(T)) + 16>(to, from, bytes[n]);
     }
     // Asks for the next row (there: it is one of the worker's).
     __device__ __forceinline__ void ask(const NormArgs& a, const Place&, bool there)
@@ -408,6 +413,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
             for (int n = 0; n < kPieces; ++n) kept[n] = kept_of(lo, n);
             team_sum.put(sums_of(rows.row(1), kept));
         }
+#pragma unroll 1
         for (uint32_t t = lo; t < hi; ++t) {
             rows.ask(a, at, t + 2 < hi);  // into the stage of row t - 1
             const bool more = t + 1 < hi, turns = more && join && t + 1 == gate_end;
@@ -430,6 +436,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
         }
     } else {
         if (join && lo < hi) set_gate(lo);
+#pragma unroll 1
         for (uint32_t t = lo; t < hi; ++t) {
             rows.template wait<0>();
             const bool turns = join && t + 1 == gate_end && t + 1 < hi;
@@ -448,26 +455,25 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
     if (reads_y && lo < hi) take_out(hi);
     pdl_launch_dependents();
     // the weights' sums, of a CTA's warps where each is a team
-    uint64_t group = at.worker;
-    if (kTeam == kWarpTeam) {
-        group = blockIdx.x;
-        __syncthreads();
-        Eight all = all_eight(0.0f);
-        if (threadIdx.x < 32)
-            for (uint32_t i = 0; i < kWarpsPerCta; ++i) all = fma(get_dp(0, i), 1.0f, all);
-        __syncthreads();
-        put_dp(0, dw[0]);
-        __syncthreads();
-        if (threadIdx.x >= 32) return;
-        dw[0] = all_eight(0.0f);
-        for (uint32_t i = 0; i < kWarpsPerCta; ++i) dw[0] = fma(get_dp(0, i), 1.0f, dw[0]);
-        put_dp(0, all);
-    }
+    float* const sums = a.sums + (uint64_t)(kTeam == kWarpTeam ? blockIdx.x : at.worker) * kWeightSlots * pitch;
+    const auto put_sums = [&](int slot) {
+        if (kTeam == kWarpTeam) __syncthreads();
+        if (kTeam == kWarpTeam && threadIdx.x >= 32) return;
 #pragma unroll
-    for (int n = 0; n < kPieces; ++n) {
-        float* sums = a.sums + group * kWeightSlots * pitch;
-        if (a.grad_weight != nullptr) store8<float, kVec>(sums + kSlotWeight * pitch, dw[n], at.tile(n), a.hidden);
-        if (a.grad_post_weight != nullptr) store8<float, kVec>(sums + kSlotPost * pitch, get_dp(n, 0), at.tile(n), a.hidden);
+        for (int n = 0; n < kPieces; ++n) {
+            Eight v = get_dp(n, 0);
+            if (kTeam == kWarpTeam)
+#pragma unroll 1
+                for (uint32_t i = 1; i < kWarpsPerCta; ++i) v = fma(get_dp(n, i), 1.0f, v);
+            store8<float, kVec>(sums + slot * pitch, v, at.tile(n), a.hidden);
+        }
+    };
+    if (a.grad_post_weight != nullptr) put_sums(kSlotPost);
+    if (a.grad_weight != nullptr) {
+        if (kTeam == kWarpTeam) __syncthreads();
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) put_dp(n, dw[n]);
+        put_sums(kSlotWeight);
     }
 }
 

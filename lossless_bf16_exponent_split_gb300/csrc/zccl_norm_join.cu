@@ -25,19 +25,20 @@ __device__ __forceinline__ void store_as(void* p, int dtype, uint64_t at, T v)
         static_cast<float*>(p)[at] = v;
 }
 
-// Adds the partial sums of 32 columns up: blockIdx.y = 0, 1 a weight's, 2 + i those of
-// gate row i.  Eight lanes hold a row's 32 columns, so that a thread has few rows, all of
-// them on their way at once.
+// Adds the partial sums of 4 kLanes columns up: blockIdx.y = 0, 1 a weight's, 2 + i those
+// of gate row i.  kLanes lanes hold a row's columns, so that a thread has few rows, all
+// of them on their way at once; fewer where there are few columns, for more CTAs.
 constexpr uint32_t kJoinThreads = 1024;
 
+template <int kLanes>
 __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(NormArgs a, int weight_dtype)
 {
-    constexpr uint32_t kRows = kJoinThreads / 8;
-    __shared__ float red[kJoinThreads / 32][33];
+    constexpr uint32_t kRows = kJoinThreads / kLanes, kCols = 4 * kLanes, kWarps = kJoinThreads / 32;
+    __shared__ float red[kWarps][kCols + 1];
     pdl_wait();
     const uint64_t pitch = (a.hidden + 7) / 8 * 8;
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, job = blockIdx.y;
-    const uint32_t col = blockIdx.x * 32 + lane % 8 * 4, first = threadIdx.x / 8;
+    const uint32_t col = blockIdx.x * kCols + lane % kLanes * 4, first = threadIdx.x / kLanes;
     float4 sum = make_float4(0, 0, 0, 0);
     const auto add = [&](const float* p) {
         const float4 v = *reinterpret_cast<const float4*>(p + col);
@@ -63,22 +64,23 @@ __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(NormArgs a, int
         at = (uint64_t)(job - 2) * a.hidden;
     }
 #pragma unroll
-    for (int o = 16; o >= 8; o /= 2) {
+    for (int o = 16; o >= kLanes; o /= 2) {
         sum.x += __shfl_xor_sync(0xFFFFFFFFu, sum.x, o);
         sum.y += __shfl_xor_sync(0xFFFFFFFFu, sum.y, o);
         sum.z += __shfl_xor_sync(0xFFFFFFFFu, sum.z, o);
         sum.w += __shfl_xor_sync(0xFFFFFFFFu, sum.w, o);
     }
-    if (lane < 8) {
+    if (lane < kLanes) {
         float* p = &red[warp][lane * 4];
         p[0] = sum.x, p[1] = sum.y, p[2] = sum.z, p[3] = sum.w;
     }
     __syncthreads();
     // a warp a column
+    if (warp >= kCols) return;
     float v = red[lane][warp];
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    const uint32_t c = blockIdx.x * 32 + warp;
+    const uint32_t c = blockIdx.x * kCols + warp;
     if (lane == 0 && c < a.hidden) store_as(out, dtype, at + c, v);
 }
 
@@ -120,7 +122,13 @@ cudaError_t launch_join(const NormArgs& a, int weight_dtype, cudaStream_t stream
     cudaError_t e = cudaSuccess;
     if (gate && !by_row) e = launch_2d(norm_join_gates_kernel, dim3((a.hidden + 255) / 256, a.workers - 1), 256, stream, a);
     if (e == cudaSuccess && (a.grad_weight != nullptr || a.grad_post_weight != nullptr || by_row))
-        e = launch_2d(norm_join_kernel, dim3((a.hidden + 31) / 32, by_row ? 2 + gate_rows : 2), kJoinThreads, stream, a, weight_dtype);
+    {
+        // 32 columns a CTA, fewer where that makes less than 128 of them
+        const uint32_t jobs = by_row ? 2 + gate_rows : 2;
+        const uint32_t lanes = a.hidden * jobs >= 128 * 32 ? 8 : a.hidden * jobs >= 128 * 16 ? 4 : 2;
+        e = launch_2d(lanes == 8 ? norm_join_kernel<8> : lanes == 4 ? norm_join_kernel<4> : norm_join_kernel<2>,
+                      dim3((a.hidden + 4 * lanes - 1) / (4 * lanes), jobs), kJoinThreads, stream, a, weight_dtype);
+    }
     return e;
 }
 
@@ -128,7 +136,7 @@ cudaError_t launch_join(const NormArgs& a, int weight_dtype, cudaStream_t stream
 
 zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weight_dtype, bool vec, cudaStream_t stream)
 {
-    const Shape s = norm_shape(a.hidden, a.rows, vec && x_dtype == ZCCL_BF16 && dtype == ZCCL_BF16);
+    const Shape s = norm_shape(a.hidden, a.rows, vec && x_dtype == ZCCL_BF16 && dtype == ZCCL_BF16, true);
     a.workers = s.workers;
     a.groups = s.grid / s.ctas;
     a.parts = a.sums + (uint64_t)a.groups * kWeightSlots * ((a.hidden + 7) / 8 * 8);
