@@ -49,16 +49,16 @@ bool on_16(const void* p, int dtype, uint64_t stride, uint64_t rows)
 
 zccl_status_t launch_norm(NormArgs& a, int x_dtype, int dtype, bool vec, cudaStream_t stream)
 {
-    const Shape s = norm_shape(a.hidden, a.rows, vec && x_dtype == ZCCL_BF16 && dtype == ZCCL_BF16, false);
+    const Shape s = norm_shape(a.hidden, a.rows, vec && x_dtype == ZCCL_BF16 && dtype == ZCCL_BF16, vec, false);
     a.workers = s.workers;
     const bool post = a.post && a.y != nullptr, drop = a.drop.below > 0;
+    uint32_t thread_bytes = 0;
     const NormKernel kernel = x_dtype == ZCCL_BF16
-                                  ? (dtype == ZCCL_BF16 ? norm_kernel_for<__nv_bfloat16, __nv_bfloat16>(s, vec, post, drop)
-                                                        : norm_kernel_for<__nv_bfloat16, float>(s, vec, post, drop))
-                                  : (dtype == ZCCL_BF16 ? norm_kernel_for<float, __nv_bfloat16>(s, vec, post, drop)
-                                                        : norm_kernel_for<float, float>(s, vec, post, drop));
-    return launched(s.team == kClusterTeam ? launch_clusters(kernel, s.grid, s.warps * 32, 0, s.ctas, stream, a)
-                                           : launch_dependent(kernel, s.grid, s.warps * 32, 0, stream, a));
+                                  ? (dtype == ZCCL_BF16 ? norm_kernel_for<__nv_bfloat16, __nv_bfloat16>(s, vec, post, drop, &thread_bytes)
+                                                        : norm_kernel_for<__nv_bfloat16, float>(s, vec, post, drop, &thread_bytes))
+                                  : (dtype == ZCCL_BF16 ? norm_kernel_for<float, __nv_bfloat16>(s, vec, post, drop, &thread_bytes)
+                                                        : norm_kernel_for<float, float>(s, vec, post, drop, &thread_bytes));
+    return launched(launch_teams(kernel, s, s.warps * 32, s.team == kLong ? 0 : s.warps * 32 * thread_bytes, stream, a));
 }
 
 }  // namespace zccl
@@ -101,8 +101,8 @@ zccl_status_t zccl_residual_norm(const zccl_norm_t* cfg, const void* d_x, int x_
 zccl_status_t zccl_residual_norm_workspace_bytes(uint64_t hidden, uint64_t rows, uint64_t* bytes)
 {
     if (bytes == nullptr || hidden == 0 || hidden > ZCCL_MAX_NORM_HIDDEN || rows >= (1ull << 31)) return ZCCL_ERR_INVALID_ARG;
-    const uint64_t narrow = norm_backward_bytes(norm_shape(hidden, rows, true, true), hidden);
-    const uint64_t wide = norm_backward_bytes(norm_shape(hidden, rows, false, true), hidden);
+    const uint64_t narrow = norm_backward_bytes(norm_shape(hidden, rows, true, true, true), hidden);
+    const uint64_t wide = norm_backward_bytes(norm_shape(hidden, rows, false, true, true), hidden);
     *bytes = narrow > wide ? narrow : wide;  // whatever the types
     return ZCCL_OK;
 }

@@ -74,21 +74,21 @@ struct Shape {
     uint32_t grid;     // CTAs
 };
 
-// 16 warps an SM (128 registers a thread), the SMs taken as 152.  `narrow`: both types
-// have 16 bits and rows begin on 16 bytes, so a warp can hold two tiles: two are better
-// (a row's sums are exchanged by half as many warps) from two tiles on, where they come
-// out even.
-inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow, bool backward)
+// The SMs are taken as 152, each with 16 warps (128 registers a thread); forward, where
+// rows begin on 16 bytes (vec) and a warp has one tile, 24 (80 registers).  `narrow`: both
+// types have 16 bits, and vec, so a warp can hold two tiles: two are better (a row costs a
+// warp about as much as two tiles do) from two tiles on, where they come out even.
+inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow, bool vec, bool backward)
 {
     constexpr uint32_t kSms = 152;
     const uint32_t tiles = (uint32_t)((hidden + kTile - 1) / kTile);
     const uint32_t pieces = narrow && (tiles % 2 == 0 || tiles > 8) ? 2 : 1, units = (tiles + pieces - 1) / pieces;
     // a cluster's CTA holds three rows in shared memory: 15 warps of two 16-bit tiles, or 16 of one tile
-    const uint32_t alone = 16, most = pieces == 2 ? 15 : 16;
+    const uint32_t alone = 16, most = pieces == 2 ? 15 : 16, sm_warps = !backward && vec && pieces == 1 ? 24 : 16;
     Shape s{};
     const auto at_most_rows = [&](uint64_t n) { return (uint32_t)(n < rows ? n : rows > 0 ? rows : 1); };
     if (tiles <= 1) {
-        s = {kWarpTeam, 1, kWarpsPerCta, 1, at_most_rows(kSms * 16), 0};
+        s = {kWarpTeam, 1, kWarpsPerCta, 1, at_most_rows(kSms * sm_warps), 0};
         s.grid = (s.workers + kWarpsPerCta - 1) / kWarpsPerCta;
     } else if (units <= most * kMaxCluster && tiles <= kTeamWarps * kMaxCluster) {
         s.ctas = units <= alone ? 1 : units <= 2 * most ? 2 : 4;
@@ -99,7 +99,7 @@ inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow, bool backwa
         s.pieces = pieces;
         s.warps = (units + s.ctas - 1) / s.ctas;
         // clusters of four do not fill every group of SMs: 36 of 38 are taken
-        s.workers = at_most_rows((uint64_t)(s.ctas == 4 ? 144 : kSms) * (16 / s.warps) / s.ctas);
+        s.workers = at_most_rows((uint64_t)(s.ctas == 4 ? 144 : kSms) * (sm_warps / s.warps) / s.ctas);
         s.grid = s.workers * s.ctas;
     } else {
         // its sums stay in the workspace: fewer workers for longer rows
@@ -342,19 +342,24 @@ __device__ __forceinline__ Kept<kVec> join_kept(const NormArgs& a, uint64_t offs
 using NormKernel = void (*)(NormArgs);
 // The kernels of a pair of types; thread_bytes: shared memory of a thread.
 template <typename Tx, typename Ty>
-NormKernel norm_kernel_for(const Shape& s, bool vec, bool post, bool drop);
+NormKernel norm_kernel_for(const Shape& s, bool vec, bool post, bool drop, uint32_t* thread_bytes);
 template <typename Tx, typename Ty>
 NormKernel norm_backward_kernel_for(const Shape& s, bool vec, bool post, bool drop, uint32_t* thread_bytes);
 
 zccl_status_t launch_norm(NormArgs& a, int x_dtype, int dtype, bool vec, cudaStream_t stream);
 zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weight_dtype, bool vec, cudaStream_t stream);
 
-// Launches `kernel` as launch_dependent does, in clusters of `ctas`.
-inline cudaError_t launch_clusters(void (*kernel)(NormArgs), uint32_t grid, uint32_t threads, size_t smem, uint32_t ctas,
-                                   cudaStream_t stream, const NormArgs& a)
+// Launches `kernel` as launch_dependent does, in clusters where a row has several CTAs.
+inline cudaError_t launch_teams(NormKernel kernel, const Shape& s, uint32_t threads, size_t smem, cudaStream_t stream,
+                                const NormArgs& a)
 {
+    if (smem + kTeamBytes > 48 << 10) {  // (the forward kernels have kTeamBytes beside it)
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    if (s.team != kClusterTeam) return launch_dependent(kernel, s.grid, threads, smem, stream, a);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3(s.grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -362,7 +367,7 @@ inline cudaError_t launch_clusters(void (*kernel)(NormArgs), uint32_t grid, uint
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.x = s.ctas;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;

@@ -10,7 +10,7 @@
 // rho (mean(k p y dh w) - c mean(k p y r)): all six sums of a row are taken at once.
 #pragma once
 
-#include "zccl_norm.h"
+#include "zccl_norm_feed.cuh"
 
 namespace zccl {
 
@@ -148,140 +148,6 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(Nor
     }
 }
 
-// A worker's rows on their way: r, dr, dh and y of the row at hand and of those behind
-// it.  What the call does not have reads as zero.
-template <typename Tx, typename Ty, bool kVec, int kPieces, int kStages>
-struct Feed;
-
-// Rows on 16 bytes come by asynchronous copies into places of the thread's own, so that
-// no thread waits for another's and no registers are held.  A lane's addresses move on
-// from row to row; what it copies lies at constant distances from them.
-// (past L1 where a lane's 16 bytes are all it wants of a 32-byte sector's neighbours; of
-// 32-bit values it wants the other half too.)
-template <bool kPast, int kTo, int kFrom>
-__device__ __forceinline__ void copy_16(uint32_t to, const char* from, uint32_t bytes)
-{
-    if (kPast)
-        asm volatile("cp.async.cg.shared.global [%0+%3], [%1+%4], 16, %2;" ::"r"(to), "l"(from), "r"(bytes), "n"(kTo), "n"(kFrom) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0+%3], [%1+%4], 16, %2;" ::"r"(to), "l"(from), "r"(bytes), "n"(kTo), "n"(kFrom) : "memory");
-}
-template <typename Tx, typename Ty, int kPieces, int kStages>
-struct Feed<Tx, Ty, true, kPieces, kStages> {
-    static constexpr int kX = sizeof(Tx) / 2, kY = sizeof(Ty) / 2, kAll = 2 * kX + 2 * kY;  // 16-byte parts of a piece
-    static constexpr uint32_t kThreadBytes = kStages * kPieces * kAll * 16;
-    static constexpr uint32_t kStage = kPieces * kAll * 32;  // 16-byte parts of a warp's stage
-    const uint4* const mine;  // a warp's parts, 32 lanes each, one behind the other
-    uint32_t to;              // the stage that the next row goes to
-    uint32_t asked = 0;
-    const char *r, *up, *dh, *y;
-    uint32_t bytes[kPieces];  // 16, or 0 where a piece lies behind the row's end
-    __device__ __forceinline__ Feed(uint4* warp_smem, const NormArgs& a, const Place& place, uint32_t t)
-        : mine(warp_smem + (threadIdx.x & 31)), to(smem_addr(warp_smem + (threadIdx.x & 31)))
-    {
-        for (uint32_t i = 0; i < kStages * kStage; i += 32) warp_smem[i + (threadIdx.x & 31)] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int n = 0; n < kPieces; ++n) bytes[n] = column<true>(place.tile(n), 0) < a.hidden ? 16 : 0;
-        const uint64_t c = bytes[0] > 0 ? column<true>(place.tile(0), 0) : 0;
-        r = static_cast<const char*>(a.x) + (t * a.x_stride + c) * sizeof(Tx);
-        up = static_cast<const char*>(a.grad_r) + (t * a.grad_r_stride + c) * sizeof(Tx);
-        dh = static_cast<const char*>(a.grad_h) + (t * a.grad_h_stride + c) * sizeof(Ty);
-        y = static_cast<const char*>(a.y) + (t * a.y_stride + c) * sizeof(Ty);
-    }
-    template <typename T, int kPart>
-    __device__ __forceinline__ void copy(const char*& from, uint64_t stride)
-    {
-        copy_piece<T, kPart, 0>(from);
-        if constexpr (kPieces == 2) copy_piece<T, kPart, 1>(from);
-        from += stride * sizeof(T);
-    }
-    template <typename T, int kPart, int n>
-    __device__ __forceinline__ void copy_piece(const char* from)
-    {
-        copy_16<sizeof(T) == 2, (n * kAll + kPart) * 512, n * (int)(kTile * sizeof(T))>(to, from, bytes[n]);
-        if constexpr (sizeof(T) == 4) copy_16<false, (n * kAll + kPart + 1) * 512, n * (int)(kTile * sizeof(T)) + 16>(to, from, bytes[n]);
-    }
-    // Asks for the next row (there: it is one of the worker's).
-    __device__ __forceinline__ void ask(const NormArgs& a, const Place&, bool there)
-    {
-        if (there) {
-            if (a.grad_h != nullptr) {
-                copy<Tx, 0>(r, a.x_stride);
-                copy<Ty, 2 * kX>(dh, a.grad_h_stride);
-            }
-            if (a.grad_r != nullptr) copy<Tx, kX>(up, a.grad_r_stride);
-            if (a.y != nullptr) copy<Ty, 2 * kX + kY>(y, a.y_stride);
-        }
-        const bool last = asked + 1 == kStages;
-        asked = last ? 0 : asked + 1;
-        to = last ? to - (kStages - 1) * kStage * 16 : to + kStage * 16;
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    // Until all but the last kLater rows that were asked for are there.
-    template <int kLater>
-    __device__ __forceinline__ void wait()
-    {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kLater) : "memory");
-    }
-    struct Row {
-        const uint4* at;
-        template <typename T>
-        __device__ __forceinline__ Eight read(int n, int part) const
-        {
-            const uint4* p = at + (n * kAll + part) * 32;
-            if (sizeof(T) == 2) return widen(*p);
-            const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 32);
-            return {{make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)}};
-        }
-        __device__ __forceinline__ Eight r(int n) const { return read<Tx>(n, 0); }
-        __device__ __forceinline__ Eight up(int n) const { return read<Tx>(n, kX); }
-        __device__ __forceinline__ Eight dh(int n) const { return read<Ty>(n, 2 * kX); }
-        __device__ __forceinline__ Eight y(int n) const { return read<Ty>(n, 2 * kX + kY); }
-    };
-    // The row that was asked for before the last `later` ones.
-    __device__ __forceinline__ Row row(uint32_t later) const
-    {
-        const uint32_t stage = asked + kStages - 1 - later;
-        return {mine + (stage >= kStages ? stage - kStages : stage) * kStage};
-    }
-};
-
-// Others by loads of single values into registers: one row, and the one that is read.
-template <typename Tx, typename Ty, int kPieces, int kStages>
-struct Feed<Tx, Ty, false, kPieces, kStages> {
-    static constexpr uint32_t kThreadBytes = 0;
-    struct Row {
-        Piece<Tx, false> pr[kPieces], pu[kPieces];
-        Piece<Ty, false> ph[kPieces], py[kPieces];
-        __device__ __forceinline__ Eight r(int n) const { return pr[n].get(); }
-        __device__ __forceinline__ Eight up(int n) const { return pu[n].get(); }
-        __device__ __forceinline__ Eight dh(int n) const { return ph[n].get(); }
-        __device__ __forceinline__ Eight y(int n) const { return py[n].get(); }
-    };
-    Row next;
-    uint32_t at;  // the row that is asked for next
-    __device__ __forceinline__ Feed(uint4*, const NormArgs&, const Place&, uint32_t t) : next{}, at(t) {}
-    __device__ __forceinline__ void ask(const NormArgs& a, const Place& place, bool there)
-    {
-        if (!there) return;
-#pragma unroll
-        for (int n = 0; n < kPieces; ++n) {
-            if (a.grad_h != nullptr) {
-                next.pr[n].load(static_cast<const Tx*>(a.x) + at * a.x_stride, place.tile(n), a.hidden);
-                next.ph[n].load(static_cast<const Ty*>(a.grad_h) + at * a.grad_h_stride, place.tile(n), a.hidden);
-            }
-            if (a.grad_r != nullptr) next.pu[n].load(static_cast<const Tx*>(a.grad_r) + at * a.grad_r_stride, place.tile(n), a.hidden);
-            if (a.y != nullptr) next.py[n].load(static_cast<const Ty*>(a.y) + at * a.y_stride, place.tile(n), a.hidden);
-        }
-        ++at;
-    }
-    template <int kLater>
-    __device__ __forceinline__ void wait()
-    {
-    }
-    __device__ __forceinline__ Row row(uint32_t) const { return next; }
-};
-
 // A team a worker; the sums over rows stay in registers.  While a gate stays the same
 // the sums of p's and of the gate's gradient are the same up to a factor of each column,
 //   e = sum of (kept) d y eta:   dp += scale gate e,   dgate = scale p e
@@ -296,7 +162,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
     extern __shared__ uint4 smem[];
     constexpr bool kAhead = kTeam == kClusterTeam && kVec;
     constexpr int kTeamSums = kKind == kAny || (kKind & 1) ? kSums : 2;
-    using Rows = Feed<Tx, Ty, kVec, kPieces, kAhead ? 3 : 2>;
+    using Rows = Feed<Tx, Ty, kVec, kPieces, !kVec ? 0 : kAhead ? 3 : 2, true>;
     // of each warp: its rows, and its sums of p's gradient (two 16-byte parts a piece); then the teams' sums
     constexpr uint32_t kWarpParts = Rows::kThreadBytes / 16 * 32 + 2 * kPieces * 32;
     uint4* const warp_smem = smem + (threadIdx.x >> 5) * kWarpParts;
@@ -361,7 +227,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
         float2 sum[kSums] = {};
 #pragma unroll
         for (int n = 0; n < kPieces; ++n)
-            add_sums(sum, post, row.r(n), mul(row.dh(n), w[n]), row.up(n), row.y(n), post ? masked(n, kept[n]) : kp[n]);
+            add_sums(sum, post, row.x(n), mul(row.y(n), w[n]), row.x1(n), row.y1(n), post ? masked(n, kept[n]) : kp[n]);
         float s[kTeamSums];
 #pragma unroll
         for (int i = 0; i < kTeamSums; ++i) s[i] = sum[i].x + sum[i].y;
@@ -379,14 +245,14 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
 #pragma unroll
         for (int n = 0; n < kPieces; ++n) {
             const uint32_t tile = at.tile(n);
-            const Eight r = row.r(n), dh = row.dh(n);
-            Eight d = joined(f, r, mul(dh, w[n]), row.up(n)), y = all_eight(0.0f);
+            const Eight r = row.x(n), dh = row.y(n);
+            Eight d = joined(f, r, mul(dh, w[n]), row.x1(n)), y = all_eight(0.0f);
             dw[n] = fma(dh, mul(r, f.rho), dw[n]);
             if (a.grad_x != nullptr) store8<Tx, kVec>(gx_at, d, tile, a.hidden);
             if (!join) continue;
             if (drop) d = where_kept<kVec>(kept[n], d);
             if (reads_y) {
-                y = row.y(n);
+                y = row.y1(n);
                 // what is dropped may be infinite; with post it would have spoilt the whole row
                 e[n] = fma(d, mul(drop && !post ? where_kept<kVec>(kept[n], y) : y, f.eta), e[n]);
             }
@@ -480,7 +346,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
 template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces>
 NormKernel backward_kind(bool post, bool drop, uint32_t* thread_bytes)
 {
-    *thread_bytes = Feed<Tx, Ty, kVec, kPieces, kVec && kTeam == kClusterTeam ? 3 : 2>::kThreadBytes + 32 * kPieces;
+    *thread_bytes = Feed<Tx, Ty, kVec, kPieces, !kVec ? 0 : kTeam == kClusterTeam ? 3 : 2, true>::kThreadBytes + 32 * kPieces;
     if constexpr (kVec)
         return post ? (drop ? norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 3> : norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 1>)
                     : (drop ? norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 2> : norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 0>);

@@ -2,5 +2,5 @@
 #include "zccl_norm_forward.cuh"
 
 namespace zccl {
-template NormKernel norm_kernel_for<__nv_bfloat16, __nv_bfloat16>(const Shape&, bool, bool, bool);
+template NormKernel norm_kernel_for<__nv_bfloat16, __nv_bfloat16>(const Shape&, bool, bool, bool, uint32_t*);
 }  // namespace zccl

@@ -2,5 +2,5 @@
 #include "zccl_norm_forward.cuh"
 
 namespace zccl {
-template NormKernel norm_kernel_for<float, float>(const Shape&, bool, bool, bool);
+template NormKernel norm_kernel_for<float, float>(const Shape&, bool, bool, bool, uint32_t*);
 }  // namespace zccl

@@ -1,0 +1,173 @@
+// zccl_norm_feed.cuh -- the norm kernels' rows on their way from memory.
+#pragma once
+
+#include "zccl_norm.h"
+
+namespace zccl {
+
+// A worker's rows: x and y of the row at hand and of those behind it; backward r (as x),
+// dh (as y), dr and y (as x1, y1).  What the call does not have reads as zero.
+// kStages: rows in shared memory, or 0 for one in registers.
+// Rows on 16 bytes may come by asynchronous copies into places of the thread's own, so that
+// no thread waits for another's and no registers are held.  A lane's addresses move on
+// from row to row; what it copies lies at constant distances from them.  16-bit values go
+// past L1, of which the rows in shared memory leave little (gradients of 4096 x 14336 94
+// us, 117 through it); a lane's two parts of 32-bit values share sectors, which L1 keeps for
+// the second (2048 columns 56 us, 85 past it).
+template <bool kPast, int kTo, int kFrom>
+__device__ __forceinline__ void copy_16(uint32_t to, const char* from, uint32_t bytes)
+{
+    if (kPast)
+        asm volatile("cp.async.cg.shared.global [%0+%3], [%1+%4], 16, %2;" ::"r"(to), "l"(from), "r"(bytes), "n"(kTo), "n"(kFrom) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0+%3], [%1+%4], 16, %2;" ::"r"(to), "l"(from), "r"(bytes), "n"(kTo), "n"(kFrom) : "memory");
+}
+template <typename Tx, typename Ty, bool kVec, int kPieces, int kStages, bool kBackward>
+struct Feed {
+    static_assert(kVec, "rows on 16 bytes");
+    static constexpr int kX = sizeof(Tx) / 2, kY = sizeof(Ty) / 2, kAll = (kX + kY) * (kBackward ? 2 : 1);  // 16-byte parts of a piece
+    static constexpr uint32_t kThreadBytes = kStages * kPieces * kAll * 16;
+    static constexpr uint32_t kStage = kPieces * kAll * 32;  // 16-byte parts of a warp's stage
+    const uint4* const mine;  // a warp's parts, 32 lanes each, one behind the other
+    uint32_t to;              // the stage that the next row goes to
+    uint32_t asked = 0;
+    const char *x, *y, *x1, *y1;
+    uint32_t bytes[kPieces];  // 16, or 0 where a piece lies behind the row's end
+    __device__ __forceinline__ Feed(uint4* warp_smem, const NormArgs& a, const Place& place, uint32_t t)
+        : mine(warp_smem + (threadIdx.x & 31)), to(smem_addr(warp_smem + (threadIdx.x & 31)))
+    {
+        for (uint32_t i = 0; i < kStages * kStage; i += 32) warp_smem[i + (threadIdx.x & 31)] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) bytes[n] = column<true>(place.tile(n), 0) < a.hidden ? 16 : 0;
+        const uint64_t c = bytes[0] > 0 ? column<true>(place.tile(0), 0) : 0;
+        x = static_cast<const char*>(a.x) + (t * a.x_stride + c) * sizeof(Tx);
+        if (kBackward) {
+            y = static_cast<const char*>(a.grad_h) + (t * a.grad_h_stride + c) * sizeof(Ty);
+            x1 = static_cast<const char*>(a.grad_r) + (t * a.grad_r_stride + c) * sizeof(Tx);
+            y1 = static_cast<const char*>(a.y) + (t * a.y_stride + c) * sizeof(Ty);
+        } else {
+            y = static_cast<const char*>(a.y) + (t * a.y_stride + c) * sizeof(Ty);
+        }
+    }
+    template <typename T, int kPart>
+    __device__ __forceinline__ void copy(const char*& from, uint64_t stride)
+    {
+        copy_piece<T, kPart, 0>(from);
+        if constexpr (kPieces == 2) copy_piece<T, kPart, 1>(from);
+        from += stride * sizeof(T);
+    }
+    template <typename T, int kPart, int n>
+    __device__ __forceinline__ void copy_piece(const char* from)
+    {
+        copy_16<sizeof(T) == 2, (n * kAll + kPart) * 512, n * (int)(kTile * sizeof(T))>(to, from, bytes[n]);
+        if constexpr (sizeof(T) == 4) copy_16<false, (n * kAll + kPart + 1) * 512, n * (int)(kTile * sizeof(T)) + 16>(to, from, bytes[n]);
+    }
+    // Asks for the next row (there: it is one of the worker's).
+    __device__ __forceinline__ void ask(const NormArgs& a, const Place&, bool there)
+    {
+        if (there) {
+            if constexpr (kBackward) {
+                if (a.grad_h != nullptr) {
+                    copy<Tx, 0>(x, a.x_stride);
+                    copy<Ty, kX>(y, a.grad_h_stride);
+                }
+                if (a.grad_r != nullptr) copy<Tx, kX + kY>(x1, a.grad_r_stride);
+                if (a.y != nullptr) copy<Ty, 2 * kX + kY>(y1, a.y_stride);
+            } else {
+                copy<Tx, 0>(x, a.x_stride);
+                if (a.y != nullptr) copy<Ty, kX>(y, a.y_stride);
+            }
+        }
+        const bool last = asked + 1 == kStages;
+        asked = last ? 0 : asked + 1;
+        to = last ? to - (kStages - 1) * kStage * 16 : to + kStage * 16;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // Until all but the last kLater rows that were asked for are there.
+    template <int kLater>
+    __device__ __forceinline__ void wait()
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kLater) : "memory");
+    }
+    struct Row {
+        const uint4* at;
+        template <typename T>
+        __device__ __forceinline__ Eight read(int n, int part) const
+        {
+            const uint4* p = at + (n * kAll + part) * 32;
+            if (sizeof(T) == 2) return widen(*p);
+            const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 32);
+            return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+        }
+        __device__ __forceinline__ Eight x(int n) const { return read<Tx>(n, 0); }
+        __device__ __forceinline__ Eight y(int n) const { return read<Ty>(n, kX); }
+        __device__ __forceinline__ Eight x1(int n) const { return read<Tx>(n, kX + kY); }
+        __device__ __forceinline__ Eight y1(int n) const { return read<Ty>(n, 2 * kX + kY); }
+    };
+    // The row that was asked for before the last `later` ones.
+    __device__ __forceinline__ Row row(uint32_t later) const
+    {
+        const uint32_t stage = asked + kStages - 1 - later;
+        return {mine + (stage >= kStages ? stage - kStages : stage) * kStage};
+    }
+};
+
+// Others come into registers: the row that is read, and the next one.
+template <typename Tx, typename Ty, bool kVec, int kPieces, bool kBackward>
+struct Feed<Tx, Ty, kVec, kPieces, 0, kBackward> {
+    static constexpr uint32_t kThreadBytes = 0;
+    struct Row {
+        Piece<Tx, kVec> px[kPieces], px1[kPieces];
+        Piece<Ty, kVec> py[kPieces], py1[kPieces];
+        __device__ __forceinline__ Eight x(int n) const { return px[n].get(); }
+        __device__ __forceinline__ Eight y(int n) const { return py[n].get(); }
+        __device__ __forceinline__ Eight x1(int n) const { return px1[n].get(); }
+        __device__ __forceinline__ Eight y1(int n) const { return py1[n].get(); }
+    };
+    Row next;
+    const Tx *x, *x1;  // the row that is asked for next
+    const Ty *y, *y1;
+    __device__ __forceinline__ Feed(uint4*, const NormArgs& a, const Place&, uint32_t t) : next{}
+    {
+        x = static_cast<const Tx*>(a.x) + t * a.x_stride;
+        if (kBackward) {
+            y = static_cast<const Ty*>(a.grad_h) + t * a.grad_h_stride;
+            x1 = static_cast<const Tx*>(a.grad_r) + t * a.grad_r_stride;
+            y1 = static_cast<const Ty*>(a.y) + t * a.y_stride;
+        } else {
+            y = static_cast<const Ty*>(a.y) + t * a.y_stride;
+        }
+    }
+    __device__ __forceinline__ void ask(const NormArgs& a, const Place& place, bool there)
+    {
+        if (!there) return;
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+            const uint32_t tile = place.tile(n);
+            if (kBackward) {
+                if (a.grad_h != nullptr) {
+                    next.px[n].load(x, tile, a.hidden);
+                    next.py[n].load(y, tile, a.hidden);
+                }
+                if (a.grad_r != nullptr) next.px1[n].load(x1, tile, a.hidden);
+                if (a.y != nullptr) next.py1[n].load(y1, tile, a.hidden);
+            } else {
+                next.px[n].load(x, tile, a.hidden);
+                if (a.y != nullptr) next.py[n].load(y, tile, a.hidden);
+            }
+        }
+        x += a.x_stride;
+        y += kBackward ? a.grad_h_stride : a.y_stride;
+        if (kBackward) {
+            x1 += a.grad_r_stride;
+            y1 += a.y_stride;
+        }
+    }
+    template <int kLater>
+    __device__ __forceinline__ void wait()
+    {
+    }
+    __device__ __forceinline__ Row row(uint32_t) const { return next; }
+};
+
+}  // namespace zccl

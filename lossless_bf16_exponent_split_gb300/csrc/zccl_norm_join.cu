@@ -136,7 +136,7 @@ cudaError_t launch_join(const NormArgs& a, int weight_dtype, cudaStream_t stream
 
 zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weight_dtype, bool vec, cudaStream_t stream)
 {
-    const Shape s = norm_shape(a.hidden, a.rows, vec && x_dtype == ZCCL_BF16 && dtype == ZCCL_BF16, true);
+    const Shape s = norm_shape(a.hidden, a.rows, vec && x_dtype == ZCCL_BF16 && dtype == ZCCL_BF16, vec, true);
     a.workers = s.workers;
     a.groups = s.grid / s.ctas;
     a.parts = a.sums + (uint64_t)a.groups * kWeightSlots * ((a.hidden + 7) / 8 * 8);
@@ -150,11 +150,7 @@ zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weig
                                   : norm_backward_kernel_for<float, float>(s, vec, post, drop, &thread_bytes));
     const uint32_t threads = s.warps * 32;
     const size_t smem = s.team == kLong ? 0 : threads * thread_bytes + kTeamBytes;
-    cudaError_t e = cudaSuccess;
-    if (smem > 48 << 10) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess)
-        e = s.team == kClusterTeam ? launch_clusters(kernel, s.grid, threads, smem, s.ctas, stream, a)
-                                   : launch_dependent(kernel, s.grid, threads, smem, stream, a);
+    cudaError_t e = launch_teams(kernel, s, threads, smem, stream, a);
     if (e == cudaSuccess) e = launch_join(a, weight_dtype, stream);
     return launched(e);
 }
