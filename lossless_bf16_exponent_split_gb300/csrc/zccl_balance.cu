@@ -6,6 +6,13 @@
 // of `chunk` tokens, a CTA each; the last part to arrive adds the parts' sums in their
 // order, and the last sequence the sequences' losses, so results depend on the sizes
 // alone.  With very many sequences each is one part.
+//
+// The bytes are few (16384 x 64 in BF16: 2 MB, 0.3 us of HBM time): a call is bound by its
+// latencies (the table, the first logits, the hand-over to the last part), 6.6 us for the
+// loss and 4.3 for the gradient; many experts by issue (65621 x 256 in 32 bits with
+// sigmoid scores: 182 and 246 instructions a warp and token, six of ten issue slots, 25 us
+// each, 2.7 TB/s).  Exponentials and reciprocals are the fast ones: nothing here decides
+// between close values.
 #include <cmath>
 
 #include "zccl_ops.cuh"
@@ -544,13 +551,19 @@ BalanceKernel balance_for(const BalanceArgs& a, int dtype, bool backward)
 }
 
 // Tokens of a part, and the CTAs that there are parts for.  One sequence: as many parts
-// as two a SM hold; several have a part each that is not whole, which is counted in.
+// as two a SM hold, or one where its registers (more than 256 experts) or the joining of
+// its parts (more than 128) ask for fewer: 16384 x 512 (loss and gradient) 26 us
+// with 152 parts, 37 with 304; x 256 21.3 and 23.5.  Several sequences have a part each that is not whole, which is counted in.
 constexpr uint32_t kPartTokens = 64;
-uint64_t most_parts(uint32_t sequences) { return sequences == 1 ? 304 : sequences < 152 ? 304 - sequences : 152; }
-uint32_t chunk_of(uint64_t tokens, uint32_t sequences)
+uint64_t most_parts(uint32_t sequences, uint32_t experts)
+{
+    const uint32_t most = experts > 256 || (sequences == 1 && experts > 128) ? 152 : 304;
+    return sequences == 1 ? most : sequences < most / 2 ? most - sequences : most / 2;
+}
+uint32_t chunk_of(uint64_t tokens, uint32_t sequences, uint32_t experts)
 {
     if (sequences > kFewSequences) return 0;
-    const uint64_t most = most_parts(sequences), chunk = (tokens + most - 1) / most;
+    const uint64_t most = most_parts(sequences, experts), chunk = (tokens + most - 1) / most;
     return (uint32_t)(chunk > kPartTokens ? chunk : kPartTokens);
 }
 uint32_t grid_of(uint64_t tokens, uint32_t sequences, uint32_t chunk, bool backward)
@@ -594,7 +607,7 @@ zccl_status_t zccl_balance_workspace_bytes(uint32_t sequences, uint32_t experts,
 {
     if (bytes == nullptr || sequences == 0 || sequences > ZCCL_MAX_SEQUENCES || experts == 0 || experts > ZCCL_MAX_EXPERTS)
         return ZCCL_ERR_INVALID_ARG;
-    const uint64_t parts = sequences > kFewSequences ? 0 : most_parts(sequences) + sequences + 1;
+    const uint64_t parts = sequences > kFewSequences ? 0 : most_parts(sequences, experts) + sequences + 1;
     *bytes = 4ull * (kCounters + sequences) + 4ull * parts * (2 * experts + 1);
     return ZCCL_OK;
 }
@@ -620,7 +633,7 @@ zccl_status_t zccl_balance(const zccl_route_t* cfg, const void* d_logits, int dt
     a.arrived = static_cast<uint32_t*>(d_ws);
     a.losses = reinterpret_cast<float*>(a.arrived + kCounters);
     a.part_scores = a.losses + sequences;
-    a.chunk = chunk_of(tokens, sequences);
+    a.chunk = chunk_of(tokens, sequences, a.E);
     const uint32_t grid = grid_of(tokens, sequences, a.chunk, false);
     a.part_counts = reinterpret_cast<int32_t*>(a.part_scores + (uint64_t)grid * a.E);
     return launched(launch_dependent(balance_for(a, dtype, false), grid, kThreads, 0, stream, a));
@@ -649,7 +662,7 @@ zccl_status_t zccl_balance_backward(const zccl_route_t* cfg, const void* d_logit
     a.grad = d_grad_logits;
     a.grad_stride = grad_stride;
     a.accumulate = accumulate != 0;
-    a.chunk = chunk_of(tokens, sequences);
+    a.chunk = chunk_of(tokens, sequences, a.E);
     const uint32_t grid = grid_of(tokens, sequences, a.chunk, true);
     return launched(launch_dependent(balance_for(a, dtype, true), grid, kThreads, 0, stream, a));
 }

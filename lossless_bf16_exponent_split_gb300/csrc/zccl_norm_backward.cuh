@@ -8,6 +8,13 @@
 //   dw  += dh r rho, dp += k d y eta, dgate += (k / gate) d N(y)
 // c' needs d, but its sum is that of three others, mean(k d p y) = mean(k p y dr) +
 // rho (mean(k p y dh w) - c mean(k p y r)): all six sums of a row are taken at once.
+//
+// Bound by HBM without post and dropout: 16384 x 2048 in BF16 55 us with the join of the
+// workers' sums (r, dr, dh in, dx, dy out: 6.1 TB/s, 90 % of measured), 4096 x 14336 94 us
+// (6.2); with post, dropout and a gate 72 us (y read too: 5.6 TB/s), where it issues in two
+// of three slots: some 390 instructions a warp and tile of 256 columns.  Rows that do not
+// begin on 16 bytes: 8203 x 1001, 32-bit residual, 48 us (3.1 TB/s), bound by loads of
+// single values.
 #pragma once
 
 #include "zccl_norm_feed.cuh"

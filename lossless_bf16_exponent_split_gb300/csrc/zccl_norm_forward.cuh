@@ -1,5 +1,11 @@
 // zccl_norm_forward.cuh -- the join of a block's output with the residual and the norm
 // of the next block's input.
+//
+// Bound by HBM: x and y in, r and h out, once.  What comes between is issue: a row costs a
+// warp about 95 instructions besides its tiles' 70 (the sums' exchange, the loop), post 40 a
+// tile, dropout 70.  16384 x 2048 in BF16: 43.7 us with the join alone (6.1 TB/s, 91 % of
+// measured), 48 with post and dropout; 4096 x 14336 (clusters of two) 85 us (5.5 TB/s);
+// one row of 4096: 2.1 us.
 #pragma once
 
 #include "zccl_norm_feed.cuh"

@@ -68,6 +68,24 @@ __device__ __forceinline__ Eight widen(const uint4& q)
              make_float2(bf16_lo(q.z), bf16_hi(q.z)), make_float2(bf16_lo(q.w), bf16_hi(q.w))}};
 }
 
+// Eight neighbours on 16 bytes.
+__device__ __forceinline__ Eight load_near(const __nv_bfloat16* p) { return widen(*reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ Eight load_near(const float* p)
+{
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+}
+__device__ __forceinline__ uint4 round_eight(const Eight& v)
+{
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ void store_near(__nv_bfloat16* p, const Eight& v) { *reinterpret_cast<uint4*>(p) = round_eight(v); }
+__device__ __forceinline__ void store_near(float* p, const Eight& v)
+{
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
 // A lane's eight values of a tile as they are held in memory, to be widened later.
 template <typename T, bool kVec>
 struct Piece;
@@ -106,9 +124,7 @@ struct Piece<float, kVec> {
     {
         if (kVec) {
             const uint32_t c = column<true>(tile, 0);
-            const float4* p = reinterpret_cast<const float4*>(row + c);
-            const float4 a = c < cols ? p[0] : make_float4(0, 0, 0, 0), b = c < cols ? p[1] : make_float4(0, 0, 0, 0);
-            v = {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+            v = c < cols ? load_near(row + c) : all_eight(0.0f);
         } else if (tile + kTile <= cols) {
             const float* p = row + column<false>(tile, 0);
 #pragma unroll
@@ -135,7 +151,7 @@ template <typename T, bool kVec>
 __device__ __forceinline__ Eight store8(T* row, const Eight& v, uint32_t tile, uint32_t cols)
 {
     if (sizeof(T) == 2) {
-        const uint4 q = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        const uint4 q = round_eight(v);
         if (kVec) {
             const uint32_t c = column<true>(tile, 0);
             if (c < cols) *reinterpret_cast<uint4*>(row + c) = q;
@@ -151,11 +167,7 @@ __device__ __forceinline__ Eight store8(T* row, const Eight& v, uint32_t tile, u
     }
     if (kVec) {
         const uint32_t c = column<true>(tile, 0);
-        if (c < cols) {
-            float4* p = reinterpret_cast<float4*>(row + c);
-            p[0] = make_float4(v[0], v[1], v[2], v[3]);
-            p[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
+        if (c < cols) store_near(reinterpret_cast<float*>(row + c), v);
     } else {
         float* p = reinterpret_cast<float*>(row);
 #pragma unroll
