@@ -52,13 +52,13 @@ zccl_status_t launch_norm(NormArgs& a, int x_dtype, int dtype, bool vec, cudaStr
     const Shape s = norm_shape(a.hidden, a.rows, vec && x_dtype == ZCCL_BF16 && dtype == ZCCL_BF16, vec, false);
     a.workers = s.workers;
     const bool post = a.post && a.y != nullptr, drop = a.drop.below > 0;
-    uint32_t thread_bytes = 0;
+    uint32_t warp_bytes = 0;
     const NormKernel kernel = x_dtype == ZCCL_BF16
-                                  ? (dtype == ZCCL_BF16 ? norm_kernel_for<__nv_bfloat16, __nv_bfloat16>(s, vec, post, drop, &thread_bytes)
-                                                        : norm_kernel_for<__nv_bfloat16, float>(s, vec, post, drop, &thread_bytes))
-                                  : (dtype == ZCCL_BF16 ? norm_kernel_for<float, __nv_bfloat16>(s, vec, post, drop, &thread_bytes)
-                                                        : norm_kernel_for<float, float>(s, vec, post, drop, &thread_bytes));
-    return launched(launch_teams(kernel, s, s.warps * 32, s.team == kLong ? 0 : s.warps * 32 * thread_bytes, stream, a));
+                                  ? (dtype == ZCCL_BF16 ? norm_kernel_for<__nv_bfloat16, __nv_bfloat16>(s, vec, post, drop, &warp_bytes)
+                                                        : norm_kernel_for<__nv_bfloat16, float>(s, vec, post, drop, &warp_bytes))
+                                  : (dtype == ZCCL_BF16 ? norm_kernel_for<float, __nv_bfloat16>(s, vec, post, drop, &warp_bytes)
+                                                        : norm_kernel_for<float, float>(s, vec, post, drop, &warp_bytes));
+    return launched(launch_teams(kernel, s, s.warps * 32, s.team == kLong ? 0 : s.warps * warp_bytes, stream, a));
 }
 
 }  // namespace zccl

@@ -340,11 +340,11 @@ __device__ __forceinline__ Kept<kVec> join_kept(const NormArgs& a, uint64_t offs
 }
 
 using NormKernel = void (*)(NormArgs);
-// The kernels of a pair of types; thread_bytes: shared memory of a thread.
+// The kernels of a pair of types; warp_bytes: shared memory of a warp.
 template <typename Tx, typename Ty>
-NormKernel norm_kernel_for(const Shape& s, bool vec, bool post, bool drop, uint32_t* thread_bytes);
+NormKernel norm_kernel_for(const Shape& s, bool vec, bool post, bool drop, uint32_t* warp_bytes);
 template <typename Tx, typename Ty>
-NormKernel norm_backward_kernel_for(const Shape& s, bool vec, bool post, bool drop, uint32_t* thread_bytes);
+NormKernel norm_backward_kernel_for(const Shape& s, bool vec, bool post, bool drop, uint32_t* warp_bytes);
 
 zccl_status_t launch_norm(NormArgs& a, int x_dtype, int dtype, bool vec, cudaStream_t stream);
 zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weight_dtype, bool vec, cudaStream_t stream);

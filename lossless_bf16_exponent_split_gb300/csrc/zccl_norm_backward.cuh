@@ -161,24 +161,23 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(Nor
 // so one sum serves both, and is taken out when the gate changes.  A cluster's exchange
 // takes longer than a row's arithmetic, so a cluster sums the next row (kAhead) before it
 // waits for this one's sums.  kKind: as in the forward kernel.
-constexpr int kAny = 4;
 template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces, int kKind>
 __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeamWarps * 32, kTeam == kWarpTeam ? 2 : 1)
     norm_backward_kernel(NormArgs a)
 {
     extern __shared__ uint4 smem[];
-    constexpr bool kAhead = kTeam == kClusterTeam && kVec;
-    constexpr int kTeamSums = kKind == kAny || (kKind & 1) ? kSums : 2;
-    using Rows = Feed<Tx, Ty, kVec, kPieces, !kVec ? 0 : kAhead ? 3 : 2, true>;
+    constexpr bool kAhead = kTeam == kClusterTeam;
+    constexpr int kTeamSums = kKind & 1 ? kSums : 2;
+    using Rows = Feed<Tx, Ty, kVec, kPieces, kAhead ? 3 : 2, true>;
     // of each warp: its rows, and its sums of p's gradient (two 16-byte parts a piece); then the teams' sums
-    constexpr uint32_t kWarpParts = Rows::kThreadBytes / 16 * 32 + 2 * kPieces * 32;
+    constexpr uint32_t kWarpParts = Rows::kWarpBytes / 16 + 2 * kPieces * 32;
     uint4* const warp_smem = smem + (threadIdx.x >> 5) * kWarpParts;
-    float4* const dp = reinterpret_cast<float4*>(warp_smem) + Rows::kThreadBytes / 16 * 32 + (threadIdx.x & 31);
+    float4* const dp = reinterpret_cast<float4*>(warp_smem) + Rows::kWarpBytes / 16 + (threadIdx.x & 31);
     TeamSum<kTeamSums, kTeam> team_sum(smem + (blockDim.x >> 5) * kWarpParts, a.status);
     pdl_wait();
     const Place at = place<kTeam, kPieces>();
     const bool join = a.grad_y != nullptr, reads_y = a.y != nullptr;
-    const bool post = kKind == kAny ? a.post != 0 : (kKind & 1) != 0, drop = kKind == kAny ? a.drop.below > 0 && join : (kKind & 2) != 0;
+    constexpr bool post = (kKind & 1) != 0, drop = (kKind & 2) != 0;
     const uint64_t offset = drop ? drop_offset(a.drop) : 0;
     const uint32_t lo = at.worker < a.workers ? first_row(a.rows, a.workers, at.worker) : 0;
     const uint32_t hi = at.worker < a.workers ? first_row(a.rows, a.workers, at.worker + 1) : 0;
@@ -351,34 +350,31 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
 }
 
 template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces>
-NormKernel backward_kind(bool post, bool drop, uint32_t* thread_bytes)
+NormKernel backward_kind(bool post, bool drop, uint32_t* warp_bytes)
 {
-    *thread_bytes = Feed<Tx, Ty, kVec, kPieces, !kVec ? 0 : kTeam == kClusterTeam ? 3 : 2, true>::kThreadBytes + 32 * kPieces;
-    if constexpr (kVec)
-        return post ? (drop ? norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 3> : norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 1>)
-                    : (drop ? norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 2> : norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 0>);
-    else
-        return norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, kAny>;
+    *warp_bytes = Feed<Tx, Ty, kVec, kPieces, kTeam == kClusterTeam ? 3 : 2, true>::kWarpBytes + 1024 * kPieces;
+    return post ? (drop ? norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 3> : norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 1>)
+                : (drop ? norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 2> : norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 0>);
 }
 template <typename Tx, typename Ty, bool kVec>
-NormKernel backward_for(const Shape& s, bool post, bool drop, uint32_t* thread_bytes)
+NormKernel backward_for(const Shape& s, bool post, bool drop, uint32_t* warp_bytes)
 {
     constexpr int kMost = kVec && sizeof(Tx) == 2 && sizeof(Ty) == 2 ? 2 : 1;
-    if (s.team == kWarpTeam) return backward_kind<Tx, Ty, kVec, kWarpTeam, 1>(post, drop, thread_bytes);
+    if (s.team == kWarpTeam) return backward_kind<Tx, Ty, kVec, kWarpTeam, 1>(post, drop, warp_bytes);
     if (s.team == kLong) return norm_backward_long_kernel<Tx, Ty, kVec>;
     if (s.team == kCtaTeam)
-        return s.pieces == 1 ? backward_kind<Tx, Ty, kVec, kCtaTeam, 1>(post, drop, thread_bytes)
-                             : backward_kind<Tx, Ty, kVec, kCtaTeam, kMost>(post, drop, thread_bytes);
-    return s.pieces == 1 ? backward_kind<Tx, Ty, kVec, kClusterTeam, 1>(post, drop, thread_bytes)
-                         : backward_kind<Tx, Ty, kVec, kClusterTeam, kMost>(post, drop, thread_bytes);
+        return s.pieces == 1 ? backward_kind<Tx, Ty, kVec, kCtaTeam, 1>(post, drop, warp_bytes)
+                             : backward_kind<Tx, Ty, kVec, kCtaTeam, kMost>(post, drop, warp_bytes);
+    return s.pieces == 1 ? backward_kind<Tx, Ty, kVec, kClusterTeam, 1>(post, drop, warp_bytes)
+                         : backward_kind<Tx, Ty, kVec, kClusterTeam, kMost>(post, drop, warp_bytes);
 }
 
 }  // namespace
 
 template <typename Tx, typename Ty>
-NormKernel norm_backward_kernel_for(const Shape& s, bool vec, bool post, bool drop, uint32_t* thread_bytes)
+NormKernel norm_backward_kernel_for(const Shape& s, bool vec, bool post, bool drop, uint32_t* warp_bytes)
 {
-    return vec ? backward_for<Tx, Ty, true>(s, post, drop, thread_bytes) : backward_for<Tx, Ty, false>(s, post, drop, thread_bytes);
+    return vec ? backward_for<Tx, Ty, true>(s, post, drop, warp_bytes) : backward_for<Tx, Ty, false>(s, post, drop, warp_bytes);
 }
 
 }  // namespace zccl

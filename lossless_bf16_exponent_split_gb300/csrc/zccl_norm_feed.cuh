@@ -26,7 +26,7 @@ template <typename Tx, typename Ty, bool kVec, int kPieces, int kStages, bool kB
 struct Feed {
     static_assert(kVec, "rows on 16 bytes");
     static constexpr int kX = sizeof(Tx) / 2, kY = sizeof(Ty) / 2, kAll = (kX + kY) * (kBackward ? 2 : 1);  // 16-byte parts of a piece
-    static constexpr uint32_t kThreadBytes = kStages * kPieces * kAll * 16;
+    static constexpr uint32_t kWarpBytes = kStages * kPieces * kAll * 512;
     static constexpr uint32_t kStage = kPieces * kAll * 32;  // 16-byte parts of a warp's stage
     const uint4* const mine;  // a warp's parts, 32 lanes each, one behind the other
     uint32_t to;              // the stage that the next row goes to
@@ -112,10 +112,127 @@ struct Feed {
     }
 };
 
+// Rows that begin anywhere: 32-bit values a lane's own ones by one, 16-bit ones by the
+// words that hold them, from the one that holds a tile's first value on.  A value then is
+// a half of a word later in a row that begins in the middle of one, and another lane may
+// have copied it.
+template <typename T>
+constexpr uint32_t kLooseBytes = sizeof(T) == 4 ? 1024 : 528;  // of a tile: 256 values, or 129 words
+template <int kTo, int kFrom>
+__device__ __forceinline__ void copy_4(uint32_t to, const char* from, uint32_t bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0+%3], [%1+%4], 4, %2;" ::"r"(to), "l"(from), "r"(bytes), "n"(kTo), "n"(kFrom) : "memory");
+}
+template <typename Tx, typename Ty, int kStages, bool kBackward>
+struct Feed<Tx, Ty, false, 1, kStages, kBackward> {
+    static constexpr int kX = kLooseBytes<Tx>, kY = kLooseBytes<Ty>, kStage = (kX + kY) * (kBackward ? 2 : 1);
+    static constexpr uint32_t kWarpBytes = kStages * kStage;
+    const char* const mine;  // the warp's stages
+    uint32_t asked = 0;      // the stage that the next row goes to
+    uint32_t shifts = 0;     // of each stage four bits: whether x, y, x1, y1 begin in the middle of a word
+    const char *x, *y, *x1, *y1;  // the tile of the row that is asked for next
+    const uint32_t left;          // columns of the row from the tile on
+    __device__ __forceinline__ Feed(uint4* warp_smem, const NormArgs& a, const Place& place, uint32_t t)
+        : mine(reinterpret_cast<const char*>(warp_smem)), left(place.tile(0) < a.hidden ? a.hidden - place.tile(0) : 0)
+    {
+        for (uint32_t i = threadIdx.x & 31; i < kWarpBytes / 16; i += 32) warp_smem[i] = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        const uint64_t c = left > 0 ? place.tile(0) : 0;
+        x = static_cast<const char*>(a.x) + (t * a.x_stride + c) * sizeof(Tx);
+        if (kBackward) {
+            y = static_cast<const char*>(a.grad_h) + (t * a.grad_h_stride + c) * sizeof(Ty);
+            x1 = static_cast<const char*>(a.grad_r) + (t * a.grad_r_stride + c) * sizeof(Tx);
+            y1 = static_cast<const char*>(a.y) + (t * a.y_stride + c) * sizeof(Ty);
+        } else {
+            y = static_cast<const char*>(a.y) + (t * a.y_stride + c) * sizeof(Ty);
+        }
+    }
+    template <typename T, int kPart, int kBit>
+    __device__ __forceinline__ void copy(const char*& from, uint64_t stride)
+    {
+        const uint32_t lane = threadIdx.x & 31, to = smem_addr(mine) + asked * kStage + kPart + lane * 4;
+        if constexpr (sizeof(T) == 4) {
+            const char* p = from + lane * 4;
+            const auto size = [&](uint32_t j) { return j * 32 + lane < left ? 4u : 0u; };
+            copy_4<0, 0>(to, p, size(0)), copy_4<128, 128>(to, p, size(1)), copy_4<256, 256>(to, p, size(2));
+            copy_4<384, 384>(to, p, size(3)), copy_4<512, 512>(to, p, size(4)), copy_4<640, 640>(to, p, size(5));
+            copy_4<768, 768>(to, p, size(6)), copy_4<896, 896>(to, p, size(7));
+        } else {
+            const uint32_t shift = (uint32_t)(reinterpret_cast<uint64_t>(from) >> 1) & 1u;
+            const char* p = from - 2 * shift + lane * 4;  // (the first word's other half is not looked at)
+            const uint32_t halves = left > 0 ? shift + (left < kTile ? left : kTile) : 0;  // those of the words that are wanted
+            const auto size = [&](uint32_t word) { return 2 * word + 1 < halves ? 4u : 2 * word < halves ? 2u : 0u; };
+            copy_4<0, 0>(to, p, size(lane)), copy_4<128, 128>(to, p, size(32 + lane));
+            copy_4<256, 256>(to, p, size(64 + lane)), copy_4<384, 384>(to, p, size(96 + lane));
+            if (lane == 0) copy_4<512, 512>(to, p, size(128));
+            const uint32_t at = 4 * asked + kBit;
+            shifts = (shifts & ~(1u << at)) | shift << at;
+        }
+        from += stride * sizeof(T);
+    }
+    // Asks for the next row (there: it is one of the worker's).
+    __device__ __forceinline__ void ask(const NormArgs& a, const Place&, bool there)
+    {
+        __syncwarp();  // all lanes have read the stage's last row
+        if (there) {
+            if constexpr (kBackward) {
+                if (a.grad_h != nullptr) {
+                    copy<Tx, 0, 0>(x, a.x_stride);
+                    copy<Ty, kX, 1>(y, a.grad_h_stride);
+                }
+                if (a.grad_r != nullptr) copy<Tx, kX + kY, 2>(x1, a.grad_r_stride);
+                if (a.y != nullptr) copy<Ty, 2 * kX + kY, 3>(y1, a.y_stride);
+            } else {
+                copy<Tx, 0, 0>(x, a.x_stride);
+                if (a.y != nullptr) copy<Ty, kX, 1>(y, a.y_stride);
+            }
+        }
+        asked = asked + 1 == kStages ? 0 : asked + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // Until all but the last kLater rows that were asked for are there.
+    template <int kLater>
+    __device__ __forceinline__ void wait()
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kLater) : "memory");
+        __syncwarp();
+    }
+    struct Row {
+        const char* at;
+        uint32_t shifts;
+        template <typename T>
+        __device__ __forceinline__ Eight read(int part, int bit) const
+        {
+            const uint32_t lane = threadIdx.x & 31;
+            Eight v;
+            if (sizeof(T) == 4) {
+                const float* p = reinterpret_cast<const float*>(at + part) + lane;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = p[32 * j];
+            } else {
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(at + part) + lane + ((shifts >> bit) & 1u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __uint_as_float((uint32_t)p[32 * j] << 16);
+            }
+            return v;
+        }
+        __device__ __forceinline__ Eight x(int) const { return read<Tx>(0, 0); }
+        __device__ __forceinline__ Eight y(int) const { return read<Ty>(kX, 1); }
+        __device__ __forceinline__ Eight x1(int) const { return read<Tx>(kX + kY, 2); }
+        __device__ __forceinline__ Eight y1(int) const { return read<Ty>(2 * kX + kY, 3); }
+    };
+    // The row that was asked for before the last `later` ones.
+    __device__ __forceinline__ Row row(uint32_t later) const
+    {
+        const uint32_t back = asked + kStages - 1 - later, stage = back >= kStages ? back - kStages : back;
+        return {mine + stage * kStage, shifts >> (4 * stage)};
+    }
+};
+
 // Others come into registers: the row that is read, and the next one.
 template <typename Tx, typename Ty, bool kVec, int kPieces, bool kBackward>
 struct Feed<Tx, Ty, kVec, kPieces, 0, kBackward> {
-    static constexpr uint32_t kThreadBytes = 0;
+    static constexpr uint32_t kWarpBytes = 0;
     struct Row {
         Piece<Tx, kVec> px[kPieces], px1[kPieces];
         Piece<Ty, kVec> py[kPieces], py1[kPieces];

@@ -141,15 +141,15 @@ zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weig
     a.groups = s.grid / s.ctas;
     a.parts = a.sums + (uint64_t)a.groups * kWeightSlots * ((a.hidden + 7) / 8 * 8);
     const bool post = a.post, drop = a.drop.below > 0 && a.grad_y != nullptr;
-    uint32_t thread_bytes = 0;
+    uint32_t warp_bytes = 0;
     const NormKernel kernel =
         x_dtype == ZCCL_BF16
-            ? (dtype == ZCCL_BF16 ? norm_backward_kernel_for<__nv_bfloat16, __nv_bfloat16>(s, vec, post, drop, &thread_bytes)
-                                  : norm_backward_kernel_for<__nv_bfloat16, float>(s, vec, post, drop, &thread_bytes))
-            : (dtype == ZCCL_BF16 ? norm_backward_kernel_for<float, __nv_bfloat16>(s, vec, post, drop, &thread_bytes)
-                                  : norm_backward_kernel_for<float, float>(s, vec, post, drop, &thread_bytes));
+            ? (dtype == ZCCL_BF16 ? norm_backward_kernel_for<__nv_bfloat16, __nv_bfloat16>(s, vec, post, drop, &warp_bytes)
+                                  : norm_backward_kernel_for<__nv_bfloat16, float>(s, vec, post, drop, &warp_bytes))
+            : (dtype == ZCCL_BF16 ? norm_backward_kernel_for<float, __nv_bfloat16>(s, vec, post, drop, &warp_bytes)
+                                  : norm_backward_kernel_for<float, float>(s, vec, post, drop, &warp_bytes));
     const uint32_t threads = s.warps * 32;
-    const size_t smem = s.team == kLong ? 0 : threads * thread_bytes + kTeamBytes;
+    const size_t smem = s.team == kLong ? 0 : s.warps * warp_bytes + kTeamBytes;
     cudaError_t e = launch_teams(kernel, s, threads, smem, stream, a);
     if (e == cudaSuccess) e = launch_join(a, weight_dtype, stream);
     return launched(e);
