@@ -153,18 +153,29 @@ struct Feed<Tx, Ty, false, 1, kStages, kBackward> {
         const uint32_t lane = threadIdx.x & 31, to = smem_addr(mine) + asked * kStage + kPart + lane * 4;
         if constexpr (sizeof(T) == 4) {
             const char* p = from + lane * 4;
-            const auto size = [&](uint32_t j) { return j * 32 + lane < left ? 4u : 0u; };
-            copy_4<0, 0>(to, p, size(0)), copy_4<128, 128>(to, p, size(1)), copy_4<256, 256>(to, p, size(2));
-            copy_4<384, 384>(to, p, size(3)), copy_4<512, 512>(to, p, size(4)), copy_4<640, 640>(to, p, size(5));
-            copy_4<768, 768>(to, p, size(6)), copy_4<896, 896>(to, p, size(7));
+            const auto all = [&](auto size) {
+                copy_4<0, 0>(to, p, size(0)), copy_4<128, 128>(to, p, size(1)), copy_4<256, 256>(to, p, size(2));
+                copy_4<384, 384>(to, p, size(3)), copy_4<512, 512>(to, p, size(4)), copy_4<640, 640>(to, p, size(5));
+                copy_4<768, 768>(to, p, size(6)), copy_4<896, 896>(to, p, size(7));
+            };
+            if (left >= kTile)
+                all([](uint32_t) { return 4u; });
+            else
+                all([&](uint32_t j) { return j * 32 + lane < left ? 4u : 0u; });
         } else {
             const uint32_t shift = (uint32_t)(reinterpret_cast<uint64_t>(from) >> 1) & 1u;
             const char* p = from - 2 * shift + lane * 4;  // (the first word's other half is not looked at)
-            const uint32_t halves = left > 0 ? shift + (left < kTile ? left : kTile) : 0;  // those of the words that are wanted
-            const auto size = [&](uint32_t word) { return 2 * word + 1 < halves ? 4u : 2 * word < halves ? 2u : 0u; };
-            copy_4<0, 0>(to, p, size(lane)), copy_4<128, 128>(to, p, size(32 + lane));
-            copy_4<256, 256>(to, p, size(64 + lane)), copy_4<384, 384>(to, p, size(96 + lane));
-            if (lane == 0) copy_4<512, 512>(to, p, size(128));
+            const auto all = [&](auto size) {
+                copy_4<0, 0>(to, p, size(lane)), copy_4<128, 128>(to, p, size(32 + lane));
+                copy_4<256, 256>(to, p, size(64 + lane)), copy_4<384, 384>(to, p, size(96 + lane));
+            };
+            if (left >= kTile) {
+                all([](uint32_t) { return 4u; });
+                if (lane == 0 && shift) copy_4<512, 512>(to, p, 2);
+            } else {
+                const uint32_t halves = left > 0 ? shift + left : 0;  // those of the words that are wanted
+                all([&](uint32_t word) { return 2 * word + 1 < halves ? 4u : 2 * word < halves ? 2u : 0u; });
+            }
             const uint32_t at = 4 * asked + kBit;
             shifts = (shifts & ~(1u << at)) | shift << at;
         }

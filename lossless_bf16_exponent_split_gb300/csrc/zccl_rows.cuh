@@ -158,10 +158,14 @@ __device__ __forceinline__ Eight store8(T* row, const Eight& v, uint32_t tile, u
         } else {
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
             uint16_t* p = reinterpret_cast<uint16_t*>(row) + column<false>(tile, 0);
-            const bool whole = tile + kTile <= cols;
+            if (tile + kTile <= cols) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (whole || column<false>(tile, j) < cols) p[32 * j] = (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
+                for (int j = 0; j < 8; ++j) p[32 * j] = (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (column<false>(tile, j) < cols) p[32 * j] = (uint16_t)(j & 1 ? w[j / 2] >> 16 : w[j / 2]);
+            }
         }
         return widen(q);
     }
@@ -169,11 +173,14 @@ __device__ __forceinline__ Eight store8(T* row, const Eight& v, uint32_t tile, u
         const uint32_t c = column<true>(tile, 0);
         if (c < cols) store_near(reinterpret_cast<float*>(row + c), v);
     } else {
-        float* p = reinterpret_cast<float*>(row);
+        float* p = reinterpret_cast<float*>(row) + column<false>(tile, 0);
+        if (tile + kTile <= cols) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t c = column<false>(tile, j);
-            if (c < cols) p[c] = v[j];
+            for (int j = 0; j < 8; ++j) p[32 * j] = v[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (column<false>(tile, j) < cols) p[32 * j] = v[j];
         }
     }
     return v;
