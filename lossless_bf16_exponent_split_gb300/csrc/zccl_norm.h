@@ -332,6 +332,15 @@ __device__ __forceinline__ Eight join_factors(const NormArgs& a, uint32_t row, u
     const uint64_t at = a.gate.p != nullptr ? (uint64_t)(row / a.gate_span) * a.gate_stride : 0;
     return mul(mul(load_vector<kVec>(a.gate, at, tile, a.hidden), a.scale), a.gain);
 }
+// Asks for the gate's part of the lane's tile, to be loaded when its first row comes.
+template <bool kVec>
+__device__ __forceinline__ void prefetch_gate(const NormArgs& a, uint32_t row, uint32_t tile)
+{
+    const uint32_t c = column<kVec>(tile, 0);
+    if (a.gate.p == nullptr || c >= a.hidden) return;
+    const uint64_t at = ((uint64_t)(row / a.gate_span) * a.gate_stride + c) * (a.gate.dtype == ZCCL_BF16 ? 2 : 4);
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const char*>(a.gate.p) + at));
+}
 // Which of the lane's values of it stay.
 template <bool kVec>
 __device__ __forceinline__ Kept<kVec> join_kept(const NormArgs& a, uint64_t offset, uint32_t row, uint32_t tile)

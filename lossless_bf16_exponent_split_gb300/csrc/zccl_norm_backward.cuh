@@ -208,6 +208,10 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
         for (int n = 0; n < kPieces; ++n)
             kp[n] = mul(join_factors<kVec>(a, t, at.tile(n)), load_vector<kVec>(a.post_weight, 0, at.tile(n), a.hidden));
     };
+    const auto prefetch_gates = [&](uint32_t t) {
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) prefetch_gate<kVec>(a, t, at.tile(n));
+    };
     const auto take_out = [&](uint32_t t) {
         const uint32_t begin = gate_row * a.gate_span;
 #pragma unroll
@@ -288,6 +292,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
 #pragma unroll 1
         for (uint32_t t = lo; t < hi; ++t) {
             rows.ask(a, at, t + 2 < hi);  // into the stage of row t - 1
+            if (join && t + 2 < hi && (a.gate_span == 1 || t + 2 == gate_end)) prefetch_gates(t + 2);
             const bool more = t + 1 < hi, turns = more && join && t + 1 == gate_end;
             float s = 0.0f;
             if (more) {
@@ -314,6 +319,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
             const bool turns = join && t + 1 == gate_end && t + 1 < hi;
             const auto row = rows.row(0);
             rows.ask(a, at, t + 1 < hi);
+            if (turns) prefetch_gates(t + 1);
             Kept<kVec> kept[kPieces];
 #pragma unroll
             for (int n = 0; n < kPieces; ++n) kept[n] = kept_of(t, n);

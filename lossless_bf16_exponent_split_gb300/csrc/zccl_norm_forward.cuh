@@ -107,6 +107,9 @@ __global__ void __launch_bounds__(kVec && kPieces == 1 ? 768 : kTeamWarps * 32) 
                     k[n] = mul(join_factors<kVec>(a, t, at.tile(n)), load_vector<kVec>(a.post_weight, 0, at.tile(n), a.hidden));
                 gate_end = a.gate.p != nullptr ? (t / a.gate_span + 1) * a.gate_span : a.rows;
             }
+            if (t + 1 == gate_end && t + 1 < hi)
+#pragma unroll
+                for (int n = 0; n < kPieces; ++n) prefetch_gate<kVec>(a, t + 1, at.tile(n));
             if (post) {
                 float2 sum = twice(0.0f);
 #pragma unroll
