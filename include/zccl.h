@@ -440,7 +440,7 @@ zccl_status_t zccl_combine_backward(const uint16_t* d_grad_out, const uint16_t* 
  *   loss  = coefficient * (mean of L_s over the sequences with m > 0); 0 without one
  * L_s is 1 where the slots or the scores are shared out evenly.  Of cfg the fields
  * experts, top_k and score are used.  Sums of q are held in fp32 in an order that
- * depends on the sizes alone.  d_loss: float; d_counts: int32 [sequences][E];
+ * depends on the sizes and the sequences alone.  d_loss: float; d_counts: int32 [sequences][E];
  * d_tokens: int32 [sequences + 1], each sequence's m and, last, how many have one.
  * sequences: 1..ZCCL_MAX_SEQUENCES.  Workspace: zeroed once before its first use. */
 #define ZCCL_MAX_SEQUENCES 65536u
@@ -556,8 +556,8 @@ typedef struct {
  *   offset    of the dropout, plus *d_offset where that is not NULL
  * rows < 2^31.  Pointers are aligned to their type; rows that all begin on 16 bytes
  * (of gate and weights too) are moved 16 bytes at a time.  d_status gets
- * ZCCL_ERR_TIMEOUT if a device wait ran out (rows of more than 4096 values are held by
- * several CTAs, which wait for one another's sums); the rows concerned are NaN then. */
+ * ZCCL_ERR_TIMEOUT if a device wait ran out (rows of more than 2048 values may be held
+ * by several CTAs, which wait for one another's sums); the rows concerned are NaN then. */
 zccl_status_t zccl_residual_norm(const zccl_norm_t* cfg, const void* d_x, int x_dtype, uint64_t x_stride,
                                  const void* d_y, int dtype, uint64_t y_stride, const void* d_weight,
                                  const void* d_post_weight, int weight_dtype, const void* d_gate, int gate_dtype,
@@ -576,7 +576,9 @@ zccl_status_t zccl_residual_norm_workspace_bytes(uint64_t hidden, uint64_t rows,
  *   d_grad_y   [rows][hidden] contiguous, of dtype; NULL: a norm alone
  *   d_grad_weight, d_grad_post_weight  [hidden]; d_grad_gate: [rows / gate_span, rounded
  *              up][hidden], contiguous.  NULL: not wanted.  Their sums over rows are
- *              held in fp32, in an order that depends on the sizes alone. */
+ *              held in fp32, in an order that depends on sizes, types and alignment
+ *              alone.
+ * d_status as above. */
 zccl_status_t zccl_residual_norm_backward(const zccl_norm_t* cfg, const void* d_grad_r, uint64_t grad_r_stride,
                                           const void* d_grad_h, uint64_t grad_h_stride, const void* d_r, int x_dtype,
                                           uint64_t r_stride, const void* d_y, int dtype, uint64_t y_stride,
