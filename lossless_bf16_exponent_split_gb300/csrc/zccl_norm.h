@@ -35,6 +35,7 @@ struct NormArgs {
     float* sums;         // workspace: weights' sums of each group (a CTA's or a cluster's teams), then gates' parts
     float* parts;
     uint32_t groups, workers;
+    int joined;          // the kernel that adds them up follows
 };
 
 // Rows are shared out over workers, each a run of neighbouring rows.  In a backward

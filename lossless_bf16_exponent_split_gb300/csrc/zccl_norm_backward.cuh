@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeam
     }
     team_sum.close();
     if (reads_y && lo < hi) take_out(hi);
-    pdl_launch_dependents();
+    if (a.joined) pdl_launch_dependents();
     // the weights' sums, of a CTA's warps where each is a team
     float* const sums = a.sums + (uint64_t)(kTeam == kWarpTeam ? blockIdx.x : at.worker) * kWeightSlots * pitch;
     const auto put_sums = [&](int slot) {

@@ -114,22 +114,24 @@ cudaError_t launch_2d(void (*kernel)(Args...), dim3 grid, uint32_t threads, cuda
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// What is to be added up: weights' sums, gate rows' parts.
+bool joins_weights(const NormArgs& a) { return a.grad_weight != nullptr || a.grad_post_weight != nullptr; }
+bool joins_gates(const NormArgs& a) { return a.grad_gate != nullptr && a.gate_span > 1 && a.workers > 1; }
+
 cudaError_t launch_join(const NormArgs& a, int weight_dtype, cudaStream_t stream)
 {
-    const bool gate = a.grad_gate != nullptr && a.gate_span > 1 && a.workers > 1;
     const uint32_t gate_rows = (a.rows - 1) / a.gate_span + 1;
-    const bool by_row = gate && gate_rows < a.workers;
-    cudaError_t e = cudaSuccess;
-    if (gate && !by_row) e = launch_2d(norm_join_gates_kernel, dim3((a.hidden + 255) / 256, a.workers - 1), 256, stream, a);
-    if (e == cudaSuccess && (a.grad_weight != nullptr || a.grad_post_weight != nullptr || by_row))
-    {
-        // 32 columns a CTA, fewer where that makes less than 128 of them
-        const uint32_t jobs = by_row ? 2 + gate_rows : 2;
-        const uint32_t lanes = a.hidden * jobs >= 128 * 32 ? 8 : a.hidden * jobs >= 128 * 16 ? 4 : 2;
-        e = launch_2d(lanes == 8 ? norm_join_kernel<8> : lanes == 4 ? norm_join_kernel<4> : norm_join_kernel<2>,
-                      dim3((a.hidden + 4 * lanes - 1) / (4 * lanes), jobs), kJoinThreads, stream, a, weight_dtype);
+    const bool by_row = joins_gates(a) && gate_rows < a.workers;
+    if (joins_gates(a) && !by_row) {
+        const cudaError_t e = launch_2d(norm_join_gates_kernel, dim3((a.hidden + 255) / 256, a.workers - 1), 256, stream, a);
+        if (e != cudaSuccess) return e;
     }
-    return e;
+    if (!joins_weights(a) && !by_row) return cudaSuccess;
+    // 32 columns a CTA, fewer where that makes less than 128 of them
+    const uint32_t jobs = by_row ? 2 + gate_rows : 2;
+    const uint32_t lanes = a.hidden * jobs >= 128 * 32 ? 8 : a.hidden * jobs >= 128 * 16 ? 4 : 2;
+    return launch_2d(lanes == 8 ? norm_join_kernel<8> : lanes == 4 ? norm_join_kernel<4> : norm_join_kernel<2>,
+                     dim3((a.hidden + 4 * lanes - 1) / (4 * lanes), jobs), kJoinThreads, stream, a, weight_dtype);
 }
 
 }  // namespace
@@ -150,8 +152,9 @@ zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weig
                                   : norm_backward_kernel_for<float, float>(s, vec, post, drop, &warp_bytes));
     const uint32_t threads = s.warps * 32;
     const size_t smem = s.team == kLong ? 0 : s.warps * warp_bytes + kTeamBytes;
+    a.joined = joins_weights(a) || joins_gates(a);
     cudaError_t e = launch_teams(kernel, s, threads, smem, stream, a);
-    if (e == cudaSuccess) e = launch_join(a, weight_dtype, stream);
+    if (e == cudaSuccess && a.joined) e = launch_join(a, weight_dtype, stream);
     return launched(e);
 }
 

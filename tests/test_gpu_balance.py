@@ -150,6 +150,24 @@ def test_one_workspace_for_calls_of_all_sizes(z):
         assert abs(float(got.loss) - loss) <= LOSS * loss
 
 
+def test_more_than_2_to_31_logits(z):
+    """Addresses beyond 32 bits: equal logits give equal shares, and the last tokens the gradient that they give by themselves."""
+    tokens, experts = (1 << 22) + 5, 512
+    l = torch.zeros(tokens, experts, dtype=B, device="cuda")
+    idx = (torch.arange(tokens, device="cuda") % experts).to(torch.int32)[:, None].contiguous()
+    l[-1, :7] = 1.0
+    moe = z.Moe(experts, 1)
+    seq = torch.tensor([0, tokens - 3, tokens], dtype=torch.int32, device="cuda")
+    got = moe.balance(l, idx, seq)
+    loss, counts, live, grad, mag = ref.balance(l[-3:], idx[-3:], [0, 3], "softmax", 0.5)
+    assert torch.equal(got.counts[1:].cpu(), counts) and got.tokens.tolist() == [tokens - 3, 3, 2]
+    assert int(got.counts[0].max() - got.counts[0].min()) <= 1
+    assert abs(float(got.loss) - (0.5 + loss)) < LOSS
+    have = moe.balance_backward(l, idx, got, seq)
+    close(have[-3:], grad, mag)
+    assert float(have[:-3].abs().max()) < 1e-9  # shares of 1 / 512, slots that differ by one of 8192
+
+
 def test_empty(z):
     moe = z.Moe(8, 2)
     l, idx = torch.zeros(0, 8, device="cuda"), torch.zeros(0, 2, dtype=torch.int32, device="cuda")

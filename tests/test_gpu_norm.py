@@ -218,6 +218,51 @@ def test_rows_that_are_not_finite_stay_their_own(z):
     assert torch.equal(r, m.add(x, y, w)[0]) and bool(r.isfinite().all()) and bool(h.isfinite().all())
 
 
+@pytest.mark.parametrize("hidden", [520, 1001, 9000])
+def test_all_dropped(z, hidden):
+    n, x, y, w, more, grad_r, grad_h = inputs(z, 8, hidden, B, B, F, True, 2, 1.0, 1.0)
+    r, h = n.add(x, y, w, **more)
+    assert torch.equal(r, x) and torch.equal(h, n.norm(x, w))
+    g = n.add_backward(grad_r, grad_h, r, y, w, **more)
+    assert torch.equal(g.x, n.norm_backward(grad_h, x, w, residual=grad_r)[0])
+    assert all(bool((t == 0).all()) for t in (g.y, g.post_weight, g.gate))
+
+
+@pytest.mark.parametrize("hidden", [2048, 1001])
+def test_more_than_2_to_31_values(z, hidden):
+    """Addresses beyond 32 bits: the last rows against the same rows by themselves, and the weight's gradient of ones."""
+    rows = (1 << 31) // hidden + 7
+    n = z.ResidualNorm(hidden, dropout=0.5, seed=3)
+    x = torch.ones(rows, hidden, dtype=B, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    tail = torch.randn(5, hidden, generator=g, device="cuda").to(B)
+    x[-5:] = tail
+    r, h = n.add(x, x, offset=4)
+    at = ref.Ref(x=tail, y=tail)
+    keep = torch.from_numpy(kept_rows(rows - 5, 5, hidden, 0.5, 3, 4))
+    want = torch.where(keep, 3 * tail.double().cpu(), tail.double().cpu())  # x + x / (1 - p)
+    close(r[-5:], want, want.abs(), "r")
+    close(h[-5:], at.h(r[-5:]), at.h(r[-5:]).abs(), "h")
+    one, half = n.norm(x[-5:]), torch.ones(hidden, device="cuda")
+    gx, gw = n.norm_backward(x, x, half)
+    want = n.norm_backward(tail, tail, half)[0]
+    assert torch.equal(gx[-5:], want) and torch.equal(one, n.norm(x)[-5:])
+    # a row of ones has the norm 1 / sqrt(1 + 1e-6) each time
+    total = (rows - 5) / (1 + 1e-6) ** 0.5 + (tail.double() * ref.inverse_rms(tail.double(), 1e-6) * tail.double()).sum(0)
+    # a worker adds its n rows, 14,200 at most, one after the other: n / 2 half steps of the sum, and the joined parts' few
+    assert float((gw.double() / total - 1).abs().max()) < 8192 * 2.0 ** -24
+
+
+def kept_rows(first, rows, cols, p, seed, offset):
+    """The dropout's kept elements of some rows."""
+    import numpy as np
+    blocks = -(-cols // 8)
+    b, r = np.meshgrid(np.arange(blocks, dtype=np.uint64), np.arange(first, first + rows, dtype=np.uint64))
+    words = ref.philox((b, r, np.full_like(b, offset), np.zeros_like(b)), (seed, 0))
+    halves = np.stack([np.stack([w & np.uint64(0xFFFF), w >> np.uint64(16)], -1) for w in words], -2)
+    return halves.reshape(rows, blocks * 8)[:, :cols] >= ref.dropped_of(p)
+
+
 def test_large_and_small_values(z):
     """Squares up to 2^126 and down to where eps takes over."""
     n = z.ResidualNorm(1024, post=True, eps=1e-20)
