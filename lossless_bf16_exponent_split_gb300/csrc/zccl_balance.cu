@@ -9,10 +9,10 @@
 //
 // The bytes are few (16384 x 64 in BF16: 2 MB, 0.3 us of HBM time): a call is bound by its
 // latencies (the table, the first logits, the hand-over to the last part), 6.6 us for the
-// loss and 4.3 for the gradient; many experts by issue (65621 x 256 in 32 bits with
-// sigmoid scores: 182 and 246 instructions a warp and token, six of ten issue slots, 25 us
-// each, 2.7 TB/s).  Exponentials and reciprocals are the fast ones: nothing here decides
-// between close values.
+// loss and 4.3 for the gradient; many experts by those and by issue (65621 x 256 in 32 bits
+// with sigmoid scores: 149 and 197 instructions a warp and token, in six of ten issue
+// slots; 46 us for both, 3.0 TB/s; logits three tokens ahead by asynchronous copies 49).
+// Exponentials and reciprocals are the fast ones: nothing here decides between close values.
 #include <cmath>
 
 #include "zccl_ops.cuh"
@@ -60,6 +60,18 @@ __device__ __forceinline__ float lanes_add(float x)
 #pragma unroll
     for (int o = L / 2; o > 0; o /= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
     return x;
+}
+
+// Two sums at once: half the lanes add up x, half y.
+template <int L>
+__device__ __forceinline__ void lanes_add(float& x, float& y)
+{
+    const bool upper = threadIdx.x & (L / 2);
+    float mine = (upper ? y : x) + __shfl_xor_sync(0xFFFFFFFFu, upper ? x : y, L / 2);
+    mine = lanes_add<L / 2>(mine);
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, mine, L / 2);
+    x = upper ? other : mine;
+    y = upper ? mine : other;
 }
 
 // A CTA's part: tokens lo..hi-1 of a sequence (`sequences`: the tokens behind the last
@@ -132,21 +144,21 @@ __device__ __forceinline__ bool part_of(const BalanceArgs& a, Part* p)
     return p->parts > 0;
 }
 
-// How a token's logits are read: eight neighbours at a time (kNeighbours; kWhole: and the
-// experts are as many as L lanes of J hold), or one by one.
+// How a token's logits are read: 16 bytes at a time, the lanes' one behind the other
+// (kNeighbours; kWhole: and the experts are as many as L lanes of J hold), or one by one.
 enum Read { kOneByOne = 0, kNeighbours = 1, kWhole = 2 };
 
-// A lane's logits of a token, as they are held in memory: eight neighbours at a time, or
+// A lane's logits of a token, as they are held in memory: 16 bytes of neighbours at a time, or
 // L apart.
 template <typename T, int kRead, int L, int J>
 struct Logits {
     static constexpr bool kVec = kRead != kOneByOne;
-    static constexpr int kWords = kVec ? J * sizeof(T) / 16 : 0;
+    static constexpr int kWords = kVec ? J * sizeof(T) / 16 : 0, kPart = 16 / sizeof(T);
     uint4 q[kVec ? kWords : 1];
     float f[kVec ? 1 : J];
     static __device__ __forceinline__ uint32_t expert(uint32_t li, int j)
     {
-        return kVec ? j / 8 * 8 * L + li * 8 + j % 8 : li + L * j;
+        return kVec ? j / kPart * kPart * L + li * kPart + j % kPart : li + L * j;
     }
     __device__ __forceinline__ void load(const T* row, uint32_t li, uint32_t E)
     {
@@ -214,10 +226,21 @@ __device__ __forceinline__ float reciprocal(float x)
     return y;
 }
 
+// exp(-l); kFinite: 2^127 at most (a NaN stays one)
+template <bool kFinite>
+__device__ __forceinline__ float exp_of_minus(float l)
+{
+    float x = l * -1.44269504f, y;
+    if (kFinite) asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(x), "f"(127.0f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // A row's scores p and the factor that makes them its shares, 0 where it has none; with
-// kSlope also the sigmoid's 1 - p.
+// kSlope also the sigmoid's 1 - p, and the sum of the shares times f in `dot`.
 template <bool kSlope, int L, int J>
-__device__ __forceinline__ float scores(const BalanceArgs& a, const float (&l)[J], float (&p)[J], float (&slope)[J])
+__device__ __forceinline__ float scores(const BalanceArgs& a, const float (&l)[J], float (&p)[J], float (&slope)[J],
+                                        const float (&f)[J], float* dot)
 {
     const auto largest = [&]() {
         float m = l[0];
@@ -227,38 +250,56 @@ __device__ __forceinline__ float scores(const BalanceArgs& a, const float (&l)[J
         for (int o = L / 2; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         return m == -kInf ? 0.0f : m;
     };
+    float total, weighted = 0.0f;
     const auto sum = [&]() {
-        float2 s = make_float2(0.0f, 0.0f);
+        float2 s = make_float2(0.0f, 0.0f), u = s;
 #pragma unroll
-        for (int j = 0; j < J; j += 2) s = __fadd2_rn(s, make_float2(p[j], p[j + 1]));
-        return lanes_add<L>(s.x + s.y);
+        for (int j = 0; j < J; j += 2) {
+            s = __fadd2_rn(s, make_float2(p[j], p[j + 1]));
+            if (kSlope) u = __ffma2_rn(make_float2(p[j], p[j + 1]), make_float2(f[j], f[j + 1]), u);
+        }
+        total = s.x + s.y;
+        if (kSlope) {
+            weighted = u.x + u.y;
+            lanes_add<L>(total, weighted);
+        } else {
+            total = lanes_add<L>(total);
+        }
     };
-    float total;
     if (a.sigmoid) {
 #pragma unroll
         for (int j = 0; j < J; j += 2) {
-            const float2 t = make_float2(exp_fast(-fabsf(l[j])), exp_fast(-fabsf(l[j + 1])));
+            // t = exp(-l), p = 1 / (1 + t), 1 - p = t p: no difference of close values; from 2^126 on p is 0, and
+            // the slope needs a finite t
+            const float2 t = make_float2(exp_of_minus<kSlope>(l[j]), exp_of_minus<kSlope>(l[j + 1]));
             const float2 n = __fadd2_rn(t, make_float2(1.0f, 1.0f)), r = make_float2(reciprocal(n.x), reciprocal(n.y));
-            const float2 tr = __fmul2_rn(t, r);
-            p[j] = l[j] >= 0.0f ? r.x : tr.x;
-            p[j + 1] = l[j + 1] >= 0.0f ? r.y : tr.y;
-            if (kSlope) slope[j] = l[j] >= 0.0f ? tr.x : r.x, slope[j + 1] = l[j + 1] >= 0.0f ? tr.y : r.y;
+            p[j] = r.x, p[j + 1] = r.y;
+            if (kSlope) {
+                const float2 q = __fmul2_rn(t, r);
+                slope[j] = q.x, slope[j + 1] = q.y;
+            }
         }
-        total = sum();
+        sum();
         // scores whose sum is below 2^-80: over a common factor, which keeps the largest from underflow (1 + exp(l) is 1)
         if (__any_sync(0xFFFFFFFFu, total < 0x1p-80f)) {
             const float m = largest();
+            const bool small = total < 0x1p-80f;
 #pragma unroll
-            for (int j = 0; j < J; ++j) p[j] = total < 0x1p-80f ? exp_fast(l[j] - m) : p[j];
-            total = sum();
+            for (int j = 0; j < J; ++j) {
+                p[j] = small ? exp_fast(l[j] - m) : p[j];
+                if (kSlope) slope[j] = small ? 1.0f : slope[j];
+            }
+            sum();
         }
     } else {
         const float m = largest();
 #pragma unroll
         for (int j = 0; j < J; ++j) p[j] = exp_fast(l[j] - m);
-        total = sum();
+        sum();
     }
-    return total == 0.0f ? 0.0f : reciprocal(total);
+    const float share = total == 0.0f ? 0.0f : reciprocal(total);
+    if (kSlope) *dot = weighted * share;
+    return share;
 }
 
 // A lane's experts of a token (entries L apart).
@@ -266,26 +307,64 @@ template <int L>
 struct Choices {
     static constexpr int kEach = ZCCL_MAX_TOP_K / L;
     int32_t e[kEach];
-    __device__ __forceinline__ void load(const BalanceArgs& a, uint64_t t, bool there, uint32_t li)
+    // `at`: the lane's first entry of the token
+    __device__ __forceinline__ void load(const int32_t* at, uint32_t K, bool there, uint32_t li)
     {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) e[i] = there && li + L * i < a.K ? a.idx[t * a.K + li + L * i] : -1;
+        for (int i = 0; i < kEach; ++i) e[i] = there && li + L * i < K ? at[L * i] : -1;
     }
     // Calls `use` with each of them; whether the token has any.
     template <typename Use>
-    __device__ __forceinline__ bool each(const BalanceArgs& a, uint32_t li, Use use) const
+    __device__ __forceinline__ bool each(uint32_t E, uint32_t li, Use use) const
     {
         bool any = false;
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
-            if (e[i] >= 0 && (uint32_t)e[i] < a.E) {
+            if ((uint32_t)e[i] < E) {
                 any = true;
                 use(e[i]);
             }
         __syncwarp();
-        const uint32_t lane = threadIdx.x & 31;
-        return (__ballot_sync(0xFFFFFFFFu, any) >> (lane - li) & (0xFFFFFFFFu >> (32 - L))) != 0;
+        const uint32_t who = __ballot_sync(0xFFFFFFFFu, any);
+        return L == 32 ? who != 0 : (who >> ((threadIdx.x & 31) - li) & (0xFFFFFFFFu >> (32 - L))) != 0;
     }
+};
+
+// The tokens of a warp: kTokens at a time, the CTA's warps behind one another.
+template <typename T, int kRead, int L, int J>
+struct Walk {
+    static constexpr uint32_t kTokens = 32 / L, kStep = kWarps * kTokens;
+    uint32_t t, hi, li;           // this lane's token
+    const T* logits;              // of the token to come
+    const int32_t* idx;
+    Logits<T, kRead, L, J> row;
+    Choices<L> next;
+    __device__ __forceinline__ void open(const BalanceArgs& a, uint64_t lo, uint64_t end, bool counted)
+    {
+        const uint32_t lane = threadIdx.x & 31;
+        li = lane % L, hi = (uint32_t)end;
+        t = (uint32_t)lo + (threadIdx.x >> 5) * kTokens + lane / L;
+        logits = static_cast<const T*>(a.logits) + t * a.stride;
+        idx = a.idx + (uint64_t)t * a.K + li;
+        load(a, t, counted);
+    }
+    __device__ __forceinline__ void load(const BalanceArgs& a, uint32_t at, bool counted)
+    {
+        if (at < hi) row.load(logits, li, a.E);
+        next.load(idx, a.K, at < hi && counted, li);
+    }
+    // Takes over what was loaded, and asks for the next.
+    __device__ __forceinline__ Choices<L> take(const BalanceArgs& a, float (&l)[J], bool counted)
+    {
+        const Choices<L> chosen = next;
+        row.get(l, li, a.E);
+        logits += kStep * a.stride;
+        idx += kStep * a.K;
+        load(a, t + kStep, counted);
+        return chosen;
+    }
+    // whether the warp has tokens left
+    __device__ __forceinline__ bool more() const { return t - (threadIdx.x & 31) / L < hi; }
 };
 
 // Whether this CTA is the last of `n` to come by; what the others wrote before is visible to it then.
@@ -301,12 +380,12 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t n)
 template <typename T, int kRead, int L, int J>
 __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
 {
-    constexpr int kExperts = L * J, kTokens = 32 / L;
+    constexpr int kExperts = L * J;
     __shared__ float sums[kWarps][kExperts];
     __shared__ int32_t slots[kExperts];
     __shared__ int32_t live_tokens;
     __shared__ float red[kWarps];
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % L;
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (uint32_t e = threadIdx.x; e < kExperts; e += kThreads) slots[e] = 0;
     if (threadIdx.x == 0) live_tokens = 0;
     __syncthreads();
@@ -314,28 +393,18 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
     Part part;
     if (!part_of<false>(a, &part)) return;
     const uint32_t s = part.sequence;
-    const uint64_t lo = part.lo, hi = part.hi;
     float sum[J] = {};
     int32_t live = 0;
-    Logits<T, kRead, L, J> row;
-    const T* const logits = static_cast<const T*>(a.logits);
-    const uint64_t t0 = lo + warp * kTokens + lane / L;
-    Choices<L> next;
-    if (t0 < hi) row.load(logits + t0 * a.stride, li, a.E);
-    next.load(a, t0, t0 < hi, li);
-    for (uint64_t t = t0; __any_sync(0xFFFFFFFFu, t < hi); t += kWarps * kTokens) {
+    Walk<T, kRead, L, J> walk;
+    for (walk.open(a, part.lo, part.hi, true); walk.more(); walk.t += walk.kStep) {
         float l[J], p[J], slope[J];
-        row.get(l, li, a.E);
-        const Choices<L> chosen = next;
-        const uint64_t t1 = t + kWarps * kTokens;
-        if (t1 < hi) row.load(logits + t1 * a.stride, li, a.E);
-        next.load(a, t1, t1 < hi, li);
-        const bool counts = chosen.each(a, li, [&](int32_t e) { atomicAdd(&slots[e], 1); });
-        live += counts && li == 0 ? 1 : 0;
+        const Choices<L> chosen = walk.take(a, l, true);
+        const bool counts = chosen.each(a.E, walk.li, [&](int32_t e) { atomicAdd(&slots[e], 1); });
+        live += counts && walk.li == 0 ? 1 : 0;
         if (!__all_sync(0xFFFFFFFFu, counts) && !counts)
 #pragma unroll
             for (int j = 0; j < J; ++j) l[j] = -kInf;  // whatever it holds
-        const float f = scores<false, L, J>(a, l, p, slope);
+        const float f = scores<false, L, J>(a, l, p, slope, l, nullptr);
 #pragma unroll
         for (int j = 0; j < J; j += 2) {
             const float2 v = __ffma2_rn(make_float2(p[j], p[j + 1]), make_float2(f, f), make_float2(sum[j], sum[j + 1]));
@@ -349,7 +418,7 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
         for (int j = 0; j < J; ++j) sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], o);
     if (lane < L)
 #pragma unroll
-        for (int j = 0; j < J; ++j) sums[warp][row.expert(li, j)] = sum[j];
+        for (int j = 0; j < J; ++j) sums[warp][walk.row.expert(walk.li, j)] = sum[j];
     live = __reduce_add_sync(0xFFFFFFFFu, live);
     if (lane == 0) atomicAdd(&live_tokens, live);
     __syncthreads();
@@ -453,28 +522,22 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
 template <typename T, int kRead, int L, int J>
 __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs a)
 {
-    constexpr int kTokens = 32 / L;
     pdl_wait();
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % L;
     Part part;
     if (!part_of<true>(a, &part)) return;
     const uint32_t s = part.sequence;
-    const uint64_t lo = part.lo, hi = part.hi;
     const bool counted = s < a.sequences;
-    if (lo >= hi || (!counted && a.accumulate)) return;
-    Logits<T, kRead, L, J> row;
-    const T* const logits = static_cast<const T*>(a.logits);
-    const uint64_t t0 = lo + warp * kTokens + lane / L;
-    Choices<L> next;
-    if (t0 < hi) row.load(logits + t0 * a.stride, li, a.E);
-    next.load(a, t0, t0 < hi && counted, li);
+    if (part.lo >= part.hi || (!counted && a.accumulate)) return;
+    Walk<T, kRead, L, J> walk;
+    walk.open(a, part.lo, part.hi, counted);
+    T* out = static_cast<T*>(a.grad) + walk.t * a.grad_stride;
     // what a unit of an expert's shares adds to the loss
     float f[J] = {};
     if (counted) {
         int32_t c[J], used = 0;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const uint32_t e = row.expert(li, j);
+            const uint32_t e = walk.row.expert(walk.li, j);
             c[j] = e < a.E ? a.counts[(uint64_t)s * a.E + e] : 0;
             used += c[j];
         }
@@ -486,42 +549,30 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs 
 #pragma unroll
         for (int j = 0; j < J; ++j) f[j] = unit * (float)c[j];
     }
-    for (uint64_t t = t0; __any_sync(0xFFFFFFFFu, t < hi); t += kWarps * kTokens) {
-        float l[J], g[J], slope[J];
-        row.get(l, li, a.E);
-        const Choices<L> chosen = next;
-        const uint64_t t1 = t + kWarps * kTokens;
-        if (t1 < hi) row.load(logits + t1 * a.stride, li, a.E);
-        next.load(a, t1, t1 < hi && counted, li);
-        const bool there = t < hi, counts = chosen.each(a, li, [](int32_t) {});
+    for (; walk.more(); walk.t += walk.kStep, out += walk.kStep * a.grad_stride) {
+        float l[J], g[J], slope[J], sum;
+        const Choices<L> chosen = walk.take(a, l, counted);
+        const bool there = walk.t < walk.hi, counts = chosen.each(a.E, walk.li, [](int32_t) {});
         if (!__all_sync(0xFFFFFFFFu, counts) && !counts)
 #pragma unroll
             for (int j = 0; j < J; ++j) l[j] = -kInf;  // whatever it holds
-        const float share = scores<true, L, J>(a, l, g, slope);
-        float2 part = make_float2(0.0f, 0.0f);
+        const float share = scores<true, L, J>(a, l, g, slope, f, &sum);
 #pragma unroll
         for (int j = 0; j < J; j += 2) {
-            const float2 q = __fmul2_rn(make_float2(g[j], g[j + 1]), make_float2(share, share));
-            part = __ffma2_rn(q, make_float2(f[j], f[j + 1]), part);
-            g[j] = q.x, g[j + 1] = q.y;
-        }
-        const float sum = lanes_add<L>(part.x + part.y);
-#pragma unroll
-        for (int j = 0; j < J; j += 2) {
-            float2 q = __fmul2_rn(make_float2(g[j], g[j + 1]), __fadd2_rn(make_float2(f[j], f[j + 1]), make_float2(-sum, -sum)));
+            float2 q = __fadd2_rn(make_float2(f[j], f[j + 1]), make_float2(-sum, -sum));
+            q = __fmul2_rn(__fmul2_rn(make_float2(g[j], g[j + 1]), make_float2(share, share)), q);
             if (a.sigmoid) q = __fmul2_rn(q, make_float2(slope[j], slope[j + 1]));
             g[j] = q.x, g[j + 1] = q.y;
         }
         if (!there || (a.accumulate && !counts)) continue;
-        T* out = static_cast<T*>(a.grad) + t * a.grad_stride;
         if (a.accumulate) {
             Logits<T, kRead, L, J> old;
-            old.load(out, li, a.E);
-            old.get(l, li, a.E);
+            old.load(out, walk.li, a.E);
+            old.get(l, walk.li, a.E);
 #pragma unroll
             for (int j = 0; j < J; ++j) g[j] += l[j];
         }
-        store_row<T, kRead, L, J>(out, g, li, a.E);
+        store_row<T, kRead, L, J>(out, g, walk.li, a.E);
     }
 }
 
@@ -540,7 +591,7 @@ BalanceKernel balance_for(const BalanceArgs& a, bool backward)
     const auto on_16 = [&](const void* p, uint64_t stride) {
         return is_aligned(p, 16) && (a.tokens <= 1 || stride * sizeof(T) % 16 == 0);
     };
-    if (a.E % 8 != 0 || !on_16(a.logits, a.stride) || (backward && !on_16(a.grad, a.grad_stride)))
+    if (a.E % (16 / sizeof(T)) != 0 || !on_16(a.logits, a.stride) || (backward && !on_16(a.grad, a.grad_stride)))
         return balance_for<T, kOneByOne>(a.E, backward);
     const bool whole = a.E == 64 || a.E == 128 || a.E == 256 || a.E == ZCCL_MAX_EXPERTS;
     return whole ? balance_for<T, kWhole>(a.E, backward) : balance_for<T, kNeighbours>(a.E, backward);

@@ -131,12 +131,46 @@ def test_tables_out_of_range_stay_in_bounds(z):
     """A table that runs backwards or past the tokens is cut to what there is."""
     l, idx = inputs(100, 16, 2, F, masked=0.0)
     moe = z.Moe(16, 2)
-    for table, bounds in (([0, 5000], [0, 100]), ([-9, 40, 20, 60], [0, 40, 40, 60]), ([0, -5], [0, 0])):
+    for table, bounds in (([0, 5000], [0, 100]), ([-9, 40, 20, 60], [0, 40, 40, 60]), ([0, -5], [0, 0]),
+                          ([0, 7, 3, 900] + [50] * 40, [0, 7])):
         seq = torch.tensor(table, dtype=torch.int32, device="cuda")
         got = moe.balance(l, idx, seq)
         assert int(got.counts.sum()) <= 2 * 200 and bool(got.loss.isfinite())
         assert bool(moe.balance_backward(l, idx, got, seq).isfinite().all())
         assert torch.equal(got.counts[0].cpu(), ref.balance(l, idx, bounds, "softmax")[1][0])
+
+
+@pytest.mark.parametrize("sequences", [31, 33, 303, 304, 305])
+@pytest.mark.parametrize("experts", [12, 256])
+def test_sequences_around_the_most_that_are_cut(z, sequences, experts):
+    """Up to 304 sequences are cut into parts, each is one beyond.  Some have no tokens."""
+    g = torch.Generator().manual_seed(sequences)
+    tokens = 5000
+    bounds = sorted(torch.randint(0, tokens - 50, (sequences + 1,), generator=g).tolist())
+    bounds[0], bounds[5] = 0, bounds[4]
+    l, idx = inputs(tokens, experts, 4, F)
+    moe, seq = z.Moe(experts, 4, score="sigmoid"), torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    loss, counts, live, grad, mag = ref.balance(l, idx, bounds, "sigmoid")
+    got = moe.balance(l, idx, seq)
+    assert torch.equal(got.counts.cpu(), counts) and torch.equal(got.tokens.cpu(), live)
+    assert abs(float(got.loss) - loss) <= LOSS * abs(loss)
+    close(moe.balance_backward(l, idx, got, seq), grad, mag)
+
+
+def test_sigmoid_of_all_sizes(z):
+    """Scores below 2^-126 may read as none: of a sum of 2^-80 or more (smaller sums take a common factor) that is a
+    share below 2^-46."""
+    g = torch.Generator().manual_seed(3)
+    level = torch.linspace(-140, 140, 2000)[:, None]
+    l = (level + torch.randn(2000, 16, generator=g) * torch.linspace(0, 40, 16)).cuda()
+    idx = torch.topk(l, 2).indices.to(torch.int32)
+    moe = z.Moe(16, 2, score="sigmoid")
+    loss, counts, live, grad, mag = ref.balance(l, idx, [0, 2000], "sigmoid")
+    got = moe.balance(l, idx)
+    assert torch.equal(got.counts.cpu(), counts) and abs(float(got.loss) - loss) <= LOSS * loss
+    f = counts.double() * 16 / (2.0 * 2000 * 2000)  # what a share weighs
+    off = (moe.balance_backward(l, idx, got).double().cpu() - grad).abs()
+    assert bool((off <= (GRAD + 2.0 ** -24) * mag + 2.0 ** -46 * f.max()).all())
 
 
 def test_one_workspace_for_calls_of_all_sizes(z):
