@@ -9,7 +9,6 @@ namespace zccl {
 namespace {
 
 bool dtype_ok(int dtype) { return dtype == ZCCL_BF16 || dtype == ZCCL_F32; }
-uint64_t size_of(int dtype) { return dtype == ZCCL_BF16 ? 2 : 4; }
 
 // The configuration and what both directions share; *drop_ok false: refused.
 bool norm_config(const zccl_norm_t* c, int x_dtype, int dtype, const void* d_weight, const void* d_post_weight,
@@ -49,7 +48,7 @@ bool on_16(const void* p, int dtype, uint64_t stride, uint64_t rows)
 
 zccl_status_t launch_norm(NormArgs& a, int x_dtype, int dtype, bool vec, cudaStream_t stream)
 {
-    const Shape s = norm_shape(a.hidden, a.rows, vec && x_dtype == ZCCL_BF16 && dtype == ZCCL_BF16, vec, false);
+    const Shape s = norm_shape(a.hidden, a.rows, size_of(x_dtype) + size_of(dtype), vec, false);
     a.workers = s.workers;
     const bool post = a.post && a.y != nullptr, drop = a.drop.below > 0;
     uint32_t warp_bytes = 0;
@@ -101,9 +100,12 @@ zccl_status_t zccl_residual_norm(const zccl_norm_t* cfg, const void* d_x, int x_
 zccl_status_t zccl_residual_norm_workspace_bytes(uint64_t hidden, uint64_t rows, uint64_t* bytes)
 {
     if (bytes == nullptr || hidden == 0 || hidden > ZCCL_MAX_NORM_HIDDEN || rows >= (1ull << 31)) return ZCCL_ERR_INVALID_ARG;
-    const uint64_t narrow = norm_backward_bytes(norm_shape(hidden, rows, true, true, true), hidden);
-    const uint64_t wide = norm_backward_bytes(norm_shape(hidden, rows, false, true, true), hidden);
-    *bytes = narrow > wide ? narrow : wide;  // whatever the types
+    *bytes = 0;  // the most, whatever the types
+    for (uint32_t of_values = 4; of_values <= 8; of_values += 2)
+        for (const bool vec : {false, true}) {
+            const uint64_t need = norm_backward_bytes(norm_shape(hidden, rows, of_values, vec, true), hidden);
+            if (need > *bytes) *bytes = need;
+        }
     return ZCCL_OK;
 }
 

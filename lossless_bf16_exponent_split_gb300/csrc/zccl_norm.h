@@ -38,6 +38,8 @@ struct NormArgs {
     int joined;          // the kernel that adds them up follows
 };
 
+inline uint32_t size_of(int dtype) { return dtype == ZCCL_BF16 ? 2 : 4; }
+
 // Rows are shared out over workers, each a run of neighbouring rows.  In a backward
 // pass a worker keeps its sums of the weights' gradients over its rows, and of the
 // gate's over the rows of a gate row.  A gate row that lies within a worker's rows it
@@ -63,8 +65,16 @@ __host__ __device__ inline uint32_t worker_of(uint32_t rows, uint32_t workers, u
 // cluster's CTAs, or (kLong) read several times by a CTA.
 enum Team { kWarpTeam = 0, kCtaTeam = 1, kClusterTeam = 2, kLong = 3 };
 constexpr uint32_t kTeamWarps = 16;    // the most of a CTA
+constexpr uint32_t kMoreWarps = 20;    // of an SM, where 16 are not a whole number of teams
 constexpr uint32_t kMaxCluster = 4;    // CTAs
 constexpr uint32_t kWarpsPerCta = 8;   // of warps that are teams
+
+// Room for the sums of a team's warps, whose halves take turns, and a barrier of each
+// half: a warp may put its sums of the next row while another still takes up those of
+// this one; those of the row after it only when all have put the next row's, which they
+// do after they have taken up this one's.
+constexpr uint32_t kTeamRed = 2 * kTeamWarps * kMaxCluster * 8;
+constexpr uint32_t kTeamBytes = kTeamRed * 4 + 16;
 
 struct Shape {
     Team team;
@@ -76,14 +86,15 @@ struct Shape {
 };
 
 // The SMs are taken as 152, each with 16 warps (128 registers a thread); forward, where
-// rows begin on 16 bytes (vec) and a warp has one tile, 24 (80 registers).  `narrow`: both
-// types have 16 bits, and vec, so a warp can hold two tiles: two are better (a row costs a
-// warp about as much as two tiles do) from two tiles on, where they come out even.
-inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow, bool vec, bool backward)
+// rows begin on 16 bytes (vec) and a warp has one tile, 24 (80 registers).  `bytes`: of a
+// value of x and one of y.  Where both have two, and vec, a warp can hold two tiles: two are
+// better (a row costs a warp about as much as two tiles do) from two tiles on, where they
+// come out even.
+inline Shape norm_shape(uint64_t hidden, uint64_t rows, uint32_t bytes, bool vec, bool backward)
 {
     constexpr uint32_t kSms = 152;
     const uint32_t tiles = (uint32_t)((hidden + kTile - 1) / kTile);
-    const uint32_t pieces = narrow && (tiles % 2 == 0 || tiles > 8) ? 2 : 1, units = (tiles + pieces - 1) / pieces;
+    const uint32_t pieces = bytes == 4 && vec && (tiles % 2 == 0 || tiles > 8) ? 2 : 1, units = (tiles + pieces - 1) / pieces;
     // a cluster's CTA holds three rows in shared memory: 15 warps of two 16-bit tiles, or 16 of one tile
     const uint32_t alone = 16, most = pieces == 2 ? 15 : 16, sm_warps = !backward && vec && pieces == 1 ? 24 : 16;
     Shape s{};
@@ -93,14 +104,20 @@ inline Shape norm_shape(uint64_t hidden, uint64_t rows, bool narrow, bool vec, b
         s.grid = (s.workers + kWarpsPerCta - 1) / kWarpsPerCta;
     } else if (units <= most * kMaxCluster && tiles <= kTeamWarps * kMaxCluster) {
         s.ctas = units <= alone ? 1 : units <= 2 * most ? 2 : 4;
-        // 9 or 10 warps leave a third of an SM empty, three clusters' CTAs of 5 do not: 5120 columns forward 45.9 us,
-        // 51.4 with 10 warps; not so the gradients (64.8 and 63.0), with three rows in shared memory
+        // 9 or 10 warps leave a third of an SM empty, three clusters' CTAs of 5 do not: 5120 columns forward 48.7 us,
+        // 52.4 with 10 warps; not so the gradients (64.8 and 63.0), with three rows in shared memory
         if (!backward && (units == 9 || units == 10)) s.ctas = 2;
         s.team = s.ctas > 1 ? kClusterTeam : kCtaTeam;
         s.pieces = pieces;
         s.warps = (units + s.ctas - 1) / s.ctas;
         // clusters of four do not fill every group of SMs: 36 of 38 are taken
-        s.workers = at_most_rows((uint64_t)(s.ctas == 4 ? 144 : kSms) * (sm_warps / s.warps) / s.ctas);
+        uint32_t sm_ctas = sm_warps / s.warps;
+        // one team more, of warps with one tile, where 16 warps are not a whole number of them: 32-bit residual, BF16
+        // block, 2560 columns 45.0 us with 20 warps, 55.9 with 10; 1280 44.2 and 46.9.  All in 32 bits their rows would
+        // take the shared memory that L1 has: 1280 columns 65 us, 54.5; rows that begin anywhere gain from a second team only
+        // (2305 columns 61.9 and 64.9, 1300 62.7 and 59.1)
+        if (backward && pieces == 1 && s.ctas == 1 && bytes < 8 && sm_ctas * s.warps < 16 && (vec || sm_ctas == 1)) sm_ctas = kMoreWarps / s.warps;
+        s.workers = at_most_rows((uint64_t)(s.ctas == 4 ? 144 : kSms) * sm_ctas / s.ctas);
         s.grid = s.workers * s.ctas;
     } else {
         // its sums stay in the workspace: fewer workers for longer rows
@@ -201,13 +218,6 @@ __device__ __forceinline__ Place place()
     const uint32_t ctas = cluster_ctas();
     return {blockIdx.x / ctas, (cluster_rank() * warps + warp) * kPieces * kTile};
 }
-
-// Room for the sums of a team's warps, whose halves take turns, and a barrier of each
-// half: a warp may put its sums of the next row while another still takes up those of
-// this one; those of the row after it only when all have put the next row's, which they
-// do after they have taken up this one's.
-constexpr uint32_t kTeamRed = 2 * kTeamWarps * kMaxCluster * 8;
-constexpr uint32_t kTeamBytes = kTeamRed * 4 + 16;
 
 // Sums N values (N <= 8) over a team, the same way in every thread, in steps: a warp's
 // own sums (warp_sums), which it puts where all of the team find them, and, after a wait

@@ -13,7 +13,7 @@
 // workers' sums (r, dr, dh in, dx, dy out: 6.1 TB/s, 90 % of measured), 4096 x 14336 94 us
 // (6.2); with post, dropout and a gate 72 us (y read too: 5.6 TB/s), where it issues in two
 // of three slots: some 390 instructions a warp and tile of 256 columns.  Rows that do not
-// begin on 16 bytes: 8203 x 1001, 32-bit residual, 48 us (3.1 TB/s), bound by loads of
+// begin on 16 bytes: 8203 x 1001, 32-bit residual, 41.5 us (3.6 TB/s), bound by loads of
 // single values.
 #pragma once
 
@@ -162,7 +162,9 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(Nor
 // takes longer than a row's arithmetic, so a cluster sums the next row (kAhead) before it
 // waits for this one's sums.  kKind: as in the forward kernel.
 template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces, int kKind>
-__global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32 : kTeamWarps * 32, kTeam == kWarpTeam ? 2 : 1)
+__global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32
+                                  : kTeam == kCtaTeam && kPieces == 1 && sizeof(Tx) + sizeof(Ty) < 8 ? kMoreWarps * 32 : kTeamWarps * 32,
+                                  kTeam == kWarpTeam ? 2 : 1)
     norm_backward_kernel(NormArgs a)
 {
     extern __shared__ uint4 smem[];

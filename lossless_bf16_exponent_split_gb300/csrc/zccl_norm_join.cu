@@ -138,7 +138,7 @@ cudaError_t launch_join(const NormArgs& a, int weight_dtype, cudaStream_t stream
 
 zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weight_dtype, bool vec, cudaStream_t stream)
 {
-    const Shape s = norm_shape(a.hidden, a.rows, vec && x_dtype == ZCCL_BF16 && dtype == ZCCL_BF16, vec, true);
+    const Shape s = norm_shape(a.hidden, a.rows, size_of(x_dtype) + size_of(dtype), vec, true);
     a.workers = s.workers;
     a.groups = s.grid / s.ctas;
     a.parts = a.sums + (uint64_t)a.groups * kWeightSlots * ((a.hidden + 7) / 8 * 8);

@@ -62,6 +62,10 @@ CASES = [  # rows, hidden, residual, block, weight (None: no weights), post, gat
     (1830, 24, F, B, F, False, 610, 1.0, 0.0),    # a gate row for three tokens
     (2600, 512, B, B, F, True, 100, 1.0, 0.0),
     (700, 2048, B, B, F, True, 1, 1.0, 0.1),
+    (1300, 1280, F, B, F, True, 13, 1.0, 0.1),    # 20 warps an SM
+    (650, 2560, F, B, B, True, 65, 1.0, 0.0),
+    (640, 1536, B, F, F, False, 1, 1.0, 0.1),
+    (310, 2305, B, B, F, True, 2, 1.0, 0.0),
 ]
 
 
