@@ -166,6 +166,26 @@ def test_strided_rows_give_the_same(z, hidden):
     assert st == z.OK and torch.equal(place, r)
 
 
+@pytest.mark.parametrize("hidden,residual", [(200, F), (2048, B), (9000, B), (16384, F), (20000, B), (1003, F)])
+def test_in_place_and_one_gate_for_all(z, hidden, residual):
+    """The residual's place for the result, and a gate row that every token's row of a wider shape is."""
+    n, x, y, w, more, grad_r, grad_h = inputs(z, 12, hidden, residual, B, F, True, 1, 1.0, 0.2)
+    r, h = n.add(x, y, w, **more)
+    place, again = x.clone(), torch.empty_like(h)
+    st = z.zccl_residual_norm(n.config, place.data_ptr(), z.F32 if residual == F else z.BF16, hidden, y.data_ptr(), z.BF16,
+                              hidden, w.data_ptr(), more["post_weight"].data_ptr(), z.F32, more["gate"].data_ptr(), z.BF16,
+                              hidden, 12, 12, 0, None, place.data_ptr(), again.data_ptr(), None,
+                              torch.cuda.current_stream().cuda_stream)
+    assert st == z.OK and torch.equal(place, r) and torch.equal(again, h)
+    each = dict(more, gate=more["gate"].expand(12, hidden))
+    r2, h2 = n.add(x, y, w, **each)
+    assert torch.equal(r2, r) and torch.equal(h2, h)
+    one, all_of = (n.add_backward(grad_r, grad_h, r, y, w, **m) for m in (more, each))
+    assert all_of.gate.shape == (12, hidden) and torch.equal(one.x, all_of.x) and torch.equal(one.y, all_of.y)
+    at = ref.Ref(x=x, y=y, weight=w, post=True, eps=1e-5, dropout=0.2, seed=0xFEDCBA9876543210, **each)
+    close(all_of.gate, *at.backward(grad_r, grad_h, r)["gate"], "gate")
+
+
 def test_nothing_is_written_outside(z):
     """Guards around every output of the calls, at sizes that end inside a tile."""
     for rows, hidden in ((3, 9), (5, 264), (4, 1001), (3, 8200)):
