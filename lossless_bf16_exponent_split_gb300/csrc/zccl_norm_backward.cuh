@@ -367,7 +367,7 @@ NormKernel backward_kind(bool post, bool drop, uint32_t* warp_bytes)
 template <typename Tx, typename Ty, bool kVec>
 NormKernel backward_for(const Shape& s, bool post, bool drop, uint32_t* warp_bytes)
 {
-    constexpr int kMost = kVec && sizeof(Tx) == 2 && sizeof(Ty) == 2 ? 2 : 1;
+    constexpr int kMost = sizeof(Tx) == 2 && sizeof(Ty) == 2 ? 2 : 1;
     if (s.team == kWarpTeam) return backward_kind<Tx, Ty, kVec, kWarpTeam, 1>(post, drop, warp_bytes);
     if (s.team == kLong) return norm_backward_long_kernel<Tx, Ty, kVec>;
     if (s.team == kCtaTeam)

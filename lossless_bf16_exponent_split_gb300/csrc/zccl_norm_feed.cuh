@@ -123,14 +123,14 @@ __device__ __forceinline__ void copy_4(uint32_t to, const char* from, uint32_t b
 {
     asm volatile("cp.async.ca.shared.global [%0+%3], [%1+%4], 4, %2;" ::"r"(to), "l"(from), "r"(bytes), "n"(kTo), "n"(kFrom) : "memory");
 }
-template <typename Tx, typename Ty, int kStages, bool kBackward>
-struct Feed<Tx, Ty, false, 1, kStages, kBackward> {
-    static constexpr int kX = kLooseBytes<Tx>, kY = kLooseBytes<Ty>, kStage = (kX + kY) * (kBackward ? 2 : 1);
+template <typename Tx, typename Ty, int kPieces, int kStages, bool kBackward>
+struct Feed<Tx, Ty, false, kPieces, kStages, kBackward> {
+    static constexpr int kX = kLooseBytes<Tx>, kY = kLooseBytes<Ty>, kAll = (kX + kY) * (kBackward ? 2 : 1), kStage = kAll * kPieces;
     static constexpr uint32_t kWarpBytes = kStages * kStage;
     const char* const mine;  // the warp's stages
     uint32_t asked = 0;      // the stage that the next row goes to
     uint32_t shifts = 0;     // of each stage four bits: whether x, y, x1, y1 begin in the middle of a word
-    const char *x, *y, *x1, *y1;  // the tile of the row that is asked for next
+    const char *x, *y, *x1, *y1;  // the first tile of the row that is asked for next
     const uint32_t left;          // columns of the row from the tile on
     __device__ __forceinline__ Feed(uint4* warp_smem, const NormArgs& a, const Place& place, uint32_t t)
         : mine(reinterpret_cast<const char*>(warp_smem)), left(place.tile(0) < a.hidden ? a.hidden - place.tile(0) : 0)
@@ -150,9 +150,22 @@ struct Feed<Tx, Ty, false, 1, kStages, kBackward> {
     template <typename T, int kPart, int kBit>
     __device__ __forceinline__ void copy(const char*& from, uint64_t stride)
     {
-        const uint32_t lane = threadIdx.x & 31, to = smem_addr(mine) + asked * kStage + kPart + lane * 4;
+        const uint32_t lane = threadIdx.x & 31, shift = sizeof(T) == 4 ? 0 : (uint32_t)(reinterpret_cast<uint64_t>(from) >> 1) & 1u;
+        const uint32_t to = smem_addr(mine) + asked * kStage + kPart + lane * 4;
+        const char* p = from - 2 * shift + lane * 4;  // (the first word's other half is not looked at)
+        copy_piece<T>(to, p, shift, left);
+        if constexpr (kPieces == 2) copy_piece<T>(to + kAll, p + kTile * sizeof(T), shift, left > kTile ? left - kTile : 0);
+        if (sizeof(T) == 2) {
+            const uint32_t at = 4 * asked + kBit;
+            shifts = (shifts & ~(1u << at)) | shift << at;
+        }
+        from += stride * sizeof(T);
+    }
+    template <typename T>
+    static __device__ __forceinline__ void copy_piece(uint32_t to, const char* p, uint32_t shift, uint32_t left)
+    {
+        const uint32_t lane = threadIdx.x & 31;
         if constexpr (sizeof(T) == 4) {
-            const char* p = from + lane * 4;
             const auto all = [&](auto size) {
                 copy_4<0, 0>(to, p, size(0)), copy_4<128, 128>(to, p, size(1)), copy_4<256, 256>(to, p, size(2));
                 copy_4<384, 384>(to, p, size(3)), copy_4<512, 512>(to, p, size(4)), copy_4<640, 640>(to, p, size(5));
@@ -163,8 +176,6 @@ struct Feed<Tx, Ty, false, 1, kStages, kBackward> {
             else
                 all([&](uint32_t j) { return j * 32 + lane < left ? 4u : 0u; });
         } else {
-            const uint32_t shift = (uint32_t)(reinterpret_cast<uint64_t>(from) >> 1) & 1u;
-            const char* p = from - 2 * shift + lane * 4;  // (the first word's other half is not looked at)
             const auto all = [&](auto size) {
                 copy_4<0, 0>(to, p, size(lane)), copy_4<128, 128>(to, p, size(32 + lane));
                 copy_4<256, 256>(to, p, size(64 + lane)), copy_4<384, 384>(to, p, size(96 + lane));
@@ -176,10 +187,7 @@ struct Feed<Tx, Ty, false, 1, kStages, kBackward> {
                 const uint32_t halves = left > 0 ? shift + left : 0;  // those of the words that are wanted
                 all([&](uint32_t word) { return 2 * word + 1 < halves ? 4u : 2 * word < halves ? 2u : 0u; });
             }
-            const uint32_t at = 4 * asked + kBit;
-            shifts = (shifts & ~(1u << at)) | shift << at;
         }
-        from += stride * sizeof(T);
     }
     // Asks for the next row (there: it is one of the worker's).
     __device__ __forceinline__ void ask(const NormArgs& a, const Place&, bool there)
@@ -212,25 +220,25 @@ struct Feed<Tx, Ty, false, 1, kStages, kBackward> {
         const char* at;
         uint32_t shifts;
         template <typename T>
-        __device__ __forceinline__ Eight read(int part, int bit) const
+        __device__ __forceinline__ Eight read(int n, int part, int bit) const
         {
             const uint32_t lane = threadIdx.x & 31;
             Eight v;
             if (sizeof(T) == 4) {
-                const float* p = reinterpret_cast<const float*>(at + part) + lane;
+                const float* p = reinterpret_cast<const float*>(at + n * kAll + part) + lane;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = p[32 * j];
             } else {
-                const uint16_t* p = reinterpret_cast<const uint16_t*>(at + part) + lane + ((shifts >> bit) & 1u);
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(at + n * kAll + part) + lane + ((shifts >> bit) & 1u);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = __uint_as_float((uint32_t)p[32 * j] << 16);
             }
             return v;
         }
-        __device__ __forceinline__ Eight x(int) const { return read<Tx>(0, 0); }
-        __device__ __forceinline__ Eight y(int) const { return read<Ty>(kX, 1); }
-        __device__ __forceinline__ Eight x1(int) const { return read<Tx>(kX + kY, 2); }
-        __device__ __forceinline__ Eight y1(int) const { return read<Ty>(2 * kX + kY, 3); }
+        __device__ __forceinline__ Eight x(int n) const { return read<Tx>(n, 0, 0); }
+        __device__ __forceinline__ Eight y(int n) const { return read<Ty>(n, kX, 1); }
+        __device__ __forceinline__ Eight x1(int n) const { return read<Tx>(n, kX + kY, 2); }
+        __device__ __forceinline__ Eight y1(int n) const { return read<Ty>(n, 2 * kX + kY, 3); }
     };
     // The row that was asked for before the last `later` ones.
     __device__ __forceinline__ Row row(uint32_t later) const
