@@ -64,16 +64,17 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_long_kernel(NormArgs a)
 // A team a worker: a row is read once and stays in registers, with others on their way;
 // weights and the gate stay there too.  kKind: which of post (1) and dropout (2) the
 // call has.
-// Two rows more on their way in shared memory; with two tiles a warp one in registers is
-// as good (2048 columns in BF16 47.4 us, 48.3; in 32 bits with a BF16 block 45.9, 34.6).
-template <int kPieces>
-constexpr int forward_stages = kPieces == 1 ? 3 : 0;
+// Two rows more on their way in shared memory; with two tiles a warp, of rows on 16 bytes,
+// one in registers is as good (2048 columns in BF16 47.4 us, 48.3; in 32 bits with a BF16
+// block 45.9, 34.6).
+template <bool kVec, int kPieces>
+constexpr int forward_stages = kPieces == 1 || !kVec ? 3 : 0;
 template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces, int kKind>
-__global__ void __launch_bounds__(kVec && kPieces == 1 ? 768 : kTeamWarps * 32) norm_kernel(NormArgs a)
+__global__ void __launch_bounds__(kPieces == 1 ? 768 : kTeamWarps * 32) norm_kernel(NormArgs a)
 {
     extern __shared__ uint4 smem[];
     __shared__ __align__(16) char red[kTeam == kWarpTeam ? 16 : kTeamBytes];
-    using Rows = Feed<Tx, Ty, kVec, kPieces, forward_stages<kPieces>, false>;
+    using Rows = Feed<Tx, Ty, kVec, kPieces, forward_stages<kVec, kPieces>, false>;
     TeamSum<1, kTeam> team_sum(red, a.status);
     pdl_wait();
     const Place at = place<kTeam, kPieces>();
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(kVec && kPieces == 1 ? 768 : kTeamWarps * 32) 
     Tx* r_at = static_cast<Tx*>(a.r) + (join ? (uint64_t)lo * a.hidden : 0);
     Ty* h_at = static_cast<Ty*>(a.h) + (normed ? (uint64_t)lo * a.hidden : 0);
     Rows rows(smem + (threadIdx.x >> 5) * (Rows::kWarpBytes / 16), a, at, lo);
-    constexpr int kLater = forward_stages<kPieces> == 3 ? 1 : 0;  // rows behind the one that is waited for
+    constexpr int kLater = forward_stages<kVec, kPieces> == 3 ? 1 : 0;  // rows behind the one that is waited for
 #pragma unroll
     for (int i = 0; i <= kLater; ++i) rows.ask(a, at, lo + i < hi);
     Eight w[kPieces], k[kPieces];
@@ -146,14 +147,14 @@ __global__ void __launch_bounds__(kVec && kPieces == 1 ? 768 : kTeamWarps * 32) 
 template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces>
 NormKernel norm_kind(bool post, bool drop, uint32_t* warp_bytes)
 {
-    *warp_bytes = Feed<Tx, Ty, kVec, kPieces, forward_stages<kPieces>, false>::kWarpBytes;
+    *warp_bytes = Feed<Tx, Ty, kVec, kPieces, forward_stages<kVec, kPieces>, false>::kWarpBytes;
     return post ? (drop ? norm_kernel<Tx, Ty, kVec, kTeam, kPieces, 3> : norm_kernel<Tx, Ty, kVec, kTeam, kPieces, 1>)
                 : (drop ? norm_kernel<Tx, Ty, kVec, kTeam, kPieces, 2> : norm_kernel<Tx, Ty, kVec, kTeam, kPieces, 0>);
 }
 template <typename Tx, typename Ty, bool kVec>
 NormKernel norm_for(const Shape& s, bool post, bool drop, uint32_t* warp_bytes)
 {
-    constexpr int kMost = kVec && sizeof(Tx) == 2 && sizeof(Ty) == 2 ? 2 : 1;
+    constexpr int kMost = sizeof(Tx) == 2 && sizeof(Ty) == 2 ? 2 : 1;
     if (s.team == kWarpTeam) return norm_kind<Tx, Ty, kVec, kWarpTeam, 1>(post, drop, warp_bytes);
     if (s.team == kLong) return norm_long_kernel<Tx, Ty, kVec>;
     if (s.team == kCtaTeam)

@@ -68,6 +68,7 @@ CASES = [  # rows, hidden, residual, block, weight (None: no weights), post, gat
     (310, 2305, B, B, F, True, 2, 1.0, 0.0),
     (400, 4095, B, B, B, True, 40, 1.0, 0.1),     # rows anywhere, two tiles a warp
     (340, 1803, B, B, F, False, 1, 0.5, 0.1),
+    (1300, 1001, B, B, F, True, 13, 1.0, 0.1),
     (130, 10001, B, B, F, True, 13, 1.0, 0.0),    # in clusters of two
     (20, 16383, B, B, F, True, 1, 1.0, 0.1),
 ]
