@@ -62,8 +62,13 @@ __host__ __device__ inline uint32_t worker_of(uint32_t rows, uint32_t workers, u
 }
 
 // How a row is held: by a warp (a tile at most), by the warps of a CTA, by those of a
-// cluster's CTAs, or (kLong) read several times by a CTA.
-enum Team { kWarpTeam = 0, kCtaTeam = 1, kClusterTeam = 2, kLong = 3 };
+// cluster's CTAs, or (kLong) read several times by a CTA; by half a warp or a quarter
+// (rows on 16 bytes of up to 128 and 64 values), whose rows a warp goes through at once.
+enum Team { kWarpTeam = 0, kCtaTeam = 1, kClusterTeam = 2, kLong = 3, kHalfTeam = 4, kQuarterTeam = 5 };
+template <int kTeam>
+constexpr uint32_t team_lanes = kTeam == kHalfTeam ? 16 : kTeam == kQuarterTeam ? 8 : 32;  // of a warp
+template <int kTeam>
+constexpr bool in_warp = kTeam == kWarpTeam || team_lanes<kTeam> < 32;
 constexpr uint32_t kTeamWarps = 16;    // the most of a CTA
 constexpr uint32_t kMoreWarps = 20;    // of an SM, where 16 are not a whole number of teams
 constexpr uint32_t kMaxCluster = 4;    // CTAs
@@ -103,8 +108,9 @@ inline Shape norm_shape(uint64_t hidden, uint64_t rows, uint32_t bytes, bool vec
     Shape s{};
     const auto at_most_rows = [&](uint64_t n) { return (uint32_t)(n < rows ? n : rows > 0 ? rows : 1); };
     if (tiles <= 1) {
-        s = {kWarpTeam, 1, kWarpsPerCta, 1, at_most_rows(kSms * sm_warps), 0};
-        s.grid = (s.workers + kWarpsPerCta - 1) / kWarpsPerCta;
+        const uint32_t of_warp = !vec || hidden > 128 ? 1 : hidden > 64 ? 2 : 4;  // teams
+        s = {of_warp == 4 ? kQuarterTeam : of_warp == 2 ? kHalfTeam : kWarpTeam, 1, kWarpsPerCta, 1, at_most_rows(kSms * sm_warps * of_warp), 0};
+        s.grid = (s.workers + kWarpsPerCta * of_warp - 1) / (kWarpsPerCta * of_warp);
     } else if (units <= most * kMaxCluster && tiles <= kTeamWarps * kMaxCluster) {
         s.ctas = units <= alone ? 1 : units <= 2 * most ? 2 : 4;
         // 9 or 10 warps leave a third of an SM empty, three clusters' CTAs of 5 do not: 5120 columns forward 48.7 us,
@@ -134,10 +140,10 @@ inline Shape norm_shape(uint64_t hidden, uint64_t rows, uint32_t bytes, bool vec
 template <int N>
 constexpr int kValues = N <= 1 ? 1 : N <= 2 ? 2 : N <= 4 ? 4 : 8;
 
-// Sums N values (N <= 8) over a warp: while a lane holds several it keeps half of them in
-// a step, so that nine exchanges do for all eight.  Lanes 32 / kValues * i and up hold
-// value i then.
-template <int N>
+// Sums N values (N <= 8) over each L lanes: while a lane holds several it keeps half of them
+// in a step, so that nine exchanges do for all eight of a warp.  Lanes L / kValues * i and
+// up hold value i then.
+template <int N, int L>
 __device__ __forceinline__ float warp_sums(const float (&s)[N])
 {
     constexpr int H = kValues<N>;
@@ -145,7 +151,7 @@ __device__ __forceinline__ float warp_sums(const float (&s)[N])
     float v[H];
 #pragma unroll
     for (int i = 0; i < H; ++i) v[i] = i < N ? s[i] : 0.0f;
-    int o = 16;
+    int o = L / 2;
 #pragma unroll
     for (int h = H / 2; h > 0; h /= 2, o /= 2) {
         const bool upper = (lane & o) != 0;
@@ -156,7 +162,7 @@ __device__ __forceinline__ float warp_sums(const float (&s)[N])
         }
     }
 #pragma unroll
-    for (int x = 32 / H / 2; x > 0; x /= 2) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], x);
+    for (int x = L / H / 2; x > 0; x /= 2) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], x);
     return v[0];
 }
 
@@ -207,7 +213,8 @@ __device__ __forceinline__ bool wait_sent(uint64_t* bar, uint32_t parity)
     }
 }
 
-// A warp's worker, and its neighbouring tiles of a row.
+// A warp's worker, and its neighbouring tiles of a row.  Of teams that share a warp, each
+// lane's: tiles then begin (modulo 2^32) where the team's first lane has column 0.
 struct Place {
     uint32_t worker, first;
     __device__ __forceinline__ uint32_t tile(int n) const { return first + n * kTile; }
@@ -216,10 +223,21 @@ template <int kTeam, int kPieces>
 __device__ __forceinline__ Place place()
 {
     const uint32_t warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    if (kTeam == kWarpTeam) return {blockIdx.x * kWarpsPerCta + warp, 0};
+    if (in_warp<kTeam>) {
+        const uint32_t team = (threadIdx.x & 31) / team_lanes<kTeam>;
+        return {(blockIdx.x * kWarpsPerCta + warp) * (32 / team_lanes<kTeam>) + team, 0u - team * team_lanes<kTeam> * 8};
+    }
     if (kTeam == kCtaTeam) return {blockIdx.x, warp * kPieces * kTile};
     const uint32_t ctas = cluster_ctas();
     return {blockIdx.x / ctas, (cluster_rank() * warps + warp) * kPieces * kTile};
+}
+
+// Where a warp's rows lo..hi-1 end: of teams that share it, where those of the one with most
+// would.
+template <int kTeam>
+__device__ __forceinline__ uint32_t last_step(uint32_t lo, uint32_t hi)
+{
+    return team_lanes<kTeam> == 32 ? hi : lo + __reduce_max_sync(0xFFFFFFFFu, hi - lo);
 }
 
 // Sums N values (N <= 8) over a team, the same way in every thread, in steps: a warp's
@@ -229,13 +247,13 @@ __device__ __forceinline__ Place place()
 // store to global memory.
 template <int N, int kTeam>
 struct TeamSum {
-    static constexpr int H = kValues<N>, kLanes = 32 / H;
+    static constexpr int H = kValues<N>, kLanes = team_lanes<kTeam> / H;
     static constexpr int kRounds = ((int)kTeamWarps * (kTeam == kClusterTeam ? (int)kMaxCluster : 1) * H + 31) / 32;
     float* const red;
     uint64_t* const bar;
     uint32_t* const status;
     uint32_t turn = 0, parity = 0;
-    float mine = 0.0f;   // a warp that is a team
+    float mine = 0.0f;   // of a team within a warp
     bool lost = false;   // a wait ran out: no other is begun, and all sums are NaN
     const uint32_t all;  // values of the team's warps
     __device__ __forceinline__ TeamSum(void* smem, uint32_t* status)
@@ -261,7 +279,7 @@ struct TeamSum {
     {
         const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         float* at = red + turn * (kTeamRed / 2) + lane / kLanes;
-        if (kTeam == kWarpTeam) mine = v;
+        if (in_warp<kTeam>) mine = v;
         if (kTeam == kCtaTeam && lane % kLanes == 0) at[warp * H] = v;
         if (kTeam == kClusterTeam) {
             if (threadIdx.x == 0) mbar_arrive_expect_tx(bar + turn, all * 4);
@@ -283,7 +301,7 @@ struct TeamSum {
     {
         const uint32_t lane = threadIdx.x & 31;
         float v = mine;
-        if (kTeam != kWarpTeam) {
+        if (!in_warp<kTeam>) {
             const float* at = red + (turn ^ 1) * (kTeamRed / 2) + lane;
             v = 0.0f;
 #pragma unroll
@@ -297,11 +315,11 @@ struct TeamSum {
             for (int o = 16; o >= H; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
         }
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = N == 1 ? v : __shfl_sync(0xFFFFFFFFu, v, kTeam == kWarpTeam ? i * kLanes : i);
+        for (int i = 0; i < N; ++i) s[i] = N == 1 ? v : __shfl_sync(0xFFFFFFFFu, v, in_warp<kTeam> ? i * kLanes : i, team_lanes<kTeam>);
     }
     __device__ __forceinline__ void operator()(float (&s)[N])
     {
-        put(warp_sums<N>(s));
+        put(warp_sums<N, team_lanes<kTeam>>(s));
         wait();
         take(s);
     }

@@ -162,9 +162,9 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(Nor
 // takes longer than a row's arithmetic, so a cluster sums the next row (kAhead) before it
 // waits for this one's sums.  kKind: as in the forward kernel.
 template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces, int kKind>
-__global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32
+__global__ void __launch_bounds__(in_warp<kTeam> ? kWarpsPerCta * 32
                                   : kTeam == kCtaTeam && kPieces == 1 && sizeof(Tx) + sizeof(Ty) < 8 ? kMoreWarps * 32 : kTeamWarps * 32,
-                                  kTeam == kWarpTeam ? 2 : 1)
+                                  in_warp<kTeam> ? 2 : 1)
     norm_backward_kernel(NormArgs a)
 {
     extern __shared__ uint4 smem[];
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32
         float s[kTeamSums];
 #pragma unroll
         for (int i = 0; i < kTeamSums; ++i) s[i] = sum[i].x + sum[i].y;
-        return warp_sums<kTeamSums>(s);
+        return warp_sums<kTeamSums, team_lanes<kTeam>>(s);
     };
     const auto factors = [&]() -> RowFactors {
         float s[kSums] = {}, got[kTeamSums];
@@ -315,8 +315,9 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32
         }
     } else {
         if (join && lo < hi) set_gate(lo);
+        const uint32_t end = last_step<kTeam>(lo, hi);
 #pragma unroll 1
-        for (uint32_t t = lo; t < hi; ++t) {
+        for (uint32_t t = lo; t < end; ++t) {
             rows.template wait<0>();
             const bool turns = join && t + 1 == gate_end && t + 1 < hi;
             const auto row = rows.row(0);
@@ -327,7 +328,8 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32
             for (int n = 0; n < kPieces; ++n) kept[n] = kept_of(t, n);
             team_sum.put(sums_of(row, kept));
             team_sum.wait();
-            gradients(row, t, factors(), kept);
+            const RowFactors f = factors();
+            if (team_lanes<kTeam> == 32 || t < hi) gradients(row, t, f, kept);
             if (turns) set_gate(t + 1);
         }
     }
@@ -335,22 +337,26 @@ __global__ void __launch_bounds__(kTeam == kWarpTeam ? kWarpsPerCta * 32
     if (reads_y && lo < hi) take_out(hi);
     if (a.joined) pdl_launch_dependents();
     // the weights' sums, of a CTA's warps where each is a team
-    float* const sums = a.sums + (uint64_t)(kTeam == kWarpTeam ? blockIdx.x : at.worker) * kWeightSlots * pitch;
+    float* const sums = a.sums + (uint64_t)(in_warp<kTeam> ? blockIdx.x : at.worker) * kWeightSlots * pitch;
     const auto put_sums = [&](int slot) {
-        if (kTeam == kWarpTeam) __syncthreads();
-        if (kTeam == kWarpTeam && threadIdx.x >= 32) return;
+        if (in_warp<kTeam>) __syncthreads();
+        if (in_warp<kTeam> && threadIdx.x >= 32) return;
 #pragma unroll
         for (int n = 0; n < kPieces; ++n) {
             Eight v = get_dp(n, 0);
-            if (kTeam == kWarpTeam)
+            if (in_warp<kTeam>)
 #pragma unroll 1
                 for (uint32_t i = 1; i < kWarpsPerCta; ++i) v = fma(get_dp(n, i), 1.0f, v);
-            store8<float, kVec>(sums + slot * pitch, v, at.tile(n), a.hidden);
+#pragma unroll
+            for (uint32_t o = 16; o >= team_lanes<kTeam>; o /= 2)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += __shfl_xor_sync(0xFFFFFFFFu, v[j], o);
+            if (team_lanes<kTeam> == 32 || threadIdx.x < team_lanes<kTeam>) store8<float, kVec>(sums + slot * pitch, v, at.tile(n), a.hidden);
         }
     };
     if (a.grad_post_weight != nullptr) put_sums(kSlotPost);
     if (a.grad_weight != nullptr) {
-        if (kTeam == kWarpTeam) __syncthreads();
+        if (in_warp<kTeam>) __syncthreads();
 #pragma unroll
         for (int n = 0; n < kPieces; ++n) put_dp(n, dw[n]);
         put_sums(kSlotWeight);
@@ -369,6 +375,10 @@ NormKernel backward_for(const Shape& s, bool post, bool drop, uint32_t* warp_byt
 {
     constexpr int kMost = sizeof(Tx) == 2 && sizeof(Ty) == 2 ? 2 : 1;
     if (s.team == kWarpTeam) return backward_kind<Tx, Ty, kVec, kWarpTeam, 1>(post, drop, warp_bytes);
+    if constexpr (kVec) {
+        if (s.team == kHalfTeam) return backward_kind<Tx, Ty, kVec, kHalfTeam, 1>(post, drop, warp_bytes);
+        if (s.team == kQuarterTeam) return backward_kind<Tx, Ty, kVec, kQuarterTeam, 1>(post, drop, warp_bytes);
+    }
     if (s.team == kLong) return norm_backward_long_kernel<Tx, Ty, kVec>;
     if (s.team == kCtaTeam)
         return s.pieces == 1 ? backward_kind<Tx, Ty, kVec, kCtaTeam, 1>(post, drop, warp_bytes)

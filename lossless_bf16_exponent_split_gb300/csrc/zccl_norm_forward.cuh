@@ -73,16 +73,17 @@ template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces, int kKind
 __global__ void __launch_bounds__(kPieces == 1 ? 768 : kTeamWarps * 32) norm_kernel(NormArgs a)
 {
     extern __shared__ uint4 smem[];
-    __shared__ __align__(16) char red[kTeam == kWarpTeam ? 16 : kTeamBytes];
+    __shared__ __align__(16) char red[in_warp<kTeam> ? 16 : kTeamBytes];
     using Rows = Feed<Tx, Ty, kVec, kPieces, forward_stages<kVec, kPieces>, false>;
     TeamSum<1, kTeam> team_sum(red, a.status);
     pdl_wait();
     const Place at = place<kTeam, kPieces>();
-    if (kTeam == kWarpTeam && at.worker >= a.workers) return;
     const bool join = a.y != nullptr, normed = a.h != nullptr;
     constexpr bool post = (kKind & 1) != 0, drop = (kKind & 2) != 0;
     const uint64_t offset = drop ? drop_offset(a.drop) : 0;
-    const uint32_t lo = first_row(a.rows, a.workers, at.worker), hi = first_row(a.rows, a.workers, at.worker + 1);
+    const uint32_t lo = at.worker < a.workers ? first_row(a.rows, a.workers, at.worker) : 0;
+    const uint32_t hi = at.worker < a.workers ? first_row(a.rows, a.workers, at.worker + 1) : 0;
+    const uint32_t end = last_step<kTeam>(lo, hi);
     Tx* r_at = static_cast<Tx*>(a.r) + (join ? (uint64_t)lo * a.hidden : 0);
     Ty* h_at = static_cast<Ty*>(a.h) + (normed ? (uint64_t)lo * a.hidden : 0);
     Rows rows(smem + (threadIdx.x >> 5) * (Rows::kWarpBytes / 16), a, at, lo);
@@ -93,7 +94,8 @@ __global__ void __launch_bounds__(kPieces == 1 ? 768 : kTeamWarps * 32) norm_ker
 #pragma unroll
     for (int n = 0; n < kPieces; ++n) w[n] = load_vector<kVec>(a.weight, 0, at.tile(n), a.hidden);
     uint32_t gate_end = lo;  // where the gate changes
-    for (uint32_t t = lo; t < hi; ++t) {
+    for (uint32_t t = lo; t < end; ++t) {
+        const bool live = team_lanes<kTeam> == 32 || t < hi;
         rows.template wait<kLater>();
         const auto row = rows.row(kLater);
         Eight x[kPieces], y[kPieces];
@@ -101,7 +103,7 @@ __global__ void __launch_bounds__(kPieces == 1 ? 768 : kTeamWarps * 32) norm_ker
         for (int n = 0; n < kPieces; ++n) x[n] = row.x(n), y[n] = row.y(n);
         rows.ask(a, at, t + kLater + 1 < hi);
         if (join) {
-            if (t == gate_end) {
+            if (t == gate_end && live) {
                 // the join's factor of each column, with the weight of the norm after the block
 #pragma unroll
                 for (int n = 0; n < kPieces; ++n)
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(kPieces == 1 ? 768 : kTeamWarps * 32) norm_ker
                 // the product rounded by itself: without post r then has the bits of the formula's operations in their order
                 const Eight r = mul_then_add(k[n], y[n], x[n]);
                 x[n] = drop ? where_kept<kVec>(kept_piece<kVec>(a.drop, offset, t, at.tile(n)), r, x[n]) : r;
-                x[n] = store8<Tx, kVec>(r_at, x[n], at.tile(n), a.hidden);
+                if (live) x[n] = store8<Tx, kVec>(r_at, x[n], at.tile(n), a.hidden);
             }
             r_at += a.hidden;
         }
@@ -138,7 +140,8 @@ __global__ void __launch_bounds__(kPieces == 1 ? 768 : kTeamWarps * 32) norm_ker
         team_sum(s);
         const float rho = rsqrtf(s[0] * a.inv_hidden + a.eps);
 #pragma unroll
-        for (int n = 0; n < kPieces; ++n) store8<Ty, kVec>(h_at, mul(mul(x[n], rho), w[n]), at.tile(n), a.hidden);
+        for (int n = 0; n < kPieces; ++n)
+            if (live) store8<Ty, kVec>(h_at, mul(mul(x[n], rho), w[n]), at.tile(n), a.hidden);
         h_at += a.hidden;
     }
     team_sum.close();
@@ -156,6 +159,10 @@ NormKernel norm_for(const Shape& s, bool post, bool drop, uint32_t* warp_bytes)
 {
     constexpr int kMost = sizeof(Tx) == 2 && sizeof(Ty) == 2 ? 2 : 1;
     if (s.team == kWarpTeam) return norm_kind<Tx, Ty, kVec, kWarpTeam, 1>(post, drop, warp_bytes);
+    if constexpr (kVec) {
+        if (s.team == kHalfTeam) return norm_kind<Tx, Ty, kVec, kHalfTeam, 1>(post, drop, warp_bytes);
+        if (s.team == kQuarterTeam) return norm_kind<Tx, Ty, kVec, kQuarterTeam, 1>(post, drop, warp_bytes);
+    }
     if (s.team == kLong) return norm_long_kernel<Tx, Ty, kVec>;
     if (s.team == kCtaTeam)
         return s.pieces == 1 ? norm_kind<Tx, Ty, kVec, kCtaTeam, 1>(post, drop, warp_bytes) : norm_kind<Tx, Ty, kVec, kCtaTeam, kMost>(post, drop, warp_bytes);

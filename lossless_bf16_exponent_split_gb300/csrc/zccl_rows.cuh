@@ -284,7 +284,7 @@ __device__ __forceinline__ Kept<kVec> kept_piece(const DropArgs& d, uint64_t off
 template <>
 __device__ __forceinline__ Kept<true> kept_piece<true>(const DropArgs& d, uint64_t offset, uint32_t row, uint32_t tile)
 {
-    return kept_block(d, offset, row, tile / 8 + (threadIdx.x & 31));
+    return kept_block(d, offset, row, column<true>(tile, 0) / 8);
 }
 template <>
 __device__ __forceinline__ Kept<false> kept_piece<false>(const DropArgs& d, uint64_t offset, uint32_t row, uint32_t tile)

@@ -71,6 +71,12 @@ CASES = [  # rows, hidden, residual, block, weight (None: no weights), post, gat
     (1300, 1001, B, B, F, True, 13, 1.0, 0.1),
     (130, 10001, B, B, F, True, 13, 1.0, 0.0),    # in clusters of two
     (20, 16383, B, B, F, True, 1, 1.0, 0.1),
+    (10000, 128, B, B, F, True, 50, 1.0, 0.1),    # two rows a warp
+    (11001, 64, B, B, B, True, 57, 0.5, 0.0),     # four
+    (777, 120, F, F, F, False, 777, 1.0, 0.1),
+    (20011, 8, F, B, F, True, 1, 1.0, 0.1),
+    (10100, 56, B, F, F, True, 5050, 1.0, 0.2),
+    (5, 72, B, B, B, True, 5, 1.0, 0.0),
 ]
 
 
