@@ -161,6 +161,14 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(Nor
 // so one sum serves both, and is taken out when the gate changes.  A cluster's exchange
 // takes longer than a row's arithmetic, so a cluster sums the next row (kAhead) before it
 // waits for this one's sums.  kKind: as in the forward kernel.
+// Rows in shared memory, where both types have 16 bits: 128 columns without a join 36 us with
+// four, 48 with two.  A wider residual's would take what L1 has (with the join 92, 87).
+template <typename Tx, typename Ty, int kTeam, int kPieces>
+constexpr int backward_stages = kTeam == kClusterTeam                ? 3
+                                : sizeof(Tx) + sizeof(Ty) > 4 ? 2
+                                : in_warp<kTeam>                     ? 4
+                                : kPieces == 1                       ? 3
+                                                                     : 2;
 template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces, int kKind>
 __global__ void __launch_bounds__(in_warp<kTeam> ? kWarpsPerCta * 32
                                   : kTeam == kCtaTeam && kPieces == 1 && sizeof(Tx) + sizeof(Ty) < 8 ? kMoreWarps * 32 : kTeamWarps * 32,
@@ -170,7 +178,8 @@ __global__ void __launch_bounds__(in_warp<kTeam> ? kWarpsPerCta * 32
     extern __shared__ uint4 smem[];
     constexpr bool kAhead = kTeam == kClusterTeam;
     constexpr int kTeamSums = kKind & 1 ? kSums : 2;
-    using Rows = Feed<Tx, Ty, kVec, kPieces, kAhead ? 3 : 2, true>;
+    constexpr int kStages = backward_stages<Tx, Ty, kTeam, kPieces>;
+    using Rows = Feed<Tx, Ty, kVec, kPieces, kStages, true>;
     // of each warp: its rows, and its sums of p's gradient (two 16-byte parts a piece); then the teams' sums
     constexpr uint32_t kWarpParts = Rows::kWarpBytes / 16 + 2 * kPieces * 32;
     uint4* const warp_smem = smem + (threadIdx.x >> 5) * kWarpParts;
@@ -314,14 +323,17 @@ __global__ void __launch_bounds__(in_warp<kTeam> ? kWarpsPerCta * 32
             for (int n = 0; n < kPieces; ++n) kept[n] = after[n];
         }
     } else {
+        constexpr int kLater = kStages - 2;  // rows behind the one that is waited for
+#pragma unroll
+        for (int i = 1; i <= kLater; ++i) rows.ask(a, at, lo + i < hi);
         if (join && lo < hi) set_gate(lo);
         const uint32_t end = last_step<kTeam>(lo, hi);
 #pragma unroll 1
         for (uint32_t t = lo; t < end; ++t) {
-            rows.template wait<0>();
+            rows.template wait<kLater>();
             const bool turns = join && t + 1 == gate_end && t + 1 < hi;
-            const auto row = rows.row(0);
-            rows.ask(a, at, t + 1 < hi);
+            const auto row = rows.row(kLater);
+            rows.ask(a, at, t + 1 + kLater < hi);
             if (turns) prefetch_gates(t + 1);
             Kept<kVec> kept[kPieces];
 #pragma unroll
@@ -366,7 +378,7 @@ __global__ void __launch_bounds__(in_warp<kTeam> ? kWarpsPerCta * 32
 template <typename Tx, typename Ty, bool kVec, int kTeam, int kPieces>
 NormKernel backward_kind(bool post, bool drop, uint32_t* warp_bytes)
 {
-    *warp_bytes = Feed<Tx, Ty, kVec, kPieces, kTeam == kClusterTeam ? 3 : 2, true>::kWarpBytes + 1024 * kPieces;
+    *warp_bytes = Feed<Tx, Ty, kVec, kPieces, backward_stages<Tx, Ty, kTeam, kPieces>, true>::kWarpBytes + 1024 * kPieces;
     return post ? (drop ? norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 3> : norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 1>)
                 : (drop ? norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 2> : norm_backward_kernel<Tx, Ty, kVec, kTeam, kPieces, 0>);
 }
