@@ -93,15 +93,16 @@ struct Shape {
 // The SMs are taken as 152, each with 16 warps (128 registers a thread); forward, where a
 // warp has one tile, 24 (80 registers).  `bytes`: of a value of x and one of y.  Where both
 // have two a warp can hold two tiles: two are better (a row costs a warp about as much as
-// two tiles do) where they come out even, of rows that begin anywhere from four tiles on,
-// in gradients six, and not where that makes clusters of four of them (gradients: 500
+// two tiles do) where they come out even, in gradients from four tiles on (512 columns 55 us
+// with one, 68 with two; 1024 with post and dropout 79, 69); of rows that begin anywhere from
+// four, in gradients six, and not where that makes clusters of four of them (gradients: 500
 // columns 48 us with one tile, 57 with two; 4095 54, 48; 10001 75, 59; 16383 61, 72.
 // Forward, with post and dropout: 1001 columns 45 us, 40; 4095 55, 44; 8191 64, 51).
 inline Shape norm_shape(uint64_t hidden, uint64_t rows, uint32_t bytes, bool vec, bool backward)
 {
     constexpr uint32_t kSms = 152;
     const uint32_t tiles = (uint32_t)((hidden + kTile - 1) / kTile);
-    const bool many = vec || (tiles > (backward ? 5 : 3) && tiles <= 60);
+    const bool many = vec ? tiles > (backward ? 2 : 1) : tiles > (backward ? 5 : 3) && tiles <= 60;
     const uint32_t pieces = bytes == 4 && many && (tiles % 2 == 0 || tiles > 8) ? 2 : 1, units = (tiles + pieces - 1) / pieces;
     // a cluster's CTA holds three rows in shared memory: 15 warps of two 16-bit tiles, or 16 of one tile
     const uint32_t alone = 16, most = pieces == 2 ? 15 : 16, sm_warps = !backward && pieces == 1 ? 24 : 16;
