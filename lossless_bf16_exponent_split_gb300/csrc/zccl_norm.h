@@ -391,12 +391,18 @@ NormKernel norm_backward_kernel_for(const Shape& s, bool vec, bool post, bool dr
 zccl_status_t launch_norm(NormArgs& a, int x_dtype, int dtype, bool vec, cudaStream_t stream);
 zccl_status_t launch_norm_backward(NormArgs& a, int x_dtype, int dtype, int weight_dtype, bool vec, cudaStream_t stream);
 
+// The most shared memory that a CTA may be launched with, beside a TeamSum's of its own (the
+// forward kernels have one).
+constexpr int kMostSmem = (227 << 10) - (int)kTeamBytes;
+
 // Launches `kernel` as launch_dependent does, in clusters where a row has several CTAs.
 inline cudaError_t launch_teams(NormKernel kernel, const Shape& s, uint32_t threads, size_t smem, cudaStream_t stream,
                                 const NormArgs& a)
 {
-    if (smem + kTeamBytes > 48 << 10) {  // (the forward kernels have kTeamBytes beside it)
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem + kTeamBytes > 48 << 10) {
+        // the limit is the kernel's and not the launch's: always the same one, as another thread may be about to
+        // launch the same kernel for longer rows
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
         if (e != cudaSuccess) return e;
     }
     if (s.team != kClusterTeam) return launch_dependent(kernel, s.grid, threads, smem, stream, a);

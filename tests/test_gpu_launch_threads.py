@@ -1,0 +1,74 @@
+"""GPU: host threads that call one kernel at different sizes at once.  How much shared
+memory a kernel may be launched with belongs to the kernel and not to the launch: a
+call must not take from another thread's what that is about to be launched with."""
+import ctypes
+import threading
+
+import pytest
+import torch
+
+from gpu_util import load_lib, require_gpu
+
+pytestmark = pytest.mark.gpu
+B, F = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def z():
+    require_gpu()
+    load_lib()
+    import lossless_bf16_exponent_split_gb300 as z
+    return z
+
+
+def statuses(calls, times):
+    """What calls[i]() returned in thread i, which makes it `times` times with nothing in between."""
+    start, got = threading.Barrier(len(calls)), [None] * len(calls)
+
+    def run(i):
+        call, seen = calls[i], set()
+        start.wait()
+        for _ in range(times):
+            seen.add(call())
+        got[i] = seen
+
+    pool = [threading.Thread(target=run, args=(i,)) for i in range(len(calls))]
+    for t in pool:
+        t.start()
+    for t in pool:
+        t.join()
+    torch.cuda.synchronize()
+    return got
+
+
+def bound(fn, *args):
+    """fn with its arguments converted once, so that a thread's calls follow one another closely."""
+    converted = [a if t is ctypes.c_void_p and a is None else t(a) for t, a in zip(fn.argtypes, args)]
+    return lambda: fn(*converted)
+
+
+# two widths that one kernel serves: two tiles a warp, one, rows that begin anywhere
+@pytest.mark.parametrize("dtype,widths", [(B, (4096, 8192)), (F, (2816, 4096)), (B, (4095, 8191))])
+def test_norms_of_two_widths(z, dtype, widths):
+    rows, code = 4, z.BF16 if dtype == B else z.F32
+    keep, forward, backward = [], [], []
+    for i in range(8):
+        hidden, stream = widths[i % 2], torch.cuda.Stream()
+        n = z.ResidualNorm(hidden, eps=1e-5)
+        x = torch.randn(rows, hidden, device="cuda").to(dtype)
+        h, gx = torch.empty_like(x), torch.empty_like(x)
+        ws = torch.empty(z.zccl_residual_norm_workspace_bytes(hidden, rows), dtype=torch.uint8, device="cuda")
+        keep.append((n, x, h, gx, ws, stream))
+        forward.append(bound(z.lib().zccl_residual_norm, ctypes.addressof(n.config), x.data_ptr(), code, hidden, None, code, 0,
+                             None, None, z.F32, None, z.F32, 0, 1, rows, 0, None, None, h.data_ptr(), n.status.data_ptr(),
+                             stream.cuda_stream))
+        backward.append(bound(z.lib().zccl_residual_norm_backward, ctypes.addressof(n.config), None, 0, x.data_ptr(), hidden,
+                              x.data_ptr(), code, hidden, None, code, 0, None, None, z.F32, None, z.F32, 0, 1, rows, 0, None,
+                              gx.data_ptr(), None, None, None, None, ws.data_ptr(), ws.numel(), n.status.data_ptr(),
+                              stream.cuda_stream))
+    torch.cuda.synchronize()
+    for calls in (forward, backward):
+        assert statuses(calls, 3000) == [{z.OK}] * 8
+    for n, x, h, gx, ws, _ in keep:
+        assert torch.equal(h, n.norm(x)) and torch.equal(gx, n.norm_backward(x, x)[0])
+        n.check_status()
