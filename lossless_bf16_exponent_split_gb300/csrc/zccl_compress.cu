@@ -565,22 +565,29 @@ size_t compress_smem_bytes(uint32_t n_segs)
     return sizeof(CompressSmem) + 4ull * ((n_segs + 2) & ~1u) + (n_segs <= kSegCache ? 16ull * n_segs : 0ull);
 }
 
+// Lets the kernel be launched with what any number of segments needs.  The limit is the
+// kernel's and not the launch's: always the same one, as another thread may be about to
+// launch it for more segments.
+static cudaError_t allow_smem()
+{
+    const size_t cached = compress_smem_bytes(kSegCache), most = compress_smem_bytes(ZCCL_MAX_SEGMENTS);
+    return cudaFuncSetAttribute(compress_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)(cached > most ? cached : most));
+}
+
 cudaError_t launch_compress(const CompressArgs& a, uint32_t grid, cudaStream_t stream)
 {
-    const size_t smem = compress_smem_bytes(a.n_segs);
-    cudaError_t e = cudaFuncSetAttribute(compress_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem();
     if (e != cudaSuccess) return e;
-    return launch_cooperative(compress_kernel, grid, kThreads, smem, stream, a);
+    return launch_cooperative(compress_kernel, grid, kThreads, compress_smem_bytes(a.n_segs), stream, a);
 }
 
 int compress_ctas_per_sm(uint32_t n_segs)
 {
     int blocks = 0;
-    const size_t smem = compress_smem_bytes(n_segs);
-    if (cudaFuncSetAttribute(compress_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+    if (allow_smem() != cudaSuccess) return 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, compress_kernel, kThreads, compress_smem_bytes(n_segs)) !=
         cudaSuccess)
-        return 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, compress_kernel, kThreads, smem) != cudaSuccess)
         return 1;
     return blocks > 0 ? blocks : 1;
 }

@@ -72,3 +72,26 @@ def test_norms_of_two_widths(z, dtype, widths):
     for n, x, h, gx, ws, _ in keep:
         assert torch.equal(h, n.norm(x)) and torch.equal(gx, n.norm_backward(x, x)[0])
         n.check_status()
+
+
+def test_compressions_of_few_and_many_segments(z):
+    keep, calls = [], []
+    lut = z.zccl_lut_from_sigma(1.0)
+    for i in range(4):
+        count, n, stream = (1, 3000)[i % 2], 40, torch.cuda.Stream()
+        codec = z.Codec()
+        x = torch.randn(count, n, device="cuda").to(B).view(torch.int16)
+        outs = torch.zeros(count, z.zccl_max_compressed_bytes(n), dtype=torch.uint8, device="cuda")
+        table = codec.segment_table(list(zip(x, outs)))
+        sizes = codec.compress_batched(list(zip(x, outs)), lut, table=table)
+        torch.cuda.synchronize()
+        want, again = (outs.clone(), sizes.clone()), torch.zeros_like(sizes)
+        outs.zero_()
+        ws, nbytes = codec.workspace(0)
+        buffer = ctypes.create_string_buffer(lut, 7)
+        keep.append((codec, x, outs, table, again, want, buffer))
+        calls.append(bound(z.lib().zccl_compress_batched, table.data_ptr(), count, count * n, ctypes.addressof(buffer),
+                           again.data_ptr(), ws, nbytes, codec.status.data_ptr(), stream.cuda_stream))
+    assert statuses(calls, 500) == [{z.OK}] * 4
+    for codec, _, outs, _, sizes, want, _ in keep:
+        assert codec.read_status() == z.OK and torch.equal(sizes, want[1]) and torch.equal(outs, want[0])
