@@ -530,15 +530,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) reduce_kernel(const Redu
 template <bool kPlain>
 static size_t reduce_smem_bytes(uint32_t S) { return sizeof(ReduceSmem) + 32ull * S; }
 
+// Lets the kernel be launched with what any number of shards needs.  The limit is the
+// kernel's and not the launch's: always the same one, as another thread may be about to
+// launch it for more shards.  (Refused after the scan kernel, a call would leave its
+// workspace in use.)
+template <bool kPlain>
+static cudaError_t allow_smem()
+{
+    return cudaFuncSetAttribute(reduce_kernel<kPlain>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)reduce_smem_bytes<kPlain>(ZCCL_MAX_SHARDS));
+}
+
 cudaError_t launch_reduce(const ScanArgs& s, const ReduceArgs& a, uint32_t grid_scan, uint32_t grid,
                           cudaStream_t stream)
 {
     const bool plain = a.local != nullptr || a.accumulate;
     const size_t smem = plain ? reduce_smem_bytes<true>(a.S) : reduce_smem_bytes<false>(a.S);
-    cudaError_t e = plain ? cudaFuncSetAttribute(reduce_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem)
-                          : cudaFuncSetAttribute(reduce_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem);
+    cudaError_t e = plain ? allow_smem<true>() : allow_smem<false>();
     if (e != cudaSuccess) return e;
     e = launch_scan(s, grid_scan, stream);
     if (e != cudaSuccess) return e;
@@ -551,9 +559,7 @@ static int reduce_occupancy(uint32_t S)
 {
     const size_t smem = reduce_smem_bytes<kPlain>(S);
     int blocks = 0;
-    if (cudaFuncSetAttribute(reduce_kernel<kPlain>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
-        return 1;
+    if (allow_smem<kPlain>() != cudaSuccess) return 1;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, reduce_kernel<kPlain>, kThreads, smem) !=
         cudaSuccess)
         return 1;

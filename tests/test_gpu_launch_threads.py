@@ -95,3 +95,30 @@ def test_compressions_of_few_and_many_segments(z):
     assert statuses(calls, 500) == [{z.OK}] * 4
     for codec, _, outs, _, sizes, want, _ in keep:
         assert codec.read_status() == z.OK and torch.equal(sizes, want[1]) and torch.equal(outs, want[0])
+
+
+@pytest.mark.parametrize("own", [False, True])
+def test_reductions_of_few_and_many_shards(z, own):
+    """own: with a plain shard of the rank's own."""
+    keep, calls = [], []
+    lut, n = z.zccl_lut_from_sigma(1.0), 40
+    codec = z.Codec()
+    x = torch.randn(n, device="cuda").to(B).view(torch.int16)
+    one, size = codec.compress(x, lut)
+    for i in range(4):
+        count, stream, codec = (2, 1000)[i % 2], torch.cuda.Stream(), z.Codec()
+        streams, sizes = [one] * count, [int(size)] * count
+        want = (codec.decompress_reduce_local(streams, sizes, n, local=x, local_pos=1) if own else
+                codec.decompress_reduce(streams, sizes, n)).clone()
+        ptrs, lengths = (torch.tensor(v, dtype=torch.int64, device="cuda") for v in ([one.data_ptr()] * count, sizes))
+        out = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        ws, nbytes = codec.workspace(0)
+        tail = (out.data_ptr(), n, ws, nbytes, codec.status.data_ptr(), stream.cuda_stream)
+        keep.append((codec, ptrs, lengths, out, want))
+        calls.append(bound(z.lib().zccl_decompress_reduce_local, ptrs.data_ptr(), lengths.data_ptr(), count, x.data_ptr(), 1, 0,
+                           *tail) if own else
+                     bound(z.lib().zccl_decompress_reduce, ptrs.data_ptr(), lengths.data_ptr(), count, *tail))
+    assert statuses(calls, 500) == [{z.OK}] * 4
+    for codec, _, _, out, want in keep:
+        assert codec.read_status() == z.OK and torch.equal(out, want)
