@@ -363,8 +363,9 @@ struct Walk {
         load(a, t + kStep, counted);
         return chosen;
     }
-    // whether the warp has tokens left
-    __device__ __forceinline__ bool more() const { return t - (threadIdx.x & 31) / L < hi; }
+    // the warp's first token, and whether it has one
+    __device__ __forceinline__ uint32_t at() const { return t - (threadIdx.x & 31) / L; }
+    __device__ __forceinline__ bool more() const { return at() < hi; }
 };
 
 // Whether this CTA is the last of `n` to come by; what the others wrote before is visible to it then.
@@ -375,6 +376,17 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t n)
     if (threadIdx.x == 0) before = atom_inc_acq_rel(counter, n - 1);
     __syncthreads();
     return before == n - 1;
+}
+
+// How many of its `steps` tokens a lane adds one after the other before their sum joins
+// those of the runs before it: 256, of more than 65536 their square root at least, so that
+// a sum has 512 roundings in a row, and of any number of tokens twice that root's (one
+// after the other 65536 equal shares were off by 0.06 %).
+__device__ __forceinline__ uint32_t run_of(uint32_t steps)
+{
+    uint32_t run = 256;
+    while ((uint64_t)run * run < steps) run *= 2;
+    return run;
 }
 
 template <typename T, int kRead, int L, int J>
@@ -396,29 +408,41 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
     float sum[J] = {};
     int32_t live = 0;
     Walk<T, kRead, L, J> walk;
-    for (walk.open(a, part.lo, part.hi, true); walk.more(); walk.t += walk.kStep) {
-        float l[J], p[J], slope[J];
-        const Choices<L> chosen = walk.take(a, l, true);
-        const bool counts = chosen.each(a.E, walk.li, [&](int32_t e) { atomicAdd(&slots[e], 1); });
-        live += counts && walk.li == 0 ? 1 : 0;
-        if (!__all_sync(0xFFFFFFFFu, counts) && !counts)
+    walk.open(a, part.lo, part.hi, true);
+    const uint32_t run = run_of((uint32_t)(part.hi - part.lo) / walk.kStep) * walk.kStep;
+    bool first = true;
+    do {
+        const uint32_t till = min(walk.hi, walk.at() + run);
+        for (; walk.at() < till; walk.t += walk.kStep) {
+            float l[J], p[J], slope[J];
+            const Choices<L> chosen = walk.take(a, l, true);
+            const bool counts = chosen.each(a.E, walk.li, [&](int32_t e) { atomicAdd(&slots[e], 1); });
+            live += counts && walk.li == 0 ? 1 : 0;
+            if (!__all_sync(0xFFFFFFFFu, counts) && !counts)
 #pragma unroll
-            for (int j = 0; j < J; ++j) l[j] = -kInf;  // whatever it holds
-        const float f = scores<false, L, J>(a, l, p, slope, l, nullptr);
+                for (int j = 0; j < J; ++j) l[j] = -kInf;  // whatever it holds
+            const float f = scores<false, L, J>(a, l, p, slope, l, nullptr);
 #pragma unroll
-        for (int j = 0; j < J; j += 2) {
-            const float2 v = __ffma2_rn(make_float2(p[j], p[j + 1]), make_float2(f, f), make_float2(sum[j], sum[j + 1]));
-            sum[j] = v.x, sum[j + 1] = v.y;
+            for (int j = 0; j < J; j += 2) {
+                const float2 v = __ffma2_rn(make_float2(p[j], p[j + 1]), make_float2(f, f), make_float2(sum[j], sum[j + 1]));
+                sum[j] = v.x, sum[j + 1] = v.y;
+            }
         }
-    }
-    // over the warp's tokens
+        // over the warp's tokens
 #pragma unroll
-    for (int o = 16; o >= L; o /= 2)
+        for (int o = 16; o >= L; o /= 2)
 #pragma unroll
-        for (int j = 0; j < J; ++j) sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], o);
-    if (lane < L)
+            for (int j = 0; j < J; ++j) sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], o);
+        if (lane < L)
 #pragma unroll
-        for (int j = 0; j < J; ++j) sums[warp][walk.row.expert(walk.li, j)] = sum[j];
+            for (int j = 0; j < J; ++j) {
+                float& of_warp = sums[warp][walk.row.expert(walk.li, j)];
+                of_warp = first ? sum[j] : of_warp + sum[j];
+            }
+#pragma unroll
+        for (int j = 0; j < J; ++j) sum[j] = 0.0f;
+        first = false;
+    } while (walk.more());
     live = __reduce_add_sync(0xFFFFFFFFu, live);
     if (lane == 0) atomicAdd(&live_tokens, live);
     __syncthreads();
