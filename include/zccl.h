@@ -430,9 +430,9 @@ zccl_status_t zccl_combine_backward(const uint16_t* d_grad_out, const uint16_t* 
 
 /* Balance of a routing: a loss that is least when every expert gets as many slots
  * as any other, and each expert's slots.  A sequence is tokens d_seq[s] ..
- * d_seq[s + 1] - 1 (d_seq: device int32 [sequences + 1], non-decreasing from 0, at
- * most tokens; NULL with one sequence: all tokens).  Its tokens with an entry of
- * d_idx in 0..E-1 count, m of them, with n such entries, c[e] of expert e (an expert
+ * d_seq[s + 1] - 1 (d_seq: device int32 [sequences + 1], non-decreasing, 0..tokens;
+ * tokens before the first and behind the last one are no sequence's; NULL with one
+ * sequence: all tokens).  Its tokens with an entry of d_idx in 0..E-1 count, m of them, with n such entries, c[e] of expert e (an expert
  * that a token names twice counts twice):
  *   q       softmax: the row's probabilities; sigmoid: the row's scores over their
  *           sum.  A logit of -infinity has q = 0, a row of them has zeros

@@ -74,8 +74,8 @@ __device__ __forceinline__ void lanes_add(float& x, float& y)
     y = upper ? mine : other;
 }
 
-// A CTA's part: tokens lo..hi-1 of a sequence (`sequences`: the tokens behind the last
-// one) that has `parts` of them, the first of them CTA `first`'s.
+// A CTA's part: tokens lo..hi-1 of a sequence (`sequences`: the tokens before the first
+// or behind the last one) that has `parts` of them, the first of them CTA `first`'s.
 struct Part {
     uint32_t sequence, first, parts;
     uint64_t lo, hi;
@@ -99,10 +99,11 @@ __device__ __forceinline__ uint32_t cta_scan(uint32_t x, uint32_t* by_warp)
     return kMax ? max(x, before) : x + before;
 }
 
-// This CTA's part; false: it has none.  Whatever the table holds, the sequences are
-// taken as runs of 0..tokens-1 one behind the other.  kTail: the tokens behind the last
-// sequence are parts too, and a sequence without tokens is none (else it is one).
-template <bool kTail>
+// This CTA's part; false: it has none.  Whatever the table holds, up to kFewSequences
+// sequences are taken as runs of 0..tokens-1 one behind the other.  kOthers: the tokens
+// before the first sequence and those behind the last one are parts too, and a sequence
+// without tokens is none (else it is one).
+template <bool kOthers>
 __device__ __forceinline__ bool part_of(const BalanceArgs& a, Part* p)
 {
     __shared__ uint32_t begins[kThreads + 1], by_warp[kWarps];
@@ -112,12 +113,19 @@ __device__ __forceinline__ bool part_of(const BalanceArgs& a, Part* p)
         const int32_t v = ld_l2(a.seq + at);
         return v < 0 ? 0 : (uint64_t)v > a.tokens ? (uint32_t)a.tokens : (uint32_t)v;
     };
-    if (a.chunk == 0) {  // a CTA a sequence, and those behind share out the tail
+    if (a.chunk == 0) {  // a CTA a sequence, and those behind share out the other tokens
         const uint32_t s = id < a.sequences ? id : a.sequences;
         const uint32_t b = bound(s), e = s < a.sequences ? bound(s + 1) : (uint32_t)a.tokens;
         *p = {s, id, 1, b, e > b ? e : b};
-        if (id >= a.sequences) {
-            const uint64_t n = p->hi - p->lo, k = gridDim.x - a.sequences, j = id - a.sequences;
+        if (kOthers && id >= a.sequences) {
+            const uint64_t before = bound(0), behind = p->hi - p->lo;
+            uint64_t k = gridDim.x - a.sequences, j = id - a.sequences;  // two CTAs at least
+            const uint64_t heads = before == 0 ? 0 : behind == 0 ? k : min(k - 1, 1 + k * before / (before + behind));
+            if (j < heads)
+                p->lo = 0, p->hi = before, k = heads;
+            else
+                j -= heads, k -= heads;
+            const uint64_t n = p->hi - p->lo;
             p->hi = p->lo + n * (j + 1) / k;
             p->lo += n * j / k;
         }
@@ -131,14 +139,17 @@ __device__ __forceinline__ bool part_of(const BalanceArgs& a, Part* p)
     begins[i] = cta_scan<true>(i <= a.sequences ? bound(i) : (uint32_t)a.tokens, by_warp);
     if (i == 0) begins[kThreads] = (uint32_t)a.tokens, found.parts = 0;
     __syncthreads();
-    const uint32_t n = begins[i + 1] - begins[i], most = kTail ? a.sequences + 1 : a.sequences;
+    const uint32_t n = begins[i + 1] - begins[i], most = kOthers ? a.sequences + 1 : a.sequences;
     uint32_t parts = i < most ? (n + a.chunk - 1) / a.chunk : 0;
-    if (!kTail && i < most && parts == 0) parts = 1;
-    const uint32_t behind = cta_scan<false>(parts, by_warp);
+    if (!kOthers && i < most && parts == 0) parts = 1;
+    const uint32_t heads = kOthers ? (begins[0] + a.chunk - 1) / a.chunk : 0;  // of the tokens before the first: the first CTAs'
+    const uint32_t behind = heads + cta_scan<false>(parts, by_warp);
     if (parts > 0 && id >= behind - parts && id < behind) {
         const uint64_t lo = begins[i] + (uint64_t)(id - (behind - parts)) * a.chunk;
         found = {i, behind - parts, parts, lo, min(lo + a.chunk, (uint64_t)begins[i + 1])};
     }
+    if (kOthers && i == 0 && id < heads)
+        found = {a.sequences, 0, heads, (uint64_t)id * a.chunk, min((uint64_t)(id + 1) * a.chunk, (uint64_t)begins[0])};
     __syncthreads();
     *p = found;
     return p->parts > 0;
@@ -644,11 +655,11 @@ uint32_t chunk_of(uint64_t tokens, uint32_t sequences, uint32_t experts)
 uint32_t grid_of(uint64_t tokens, uint32_t sequences, uint32_t chunk, bool backward)
 {
     if (chunk == 0) {
-        const uint64_t tail = (tokens + kPartTokens - 1) / kPartTokens;
-        return sequences + (backward ? (uint32_t)(tail < 1216 ? tail : 1216) : 0);
+        const uint64_t others = (tokens + kPartTokens - 1) / kPartTokens + 1;
+        return sequences + (backward ? (uint32_t)(others < 1216 ? others : 1216) : 0);
     }
-    // each sequence (and the tail) has at most one part that is not whole
-    return (uint32_t)(tokens / chunk) + sequences + 1;
+    // each sequence (and the tokens before and behind them) has at most one part that is not whole
+    return (uint32_t)(tokens / chunk) + sequences + (backward ? 2 : 1);
 }
 
 bool balance_config(const zccl_route_t* c, int dtype, uint64_t stride, uint64_t tokens, uint32_t sequences,

@@ -194,7 +194,8 @@ class Moe:
         slots: a loss that is `coefficient` where the slots or the scores are shared
         out evenly, and each expert's slots.  sequences: int32 [n + 1], each sequence's
         first token and, last, where they end: the loss is then the mean of each one's
-        (default: all tokens as one).  Tokens without a choice do not count."""
+        (default: all tokens as one).  Tokens outside of them, or without a choice, do
+        not count."""
         tokens, stride, dtype = self._logits(logits)
         self._slots(idx, "idx", torch.int32, tokens)
         seq, n = self._sequences(sequences)
