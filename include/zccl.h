@@ -442,6 +442,9 @@ zccl_status_t zccl_combine_backward(const uint16_t* d_grad_out, const uint16_t* 
  * experts, top_k and score are used.  Sums of q are held in fp32 in an order that
  * depends on the sizes and the sequences alone.  d_loss: float; d_counts: int32 [sequences][E];
  * d_tokens: int32 [sequences + 1], each sequence's m and, last, how many have one.
+ * A table that runs backwards: up to 304 sequences begin where the last one ended; with
+ * more the loss is NaN, there is no gradient, d_tokens[s] is -1 where s would end before
+ * it begins and its last entry 0.
  * sequences: 1..ZCCL_MAX_SEQUENCES.  Workspace: zeroed once before its first use. */
 #define ZCCL_MAX_SEQUENCES 65536u
 zccl_status_t zccl_balance_workspace_bytes(uint32_t sequences, uint32_t experts, uint64_t* bytes);

@@ -100,7 +100,8 @@ __device__ __forceinline__ uint32_t cta_scan(uint32_t x, uint32_t* by_warp)
 }
 
 // This CTA's part; false: it has none.  Whatever the table holds, up to kFewSequences
-// sequences are taken as runs of 0..tokens-1 one behind the other.  kOthers: the tokens
+// sequences are taken as runs of 0..tokens-1 one behind the other; of more, one that would
+// end before it begins has no tokens and no parts.  kOthers: the tokens
 // before the first sequence and those behind the last one are parts too, and a sequence
 // without tokens is none (else it is one).
 template <bool kOthers>
@@ -116,7 +117,7 @@ __device__ __forceinline__ bool part_of(const BalanceArgs& a, Part* p)
     if (a.chunk == 0) {  // a CTA a sequence, and those behind share out the other tokens
         const uint32_t s = id < a.sequences ? id : a.sequences;
         const uint32_t b = bound(s), e = s < a.sequences ? bound(s + 1) : (uint32_t)a.tokens;
-        *p = {s, id, 1, b, e > b ? e : b};
+        *p = {s, id, e >= b ? 1u : 0u, b, e > b ? e : b};
         if (kOthers && id >= a.sequences) {
             const uint64_t before = bound(0), behind = p->hi - p->lo;
             uint64_t k = gridDim.x - a.sequences, j = id - a.sequences;  // two CTAs at least
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) d += red[w], u += used_by[w];
         a.losses[s] = live_tokens > 0 ? d * ((float)a.E / ((float)u * (float)live_tokens)) : 0.0f;
-        a.live[s] = live_tokens;
+        a.live[s] = part.parts > 0 ? live_tokens : -1;
     }
     // the call's
     if (a.sequences == 1)
@@ -536,12 +537,16 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
         return;
     dot = 0.0f;
     int32_t alive = 0;
+    bool backwards = false;
     for (uint32_t i = threadIdx.x; i < a.sequences; i += kThreads) {
+        const int32_t m = a.live[i];
         dot += a.losses[i];
-        alive += a.live[i] > 0 ? 1 : 0;
+        alive += m > 0 ? 1 : 0;
+        backwards |= m < 0;
     }
     dot = lanes_add<32>(dot);
     alive = __reduce_add_sync(0xFFFFFFFFu, alive);
+    if (__any_sync(0xFFFFFFFFu, backwards)) alive = -2 * (int32_t)ZCCL_MAX_SEQUENCES;  // below 0 whatever the others have
     if (lane == 0) red[warp] = dot, used_by[warp] = alive;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -549,7 +554,9 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(BalanceArgs a)
         int32_t n = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) d += red[w], n += used_by[w];
-        *a.loss = n > 0 ? a.coefficient * (d / (float)n) : 0.0f;
+        // sequences of a table that runs backwards may share tokens: none of them has a loss, or a gradient
+        *a.loss = n > 0 ? a.coefficient * (d / (float)n) : n < 0 ? __uint_as_float(0x7FC00000u) : 0.0f;
+        n = max(n, 0);
         a.live[a.sequences] = n;
     }
 }
@@ -568,6 +575,7 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs 
     T* out = static_cast<T*>(a.grad) + walk.t * a.grad_stride;
     // what a unit of an expert's shares adds to the loss
     float f[J] = {};
+    uint32_t named = 0;  // experts below it count
     if (counted) {
         int32_t c[J], used = 0;
 #pragma unroll
@@ -580,14 +588,16 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs 
         for (int o = L / 2; o > 0; o /= 2) used += __shfl_xor_sync(0xFFFFFFFFu, used, o);
         const float up = a.coefficient * (a.grad_loss != nullptr ? *a.grad_loss : 1.0f);
         const float each = (float)used * (float)a.live[s] * (float)a.live[a.sequences];
-        const float unit = each > 0.0f ? up * ((float)a.E / each) : 0.0f;
+        named = each > 0.0f ? a.E : 0;
+        if (named == 0 && a.accumulate) return;
+        const float unit = named > 0 ? up * ((float)a.E / each) : 0.0f;
 #pragma unroll
         for (int j = 0; j < J; ++j) f[j] = unit * (float)c[j];
     }
     for (; walk.more(); walk.t += walk.kStep, out += walk.kStep * a.grad_stride) {
         float l[J], g[J], slope[J], sum;
         const Choices<L> chosen = walk.take(a, l, counted);
-        const bool there = walk.t < walk.hi, counts = chosen.each(a.E, walk.li, [](int32_t) {});
+        const bool there = walk.t < walk.hi, counts = chosen.each(named, walk.li, [](int32_t) {});
         if (!__all_sync(0xFFFFFFFFu, counts) && !counts)
 #pragma unroll
             for (int j = 0; j < J; ++j) l[j] = -kInf;  // whatever it holds
