@@ -609,7 +609,13 @@ __global__ void __launch_bounds__(kThreads) balance_backward_kernel(BalanceArgs 
             if (a.sigmoid) q = __fmul2_rn(q, make_float2(slope[j], slope[j + 1]));
             g[j] = q.x, g[j + 1] = q.y;
         }
-        if (!there || (a.accumulate && !counts)) continue;
+        if (!counts) {  // none, whatever the loss's gradient is
+            if (!there || a.accumulate) continue;
+#pragma unroll
+            for (int j = 0; j < J; ++j) g[j] = 0.0f;
+            store_row<T, kRead, L, J>(out, g, walk.li, a.E);
+            continue;
+        }
         if (a.accumulate) {
             Logits<T, kRead, L, J> old;
             old.load(out, walk.li, a.E);

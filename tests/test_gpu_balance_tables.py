@@ -94,3 +94,21 @@ def test_many_sequences_out_of_order_have_no_loss(z, at, value):
     got = moe.balance(l, idx, seq)
     assert torch.equal(got.counts.cpu(), counts) and abs(float(got.loss) - loss) <= LOSS * loss
     close(gradient(z, moe, l, idx, got, seq, 7.0), grad, mag)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bounds", [[0, 500], [10, 200, 460], [10] + list(range(11, 471))])
+def test_what_does_not_count_has_no_gradient_of_any_loss(z, bounds, score):
+    """Also where the loss's own gradient has overflowed."""
+    l, idx = inputs(500, 12, 3, F, masked=0.3)
+    moe, seq = z.Moe(12, 3, score=score), torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    got = moe.balance(l, idx, seq)
+    counts = (idx >= 0).any(1)
+    counts[:bounds[0]] = counts[bounds[-1]:] = False
+    assert 0 < int(counts.sum()) < 400
+    for value in (float("inf"), float("nan")):
+        grad = moe.balance_backward(l, idx, got, seq, grad_loss=torch.full((1,), value, device="cuda"))
+        assert bool((grad[~counts] == 0).all()) and not bool(grad[counts].isfinite().all(1).any())
+        base = torch.randn_like(l)
+        out = moe.balance_backward(l, idx, got, seq, grad_loss=torch.full((1,), value, device="cuda"), out=base.clone())
+        assert torch.equal(out[~counts], base[~counts])
