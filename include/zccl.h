@@ -581,6 +581,8 @@ zccl_status_t zccl_residual_norm_workspace_bytes(uint64_t hidden, uint64_t rows,
  *              up][hidden], contiguous.  NULL: not wanted.  Their sums over rows are
  *              held in fp32, in an order that depends on sizes, types and alignment
  *              alone.
+ * Without post a dropped element's own gradient has no part in those of y, the weights
+ * and the gate, whatever it is.
  * d_status as above. */
 zccl_status_t zccl_residual_norm_backward(const zccl_norm_t* cfg, const void* d_grad_r, uint64_t grad_r_stride,
                                           const void* d_grad_h, uint64_t grad_h_stride, const void* d_r, int x_dtype,

@@ -131,15 +131,17 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(Nor
             const Eight r = load_or_zero<Tx, kVec>(a.x, t * a.x_stride, tile, a.hidden);
             const Eight dh = load_or_zero<Ty, kVec>(a.grad_h, t * a.grad_h_stride, tile, a.hidden);
             const Eight up = load_or_zero<Tx, kVec>(a.grad_r, t * a.grad_r_stride, tile, a.hidden);
-            const Eight d = joined(f, r, mul(dh, load_vector<kVec>(a.weight, 0, tile, a.hidden)), up);
+            Eight d = joined(f, r, mul(dh, load_vector<kVec>(a.weight, 0, tile, a.hidden)), up);
             if (a.grad_x != nullptr) store8<Tx, kVec>(static_cast<Tx*>(a.grad_x) + (uint64_t)t * a.hidden, d, tile, a.hidden);
             if (a.grad_weight != nullptr)
                 add_to<kVec>(sums + kSlotWeight * pitch, mul(dh, mul(r, f.rho)), t == lo, tile, a.hidden);
             if (!join) continue;
-            const Eight y = load_or_zero<Ty, kVec>(a.y, t * a.y_stride, tile, a.hidden);
-            const Eight k = join_factors<kVec>(a, t, tile), p = load_vector<kVec>(a.post_weight, 0, tile, a.hidden);
             const Kept<kVec> kept = join_kept<kVec>(a, offset, t, tile);
-            const Eight e = where_kept<kVec>(kept, mul(d, mul(y, f.eta)));
+            d = where_kept<kVec>(kept, d);
+            Eight y = load_or_zero<Ty, kVec>(a.y, t * a.y_stride, tile, a.hidden);
+            if (!a.post) y = where_kept<kVec>(kept, y);
+            const Eight k = join_factors<kVec>(a, t, tile), p = load_vector<kVec>(a.post_weight, 0, tile, a.hidden);
+            const Eight e = mul(d, mul(y, f.eta));
             if (a.grad_gate != nullptr) {
                 const Eight v = mul(e, mul(p, a.factor));
                 const uint32_t begin = gate_row * a.gate_span, end = begin + a.gate_span;
@@ -149,8 +151,7 @@ __global__ void __launch_bounds__(kTeamWarps * 32) norm_backward_long_kernel(Nor
                 if (begin >= lo && (t + 1 == end || t + 1 == a.rows)) store_gate<kVec>(a, gate_row, all, tile);
             }
             if (a.grad_post_weight != nullptr) add_to<kVec>(sums + kSlotPost * pitch, mul(e, k), t == lo, tile, a.hidden);
-            store8<Ty, kVec>(static_cast<Ty*>(a.grad_y) + (uint64_t)t * a.hidden, branch(a.post, f, d, y, where_kept<kVec>(kept, mul(k, p))), tile,
-                             a.hidden);
+            store8<Ty, kVec>(static_cast<Ty*>(a.grad_y) + (uint64_t)t * a.hidden, branch(a.post, f, d, y, mul(k, p)), tile, a.hidden);
         }
     }
 }
