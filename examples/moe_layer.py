@@ -67,16 +67,17 @@ class MoeLayer:
         self.wire_bytes, self.payload_bytes = sum(sizes), 2 * row * hidden
         return received
 
-    def forward(self, x, step=0):
-        """step: another one for each call has another dropout mask."""
+    def forward(self, x, step=0, train=True):
+        """step: another one for each call has another dropout mask; train: False for an evaluation, without one."""
         logits = x @ self.router.t()
         idx, weights = self.moe.route(logits, self.bias)
         d = self.moe.dispatch(x, idx, capacity=self.capacity)
         rows = self.exchange(d)
         h = self.fp8.linear(rows, self.up, d.offsets)
         a = torch.nn.functional.silu(h)
-        if self.dropout:
-            a = self.dropout.apply(a, offset=step)
+        self.drops = self.dropout if train else None
+        if self.drops:
+            a = self.drops.apply(a, offset=step)
         y = self.fp8.linear(a, self.down, d.offsets)
         self.kept, self.step = (x, logits, idx, weights, d, rows, h, a, y), step
         return self.moe.combine(y, d.pos, weights)
@@ -87,8 +88,8 @@ class MoeLayer:
         x, logits, idx, weights, d, rows, h, a, y = self.kept
         grad_y, grad_weights = self.moe.combine_backward(grad, y, d.pos, weights, d.offsets)
         grad_a, grad_down = self.fp8.linear_backward(grad_y, a, self.down, d.offsets)
-        if self.dropout:
-            grad_a = self.dropout.apply(grad_a, offset=self.step)
+        if self.drops:
+            grad_a = self.drops.apply(grad_a, offset=self.step)
         s = torch.sigmoid(h.float())
         grad_h = (grad_a.float() * s * (1 + h.float() * (1 - s))).bfloat16()
         grad_rows, grad_up = self.fp8.linear_backward(grad_h, rows, self.up, d.offsets)
@@ -104,37 +105,42 @@ class MoeLayer:
 
 
 class MoeBlock:
-    """h = N(x), r = x + scale * drop(N(layer(h))), and N(r) for the next block."""
+    """h = N(x), r = x + scale * drop(N(layer(h))), and N(r) for the next block.  A handle's
+    dropout is its own: evaluations have a second one without."""
 
     def __init__(self, experts, top_k, hidden, inner, *, scale=1.0, dropout=0.0, balance=0.01, seed=0, **layer):
         self.layer = MoeLayer(experts, top_k, hidden, inner, seed=seed, dropout=dropout, **layer)
         self.norm = z.ResidualNorm(hidden, post=True, scale=scale, dropout=dropout, seed=seed + 1)
+        self.plain = z.ResidualNorm(hidden, post=True, scale=scale)
         self.weight, self.post_weight, self.next_weight = (torch.ones(hidden, device="cuda") for _ in range(3))
         self.coefficient = balance
 
-    def forward(self, x, step=0, sequences=None):
+    def forward(self, x, step=0, sequences=None, train=True):
         """(the residual behind the block, the next block's input, the balance loss);
-        sequences: where each sequence of the batch begins, and where the last ends."""
-        h = self.norm.norm(x, self.weight)
-        y = self.layer.forward(h, step)
+        sequences: where each sequence of the batch begins, and where the last ends;
+        train: False for an evaluation, where nothing is dropped."""
+        norm = self.norm if train else self.plain
+        h = norm.norm(x, self.weight)
+        y = self.layer.forward(h, step, train)
         _, logits, idx, *_ = self.layer.kept
         balance = self.layer.moe.balance(logits, idx, sequences, self.coefficient)
-        r, h_next = self.norm.add(x, y, self.next_weight, post_weight=self.post_weight, offset=step)
-        self.kept = x, y, r, balance, sequences, step
+        r, h_next = norm.add(x, y, self.next_weight, post_weight=self.post_weight, offset=step)
+        self.kept = norm, x, y, r, balance, sequences, step
         return r, h_next, balance.loss
 
     def backward(self, grad_r, grad_h):
         """Gradients of (x, weight, post_weight, next_weight, router, up, down) from those of
         the residual behind the block and the next block's input, and of the balance loss."""
-        x, y, r, balance, sequences, step = self.kept
-        g = self.norm.add_backward(grad_r, grad_h, r, y, self.next_weight, post_weight=self.post_weight, offset=step)
+        norm, x, y, r, balance, sequences, step = self.kept
+        g = norm.add_backward(grad_r, grad_h, r, y, self.next_weight, post_weight=self.post_weight, offset=step)
         grad_in, *grads = self.layer.backward(g.y, balance, sequences, self.coefficient)
-        grad_x, grad_weight = self.norm.norm_backward(grad_in, x, self.weight, residual=g.x)
+        grad_x, grad_weight = norm.norm_backward(grad_in, x, self.weight, residual=g.x)
         return grad_x, grad_weight, g.post_weight, g.weight, *grads
 
     def check_status(self):
         self.layer.check_status()
-        self.norm.check_status("moe block")
+        for norm in (self.norm, self.plain):
+            norm.check_status("moe block")
 
 
 def main():
@@ -148,7 +154,7 @@ def main():
     names = ("x", "weight", "post weight", "next weight", "router", "up", "down")
     for step, tokens in enumerate((a.tokens, 1)):  # a training step, a serving step
         x = torch.randn(tokens, a.hidden, device="cuda").bfloat16()
-        r, h, loss = block.forward(x, step)
+        r, h, loss = block.forward(x, step, train=tokens > 1)
         block.check_status()
         print(f"{tokens} tokens: output {tuple(r.shape)}, {layer.wire_bytes} bytes sent for {layer.payload_bytes}, "
               f"balance loss {loss.item():.4f}")

@@ -65,9 +65,10 @@ class ResidualNorm:
         N(v; w) = w * v / sqrt(mean(v^2) + eps) over a row
 
     hidden: values of a row; post: the block's output is normed too; scale: the
-    block's factor; dropout, seed: the share of the block's output that is
-    dropped (``Dropout``'s mask on the row and column).  device: default the
-    current one; calls refuse to run while another one is current."""
+    block's factor; dropout, seed: the share of the block's output that every call
+    of ``add`` drops (``Dropout``'s mask on the row and column); an evaluation has a
+    handle of its own, without.  device: default the current one; calls refuse to
+    run while another one is current."""
 
     def __init__(self, hidden: int, *, post: bool = False, eps: float = 1e-6, scale: float = 1.0, dropout: float = 0.0,
                  seed: int = 0, device=None):
