@@ -248,56 +248,34 @@ struct Feed<Tx, Ty, false, kPieces, kStages, kBackward> {
     }
 };
 
-// Others come into registers: the row that is read, and the next one.
-template <typename Tx, typename Ty, bool kVec, int kPieces, bool kBackward>
-struct Feed<Tx, Ty, kVec, kPieces, 0, kBackward> {
+// Forward, rows of two tiles a warp come into registers: the row that is read, and the
+// next one.
+template <typename Tx, typename Ty, int kPieces>
+struct Feed<Tx, Ty, true, kPieces, 0, false> {
     static constexpr uint32_t kWarpBytes = 0;
     struct Row {
-        Piece<Tx, kVec> px[kPieces], px1[kPieces];
-        Piece<Ty, kVec> py[kPieces], py1[kPieces];
+        Piece<Tx, true> px[kPieces];
+        Piece<Ty, true> py[kPieces];
         __device__ __forceinline__ Eight x(int n) const { return px[n].get(); }
         __device__ __forceinline__ Eight y(int n) const { return py[n].get(); }
-        __device__ __forceinline__ Eight x1(int n) const { return px1[n].get(); }
-        __device__ __forceinline__ Eight y1(int n) const { return py1[n].get(); }
     };
     Row next;
-    const Tx *x, *x1;  // the row that is asked for next
-    const Ty *y, *y1;
-    __device__ __forceinline__ Feed(uint4*, const NormArgs& a, const Place&, uint32_t t) : next{}
+    const Tx* x;  // the row that is asked for next
+    const Ty* y;
+    __device__ __forceinline__ Feed(uint4*, const NormArgs& a, const Place&, uint32_t t)
+        : next{}, x(static_cast<const Tx*>(a.x) + t * a.x_stride), y(static_cast<const Ty*>(a.y) + t * a.y_stride)
     {
-        x = static_cast<const Tx*>(a.x) + t * a.x_stride;
-        if (kBackward) {
-            y = static_cast<const Ty*>(a.grad_h) + t * a.grad_h_stride;
-            x1 = static_cast<const Tx*>(a.grad_r) + t * a.grad_r_stride;
-            y1 = static_cast<const Ty*>(a.y) + t * a.y_stride;
-        } else {
-            y = static_cast<const Ty*>(a.y) + t * a.y_stride;
-        }
     }
     __device__ __forceinline__ void ask(const NormArgs& a, const Place& place, bool there)
     {
         if (!there) return;
 #pragma unroll
         for (int n = 0; n < kPieces; ++n) {
-            const uint32_t tile = place.tile(n);
-            if (kBackward) {
-                if (a.grad_h != nullptr) {
-                    next.px[n].load(x, tile, a.hidden);
-                    next.py[n].load(y, tile, a.hidden);
-                }
-                if (a.grad_r != nullptr) next.px1[n].load(x1, tile, a.hidden);
-                if (a.y != nullptr) next.py1[n].load(y1, tile, a.hidden);
-            } else {
-                next.px[n].load(x, tile, a.hidden);
-                if (a.y != nullptr) next.py[n].load(y, tile, a.hidden);
-            }
+            next.px[n].load(x, place.tile(n), a.hidden);
+            if (a.y != nullptr) next.py[n].load(y, place.tile(n), a.hidden);
         }
         x += a.x_stride;
-        y += kBackward ? a.grad_h_stride : a.y_stride;
-        if (kBackward) {
-            x1 += a.grad_r_stride;
-            y1 += a.y_stride;
-        }
+        y += a.y_stride;
     }
     template <int kLater>
     __device__ __forceinline__ void wait()
