@@ -32,8 +32,9 @@
  *   - all calls are stateless and thread-safe, never throw, and never
  *     allocate: the caller owns every buffer, including the workspace;
  *   - device pointers refer to memory of the current CUDA device; data
- *     buffers (inputs, outputs, streams, workspace) must be 16-byte aligned,
- *     else ZCCL_ERR_INVALID_ARG; d_out_bytes must be 8-byte aligned;
+ *     buffers (inputs, outputs, streams, workspace) must be 16-byte aligned
+ *     (the calls from the mixture of experts on state their own alignments), else
+ *     ZCCL_ERR_INVALID_ARG; d_out_bytes must be 8-byte aligned;
  *   - all device work is queued asynchronously on `stream`; errors the host
  *     can see are returned at once and then nothing is launched;
  *   - data-dependent errors (corrupt stream, bad segment, timeout) are
@@ -432,20 +433,28 @@ zccl_status_t zccl_combine_backward(const uint16_t* d_grad_out, const uint16_t* 
  * as any other, and each expert's slots.  A sequence is tokens d_seq[s] ..
  * d_seq[s + 1] - 1 (d_seq: device int32 [sequences + 1], non-decreasing, 0..tokens;
  * tokens before the first and behind the last one are no sequence's; NULL with one
- * sequence: all tokens).  Its tokens with an entry of d_idx in 0..E-1 count, m of them, with n such entries, c[e] of expert e (an expert
- * that a token names twice counts twice):
+ * sequence: all tokens).  Its tokens with an entry of d_idx in 0..E-1 count, m of them,
+ * with n such entries, c[e] of expert e (an expert that a token names twice counts twice):
  *   q       softmax: the row's probabilities; sigmoid: the row's scores over their
  *           sum.  A logit of -infinity has q = 0, a row of them has zeros
  *   L_s   = E / (n m) * sum over e of c[e] * (sum over its tokens of q[e])
  *   loss  = coefficient * (mean of L_s over the sequences with m > 0); 0 without one
  * L_s is 1 where the slots or the scores are shared out evenly.  Of cfg the fields
- * experts, top_k and score are used.  Sums of q are held in fp32 in an order that
- * depends on the sizes and the sequences alone.  d_loss: float; d_counts: int32 [sequences][E];
- * d_tokens: int32 [sequences + 1], each sequence's m and, last, how many have one.
+ * experts, top_k and score are used.  q comes from the GPU's approximate exponential and
+ * reciprocal: it is off by at most (d + 16) 2^-22 of itself, d how far its logit is below
+ * the row's largest (sigmoid: the logit's size), and 0 where its score is below 2^-126 of
+ * the largest (sigmoid: of 1, in a row whose scores add up to 2^-80 or more).  Sums of q are
+ * held in fp32 in an order that depends on sizes, types, alignment and the sequences
+ * alone.  Up to 304 sequences are shared out over the GPU whatever their lengths; of
+ * more each is one CTA's.
+ *   d_loss    float
+ *   d_counts  int32 [sequences][E]
+ *   d_tokens  int32 [sequences + 1]: each sequence's m and, last, how many have one
  * A table that runs backwards: up to 304 sequences begin where the last one ended; with
  * more the loss is NaN, there is no gradient, d_tokens[s] is -1 where s would end before
  * it begins and its last entry 0.
- * sequences: 1..ZCCL_MAX_SEQUENCES.  Workspace: zeroed once before its first use. */
+ * sequences: 1..ZCCL_MAX_SEQUENCES.  Workspace: zeroed once before its first use.
+ * Pointers are aligned to their type, the workspace to 4 bytes. */
 #define ZCCL_MAX_SEQUENCES 65536u
 zccl_status_t zccl_balance_workspace_bytes(uint32_t sequences, uint32_t experts, uint64_t* bytes);
 zccl_status_t zccl_balance(const zccl_route_t* cfg, const void* d_logits, int dtype, uint64_t stride,
@@ -568,7 +577,8 @@ zccl_status_t zccl_residual_norm(const zccl_norm_t* cfg, const void* d_x, int x_
                                  const uint64_t* d_offset, void* d_r, void* d_h, uint32_t* d_status,
                                  cudaStream_t stream);
 
-/* Workspace of zccl_residual_norm_backward; its contents before a call do not matter. */
+/* Workspace of zccl_residual_norm_backward, 16-byte aligned; its contents before a call do
+ * not matter. */
 zccl_status_t zccl_residual_norm_workspace_bytes(uint64_t hidden, uint64_t rows, uint64_t* bytes);
 
 /* Gradients of zccl_residual_norm, from those of r (d_grad_r, of x_dtype) and h
@@ -606,8 +616,8 @@ zccl_status_t zccl_residual_norm_backward(const zccl_norm_t* cfg, const void* d_
  * call on the output's gradient.  offset: another one for each mask; *d_offset, where
  * not NULL, is added to it, so that a captured graph's replays can have masks of
  * their own.  d_x: [rows] of cols values (dtype), `stride` elements apart; d_out:
- * contiguous, and may be d_x where that is contiguous.  rows < 2^32, cols < 2^24,
- * 0 <= p <= 1. */
+ * contiguous, and may be d_x where that is contiguous.  Pointers are aligned to their
+ * type.  rows < 2^32, cols < 2^24, 0 <= p <= 1. */
 zccl_status_t zccl_dropout(const void* d_x, int dtype, uint64_t stride, uint64_t rows, uint64_t cols, float p,
                            uint64_t seed, uint64_t offset, const uint64_t* d_offset, void* d_out, cudaStream_t stream);
 

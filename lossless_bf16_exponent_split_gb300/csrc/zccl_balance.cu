@@ -4,15 +4,16 @@
 // 8, 16 or 32 lanes hold a token's logits, 8 or 16 each, and keep the sums of their
 // experts' shares over the tokens that come by.  A sequence's tokens are cut into parts
 // of `chunk` tokens, a CTA each; the last part to arrive adds the parts' sums in their
-// order, and the last sequence the sequences' losses, so results depend on the sizes
-// alone.  With very many sequences each is one part.
+// order, and the last sequence the sequences' losses, so results do not depend on who
+// comes when.  Of more than kFewSequences sequences each is one part, however long.
 //
 // The bytes are few (16384 x 64 in BF16: 2 MB, 0.3 us of HBM time): a call is bound by its
-// latencies (the table, the first logits, the hand-over to the last part), 6.6 us for the
-// loss and 4.3 for the gradient; many experts by those and by issue (65621 x 256 in 32 bits
-// with sigmoid scores: 149 and 197 instructions a warp and token, in six of ten issue
-// slots; 46 us for both, 3.0 TB/s; logits three tokens ahead by asynchronous copies 49).
-// Exponentials and reciprocals are the fast ones: nothing here decides between close values.
+// latencies (the table, the first logits, the hand-over to the last part), 10.7 us for the
+// loss and the gradient; many experts by those and by a warp's one token at hand (65621 x 256
+// in 32 bits with sigmoid scores: 152 and 194 instructions a warp and token, in 53 and 59 %
+// of the issue slots; 46 us for both, 3.0 TB/s; logits three tokens ahead by asynchronous
+// copies 49).  Exponentials and reciprocals are the fast ones: nothing here decides between
+// close values.
 #include <cmath>
 
 #include "zccl_ops.cuh"
@@ -654,8 +655,8 @@ BalanceKernel balance_for(const BalanceArgs& a, int dtype, bool backward)
 
 // Tokens of a part, and the CTAs that there are parts for.  One sequence: as many parts
 // as two a SM hold, or one where its registers (more than 256 experts) or the joining of
-// its parts (more than 128) ask for fewer: 16384 x 512 (loss and gradient) 26 us
-// with 152 parts, 37 with 304; x 256 21.3 and 23.5.  Several sequences have a part each that is not whole, which is counted in.
+// its parts (more than 128) ask for fewer: 16384 x 512 (loss and gradient) 25 us
+// with 152 parts, 36 with 304; x 256 19.3 and 21.5.  Several sequences have a part each that is not whole, which is counted in.
 constexpr uint32_t kPartTokens = 64;
 uint64_t most_parts(uint32_t sequences, uint32_t experts)
 {

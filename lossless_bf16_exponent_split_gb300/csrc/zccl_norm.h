@@ -130,7 +130,7 @@ inline Shape norm_shape(uint64_t hidden, uint64_t rows, uint32_t bytes, bool vec
         s.workers = at_most_rows((uint64_t)(s.ctas == 4 ? 144 : kSms) * sm_ctas / s.ctas);
         s.grid = s.workers * s.ctas;
     } else {
-        // its sums stay in the workspace: fewer workers for longer rows
+        // gradients' sums stay in the workspace: fewer workers for longer rows (forward alike, where nothing asks for it)
         s = {kLong, 1, kTeamWarps, 1, at_most_rows(kSms * 16384 / hidden * 2), 0};
         s.grid = s.workers;
     }
