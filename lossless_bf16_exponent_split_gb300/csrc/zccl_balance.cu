@@ -393,7 +393,7 @@ __device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t n)
 
 // How many of its `steps` tokens a lane adds one after the other before their sum joins
 // those of the runs before it: 256, of more than 65536 their square root at least, so that
-// a sum has 512 roundings in a row, and of any number of tokens twice that root's (one
+// a sum has 512 roundings in a row, and of any number of tokens three times that root's (one
 // after the other 65536 equal shares were off by 0.06 %).
 __device__ __forceinline__ uint32_t run_of(uint32_t steps)
 {

@@ -195,7 +195,9 @@ class Moe:
         out evenly, and each expert's slots.  sequences: int32 [n + 1], each sequence's
         first token and, last, where they end: the loss is then the mean of each one's
         (default: all tokens as one).  Tokens outside of them, or without a choice, do
-        not count."""
+        not count.  The entries are in order: of up to 304 sequences one that is not
+        begins where the one before it ended, of more the loss is NaN and there is no
+        gradient."""
         tokens, stride, dtype = self._logits(logits)
         self._slots(idx, "idx", torch.int32, tokens)
         seq, n = self._sequences(sequences)
