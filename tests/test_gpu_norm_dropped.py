@@ -36,3 +36,18 @@ def test_gradients_that_overflowed_where_the_mask_drops(z, hidden, dtype, bad):
         assert torch.equal(got.y, want.y) and bool((got.y[~keep] == 0).all())
         assert torch.equal(got.gate, want.gate) and (gh is None or torch.equal(got.weight, want.weight))
         assert torch.equal(got.x[keep], want.x[keep]) and not bool(got.x[~keep].isfinite().any())
+
+
+@pytest.mark.parametrize("hidden", [64, 255, 2048, 2047, 9600, 16383, 16385, 16392])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_values_that_the_mask_drops_may_be_anything(z, hidden, bad):
+    rows, g = 6, torch.Generator(device="cuda").manual_seed(hidden)
+    x, y, grad_r, grad_h = (torch.randn(rows, hidden, generator=g, device="cuda").to(B) for _ in range(4))
+    w, gate = torch.rand(hidden, generator=g, device="cuda"), torch.rand(2, hidden, generator=g, device="cuda")
+    n = z.ResidualNorm(hidden, dropout=0.5, seed=4)
+    keep = ref.kept(rows, hidden, 0.5, 4, 0).cuda()
+    spoilt = torch.where(keep, y, torch.full_like(y, bad))
+    r, h = n.add(x, y, w, gate=gate)
+    assert all(torch.equal(a, b) for a, b in zip(n.add(x, spoilt, w, gate=gate), (r, h)))
+    for a, b in zip(n.add_backward(grad_r, grad_h, r, spoilt, w, gate=gate), n.add_backward(grad_r, grad_h, r, y, w, gate=gate)):
+        assert (a is None and b is None) or torch.equal(a, b)
